@@ -203,8 +203,14 @@ def prepare(case, seed):
     flat = _normal((sum(counts),), 1e-3, g, 1e-4).to(_type(case["src"]))
     out = flat if case["inplace"] else torch.empty(flat.numel(), dtype=_type(case["dst"]), device=DEV)
     norm = math.sqrt(flat.numel()) * 1e-3
-    return dict(case=case, flat=flat, grads=_views(flat, counts), out=out,
-                outs=_views(out, counts), max_norm=0.25 * norm if case["clipped"] else 8.0 * norm)
+    st = dict(case=case, flat=flat, grads=_views(flat, counts), out=out,
+              outs=_views(out, counts), max_norm=0.25 * norm if case["clipped"] else 8.0 * norm)
+    if own:
+        # a program names its gradient buffers once, before its first step
+        from weight_communication_gb300 import gradnorm
+        st["list"] = gradnorm.TensorList(st["grads"])
+        st["out_list"] = None if case["inplace"] else gradnorm.TensorList(st["outs"])
+    return st
 
 
 # ---------------------------------------------------------------------------
@@ -319,8 +325,7 @@ def _own_embed_grad(st):
 
 def _own_clip(st):
     from weight_communication_gb300 import gradnorm
-    out = None if st["case"]["inplace"] else st["outs"]
-    stats = gradnorm.clip(st["grads"], st["max_norm"], out=out, eps=EPS)
+    stats = gradnorm.clip(st["list"], st["max_norm"], out=st["out_list"], eps=EPS)
     return {"norm": stats[0], "coef": stats[1], "out": st["out"]}
 
 
