@@ -3,7 +3,9 @@
  *
  * The hot path of ZeRO++ quantized gradient reduction (qgZ) with LoCo error
  * feedback, plus qwZ weight quantization and ZeRO-2 stochastic-rounding
- * gradient accumulation, as sm_103a CUDA kernels.  Several data-parallel
+ * gradient accumulation, and the operators of a training step that stand next
+ * to them -- gradient norm and clipping, the embedding and its gradient, and
+ * the 8-bit block-scaled matrix product -- as sm_103a CUDA kernels.  Several data-parallel
  * ranks are simulated as slices of one device allocation: the all-to-all of
  * the real system becomes the address arithmetic by which each reducing
  * kernel reads its chunks.
@@ -29,9 +31,11 @@
  *   - Kernels launch on the calling thread's current device: the pointers
  *     and the stream must belong to it.
  *   - bf16 values are passed as uint16_t bit patterns.
- *   - Every device pointer must be 16-byte aligned (WC_EALIGN otherwise).
+ *   - Every device pointer must be 16-byte aligned (WC_EALIGN otherwise), the
+ *     addresses in a wc_span excepted.
  *   - Buffers must not overlap unless an entry point says so.
- *   - Inputs must be finite (not checked).
+ *   - Inputs must be finite (not checked) unless an entry point says what
+ *     infinities and NaN do.
  *   - Return value: WC_OK, or a negative WC_E* code with nothing launched
  *     (argument errors) or with the launch failed (WC_ECUDA).  The message
  *     of the calling thread's last failure is returned by wc_last_error().
@@ -39,7 +43,8 @@
  *
  * Arithmetic (shared with the reference definitions): IEEE binary32 with one
  * rounding per operation (no contraction into fused multiply-adds, no flush
- * to zero); bf16 results are rounded to nearest even unless stated.
+ * to zero); bf16 results are rounded to nearest even unless stated.  The sums
+ * of wc_grad_norm, wc_grad_clip and wc_fp8_matmul use fused multiply-adds.
  */
 #ifndef WC_H
 #define WC_H
@@ -63,9 +68,13 @@ extern "C" {
 #define WC_ERANGE (-3)   /* a size exceeds what the kernel indexes */
 #define WC_ECUDA (-4)    /* the kernel launch failed; see wc_last_error() */
 
-/* output element types for the reductions */
+/* floating-point element types */
 #define WC_F32 0
 #define WC_BF16 1
+
+/* integer types of token ids */
+#define WC_I32 0
+#define WC_I64 1
 
 /*
  * wc_ef_quant_int4 -- error-feedback compensation and int4 quantization of
@@ -342,6 +351,129 @@ WC_API int wc_qwz_dequant_int8(const int8_t *codes, const float *scales,
  */
 WC_API int wc_sr_accumulate_bf16(uint16_t *dst, uint16_t *src, int64_t n,
                                  uint32_t seed, uint32_t step, void *stream);
+
+/*
+ * wc_grad_norm, wc_grad_clip -- the global norm of a list of gradient tensors,
+ * and clipping by it: what a training step does with its reduced shards
+ * before the update.
+ *   norm = sqrt(sum over every value x of every tensor of x^2)
+ *   coef = min(1, max_norm / (norm + eps)),  out = coef * x  (one rounding, to
+ *          the output's type)
+ * The sum of squares is as exact as in fp64, in a fixed order (the same bits
+ * every run), and does not overflow or vanish for finite values.  A norm that
+ * is infinite gives coef 0, one that is not a number gives coef NaN, and the
+ * values follow by the same product (0 * inf is NaN): look at stats before the
+ * update.
+ * spans, dst : HOST arrays of count tensors; only the addresses in them are
+ *              device memory, aligned to their element (2 or 4 bytes; any
+ *              offset into a flat buffer will do).  The arrays may be freed
+ *              when the call returns.  dst == NULL clips in place; in place,
+ *              coef 1 writes nothing.  Otherwise dst[i] has as many values as
+ *              spans[i], in either type, and receives coef * x whatever coef
+ *              is.  No written tensor may overlap another one.
+ * stats      : fp32, written: [0] norm and, for wc_grad_clip, [1] coef.
+ * workspace  : wc_grad_norm_workspace(count) bytes; needs no initial value.
+ * Requires count >= 0, max_norm >= 0 (infinity allowed), eps >= 0 and finite,
+ * each n in [0, 2^40).  stats is written for an empty list too (norm 0).
+ * At most two launches per 1024 tensors (and one more for wc_grad_norm).
+ */
+typedef struct {
+    void *data;     /* device address of the first value (or NULL if n is 0) */
+    int64_t n;      /* values, consecutive */
+    int32_t dtype;  /* WC_F32 or WC_BF16 */
+    int32_t pad;    /* 0 */
+} wc_span;
+WC_API int64_t wc_grad_norm_workspace(int count);
+WC_API int wc_grad_norm(const wc_span *spans, int count, float *stats, void *workspace,
+                        int64_t workspace_bytes, void *stream);
+WC_API int wc_grad_clip(const wc_span *spans, const wc_span *dst, int count, double max_norm,
+                        double eps, float *stats, void *workspace, int64_t workspace_bytes,
+                        void *stream);
+
+/*
+ * wc_embedding -- embedding lookup with scaling:
+ *   out[t][c] = scale * table[ids[t] - first][c]  (fp32, rounded once to the
+ *               type), and 0 where ids[t] is outside [first, first + V)
+ * so that negative ids are padding, and a table that holds rows [first,
+ * first + V) of a vocabulary split over ranks contributes its own tokens.
+ * table : [V][ld_table], out : [n][ld_out], both of `dtype`; rows of D values.
+ * ids   : [n] of `id_type` (WC_I32 or WC_I64).
+ * Requires n < 2^31, 0 <= V < 2^31 - 1, D < 2^31, n * D < 2^40, ld_table >= D,
+ * ld_out >= D, 0 <= first < 2^62.
+ */
+WC_API int wc_embedding(const void *table, int dtype, int64_t ld_table, const void *ids,
+                        int id_type, int64_t n, int64_t first, int64_t V, int64_t D, float scale,
+                        void *out, int64_t ld_out, void *stream);
+
+/*
+ * wc_embedding_grad -- the gradient of wc_embedding with respect to its table:
+ *   dtable[v][c] = scale * (sum over the t with ids[t] - first = v, of dy[t][c])
+ * summed in fp32 in an order that the sizes and ids fix (within a stretch of
+ * tokens, t ascending), rounded once to dtable's type.  accumulate != 0 adds
+ * to what dtable holds, and leaves rows without a token alone; otherwise the
+ * whole table is written, zeros included.
+ * dy : [n][ld_dy] of dy_dtype.  dtable : [V][ld_out] of out_dtype.
+ * workspace : wc_embedding_grad_workspace(n, V, D) bytes, no initial value.
+ * Requires the sizes of wc_embedding.  Three launches.
+ */
+WC_API int64_t wc_embedding_grad_workspace(int64_t n, int64_t V, int64_t D);
+WC_API int wc_embedding_grad(const void *dy, int dy_dtype, int64_t ld_dy, const void *ids,
+                             int id_type, int64_t n, int64_t first, int64_t V, int64_t D,
+                             float scale, int accumulate, void *dtable, int out_dtype,
+                             int64_t ld_out, void *workspace, int64_t workspace_bytes,
+                             void *stream);
+
+/*
+ * wc_fp8_quant -- quantization to 8-bit floating point (e4m3, largest value
+ * 448) with one fp32 scale per block of 128 values along the axis that a
+ * product sums over.  Per block, m = max |x|:
+ *   m < 448 * 2^-126            : scale 0, codes 0
+ *   m infinite or not a number  : scale NaN, codes 0 (so that every sum the
+ *                                 block enters is NaN)
+ *   else scale = m / 448, code = e4m3(x * fl(448 / m)), ties to even
+ * x : [rows][ld] of `dtype`, read once.
+ * q, s   : codes [rows][ld_q] and scales [ceil(cols/128)][ld_s] of blocks of
+ *          128 columns, one scale per row and block; s[b][r].  Or both NULL.
+ * qt, st : the same of the transposed matrix: codes [cols][ld_qt] and scales
+ *          [ceil(rows/128)][ld_st] of blocks of 128 rows; st[b][c].  Or NULL.
+ * square != 0 : one scale per 128 x 128 instead (weights): s[b][r/128] and
+ *          st[b][c/128], and the same codes in both layouts.
+ * Codes between a row's end and the next multiple of 16 are written as 0.
+ * Requires rows, cols <= 8388480, ld >= cols, ld_q and ld_qt
+ * multiples of 16 that hold a row, ld_s and ld_st that hold a block's scales.
+ */
+WC_API int wc_fp8_quant(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                        int square, uint8_t *q, int64_t ld_q, float *s, int64_t ld_s, uint8_t *qt,
+                        int64_t ld_qt, float *st, int64_t ld_st, void *stream);
+
+/*
+ * wc_fp8_matmul -- product of two such operands, out = A B^T:
+ *   out[m][n] = sum over blocks b of sa[b][m] * sb[b][n] *
+ *               (sum over the block's k of A[m][k] * B[n][k])
+ * each block's sum on the tensor cores, all else in fp32, rounded once to
+ * out's type; accumulate != 0 adds to what out holds (out's own value, widened,
+ * plus the fp32 sum, rounded once).
+ * a, b : codes [M][lda], [N][ldb], multiples of 16 bytes per row; values past
+ *        column K are not read.
+ * sa, sb : scales [ceil(K/128)][ldsa], one per row (a_rows_per_scale 1) or per
+ *        128 rows (128); the same for b.
+ * out  : [M][ld_out] of out_dtype.
+ * Requires M, N, K < 2^31, M * N < 2^44, lda, ldb >= K, ld_out >= N, and ldsa,
+ * ldsb that hold a block's scales.  K = 0 writes zeros (or adds none).
+ */
+WC_API int wc_fp8_matmul(const uint8_t *a, int64_t lda, const float *sa, int64_t ldsa,
+                         int a_rows_per_scale, const uint8_t *b, int64_t ldb, const float *sb,
+                         int64_t ldsb, int b_rows_per_scale, int64_t M, int64_t N, int64_t K,
+                         void *out, int out_dtype, int64_t ld_out, int accumulate, void *stream);
+
+/*
+ * wc_wait_timeouts -- a debugging aid: waits inside wc_fp8_matmul's kernels
+ * that were given up after about two seconds, since the library was loaded or
+ * last reset (reset != 0).  0 in every run whose launches were complete; a
+ * launch that counted here has left its output unfinished.  Reads device
+ * memory synchronously: synchronize the streams it should cover first.
+ */
+WC_API int wc_wait_timeouts(int reset);
 
 /*
  * wc_checked_violations -- a debugging aid with no counterpart on the pages.

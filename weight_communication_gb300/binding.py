@@ -18,14 +18,25 @@ from . import build as _build
 
 WC_OK, WC_EINVAL, WC_EALIGN, WC_ERANGE, WC_ECUDA = 0, -1, -2, -3, -4
 WC_F32, WC_BF16 = 0, 1
+WC_I32, WC_I64 = 0, 1
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I = ctypes.c_int
 _F = ctypes.c_float
 _U32 = ctypes.c_uint32
+_D = ctypes.c_double
 
-# name -> argtypes (all return int except the two informational calls)
+
+class WcSpan(ctypes.Structure):
+    """wc_span: one tensor of a list."""
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("pad", ctypes.c_int32)]
+
+
+_SPANS = ctypes.POINTER(WcSpan)
+
+# name -> argtypes (all return int except those in RESTYPES)
 SIGNATURES = {
     "wc_ef_quant_int4": [_P, _P, _P, _P, _I64, _I, _I, _I, _F, _F, _P],
     "wc_dequant_reduce": [_P, _P, _I64, _I, _I, _I, _F, _P, _I, _P],
@@ -44,10 +55,23 @@ SIGNATURES = {
     "wc_qwz_quant_replica_int8": [_P, _P, _P, _P, _I64, _I, _P],
     "wc_qwz_dequant_int8": [_P, _P, _P, _I64, _I, _P],
     "wc_sr_accumulate_bf16": [_P, _P, _I64, _U32, _U32, _P],
+    "wc_grad_norm_workspace": [_I],
+    "wc_grad_norm": [_SPANS, _I, _P, _P, _I64, _P],
+    "wc_grad_clip": [_SPANS, _SPANS, _I, _D, _D, _P, _P, _I64, _P],
+    "wc_embedding": [_P, _I, _I64, _P, _I, _I64, _I64, _I64, _I64, _F, _P, _I64, _P],
+    "wc_embedding_grad_workspace": [_I64, _I64, _I64],
+    "wc_embedding_grad": [_P, _I, _I64, _P, _I, _I64, _I64, _I64, _I64, _F, _I, _P, _I, _I64, _P,
+                          _I64, _P],
+    "wc_fp8_quant": [_P, _I, _I64, _I64, _I64, _I, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P],
+    "wc_fp8_matmul": [_P, _I64, _P, _I64, _I, _P, _I64, _P, _I64, _I, _I64, _I64, _I64, _P, _I,
+                      _I64, _I, _P],
+    "wc_wait_timeouts": [_I],
     "wc_checked_violations": [_I],
     "wc_last_error": [],
     "wc_version": [],
 }
+RESTYPES = {"wc_last_error": ctypes.c_char_p, "wc_grad_norm_workspace": _I64,
+            "wc_embedding_grad_workspace": _I64}
 
 
 class WcError(RuntimeError):
@@ -79,7 +103,7 @@ def load(path: str | Path | None = None) -> ctypes.CDLL:
     for name, args in SIGNATURES.items():
         fn = getattr(lib, name)
         fn.argtypes = args
-        fn.restype = ctypes.c_char_p if name == "wc_last_error" else ctypes.c_int
+        fn.restype = RESTYPES.get(name, ctypes.c_int)
     if path is None:
         _lib = lib
     return lib
@@ -105,6 +129,16 @@ def checked_violations(reset: bool = False, probe: bool = False) -> int:
                                    (WC_CHECK_PROBE if probe else 0))
     if rc < 0:
         raise WcError("wc_checked_violations", rc, lib.wc_last_error().decode())
+    return rc
+
+
+def wait_timeouts(reset: bool = False) -> int:
+    """wc_wait_timeouts: waits of the product's kernels that were given up
+    (synchronize first); 0 unless a launch went wrong."""
+    lib = load()
+    rc = lib.wc_wait_timeouts(1 if reset else 0)
+    if rc < 0:
+        raise WcError("wc_wait_timeouts", rc, lib.wc_last_error().decode())
     return rc
 
 
@@ -324,3 +358,181 @@ def sr_accumulate_bf16(dst: torch.Tensor, src: torch.Tensor, seed: int, step: in
     _call(d, "wc_sr_accumulate_bf16", _dev(dst, "dst", torch.bfloat16, n, d),
           _dev(src, "src", torch.bfloat16, n, d), n, seed & 0xFFFFFFFF, step & 0xFFFFFFFF,
           _stream(dst, stream))
+
+
+def _float_type(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.float32:
+        return WC_F32
+    if t.dtype == torch.bfloat16:
+        return WC_BF16
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, device=None):
+    """Pointer and row stride of a CUDA matrix [rows, >= cols] whose rows are
+    consecutive values."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have consecutive values in a row")
+    ld = t.stride(0) if rows > 1 else t.shape[1]
+    if ld < t.shape[1]:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return ctypes.c_void_p(t.data_ptr()), ld
+
+
+def spans(tensors, name: str = "tensors"):
+    """The wc_span array of a list of dense CUDA tensors on one GPU, with that
+    GPU (None for an empty list).  It holds addresses: keep the tensors."""
+    arr = (WcSpan * max(1, len(tensors)))()
+    device = None
+    for i, t in enumerate(tensors):
+        if not t.is_cuda:
+            raise ValueError(f"{name}[{i}] must be a CUDA tensor")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{name}[{i}] is on {t.device}, expected {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous")
+        arr[i] = WcSpan(t.data_ptr() if t.numel() else None, t.numel(),
+                        _float_type(t, f"{name}[{i}]"), 0)
+    return arr, device
+
+
+def grad_norm_workspace(count: int) -> int:
+    """wc_grad_norm_workspace: bytes for a list of count tensors."""
+    return load().wc_grad_norm_workspace(count)
+
+
+def grad_norm(span_array, count: int, stats: torch.Tensor, workspace: torch.Tensor,
+              stream=None) -> None:
+    """wc_grad_norm: stats fp32 [1] <- the norm of the tensors in span_array
+    (see spans); workspace uint8."""
+    d = stats.device
+    _call(d, "wc_grad_norm", span_array, count, _dev(stats, "stats", torch.float32, 1, d),
+          _dev(workspace, "workspace", torch.uint8, workspace.numel(), d), workspace.numel(),
+          _stream(stats, stream))
+
+
+def grad_clip(span_array, dst_array, count: int, max_norm: float, eps: float,
+              stats: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """wc_grad_clip: stats fp32 [2] <- norm and coefficient; the scaled values
+    go to dst_array's tensors, or in place if that is None."""
+    d = stats.device
+    _call(d, "wc_grad_clip", span_array, dst_array, count, max_norm, eps,
+          _dev(stats, "stats", torch.float32, 2, d),
+          _dev(workspace, "workspace", torch.uint8, workspace.numel(), d), workspace.numel(),
+          _stream(stats, stream))
+
+
+def _ids(ids: torch.Tensor, device) -> tuple:
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
+    return (_dev(ids, "ids", ids.dtype, ids.numel(), device),
+            WC_I64 if ids.dtype == torch.int64 else WC_I32)
+
+
+def embedding(table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, scale: float = 1.0,
+              first_row: int = 0, stream=None) -> None:
+    """wc_embedding: out [n, D] <- scale * table[ids - first_row], zero for
+    ids outside the table's rows [first_row, first_row + V)."""
+    d = table.device
+    if table.dim() != 2:
+        raise ValueError(f"table must be a matrix, got shape {tuple(table.shape)}")
+    V, D = table.shape
+    tp, ld_table = _matrix(table, "table", V, D, d)
+    ip, it = _ids(ids, d)
+    if out.dtype != table.dtype:
+        raise TypeError(f"out must be {table.dtype}, got {out.dtype}")
+    op, ld_out = _matrix(out, "out", ids.numel(), D, d)
+    _call(d, "wc_embedding", tp, _float_type(table, "table"), max(ld_table, D), ip, it,
+          ids.numel(), first_row, V, D, scale, op, max(ld_out, D), _stream(table, stream))
+
+
+def embedding_grad_workspace(n: int, V: int, D: int) -> int:
+    """wc_embedding_grad_workspace: bytes."""
+    lib = load()
+    rc = lib.wc_embedding_grad_workspace(n, V, D)
+    if rc < 0:
+        raise WcError("wc_embedding_grad_workspace", rc, lib.wc_last_error().decode())
+    return rc
+
+
+def embedding_grad(dy: torch.Tensor, ids: torch.Tensor, dtable: torch.Tensor,
+                   workspace: torch.Tensor, scale: float = 1.0, first_row: int = 0,
+                   accumulate: bool = False, stream=None) -> None:
+    """wc_embedding_grad: dtable [V, D] <- (or +=) scale * the sum of dy's rows
+    over the tokens of each row; workspace uint8."""
+    d = dy.device
+    if dtable.dim() != 2:
+        raise ValueError(f"dtable must be a matrix, got shape {tuple(dtable.shape)}")
+    V, D = dtable.shape
+    n = ids.numel()
+    yp, ld_dy = _matrix(dy, "dy", n, D, d)
+    if dy.shape[1] != D:
+        raise ValueError(f"dy has {dy.shape[1]} columns, dtable {D}")
+    ip, it = _ids(ids, d)
+    op, ld_out = _matrix(dtable, "dtable", V, D, d)
+    _call(d, "wc_embedding_grad", yp, _float_type(dy, "dy"), max(ld_dy, D), ip, it, n, first_row,
+          V, D, scale, 1 if accumulate else 0, op, _float_type(dtable, "dtable"), max(ld_out, D),
+          _dev(workspace, "workspace", torch.uint8, workspace.numel(), d), workspace.numel(),
+          _stream(dy, stream))
+
+
+def _fp8_part(codes, scales, name: str, rows: int, cols: int, square: bool, device,
+              written: bool):
+    """Pointers and strides of codes [rows, >= cols] and scales
+    [ceil(cols/128), >= rows or ceil(rows/128)], or NULLs.  Written codes need
+    room for their rows' padding to 16 bytes."""
+    if (codes is None) != (scales is None):
+        raise ValueError(f"{name}: codes and scales must both be given or both be None")
+    if codes is None:
+        return None, 0, None, 0
+    if codes.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"{name} codes must be float8_e4m3fn, got {codes.dtype}")
+    if scales.dtype != torch.float32:
+        raise TypeError(f"{name} scales must be float32, got {scales.dtype}")
+    per = -(-rows // 128) if square else rows
+    padded = -(-cols // 16) * 16
+    cp, ld = _matrix(codes, f"{name} codes", rows, padded if written else cols, device)
+    if rows <= 1 or codes.shape[1] == 0:
+        ld = padded  # there is no second row to be apart from
+    sp, lds = _matrix(scales, f"{name} scales", -(-cols // 128), per, device)
+    return cp, ld, sp, lds
+
+
+def fp8_quant(x: torch.Tensor, codes: torch.Tensor | None, scales: torch.Tensor | None,
+              codes_t: torch.Tensor | None = None, scales_t: torch.Tensor | None = None,
+              square: bool = False, stream=None) -> None:
+    """wc_fp8_quant: x [rows, cols] to e4m3 codes and scales by blocks of 128
+    along the columns (codes, scales), along the rows of the transposed matrix
+    (codes_t, scales_t), or both; square: one scale per 128 x 128."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be a matrix, got shape {tuple(x.shape)}")
+    d = x.device
+    rows, cols = x.shape
+    xp, ld = _matrix(x, "x", rows, cols, d)
+    q, ldq, s, lds = _fp8_part(codes, scales, "row", rows, cols, square, d, True)
+    qt, ldqt, st, ldst = _fp8_part(codes_t, scales_t, "transposed", cols, rows, square, d, True)
+    _call(d, "wc_fp8_quant", xp, _float_type(x, "x"), rows, cols, max(ld, cols), 1 if square else 0,
+          q, ldq, s, lds, qt, ldqt, st, ldst, _stream(x, stream))
+
+
+def fp8_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, a_rows_per_scale: int,
+               b_codes: torch.Tensor, b_scales: torch.Tensor, b_rows_per_scale: int, K: int,
+               out: torch.Tensor, accumulate: bool = False, stream=None) -> None:
+    """wc_fp8_matmul: out [M, N] <- (or +=) A B^T of two quantized operands
+    with K columns each."""
+    d = a_codes.device
+    M, N = a_codes.shape[0], b_codes.shape[0]
+    ap, lda, sap, ldsa = _fp8_part(a_codes, a_scales, "a", M, K, a_rows_per_scale == 128, d, False)
+    bp, ldb, sbp, ldsb = _fp8_part(b_codes, b_scales, "b", N, K, b_rows_per_scale == 128, d, False)
+    op, ld_out = _matrix(out, "out", M, N, d)
+    _call(d, "wc_fp8_matmul", ap, lda, sap, ldsa, a_rows_per_scale, bp, ldb, sbp, ldsb,
+          b_rows_per_scale, M, N, K, op, _float_type(out, "out"), max(ld_out, N),
+          1 if accumulate else 0, _stream(a_codes, stream))

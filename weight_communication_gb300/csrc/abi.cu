@@ -1,8 +1,14 @@
 // abi.cu -- the extern "C" entry points declared in include/wc.h: argument
-// validation on the host, then exactly one kernel launch per call.
+// validation on the host, then one kernel launch per call (the gradient norm,
+// clipping and the embedding's gradient: two or three, back to back).
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
+
+#include <algorithm>
+#include <new>
+#include <vector>
 
 #include "../../include/wc.h"
 #include "wc_internal.h"
@@ -363,6 +369,313 @@ WC_API int wc_sr_accumulate_bf16(uint16_t *dst, uint16_t *src, int64_t n, uint32
     return from_cuda(wc::launch_sr_accumulate(dst, src, uint32_t(n), seed, step,
                                               static_cast<cudaStream_t>(stream)),
                      fn);
+}
+
+namespace {
+
+bool float_type(int t) { return t == WC_F32 || t == WC_BF16; }
+
+struct Extent {
+    uintptr_t begin, end;
+    bool written;
+};
+
+// Checks one list of tensors and appends them (dst: where the values go).
+int span_list(const char *fn, const char *name, const wc_span *spans, int count) {
+    for (int i = 0; i < count; ++i) {
+        const wc_span &s = spans[i];
+        if (!float_type(s.dtype))
+            return fail(WC_EINVAL, "%s: %s[%d] has dtype %d, neither WC_F32 nor WC_BF16", fn, name, i,
+                        s.dtype);
+        if (s.n < 0) return fail(WC_EINVAL, "%s: %s[%d] has n = %lld", fn, name, i, (long long)s.n);
+        if (s.n >= (int64_t(1) << 40)) return fail(WC_ERANGE, "%s: %s[%d] has 2^40 values or more", fn, name, i);
+        if (s.n > 0 && s.data == nullptr) return fail(WC_EINVAL, "%s: %s[%d] is NULL", fn, name, i);
+        const uintptr_t size = s.dtype == WC_BF16 ? 2 : 4;
+        if (reinterpret_cast<uintptr_t>(s.data) % size)
+            return fail(WC_EALIGN, "%s: %s[%d] is not aligned to its %d-byte values", fn, name, i, int(size));
+    }
+    return WC_OK;
+}
+
+// No written tensor may share memory with another tensor of the call.
+int disjoint(const char *fn, const std::vector<Extent> &extents) {
+    bool ordered = true;  // usually the list is in address order already
+    for (size_t i = 1; ordered && i < extents.size(); ++i)
+        ordered = extents[i - 1].begin <= extents[i].begin;
+    const std::vector<Extent> *v = &extents;
+    std::vector<Extent> sorted;
+    if (!ordered) {
+        sorted = extents;
+        std::sort(sorted.begin(), sorted.end(),
+                  [](const Extent &a, const Extent &b) { return a.begin < b.begin; });
+        v = &sorted;
+    }
+    uintptr_t read_end = 0, write_end = 0;
+    for (const Extent &e : *v) {
+        if (e.begin < write_end || (e.written && e.begin < read_end))
+            return fail(WC_EINVAL, "%s: a written tensor overlaps another one", fn);
+        uintptr_t &end = e.written ? write_end : read_end;
+        end = std::max(end, e.end);
+    }
+    return WC_OK;
+}
+
+int grad_call(const char *fn, const wc_span *spans, const wc_span *dst, int count, bool clip,
+              double max_norm, double eps, float *stats, void *workspace, int64_t workspace_bytes,
+              void *stream) {
+    if (count < 0) return fail(WC_EINVAL, "%s: count = %d is negative", fn, count);
+    if (count > 0 && spans == nullptr) return fail(WC_EINVAL, "%s: spans is NULL", fn);
+    if (clip && !(max_norm >= 0.0)) return fail(WC_EINVAL, "%s: max_norm = %g must be at least 0", fn, max_norm);
+    if (clip && !(eps >= 0.0 && eps < HUGE_VAL))
+        return fail(WC_EINVAL, "%s: eps = %g must be finite and at least 0", fn, eps);
+    int rc = span_list(fn, "spans", spans, count);
+    if (rc == WC_OK && dst != nullptr) rc = span_list(fn, "dst", dst, count);
+    if (rc != WC_OK) return rc;
+    WC_REQUIRE_PTR(fn, stats);
+    WC_REQUIRE_PTR(fn, workspace);
+    if (workspace_bytes < wc_grad_norm_workspace(count))
+        return fail(WC_EINVAL, "%s: workspace of %lld bytes, %lld are needed", fn,
+                    (long long)workspace_bytes, (long long)wc_grad_norm_workspace(count));
+    try {
+        std::vector<wc::GradSpan> list;
+        list.reserve(size_t(count));
+        std::vector<Extent> extents;
+        if (clip) extents.reserve(size_t(count) * (dst ? 2 : 1));
+        int64_t total = 0;
+        for (int i = 0; i < count; ++i) {
+            const wc_span &s = spans[i];
+            const wc_span &d = dst ? dst[i] : s;
+            if (d.n != s.n)
+                return fail(WC_EINVAL, "%s: dst[%d] has %lld values, spans[%d] %lld", fn, i,
+                            (long long)d.n, i, (long long)s.n);
+            list.push_back({s.data, d.data, s.n, s.dtype == WC_BF16, d.dtype == WC_BF16});
+            total += s.n;
+            if (total >= (int64_t(1) << 40)) return fail(WC_ERANGE, "%s: 2^40 values or more in all", fn);
+            if (!clip || s.n == 0) continue;
+            const uintptr_t a = reinterpret_cast<uintptr_t>(s.data), b = reinterpret_cast<uintptr_t>(d.data);
+            extents.push_back({a, a + uintptr_t(s.n) * (s.dtype == WC_BF16 ? 2 : 4), dst == nullptr});
+            if (dst) extents.push_back({b, b + uintptr_t(s.n) * (d.dtype == WC_BF16 ? 2 : 4), true});
+        }
+        if (clip && (rc = disjoint(fn, extents)) != WC_OK) return rc;
+        return from_cuda(wc::launch_grad_norm(list.data(), count, static_cast<double *>(workspace),
+                                              clip, dst == nullptr, max_norm, eps, stats,
+                                              static_cast<cudaStream_t>(stream)),
+                         fn);
+    } catch (const std::bad_alloc &) {
+        return fail(WC_EINVAL, "%s: no host memory for a list of %d tensors", fn, count);
+    }
+}
+
+// Sizes shared by the embedding's two directions.
+int embedding_sizes(const char *fn, int id_type, int64_t n, int64_t first, int64_t V, int64_t D) {
+    if (id_type != WC_I32 && id_type != WC_I64)
+        return fail(WC_EINVAL, "%s: id_type %d is neither WC_I32 nor WC_I64", fn, id_type);
+    if (n < 0 || V < 0 || D < 0)
+        return fail(WC_EINVAL, "%s: n = %lld, V = %lld, D = %lld must not be negative", fn, (long long)n,
+                    (long long)V, (long long)D);
+    if (first < 0 || first >= (int64_t(1) << 62))
+        return fail(WC_EINVAL, "%s: first = %lld must be in [0, 2^62)", fn, (long long)first);
+    const int64_t limit = int64_t(1) << 31;
+    if (n >= limit || V >= limit - 1 || D >= limit) return fail(WC_ERANGE, "%s: n, V or D reaches 2^31", fn);
+    if (D > 0 && n >= (int64_t(1) << 40) / D) return fail(WC_ERANGE, "%s: n * D reaches 2^40", fn);
+    return WC_OK;
+}
+
+int64_t blocks128(int64_t n) { return (n + 127) / 128; }
+
+}  // namespace
+
+WC_API int64_t wc_grad_norm_workspace(int count) {
+    const int64_t launches = count > 0 ? (int64_t(count) + wc::kGradSpansPerLaunch - 1) / wc::kGradSpansPerLaunch : 1;
+    return launches * wc::kGradPartialsPerLaunch * int64_t(sizeof(double));
+}
+
+WC_API int wc_grad_norm(const wc_span *spans, int count, float *stats, void *workspace,
+                        int64_t workspace_bytes, void *stream) {
+    return grad_call("wc_grad_norm", spans, nullptr, count, false, 0.0, 0.0, stats, workspace,
+                     workspace_bytes, stream);
+}
+
+WC_API int wc_grad_clip(const wc_span *spans, const wc_span *dst, int count, double max_norm,
+                        double eps, float *stats, void *workspace, int64_t workspace_bytes,
+                        void *stream) {
+    return grad_call("wc_grad_clip", spans, dst, count, true, max_norm, eps, stats, workspace,
+                     workspace_bytes, stream);
+}
+
+WC_API int wc_embedding(const void *table, int dtype, int64_t ld_table, const void *ids,
+                        int id_type, int64_t n, int64_t first, int64_t V, int64_t D, float scale,
+                        void *out, int64_t ld_out, void *stream) {
+    static const char *fn = "wc_embedding";
+    int rc = embedding_sizes(fn, id_type, n, first, V, D);
+    if (rc != WC_OK) return rc;
+    if (!float_type(dtype)) return fail(WC_EINVAL, "%s: dtype %d is neither WC_F32 nor WC_BF16", fn, dtype);
+    if (ld_table < D || ld_out < D)
+        return fail(WC_EINVAL, "%s: ld_table = %lld, ld_out = %lld are below D = %lld", fn,
+                    (long long)ld_table, (long long)ld_out, (long long)D);
+    if (n == 0 || D == 0) return WC_OK;
+    if (V > 0) WC_REQUIRE_PTR(fn, table);
+    WC_REQUIRE_PTR(fn, ids);
+    WC_REQUIRE_PTR(fn, out);
+    return from_cuda(wc::launch_embedding(table, dtype == WC_BF16, ld_table, ids, id_type == WC_I64,
+                                          n, first, V, D, scale, out, ld_out,
+                                          static_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+WC_API int64_t wc_embedding_grad_workspace(int64_t n, int64_t V, int64_t D) {
+    static const char *fn = "wc_embedding_grad_workspace";
+    const int rc = embedding_sizes(fn, WC_I32, n, 0, V, D);
+    if (rc != WC_OK) return rc;
+    if (D == 0) return 0;
+    wc::EmbeddingGrad a = {};
+    a.n = n;
+    a.V = V;
+    a.D = D;
+    return wc::embedding_grad_workspace(a);
+}
+
+WC_API int wc_embedding_grad(const void *dy, int dy_dtype, int64_t ld_dy, const void *ids,
+                             int id_type, int64_t n, int64_t first, int64_t V, int64_t D,
+                             float scale, int accumulate, void *dtable, int out_dtype,
+                             int64_t ld_out, void *workspace, int64_t workspace_bytes,
+                             void *stream) {
+    static const char *fn = "wc_embedding_grad";
+    int rc = embedding_sizes(fn, id_type, n, first, V, D);
+    if (rc != WC_OK) return rc;
+    if (!float_type(dy_dtype) || !float_type(out_dtype))
+        return fail(WC_EINVAL, "%s: dy_dtype %d or out_dtype %d is neither WC_F32 nor WC_BF16", fn,
+                    dy_dtype, out_dtype);
+    if (ld_dy < D || ld_out < D)
+        return fail(WC_EINVAL, "%s: ld_dy = %lld, ld_out = %lld are below D = %lld", fn,
+                    (long long)ld_dy, (long long)ld_out, (long long)D);
+    if (V == 0 || D == 0 || (n == 0 && accumulate)) return WC_OK;
+    if (n > 0) {
+        WC_REQUIRE_PTR(fn, dy);
+        WC_REQUIRE_PTR(fn, ids);
+    }
+    WC_REQUIRE_PTR(fn, dtable);
+    WC_REQUIRE_PTR(fn, workspace);
+    const int64_t need = wc_embedding_grad_workspace(n, V, D);
+    if (workspace_bytes < need)
+        return fail(WC_EINVAL, "%s: workspace of %lld bytes, %lld are needed", fn,
+                    (long long)workspace_bytes, (long long)need);
+    wc::EmbeddingGrad a;
+    a.dy = dy;
+    a.dy_bf16 = dy_dtype == WC_BF16;
+    a.ld_dy = ld_dy;
+    a.ids = ids;
+    a.wide = id_type == WC_I64;
+    a.n = n;
+    a.first = first;
+    a.V = V;
+    a.D = D;
+    a.scale = scale;
+    a.accumulate = accumulate != 0;
+    a.dtable = dtable;
+    a.out_bf16 = out_dtype == WC_BF16;
+    a.ld_out = ld_out;
+    a.workspace = workspace;
+    return from_cuda(wc::launch_embedding_grad(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+WC_API int wc_fp8_quant(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                        int square, uint8_t *q, int64_t ld_q, float *s, int64_t ld_s, uint8_t *qt,
+                        int64_t ld_qt, float *st, int64_t ld_st, void *stream) {
+    static const char *fn = "wc_fp8_quant";
+    if (!float_type(dtype)) return fail(WC_EINVAL, "%s: dtype %d is neither WC_F32 nor WC_BF16", fn, dtype);
+    if (rows < 0 || cols < 0)
+        return fail(WC_EINVAL, "%s: rows = %lld, cols = %lld must not be negative", fn, (long long)rows, (long long)cols);
+    if (rows > 65535 * 128 || cols > 65535 * 128)
+        return fail(WC_ERANGE, "%s: rows or cols exceeds 8388480", fn);
+    if (ld < cols) return fail(WC_EINVAL, "%s: ld = %lld is below cols = %lld", fn, (long long)ld, (long long)cols);
+    if ((q == nullptr) != (s == nullptr) || (qt == nullptr) != (st == nullptr))
+        return fail(WC_EINVAL, "%s: codes and scales must both be given or both be NULL", fn);
+    if (q != nullptr && (ld_q % 16 || ld_q < cols))
+        return fail(WC_EINVAL, "%s: ld_q = %lld must be a multiple of 16 and at least cols", fn, (long long)ld_q);
+    if (qt != nullptr && (ld_qt % 16 || ld_qt < rows))
+        return fail(WC_EINVAL, "%s: ld_qt = %lld must be a multiple of 16 and at least rows", fn, (long long)ld_qt);
+    if (q != nullptr && ld_s < (square ? blocks128(rows) : rows))
+        return fail(WC_EINVAL, "%s: ld_s = %lld does not hold a block's scales", fn, (long long)ld_s);
+    if (qt != nullptr && ld_st < (square ? blocks128(cols) : cols))
+        return fail(WC_EINVAL, "%s: ld_st = %lld does not hold a block's scales", fn, (long long)ld_st);
+    if (rows == 0 || cols == 0) return WC_OK;
+    if (q == nullptr && qt == nullptr) return fail(WC_EINVAL, "%s: q and qt are both NULL", fn);
+    WC_REQUIRE_PTR(fn, x);
+    if (q != nullptr && (!aligned16(q) || !aligned16(s)))
+        return fail(WC_EALIGN, "%s: q or s is not 16-byte aligned", fn);
+    if (qt != nullptr && (!aligned16(qt) || !aligned16(st)))
+        return fail(WC_EALIGN, "%s: qt or st is not 16-byte aligned", fn);
+    wc::Fp8Quant a;
+    a.x = x;
+    a.x_bf16 = dtype == WC_BF16;
+    a.rows = rows;
+    a.cols = cols;
+    a.ld = ld;
+    a.square = square != 0;
+    a.q = q;
+    a.ld_q = ld_q;
+    a.s = s;
+    a.ld_s = ld_s;
+    a.qt = qt;
+    a.ld_qt = ld_qt;
+    a.st = st;
+    a.ld_st = ld_st;
+    return from_cuda(wc::launch_fp8_quant(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+WC_API int wc_fp8_matmul(const uint8_t *a, int64_t lda, const float *sa, int64_t ldsa,
+                         int a_rows_per_scale, const uint8_t *b, int64_t ldb, const float *sb,
+                         int64_t ldsb, int b_rows_per_scale, int64_t M, int64_t N, int64_t K,
+                         void *out, int out_dtype, int64_t ld_out, int accumulate, void *stream) {
+    static const char *fn = "wc_fp8_matmul";
+    if (M < 0 || N < 0 || K < 0)
+        return fail(WC_EINVAL, "%s: M = %lld, N = %lld, K = %lld must not be negative", fn, (long long)M,
+                    (long long)N, (long long)K);
+    const int64_t limit = int64_t(1) << 31;
+    // (2^31 - 128: the tiles' coordinates are 32-bit and go up to the next 256)
+    if (M > limit - 256 || N > limit - 256 || K > limit - 256)
+        return fail(WC_ERANGE, "%s: M, N or K exceeds 2^31 - 256", fn);
+    if (N > 0 && M >= (int64_t(1) << 44) / N) return fail(WC_ERANGE, "%s: M * N reaches 2^44", fn);
+    if (!float_type(out_dtype))
+        return fail(WC_EINVAL, "%s: out_dtype %d is neither WC_F32 nor WC_BF16", fn, out_dtype);
+    if ((a_rows_per_scale != 1 && a_rows_per_scale != 128) || (b_rows_per_scale != 1 && b_rows_per_scale != 128))
+        return fail(WC_EINVAL, "%s: rows per scale (%d and %d) must be 1 or 128", fn, a_rows_per_scale,
+                    b_rows_per_scale);
+    if (lda % 16 || ldb % 16 || lda < K || ldb < K)
+        return fail(WC_EINVAL, "%s: lda = %lld, ldb = %lld must be multiples of 16 and at least K", fn,
+                    (long long)lda, (long long)ldb);
+    if (ldsa < (a_rows_per_scale == 128 ? blocks128(M) : M) || ldsb < (b_rows_per_scale == 128 ? blocks128(N) : N))
+        return fail(WC_EINVAL, "%s: ldsa = %lld or ldsb = %lld does not hold a block's scales", fn,
+                    (long long)ldsa, (long long)ldsb);
+    if (ld_out < N) return fail(WC_EINVAL, "%s: ld_out = %lld is below N = %lld", fn, (long long)ld_out, (long long)N);
+    if (M == 0 || N == 0) return WC_OK;
+    if (K > 0) {
+        WC_REQUIRE_PTR(fn, a);
+        WC_REQUIRE_PTR(fn, sa);
+        WC_REQUIRE_PTR(fn, b);
+        WC_REQUIRE_PTR(fn, sb);
+    }
+    WC_REQUIRE_PTR(fn, out);
+    wc::Fp8Matmul m;
+    m.a = {a, lda, sa, ldsa, a_rows_per_scale};
+    m.b = {b, ldb, sb, ldsb, b_rows_per_scale};
+    m.M = M;
+    m.N = N;
+    m.K = K;
+    m.out = out;
+    m.out_bf16 = out_dtype == WC_BF16;
+    m.ld_out = ld_out;
+    m.accumulate = accumulate != 0;
+    return from_cuda(wc::launch_fp8_matmul(m, static_cast<cudaStream_t>(stream)), fn);
+}
+
+WC_API int wc_wait_timeouts(int reset) {
+    static const char *fn = "wc_wait_timeouts";
+    unsigned int n = 0;
+    const cudaError_t e = wc::fp8_wait_timeouts(&n, reset != 0);
+    if (e != cudaSuccess) return from_cuda(e, fn);
+    return n > 0x7FFFFFFFu ? 0x7FFFFFFF : int(n);
 }
 
 WC_API int wc_checked_violations(int flags) {

@@ -1,0 +1,606 @@
+// embedding.cu -- embedding lookup with scaling, and its gradient.
+//
+//   out[t]    = scale * table[ids[t] - first]        (zero for ids outside)
+//   dtable[v] = scale * sum over t with ids[t] - first = v, t ascending, of dy[t]
+//
+// ids outside [first, first + V) -- padding, or rows of another rank's shard --
+// read as zero and receive nothing.
+//
+// Lookup: one 16-byte vector per thread and step, four in flight; HBM-bound.
+//
+// Gradient: three kernels, no atomics on global memory, the same bits every
+// run.  (1) sort: each CTA owns a run of table rows, reads every id (they sit
+// in L2) and writes the positions of its rows' tokens, in token order, at
+// their sorted places -- a stable counting sort in one launch, because a CTA
+// learns its place in the output by counting the ids below its rows.
+// (2) sum: the sorted tokens are cut into equal runs, one per worker, so that
+// a row with many tokens (Zipf's law) is spread over many workers; a worker
+// writes the rows that lie inside its run and leaves fp32 partial sums of the
+// at most two rows that cross its ends.  (3) join: adds those partial sums in
+// order.  Bound: HBM, reading dy once and writing the table's gradient once.
+#include "wc_device.cuh"
+#include "wc_internal.h"
+
+namespace wc {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// element access: E values of bf16 or fp32 as one vector
+// ---------------------------------------------------------------------------
+
+template <typename T, int E>
+struct Pack {
+    static constexpr int kBytes = E * int(sizeof(T));
+    static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
+    uint32_t w[kWords];
+};
+
+template <typename T, int E, bool STREAM>
+__device__ __forceinline__ Pack<T, E> load_pack(const T *p) {
+    Pack<T, E> r;
+    constexpr int B = Pack<T, E>::kBytes;
+    if constexpr (B >= 16) {
+#pragma unroll
+        for (int i = 0; i < B / 16; ++i) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(p) + i;
+            const uint4 v = STREAM ? __ldcs(q) : *q;
+            r.w[4 * i] = v.x;
+            r.w[4 * i + 1] = v.y;
+            r.w[4 * i + 2] = v.z;
+            r.w[4 * i + 3] = v.w;
+        }
+    } else if constexpr (B == 8) {
+        const uint2 *q = reinterpret_cast<const uint2 *>(p);
+        const uint2 v = STREAM ? __ldcs(q) : *q;
+        r.w[0] = v.x;
+        r.w[1] = v.y;
+    } else if constexpr (B == 4) {
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
+        r.w[0] = STREAM ? __ldcs(q) : *q;
+    } else {
+        const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+        r.w[0] = STREAM ? __ldcs(q) : *q;
+    }
+    return r;
+}
+
+template <typename T, int E>
+__device__ __forceinline__ void store_pack(T *p, const Pack<T, E> &v) {
+    constexpr int B = Pack<T, E>::kBytes;
+    if constexpr (B >= 16) {
+#pragma unroll
+        for (int i = 0; i < B / 16; ++i)
+            __stcs(reinterpret_cast<uint4 *>(p) + i,
+                   make_uint4(v.w[4 * i], v.w[4 * i + 1], v.w[4 * i + 2], v.w[4 * i + 3]));
+    } else if constexpr (B == 8) {
+        __stcs(reinterpret_cast<uint2 *>(p), make_uint2(v.w[0], v.w[1]));
+    } else if constexpr (B == 4) {
+        __stcs(reinterpret_cast<uint32_t *>(p), v.w[0]);
+    } else {
+        __stcs(reinterpret_cast<uint16_t *>(p), uint16_t(v.w[0]));
+    }
+}
+
+template <typename T, int E>
+__device__ __forceinline__ float pack_value(const Pack<T, E> &v, int e) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(v.w[e]);
+    return __uint_as_float((e & 1) ? (v.w[e / 2] & 0xFFFF0000u) : (v.w[e / 2] << 16));
+}
+
+template <typename T, int E>
+__device__ __forceinline__ Pack<T, E> pack_of(const float x[E]) {
+    Pack<T, E> r;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) r.w[e] = __float_as_uint(x[e]);
+    } else if constexpr (E == 1) {
+        r.w[0] = f32_to_bf16_bits(x[0]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) r.w[e / 2] = f32x2_to_bf16x2_bits(x[e], x[e + 1]);
+    }
+    return r;
+}
+
+// id - first; ids at the far negative end wrap to a row beyond any table.
+__device__ __forceinline__ int64_t relative(int64_t id, int64_t first) {
+    return int64_t(uint64_t(id) - uint64_t(first));
+}
+
+template <typename I>
+__device__ __forceinline__ int64_t row_of(const I *ids, int64_t t, int64_t first, int64_t V) {
+    const int64_t r = relative(ids[t], first);
+    return r >= 0 && r < V ? r : -1;
+}
+
+// ---------------------------------------------------------------------------
+// lookup
+// ---------------------------------------------------------------------------
+
+constexpr int kLookupThreads = 256;
+constexpr int kLookupUnroll = 4;
+
+// vecs: vectors of E values in a row; a CTA covers kLookupThreads *
+// kLookupUnroll consecutive vectors of the [n][vecs] output.
+template <typename T, typename I, int E>
+__global__ void __launch_bounds__(kLookupThreads)
+lookup_kernel(const T *__restrict__ table, int64_t ld_table, const I *__restrict__ ids, int64_t n,
+              int64_t first, int64_t V, uint32_t vecs, float scale, T *__restrict__ out,
+              int64_t ld_out) {
+    const int64_t base = int64_t(blockIdx.x) * (kLookupThreads * kLookupUnroll);
+    const int64_t t0 = base / vecs;
+    const uint32_t v0 = uint32_t(base - t0 * vecs);
+    Pack<T, E> r[kLookupUnroll];
+    int64_t tok[kLookupUnroll], row[kLookupUnroll];
+    uint32_t vec[kLookupUnroll];
+#pragma unroll
+    for (int j = 0; j < kLookupUnroll; ++j) {
+        const uint32_t at = v0 + threadIdx.x + j * kLookupThreads;  // < vecs + 1024
+        const uint32_t dt = at / vecs;
+        tok[j] = t0 + dt;
+        vec[j] = at - dt * vecs;
+        row[j] = tok[j] < n ? row_of(ids, tok[j], first, V) : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kLookupUnroll; ++j) {
+        if (row[j] >= 0) {
+            r[j] = load_pack<T, E, false>(table + row[j] * ld_table + int64_t(vec[j]) * E);
+        } else {
+#pragma unroll
+            for (int w = 0; w < Pack<T, E>::kWords; ++w) r[j].w[w] = 0u;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kLookupUnroll; ++j) {
+        if (tok[j] >= n) continue;
+        if (scale != 1.0f && row[j] >= 0) {
+            float x[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = __fmul_rn(pack_value<T, E>(r[j], e), scale);
+            r[j] = pack_of<T, E>(x);
+        }
+        store_pack<T, E>(out + tok[j] * ld_out + int64_t(vec[j]) * E, r[j]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// gradient (1): stable counting sort of the tokens by row
+// ---------------------------------------------------------------------------
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortPitch = kSortWarps + 1;  // counters of a row; odd, so that a warp's
+                                            // counters of different rows are in different banks
+
+// order[p], rows[p]: token and row at sorted place p.  row_start[v]: first
+// place of row v; row_start[V]: tokens with a row.  CTA b owns rows
+// [b * per_cta, (b + 1) * per_cta).  Dynamic shared memory: per_cta *
+// (kSortPitch + 1) counters.
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads)
+sort_kernel(const I *__restrict__ ids, int32_t n, int64_t first, int32_t V, int32_t per_cta,
+            int32_t *__restrict__ order, int32_t *__restrict__ rows,
+            int32_t *__restrict__ row_start) {
+    extern __shared__ int32_t counters[];
+    __shared__ int32_t warp_total[kSortWarps];
+    __shared__ int32_t below_total;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t lo = int32_t(blockIdx.x) * per_cta;
+    const int32_t hi = min(V, lo + per_cta);
+    const int32_t own = hi - lo;
+    int32_t *base = counters + per_cta * kSortPitch;  // first place of each row
+    for (int i = threadIdx.x; i < per_cta * (kSortPitch + 1); i += kSortThreads) counters[i] = 0;
+    if (threadIdx.x == 0) below_total = 0;
+    __syncthreads();
+
+    // each warp counts its own consecutive stretch of tokens
+    const int32_t stretch = ((n + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+    const int64_t begin = int64_t(stretch) * warp;
+    const int64_t end = begin + stretch < int64_t(n) ? begin + stretch : int64_t(n);
+    int32_t below = 0;
+#pragma unroll 4
+    for (int64_t t = begin + lane; t < end; t += 32) {
+        const int64_t r = relative(ids[t], first);
+        if (r >= lo && r < hi) atomicAdd(&counters[int32_t(r - lo) * kSortPitch + warp], 1);
+        else if (r >= 0 && r < lo) ++below;
+    }
+    below = __reduce_add_sync(kFull, below);
+    if (lane == 0) atomicAdd(&below_total, below);
+    __syncthreads();
+
+    // places: rows in order, and within a row the warps in order
+    for (int32_t r = warp; r < own; r += kSortWarps) {
+        const int32_t c = counters[r * kSortPitch + lane];
+        int32_t inc = c;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int32_t u = __shfl_up_sync(kFull, inc, off);
+            if (lane >= off) inc += u;
+        }
+        counters[r * kSortPitch + lane] = inc - c;
+        if (lane == 31) base[r] = inc;
+    }
+    __syncthreads();
+    int32_t carry = below_total;
+    for (int32_t r0 = 0; r0 < own; r0 += kSortThreads) {
+        const int32_t r = r0 + int32_t(threadIdx.x);
+        const int32_t c = r < own ? base[r] : 0;
+        int32_t inc = c;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int32_t u = __shfl_up_sync(kFull, inc, off);
+            if (lane >= off) inc += u;
+        }
+        if (lane == 31) warp_total[warp] = inc;
+        __syncthreads();
+        int32_t before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+            if (w < warp) before += warp_total[w];
+            all += warp_total[w];
+        }
+        const int32_t at = carry + before + inc - c;
+        if (r < own) {
+            base[r] = at;
+            row_start[lo + r] = at;
+        }
+        carry += all;
+        __syncthreads();
+    }
+    if (hi == V && threadIdx.x == 0) row_start[V] = carry;
+
+    // the same stretch again, in order: equal rows of a step keep lane order
+    for (int64_t t0 = begin; t0 < end; t0 += 32) {
+        const int64_t t = t0 + lane;
+        const int64_t r = t < end ? relative(ids[t], first) : -1;
+        const bool mine = r >= lo && r < hi;
+        const unsigned live = __ballot_sync(kFull, mine);
+        if (mine) {
+            const int32_t k = int32_t(r - lo);
+            const unsigned peers = __match_any_sync(live, k);
+            int32_t *counter = &counters[k * kSortPitch + warp];
+            const int32_t at = base[k] + *counter + __popc(peers & ((1u << lane) - 1u));
+            order[at] = int32_t(t);
+            rows[at] = int32_t(r);
+            __syncwarp(live);
+            if ((peers & ((1u << lane) - 1u)) == 0u) *counter += __popc(peers);
+        }
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// gradient (2): sums over equal runs of sorted tokens
+// ---------------------------------------------------------------------------
+
+constexpr int kSumThreads = 256;
+constexpr int kSumUnroll = 4;
+
+struct SumPlan {
+    int32_t n;        // tokens
+    int32_t V;        // rows
+    uint32_t D;       // columns
+    uint32_t vecs;    // vectors of E columns
+    uint32_t lanes;   // threads of a worker along the columns (power of two <= 256)
+    uint32_t workers;
+};
+
+// Sorted places [begin, end) of a worker.
+__device__ __forceinline__ void run_of(const int32_t *row_start, const SumPlan &p, uint32_t w,
+                                       int32_t *begin, int32_t *end) {
+    const uint32_t live = uint32_t(row_start[p.V]);
+    const uint32_t per = (live + p.workers - 1) / p.workers;
+    const uint64_t b = uint64_t(per) * w, e = b + per;
+    *begin = int32_t(b < live ? b : live);
+    *end = int32_t(e < live ? e : live);
+}
+
+template <typename TO, int E>
+__device__ __forceinline__ void write_row(TO *p, const float acc[E], float scale, bool accumulate) {
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = __fmul_rn(acc[e], scale);
+    if (accumulate) {
+        const Pack<TO, E> old = load_pack<TO, E, true>(p);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = __fadd_rn(pack_value<TO, E>(old, e), x[e]);
+    }
+    store_pack<TO, E>(p, pack_of<TO, E>(x));
+}
+
+// heads, tails: [workers][D] fp32.  heads[w]: the part in run w of a row that
+// began in an earlier run and ends in this one.  tails[w]: the part in run w
+// of a row that goes on in the next run.
+template <typename TI, typename TO, int E>
+__global__ void __launch_bounds__(kSumThreads)
+sum_kernel(const TI *__restrict__ dy, int64_t ld_dy, const int32_t *__restrict__ order,
+           const int32_t *__restrict__ rows, const int32_t *__restrict__ row_start, SumPlan p,
+           float scale, int accumulate, TO *__restrict__ dtable, int64_t ld_out,
+           float *__restrict__ heads, float *__restrict__ tails) {
+    const uint32_t lane = threadIdx.x & (p.lanes - 1);
+    const uint32_t w = blockIdx.x * (kSumThreads / p.lanes) + threadIdx.x / p.lanes;
+    const uint32_t v = blockIdx.y * p.lanes + lane;
+    if (w >= p.workers || v >= p.vecs) return;
+    const int64_t col = int64_t(v) * E;
+    int32_t begin, end;
+    run_of(row_start, p, w, &begin, &end);
+    if (begin < end) {
+        const int32_t live = row_start[p.V];
+        const int32_t prior = begin > 0 ? rows[begin - 1] : -1;
+        const int32_t next = end < live ? rows[end] : -1;
+        int32_t row = rows[begin];
+        float acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+        for (int32_t j = begin; j < end; j += kSumUnroll) {
+            Pack<TI, E> g[kSumUnroll];
+            int32_t r[kSumUnroll];
+#pragma unroll
+            for (int u = 0; u < kSumUnroll; ++u) {
+                if (j + u < end) {
+                    r[u] = rows[j + u];
+                    g[u] = load_pack<TI, E, true>(dy + int64_t(order[j + u]) * ld_dy + col);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kSumUnroll; ++u) {
+                if (j + u >= end) break;
+                if (r[u] != row) {
+                    if (row == prior) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) heads[int64_t(w) * p.D + col + e] = acc[e];
+                    } else {
+                        write_row<TO, E>(dtable + int64_t(row) * ld_out + col, acc, scale, accumulate);
+                    }
+                    row = r[u];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = __fadd_rn(acc[e], pack_value<TI, E>(g[u], e));
+            }
+        }
+        if (row == next) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) tails[int64_t(w) * p.D + col + e] = acc[e];
+        } else if (row == prior) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) heads[int64_t(w) * p.D + col + e] = acc[e];
+        } else {
+            write_row<TO, E>(dtable + int64_t(row) * ld_out + col, acc, scale, accumulate);
+        }
+    }
+    if (!accumulate) {  // this worker's share of the rows, zero where no token is
+        const uint32_t per = (uint32_t(p.V) + p.workers - 1) / p.workers;
+        const uint64_t b = uint64_t(per) * w, e = b + per < uint64_t(p.V) ? b + per : uint64_t(p.V);
+        if (b < e) {
+            Pack<TO, E> zero;
+#pragma unroll
+            for (int i = 0; i < Pack<TO, E>::kWords; ++i) zero.w[i] = 0u;
+            int32_t at = row_start[b];
+            for (uint64_t i = b; i < e; ++i) {
+                const int32_t after = row_start[i + 1];
+                if (after == at) store_pack<TO, E>(dtable + int64_t(i) * ld_out + col, zero);
+                at = after;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// gradient (3): rows that cross runs
+// ---------------------------------------------------------------------------
+
+constexpr int kJoinCols = 64;    // columns of a CTA
+constexpr int kJoinParts = 4;    // threads that share a row's runs
+constexpr int kJoinUnroll = 8;
+
+// CTA (w, c): if a row that began earlier ends in run w, adds its parts over
+// the runs, split in four consecutive shares that are added in order.
+template <typename TO>
+__global__ void __launch_bounds__(kJoinCols * kJoinParts)
+join_kernel(const int32_t *__restrict__ rows, const int32_t *__restrict__ row_start, SumPlan p,
+            float scale, int accumulate, TO *__restrict__ dtable, int64_t ld_out,
+            const float *__restrict__ heads, const float *__restrict__ tails) {
+    __shared__ float part[kJoinParts][kJoinCols];
+    const uint32_t w = blockIdx.x;
+    int32_t begin, end;
+    run_of(row_start, p, w, &begin, &end);
+    if (begin >= end || begin == 0) return;
+    const int32_t row = rows[begin];
+    if (rows[begin - 1] != row) return;                                  // starts here
+    const int32_t live = row_start[p.V];
+    if (rows[end - 1] == row && end < live && rows[end] == row) return;  // goes on
+    const uint32_t per = uint32_t(live + p.workers - 1) / p.workers;
+    const uint32_t first = uint32_t(row_start[row]) / per;               // run of its first token
+    const uint32_t c = threadIdx.x % kJoinCols, s = threadIdx.x / kJoinCols;
+    const uint32_t col = blockIdx.y * kJoinCols + c;
+    // parts first .. w - 1 are tails, part w is a head
+    const uint32_t count = w - first, share = (count + kJoinParts - 1) / kJoinParts;
+    const uint32_t b = first + s * share < w ? first + s * share : w;
+    const uint32_t e = b + share < w ? b + share : w;
+    float sum = 0.0f;
+    if (col < p.D) {
+        for (uint32_t i = b; i < e; i += kJoinUnroll) {
+            float x[kJoinUnroll];
+#pragma unroll
+            for (int u = 0; u < kJoinUnroll; ++u)
+                x[u] = i + u < e ? tails[int64_t(i + u) * p.D + col] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < kJoinUnroll; ++u) sum = __fadd_rn(sum, x[u]);
+        }
+    }
+    part[s][c] = sum;
+    __syncthreads();
+    if (s != 0 || col >= p.D) return;
+#pragma unroll
+    for (int i = 1; i < kJoinParts; ++i) sum = __fadd_rn(sum, part[i][c]);
+    const float acc[1] = {__fadd_rn(sum, heads[int64_t(w) * p.D + col])};
+    write_row<TO, 1>(dtable + int64_t(row) * ld_out + col, acc, scale, accumulate);
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+constexpr int kSms = 152;
+// The sort's counters fill at most 128 KB of shared memory (larger tables
+// take more CTAs than SMs).
+constexpr int32_t kSortRowsMax = 1024;
+constexpr int kSumCtas = 4 * kSms;
+
+// Widest vector (in values) that every row of both buffers starts on.
+int vector_width(uint32_t D, int64_t ld_a, int size_a, int64_t ld_b, int size_b) {
+    int e = 8;
+    while (e > 1 && (D % e || (ld_a * size_a) % (e * size_a > 16 ? 16 : e * size_a) ||
+                     (ld_b * size_b) % (e * size_b > 16 ? 16 : e * size_b)))
+        e /= 2;
+    return e;
+}
+
+SumPlan plan_of(const EmbeddingGrad &a, int e) {
+    SumPlan p;
+    p.n = int32_t(a.n);
+    p.V = int32_t(a.V);
+    p.D = uint32_t(a.D);
+    p.vecs = p.D / e;
+    p.lanes = 8;
+    while (p.lanes < p.vecs && p.lanes < uint32_t(kSumThreads)) p.lanes *= 2;
+    const uint32_t slices = (p.vecs + p.lanes - 1) / p.lanes;
+    const uint32_t ctas = (kSumCtas + slices - 1) / slices;
+    p.workers = ctas * (kSumThreads / p.lanes);
+    return p;
+}
+
+int grad_width(const EmbeddingGrad &a) {
+    return vector_width(uint32_t(a.D), a.ld_dy, a.dy_bf16 ? 2 : 4, a.ld_out, a.out_bf16 ? 2 : 4);
+}
+
+int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+
+template <typename T, typename I>
+cudaError_t lookup(const void *table, int64_t ld_table, const void *ids, int64_t n, int64_t first,
+                   int64_t V, int64_t D, float scale, void *out, int64_t ld_out,
+                   cudaStream_t stream) {
+    int e = vector_width(uint32_t(D), ld_table, int(sizeof(T)), ld_out, int(sizeof(T)));
+    if (sizeof(T) == 4 && e > 4) e = 4;
+    const uint32_t vecs = uint32_t(D / e);
+    const int64_t per = kLookupThreads * kLookupUnroll;
+    const uint32_t grid = uint32_t((n * vecs + per - 1) / per);
+#define WC_LOOKUP(E)                                                                          \
+    lookup_kernel<T, I, E><<<grid, kLookupThreads, 0, stream>>>(                              \
+        static_cast<const T *>(table), ld_table, static_cast<const I *>(ids), n, first, V,    \
+        vecs, scale, static_cast<T *>(out), ld_out)
+    if constexpr (sizeof(T) == 2) {
+        if (e == 8) {
+            WC_LOOKUP(8);
+            return cudaPeekAtLastError();
+        }
+    }
+    if (e >= 4) WC_LOOKUP(4);
+    else if (e == 2) WC_LOOKUP(2);
+    else WC_LOOKUP(1);
+#undef WC_LOOKUP
+    return cudaPeekAtLastError();
+}
+
+template <typename TI, typename TO>
+void launch_sum(const EmbeddingGrad &a, const SumPlan &p, int e, const int32_t *order,
+                const int32_t *rows, const int32_t *row_start, float *heads, float *tails,
+                cudaStream_t stream) {
+    const dim3 grid((p.workers + kSumThreads / p.lanes - 1) / (kSumThreads / p.lanes),
+                    (p.vecs + p.lanes - 1) / p.lanes);
+#define WC_SUM(E)                                                                             \
+    sum_kernel<TI, TO, E><<<grid, kSumThreads, 0, stream>>>(                                  \
+        static_cast<const TI *>(a.dy), a.ld_dy, order, rows, row_start, p, a.scale,           \
+        a.accumulate ? 1 : 0, static_cast<TO *>(a.dtable), a.ld_out, heads, tails)
+    if (e == 8) WC_SUM(8);
+    else if (e == 4) WC_SUM(4);
+    else if (e == 2) WC_SUM(2);
+    else WC_SUM(1);
+#undef WC_SUM
+}
+
+}  // namespace
+
+cudaError_t launch_embedding(const void *table, bool bf16, int64_t ld_table, const void *ids,
+                             bool wide, int64_t n, int64_t first, int64_t V, int64_t D,
+                             float scale, void *out, int64_t ld_out, cudaStream_t stream) {
+    if (bf16)
+        return wide ? lookup<uint16_t, int64_t>(table, ld_table, ids, n, first, V, D, scale, out, ld_out, stream)
+                    : lookup<uint16_t, int32_t>(table, ld_table, ids, n, first, V, D, scale, out, ld_out, stream);
+    return wide ? lookup<float, int64_t>(table, ld_table, ids, n, first, V, D, scale, out, ld_out, stream)
+                : lookup<float, int32_t>(table, ld_table, ids, n, first, V, D, scale, out, ld_out, stream);
+}
+
+int64_t embedding_grad_workspace(const EmbeddingGrad &a) {
+    // the plan with the fewest columns per vector has the most workers x D
+    int64_t most = 0;
+    for (int e = 1; e <= 8; e *= 2) {
+        if (a.D % e) continue;
+        const SumPlan p = plan_of(a, e);
+        const int64_t bytes = 2 * align16(int64_t(p.workers) * p.D * 4);
+        if (bytes > most) most = bytes;
+    }
+    return 2 * align16(a.n * 4) + align16((a.V + 1) * 4) + most;
+}
+
+cudaError_t launch_embedding_grad(const EmbeddingGrad &a, cudaStream_t stream) {
+    const int e = grad_width(a);
+    const SumPlan p = plan_of(a, e);
+    char *ws = static_cast<char *>(a.workspace);
+    int32_t *order = reinterpret_cast<int32_t *>(ws);
+    ws += align16(a.n * 4);
+    int32_t *rows = reinterpret_cast<int32_t *>(ws);
+    ws += align16(a.n * 4);
+    int32_t *row_start = reinterpret_cast<int32_t *>(ws);
+    ws += align16((a.V + 1) * 4);
+    float *heads = reinterpret_cast<float *>(ws);
+    ws += align16(int64_t(p.workers) * p.D * 4);
+    float *tails = reinterpret_cast<float *>(ws);
+
+    int32_t per_cta = int32_t((a.V + kSms - 1) / kSms);
+    if (per_cta > kSortRowsMax) per_cta = kSortRowsMax;
+    const uint32_t sort_grid = uint32_t((a.V + per_cta - 1) / per_cta);
+    const size_t smem = size_t(per_cta) * (kSortPitch + 1) * 4;
+    cudaError_t err = cudaSuccess;
+    if (smem > 48 * 1024)
+        err = a.wide ? cudaFuncSetAttribute(sort_kernel<int64_t>,
+                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            kSortRowsMax * (kSortPitch + 1) * 4)
+                     : cudaFuncSetAttribute(sort_kernel<int32_t>,
+                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            kSortRowsMax * (kSortPitch + 1) * 4);
+    if (err != cudaSuccess) return err;
+    if (a.wide)
+        sort_kernel<int64_t><<<sort_grid, kSortThreads, smem, stream>>>(
+            static_cast<const int64_t *>(a.ids), p.n, a.first, p.V, per_cta, order, rows, row_start);
+    else
+        sort_kernel<int32_t><<<sort_grid, kSortThreads, smem, stream>>>(
+            static_cast<const int32_t *>(a.ids), p.n, a.first, p.V, per_cta, order, rows, row_start);
+    err = cudaPeekAtLastError();
+    if (err != cudaSuccess) return err;
+
+    if (a.dy_bf16) {
+        if (a.out_bf16) launch_sum<uint16_t, uint16_t>(a, p, e, order, rows, row_start, heads, tails, stream);
+        else launch_sum<uint16_t, float>(a, p, e, order, rows, row_start, heads, tails, stream);
+    } else {
+        if (a.out_bf16) launch_sum<float, uint16_t>(a, p, e, order, rows, row_start, heads, tails, stream);
+        else launch_sum<float, float>(a, p, e, order, rows, row_start, heads, tails, stream);
+    }
+    err = cudaPeekAtLastError();
+    if (err != cudaSuccess || a.n < 2) return err;
+    const dim3 grid(p.workers, (p.D + kJoinCols - 1) / kJoinCols);
+    if (a.out_bf16)
+        join_kernel<uint16_t><<<grid, kJoinCols * kJoinParts, 0, stream>>>(
+            rows, row_start, p, a.scale, a.accumulate ? 1 : 0, static_cast<uint16_t *>(a.dtable),
+            a.ld_out, heads, tails);
+    else
+        join_kernel<float><<<grid, kJoinCols * kJoinParts, 0, stream>>>(
+            rows, row_start, p, a.scale, a.accumulate ? 1 : 0, static_cast<float *>(a.dtable),
+            a.ld_out, heads, tails);
+    return cudaPeekAtLastError();
+}
+
+}  // namespace wc

@@ -55,6 +55,77 @@ cudaError_t launch_sr_accumulate(uint16_t *dst, uint16_t *src, uint32_t n, uint3
                                  uint32_t step, cudaStream_t stream);
 uint32_t sr_key(uint32_t seed, uint32_t step);
 
+// One gradient tensor: n values at src, and where its clipped values go.
+struct GradSpan {
+    const void *src;
+    void *dst;
+    int64_t n;
+    bool src_bf16, dst_bf16;
+};
+// Tensors whose addresses fit one launch's arguments, and the partial sums
+// (fp64) that a launch leaves.
+constexpr int kGradSpansPerLaunch = 1024, kGradPartialsPerLaunch = 608;
+// stats: [0] norm and, with clip, [1] coefficient.
+cudaError_t launch_grad_norm(const GradSpan *spans, int count, double *partials, bool clip,
+                             bool in_place, double max_norm, double eps, float *stats,
+                             cudaStream_t stream);
+
+cudaError_t launch_embedding(const void *table, bool bf16, int64_t ld_table, const void *ids,
+                             bool wide, int64_t n, int64_t first, int64_t V, int64_t D,
+                             float scale, void *out, int64_t ld_out, cudaStream_t stream);
+struct EmbeddingGrad {
+    const void *dy;
+    bool dy_bf16;
+    int64_t ld_dy;
+    const void *ids;
+    bool wide;  // 64-bit ids
+    int64_t n, first, V, D;
+    float scale;
+    bool accumulate;
+    void *dtable;
+    bool out_bf16;
+    int64_t ld_out;
+    void *workspace;
+};
+// Bytes of workspace; reads n, V and D alone.
+int64_t embedding_grad_workspace(const EmbeddingGrad &a);
+cudaError_t launch_embedding_grad(const EmbeddingGrad &a, cudaStream_t stream);
+
+// 8-bit floating point (e4m3) with one fp32 scale per block of 128.
+struct Fp8Quant {
+    const void *x;
+    bool x_bf16;
+    int64_t rows, cols, ld;
+    bool square;               // one scale per 128 x 128 instead of 1 x 128
+    uint8_t *q;                // [rows][ld_q], or NULL
+    int64_t ld_q;
+    float *s;                  // [ceil(cols/128)][ld_s]
+    int64_t ld_s;
+    uint8_t *qt;               // [cols][ld_qt], or NULL
+    int64_t ld_qt;
+    float *st;                 // [ceil(rows/128)][ld_st]
+    int64_t ld_st;
+};
+cudaError_t launch_fp8_quant(const Fp8Quant &a, cudaStream_t stream);
+struct Fp8Operand {
+    const uint8_t *q;          // [rows][ld]
+    int64_t ld;
+    const float *s;            // [ceil(K/128)][ld_s]
+    int64_t ld_s;
+    int rows_per_scale;        // 1 or 128
+};
+struct Fp8Matmul {
+    Fp8Operand a, b;
+    int64_t M, N, K;
+    void *out;                 // [M][ld_out]
+    bool out_bf16;
+    int64_t ld_out;
+    bool accumulate;
+};
+cudaError_t launch_fp8_matmul(const Fp8Matmul &a, cudaStream_t stream);
+// Waits of the product's kernels that ran out (0 unless a launch went wrong).
+cudaError_t fp8_wait_timeouts(unsigned int *count, bool reset);
+
 // Violation record of one source file's kernels in a checked build (see
 // WC_IN_BOUNDS in wc_device.cuh).  sr_accumulate.cu has none: its kernel
 // tests every access against the element count as part of its own logic.

@@ -1,0 +1,147 @@
+"""Linear layers in 8-bit floating point (e4m3) with a scale per block of 128.
+
+A matrix is held as e4m3 codes and fp32 scales: one scale for every 128 values
+along the axis that a product sums over (activations and gradients), or one
+for every 128 x 128 (weights).  `quantize` and `quantize_weight` make such
+matrices, `matmul` multiplies two of them on the tensor cores with fp32 sums,
+and `Fp8Linear` composes them into a layer's forward and backward pass:
+
+    lin = Fp8Linear(weight)                    # [N, K] bf16 or fp32
+    y = lin.forward(x)                         # x W^T
+    y, saved = lin.forward(x, save=True)       # training
+    dx, dw = lin.backward(dy, saved)           # dy W, dy^T x (fp32)
+    lin.load(weight)                           # after an update of the weights
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding
+
+BLOCK = 128
+
+
+def _ceil(n: int, m: int) -> int:
+    return -(-n // m) * m
+
+
+class Fp8Tensor:
+    """A matrix [rows, cols] in 8 bits.
+
+    codes  : float8_e4m3fn [rows, >= cols], rows a multiple of 16 bytes apart
+    scales : float32 [ceil(cols / 128), rows] (block_rows 1) or
+             [ceil(cols / 128), ceil(rows / 128)] (block_rows 128)
+    Row r, column c stands for codes[r, c] * scales[c // 128, r // block_rows].
+    """
+
+    __slots__ = ("codes", "scales", "rows", "cols", "block_rows")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int,
+                 block_rows: int = 1):
+        if block_rows not in (1, BLOCK):
+            raise ValueError(f"block_rows must be 1 or {BLOCK}, got {block_rows}")
+        if codes.dim() != 2 or codes.shape[0] != rows or codes.shape[1] < cols:
+            raise ValueError(f"codes have shape {tuple(codes.shape)}, expected ({rows}, {cols})")
+        self.codes, self.scales = codes, scales
+        self.rows, self.cols, self.block_rows = rows, cols, block_rows
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda") -> "Fp8Tensor":
+        return cls(torch.empty(rows, _ceil(cols, 16), dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(-(-cols // BLOCK), -(-rows // block_rows), dtype=torch.float32,
+                               device=device), rows, cols, block_rows)
+
+
+def _current(t: torch.Tensor, stream):
+    return stream if stream is not None else torch.cuda.current_stream(t.device)
+
+
+def quantize(x: torch.Tensor, rows: bool = True, columns: bool = False, stream=None):
+    """x [M, K] (bf16 or fp32) as (x, x^T): an Fp8Tensor [M, K] with a scale per
+    128 columns of a row (None unless `rows`) and an Fp8Tensor [K, M] with a
+    scale per 128 rows of a column (None unless `columns`), both from one
+    reading of x."""
+    return _quantize(x, rows, columns, 1, stream)
+
+
+def quantize_weight(w: torch.Tensor, rows: bool = True, columns: bool = False, stream=None):
+    """The same with one scale per 128 x 128, shared by the two layouts."""
+    return _quantize(w, rows, columns, BLOCK, stream)
+
+
+def _quantize(x, rows, columns, block_rows, stream):
+    if x.dim() != 2:
+        raise ValueError(f"x must be a matrix, got shape {tuple(x.shape)}")
+    if not (rows or columns):
+        raise ValueError("neither rows nor columns asked for")
+    M, K = x.shape
+    s = _current(x, stream)
+    with torch.cuda.stream(s):
+        q = Fp8Tensor.empty(M, K, block_rows, x.device) if rows else None
+        qt = Fp8Tensor.empty(K, M, block_rows, x.device) if columns else None
+    _quantize_into(x, q, qt, block_rows, s)
+    return q, qt
+
+
+def _quantize_into(x, q, qt, block_rows, stream):
+    binding.fp8_quant(x, q.codes if q else None, q.scales if q else None,
+                      qt.codes if qt else None, qt.scales if qt else None,
+                      square=block_rows == BLOCK, stream=stream)
+
+
+def matmul(a: Fp8Tensor, b: Fp8Tensor, out: torch.Tensor | None = None,
+           out_dtype: torch.dtype = torch.bfloat16, accumulate: bool = False,
+           stream=None) -> torch.Tensor:
+    """a [M, K] times b [N, K] transposed: [M, N] in bf16 or fp32, a new tensor
+    or `out`; with accumulate, added to what `out` holds."""
+    if a.cols != b.cols:
+        raise ValueError(f"a has {a.cols} columns, b {b.cols}")
+    s = _current(a.codes, stream)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs the matrix to add to as out")
+        with torch.cuda.stream(s):
+            out = torch.empty(a.rows, b.rows, dtype=out_dtype, device=a.codes.device)
+    elif out.dim() != 2 or tuple(out.shape) != (a.rows, b.rows):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected ({a.rows}, {b.rows})")
+    binding.fp8_matmul(a.codes, a.scales, a.block_rows, b.codes, b.scales, b.block_rows, a.cols,
+                       out, accumulate, s)
+    return out
+
+
+class Fp8Linear:
+    """y = x W^T with W [N, K] kept in 8 bits (one scale per 128 x 128), in
+    both layouts if `training`."""
+
+    def __init__(self, weight: torch.Tensor, training: bool = True, stream=None):
+        if weight.dim() != 2:
+            raise ValueError(f"weight must be a matrix, got shape {tuple(weight.shape)}")
+        self.N, self.K = weight.shape
+        self.w, self.wt = quantize_weight(weight, columns=training, stream=stream)
+
+    def load(self, weight: torch.Tensor, stream=None) -> None:
+        """Quantizes new values of the weight into the same buffers."""
+        if tuple(weight.shape) != (self.N, self.K):
+            raise ValueError(f"weight has shape {tuple(weight.shape)}, expected ({self.N}, {self.K})")
+        _quantize_into(weight, self.w, self.wt, BLOCK, _current(weight, stream))
+
+    def forward(self, x: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
+                save: bool = False, stream=None):
+        """y [M, N]; with save, also what backward needs of x (x^T in 8 bits)."""
+        q, qt = quantize(x, columns=save, stream=stream)
+        y = matmul(q, self.w, out_dtype=out_dtype, stream=stream)
+        return (y, qt) if save else y
+
+    def backward(self, dy: torch.Tensor, saved: Fp8Tensor, dx_dtype: torch.dtype = torch.bfloat16,
+                 dw: torch.Tensor | None = None, dw_dtype: torch.dtype = torch.float32,
+                 accumulate: bool = False, stream=None):
+        """(dx [M, K], dw [N, K]).  dw: a buffer to write, or with accumulate
+        to add to (the gradient of earlier micro-batches)."""
+        if self.wt is None:
+            raise ValueError("backward needs Fp8Linear(training=True)")
+        if dy.dim() != 2 or tuple(dy.shape) != (saved.cols, self.N):
+            raise ValueError(f"dy has shape {tuple(dy.shape)}, expected ({saved.cols}, {self.N})")
+        q, qt = quantize(dy, columns=True, stream=stream)
+        dx = matmul(q, self.wt, out_dtype=dx_dtype, stream=stream)
+        dw = matmul(qt, saved, out=dw, out_dtype=dw_dtype, accumulate=accumulate, stream=stream)
+        return dx, dw

@@ -1,0 +1,75 @@
+"""Global gradient norm over many tensors, and clipping.
+
+    norm = sqrt(sum of every x^2),  coef = min(1, max_norm / (norm + eps))
+
+The step between the reduced gradient shards (`qgz`) and the update.  All on
+the device: nothing here waits for the GPU, and the norm and the coefficient
+come back as a tensor that the update, or a log line some steps later, reads.
+
+    grads = TensorList(model_gradients)         # once: the buffers stay
+    stats = clip(grads, max_norm=1.0)           # every step; stats = [norm, coef]
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding
+
+
+class TensorList:
+    """A list of gradient tensors (float32 or bfloat16, contiguous, on one GPU,
+    of any sizes and at any offsets into larger buffers), checked once and
+    described to the library as addresses and lengths.  It keeps the tensors
+    alive; make another one if a gradient moves to another buffer."""
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        self.spans, self.device = binding.spans(self.tensors)
+        self.workspace_bytes = binding.grad_norm_workspace(len(self.tensors))
+
+    def __len__(self) -> int:
+        return len(self.tensors)
+
+
+def _listed(tensors) -> TensorList:
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+
+
+def _buffers(lst: TensorList, stats: torch.Tensor | None, n: int, stream):
+    if lst.device is None:
+        raise ValueError("an empty list has no GPU to run on")
+    s = stream if stream is not None else torch.cuda.current_stream(lst.device)
+    if s.device != lst.device:
+        raise ValueError(f"stream is on {s.device}, the tensors on {lst.device}")
+    with torch.cuda.stream(s):
+        if stats is None:
+            stats = torch.empty(n, dtype=torch.float32, device=lst.device)
+        workspace = torch.empty(lst.workspace_bytes, dtype=torch.uint8, device=lst.device)
+    return s, stats, workspace
+
+
+def norm(tensors, stats: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The norm of a TensorList or a list of tensors, as stats [1] fp32 on the
+    device.  Runs on `stream` or the current one."""
+    lst = _listed(tensors)
+    s, stats, workspace = _buffers(lst, stats, 1, stream)
+    binding.grad_norm(lst.spans, len(lst), stats, workspace, s)
+    return stats
+
+
+def clip(tensors, max_norm: float, out=None, eps: float = 1e-6,
+         stats: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Scales the tensors by coef = min(1, max_norm / (norm + eps)), in place
+    or into `out` (a TensorList or list of as many tensors of the same lengths;
+    their type may be the other one, for instance fp32 gradients for the update
+    from bf16 ones).  Returns stats [2] fp32 on the device: norm and coef."""
+    lst = _listed(tensors)
+    dst = None if out is None else _listed(out)
+    if dst is not None and len(dst) != len(lst):
+        raise ValueError(f"out has {len(dst)} tensors, expected {len(lst)}")
+    if dst is not None and dst.device != lst.device:
+        raise ValueError(f"out is on {dst.device}, expected {lst.device}")
+    s, stats, workspace = _buffers(lst, stats, 2, stream)
+    binding.grad_clip(lst.spans, None if dst is None else dst.spans, len(lst), float(max_norm),
+                      float(eps), stats, workspace, s)
+    return stats
