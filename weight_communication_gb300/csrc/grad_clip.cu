@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 norm_partials_kernel(const __grid_constant__ SpanTable<CAP> t, double *__restrict__ partials) {
     __shared__ double scratch[kThreads / 32];
     // the clipping kernel may be scheduled now; it waits for this one's end
-    asm volatile("griddepcontrol.launch_dependents;");
+    let_successor_start();
     NormSum sum;
     for (uint32_t i = blockIdx.x; i < t.tiles; i += gridDim.x) {
         const Tile tile = find_tile(t, i);
@@ -243,6 +243,14 @@ __device__ __forceinline__ void store_one(void *dst, bool bf16, int64_t i, float
     else static_cast<float *>(dst)[i] = x;
 }
 
+// 32 consecutive bytes in one store: two 16-byte ones would each write half of
+// every 32-byte sector they touch.
+__device__ __forceinline__ void store_f32x8(float *p, const float x[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]),
+                 "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
+
 template <bool BF16>
 __device__ __forceinline__ void scale_tile(const uint4 raw[BF16 ? 4 : 8], const Tile &tile,
                                            void *dst, bool dst_bf16, float coef) {
@@ -250,7 +258,7 @@ __device__ __forceinline__ void scale_tile(const uint4 raw[BF16 ? 4 : 8], const 
     const uint32_t size = dst_bf16 ? 2u : 4u;
     char *base = static_cast<char *>(dst) + tile.begin * size;
     // one store per W values where the destination starts on a boundary too
-    const bool vec = (reinterpret_cast<uintptr_t>(base) & (dst_bf16 ? 2 * W - 1 : 15u)) == 0;
+    const bool vec = (reinterpret_cast<uintptr_t>(base) & (W * size - 1)) == 0;
 #pragma unroll
     for (int j = 0; j < (BF16 ? 4 : 8); ++j) {
         const uint32_t v = threadIdx.x + kThreads * j;
@@ -266,11 +274,10 @@ __device__ __forceinline__ void scale_tile(const uint4 raw[BF16 ? 4 : 8], const 
                     __stcs(reinterpret_cast<uint4 *>(base) + v, make_uint4(w[0], w[1], w[2], w[3]));
                 else
                     __stcs(reinterpret_cast<uint2 *>(base) + v, make_uint2(w[0], w[1]));
+            } else if constexpr (BF16) {
+                store_f32x8(reinterpret_cast<float *>(base) + v * W, x);
             } else {
-#pragma unroll
-                for (uint32_t e = 0; e < W; e += 4)
-                    __stcs(reinterpret_cast<float4 *>(base) + v * (W / 4) + e / 4,
-                           make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]));
+                __stcs(reinterpret_cast<float4 *>(base) + v, make_float4(x[0], x[1], x[2], x[3]));
             }
         } else {
 #pragma unroll
@@ -287,7 +294,7 @@ clip_kernel(const __grid_constant__ SpanTable<CAP> t, const double *__restrict__
             int count, double max_norm, double eps, float *__restrict__ stats, int in_place,
             int write_stats) {
     __shared__ double scratch[kThreads / 32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_predecessor();
     const NormCoef c = finish(partials, count, max_norm, eps, scratch);
     if (write_stats && blockIdx.x == 0 && threadIdx.x == 0) {
         stats[0] = c.norm;
@@ -361,19 +368,15 @@ cudaError_t launch_clip(const GradSpan *spans, int count, const double *partials
     SpanTable<CAP> t;
     fill(t, spans, count);
     if (t.tiles == 0) return cudaSuccess;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid_of(t.tiles));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = overlap ? 1 : 0;
     const int first = *write_stats;
     *write_stats = 0;
-    return cudaLaunchKernelEx(&cfg, clip_kernel<CAP>, t, partials, used, max_norm, eps, stats,
-                              in_place ? 1 : 0, first);
+    const uint32_t grid = grid_of(t.tiles);
+    if (overlap)
+        return launch_after(clip_kernel<CAP>, dim3(grid), dim3(kThreads), 0, stream, t, partials, used,
+                            max_norm, eps, stats, in_place ? 1 : 0, first);
+    clip_kernel<CAP><<<grid, kThreads, 0, stream>>>(t, partials, used, max_norm, eps, stats,
+                                                    in_place ? 1 : 0, first);
+    return cudaPeekAtLastError();
 }
 
 }  // namespace

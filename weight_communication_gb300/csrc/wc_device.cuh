@@ -333,6 +333,17 @@ __device__ __forceinline__ void accumulate_word(uint32_t x, float table, f32x2 s
     }
 }
 
+// A kernel launched with launch_after() may start before its predecessor in
+// the stream has ended, and calls wait_for_predecessor() before it touches any
+// memory; a predecessor that calls let_successor_start() allows that as soon
+// as all its CTAs have started, any other one when it ends.
+__device__ __forceinline__ void let_successor_start() {
+    asm volatile("griddepcontrol.launch_dependents;");
+}
+__device__ __forceinline__ void wait_for_predecessor() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Streaming (read-once) and plain vector accesses.
 __device__ __forceinline__ float4 ld_stream_f4(const float *p) {
     return __ldcs(reinterpret_cast<const float4 *>(p));
@@ -342,6 +353,23 @@ __device__ __forceinline__ uint2 ld_stream_u2(const void *p) {
 }
 __device__ __forceinline__ uint4 ld_stream_u4(const void *p) {
     return __ldcs(reinterpret_cast<const uint4 *>(p));
+}
+
+// Launch of a kernel that may overlap its predecessor's end (see above).
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t stream, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
 }
 
 }  // namespace wc
