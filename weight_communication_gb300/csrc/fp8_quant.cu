@@ -14,9 +14,12 @@
 // training step needs: the rows' codes (blocks along the columns) and the
 // columns' codes (blocks along the rows, stored transposed).  Square blocks,
 // for weights, share one scale between the two layouts.  Thread (g, l) holds
-// rows 8g..8g+7 and columns 8l..8l+7: rows reduce over 16 lanes, columns over
-// the threads' own 8 rows first; the transposed codes go through shared memory
-// as 8-byte words of a column's 8 consecutive rows.
+// rows 8g..8g+7 and columns 8l..8l+7, bf16 values two to a word, and takes
+// maxima of encodings two at a time.  The 16 lanes of a row group reduce
+// their 8 rows together (each exchange halves the rows a lane still carries),
+// so that a lane divides for one row and not for eight; the columns' scales
+// are likewise formed once each, by 128 threads.  The transposed codes go
+// through shared memory as 8-byte words of a column's 8 consecutive rows.
 // Bound: HBM (2 bytes read and 1 or 2 written per value).
 #include <cuda_fp8.h>
 
@@ -50,154 +53,200 @@ __device__ __forceinline__ Scale8 scale_of(float m) {
     return s;
 }
 
-// Codes of 8 values in order, 0 where the block is not finite (inv = 0 times
-// an infinity is not a number, so those are set, not computed).
-__device__ __forceinline__ uint2 codes_of(const float x[8], const float inv[8]) {
+// The 8 x 8 values of a thread, and the operations on them that depend on the
+// type.  An encoding without its sign orders magnitudes, infinities and NaN
+// above all finite ones; Max holds such encodings (bf16: of two columns).
+template <typename T>
+struct Values;
+
+template <>
+struct Values<uint16_t> {
+    static constexpr int kMaxes = 4;  // words of a row's 8 maxima
+    uint32_t w[8][4];
+    __device__ __forceinline__ void load(int i, const uint16_t *p) {
+        const uint4 q = ld_stream_u4(p);
+        w[i][0] = q.x;
+        w[i][1] = q.y;
+        w[i][2] = q.z;
+        w[i][3] = q.w;
+    }
+    __device__ __forceinline__ void load_edge(int i, const uint16_t *p, int64_t left) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t lo = 2 * k < left ? p[2 * k] : 0u;
+            const uint32_t hi = 2 * k + 1 < left ? p[2 * k + 1] : 0u;
+            w[i][k] = lo | (hi << 16);
+        }
+    }
+    __device__ __forceinline__ float at(int i, int j) const {
+        return __uint_as_float((j & 1) ? (w[i][j / 2] & 0xFFFF0000u) : (w[i][j / 2] << 16));
+    }
+    __device__ __forceinline__ uint32_t mag(int i, int k) const { return w[i][k] & 0x7FFF7FFFu; }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+    // the largest of a word's two, as a binary32 encoding
+    static __device__ __forceinline__ uint32_t single(uint32_t m) { return max(m << 16, m & 0xFFFF0000u); }
+    // column j of a row's maxima, as a binary32 encoding
+    static __device__ __forceinline__ uint32_t column(const uint32_t *m, int j) {
+        return uint32_t(reinterpret_cast<const uint16_t *>(m)[j]) << 16;
+    }
+};
+
+template <>
+struct Values<float> {
+    static constexpr int kMaxes = 8;
+    uint32_t w[8][8];
+    __device__ __forceinline__ void load(int i, const float *p) {
+        const uint4 a = ld_stream_u4(p), b = ld_stream_u4(p + 4);
+        w[i][0] = a.x;
+        w[i][1] = a.y;
+        w[i][2] = a.z;
+        w[i][3] = a.w;
+        w[i][4] = b.x;
+        w[i][5] = b.y;
+        w[i][6] = b.z;
+        w[i][7] = b.w;
+    }
+    __device__ __forceinline__ void load_edge(int i, const float *p, int64_t left) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[i][k] = k < left ? __float_as_uint(p[k]) : 0u;
+    }
+    __device__ __forceinline__ float at(int i, int j) const { return __uint_as_float(w[i][j]); }
+    __device__ __forceinline__ uint32_t mag(int i, int k) const { return w[i][k] & 0x7FFFFFFFu; }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+    static __device__ __forceinline__ uint32_t single(uint32_t m) { return m; }
+    static __device__ __forceinline__ uint32_t column(const uint32_t *m, int j) { return m[j]; }
+};
+
+// Codes of 8 values of blocks with one inv.  inv 0 gives codes 0 also where
+// the product is not a number.
+__device__ __forceinline__ uint2 codes_of(const float (&x)[8], float inv) {
     uint32_t h[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float a = inv[2 * j] == 0.0f ? 0.0f : __fmul_rn(x[2 * j], inv[2 * j]);
-        const float b = inv[2 * j + 1] == 0.0f ? 0.0f : __fmul_rn(x[2 * j + 1], inv[2 * j + 1]);
-        h[j] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    }
-    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    for (int j = 0; j < 4; ++j)
+        h[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(x[2 * j], inv), __fmul_rn(x[2 * j + 1], inv)),
+                                        __NV_SATFINITE, __NV_E4M3);
+    return inv == 0.0f ? make_uint2(0u, 0u) : make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-// |x| with infinities and NaN ordered above every finite value, for a maximum
-// over encodings.
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
 // Shared transposed codes: column c's 128 rows as 16 words of 8 bytes, word w
-// at slot w ^ (c / 8 % 16) so that the 16 lanes of a store hit 16 banks pairs.
+// at slot w ^ (c / 8 % 16), so that the 16 lanes of a store hit all banks.
 __device__ __forceinline__ int slot_of(int c, int w) { return c * 16 + (w ^ ((c >> 3) & 15)); }
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, bool VEC, bool ROWS, bool COLS, bool SQUARE>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
 fp8_quant_kernel(const Fp8Quant a) {
-    __shared__ uint2 turned[kTile * 16];
-    __shared__ uint32_t col_max[kThreads / 32][kTile];
+    using V = Values<T>;
+    __shared__ uint2 turned[COLS ? kTile * 16 : 1];
+    __shared__ uint32_t col_max[COLS && !SQUARE ? kThreads / 32 : 1][COLS && !SQUARE ? 16 * V::kMaxes : 1];
+    __shared__ __align__(16) float col_inv[COLS && !SQUARE ? kTile : 1];
     __shared__ uint32_t tile_max[kThreads / 32];
     const int l = threadIdx.x & 15, g = threadIdx.x >> 4;  // column group, row group
     const int warp = threadIdx.x >> 5;
     const int64_t r0 = int64_t(blockIdx.y) * kTile, c0 = int64_t(blockIdx.x) * kTile;
     const int64_t c = c0 + 8 * l;
-    const T *x = static_cast<const T *>(a.x);
 
-    float v[8][8];
+    // the product that follows may set itself up; it waits for this kernel's end
+    let_successor_start();
+    V v;
+    const T *x = static_cast<const T *>(a.x) + (r0 + 8 * g) * a.ld + c;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int64_t r = r0 + 8 * g + i;
-        if (VEC && r < a.rows && c + 8 <= a.cols) {
-            const T *p = x + r * a.ld + c;
-            if constexpr (sizeof(T) == 2) {
-                const uint4 w = ld_stream_u4(p);
-                const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[i][2 * j] = __uint_as_float(h[j] << 16);
-                    v[i][2 * j + 1] = __uint_as_float(h[j] & 0xFFFF0000u);
-                }
-            } else {
-                const float4 w0 = ld_stream_f4(p), w1 = ld_stream_f4(p + 4);
-                v[i][0] = w0.x;
-                v[i][1] = w0.y;
-                v[i][2] = w0.z;
-                v[i][3] = w0.w;
-                v[i][4] = w1.x;
-                v[i][5] = w1.y;
-                v[i][6] = w1.z;
-                v[i][7] = w1.w;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[i][j] = 0.0f;
-                if (r < a.rows && c + j < a.cols) {
-                    if constexpr (sizeof(T) == 2) v[i][j] = bf16_bits_to_f32(x[r * a.ld + c + j]);
-                    else v[i][j] = x[r * a.ld + c + j];
-                }
-            }
-        }
+        const int64_t left = r0 + 8 * g + i < a.rows ? a.cols - c : 0;
+        if (VEC && left >= 8) v.load(i, x + i * a.ld);
+        else v.load_edge(i, x + i * a.ld, left);
     }
 
     Scale8 square = {0.0f, 0.0f};
-    if (a.square) {
+    if (SQUARE) {
         uint32_t m = 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = max(m, magnitude(v[i][j]));
-        m = __reduce_max_sync(kFull, m);
+            for (int k = 0; k < V::kMaxes; ++k) m = V::larger(m, v.mag(i, k));
+        m = __reduce_max_sync(kFull, V::single(m));
         if ((threadIdx.x & 31) == 0) tile_max[warp] = m;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) m = max(m, tile_max[w]);
         square = scale_of(__uint_as_float(m));
         if (threadIdx.x == 0) {
-            if (a.q) a.s[int64_t(blockIdx.x) * a.ld_s + blockIdx.y] = square.scale;
-            if (a.qt) a.st[int64_t(blockIdx.y) * a.ld_st + blockIdx.x] = square.scale;
+            if (ROWS) a.s[int64_t(blockIdx.x) * a.ld_s + blockIdx.y] = square.scale;
+            if (COLS) a.st[int64_t(blockIdx.y) * a.ld_st + blockIdx.x] = square.scale;
+        }
+    }
+    if (COLS && !SQUARE) {  // the columns' maxima over this warp's 16 rows
+#pragma unroll
+        for (int k = 0; k < V::kMaxes; ++k) {
+            uint32_t m = v.mag(0, k);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) m = V::larger(m, v.mag(i, k));
+            m = V::larger(m, __shfl_xor_sync(kFull, m, 16));
+            if ((threadIdx.x & 16) == 0) col_max[warp][V::kMaxes * l + k] = m;
         }
     }
 
-    if (a.q) {
+    if (ROWS) {
+        Scale8 own = square;
+        if (!SQUARE) {
+            uint32_t m[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t n = v.mag(i, 0);
+#pragma unroll
+                for (int k = 1; k < V::kMaxes; ++k) n = V::larger(n, v.mag(i, k));
+                m[i] = V::single(n);
+            }
+            // lane l ends with the maximum of row l / 2
+#pragma unroll
+            for (int half = 4; half > 0; half /= 2) {
+                const bool upper = (l & (2 * half)) != 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= half) continue;
+                    const uint32_t give = upper ? m[k] : m[k + half];
+                    const uint32_t keep = upper ? m[k + half] : m[k];
+                    m[k] = max(keep, __shfl_xor_sync(kFull, give, 2 * half));
+                }
+            }
+            m[0] = max(m[0], __shfl_xor_sync(kFull, m[0], 1));
+            own = scale_of(__uint_as_float(m[0]));
+            const int64_t r = r0 + 8 * g + l / 2;
+            if ((l & 1) == 0 && r < a.rows) a.s[int64_t(blockIdx.x) * a.ld_s + r] = own.scale;
+        }
+        // a row's padding up to a multiple of 16 bytes is written too, as
+        // zeros; ld_q is such a multiple, so the 8 bytes fit
+        const bool inside = c < (a.cols + 15) / 16 * 16;
+        uint8_t *q = a.q + (r0 + 8 * g) * a.ld_q + c;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int64_t r = r0 + 8 * g + i;
-            Scale8 s = square;
-            if (!a.square) {
-                uint32_t m = 0u;
+            const float inv = SQUARE ? own.inv : __shfl_sync(kFull, own.inv, 2 * i, 16);
+            float t[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m = max(m, magnitude(v[i][j]));
-#pragma unroll
-                for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(kFull, m, off));
-                s = scale_of(__uint_as_float(m));
-                if (l == 0 && r < a.rows) a.s[int64_t(blockIdx.x) * a.ld_s + r] = s.scale;
-            }
-            float inv[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) inv[j] = s.inv;
-            const uint2 w = codes_of(v[i], inv);
-            // a row's padding up to a multiple of 16 bytes is written too, as
-            // zeros; ld_q is such a multiple, so the 8 bytes fit
-            if (r < a.rows && c < (a.cols + 15) / 16 * 16)
-                *reinterpret_cast<uint2 *>(a.q + r * a.ld_q + c) = w;
+            for (int j = 0; j < 8; ++j) t[j] = v.at(i, j);
+            const uint2 w = codes_of(t, inv);
+            if (inside && r0 + 8 * g + i < a.rows) *reinterpret_cast<uint2 *>(q + i * a.ld_q) = w;
         }
     }
 
-    if (a.qt) {
-        float inv[8];
-        if (a.square) {
+    if (COLS) {
+        if (!SQUARE) {
+            __syncthreads();
+            if (threadIdx.x < kTile) {
+                uint32_t m = V::column(col_max[0], threadIdx.x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) inv[j] = square.inv;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t m = 0u;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m = max(m, magnitude(v[i][j]));
-                m = max(m, __shfl_xor_sync(kFull, m, 16));
-                if ((threadIdx.x & 16) == 0) col_max[warp][8 * l + j] = m;
+                for (int w = 1; w < kThreads / 32; ++w) m = max(m, V::column(col_max[w], threadIdx.x));
+                const Scale8 s = scale_of(__uint_as_float(m));
+                col_inv[threadIdx.x] = s.inv;
+                if (c0 + threadIdx.x < a.cols) a.st[int64_t(blockIdx.y) * a.ld_st + c0 + threadIdx.x] = s.scale;
             }
             __syncthreads();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t m = 0u;
-#pragma unroll
-                for (int w = 0; w < kThreads / 32; ++w) m = max(m, col_max[w][8 * l + j]);
-                const Scale8 s = scale_of(__uint_as_float(m));
-                inv[j] = s.inv;
-                if (g == 0 && c + j < a.cols) a.st[int64_t(blockIdx.y) * a.ld_st + c + j] = s.scale;
-            }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float t[8], in[8];
+            float t[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                t[i] = v[i][j];
-                in[i] = inv[j];
-            }
-            turned[slot_of(8 * l + j, g)] = codes_of(t, in);
+            for (int i = 0; i < 8; ++i) t[i] = v.at(i, j);
+            turned[slot_of(8 * l + j, g)] = codes_of(t, SQUARE ? square.inv : col_inv[SQUARE ? 0 : 8 * l + j]);
         }
         __syncthreads();
 #pragma unroll
@@ -210,17 +259,28 @@ fp8_quant_kernel(const Fp8Quant a) {
     }
 }
 
+template <typename T, bool VEC, bool SQUARE>
+void launch(const Fp8Quant &a, cudaStream_t stream) {
+    const dim3 grid(uint32_t((a.cols + kTile - 1) / kTile), uint32_t((a.rows + kTile - 1) / kTile));
+    if (a.q && a.qt) fp8_quant_kernel<T, VEC, true, true, SQUARE><<<grid, kThreads, 0, stream>>>(a);
+    else if (a.q) fp8_quant_kernel<T, VEC, true, false, SQUARE><<<grid, kThreads, 0, stream>>>(a);
+    else fp8_quant_kernel<T, VEC, false, true, SQUARE><<<grid, kThreads, 0, stream>>>(a);
+}
+
+template <typename T>
+void launch(const Fp8Quant &a, cudaStream_t stream) {
+    const bool vec = a.ld % (16 / sizeof(T)) == 0;  // rows start on 16 bytes
+    if (vec && a.square) launch<T, true, true>(a, stream);
+    else if (vec) launch<T, true, false>(a, stream);
+    else if (a.square) launch<T, false, true>(a, stream);
+    else launch<T, false, false>(a, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_quant(const Fp8Quant &a, cudaStream_t stream) {
-    const dim3 grid(uint32_t((a.cols + kTile - 1) / kTile), uint32_t((a.rows + kTile - 1) / kTile));
-    if (a.x_bf16) {
-        if (a.ld % 8 == 0) fp8_quant_kernel<uint16_t, true><<<grid, kThreads, 0, stream>>>(a);
-        else fp8_quant_kernel<uint16_t, false><<<grid, kThreads, 0, stream>>>(a);
-    } else {
-        if (a.ld % 4 == 0) fp8_quant_kernel<float, true><<<grid, kThreads, 0, stream>>>(a);
-        else fp8_quant_kernel<float, false><<<grid, kThreads, 0, stream>>>(a);
-    }
+    if (a.x_bf16) launch<uint16_t>(a, stream);
+    else launch<float>(a, stream);
     return cudaPeekAtLastError();
 }
 
