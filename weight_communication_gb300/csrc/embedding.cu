@@ -12,7 +12,9 @@
 // run.  (1) sort: each CTA owns a run of table rows, reads every id (they sit
 // in L2) and writes the positions of its rows' tokens, in token order, at
 // their sorted places -- a stable counting sort in one launch, because a CTA
-// learns its place in the output by counting the ids below its rows.
+// learns its place in the output by counting the ids below its rows.  It also
+// writes the zeros of its rows without a token: the sort waits on latencies,
+// and leaves the memory idle for them.
 // (2) sum: the sorted tokens are cut into equal runs, one per worker, so that
 // a row with many tokens (Zipf's law) is spread over many workers; a worker
 // writes the rows that lie inside its run and leaves fp32 partial sums of the
@@ -165,13 +167,30 @@ lookup_kernel(const T *__restrict__ table, int64_t ld_table, const I *__restrict
 }
 
 // ---------------------------------------------------------------------------
-// gradient (1): stable counting sort of the tokens by row
+// gradient (1): stable counting sort of the tokens by row, and zero rows
 // ---------------------------------------------------------------------------
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortUnroll = 8;
 constexpr int kSortPitch = kSortWarps + 1;  // counters of a row; odd, so that a warp's
                                             // counters of different rows are in different banks
+
+// Zeros for the rows without a token: bytes of a row, distance of rows, and
+// the widest store that every row allows.  base NULL: none are written.
+struct ZeroRows {
+    char *base;
+    int64_t pitch;
+    uint64_t bytes;
+    uint32_t unit;  // 16, 4 or 2
+};
+
+template <typename W>
+__device__ __forceinline__ void zero_row(char *p, uint64_t bytes, int lane) {
+    const W zero = {};
+    for (uint64_t i = lane * sizeof(W); i < bytes; i += 32 * sizeof(W))
+        __stcs(reinterpret_cast<W *>(p + i), zero);
+}
 
 // order[p], rows[p]: token and row at sorted place p.  row_start[v]: first
 // place of row v; row_start[V]: tokens with a row.  CTA b owns rows
@@ -181,10 +200,11 @@ template <typename I>
 __global__ void __launch_bounds__(kSortThreads)
 sort_kernel(const I *__restrict__ ids, int32_t n, int64_t first, int32_t V, int32_t per_cta,
             int32_t *__restrict__ order, int32_t *__restrict__ rows,
-            int32_t *__restrict__ row_start) {
+            int32_t *__restrict__ row_start, const ZeroRows zeros) {
     extern __shared__ int32_t counters[];
     __shared__ int32_t warp_total[kSortWarps];
     __shared__ int32_t below_total;
+    let_successor_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t lo = int32_t(blockIdx.x) * per_cta;
     const int32_t hi = min(V, lo + per_cta);
@@ -199,11 +219,18 @@ sort_kernel(const I *__restrict__ ids, int32_t n, int64_t first, int32_t V, int3
     const int64_t begin = int64_t(stretch) * warp;
     const int64_t end = begin + stretch < int64_t(n) ? begin + stretch : int64_t(n);
     int32_t below = 0;
-#pragma unroll 4
-    for (int64_t t = begin + lane; t < end; t += 32) {
-        const int64_t r = relative(ids[t], first);
-        if (r >= lo && r < hi) atomicAdd(&counters[int32_t(r - lo) * kSortPitch + warp], 1);
-        else if (r >= 0 && r < lo) ++below;
+    for (int64_t t0 = begin + lane; t0 < end; t0 += 32 * kSortUnroll) {
+        int64_t r[kSortUnroll];
+#pragma unroll
+        for (int u = 0; u < kSortUnroll; ++u) {
+            const int64_t t = t0 + 32 * u;
+            r[u] = t < end ? relative(ids[t], first) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kSortUnroll; ++u) {
+            if (r[u] >= lo && r[u] < hi) atomicAdd(&counters[int32_t(r[u] - lo) * kSortPitch + warp], 1);
+            else if (r[u] >= 0 && r[u] < lo) ++below;
+        }
     }
     below = __reduce_add_sync(kFull, below);
     if (lane == 0) atomicAdd(&below_total, below);
@@ -250,23 +277,40 @@ sort_kernel(const I *__restrict__ ids, int32_t n, int64_t first, int32_t V, int3
     }
     if (hi == V && threadIdx.x == 0) row_start[V] = carry;
 
-    // the same stretch again, in order: equal rows of a step keep lane order
-    for (int64_t t0 = begin; t0 < end; t0 += 32) {
-        const int64_t t = t0 + lane;
-        const int64_t r = t < end ? relative(ids[t], first) : -1;
-        const bool mine = r >= lo && r < hi;
-        const unsigned live = __ballot_sync(kFull, mine);
-        if (mine) {
-            const int32_t k = int32_t(r - lo);
-            const unsigned peers = __match_any_sync(live, k);
-            int32_t *counter = &counters[k * kSortPitch + warp];
-            const int32_t at = base[k] + *counter + __popc(peers & ((1u << lane) - 1u));
-            order[at] = int32_t(t);
-            rows[at] = int32_t(r);
-            __syncwarp(live);
-            if ((peers & ((1u << lane) - 1u)) == 0u) *counter += __popc(peers);
+    if (zeros.base != nullptr) {  // drained by the memory system while the rest runs
+        for (int32_t r = warp; r < own; r += kSortWarps) {
+            if (base[r] != (r + 1 < own ? base[r + 1] : carry)) continue;
+            char *p = zeros.base + int64_t(lo + r) * zeros.pitch;
+            if (zeros.unit == 16) zero_row<uint4>(p, zeros.bytes, lane);
+            else if (zeros.unit == 4) zero_row<uint32_t>(p, zeros.bytes, lane);
+            else zero_row<uint16_t>(p, zeros.bytes, lane);
         }
-        __syncwarp();
+    }
+
+    // the same stretch again, in order: equal rows of a step keep lane order
+    for (int64_t t0 = begin; t0 < end; t0 += 32 * kSortUnroll) {
+        int64_t r[kSortUnroll];
+#pragma unroll
+        for (int u = 0; u < kSortUnroll; ++u) {
+            const int64_t t = t0 + 32 * u + lane;
+            r[u] = t < end ? relative(ids[t], first) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kSortUnroll; ++u) {
+            const bool mine = r[u] >= lo && r[u] < hi;
+            const unsigned live = __ballot_sync(kFull, mine);
+            if (mine) {
+                const int32_t k = int32_t(r[u] - lo);
+                const unsigned peers = __match_any_sync(live, k);
+                int32_t *counter = &counters[k * kSortPitch + warp];
+                const int32_t at = base[k] + *counter + __popc(peers & ((1u << lane) - 1u));
+                order[at] = int32_t(t0 + 32 * u + lane);
+                rows[at] = int32_t(r[u]);
+                __syncwarp(live);
+                if ((peers & ((1u << lane) - 1u)) == 0u) *counter += __popc(peers);
+            }
+            __syncwarp();
+        }
     }
 }
 
@@ -286,14 +330,15 @@ struct SumPlan {
     uint32_t workers;
 };
 
-// Sorted places [begin, end) of a worker.
-__device__ __forceinline__ void run_of(const int32_t *row_start, const SumPlan &p, uint32_t w,
+// Sorted places [begin, end) of a worker; returns the length of a run.
+__device__ __forceinline__ uint32_t run_of(const int32_t *row_start, const SumPlan &p, uint32_t w,
                                        int32_t *begin, int32_t *end) {
     const uint32_t live = uint32_t(row_start[p.V]);
     const uint32_t per = (live + p.workers - 1) / p.workers;
     const uint64_t b = uint64_t(per) * w, e = b + per;
     *begin = int32_t(b < live ? b : live);
     *end = int32_t(e < live ? e : live);
+    return per;
 }
 
 template <typename TO, int E>
@@ -311,20 +356,24 @@ __device__ __forceinline__ void write_row(TO *p, const float acc[E], float scale
 
 // heads, tails: [workers][D] fp32.  heads[w]: the part in run w of a row that
 // began in an earlier run and ends in this one.  tails[w]: the part in run w
-// of a row that goes on in the next run.
+// of a row that goes on in the next run.  joins[w]: the row that heads[w] is a
+// part of (-1: none) and the run it begins in.
 template <typename TI, typename TO, int E>
 __global__ void __launch_bounds__(kSumThreads)
 sum_kernel(const TI *__restrict__ dy, int64_t ld_dy, const int32_t *__restrict__ order,
            const int32_t *__restrict__ rows, const int32_t *__restrict__ row_start, SumPlan p,
            float scale, int accumulate, TO *__restrict__ dtable, int64_t ld_out,
-           float *__restrict__ heads, float *__restrict__ tails) {
+           float *__restrict__ heads, float *__restrict__ tails, int2 *__restrict__ joins) {
     const uint32_t lane = threadIdx.x & (p.lanes - 1);
     const uint32_t w = blockIdx.x * (kSumThreads / p.lanes) + threadIdx.x / p.lanes;
     const uint32_t v = blockIdx.y * p.lanes + lane;
     if (w >= p.workers || v >= p.vecs) return;
     const int64_t col = int64_t(v) * E;
+    let_successor_start();
+    wait_for_predecessor();
     int32_t begin, end;
-    run_of(row_start, p, w, &begin, &end);
+    const uint32_t per = run_of(row_start, p, w, &begin, &end);
+    int2 join = make_int2(-1, 0);
     if (begin < end) {
         const int32_t live = row_start[p.V];
         const int32_t prior = begin > 0 ? rows[begin - 1] : -1;
@@ -348,6 +397,7 @@ sum_kernel(const TI *__restrict__ dy, int64_t ld_dy, const int32_t *__restrict__
                 if (j + u >= end) break;
                 if (r[u] != row) {
                     if (row == prior) {
+                        join = make_int2(row, int32_t(uint32_t(row_start[row]) / per));
 #pragma unroll
                         for (int e = 0; e < E; ++e) heads[int64_t(w) * p.D + col + e] = acc[e];
                     } else {
@@ -365,79 +415,72 @@ sum_kernel(const TI *__restrict__ dy, int64_t ld_dy, const int32_t *__restrict__
 #pragma unroll
             for (int e = 0; e < E; ++e) tails[int64_t(w) * p.D + col + e] = acc[e];
         } else if (row == prior) {
+            join = make_int2(row, int32_t(uint32_t(row_start[row]) / per));
 #pragma unroll
             for (int e = 0; e < E; ++e) heads[int64_t(w) * p.D + col + e] = acc[e];
         } else {
             write_row<TO, E>(dtable + int64_t(row) * ld_out + col, acc, scale, accumulate);
         }
     }
-    if (!accumulate) {  // this worker's share of the rows, zero where no token is
-        const uint32_t per = (uint32_t(p.V) + p.workers - 1) / p.workers;
-        const uint64_t b = uint64_t(per) * w, e = b + per < uint64_t(p.V) ? b + per : uint64_t(p.V);
-        if (b < e) {
-            Pack<TO, E> zero;
-#pragma unroll
-            for (int i = 0; i < Pack<TO, E>::kWords; ++i) zero.w[i] = 0u;
-            int32_t at = row_start[b];
-            for (uint64_t i = b; i < e; ++i) {
-                const int32_t after = row_start[i + 1];
-                if (after == at) store_pack<TO, E>(dtable + int64_t(i) * ld_out + col, zero);
-                at = after;
-            }
-        }
-    }
+    if (blockIdx.y == 0 && lane == 0) joins[w] = join;
 }
 
 // ---------------------------------------------------------------------------
 // gradient (3): rows that cross runs
 // ---------------------------------------------------------------------------
 
-constexpr int kJoinCols = 64;    // columns of a CTA
+constexpr int kJoinLanes = 64;   // threads along the columns, E columns each
 constexpr int kJoinParts = 4;    // threads that share a row's runs
-constexpr int kJoinUnroll = 8;
+constexpr int kJoinUnroll = 4;
 
 // CTA (w, c): if a row that began earlier ends in run w, adds its parts over
 // the runs, split in four consecutive shares that are added in order.
-template <typename TO>
-__global__ void __launch_bounds__(kJoinCols * kJoinParts)
-join_kernel(const int32_t *__restrict__ rows, const int32_t *__restrict__ row_start, SumPlan p,
-            float scale, int accumulate, TO *__restrict__ dtable, int64_t ld_out,
-            const float *__restrict__ heads, const float *__restrict__ tails) {
-    __shared__ float part[kJoinParts][kJoinCols];
+template <typename TO, int E>
+__global__ void __launch_bounds__(kJoinLanes * kJoinParts)
+join_kernel(SumPlan p, float scale, int accumulate, TO *__restrict__ dtable, int64_t ld_out,
+            const float *__restrict__ heads, const float *__restrict__ tails,
+            const int2 *__restrict__ joins) {
+    __shared__ float part[kJoinParts][kJoinLanes * E];
     const uint32_t w = blockIdx.x;
-    int32_t begin, end;
-    run_of(row_start, p, w, &begin, &end);
-    if (begin >= end || begin == 0) return;
-    const int32_t row = rows[begin];
-    if (rows[begin - 1] != row) return;                                  // starts here
-    const int32_t live = row_start[p.V];
-    if (rows[end - 1] == row && end < live && rows[end] == row) return;  // goes on
-    const uint32_t per = uint32_t(live + p.workers - 1) / p.workers;
-    const uint32_t first = uint32_t(row_start[row]) / per;               // run of its first token
-    const uint32_t c = threadIdx.x % kJoinCols, s = threadIdx.x / kJoinCols;
-    const uint32_t col = blockIdx.y * kJoinCols + c;
+    wait_for_predecessor();
+    const int2 join = joins[w];
+    if (join.x < 0) return;
+    const uint32_t first = uint32_t(join.y);
+    const uint32_t c = threadIdx.x % kJoinLanes, s = threadIdx.x / kJoinLanes;
+    const uint32_t col = (blockIdx.y * kJoinLanes + c) * E;
     // parts first .. w - 1 are tails, part w is a head
     const uint32_t count = w - first, share = (count + kJoinParts - 1) / kJoinParts;
     const uint32_t b = first + s * share < w ? first + s * share : w;
     const uint32_t e = b + share < w ? b + share : w;
-    float sum = 0.0f;
+    float sum[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) sum[k] = 0.0f;
     if (col < p.D) {
         for (uint32_t i = b; i < e; i += kJoinUnroll) {
-            float x[kJoinUnroll];
+            Pack<float, E> x[kJoinUnroll];
 #pragma unroll
             for (int u = 0; u < kJoinUnroll; ++u)
-                x[u] = i + u < e ? tails[int64_t(i + u) * p.D + col] : 0.0f;
+                if (i + u < e) x[u] = load_pack<float, E, true>(tails + int64_t(i + u) * p.D + col);
 #pragma unroll
-            for (int u = 0; u < kJoinUnroll; ++u) sum = __fadd_rn(sum, x[u]);
+            for (int u = 0; u < kJoinUnroll; ++u)
+                if (i + u < e) {
+#pragma unroll
+                    for (int k = 0; k < E; ++k) sum[k] = __fadd_rn(sum[k], pack_value<float, E>(x[u], k));
+                }
         }
     }
-    part[s][c] = sum;
+#pragma unroll
+    for (int k = 0; k < E; ++k) part[s][c * E + k] = sum[k];
     __syncthreads();
     if (s != 0 || col >= p.D) return;
+    const Pack<float, E> head = load_pack<float, E, true>(heads + int64_t(w) * p.D + col);
 #pragma unroll
-    for (int i = 1; i < kJoinParts; ++i) sum = __fadd_rn(sum, part[i][c]);
-    const float acc[1] = {__fadd_rn(sum, heads[int64_t(w) * p.D + col])};
-    write_row<TO, 1>(dtable + int64_t(row) * ld_out + col, acc, scale, accumulate);
+    for (int k = 0; k < E; ++k) {
+#pragma unroll
+        for (int i = 1; i < kJoinParts; ++i) sum[k] = __fadd_rn(sum[k], part[i][c * E + k]);
+        sum[k] = __fadd_rn(sum[k], pack_value<float, E>(head, k));
+    }
+    write_row<TO, E>(dtable + int64_t(join.x) * ld_out + col, sum, scale, accumulate);
 }
 
 // ---------------------------------------------------------------------------
@@ -506,20 +549,26 @@ cudaError_t lookup(const void *table, int64_t ld_table, const void *ids, int64_t
 }
 
 template <typename TI, typename TO>
-void launch_sum(const EmbeddingGrad &a, const SumPlan &p, int e, const int32_t *order,
-                const int32_t *rows, const int32_t *row_start, float *heads, float *tails,
-                cudaStream_t stream) {
+cudaError_t launch_sum(const EmbeddingGrad &a, const SumPlan &p, int e, const int32_t *order,
+                       const int32_t *rows, const int32_t *row_start, float *heads, float *tails,
+                       int2 *joins, cudaStream_t stream) {
     const dim3 grid((p.workers + kSumThreads / p.lanes - 1) / (kSumThreads / p.lanes),
                     (p.vecs + p.lanes - 1) / p.lanes);
 #define WC_SUM(E)                                                                             \
-    sum_kernel<TI, TO, E><<<grid, kSumThreads, 0, stream>>>(                                  \
-        static_cast<const TI *>(a.dy), a.ld_dy, order, rows, row_start, p, a.scale,           \
-        a.accumulate ? 1 : 0, static_cast<TO *>(a.dtable), a.ld_out, heads, tails)
-    if (e == 8) WC_SUM(8);
-    else if (e == 4) WC_SUM(4);
-    else if (e == 2) WC_SUM(2);
-    else WC_SUM(1);
+    launch_after(sum_kernel<TI, TO, E>, grid, dim3(kSumThreads), 0, stream,                   \
+                 static_cast<const TI *>(a.dy), a.ld_dy, order, rows, row_start, p, a.scale,  \
+                 a.accumulate ? 1 : 0, static_cast<TO *>(a.dtable), a.ld_out, heads, tails, joins)
+    cudaError_t err = e == 8 ? WC_SUM(8) : e == 4 ? WC_SUM(4) : e == 2 ? WC_SUM(2) : WC_SUM(1);
 #undef WC_SUM
+    if (err != cudaSuccess || a.n < 2) return err;  // one token crosses no run
+    const int je = e >= 4 ? 4 : 1;
+    const dim3 join_grid(p.workers, (p.D + kJoinLanes * je - 1) / (kJoinLanes * je));
+    const dim3 join_block(kJoinLanes * kJoinParts);
+    TO *dtable = static_cast<TO *>(a.dtable);
+    return je == 4 ? launch_after(join_kernel<TO, 4>, join_grid, join_block, 0, stream, p, a.scale,
+                                  a.accumulate ? 1 : 0, dtable, a.ld_out, heads, tails, joins)
+                   : launch_after(join_kernel<TO, 1>, join_grid, join_block, 0, stream, p, a.scale,
+                                  a.accumulate ? 1 : 0, dtable, a.ld_out, heads, tails, joins);
 }
 
 }  // namespace
@@ -540,7 +589,7 @@ int64_t embedding_grad_workspace(const EmbeddingGrad &a) {
     for (int e = 1; e <= 8; e *= 2) {
         if (a.D % e) continue;
         const SumPlan p = plan_of(a, e);
-        const int64_t bytes = 2 * align16(int64_t(p.workers) * p.D * 4);
+        const int64_t bytes = 2 * align16(int64_t(p.workers) * p.D * 4) + align16(int64_t(p.workers) * 8);
         if (bytes > most) most = bytes;
     }
     return 2 * align16(a.n * 4) + align16((a.V + 1) * 4) + most;
@@ -559,6 +608,8 @@ cudaError_t launch_embedding_grad(const EmbeddingGrad &a, cudaStream_t stream) {
     float *heads = reinterpret_cast<float *>(ws);
     ws += align16(int64_t(p.workers) * p.D * 4);
     float *tails = reinterpret_cast<float *>(ws);
+    ws += align16(int64_t(p.workers) * p.D * 4);
+    int2 *joins = reinterpret_cast<int2 *>(ws);
 
     int32_t per_cta = int32_t((a.V + kSms - 1) / kSms);
     if (per_cta > kSortRowsMax) per_cta = kSortRowsMax;
@@ -573,34 +624,28 @@ cudaError_t launch_embedding_grad(const EmbeddingGrad &a, cudaStream_t stream) {
                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             kSortRowsMax * (kSortPitch + 1) * 4);
     if (err != cudaSuccess) return err;
+    ZeroRows zeros = {};
+    if (!a.accumulate) {
+        const int64_t size = a.out_bf16 ? 2 : 4;
+        zeros.base = static_cast<char *>(a.dtable);
+        zeros.pitch = a.ld_out * size;
+        zeros.bytes = uint64_t(a.D * size);
+        const uint64_t both = uint64_t(zeros.pitch) | zeros.bytes;
+        zeros.unit = both % 16 == 0 ? 16 : both % 4 == 0 ? 4 : 2;
+    }
     if (a.wide)
         sort_kernel<int64_t><<<sort_grid, kSortThreads, smem, stream>>>(
-            static_cast<const int64_t *>(a.ids), p.n, a.first, p.V, per_cta, order, rows, row_start);
+            static_cast<const int64_t *>(a.ids), p.n, a.first, p.V, per_cta, order, rows, row_start, zeros);
     else
         sort_kernel<int32_t><<<sort_grid, kSortThreads, smem, stream>>>(
-            static_cast<const int32_t *>(a.ids), p.n, a.first, p.V, per_cta, order, rows, row_start);
+            static_cast<const int32_t *>(a.ids), p.n, a.first, p.V, per_cta, order, rows, row_start, zeros);
     err = cudaPeekAtLastError();
-    if (err != cudaSuccess) return err;
-
-    if (a.dy_bf16) {
-        if (a.out_bf16) launch_sum<uint16_t, uint16_t>(a, p, e, order, rows, row_start, heads, tails, stream);
-        else launch_sum<uint16_t, float>(a, p, e, order, rows, row_start, heads, tails, stream);
-    } else {
-        if (a.out_bf16) launch_sum<float, uint16_t>(a, p, e, order, rows, row_start, heads, tails, stream);
-        else launch_sum<float, float>(a, p, e, order, rows, row_start, heads, tails, stream);
-    }
-    err = cudaPeekAtLastError();
-    if (err != cudaSuccess || a.n < 2) return err;
-    const dim3 grid(p.workers, (p.D + kJoinCols - 1) / kJoinCols);
-    if (a.out_bf16)
-        join_kernel<uint16_t><<<grid, kJoinCols * kJoinParts, 0, stream>>>(
-            rows, row_start, p, a.scale, a.accumulate ? 1 : 0, static_cast<uint16_t *>(a.dtable),
-            a.ld_out, heads, tails);
-    else
-        join_kernel<float><<<grid, kJoinCols * kJoinParts, 0, stream>>>(
-            rows, row_start, p, a.scale, a.accumulate ? 1 : 0, static_cast<float *>(a.dtable),
-            a.ld_out, heads, tails);
-    return cudaPeekAtLastError();
+    if (err != cudaSuccess || a.n == 0) return err;
+    if (a.dy_bf16)
+        return a.out_bf16 ? launch_sum<uint16_t, uint16_t>(a, p, e, order, rows, row_start, heads, tails, joins, stream)
+                          : launch_sum<uint16_t, float>(a, p, e, order, rows, row_start, heads, tails, joins, stream);
+    return a.out_bf16 ? launch_sum<float, uint16_t>(a, p, e, order, rows, row_start, heads, tails, joins, stream)
+                      : launch_sum<float, float>(a, p, e, order, rows, row_start, heads, tails, joins, stream);
 }
 
 }  // namespace wc
