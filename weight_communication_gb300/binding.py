@@ -8,6 +8,7 @@ is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from pathlib import Path
@@ -145,9 +146,12 @@ def wait_timeouts(reset: bool = False) -> int:
 def _call(device: torch.device, name: str, *args) -> None:
     """Calls the entry point with the tensors' GPU as the current device (the
     kernels launch on the current device)."""
-    lib = load()
-    with torch.cuda.device(device):
+    lib = _lib or load()
+    if device.type != "cuda" or torch.cuda.current_device() == device.index:
         rc = getattr(lib, name)(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(lib, name)(*args)
     if rc != WC_OK:
         raise WcError(name, rc, lib.wc_last_error().decode())
 
@@ -160,6 +164,16 @@ def _stream(t: torch.Tensor, stream: torch.cuda.Stream | None):
     if stream.device != t.device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _raw_stream(device: torch.device, stream: torch.cuda.Stream | None) -> int:
+    """_stream as an integer, by the shortest way: the training-step calls are
+    made many times per step."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return stream.cuda_stream
 
 
 def _dev(t: torch.Tensor | None, name: str, dtype: torch.dtype, numel: int, device=None):
@@ -360,6 +374,15 @@ def sr_accumulate_bf16(dst: torch.Tensor, src: torch.Tensor, seed: int, step: in
           _stream(dst, stream))
 
 
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def allocating_on(stream: torch.cuda.Stream | None):
+    """Context in which new tensors belong to `stream`; without one they
+    belong to the current stream, which is where the call goes."""
+    return _NO_CONTEXT if stream is None else torch.cuda.stream(stream)
+
+
 def _float_type(t: torch.Tensor, name: str) -> int:
     if t.dtype == torch.float32:
         return WC_F32
@@ -375,14 +398,17 @@ def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, device=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < cols:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] < cols:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected ({rows}, {cols})")
+    ld, step = t.stride()
+    if shape[1] > 1 and step != 1:
         raise ValueError(f"{name} must have consecutive values in a row")
-    ld = t.stride(0) if rows > 1 else t.shape[1]
-    if ld < t.shape[1]:
+    if rows <= 1:
+        ld = shape[1]
+    elif ld < shape[1]:
         raise ValueError(f"{name} must not have overlapping rows")
-    return ctypes.c_void_p(t.data_ptr()), ld
+    return t.data_ptr(), ld
 
 
 def spans(tensors, name: str = "tensors"):
@@ -416,7 +442,7 @@ def grad_norm(span_array, count: int, stats: torch.Tensor, workspace: torch.Tens
     d = stats.device
     _call(d, "wc_grad_norm", span_array, count, _dev(stats, "stats", torch.float32, 1, d),
           _dev(workspace, "workspace", torch.uint8, workspace.numel(), d), workspace.numel(),
-          _stream(stats, stream))
+          _raw_stream(d, stream))
 
 
 def grad_clip(span_array, dst_array, count: int, max_norm: float, eps: float,
@@ -427,7 +453,7 @@ def grad_clip(span_array, dst_array, count: int, max_norm: float, eps: float,
     _call(d, "wc_grad_clip", span_array, dst_array, count, max_norm, eps,
           _dev(stats, "stats", torch.float32, 2, d),
           _dev(workspace, "workspace", torch.uint8, workspace.numel(), d), workspace.numel(),
-          _stream(stats, stream))
+          _raw_stream(d, stream))
 
 
 def _ids(ids: torch.Tensor, device) -> tuple:
@@ -451,7 +477,7 @@ def embedding(table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, scale: 
         raise TypeError(f"out must be {table.dtype}, got {out.dtype}")
     op, ld_out = _matrix(out, "out", ids.numel(), D, d)
     _call(d, "wc_embedding", tp, _float_type(table, "table"), max(ld_table, D), ip, it,
-          ids.numel(), first_row, V, D, scale, op, max(ld_out, D), _stream(table, stream))
+          ids.numel(), first_row, V, D, scale, op, max(ld_out, D), _raw_stream(d, stream))
 
 
 def embedding_grad_workspace(n: int, V: int, D: int) -> int:
@@ -481,7 +507,7 @@ def embedding_grad(dy: torch.Tensor, ids: torch.Tensor, dtable: torch.Tensor,
     _call(d, "wc_embedding_grad", yp, _float_type(dy, "dy"), max(ld_dy, D), ip, it, n, first_row,
           V, D, scale, 1 if accumulate else 0, op, _float_type(dtable, "dtable"), max(ld_out, D),
           _dev(workspace, "workspace", torch.uint8, workspace.numel(), d), workspace.numel(),
-          _stream(dy, stream))
+          _raw_stream(d, stream))
 
 
 def _fp8_part(codes, scales, name: str, rows: int, cols: int, square: bool, device,
@@ -520,7 +546,7 @@ def fp8_quant(x: torch.Tensor, codes: torch.Tensor | None, scales: torch.Tensor 
     q, ldq, s, lds = _fp8_part(codes, scales, "row", rows, cols, square, d, True)
     qt, ldqt, st, ldst = _fp8_part(codes_t, scales_t, "transposed", cols, rows, square, d, True)
     _call(d, "wc_fp8_quant", xp, _float_type(x, "x"), rows, cols, max(ld, cols), 1 if square else 0,
-          q, ldq, s, lds, qt, ldqt, st, ldst, _stream(x, stream))
+          q, ldq, s, lds, qt, ldqt, st, ldst, _raw_stream(d, stream))
 
 
 def fp8_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, a_rows_per_scale: int,
@@ -535,4 +561,4 @@ def fp8_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, a_rows_per_scale: 
     op, ld_out = _matrix(out, "out", M, N, d)
     _call(d, "wc_fp8_matmul", ap, lda, sap, ldsa, a_rows_per_scale, bp, ldb, sbp, ldsb,
           b_rows_per_scale, M, N, K, op, _float_type(out, "out"), max(ld_out, N),
-          1 if accumulate else 0, _stream(a_codes, stream))
+          1 if accumulate else 0, _raw_stream(d, stream))

@@ -31,12 +31,11 @@ def lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, first_row
     flat = _flat(ids)
     if table.dim() != 2:
         raise ValueError(f"table must be a matrix, got shape {tuple(table.shape)}")
-    s = stream if stream is not None else torch.cuda.current_stream(table.device)
     given = out
     if out is None:
-        with torch.cuda.stream(s):
+        with binding.allocating_on(stream):
             out = torch.empty(flat.numel(), table.shape[1], dtype=table.dtype, device=table.device)
-    binding.embedding(table, flat, out, scale, first_row, s)
+    binding.embedding(table, flat, out, scale, first_row, stream)
     return out.view(*ids.shape, table.shape[1]) if given is None else out
 
 
@@ -52,18 +51,17 @@ def grad(dy: torch.Tensor, ids: torch.Tensor, rows: int, scale: float = 1.0, fir
         if dy.shape[:-1] != ids.shape or not dy.is_contiguous():
             raise ValueError(f"dy has shape {tuple(dy.shape)}, expected {(*ids.shape, D)}, contiguous")
         dy = dy.view(-1, D)
-    s = stream if stream is not None else torch.cuda.current_stream(dy.device)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs the gradient to add to as out")
-        with torch.cuda.stream(s):
+        with binding.allocating_on(stream):
             out = torch.empty(rows, D, dtype=out_dtype or dy.dtype, device=dy.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
     elif out.dim() != 2 or out.shape[0] != rows:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected ({rows}, {D})")
-    with torch.cuda.stream(s):
+    with binding.allocating_on(stream):
         workspace = torch.empty(max(16, binding.embedding_grad_workspace(flat.numel(), rows, D)),
                                 dtype=torch.uint8, device=dy.device)
-    binding.embedding_grad(dy, flat, out, workspace, scale, first_row, accumulate, s)
+    binding.embedding_grad(dy, flat, out, workspace, scale, first_row, accumulate, stream)
     return out

@@ -52,10 +52,6 @@ class Fp8Tensor:
                                device=device), rows, cols, block_rows)
 
 
-def _current(t: torch.Tensor, stream):
-    return stream if stream is not None else torch.cuda.current_stream(t.device)
-
-
 def quantize(x: torch.Tensor, rows: bool = True, columns: bool = False, stream=None):
     """x [M, K] (bf16 or fp32) as (x, x^T): an Fp8Tensor [M, K] with a scale per
     128 columns of a row (None unless `rows`) and an Fp8Tensor [K, M] with a
@@ -75,11 +71,10 @@ def _quantize(x, rows, columns, block_rows, stream):
     if not (rows or columns):
         raise ValueError("neither rows nor columns asked for")
     M, K = x.shape
-    s = _current(x, stream)
-    with torch.cuda.stream(s):
+    with binding.allocating_on(stream):
         q = Fp8Tensor.empty(M, K, block_rows, x.device) if rows else None
         qt = Fp8Tensor.empty(K, M, block_rows, x.device) if columns else None
-    _quantize_into(x, q, qt, block_rows, s)
+    _quantize_into(x, q, qt, block_rows, stream)
     return q, qt
 
 
@@ -96,16 +91,15 @@ def matmul(a: Fp8Tensor, b: Fp8Tensor, out: torch.Tensor | None = None,
     or `out`; with accumulate, added to what `out` holds."""
     if a.cols != b.cols:
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
-    s = _current(a.codes, stream)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs the matrix to add to as out")
-        with torch.cuda.stream(s):
+        with binding.allocating_on(stream):
             out = torch.empty(a.rows, b.rows, dtype=out_dtype, device=a.codes.device)
     elif out.dim() != 2 or tuple(out.shape) != (a.rows, b.rows):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected ({a.rows}, {b.rows})")
     binding.fp8_matmul(a.codes, a.scales, a.block_rows, b.codes, b.scales, b.block_rows, a.cols,
-                       out, accumulate, s)
+                       out, accumulate, stream)
     return out
 
 
@@ -123,7 +117,7 @@ class Fp8Linear:
         """Quantizes new values of the weight into the same buffers."""
         if tuple(weight.shape) != (self.N, self.K):
             raise ValueError(f"weight has shape {tuple(weight.shape)}, expected ({self.N}, {self.K})")
-        _quantize_into(weight, self.w, self.wt, BLOCK, _current(weight, stream))
+        _quantize_into(weight, self.w, self.wt, BLOCK, stream)
 
     def forward(self, x: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
                 save: bool = False, stream=None):

@@ -38,22 +38,21 @@ def _listed(tensors) -> TensorList:
 def _buffers(lst: TensorList, stats: torch.Tensor | None, n: int, stream):
     if lst.device is None:
         raise ValueError("an empty list has no GPU to run on")
-    s = stream if stream is not None else torch.cuda.current_stream(lst.device)
-    if s.device != lst.device:
-        raise ValueError(f"stream is on {s.device}, the tensors on {lst.device}")
-    with torch.cuda.stream(s):
+    if stream is not None and stream.device != lst.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {lst.device}")
+    with binding.allocating_on(stream):
         if stats is None:
             stats = torch.empty(n, dtype=torch.float32, device=lst.device)
         workspace = torch.empty(lst.workspace_bytes, dtype=torch.uint8, device=lst.device)
-    return s, stats, workspace
+    return stats, workspace
 
 
 def norm(tensors, stats: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The norm of a TensorList or a list of tensors, as stats [1] fp32 on the
     device.  Runs on `stream` or the current one."""
     lst = _listed(tensors)
-    s, stats, workspace = _buffers(lst, stats, 1, stream)
-    binding.grad_norm(lst.spans, len(lst), stats, workspace, s)
+    stats, workspace = _buffers(lst, stats, 1, stream)
+    binding.grad_norm(lst.spans, len(lst), stats, workspace, stream)
     return stats
 
 
@@ -69,7 +68,7 @@ def clip(tensors, max_norm: float, out=None, eps: float = 1e-6,
         raise ValueError(f"out has {len(dst)} tensors, expected {len(lst)}")
     if dst is not None and dst.device != lst.device:
         raise ValueError(f"out is on {dst.device}, expected {lst.device}")
-    s, stats, workspace = _buffers(lst, stats, 2, stream)
+    stats, workspace = _buffers(lst, stats, 2, stream)
     binding.grad_clip(lst.spans, None if dst is None else dst.spans, len(lst), float(max_norm),
-                      float(eps), stats, workspace, s)
+                      float(eps), stats, workspace, stream)
     return stats
