@@ -555,7 +555,7 @@ cudaError_t launch_sum(const EmbeddingGrad &a, const SumPlan &p, int e, const in
     const dim3 grid((p.workers + kSumThreads / p.lanes - 1) / (kSumThreads / p.lanes),
                     (p.vecs + p.lanes - 1) / p.lanes);
 #define WC_SUM(E)                                                                             \
-    launch_after(sum_kernel<TI, TO, E>, grid, dim3(kSumThreads), 0, stream,                   \
+    launch_after(sum_kernel<TI, TO, E>, grid, dim3(kSumThreads), 0, stream, 1,                   \
                  static_cast<const TI *>(a.dy), a.ld_dy, order, rows, row_start, p, a.scale,  \
                  a.accumulate ? 1 : 0, static_cast<TO *>(a.dtable), a.ld_out, heads, tails, joins)
     cudaError_t err = e == 8 ? WC_SUM(8) : e == 4 ? WC_SUM(4) : e == 2 ? WC_SUM(2) : WC_SUM(1);
@@ -565,9 +565,9 @@ cudaError_t launch_sum(const EmbeddingGrad &a, const SumPlan &p, int e, const in
     const dim3 join_grid(p.workers, (p.D + kJoinLanes * je - 1) / (kJoinLanes * je));
     const dim3 join_block(kJoinLanes * kJoinParts);
     TO *dtable = static_cast<TO *>(a.dtable);
-    return je == 4 ? launch_after(join_kernel<TO, 4>, join_grid, join_block, 0, stream, p, a.scale,
+    return je == 4 ? launch_after(join_kernel<TO, 4>, join_grid, join_block, 0, stream, 1, p, a.scale,
                                   a.accumulate ? 1 : 0, dtable, a.ld_out, heads, tails, joins)
-                   : launch_after(join_kernel<TO, 1>, join_grid, join_block, 0, stream, p, a.scale,
+                   : launch_after(join_kernel<TO, 1>, join_grid, join_block, 0, stream, 1, p, a.scale,
                                   a.accumulate ? 1 : 0, dtable, a.ld_out, heads, tails, joins);
 }
 

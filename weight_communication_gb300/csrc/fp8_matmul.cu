@@ -13,11 +13,20 @@
 // on the next buffers.  The inner sum of 128 products is the tensor core's
 // fp32 accumulation; every sum beyond it is an fp32 fma.
 //
-// A persistent CTA has one TMA thread, one MMA thread and one or two
-// warpgroups of epilogue; the three run ahead of one another across tiles.
-// The operand with its rows on the MMA's 128 rows is called i, the one on its
-// NT columns j.  Few rows of `a` (decoding, short batches) go on j, with the
-// weights on i, so the tensor core's 128 rows are full either way.
+// A persistent CTA has a TMA warp, an MMA warp, a warp that brings scales, and
+// one or two warpgroups of epilogue; they run ahead of one another across
+// tiles.  The operand with its rows on the MMA's 128 rows is called i, the one
+// on its NT columns j.  Few rows of `a` (decoding, short batches) go on j, with
+// the weights on i, so the tensor core's rows are full either way.
+//
+// What bounds it: a step keeps half of the TMEM from its products' issue until
+// its epilogue has read it -- 512 cycles of products, 190 until their end is
+// seen, 380 of reading, 280 until the MMA warp has seen that and issued again --
+// so two steps in flight fill the tensor core for 1024 cycles of every 1400.
+// 8192 x 11008 x 4096 (weights, one scale per 128 x 128): 0.278 ms, 2.66
+// PFLOP/s; 4096 x 5504 x 2048 with a scale per row on both sides (a weight's
+// gradient): 63 us, bound by the fp32 units, which have two operations per
+// product of scales there.
 #include <cuda.h>
 
 #include "wc_device.cuh"
@@ -37,6 +46,18 @@ __device__ __forceinline__ uint32_t smem_of(const void *p) {
     return uint32_t(__cvta_generic_to_shared(p));
 }
 
+// One lane of a converged warp.  (The loops of the TMA and MMA warps are run by
+// all lanes alike, so their counters and descriptors are uniform registers.)
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "elect.sync _|p, 0xFFFFFFFF;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(r));
+    return r != 0;
+}
+
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
@@ -53,26 +74,33 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
-// Waits for the phase of that parity to end.  A wait that does not end within
-// about two seconds is given up: the role that sees it returns, the others
-// run out in turn, and the count of such waits is left for the host.
-__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
+// A converged warp waits for the phase of that parity to end.  A wait that does
+// not end within about two seconds is given up: the role that sees it returns,
+// the others run out in turn, and the count of such waits is left for the host.
+// (The vote makes the answer, and the branch on it, uniform.)
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+    if (__all_sync(kFull, mbar_try(bar, parity))) return true;
     unsigned long long start, now;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(start));
     for (uint32_t i = 0; i < (1u << 28); ++i) {
-        if (mbar_try(bar, parity)) return true;
+        if (__all_sync(kFull, mbar_try(bar, parity))) return true;
         if ((i & 63u) == 63u) {
             asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
-            if (now - start > 2000000000ull) break;
+            if (__any_sync(kFull, now - start > 2000000000ull)) break;
         }
     }
-    atomicAdd(&g_wait_timeouts, 1u);
+    if (elected()) atomicAdd(&g_wait_timeouts, 1u);
+    __syncwarp();
     return false;
 }
 
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-    if (mbar_try(bar, parity)) return true;
-    return mbar_wait_slow(bar, parity);
+// 16 bytes, those past `bytes` zero.
+__device__ __forceinline__ void copy16(uint32_t dst, const float *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void copy4(uint32_t dst, const float *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
@@ -84,30 +112,107 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// x: byte of the row (a multiple of 128 here), y: row.
+// The address of the same shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+// What it hands over is TMEM, ordered by the tcgen05 fences; a release at
+// cluster scope would wait for all of the thread's memory accesses (1300
+// cycles measured, against 70).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void buffer_free(uint32_t bar) {
+    if (PAIR) mbar_arrive_cluster(bar);
+    else mbar_arrive(bar);
+}
+
+// x: byte of the row (a multiple of 128 here), y: row.  PAIR: the barrier may
+// be the other CTA's.
+template <bool PAIR>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, uint32_t bar,
                                          int32_t x, int32_t y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(map), "r"(bar), "r"(x), "r"(y)
-        : "memory");
+    if (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+            "l"(map), "r"(bar), "r"(x), "r"(y)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+            "l"(map), "r"(bar), "r"(x), "r"(y)
+            : "memory");
 }
 
+__device__ __forceinline__ void wait_ms(unsigned int ms) {
+    unsigned long long start, now;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(start));
+    for (uint32_t i = 0; i < (1u << 28); ++i) {
+        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+        if (now - start > ms * 1000000ull) break;
+    }
+}
+
+template <bool PAIR>
 __device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                         uint32_t add) {
-    asm volatile(
-        "{\n.reg .pred p;\n"
-        "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(add)
-        : "memory");
+    if (PAIR)
+        asm volatile(
+            "{\n.reg .pred p;\n"
+            "setp.ne.b32 p, %4, 0;\n"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n.reg .pred p;\n"
+            "setp.ne.b32 p, %4, 0;\n"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(add)
+            : "memory");
 }
 
+// Arrives on the barrier (PAIR: on both CTAs') when the products issued so far
+// have ended.
+template <bool PAIR>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
+    if (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+            "[%0], %1;" ::"r"(bar),
+            "h"(uint16_t(3))
+            : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+            : "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+    if (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    if (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
 }
 
 __device__ __forceinline__ void tc_before_sync() {
@@ -130,7 +235,7 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
-                 : "memory");
+                 :);
 }
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
     asm volatile(
@@ -143,7 +248,17 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                  :
-                 : "memory");
+                 :);
+}
+
+// 16 lanes x 32 columns: registers 4g .. 4g + 3 of lane l hold row l / 4, columns
+// 8g + 2 (l % 4) and the next one, and the same columns of row l / 4 + 8.
+__device__ __forceinline__ void tmem_load_fragment(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
 }
 
 // Shared-memory operand descriptor: rows of 128 bytes, 128-byte swizzle,
@@ -154,10 +269,9 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
-// Instruction descriptor: fp32 accumulators, e4m3 x e4m3, both K-major,
-// M = 128, N = nt.
-__host__ __device__ constexpr uint32_t instr_desc(int nt) {
-    return (1u << 4) | (uint32_t(nt >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+// Instruction descriptor: fp32 accumulators, e4m3 x e4m3, both K-major.
+__host__ __device__ constexpr uint32_t instr_desc(int m, int nt) {
+    return (1u << 4) | (uint32_t(nt >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
 
 // ---------------------------------------------------------------------------
@@ -175,25 +289,43 @@ constexpr int kStagingBytes = 32 * kStagingPitch;
 
 template <int NT>
 struct Shape {
-    static constexpr int kGroups = NT == 256 ? 2 : 1;  // epilogue warpgroups
+    static constexpr int kGroups = NT >= 128 ? 2 : 1;  // epilogue warpgroups
     static constexpr int kCols = NT / kGroups;         // columns of one
     static constexpr int kBuffers = NT == 256 ? 2 : 4;
     static constexpr int kTmemCols = kBuffers * NT;
     static constexpr int kChunk = kCols < 32 ? 16 : 32;  // columns of one TMEM load
-    static constexpr int kStageBytes = (kRows + NT) * kBlock;
-    static constexpr int kStages = NT == 256 ? 4 : NT == 128 ? 6 : 8;
+    // NT = 256: two CTAs on neighbouring SMs share a tile of 256 x 256.  Each
+    // holds the sums of its own 128 rows of i and brings half the rows of j;
+    // the first one's MMA thread multiplies for both.  A lone CTA would need
+    // 48 KB per step where each of the pair needs 32 KB, and L2 to shared
+    // memory, with the copies and the products sharing shared memory's port,
+    // has less to do.  (Alone, 128 x 256 tiles: 8192 x 11008 x 4096 in 0.283 ms
+    // at best without any epilogue work; pairs with it: 0.278 ms.)
+    static constexpr bool kPair = NT == 256;
+    static constexpr int kRowsJ = kPair ? NT / 2 : NT;  // rows of j that this CTA brings
+    static constexpr int kStageBytes = (kRows + kRowsJ) * kBlock;
+    static constexpr int kStages = NT >= 128 ? 6 : 8;
     // two epilogue warpgroups need more than a third of the registers each, so
     // the TMA and MMA warps are part of a full warpgroup that gives its up
-    static constexpr bool kSplitRegs = kGroups == 2;
-    static constexpr int kThreads = kGroups * 128 + (kSplitRegs ? 128 : 64);
-    // stages, one staging buffer per epilogue warp, and room to align
-    static constexpr int kSmem = kStages * kStageBytes + kGroups * 4 * kStagingBytes + 1024;
+    static constexpr bool kSplitRegs = NT == 256;
+    static constexpr int kThreads = kGroups * 128 + 128;
+    // Scales of a step (i's rows, then j's columns) come to shared memory three
+    // steps ahead, a latency from L2 that one step does not cover.  Copies for
+    // step c wait for the product of step c - kScaleSlots + kBuffers + 1, which
+    // began after every warp had left the scales of step c - kScaleSlots.
+    static constexpr int kScales = kRows + NT;
+    static constexpr int kAhead = 3;
+    static constexpr int kScaleSlots = kAhead + kBuffers + 3;
+    // stages, one staging buffer per epilogue warp, scales, and room to align
+    static constexpr int kScalesAt = kStages * kStageBytes + kGroups * 4 * kStagingBytes;
+    static constexpr int kSmem = kScalesAt + kScaleSlots * kScales * 4 + 1024;
 };
 
 struct Side {
     const float *s;
     int64_t ld_s;
     int shift;      // rows per scale: 1 << shift
+    int quads;      // four rows' scales are 16 aligned bytes
     int32_t rows;
 };
 
@@ -204,6 +336,45 @@ struct Args {
     void *out;
     int64_t ld_out;
     int out_bf16, accumulate, vector_out;
+};
+
+// A warp's part in copying the scales of ROWS rows of a tile, block after block:
+// four consecutive rows per lane where the layout allows, else one by one.
+// Rows past the operand's end get a scale that no stored output uses.
+template <int ROWS>
+struct ScaleRows {
+    static constexpr int kSingles = (ROWS + 31) / 32, kQuads = (ROWS + 127) / 128;
+    const float *p[kSingles];
+    uint32_t bytes[kQuads];
+    __device__ __forceinline__ void start(const Side &s, int32_t row0, int step, int lane) {
+        if (ROWS >= 16 && s.quads) {
+#pragma unroll
+            for (int r = 0; r < kQuads; ++r) {
+                const int32_t row = row0 + 128 * r + 4 * lane, left = s.rows - row;
+                p[r] = s.s + (left > 0 ? row : 0);
+                bytes[r] = left >= 4 ? 16u : left > 0 ? 4u * left : 0u;
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < kSingles; ++r)
+                p[r] = s.s + (min(row0 + (32 * r + lane) * step, s.rows - 1) >> s.shift);
+        }
+    }
+    __device__ __forceinline__ void copy(const Side &s, uint32_t to, int lane) {
+        if (ROWS >= 16 && s.quads) {
+#pragma unroll
+            for (int r = 0; r < kQuads; ++r) {
+                if (ROWS >= 128 || lane < ROWS / 4) copy16(to + r * 512 + lane * 16, p[r], bytes[r]);
+                p[r] += s.ld_s;
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < kSingles; ++r) {
+                if (ROWS >= 32 || lane < ROWS) copy4(to + r * 128 + lane * 4, p[r]);
+                p[r] += s.ld_s;
+            }
+        }
+    }
 };
 
 // Tile order: bands of 16 tiles of i, all of j within a band, so that the CTAs
@@ -232,9 +403,9 @@ __device__ __forceinline__ void put(const Args &a, int64_t at, float x) {
 // A warp's 32 rows x COLS columns of a tile (one row per lane) to out [i][j],
 // through shared memory: a lane's row is 64 bytes wide there, and the warp
 // writes 64 consecutive bytes of 8 rows at a time, where a store straight from
-// the registers would touch 32 rows (measured on 8192 x 11008 x 4096 together
-// with the chunked TMEM reads: 0.337 -> 0.306 ms).
-template <int COLS, bool BF16>
+// the registers would touch 32 rows (8192 x 11008 x 4096, with the chunked
+// TMEM reads: 0.337 -> 0.306 ms).
+template <int COLS, bool BF16, bool FRAGMENT>
 __device__ __forceinline__ void store_rows(const Args &a, const f32x2 (&acc)[COLS / 2],
                                            uint8_t *staging, int32_t row0, int32_t j0, int lane) {
     constexpr int W = BF16 ? 32 : 16;  // columns of a pass
@@ -244,28 +415,46 @@ __device__ __forceinline__ void store_rows(const Args &a, const f32x2 (&acc)[COL
     for (int c0 = 0; c0 < COLS; c0 += W) {
         const int32_t cols = a.j.rows - (j0 + c0);  // of this pass and later ones
         if (cols <= 0 || rows <= 0) break;
+        if (FRAGMENT) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t w[4];
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (BF16) {
+                for (int g = 0; g < W / 8; ++g) {
                     float x, y;
-                    unpack2(acc[(c0 + q * 8) / 2 + k], x, y);
-                    w[k] = f32x2_to_bf16x2_bits(x, y);
-                } else if (k % 2 == 0) {
-                    float x, y;
-                    unpack2(acc[(c0 + q * 4 + k) / 2], x, y);
-                    w[k] = __float_as_uint(x);
-                    w[k + 1] = __float_as_uint(y);
+                    unpack2(acc[r * (COLS / 8) + c0 / 8 + g], x, y);
+                    uint8_t *to = staging + (8 * r + lane / 4) * kStagingPitch + (8 * g + 2 * (lane & 3)) * SIZE;
+                    if (BF16) *reinterpret_cast<uint32_t *>(to) = f32x2_to_bf16x2_bits(x, y);
+                    else *reinterpret_cast<float2 *>(to) = make_float2(x, y);
                 }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float x, y;
+                    if (BF16) {
+                        unpack2(acc[(c0 + q * 8) / 2 + k], x, y);
+                        w[k] = f32x2_to_bf16x2_bits(x, y);
+                    } else if (k % 2 == 0) {
+                        unpack2(acc[(c0 + q * 4 + k) / 2], x, y);
+                        w[k] = __float_as_uint(x);
+                        w[k + 1] = __float_as_uint(y);
+                    }
+                }
+                *reinterpret_cast<uint4 *>(staging + lane * kStagingPitch + q * 16) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
             }
-            *reinterpret_cast<uint4 *>(staging + lane * kStagingPitch + q * 16) =
-                make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
         char *base = static_cast<char *>(a.out) + (int64_t(row0) * a.ld_out + j0 + c0) * SIZE;
-        if (a.vector_out && cols >= W) {
+        if (FRAGMENT && a.accumulate) {  // (fp32 sums here, W = 16)
+            const int c = lane % 16;
+            for (int r = lane / 16; r < 32 && r < rows; r += 2)
+                if (c < cols)
+                    put(a, (int64_t(row0) + r) * a.ld_out + j0 + c0 + c,
+                        *reinterpret_cast<const float *>(staging + r * kStagingPitch + c * 4));
+        } else if (a.vector_out && cols >= W) {
             const int r0 = lane >> 2, seg = (lane & 3) * 16;
 #pragma unroll
             for (int r = r0; r < 32; r += 8)
@@ -307,38 +496,41 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
 fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_constant__ CUtensorMap map_j,
                   const Args a) {
     using S = Shape<NT>;
+    constexpr bool kPair = S::kPair;
+    constexpr int kTileRows = kPair ? 2 * kRows : kRows;
+    constexpr bool kFragment = VECJ && NT == 256;  // TMEM is read in fragments
+    constexpr int kProducer = S::kGroups * 4, kMma = kProducer + 1, kScaler = kProducer + 2;
     extern __shared__ uint8_t dynamic_smem[];
-    __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[S::kBuffers],
-        acc_empty[S::kBuffers], drained;
+    // full[stage]: the step's operands are here, and the TMEM buffer it goes to
+    // is free.  done[stage]: its product is complete, and its scales are here.
+    // (One barrier to wait for and one to arrive on keep the MMA thread's work
+    // beside the products short: the queue of products is two deep.)
+    __shared__ uint64_t full[S::kStages], done[S::kStages], drained;
     __shared__ uint32_t tmem_slot;
-    __shared__ __align__(16) float sj_smem[VECJ ? S::kGroups : 1][2][VECJ ? S::kCols : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kProducer = S::kGroups * 4, kMma = kProducer + 1;
     const uint32_t stages = (smem_of(dynamic_smem) + 1023u) & ~1023u;
+    uint8_t *const aligned_smem = dynamic_smem + (stages - smem_of(dynamic_smem));
+    float *const scales = reinterpret_cast<float *>(aligned_smem + S::kScalesAt);
     const int32_t tiles = a.tiles_i * a.tiles_j;
+    // the CTAs of a pair are neighbours in the grid and work on one tile
+    const int32_t rank = kPair ? int32_t(blockIdx.x & 1) : 0;
+    const int32_t first_tile = kPair ? int32_t(blockIdx.x >> 1) : int32_t(blockIdx.x);
+    const int32_t tile_step = kPair ? int32_t(gridDim.x >> 1) : int32_t(gridDim.x);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
-            mbar_init(smem_of(&full[s]), 1);
-            mbar_init(smem_of(&empty[s]), 1);
-        }
-        for (int b = 0; b < S::kBuffers; ++b) {
-            mbar_init(smem_of(&acc_full[b]), 1);
-            mbar_init(smem_of(&acc_empty[b]), S::kGroups * 4);
+            mbar_init(smem_of(&full[s]), 1 + S::kGroups * 4 * (kPair ? 2 : 1));
+            mbar_init(smem_of(&done[s]), 2);
         }
         mbar_init(smem_of(&drained), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == kMma) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_of(&tmem_slot)),
-                     "r"(uint32_t(S::kTmemCols))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
+    __syncwarp();
+    if (warp == kMma) tmem_alloc<kPair>(smem_of(&tmem_slot), S::kTmemCols);
     tc_before_sync();
     __syncthreads();
+    if (kPair) cluster_sync();  // the other CTA's barriers are ready too
     tc_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&tmem_slot);
     wait_for_predecessor();  // all above is set-up that reads no operand
@@ -347,108 +539,192 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
     // 64512 = 384 x 168
     if (warp >= kProducer) {
         if (S::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == kProducer && lane == 0) {
-            uint32_t stage = 0, phase = 0, issued = 0;
+        if (warp == kProducer) {
+            uint32_t stage = 0, phase = 0;
             bool ok = true;
-            for (int32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            for (int32_t t = first_tile; ok && t < tiles; t += tile_step) {
                 int32_t ti, tj;
                 tile_at(a, t, &ti, &tj);
                 for (int32_t kb = 0; kb < a.blocks; ++kb) {
-                    if (!mbar_wait(smem_of(&empty[stage]), phase ^ 1u)) {
-                        ok = false;
-                        break;
+                    ok = mbar_wait(smem_of(&done[stage]), phase ^ 1u);
+                    if (!ok) break;
+                    if (elected()) {
+                        // the first CTA's barrier counts the bytes of both
+                        const uint32_t local = smem_of(&full[stage]);
+                        const uint32_t bar = kPair ? in_cta(local, 0) : local;
+                        const uint32_t base = stages + stage * S::kStageBytes;
+                        if (rank == 0) mbar_expect(local, S::kStageBytes * (kPair ? 2 : 1));
+                        tma_load<kPair>(base, &map_i, bar, kb * kBlock, ti * kTileRows + rank * kRows);
+                        tma_load<kPair>(base + kRows * kBlock, &map_j, bar, kb * kBlock,
+                                        tj * NT + rank * S::kRowsJ);
                     }
-                    const uint32_t bar = smem_of(&full[stage]);
-                    const uint32_t base = stages + stage * S::kStageBytes;
-                    mbar_expect(bar, S::kStageBytes);
-                    tma_load(base, &map_i, bar, kb * kBlock, ti * kRows);
-                    tma_load(base + kRows * kBlock, &map_j, bar, kb * kBlock, tj * NT);
-                    ++issued;
+                    __syncwarp();
                     if (++stage == S::kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            if (!ok) {  // let the copies in flight land before the CTA goes
-                const uint32_t pending = issued < uint32_t(S::kStages) ? issued : S::kStages;
-                for (uint32_t back = pending; back > 0; --back) {
-                    const uint32_t n = issued - back;
-                    mbar_wait(smem_of(&full[n % S::kStages]), (n / S::kStages) & 1u);
-                }
-            }
-        } else if (warp == kMma && lane == 0) {
-            uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+            if (!ok) wait_ms(20);  // for the copies in flight to land before the CTA goes
+        } else if (warp == kMma && rank == 0) {
+            uint32_t stage = 0, phase = 0, buf = 0;
             bool ok = true;
-            for (int32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            const bool lead = elected();
+            for (int32_t t = first_tile; ok && t < tiles; t += tile_step) {
                 for (int32_t kb = 0; kb < a.blocks; ++kb) {
-                    if (!mbar_wait(smem_of(&acc_empty[buf]), buf_phase ^ 1u) ||
-                        !mbar_wait(smem_of(&full[stage]), phase)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = mbar_wait(smem_of(&full[stage]), phase);
+                    if (!ok) break;
                     tc_after_sync();
-                    const uint32_t base = stages + stage * S::kStageBytes;
-                    const uint64_t di = smem_desc(base), dj = smem_desc(base + kRows * kBlock);
+                    if (lead) {
+                        const uint32_t base = stages + stage * S::kStageBytes;
+                        const uint64_t di = smem_desc(base), dj = smem_desc(base + kRows * kBlock);
 #pragma unroll
-                    for (int k = 0; k < kBlock / 32; ++k)  // 32 bytes on, in 16-byte units
-                        mma_fp8(tmem + buf * NT, di + 2 * k, dj + 2 * k, instr_desc(NT), k > 0);
-                    mma_commit(smem_of(&empty[stage]));
-                    mma_commit(smem_of(&acc_full[buf]));
+                        for (int k = 0; k < kBlock / 32; ++k)  // 32 bytes on, in 16-byte units
+                            mma_fp8<kPair>(tmem + buf * NT, di + 2 * k, dj + 2 * k,
+                                           instr_desc(kTileRows, NT), k > 0);
+                        mma_commit<kPair>(smem_of(&done[stage]));
+                    }
+                    __syncwarp();
                     if (++stage == S::kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if (++buf == S::kBuffers) {
-                        buf = 0;
-                        buf_phase ^= 1u;
-                    }
+                    if (++buf == S::kBuffers) buf = 0;
                 }
             }
             if (!ok) {  // no product may be in flight when the TMEM is freed
-                mma_commit(smem_of(&drained));
+                if (lead) mma_commit<kPair>(smem_of(&drained));
+                __syncwarp();
                 mbar_wait(smem_of(&drained), 0);
             }
+        } else if (warp == kScaler) {
+            const int32_t mine = first_tile < tiles ? (tiles - 1 - first_tile) / tile_step + 1 : 0;
+            const int64_t steps = int64_t(mine) * a.blocks;
+            int32_t t = first_tile, kb = 0;  // of the next step to copy
+            uint32_t slot = 0, stage = 0, seen = 0, seen_phase = 0;
+            ScaleRows<kRows> si;
+            ScaleRows<VECJ ? NT : S::kGroups> sj;
+            bool ok = true;
+            for (int64_t g = -S::kAhead; ok && g < steps; ++g) {
+                if (g + S::kAhead - S::kScaleSlots + S::kBuffers + 1 >= 0) {
+                    ok = mbar_wait(smem_of(&done[seen]), seen_phase);
+                    if (++seen == S::kStages) {
+                        seen = 0;
+                        seen_phase ^= 1u;
+                    }
+                }
+                if (t < tiles) {
+                    if (kb == 0) {
+                        int32_t ti, tj;
+                        tile_at(a, t, &ti, &tj);
+                        si.start(a.i, ti * kTileRows + rank * kRows, 1, lane);
+                        sj.start(a.j, tj * NT, VECJ ? 1 : S::kCols, lane);
+                    }
+                    const uint32_t to = smem_of(scales + slot * S::kScales);
+                    si.copy(a.i, to, lane);
+                    sj.copy(a.j, to + kRows * 4, lane);
+                    if (++slot == S::kScaleSlots) slot = 0;
+                    if (++kb == a.blocks) {
+                        kb = 0;
+                        t += tile_step;
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (g < 0) continue;
+                // all but the last kAhead steps' copies have landed
+                asm volatile("cp.async.wait_group %0;" ::"n"(S::kAhead) : "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_of(&done[stage]));
+                __syncwarp();
+                if (++stage == S::kStages) stage = 0;
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
         if (S::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int group = warp >> 2, in_group = threadIdx.x & 127;
-        const uint32_t lane_base = tmem + (uint32_t(warp & 3) << 21);
-        uint32_t buf = 0, buf_phase = 0;
+        const uint32_t from0 = tmem + (uint32_t(warp & 3) << 21) + group * S::kCols;
+        uint32_t stage = 0, phase = 0, buf = 0, slot = 0;
         bool ok = true;
+        // The buffer of step g is free for step g + kBuffers: an arrival on that
+        // step's barrier in the first CTA.  All buffers are free at the start.
+        const bool lead = elected();
+        const uint32_t full0 = kPair ? in_cta(smem_of(&full[0]), 0) : smem_of(&full[0]);
+        uint32_t freed = S::kBuffers;
+        for (int b = 0; b < S::kBuffers; ++b)
+            if (lead) buffer_free<kPair>(full0 + b * 8);
         // After a wait that ran out the warps go through the rest without
-        // waiting or storing, so the barriers below still meet.
-        for (int32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        // waiting or storing.
+        for (int32_t t = first_tile; t < tiles; t += tile_step) {
             int32_t ti, tj;
             tile_at(a, t, &ti, &tj);
-            const int32_t i = ti * kRows + in_group;
+            const int32_t i = ti * kTileRows + rank * kRows + in_group;
             const int32_t j0 = tj * NT + group * S::kCols;
-            const int32_t row_i = min(i, a.i.rows - 1) >> a.i.shift;
-            const int32_t row_j = VECJ ? min(j0 + in_group, a.j.rows - 1)
-                                       : min(j0, a.j.rows - 1) >> a.j.shift;
             f32x2 acc[S::kCols / 2];
 #pragma unroll
             for (int c = 0; c < S::kCols / 2; ++c) acc[c] = pack2(0.0f, 0.0f);
-            float si = __ldg(a.i.s + row_i), sj = __ldg(a.j.s + row_j);
             for (int32_t kb = 0; kb < a.blocks; ++kb) {
-                float si_next = 0.0f, sj_next = 0.0f;
-                if (kb + 1 < a.blocks) {
-                    si_next = __ldg(a.i.s + (kb + 1) * a.i.ld_s + row_i);
-                    sj_next = __ldg(a.j.s + (kb + 1) * a.j.ld_s + row_j);
-                }
-                if (VECJ) {
-                    if (in_group < S::kCols) sj_smem[group][kb & 1][in_group] = sj;
-                    asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
-                }
-                ok = __all_sync(kFull, ok && mbar_wait(smem_of(&acc_full[buf]), buf_phase));
+                if (ok) ok = mbar_wait(smem_of(&done[stage]), phase);
                 tc_after_sync();
-                const float s = VECJ ? si : __fmul_rn(si, sj);
-                const f32x2 s2 = pack2(s, s);
-// one chunk's columns load while the previous chunk's are added
-                const uint32_t from = lane_base + buf * NT + group * S::kCols;
+                const uint32_t from = from0 + buf * NT;
+                const float *sc = scales + slot * S::kScales;
+                if (++slot == S::kScaleSlots) slot = 0;
+                if (++buf == S::kBuffers) buf = 0;
+                if (++stage == S::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                const float *sj = sc + kRows + group * S::kCols;
+                if (kFragment) {
+                    // rows 16 h + l / 4 + 8 q, columns 8 k + 2 (l % 4): a lane meets a
+                    // quarter of the columns, so their scales cost a quarter of the
+                    // shared-memory reads of one row per lane
+                    f32x2 si[2][2];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float x = sc[(warp & 3) * 32 + 8 * r + lane / 4];
+                        si[r / 2][r % 2] = pack2(x, x);
+                    }
+                    const f32x2 zero = pack2(-0.0f, -0.0f);
+                    uint32_t p[2][16];
+                    tmem_load_fragment(from, p[0]);
+                    tmem_wait(p[0]);
+                    f32x2 wj[4];
+#pragma unroll
+                    for (int u = 0; u < S::kCols / 16; ++u) {
+                        const int c0 = u / 2 * 32, h = u % 2;
+                        if (u + 1 < S::kCols / 16) {
+                            tmem_load_fragment(from + (u + 1) / 2 * 32 + (((u + 1) % 2) << 20), p[(u + 1) & 1]);
+                        } else {
+                            tc_before_sync();  // all read: the tensor core may have the buffer
+                            __syncwarp();
+                            if (lead) buffer_free<kPair>(full0 + freed * 8);
+                            if (++freed == S::kStages) freed = 0;
+                        }
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            if (h == 0) {
+                                const float2 x = *reinterpret_cast<const float2 *>(sj + c0 + 8 * g + 2 * (lane & 3));
+                                wj[g] = pack2(x.x, x.y);
+                            }
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const uint32_t *v = &p[u & 1][4 * g + 2 * q];
+                                const int at = (h * 2 + q) * (S::kCols / 8) + c0 / 8 + g;
+                                acc[at] = fma2_rn(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                                                  fma2_rn(si[h][q], wj[g], zero), acc[at]);
+                            }
+                        }
+                        if (u + 1 < S::kCols / 16) tmem_wait(p[(u + 1) & 1]);
+                    }
+                    continue;
+                }
                 uint32_t p[2][S::kChunk];
                 tmem_load(from, p[0]);
+                const float s = VECJ ? sc[in_group] : __fmul_rn(sc[in_group], sc[kRows + group]);
+                const f32x2 s2 = pack2(s, s);
                 tmem_wait(p[0]);
+                // one chunk's columns load while the previous chunk's are added
 #pragma unroll
                 for (int k = 0; k < S::kCols / S::kChunk; ++k) {
                     const int c0 = k * S::kChunk;
@@ -458,7 +734,8 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
                     } else {  // all read: the tensor core may have the buffer
                         tc_before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_of(&acc_empty[buf]));
+                        if (lead) buffer_free<kPair>(full0 + freed * 8);
+                        if (++freed == S::kStages) freed = 0;
                     }
 #pragma unroll
                     for (int c = 0; c < S::kChunk; c += 4) {
@@ -467,8 +744,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
                         const f32x2 v1 = pack2(__uint_as_float(q[2]), __uint_as_float(q[3]));
                         const int at = (c0 + c) / 2;
                         if (VECJ) {
-                            const float4 w = *reinterpret_cast<const float4 *>(
-                                &sj_smem[group][kb & 1][VECJ ? c0 + c : 0]);
+                            const float4 w = *reinterpret_cast<const float4 *>(sj + c0 + c);
                             const f32x2 zero = pack2(-0.0f, -0.0f);
                             acc[at] = fma2_rn(v0, fma2_rn(s2, pack2(w.x, w.y), zero), acc[at]);
                             acc[at + 1] = fma2_rn(v1, fma2_rn(s2, pack2(w.z, w.w), zero), acc[at + 1]);
@@ -479,12 +755,6 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
                     }
                     if (more) tmem_wait(p[(k + 1) & 1]);
                 }
-                if (++buf == S::kBuffers) {
-                    buf = 0;
-                    buf_phase ^= 1u;
-                }
-                si = si_next;
-                sj = sj_next;
             }
             if (!ok) continue;
             if (TRANS) {
@@ -498,22 +768,25 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
                     }
                 }
             } else {
-                uint8_t *staging = dynamic_smem + (stages - smem_of(dynamic_smem)) +
-                                   S::kStages * S::kStageBytes + warp * kStagingBytes;
-                const int32_t row0 = ti * kRows + (warp & 3) * 32;
-                if (a.accumulate) add_row<S::kCols>(a, acc, i, j0);
-                else if (a.out_bf16) store_rows<S::kCols, true>(a, acc, staging, row0, j0, lane);
-                else store_rows<S::kCols, false>(a, acc, staging, row0, j0, lane);
+                uint8_t *staging = aligned_smem + S::kStages * S::kStageBytes + warp * kStagingBytes;
+                const int32_t row0 = ti * kTileRows + rank * kRows + (warp & 3) * 32;
+                // sums to be added to out stay fp32 until then
+                if (!kFragment && a.accumulate)
+                    add_row<S::kCols>(a, acc, i, j0);
+                else if (a.out_bf16 && !a.accumulate)
+                    store_rows<S::kCols, true, kFragment>(a, acc, staging, row0, j0, lane);
+                else
+                    store_rows<S::kCols, false, kFragment>(a, acc, staging, row0, j0, lane);
             }
         }
     }
 
     tc_before_sync();
     __syncthreads();
+    // neither CTA's memory goes before the other one is done with it
+    if (kPair) cluster_sync();
     tc_after_sync();
-    if (warp == kMma)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(uint32_t(S::kTmemCols)));
+    if (warp == kMma) tmem_free<kPair>(tmem, S::kTmemCols);
 }
 
 // out = 0 (or unchanged) where there is nothing to sum.
@@ -566,22 +839,28 @@ cudaError_t operand_map(CUtensorMap *map, const Fp8Operand &op, int64_t rows, in
 
 constexpr int kSms = 152;
 
+Side side_of(const Fp8Operand &op, int64_t rows) {
+    const bool each = op.rows_per_scale == 1;
+    return {op.s, op.ld_s, each ? 0 : 7, each && op.ld_s % 4 == 0, int32_t(rows)};
+}
+
 template <int NT, bool VECJ, bool TRANS>
 cudaError_t run(const Fp8Matmul &m, const Fp8Operand &oi, const Fp8Operand &oj, int64_t rows_i,
                 int64_t rows_j, cudaStream_t stream) {
     using S = Shape<NT>;
     CUtensorMap map_i, map_j;
     cudaError_t e = operand_map(&map_i, oi, rows_i, m.K, kRows);
-    if (e == cudaSuccess) e = operand_map(&map_j, oj, rows_j, m.K, NT);
+    if (e == cudaSuccess) e = operand_map(&map_j, oj, rows_j, m.K, S::kRowsJ);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(fp8_matmul_kernel<NT, VECJ, TRANS>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     Args a;
-    a.i = {oi.s, oi.ld_s, oi.rows_per_scale == 128 ? 7 : 0, int32_t(rows_i)};
-    a.j = {oj.s, oj.ld_s, oj.rows_per_scale == 128 ? 7 : 0, int32_t(rows_j)};
+    a.i = side_of(oi, rows_i);
+    a.j = side_of(oj, rows_j);
     a.blocks = int32_t((m.K + kBlock - 1) / kBlock);
-    a.tiles_i = int32_t((rows_i + kRows - 1) / kRows);
+    const int tile_rows = S::kPair ? 2 * kRows : kRows;
+    a.tiles_i = int32_t((rows_i + tile_rows - 1) / tile_rows);
     a.tiles_j = int32_t((rows_j + NT - 1) / NT);
     a.out = m.out;
     a.ld_out = m.ld_out;
@@ -589,9 +868,10 @@ cudaError_t run(const Fp8Matmul &m, const Fp8Operand &oi, const Fp8Operand &oj, 
     a.accumulate = m.accumulate;
     a.vector_out = !m.accumulate && m.ld_out % (m.out_bf16 ? 8 : 4) == 0;
     const int64_t tiles = int64_t(a.tiles_i) * a.tiles_j;
-    const uint32_t grid = uint32_t(tiles < kSms ? tiles : kSms);
+    const int64_t places = S::kPair ? kSms / 2 : kSms;
+    const uint32_t grid = uint32_t(tiles < places ? tiles : places) * (S::kPair ? 2 : 1);
     return launch_after(fp8_matmul_kernel<NT, VECJ, TRANS>, dim3(grid), dim3(S::kThreads), S::kSmem,
-                        stream, map_i, map_j, a);
+                        stream, S::kPair ? 2 : 1, map_i, map_j, a);
 }
 
 template <int NT, bool TRANS>
@@ -614,8 +894,8 @@ cudaError_t launch_fp8_matmul(const Fp8Matmul &m, cudaStream_t stream) {
     if (m.M <= 16) return run<16, true>(m, m.b, m.a, m.N, m.M, stream);
     if (m.M <= 32) return run<32, true>(m, m.b, m.a, m.N, m.M, stream);
     if (m.M <= 64) return run<64, true>(m, m.b, m.a, m.N, m.M, stream);
-    const int64_t wide = ((m.M + 127) / 128) * ((m.N + 255) / 256);
-    if (wide < kSms) return run<128, false>(m, m.a, m.b, m.M, m.N, stream);
+    const int64_t wide = ((m.M + 255) / 256) * ((m.N + 255) / 256);
+    if (wide < kSms / 2) return run<128, false>(m, m.a, m.b, m.M, m.N, stream);
     return run<256, false>(m, m.a, m.b, m.M, m.N, stream);
 }
 

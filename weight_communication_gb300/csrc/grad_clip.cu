@@ -372,7 +372,7 @@ cudaError_t launch_clip(const GradSpan *spans, int count, const double *partials
     *write_stats = 0;
     const uint32_t grid = grid_of(t.tiles);
     if (overlap)
-        return launch_after(clip_kernel<CAP>, dim3(grid), dim3(kThreads), 0, stream, t, partials, used,
+        return launch_after(clip_kernel<CAP>, dim3(grid), dim3(kThreads), 0, stream, 1, t, partials, used,
                             max_norm, eps, stats, in_place ? 1 : 0, first);
     clip_kernel<CAP><<<grid, kThreads, 0, stream>>>(t, partials, used, max_norm, eps, stats,
                                                     in_place ? 1 : 0, first);

@@ -47,9 +47,12 @@ class Fp8Tensor:
 
     @classmethod
     def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda") -> "Fp8Tensor":
+        """Uninitialised.  The scales of a block start on 16 bytes, where a
+        product fetches them four at a time."""
+        per = -(-rows // block_rows)
+        scales = torch.empty(-(-cols // BLOCK), _ceil(per, 4), dtype=torch.float32, device=device)
         return cls(torch.empty(rows, _ceil(cols, 16), dtype=torch.float8_e4m3fn, device=device),
-                   torch.empty(-(-cols // BLOCK), -(-rows // block_rows), dtype=torch.float32,
-                               device=device), rows, cols, block_rows)
+                   scales if per % 4 == 0 else scales[:, :per], rows, cols, block_rows)
 
 
 def quantize(x: torch.Tensor, rows: bool = True, columns: bool = False, stream=None):
