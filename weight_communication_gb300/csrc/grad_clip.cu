@@ -11,20 +11,23 @@
 //
 // The tensors' addresses and lengths travel as kernel arguments (up to 1024
 // per launch, in the constant bank), so a call copies no table to the device.
-// Each tensor is cut into tiles of 8192 values that start on its first 16-byte
+// Each tensor is cut into tiles of 32 KB that start on its first 16-byte
 // boundary; the values before that boundary belong to its first tile.
 //
 // Range: x^2 leaves binary32 for |x| beyond 2^64 or below 2^-63.  A thread
-// sums its 32 values of a tile in fp32; where that sum is outside
+// sums 32 values at a time in fp32; where that sum is outside
 // [2^-90, 2^100) it is taken again in fp64 from the values it still holds, so
 // any finite gradient has a finite norm and tiny ones do not vanish.  Tile
 // sums are added with their rounding errors kept (TwoSum, Knuth), which makes
 // the result as good as an fp64 sum at the cost of fp32 adds: GB300 does two
 // fp64 fmas per clock and SM.
 //
-// Bound: HBM.  The norm reads each value once; clipping has to read it again,
-// and walks the tiles backwards so that what the first pass read last is
-// still in L2.
+// Bound: HBM.  The norm reads each value once (875 M bf16 values: 0.252 ms in
+// all, 6.9 TB/s); clipping has to read it again, and walks the tiles backwards
+// so that what the first pass read last is still in L2 (one d = 2048 layer,
+// bf16 into fp32: 68 us for 303 MB read once and written, 72 us forwards).  A
+// thread has 128 bytes of a tile in flight; half as many left the norm at 6.4
+// TB/s.
 #include <math.h>
 
 #include "wc_device.cuh"
@@ -35,8 +38,10 @@ namespace wc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr uint32_t kTile = 8192;              // values per tile
-constexpr int kPerThread = kTile / kThreads;  // 32
+constexpr int kLoads = 8;                     // 16-byte loads of a thread per tile
+constexpr uint32_t kTileBytes = kThreads * kLoads * 16;  // 32 KB
+
+__host__ __device__ constexpr uint32_t tile_values(bool bf16) { return kTileBytes / (bf16 ? 2 : 4); }
 
 template <int CAP>
 struct SpanTable {
@@ -52,7 +57,7 @@ struct SpanTable {
 struct Tile {
     int span;
     int64_t begin;       // first value of the vector part
-    uint32_t len;        // values from begin, <= kTile
+    uint32_t len;        // values from begin, at most a tile's
     uint32_t head;       // values before begin that belong to this tile (first tile only)
 };
 
@@ -72,27 +77,27 @@ __device__ __forceinline__ Tile find_tile(const SpanTable<CAP> &t, uint32_t tile
         else lo = mid + 1;
     }
     const uint32_t k = tile - (lo == 0 ? 0u : t.tile_end[lo - 1]);
-    const uint32_t head = head_of(t.src[lo], t.kind[lo] & 1, t.n[lo]);
+    const bool bf16 = t.kind[lo] & 1;
+    const uint32_t head = head_of(t.src[lo], bf16, t.n[lo]), most = tile_values(bf16);
     Tile r;
     r.span = lo;
-    r.begin = int64_t(head) + int64_t(k) * kTile;
+    r.begin = int64_t(head) + int64_t(k) * most;
     const int64_t left = t.n[lo] - r.begin;
-    r.len = left < int64_t(kTile) ? uint32_t(left) : kTile;
+    r.len = left < int64_t(most) ? uint32_t(left) : most;
     r.head = k == 0 ? head : 0u;
     return r;
 }
 
-// The 32 values of a tile that thread t holds: slot j is value
-// 8 (t + 256 (j / 8)) + j % 8 of the tile for bf16, 4 (t + 256 (j / 4)) + j % 4
-// for fp32.  Past the end they are zero, which adds nothing.
+// The values of a tile that thread t holds: 16-byte vectors t, t + 256, ... of
+// it.  Past the end they are zero, which adds nothing.
 template <bool BF16>
 __device__ __forceinline__ void load_tile(const void *src, int64_t begin, uint32_t len,
-                                          uint4 raw[BF16 ? 4 : 8], bool last_use) {
+                                          uint4 (&raw)[kLoads], bool last_use) {
     constexpr uint32_t W = BF16 ? 8 : 4;
     const uint4 *p = reinterpret_cast<const uint4 *>(
         static_cast<const char *>(src) + begin * (BF16 ? 2 : 4));
 #pragma unroll
-    for (int j = 0; j < (BF16 ? 4 : 8); ++j) {
+    for (int j = 0; j < kLoads; ++j) {
         const uint32_t v = threadIdx.x + kThreads * j;
         raw[j] = make_uint4(0u, 0u, 0u, 0u);
         if ((v + 1) * W <= len) {
@@ -111,8 +116,9 @@ __device__ __forceinline__ void load_tile(const void *src, int64_t begin, uint32
     }
 }
 
+// Value j of consecutive vectors.
 template <bool BF16>
-__device__ __forceinline__ float value_of(const uint4 raw[], int j) {
+__device__ __forceinline__ float value_of(const uint4 *raw, int j) {
     if (BF16) {
         const uint4 q = raw[j / 8];
         const uint32_t w = (j % 8) / 2 == 0 ? q.x : (j % 8) / 2 == 1 ? q.y : (j % 8) / 2 == 2 ? q.z : q.w;
@@ -137,13 +143,14 @@ struct NormSum {
 constexpr float kSafeLow = 8.0779356694631608874e-28f;   // 2^-90
 constexpr float kSafeHigh = 1.2676506002282294015e30f;   // 2^100
 
+// 32 values: 4 bf16 vectors or 8 fp32 ones.
 template <bool BF16>
-__device__ __forceinline__ void add_tile(const uint4 raw[BF16 ? 4 : 8], NormSum &sum) {
+__device__ __forceinline__ void add_squares(const uint4 *raw, NormSum &sum) {
     f32x2 acc[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = pack2(0.0f, 0.0f);
 #pragma unroll
-    for (int j = 0; j < kPerThread; j += 2) {
+    for (int j = 0; j < 32; j += 2) {
         const f32x2 x = pack2(value_of<BF16>(raw, j), value_of<BF16>(raw, j + 1));
         acc[(j / 2) % 4] = fma2_rn(x, x, acc[(j / 2) % 4]);
     }
@@ -160,7 +167,7 @@ __device__ __forceinline__ void add_tile(const uint4 raw[BF16 ? 4 : 8], NormSum 
         for (int j = 0; j < (BF16 ? 4 : 8); ++j) bits |= raw[j].x | raw[j].y | raw[j].z | raw[j].w;
         if ((bits & (BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu)) != 0u) {
 #pragma unroll
-            for (int j = 0; j < kPerThread; ++j) {
+            for (int j = 0; j < 32; ++j) {
                 const double x = double(value_of<BF16>(raw, j));
                 sum.rare = fma(x, x, sum.rare);
             }
@@ -168,15 +175,26 @@ __device__ __forceinline__ void add_tile(const uint4 raw[BF16 ? 4 : 8], NormSum 
     }
 }
 
-// Sum over the CTA; every thread returns it.  The same order every time.
-__device__ __forceinline__ double block_sum(double v, double *scratch) {
+// Sum over the CTA, in thread 0.  The same order every time.  Lanes are joined
+// in fp32 with the errors kept; fp64 is left for one add per warp (GB300's fp64
+// is slow enough that a tree over 256 threads costs microseconds).
+__device__ __forceinline__ double block_sum(NormSum sum, double *scratch) {
+    if (__any_sync(kFull, sum.rare != 0.0)) {  // (true for a NaN too)
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+        for (int off = 16; off > 0; off >>= 1) sum.rare += __shfl_xor_sync(kFull, sum.rare, off);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const float hi = __shfl_down_sync(kFull, sum.hi, off), lo = __shfl_down_sync(kFull, sum.lo, off);
+        sum.add(hi);
+        sum.lo = __fadd_rn(sum.lo, lo);
+    }
+    if ((threadIdx.x & 31) == 0)
+        scratch[threadIdx.x >> 5] = double(sum.hi) + double(sum.lo) + sum.rare;
     __syncthreads();
-    double total = scratch[0];
-#pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) total += scratch[w];
+    double total = 0.0;
+    if (threadIdx.x == 0)
+        for (int w = 0; w < kThreads / 32; ++w) total += scratch[w];
     return total;
 }
 
@@ -190,14 +208,14 @@ norm_partials_kernel(const __grid_constant__ SpanTable<CAP> t, double *__restric
     for (uint32_t i = blockIdx.x; i < t.tiles; i += gridDim.x) {
         const Tile tile = find_tile(t, i);
         const void *src = t.src[tile.span];
+        uint4 raw[kLoads];
         if (t.kind[tile.span] & 1) {
-            uint4 raw[4];
             load_tile<true>(src, tile.begin, tile.len, raw, false);
-            add_tile<true>(raw, sum);
+            add_squares<true>(raw, sum);
+            add_squares<true>(raw + kLoads / 2, sum);
         } else {
-            uint4 raw[8];
             load_tile<false>(src, tile.begin, tile.len, raw, false);
-            add_tile<false>(raw, sum);
+            add_squares<false>(raw, sum);
         }
         if (threadIdx.x < tile.head) {
             const float x = (t.kind[tile.span] & 1)
@@ -206,7 +224,7 @@ norm_partials_kernel(const __grid_constant__ SpanTable<CAP> t, double *__restric
             sum.rare = fma(double(x), double(x), sum.rare);
         }
     }
-    const double total = block_sum(double(sum.hi) + double(sum.lo) + sum.rare, scratch);
+    const double total = block_sum(sum, scratch);
     if (threadIdx.x == 0) partials[blockIdx.x] = total;
 }
 
@@ -214,24 +232,31 @@ struct NormCoef {
     float norm, coef;
 };
 
-// The norm and the coefficient from the partials, the same in every CTA.
+// The norm and the coefficient from the partials, the same in every CTA: the
+// first warp adds them in order of their index modulo 32, then the lanes.
 __device__ __forceinline__ NormCoef finish(const double *partials, int count, double max_norm,
-                                           double eps, double *scratch) {
-    double v = 0.0;
-    for (int i = threadIdx.x; i < count; i += kThreads) v += partials[i];
-    const double norm = sqrt(block_sum(v, scratch));
-    const double q = max_norm / (norm + eps);
-    NormCoef r;
-    r.norm = float(norm);
-    r.coef = q >= 1.0 ? 1.0f : float(q);  // not a number stays not a number
-    return r;
+                                           double eps, NormCoef *shared) {
+    if (threadIdx.x < 32) {
+        double v = 0.0;
+#pragma unroll 8
+        for (int i = threadIdx.x; i < count; i += 32) v += partials[i];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+        if (threadIdx.x == 0) {
+            const double norm = sqrt(v), q = max_norm / (norm + eps);
+            shared->norm = float(norm);
+            shared->coef = q >= 1.0 ? 1.0f : float(q);  // not a number stays not a number
+        }
+    }
+    __syncthreads();
+    return *shared;
 }
 
 __global__ void __launch_bounds__(kThreads)
 norm_finish_kernel(const double *__restrict__ partials, int count, double max_norm, double eps,
                    int with_coef, float *__restrict__ stats) {
-    __shared__ double scratch[kThreads / 32];
-    const NormCoef c = finish(partials, count, max_norm, eps, scratch);
+    __shared__ NormCoef shared;
+    const NormCoef c = finish(partials, count, max_norm, eps, &shared);
     if (threadIdx.x == 0) {
         stats[0] = c.norm;
         if (with_coef) stats[1] = c.coef;
@@ -252,19 +277,19 @@ __device__ __forceinline__ void store_f32x8(float *p, const float x[8]) {
 }
 
 template <bool BF16>
-__device__ __forceinline__ void scale_tile(const uint4 raw[BF16 ? 4 : 8], const Tile &tile,
-                                           void *dst, bool dst_bf16, float coef) {
+__device__ __forceinline__ void scale_tile(const uint4 (&raw)[kLoads], const Tile &tile, void *dst,
+                                           bool dst_bf16, float coef) {
     constexpr uint32_t W = BF16 ? 8 : 4;
     const uint32_t size = dst_bf16 ? 2u : 4u;
     char *base = static_cast<char *>(dst) + tile.begin * size;
     // one store per W values where the destination starts on a boundary too
     const bool vec = (reinterpret_cast<uintptr_t>(base) & (W * size - 1)) == 0;
 #pragma unroll
-    for (int j = 0; j < (BF16 ? 4 : 8); ++j) {
+    for (int j = 0; j < kLoads; ++j) {
         const uint32_t v = threadIdx.x + kThreads * j;
         float x[W];
 #pragma unroll
-        for (uint32_t e = 0; e < W; ++e) x[e] = __fmul_rn(value_of<BF16>(raw, j * W + e), coef);
+        for (uint32_t e = 0; e < W; ++e) x[e] = __fmul_rn(value_of<BF16>(raw + j, e), coef);
         if (vec && (v + 1) * W <= tile.len) {
             if (dst_bf16) {
                 uint32_t w[W / 2];
@@ -293,33 +318,35 @@ __global__ void __launch_bounds__(kThreads, 4)
 clip_kernel(const __grid_constant__ SpanTable<CAP> t, const double *__restrict__ partials,
             int count, double max_norm, double eps, float *__restrict__ stats, int in_place,
             int write_stats) {
-    __shared__ double scratch[kThreads / 32];
+    __shared__ NormCoef shared;
+    // The norm's kernel only reads the gradients, so the first tile may be
+    // fetched beside its end.
+    Tile tile = find_tile(t, t.tiles - 1u - blockIdx.x);
+    uint4 raw[kLoads];
+    if (t.kind[tile.span] & 1) load_tile<true>(t.src[tile.span], tile.begin, tile.len, raw, true);
+    else load_tile<false>(t.src[tile.span], tile.begin, tile.len, raw, true);
     wait_for_predecessor();
-    const NormCoef c = finish(partials, count, max_norm, eps, scratch);
+    const NormCoef c = finish(partials, count, max_norm, eps, &shared);
     if (write_stats && blockIdx.x == 0 && threadIdx.x == 0) {
         stats[0] = c.norm;
         stats[1] = c.coef;
     }
     if (in_place && c.coef == 1.0f) return;  // x * 1 = x, and it is there already
     for (uint32_t i = blockIdx.x; i < t.tiles; i += gridDim.x) {
-        const Tile tile = find_tile(t, t.tiles - 1u - i);
         const void *src = t.src[tile.span];
         void *dst = t.dst[tile.span];
         const bool src_bf16 = t.kind[tile.span] & 1, dst_bf16 = (t.kind[tile.span] & 2) != 0;
-        if (src_bf16) {
-            uint4 raw[4];
-            load_tile<true>(src, tile.begin, tile.len, raw, true);
-            scale_tile<true>(raw, tile, dst, dst_bf16, c.coef);
-        } else {
-            uint4 raw[8];
-            load_tile<false>(src, tile.begin, tile.len, raw, true);
-            scale_tile<false>(raw, tile, dst, dst_bf16, c.coef);
-        }
+        if (src_bf16) scale_tile<true>(raw, tile, dst, dst_bf16, c.coef);
+        else scale_tile<false>(raw, tile, dst, dst_bf16, c.coef);
         if (threadIdx.x < tile.head) {
             const float x = src_bf16 ? bf16_bits_to_f32(static_cast<const uint16_t *>(src)[threadIdx.x])
                                      : static_cast<const float *>(src)[threadIdx.x];
             store_one(dst, dst_bf16, threadIdx.x, __fmul_rn(x, c.coef));
         }
+        if (i + gridDim.x >= t.tiles) return;
+        tile = find_tile(t, t.tiles - 1u - (i + gridDim.x));
+        if (t.kind[tile.span] & 1) load_tile<true>(t.src[tile.span], tile.begin, tile.len, raw, true);
+        else load_tile<false>(t.src[tile.span], tile.begin, tile.len, raw, true);
     }
 }
 
@@ -339,7 +366,8 @@ void fill(SpanTable<CAP> &t, const GradSpan *spans, int count) {
         t.dst[t.count] = s.dst;
         t.n[t.count] = s.n;
         t.kind[t.count] = uint8_t((s.src_bf16 ? 1 : 0) | (s.dst_bf16 ? 2 : 0));
-        t.tiles += uint32_t(rest > 0 ? (rest + kTile - 1) / kTile : 1);
+        const int64_t most = tile_values(s.src_bf16);
+        t.tiles += uint32_t(rest > 0 ? (rest + most - 1) / most : 1);
         t.tile_end[t.count] = t.tiles;
         ++t.count;
     }
