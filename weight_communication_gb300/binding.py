@@ -398,6 +398,11 @@ def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, device=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr(), _rows_of(t, name, rows, cols)
+
+
+def _rows_of(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
+    """The checks of _matrix that don't depend on the device; the row stride."""
     shape = t.shape
     if len(shape) != 2 or shape[0] != rows or shape[1] < cols:
         raise ValueError(f"{name} has shape {tuple(shape)}, expected ({rows}, {cols})")
@@ -408,7 +413,7 @@ def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, device=None):
         ld = shape[1]
     elif ld < shape[1]:
         raise ValueError(f"{name} must not have overlapping rows")
-    return t.data_ptr(), ld
+    return ld
 
 
 def spans(tensors, name: str = "tensors"):
@@ -530,6 +535,44 @@ def _fp8_part(codes, scales, name: str, rows: int, cols: int, square: bool, devi
         ld = padded  # there is no second row to be apart from
     sp, lds = _matrix(scales, f"{name} scales", -(-cols // 128), per, device)
     return cp, ld, sp, lds
+
+
+def fp8_strides(codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int,
+                rows_per_scale: int) -> tuple:
+    """Checks a quantized matrix that is read; its row strides."""
+    per = -(-rows // rows_per_scale)
+    if codes.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"codes must be float8_e4m3fn, got {codes.dtype}")
+    if scales.dtype != torch.float32:
+        raise TypeError(f"scales must be float32, got {scales.dtype}")
+    if scales.device != codes.device:
+        raise ValueError(f"scales are on {scales.device}, codes on {codes.device}")
+    ld = _rows_of(codes, "codes", rows, cols)
+    lds = _rows_of(scales, "scales", -(-cols // 128), per)
+    if rows <= 1 or codes.shape[1] == 0:
+        ld = -(-cols // 16) * 16  # there is no second row to be apart from
+    return ld, lds
+
+
+def fp8_quant_parts(x: torch.Tensor, q: tuple, qt: tuple, square: bool, stream=None) -> None:
+    """wc_fp8_quant with outputs given as (codes address, stride, scales
+    address, stride) or (None, 0, None, 0); fp8.py makes them to fit."""
+    rows, cols = x.shape
+    d = x.device
+    xp, ld = _matrix(x, "x", rows, cols, d)
+    _call(d, "wc_fp8_quant", xp, _float_type(x, "x"), rows, cols, max(ld, cols), 1 if square else 0,
+          *q, *qt, _raw_stream(d, stream))
+
+
+def fp8_matmul_parts(a: tuple, a_rows_per_scale: int, b: tuple, b_rows_per_scale: int, M: int,
+                     N: int, K: int, device: torch.device, out: torch.Tensor,
+                     accumulate: bool = False, stream=None) -> None:
+    """wc_fp8_matmul with operands given as (codes address, stride, scales
+    address, stride)."""
+    op, ld_out = _matrix(out, "out", M, N, device)
+    _call(device, "wc_fp8_matmul", *a, a_rows_per_scale, *b, b_rows_per_scale, M, N, K, op,
+          _float_type(out, "out"), max(ld_out, N), 1 if accumulate else 0,
+          _raw_stream(device, stream))
 
 
 def fp8_quant(x: torch.Tensor, codes: torch.Tensor | None, scales: torch.Tensor | None,

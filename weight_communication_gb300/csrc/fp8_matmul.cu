@@ -29,6 +29,8 @@
 // product of scales there.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "wc_device.cuh"
 #include "wc_internal.h"
 
@@ -851,10 +853,18 @@ cudaError_t run(const Fp8Matmul &m, const Fp8Operand &oi, const Fp8Operand &oj, 
     CUtensorMap map_i, map_j;
     cudaError_t e = operand_map(&map_i, oi, rows_i, m.K, kRows);
     if (e == cudaSuccess) e = operand_map(&map_j, oj, rows_j, m.K, S::kRowsJ);
-    if (e == cudaSuccess)
+    if (e != cudaSuccess) return e;
+    // once for each GPU: the kernel's attribute stays set
+    static std::atomic<uint64_t> prepared{0};
+    int device = 0;
+    if ((e = cudaGetDevice(&device)) != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (device & 63);
+    if (device > 63 || !(prepared.load(std::memory_order_relaxed) & bit)) {
         e = cudaFuncSetAttribute(fp8_matmul_kernel<NT, VECJ, TRANS>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (e != cudaSuccess) return e;
+        if (e != cudaSuccess) return e;
+        prepared.fetch_or(bit, std::memory_order_relaxed);
+    }
     Args a;
     a.i = side_of(oi, rows_i);
     a.j = side_of(oj, rows_j);

@@ -29,19 +29,19 @@ class Fp8Tensor:
     """A matrix [rows, cols] in 8 bits.
 
     codes  : float8_e4m3fn [rows, >= cols], rows a multiple of 16 bytes apart
-    scales : float32 [ceil(cols / 128), rows] (block_rows 1) or
-             [ceil(cols / 128), ceil(rows / 128)] (block_rows 128)
+    scales : float32 [ceil(cols / 128), >= rows] (block_rows 1) or
+             [ceil(cols / 128), >= ceil(rows / 128)] (block_rows 128)
     Row r, column c stands for codes[r, c] * scales[c // 128, r // block_rows].
+    The two tensors are checked here, once; don't resize them afterwards.
     """
 
-    __slots__ = ("codes", "scales", "rows", "cols", "block_rows")
+    __slots__ = ("codes", "scales", "rows", "cols", "block_rows", "ld_codes", "ld_scales")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int,
                  block_rows: int = 1):
         if block_rows not in (1, BLOCK):
             raise ValueError(f"block_rows must be 1 or {BLOCK}, got {block_rows}")
-        if codes.dim() != 2 or codes.shape[0] != rows or codes.shape[1] < cols:
-            raise ValueError(f"codes have shape {tuple(codes.shape)}, expected ({rows}, {cols})")
+        self.ld_codes, self.ld_scales = binding.fp8_strides(codes, scales, rows, cols, block_rows)
         self.codes, self.scales = codes, scales
         self.rows, self.cols, self.block_rows = rows, cols, block_rows
 
@@ -49,10 +49,18 @@ class Fp8Tensor:
     def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda") -> "Fp8Tensor":
         """Uninitialised.  The scales of a block start on 16 bytes, where a
         product fetches them four at a time."""
+        t = cls.__new__(cls)
+        t.rows, t.cols, t.block_rows = rows, cols, block_rows
         per = -(-rows // block_rows)
-        scales = torch.empty(-(-cols // BLOCK), _ceil(per, 4), dtype=torch.float32, device=device)
-        return cls(torch.empty(rows, _ceil(cols, 16), dtype=torch.float8_e4m3fn, device=device),
-                   scales if per % 4 == 0 else scales[:, :per], rows, cols, block_rows)
+        t.ld_codes, t.ld_scales = _ceil(cols, 16), _ceil(per, 4)
+        t.codes = torch.empty((rows, t.ld_codes), dtype=torch.float8_e4m3fn, device=device)
+        t.scales = torch.empty_strided((-(-cols // BLOCK), per), (t.ld_scales, 1),
+                                       dtype=torch.float32, device=device)
+        return t
+
+    def parts(self) -> tuple:
+        """Addresses and strides, as the C calls take them."""
+        return self.codes.data_ptr(), self.ld_codes, self.scales.data_ptr(), self.ld_scales
 
 
 def quantize(x: torch.Tensor, rows: bool = True, columns: bool = False, stream=None):
@@ -81,10 +89,12 @@ def _quantize(x, rows, columns, block_rows, stream):
     return q, qt
 
 
+_NO_PARTS = (None, 0, None, 0)
+
+
 def _quantize_into(x, q, qt, block_rows, stream):
-    binding.fp8_quant(x, q.codes if q else None, q.scales if q else None,
-                      qt.codes if qt else None, qt.scales if qt else None,
-                      square=block_rows == BLOCK, stream=stream)
+    binding.fp8_quant_parts(x, q.parts() if q is not None else _NO_PARTS,
+                            qt.parts() if qt is not None else _NO_PARTS, block_rows == BLOCK, stream)
 
 
 def matmul(a: Fp8Tensor, b: Fp8Tensor, out: torch.Tensor | None = None,
@@ -94,15 +104,18 @@ def matmul(a: Fp8Tensor, b: Fp8Tensor, out: torch.Tensor | None = None,
     or `out`; with accumulate, added to what `out` holds."""
     if a.cols != b.cols:
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
+    device = a.codes.device
+    if b.codes.device != device:
+        raise ValueError(f"b is on {b.codes.device}, expected {device}")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs the matrix to add to as out")
         with binding.allocating_on(stream):
-            out = torch.empty(a.rows, b.rows, dtype=out_dtype, device=a.codes.device)
+            out = torch.empty((a.rows, b.rows), dtype=out_dtype, device=device)
     elif out.dim() != 2 or tuple(out.shape) != (a.rows, b.rows):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected ({a.rows}, {b.rows})")
-    binding.fp8_matmul(a.codes, a.scales, a.block_rows, b.codes, b.scales, b.block_rows, a.cols,
-                       out, accumulate, stream)
+    binding.fp8_matmul_parts(a.parts(), a.block_rows, b.parts(), b.block_rows, a.rows, b.rows,
+                             a.cols, device, out, accumulate, stream)
     return out
 
 
