@@ -147,7 +147,7 @@ def _call(device: torch.device, name: str, *args) -> None:
     """Calls the entry point with the tensors' GPU as the current device (the
     kernels launch on the current device)."""
     lib = _lib or load()
-    if device.type != "cuda" or torch.cuda.current_device() == device.index:
+    if device.type != "cuda" or torch._C._cuda_getDevice() == device.index:
         rc = getattr(lib, name)(*args)
     else:
         with torch.cuda.device(device):
@@ -391,13 +391,13 @@ def _float_type(t: torch.Tensor, name: str) -> int:
     raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
 
 
-def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, device=None):
+def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, device):
     """Pointer and row stride of a CUDA matrix [rows, >= cols] whose rows are
     consecutive values."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
     return t.data_ptr(), _rows_of(t, name, rows, cols)
 
 
@@ -446,8 +446,7 @@ def grad_norm(span_array, count: int, stats: torch.Tensor, workspace: torch.Tens
     (see spans); workspace uint8."""
     d = stats.device
     _call(d, "wc_grad_norm", span_array, count, _dev(stats, "stats", torch.float32, 1, d),
-          _dev(workspace, "workspace", torch.uint8, workspace.numel(), d), workspace.numel(),
-          _raw_stream(d, stream))
+          *_workspace(workspace, d), _raw_stream(d, stream))
 
 
 def grad_clip(span_array, dst_array, count: int, max_norm: float, eps: float,
@@ -457,15 +456,27 @@ def grad_clip(span_array, dst_array, count: int, max_norm: float, eps: float,
     d = stats.device
     _call(d, "wc_grad_clip", span_array, dst_array, count, max_norm, eps,
           _dev(stats, "stats", torch.float32, 2, d),
-          _dev(workspace, "workspace", torch.uint8, workspace.numel(), d), workspace.numel(),
-          _raw_stream(d, stream))
+          *_workspace(workspace, d), _raw_stream(d, stream))
 
 
 def _ids(ids: torch.Tensor, device) -> tuple:
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
-    return (_dev(ids, "ids", ids.dtype, ids.numel(), device),
-            WC_I64 if ids.dtype == torch.int64 else WC_I32)
+    if ids.device != device:
+        raise ValueError(f"ids is on {ids.device}, expected {device}")
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    return ids.data_ptr(), WC_I64 if ids.dtype == torch.int64 else WC_I32
+
+
+def _workspace(t: torch.Tensor, device) -> tuple:
+    if t.dtype != torch.uint8:
+        raise TypeError(f"workspace must be uint8, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"workspace is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel()
 
 
 def embedding(table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, scale: float = 1.0,
@@ -480,9 +491,10 @@ def embedding(table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, scale: 
     ip, it = _ids(ids, d)
     if out.dtype != table.dtype:
         raise TypeError(f"out must be {table.dtype}, got {out.dtype}")
-    op, ld_out = _matrix(out, "out", ids.numel(), D, d)
-    _call(d, "wc_embedding", tp, _float_type(table, "table"), max(ld_table, D), ip, it,
-          ids.numel(), first_row, V, D, scale, op, max(ld_out, D), _raw_stream(d, stream))
+    n = ids.numel()
+    op, ld_out = _matrix(out, "out", n, D, d)
+    _call(d, "wc_embedding", tp, _float_type(table, "table"), ld_table, ip, it, n, first_row, V,
+          D, scale, op, ld_out, _raw_stream(d, stream))
 
 
 def embedding_grad_workspace(n: int, V: int, D: int) -> int:
@@ -509,10 +521,9 @@ def embedding_grad(dy: torch.Tensor, ids: torch.Tensor, dtable: torch.Tensor,
         raise ValueError(f"dy has {dy.shape[1]} columns, dtable {D}")
     ip, it = _ids(ids, d)
     op, ld_out = _matrix(dtable, "dtable", V, D, d)
-    _call(d, "wc_embedding_grad", yp, _float_type(dy, "dy"), max(ld_dy, D), ip, it, n, first_row,
-          V, D, scale, 1 if accumulate else 0, op, _float_type(dtable, "dtable"), max(ld_out, D),
-          _dev(workspace, "workspace", torch.uint8, workspace.numel(), d), workspace.numel(),
-          _raw_stream(d, stream))
+    _call(d, "wc_embedding_grad", yp, _float_type(dy, "dy"), ld_dy, ip, it, n, first_row, V, D,
+          scale, 1 if accumulate else 0, op, _float_type(dtable, "dtable"), ld_out,
+          *_workspace(workspace, d), _raw_stream(d, stream))
 
 
 def _fp8_part(codes, scales, name: str, rows: int, cols: int, square: bool, device,
@@ -560,7 +571,7 @@ def fp8_quant_parts(x: torch.Tensor, q: tuple, qt: tuple, square: bool, stream=N
     rows, cols = x.shape
     d = x.device
     xp, ld = _matrix(x, "x", rows, cols, d)
-    _call(d, "wc_fp8_quant", xp, _float_type(x, "x"), rows, cols, max(ld, cols), 1 if square else 0,
+    _call(d, "wc_fp8_quant", xp, _float_type(x, "x"), rows, cols, ld, 1 if square else 0,
           *q, *qt, _raw_stream(d, stream))
 
 
@@ -571,7 +582,7 @@ def fp8_matmul_parts(a: tuple, a_rows_per_scale: int, b: tuple, b_rows_per_scale
     address, stride)."""
     op, ld_out = _matrix(out, "out", M, N, device)
     _call(device, "wc_fp8_matmul", *a, a_rows_per_scale, *b, b_rows_per_scale, M, N, K, op,
-          _float_type(out, "out"), max(ld_out, N), 1 if accumulate else 0,
+          _float_type(out, "out"), ld_out, 1 if accumulate else 0,
           _raw_stream(device, stream))
 
 
@@ -588,7 +599,7 @@ def fp8_quant(x: torch.Tensor, codes: torch.Tensor | None, scales: torch.Tensor 
     xp, ld = _matrix(x, "x", rows, cols, d)
     q, ldq, s, lds = _fp8_part(codes, scales, "row", rows, cols, square, d, True)
     qt, ldqt, st, ldst = _fp8_part(codes_t, scales_t, "transposed", cols, rows, square, d, True)
-    _call(d, "wc_fp8_quant", xp, _float_type(x, "x"), rows, cols, max(ld, cols), 1 if square else 0,
+    _call(d, "wc_fp8_quant", xp, _float_type(x, "x"), rows, cols, ld, 1 if square else 0,
           q, ldq, s, lds, qt, ldqt, st, ldst, _raw_stream(d, stream))
 
 
@@ -603,5 +614,5 @@ def fp8_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, a_rows_per_scale: 
     bp, ldb, sbp, ldsb = _fp8_part(b_codes, b_scales, "b", N, K, b_rows_per_scale == 128, d, False)
     op, ld_out = _matrix(out, "out", M, N, d)
     _call(d, "wc_fp8_matmul", ap, lda, sap, ldsa, a_rows_per_scale, bp, ldb, sbp, ldsb,
-          b_rows_per_scale, M, N, K, op, _float_type(out, "out"), max(ld_out, N),
+          b_rows_per_scale, M, N, K, op, _float_type(out, "out"), ld_out,
           1 if accumulate else 0, _raw_stream(d, stream))

@@ -20,7 +20,7 @@ from . import binding
 def _flat(ids: torch.Tensor) -> torch.Tensor:
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
-    return ids.view(-1)
+    return ids if ids.dim() == 1 else ids.view(-1)
 
 
 def lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, first_row: int = 0,
@@ -34,9 +34,9 @@ def lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, first_row
     given = out
     if out is None:
         with binding.allocating_on(stream):
-            out = torch.empty(flat.numel(), table.shape[1], dtype=table.dtype, device=table.device)
+            out = torch.empty((flat.numel(), table.shape[1]), dtype=table.dtype, device=table.device)
     binding.embedding(table, flat, out, scale, first_row, stream)
-    return out.view(*ids.shape, table.shape[1]) if given is None else out
+    return out.view(*ids.shape, table.shape[1]) if given is None and ids.dim() != 1 else out
 
 
 def grad(dy: torch.Tensor, ids: torch.Tensor, rows: int, scale: float = 1.0, first_row: int = 0,
