@@ -398,7 +398,7 @@ WC_API int wc_grad_clip(const wc_span *spans, const wc_span *dst, int count, dou
  * first + V) of a vocabulary split over ranks contributes its own tokens.
  * table : [V][ld_table], out : [n][ld_out], both of `dtype`; rows of D values.
  * ids   : [n] of `id_type` (WC_I32 or WC_I64).
- * Requires n < 2^31, 0 <= V < 2^31 - 1, D < 2^31, n * D < 2^40, ld_table >= D,
+ * Requires n < 2^31, 0 <= V < 2^31 - 1, D <= 2^22, n * D < 2^40, ld_table >= D,
  * ld_out >= D, 0 <= first < 2^62.
  */
 WC_API int wc_embedding(const void *table, int dtype, int64_t ld_table, const void *ids,
