@@ -192,6 +192,22 @@ __device__ __forceinline__ void zero_row(char *p, uint64_t bytes, int lane) {
         __stcs(reinterpret_cast<W *>(p + i), zero);
 }
 
+// Rows of tokens t, t + 32, ..., as places in [lo, hi), -1 outside; counts the
+// ones below.
+template <typename I>
+__device__ __forceinline__ void load_rows(const I *ids, int64_t t, int64_t end, int64_t first,
+                                          int32_t lo, int32_t hi, int32_t (&k)[kSortUnroll],
+                                          int32_t &below) {
+    int64_t r[kSortUnroll];
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) r[u] = t + 32 * u < end ? relative(ids[t + 32 * u], first) : -1;
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) {
+        if (r[u] >= 0 && r[u] < lo) ++below;
+        k[u] = r[u] >= lo && r[u] < hi ? int32_t(r[u] - lo) : -1;
+    }
+}
+
 // order[p], rows[p]: token and row at sorted place p.  row_start[v]: first
 // place of row v; row_start[V]: tokens with a row.  CTA b owns rows
 // [b * per_cta, (b + 1) * per_cta).  Dynamic shared memory: per_cta *
@@ -214,45 +230,37 @@ sort_kernel(const I *__restrict__ ids, int32_t n, int64_t first, int32_t V, int3
     if (threadIdx.x == 0) below_total = 0;
     __syncthreads();
 
-    // each warp counts its own consecutive stretch of tokens
+    // each warp counts its own consecutive stretch of tokens; one that fits is
+    // kept for the second pass
     const int32_t stretch = ((n + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
     const int64_t begin = int64_t(stretch) * warp;
     const int64_t end = begin + stretch < int64_t(n) ? begin + stretch : int64_t(n);
-    int32_t below = 0;
-    for (int64_t t0 = begin + lane; t0 < end; t0 += 32 * kSortUnroll) {
-        int64_t r[kSortUnroll];
+    const bool kept = stretch <= 32 * kSortUnroll;
+    int32_t below = 0, k[kSortUnroll];
+    for (int64_t t0 = begin; t0 < end; t0 += 32 * kSortUnroll) {
+        load_rows(ids, t0 + lane, end, first, lo, hi, k, below);
 #pragma unroll
-        for (int u = 0; u < kSortUnroll; ++u) {
-            const int64_t t = t0 + 32 * u;
-            r[u] = t < end ? relative(ids[t], first) : -1;
-        }
-#pragma unroll
-        for (int u = 0; u < kSortUnroll; ++u) {
-            if (r[u] >= lo && r[u] < hi) atomicAdd(&counters[int32_t(r[u] - lo) * kSortPitch + warp], 1);
-            else if (r[u] >= 0 && r[u] < lo) ++below;
-        }
+        for (int u = 0; u < kSortUnroll; ++u)
+            if (k[u] >= 0) atomicAdd(&counters[k[u] * kSortPitch + warp], 1);
     }
     below = __reduce_add_sync(kFull, below);
     if (lane == 0) atomicAdd(&below_total, below);
     __syncthreads();
 
     // places: rows in order, and within a row the warps in order
-    for (int32_t r = warp; r < own; r += kSortWarps) {
-        const int32_t c = counters[r * kSortPitch + lane];
-        int32_t inc = c;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int32_t u = __shfl_up_sync(kFull, inc, off);
-            if (lane >= off) inc += u;
-        }
-        counters[r * kSortPitch + lane] = inc - c;
-        if (lane == 31) base[r] = inc;
-    }
-    __syncthreads();
     int32_t carry = below_total;
     for (int32_t r0 = 0; r0 < own; r0 += kSortThreads) {
         const int32_t r = r0 + int32_t(threadIdx.x);
-        const int32_t c = r < own ? base[r] : 0;
+        int32_t c = 0;
+        if (r < own) {
+            int32_t *of = counters + r * kSortPitch;
+#pragma unroll 8
+            for (int w = 0; w < kSortWarps; ++w) {
+                const int32_t x = of[w];
+                of[w] = c;
+                c += x;
+            }
+        }
         int32_t inc = c;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -289,23 +297,17 @@ sort_kernel(const I *__restrict__ ids, int32_t n, int64_t first, int32_t V, int3
 
     // the same stretch again, in order: equal rows of a step keep lane order
     for (int64_t t0 = begin; t0 < end; t0 += 32 * kSortUnroll) {
-        int64_t r[kSortUnroll];
+        int32_t unused = 0;
+        if (!kept) load_rows(ids, t0 + lane, end, first, lo, hi, k, unused);
 #pragma unroll
         for (int u = 0; u < kSortUnroll; ++u) {
-            const int64_t t = t0 + 32 * u + lane;
-            r[u] = t < end ? relative(ids[t], first) : -1;
-        }
-#pragma unroll
-        for (int u = 0; u < kSortUnroll; ++u) {
-            const bool mine = r[u] >= lo && r[u] < hi;
-            const unsigned live = __ballot_sync(kFull, mine);
-            if (mine) {
-                const int32_t k = int32_t(r[u] - lo);
-                const unsigned peers = __match_any_sync(live, k);
-                int32_t *counter = &counters[k * kSortPitch + warp];
-                const int32_t at = base[k] + *counter + __popc(peers & ((1u << lane) - 1u));
+            const unsigned live = __ballot_sync(kFull, k[u] >= 0);
+            if (k[u] >= 0) {
+                const unsigned peers = __match_any_sync(live, k[u]);
+                int32_t *counter = &counters[k[u] * kSortPitch + warp];
+                const int32_t at = base[k[u]] + *counter + __popc(peers & ((1u << lane) - 1u));
                 order[at] = int32_t(t0 + 32 * u + lane);
-                rows[at] = int32_t(r[u]);
+                rows[at] = lo + k[u];
                 __syncwarp(live);
                 if ((peers & ((1u << lane) - 1u)) == 0u) *counter += __popc(peers);
             }

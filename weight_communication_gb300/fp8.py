@@ -35,32 +35,53 @@ class Fp8Tensor:
     The two tensors are checked here, once; don't resize them afterwards.
     """
 
-    __slots__ = ("codes", "scales", "rows", "cols", "block_rows", "ld_codes", "ld_scales")
+    __slots__ = ("_codes", "_scales", "_buffer", "_scales_at", "rows", "cols", "block_rows",
+                 "ld_codes", "ld_scales", "device")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int,
                  block_rows: int = 1):
         if block_rows not in (1, BLOCK):
             raise ValueError(f"block_rows must be 1 or {BLOCK}, got {block_rows}")
         self.ld_codes, self.ld_scales = binding.fp8_strides(codes, scales, rows, cols, block_rows)
-        self.codes, self.scales = codes, scales
+        self._codes, self._scales, self.device = codes, scales, codes.device
         self.rows, self.cols, self.block_rows = rows, cols, block_rows
+        self._buffer = None
 
     @classmethod
     def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda") -> "Fp8Tensor":
-        """Uninitialised.  The scales of a block start on 16 bytes, where a
-        product fetches them four at a time."""
+        """Uninitialised, codes and scales in one allocation.  The scales of a
+        block start on 16 bytes, where a product fetches them four at a time."""
         t = cls.__new__(cls)
         t.rows, t.cols, t.block_rows = rows, cols, block_rows
-        per = -(-rows // block_rows)
-        t.ld_codes, t.ld_scales = _ceil(cols, 16), _ceil(per, 4)
-        t.codes = torch.empty((rows, t.ld_codes), dtype=torch.float8_e4m3fn, device=device)
-        t.scales = torch.empty_strided((-(-cols // BLOCK), per), (t.ld_scales, 1),
-                                       dtype=torch.float32, device=device)
+        t.ld_codes, t.ld_scales = _ceil(cols, 16), _ceil(-(-rows // block_rows), 4)
+        t._scales_at = _ceil(rows * t.ld_codes, 16)
+        t._buffer = torch.empty(t._scales_at + -(-cols // BLOCK) * t.ld_scales * 4,
+                                dtype=torch.uint8, device=device)
+        t._codes = t._scales = None
+        t.device = t._buffer.device
         return t
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            self._codes = (self._buffer[:self.rows * self.ld_codes].view(torch.float8_e4m3fn)
+                           .view(self.rows, self.ld_codes))
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            per = -(-self.rows // self.block_rows)
+            self._scales = (self._buffer[self._scales_at:].view(torch.float32)
+                            .view(-(-self.cols // BLOCK), self.ld_scales)[:, :per])
+        return self._scales
 
     def parts(self) -> tuple:
         """Addresses and strides, as the C calls take them."""
-        return self.codes.data_ptr(), self.ld_codes, self.scales.data_ptr(), self.ld_scales
+        if self._buffer is not None:
+            at = self._buffer.data_ptr()
+            return at, self.ld_codes, at + self._scales_at, self.ld_scales
+        return self._codes.data_ptr(), self.ld_codes, self._scales.data_ptr(), self.ld_scales
 
 
 def quantize(x: torch.Tensor, rows: bool = True, columns: bool = False, stream=None):
@@ -104,9 +125,9 @@ def matmul(a: Fp8Tensor, b: Fp8Tensor, out: torch.Tensor | None = None,
     or `out`; with accumulate, added to what `out` holds."""
     if a.cols != b.cols:
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
-    device = a.codes.device
-    if b.codes.device != device:
-        raise ValueError(f"b is on {b.codes.device}, expected {device}")
+    device = a.device
+    if b.device != device:
+        raise ValueError(f"b is on {b.device}, expected {device}")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs the matrix to add to as out")
