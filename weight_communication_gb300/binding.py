@@ -1,4 +1,6 @@
 """ctypes binding of libwc.so (include/wc.h): argument marshalling only.
+(`calls` has the composed calls of the training-step operators, which reach
+the library without ctypes.)
 
 Every function takes torch CUDA tensors, checks dtype, device, contiguity and
 sizes, and calls the entry point of the same name on the tensors' current
@@ -8,8 +10,9 @@ is raised.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from pathlib import Path
 
@@ -108,6 +111,40 @@ def load(path: str | Path | None = None) -> ctypes.CDLL:
     if path is None:
         _lib = lib
     return lib
+
+
+_calls = None
+
+
+def calls():
+    """The extension module with the Python calls of the training-step
+    operators, set up to call the loaded library.  Raises if it has not been
+    built."""
+    global _calls
+    if _calls is not None:
+        return _calls
+    lib = load()
+    if not _build.CALLS.exists():
+        raise RuntimeError(f"extension module {_build.CALLS} is missing: build it with "
+                           "`python -m weight_communication_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader("wc_calls", str(_build.CALLS))
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("wc_calls", loader))
+    loader.exec_module(module)
+    module.setup({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in SIGNATURES},
+                 WcError)
+    _calls = module
+    return module
+
+
+def on_stream(stream, device: torch.device, call, *args):
+    """call(*args), which allocates and launches on the current stream, with
+    `stream` as the current one if it is given."""
+    if stream is None:
+        return call(*args)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 def last_error() -> str:
@@ -374,15 +411,6 @@ def sr_accumulate_bf16(dst: torch.Tensor, src: torch.Tensor, seed: int, step: in
           _stream(dst, stream))
 
 
-_NO_CONTEXT = contextlib.nullcontext()
-
-
-def allocating_on(stream: torch.cuda.Stream | None):
-    """Context in which new tensors belong to `stream`; without one they
-    belong to the current stream, which is where the call goes."""
-    return _NO_CONTEXT if stream is None else torch.cuda.stream(stream)
-
-
 def _float_type(t: torch.Tensor, name: str) -> int:
     if t.dtype == torch.float32:
         return WC_F32
@@ -546,44 +574,6 @@ def _fp8_part(codes, scales, name: str, rows: int, cols: int, square: bool, devi
         ld = padded  # there is no second row to be apart from
     sp, lds = _matrix(scales, f"{name} scales", -(-cols // 128), per, device)
     return cp, ld, sp, lds
-
-
-def fp8_strides(codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int,
-                rows_per_scale: int) -> tuple:
-    """Checks a quantized matrix that is read; its row strides."""
-    per = -(-rows // rows_per_scale)
-    if codes.dtype != torch.float8_e4m3fn:
-        raise TypeError(f"codes must be float8_e4m3fn, got {codes.dtype}")
-    if scales.dtype != torch.float32:
-        raise TypeError(f"scales must be float32, got {scales.dtype}")
-    if scales.device != codes.device:
-        raise ValueError(f"scales are on {scales.device}, codes on {codes.device}")
-    ld = _rows_of(codes, "codes", rows, cols)
-    lds = _rows_of(scales, "scales", -(-cols // 128), per)
-    if rows <= 1 or codes.shape[1] == 0:
-        ld = -(-cols // 16) * 16  # there is no second row to be apart from
-    return ld, lds
-
-
-def fp8_quant_parts(x: torch.Tensor, q: tuple, qt: tuple, square: bool, stream=None) -> None:
-    """wc_fp8_quant with outputs given as (codes address, stride, scales
-    address, stride) or (None, 0, None, 0); fp8.py makes them to fit."""
-    rows, cols = x.shape
-    d = x.device
-    xp, ld = _matrix(x, "x", rows, cols, d)
-    _call(d, "wc_fp8_quant", xp, _float_type(x, "x"), rows, cols, ld, 1 if square else 0,
-          *q, *qt, _raw_stream(d, stream))
-
-
-def fp8_matmul_parts(a: tuple, a_rows_per_scale: int, b: tuple, b_rows_per_scale: int, M: int,
-                     N: int, K: int, device: torch.device, out: torch.Tensor,
-                     accumulate: bool = False, stream=None) -> None:
-    """wc_fp8_matmul with operands given as (codes address, stride, scales
-    address, stride)."""
-    op, ld_out = _matrix(out, "out", M, N, device)
-    _call(device, "wc_fp8_matmul", *a, a_rows_per_scale, *b, b_rows_per_scale, M, N, K, op,
-          _float_type(out, "out"), ld_out, 1 if accumulate else 0,
-          _raw_stream(device, stream))
 
 
 def fp8_quant(x: torch.Tensor, codes: torch.Tensor | None, scales: torch.Tensor | None,

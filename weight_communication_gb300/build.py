@@ -4,7 +4,9 @@
 
 Each .cu file under csrc/ compiles to an object in parallel; the objects link
 into one shared library with the CUDA runtime linked statically, so the
-library needs only the driver at run time.
+library needs only the driver at run time.  Beside it, csrc/calls.cpp becomes
+wc_calls.so: the Python calls of the training-step operators on torch's
+tensors, which call the library.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -20,6 +23,7 @@ CSRC = PKG / "csrc"
 INCLUDE = PKG.parent / "include"
 BUILD = PKG / "_build"
 LIB = BUILD / "libwc.so"
+CALLS = BUILD / "wc_calls.so"
 # The checked build (every kernel access compared with its buffer's extent,
 # see wc_checked_violations in include/wc.h) goes to a folder of its own.
 CHECKED_BUILD = BUILD / "checked"
@@ -54,14 +58,33 @@ def _compile(src: Path, out: Path, defines: list[str]) -> tuple[Path, str]:
     return obj, proc.stderr
 
 
+def _compile_calls() -> Path:
+    """csrc/calls.cpp against the installed torch, into a temporary file."""
+    import torch
+    root = Path(torch.__file__).parent
+    cuda = Path(nvcc()).resolve().parent.parent
+    includes = [root / "include", root / "include" / "torch" / "csrc" / "api" / "include",
+                cuda / "include", sysconfig.get_paths()["include"]]
+    tmp = BUILD / "wc_calls.so.tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-I{INCLUDE}", *[f"-isystem{p}" for p in includes], str(CSRC / "calls.cpp"), "-o", str(tmp),
+           f"-L{root / 'lib'}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"the compiler failed on calls.cpp:\n{proc.stdout}\n{proc.stderr}")
+    return tmp
+
+
 def build(verbose: bool = False, checked: bool = False) -> Path:
-    """Compile every kernel file and link libwc.so; checked=True builds the
-    bounds-checked library (WC_CHECKED=1) into its own folder instead."""
+    """Compile every kernel file and link libwc.so, and the Python calls;
+    checked=True builds the bounds-checked library (WC_CHECKED=1) into its own
+    folder instead (the Python calls work with either library)."""
     out, lib = (CHECKED_BUILD, CHECKED_LIB) if checked else (BUILD, LIB)
     defines = ["-DWC_CHECKED=1"] if checked else []
     out.mkdir(parents=True, exist_ok=True)
     srcs = sources()
-    with ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        calls = None if checked else ex.submit(_compile_calls)
         results = list(ex.map(lambda s: _compile(s, out, defines), srcs))
     log = "\n".join(f"== {o.name}\n{err}" for o, err in results)
     (out / "ptxas.log").write_text(log)
@@ -71,6 +94,8 @@ def build(verbose: bool = False, checked: bool = False) -> Path:
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", str(tmp),
            *[str(o) for o, _ in results]]
     subprocess.run(cmd, check=True)
+    if calls is not None:
+        os.replace(calls.result(), CALLS)
     os.replace(tmp, lib)
     return lib
 

@@ -21,10 +21,6 @@ from . import binding
 BLOCK = 128
 
 
-def _ceil(n: int, m: int) -> int:
-    return -(-n // m) * m
-
-
 class Fp8Tensor:
     """A matrix [rows, cols] in 8 bits.
 
@@ -35,53 +31,44 @@ class Fp8Tensor:
     The two tensors are checked here, once; don't resize them afterwards.
     """
 
-    __slots__ = ("_codes", "_scales", "_buffer", "_scales_at", "rows", "cols", "block_rows",
-                 "ld_codes", "ld_scales", "device")
+    __slots__ = ("rows", "cols", "block_rows", "device", "_buffer", "_codes", "_scales", "_parts")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int,
                  block_rows: int = 1):
-        if block_rows not in (1, BLOCK):
-            raise ValueError(f"block_rows must be 1 or {BLOCK}, got {block_rows}")
-        self.ld_codes, self.ld_scales = binding.fp8_strides(codes, scales, rows, cols, block_rows)
+        # addresses, strides and sizes, as the calls take them
+        self._parts = binding.calls().fp8_view(codes, scales, rows, cols, block_rows)
         self._codes, self._scales, self.device = codes, scales, codes.device
         self.rows, self.cols, self.block_rows = rows, cols, block_rows
-        self._buffer = None
+
+    @classmethod
+    def _made(cls, described: tuple) -> "Fp8Tensor":
+        """From what the calls say of a matrix they have made: codes and scales
+        in one allocation."""
+        t = cls.__new__(cls)
+        t.rows, t.cols, t.block_rows, t.device, t._buffer, t._parts = described
+        t._codes = t._scales = None
+        return t
 
     @classmethod
     def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda") -> "Fp8Tensor":
-        """Uninitialised, codes and scales in one allocation.  The scales of a
-        block start on 16 bytes, where a product fetches them four at a time."""
-        t = cls.__new__(cls)
-        t.rows, t.cols, t.block_rows = rows, cols, block_rows
-        t.ld_codes, t.ld_scales = _ceil(cols, 16), _ceil(-(-rows // block_rows), 4)
-        t._scales_at = _ceil(rows * t.ld_codes, 16)
-        t._buffer = torch.empty(t._scales_at + -(-cols // BLOCK) * t.ld_scales * 4,
-                                dtype=torch.uint8, device=device)
-        t._codes = t._scales = None
-        t.device = t._buffer.device
-        return t
+        """Uninitialised."""
+        return cls._made(binding.calls().fp8_empty(rows, cols, block_rows, torch.device(device)))
 
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
-            self._codes = (self._buffer[:self.rows * self.ld_codes].view(torch.float8_e4m3fn)
-                           .view(self.rows, self.ld_codes))
+            ld = self._parts[1]
+            self._codes = (self._buffer[:self.rows * ld].view(torch.float8_e4m3fn)
+                           .view(self.rows, ld))
         return self._codes
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
-            per = -(-self.rows // self.block_rows)
-            self._scales = (self._buffer[self._scales_at:].view(torch.float32)
-                            .view(-(-self.cols // BLOCK), self.ld_scales)[:, :per])
+            codes, _, scales, ld = self._parts[:4]
+            self._scales = (self._buffer[scales - codes:].view(torch.float32)
+                            .view(-(-self.cols // BLOCK), ld)[:, :-(-self.rows // self.block_rows)])
         return self._scales
-
-    def parts(self) -> tuple:
-        """Addresses and strides, as the C calls take them."""
-        if self._buffer is not None:
-            at = self._buffer.data_ptr()
-            return at, self.ld_codes, at + self._scales_at, self.ld_scales
-        return self._codes.data_ptr(), self.ld_codes, self._scales.data_ptr(), self.ld_scales
 
 
 def quantize(x: torch.Tensor, rows: bool = True, columns: bool = False, stream=None):
@@ -98,24 +85,9 @@ def quantize_weight(w: torch.Tensor, rows: bool = True, columns: bool = False, s
 
 
 def _quantize(x, rows, columns, block_rows, stream):
-    if x.dim() != 2:
-        raise ValueError(f"x must be a matrix, got shape {tuple(x.shape)}")
-    if not (rows or columns):
-        raise ValueError("neither rows nor columns asked for")
-    M, K = x.shape
-    with binding.allocating_on(stream):
-        q = Fp8Tensor.empty(M, K, block_rows, x.device) if rows else None
-        qt = Fp8Tensor.empty(K, M, block_rows, x.device) if columns else None
-    _quantize_into(x, q, qt, block_rows, stream)
-    return q, qt
-
-
-_NO_PARTS = (None, 0, None, 0)
-
-
-def _quantize_into(x, q, qt, block_rows, stream):
-    binding.fp8_quant_parts(x, q.parts() if q is not None else _NO_PARTS,
-                            qt.parts() if qt is not None else _NO_PARTS, block_rows == BLOCK, stream)
+    q, qt = binding.on_stream(stream, x.device, binding.calls().fp8_quantize, x, rows, columns,
+                              block_rows)
+    return (None if q is None else Fp8Tensor._made(q), None if qt is None else Fp8Tensor._made(qt))
 
 
 def matmul(a: Fp8Tensor, b: Fp8Tensor, out: torch.Tensor | None = None,
@@ -123,21 +95,8 @@ def matmul(a: Fp8Tensor, b: Fp8Tensor, out: torch.Tensor | None = None,
            stream=None) -> torch.Tensor:
     """a [M, K] times b [N, K] transposed: [M, N] in bf16 or fp32, a new tensor
     or `out`; with accumulate, added to what `out` holds."""
-    if a.cols != b.cols:
-        raise ValueError(f"a has {a.cols} columns, b {b.cols}")
-    device = a.device
-    if b.device != device:
-        raise ValueError(f"b is on {b.device}, expected {device}")
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate needs the matrix to add to as out")
-        with binding.allocating_on(stream):
-            out = torch.empty((a.rows, b.rows), dtype=out_dtype, device=device)
-    elif out.dim() != 2 or tuple(out.shape) != (a.rows, b.rows):
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected ({a.rows}, {b.rows})")
-    binding.fp8_matmul_parts(a.parts(), a.block_rows, b.parts(), b.block_rows, a.rows, b.rows,
-                             a.cols, device, out, accumulate, stream)
-    return out
+    return binding.on_stream(stream, a.device, binding.calls().fp8_matmul, a._parts, b._parts, out,
+                             out_dtype, accumulate)
 
 
 class Fp8Linear:
@@ -152,9 +111,8 @@ class Fp8Linear:
 
     def load(self, weight: torch.Tensor, stream=None) -> None:
         """Quantizes new values of the weight into the same buffers."""
-        if tuple(weight.shape) != (self.N, self.K):
-            raise ValueError(f"weight has shape {tuple(weight.shape)}, expected ({self.N}, {self.K})")
-        _quantize_into(weight, self.w, self.wt, BLOCK, stream)
+        binding.on_stream(stream, weight.device, binding.calls().fp8_quantize_into, weight,
+                          self.w._parts, None if self.wt is None else self.wt._parts)
 
     def forward(self, x: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
                 save: bool = False, stream=None):

@@ -11,6 +11,8 @@ come back as a tensor that the update, or a log line some steps later, reads.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import binding
@@ -25,7 +27,7 @@ class TensorList:
     def __init__(self, tensors):
         self.tensors = tuple(tensors)
         self.spans, self.device = binding.spans(self.tensors)
-        self.workspace_bytes = binding.grad_norm_workspace(len(self.tensors))
+        self.address = ctypes.addressof(self.spans)
 
     def __len__(self) -> int:
         return len(self.tensors)
@@ -35,25 +37,19 @@ def _listed(tensors) -> TensorList:
     return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
 
 
-def _buffers(lst: TensorList, stats: torch.Tensor | None, n: int, stream):
+def _run(lst: TensorList, dst: TensorList | None, clipping: bool, max_norm: float, eps: float,
+         stats: torch.Tensor | None, stream) -> torch.Tensor:
     if lst.device is None:
         raise ValueError("an empty list has no GPU to run on")
-    if stream is not None and stream.device != lst.device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {lst.device}")
-    with binding.allocating_on(stream):
-        if stats is None:
-            stats = torch.empty(n, dtype=torch.float32, device=lst.device)
-        workspace = torch.empty(lst.workspace_bytes, dtype=torch.uint8, device=lst.device)
-    return stats, workspace
+    return binding.on_stream(stream, lst.device, binding.calls().grad_norm, lst.address,
+                             0 if dst is None else dst.address, len(lst.tensors), clipping,
+                             max_norm, eps, stats, lst.device)
 
 
 def norm(tensors, stats: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The norm of a TensorList or a list of tensors, as stats [1] fp32 on the
     device.  Runs on `stream` or the current one."""
-    lst = _listed(tensors)
-    stats, workspace = _buffers(lst, stats, 1, stream)
-    binding.grad_norm(lst.spans, len(lst), stats, workspace, stream)
-    return stats
+    return _run(_listed(tensors), None, False, 0.0, 0.0, stats, stream)
 
 
 def clip(tensors, max_norm: float, out=None, eps: float = 1e-6,
@@ -64,11 +60,9 @@ def clip(tensors, max_norm: float, out=None, eps: float = 1e-6,
     from bf16 ones).  Returns stats [2] fp32 on the device: norm and coef."""
     lst = _listed(tensors)
     dst = None if out is None else _listed(out)
-    if dst is not None and len(dst) != len(lst):
-        raise ValueError(f"out has {len(dst)} tensors, expected {len(lst)}")
-    if dst is not None and dst.device != lst.device:
-        raise ValueError(f"out is on {dst.device}, expected {lst.device}")
-    stats, workspace = _buffers(lst, stats, 2, stream)
-    binding.grad_clip(lst.spans, None if dst is None else dst.spans, len(lst), float(max_norm),
-                      float(eps), stats, workspace, stream)
-    return stats
+    if dst is not None:
+        if len(dst) != len(lst):
+            raise ValueError(f"out has {len(dst)} tensors, expected {len(lst)}")
+        if dst.device != lst.device:
+            raise ValueError(f"out is on {dst.device}, expected {lst.device}")
+    return _run(lst, dst, True, max_norm, eps, stats, stream)
