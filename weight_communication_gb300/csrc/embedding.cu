@@ -19,7 +19,12 @@
 // a row with many tokens (Zipf's law) is spread over many workers; a worker
 // writes the rows that lie inside its run and leaves fp32 partial sums of the
 // at most two rows that cross its ends.  (3) join: adds those partial sums in
-// order.  Bound: HBM, reading dy once and writing the table's gradient once.
+// order.  Bound: HBM, reading dy once and writing the table's gradient once:
+// 16384 tokens into 32000 x 2048 bf16 take 44.8 us (197 MB, 4.4 TB/s), of which
+// the sort waits on latencies for about 8 and the zero rows are written in the
+// next 16.  (Zeros for every row at the start of the sort: 52.5 us, its reads
+// queue behind them.)  Few tokens are bound by latencies: 3001 x 1002 into
+// 50021 fp32 rows 14.5 us.
 #include "wc_device.cuh"
 #include "wc_internal.h"
 
@@ -343,15 +348,14 @@ __device__ __forceinline__ uint32_t run_of(const int32_t *row_start, const SumPl
     return per;
 }
 
-template <typename TO, int E>
-__device__ __forceinline__ void write_row(TO *p, const float acc[E], float scale, bool accumulate) {
+// scale * acc, added to `old` if ACC.
+template <bool ACC, typename TO, int E>
+__device__ __forceinline__ void write_row(TO *p, const float acc[E], float scale, const Pack<TO, E> &old) {
     float x[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = __fmul_rn(acc[e], scale);
-    if (accumulate) {
-        const Pack<TO, E> old = load_pack<TO, E, true>(p);
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = __fadd_rn(pack_value<TO, E>(old, e), x[e]);
+    for (int e = 0; e < E; ++e) {
+        x[e] = __fmul_rn(acc[e], scale);
+        if (ACC) x[e] = __fadd_rn(pack_value<TO, E>(old, e), x[e]);
     }
     store_pack<TO, E>(p, pack_of<TO, E>(x));
 }
@@ -360,11 +364,15 @@ __device__ __forceinline__ void write_row(TO *p, const float acc[E], float scale
 // began in an earlier run and ends in this one.  tails[w]: the part in run w
 // of a row that goes on in the next run.  joins[w]: the row that heads[w] is a
 // part of (-1: none) and the run it begins in.
-template <typename TI, typename TO, int E>
+// The places of the next step are read during this one, and with ACC the old
+// values of every row that ends in a step beside its tokens: a worker has few
+// tokens, and what it waits for is one memory latency after another (3001
+// tokens added to fp32 rows: 11.3 -> 7.6 us).
+template <typename TI, typename TO, int E, bool ACC>
 __global__ void __launch_bounds__(kSumThreads)
 sum_kernel(const TI *__restrict__ dy, int64_t ld_dy, const int32_t *__restrict__ order,
            const int32_t *__restrict__ rows, const int32_t *__restrict__ row_start, SumPlan p,
-           float scale, int accumulate, TO *__restrict__ dtable, int64_t ld_out,
+           float scale, TO *__restrict__ dtable, int64_t ld_out,
            float *__restrict__ heads, float *__restrict__ tails, int2 *__restrict__ joins) {
     const uint32_t lane = threadIdx.x & (p.lanes - 1);
     const uint32_t w = blockIdx.x * (kSumThreads / p.lanes) + threadIdx.x / p.lanes;
@@ -380,48 +388,53 @@ sum_kernel(const TI *__restrict__ dy, int64_t ld_dy, const int32_t *__restrict__
         const int32_t live = row_start[p.V];
         const int32_t prior = begin > 0 ? rows[begin - 1] : -1;
         const int32_t next = end < live ? rows[end] : -1;
-        int32_t row = rows[begin];
         float acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+        // rows of places j .. j + kSumUnroll, `next` at `end`; tokens of all but the last
+        int32_t r[kSumUnroll + 1], token[kSumUnroll];
+        auto places = [&](int32_t j) {
+#pragma unroll
+            for (int u = 0; u <= kSumUnroll; ++u) {
+                r[u] = j + u < end ? rows[j + u] : next;
+                if (u < kSumUnroll && j + u < end) token[u] = order[j + u];
+            }
+        };
+        places(begin);
         for (int32_t j = begin; j < end; j += kSumUnroll) {
             Pack<TI, E> g[kSumUnroll];
-            int32_t r[kSumUnroll];
+            Pack<TO, E> old[kSumUnroll] = {};
+            int32_t row[kSumUnroll + 1];
+#pragma unroll
+            for (int u = 0; u <= kSumUnroll; ++u) row[u] = r[u];
 #pragma unroll
             for (int u = 0; u < kSumUnroll; ++u) {
-                if (j + u < end) {
-                    r[u] = rows[j + u];
-                    g[u] = load_pack<TI, E, true>(dy + int64_t(order[j + u]) * ld_dy + col);
-                }
+                if (j + u >= end) continue;
+                g[u] = load_pack<TI, E, true>(dy + int64_t(token[u]) * ld_dy + col);
+                if (ACC && row[u] != row[u + 1] && row[u] != prior)
+                    old[u] = load_pack<TO, E, true>(dtable + int64_t(row[u]) * ld_out + col);
             }
+            if (j + kSumUnroll < end) places(j + kSumUnroll);
 #pragma unroll
             for (int u = 0; u < kSumUnroll; ++u) {
                 if (j + u >= end) break;
-                if (r[u] != row) {
-                    if (row == prior) {
-                        join = make_int2(row, int32_t(uint32_t(row_start[row]) / per));
-#pragma unroll
-                        for (int e = 0; e < E; ++e) heads[int64_t(w) * p.D + col + e] = acc[e];
-                    } else {
-                        write_row<TO, E>(dtable + int64_t(row) * ld_out + col, acc, scale, accumulate);
-                    }
-                    row = r[u];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-                }
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[e] = __fadd_rn(acc[e], pack_value<TI, E>(g[u], e));
+                if (row[u] == row[u + 1]) continue;  // goes on, maybe in the next run
+                if (row[u] == prior) {
+                    join = make_int2(row[u], int32_t(uint32_t(row_start[row[u]]) / per));
+#pragma unroll
+                    for (int e = 0; e < E; ++e) heads[int64_t(w) * p.D + col + e] = acc[e];
+                } else {
+                    write_row<ACC, TO, E>(dtable + int64_t(row[u]) * ld_out + col, acc, scale, old[u]);
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = 0.0f;
             }
         }
-        if (row == next) {
+        if (rows[end - 1] == next) {
 #pragma unroll
             for (int e = 0; e < E; ++e) tails[int64_t(w) * p.D + col + e] = acc[e];
-        } else if (row == prior) {
-            join = make_int2(row, int32_t(uint32_t(row_start[row]) / per));
-#pragma unroll
-            for (int e = 0; e < E; ++e) heads[int64_t(w) * p.D + col + e] = acc[e];
-        } else {
-            write_row<TO, E>(dtable + int64_t(row) * ld_out + col, acc, scale, accumulate);
         }
     }
     if (blockIdx.y == 0 && lane == 0) joins[w] = join;
@@ -433,13 +446,19 @@ sum_kernel(const TI *__restrict__ dy, int64_t ld_dy, const int32_t *__restrict__
 
 constexpr int kJoinLanes = 64;   // threads along the columns, E columns each
 constexpr int kJoinParts = 4;    // threads that share a row's runs
+constexpr int kJoinThreads = kJoinLanes * kJoinParts;
 constexpr int kJoinUnroll = 4;
 
-// CTA (w, c): if a row that began earlier ends in run w, adds its parts over
-// the runs, split in four consecutive shares that are added in order.
-template <typename TO, int E>
-__global__ void __launch_bounds__(kJoinLanes * kJoinParts)
-join_kernel(SumPlan p, float scale, int accumulate, TO *__restrict__ dtable, int64_t ld_out,
+// CTA (w, y): if a row that began earlier ends in run w, adds its parts over
+// the runs, split in four consecutive shares that are added in order.  Up to
+// four parts -- all but the rows with many tokens -- are a share each; a thread
+// adds its columns' alone then, and fewer CTAs have work.  (A CTA per 256
+// columns: with two CTAs for all of a run's columns the row of the most
+// frequent token took 11.5 us instead of 6.9; with eight shares the start of
+// the idle CTAs cost as much.)
+template <typename TO, int E, bool ACC>
+__global__ void __launch_bounds__(kJoinThreads)
+join_kernel(SumPlan p, float scale, TO *__restrict__ dtable, int64_t ld_out,
             const float *__restrict__ heads, const float *__restrict__ tails,
             const int2 *__restrict__ joins) {
     __shared__ float part[kJoinParts][kJoinLanes * E];
@@ -448,12 +467,45 @@ join_kernel(SumPlan p, float scale, int accumulate, TO *__restrict__ dtable, int
     const int2 join = joins[w];
     if (join.x < 0) return;
     const uint32_t first = uint32_t(join.y);
-    const uint32_t c = threadIdx.x % kJoinLanes, s = threadIdx.x / kJoinLanes;
-    const uint32_t col = (blockIdx.y * kJoinLanes + c) * E;
+    TO *row = dtable + int64_t(join.x) * ld_out;
     // parts first .. w - 1 are tails, part w is a head
-    const uint32_t count = w - first, share = (count + kJoinParts - 1) / kJoinParts;
+    const uint32_t count = w - first;
+    auto tail = [&](uint32_t i, uint32_t col) {
+        return load_pack<float, E, true>(tails + int64_t(i) * p.D + col);
+    };
+    auto finish = [&](float (&sum)[E], const Pack<float, E> &head, const Pack<TO, E> &old, uint32_t col) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) sum[k] = __fadd_rn(sum[k], pack_value<float, E>(head, k));
+        write_row<ACC, TO, E>(row + col, sum, scale, old);
+    };
+    if (count <= uint32_t(kJoinParts)) {
+        const uint32_t col = (blockIdx.y * kJoinThreads + threadIdx.x) * E;
+        if (col < p.D) {
+            Pack<float, E> x[kJoinParts];
+#pragma unroll
+            for (uint32_t u = 0; u < kJoinParts; ++u)
+                if (u < count) x[u] = tail(first + u, col);
+            const Pack<float, E> head = load_pack<float, E, true>(heads + int64_t(w) * p.D + col);
+            Pack<TO, E> old = {};
+            if (ACC) old = load_pack<TO, E, true>(row + col);
+            float sum[E];
+#pragma unroll
+            for (int k = 0; k < E; ++k) sum[k] = 0.0f;
+#pragma unroll
+            for (uint32_t u = 0; u < kJoinParts; ++u)
+                if (u < count) {
+#pragma unroll
+                    for (int k = 0; k < E; ++k) sum[k] = __fadd_rn(sum[k], pack_value<float, E>(x[u], k));
+                }
+            finish(sum, head, old, col);
+        }
+        return;
+    }
+    const uint32_t c = threadIdx.x % kJoinLanes, s = threadIdx.x / kJoinLanes;
+    const uint32_t share = (count + kJoinParts - 1) / kJoinParts;
     const uint32_t b = first + s * share < w ? first + s * share : w;
     const uint32_t e = b + share < w ? b + share : w;
+    const uint32_t col = (blockIdx.y * kJoinLanes + c) * E;
     float sum[E];
 #pragma unroll
     for (int k = 0; k < E; ++k) sum[k] = 0.0f;
@@ -462,7 +514,7 @@ join_kernel(SumPlan p, float scale, int accumulate, TO *__restrict__ dtable, int
             Pack<float, E> x[kJoinUnroll];
 #pragma unroll
             for (int u = 0; u < kJoinUnroll; ++u)
-                if (i + u < e) x[u] = load_pack<float, E, true>(tails + int64_t(i + u) * p.D + col);
+                if (i + u < e) x[u] = tail(i + u, col);
 #pragma unroll
             for (int u = 0; u < kJoinUnroll; ++u)
                 if (i + u < e) {
@@ -476,13 +528,13 @@ join_kernel(SumPlan p, float scale, int accumulate, TO *__restrict__ dtable, int
     __syncthreads();
     if (s != 0 || col >= p.D) return;
     const Pack<float, E> head = load_pack<float, E, true>(heads + int64_t(w) * p.D + col);
+    Pack<TO, E> old = {};
+    if (ACC) old = load_pack<TO, E, true>(row + col);
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
+    for (int k = 0; k < E; ++k)
 #pragma unroll
         for (int i = 1; i < kJoinParts; ++i) sum[k] = __fadd_rn(sum[k], part[i][c * E + k]);
-        sum[k] = __fadd_rn(sum[k], pack_value<float, E>(head, k));
-    }
-    write_row<TO, E>(dtable + int64_t(join.x) * ld_out + col, sum, scale, accumulate);
+    finish(sum, head, old, col);
 }
 
 // ---------------------------------------------------------------------------
@@ -490,7 +542,7 @@ join_kernel(SumPlan p, float scale, int accumulate, TO *__restrict__ dtable, int
 // ---------------------------------------------------------------------------
 
 constexpr int kSms = 152;
-// The sort's counters fill at most 128 KB of shared memory (larger tables
+// The sort's counters fill at most 136 KB of shared memory (larger tables
 // take more CTAs than SMs).
 constexpr int32_t kSortRowsMax = 1024;
 constexpr int kSumCtas = 4 * kSms;
@@ -550,27 +602,34 @@ cudaError_t lookup(const void *table, int64_t ld_table, const void *ids, int64_t
     return cudaPeekAtLastError();
 }
 
-template <typename TI, typename TO>
+template <typename TI, typename TO, bool ACC>
 cudaError_t launch_sum(const EmbeddingGrad &a, const SumPlan &p, int e, const int32_t *order,
                        const int32_t *rows, const int32_t *row_start, float *heads, float *tails,
                        int2 *joins, cudaStream_t stream) {
     const dim3 grid((p.workers + kSumThreads / p.lanes - 1) / (kSumThreads / p.lanes),
                     (p.vecs + p.lanes - 1) / p.lanes);
+    TO *dtable = static_cast<TO *>(a.dtable);
 #define WC_SUM(E)                                                                             \
-    launch_after(sum_kernel<TI, TO, E>, grid, dim3(kSumThreads), 0, stream, 1,                   \
+    launch_after(sum_kernel<TI, TO, E, ACC>, grid, dim3(kSumThreads), 0, stream, 1,           \
                  static_cast<const TI *>(a.dy), a.ld_dy, order, rows, row_start, p, a.scale,  \
-                 a.accumulate ? 1 : 0, static_cast<TO *>(a.dtable), a.ld_out, heads, tails, joins)
+                 dtable, a.ld_out, heads, tails, joins)
     cudaError_t err = e == 8 ? WC_SUM(8) : e == 4 ? WC_SUM(4) : e == 2 ? WC_SUM(2) : WC_SUM(1);
 #undef WC_SUM
     if (err != cudaSuccess || a.n < 2) return err;  // one token crosses no run
-    const int je = e >= 4 ? 4 : 1;
-    const dim3 join_grid(p.workers, (p.D + kJoinLanes * je - 1) / (kJoinLanes * je));
-    const dim3 join_block(kJoinLanes * kJoinParts);
-    TO *dtable = static_cast<TO *>(a.dtable);
-    return je == 4 ? launch_after(join_kernel<TO, 4>, join_grid, join_block, 0, stream, 1, p, a.scale,
-                                  a.accumulate ? 1 : 0, dtable, a.ld_out, heads, tails, joins)
-                   : launch_after(join_kernel<TO, 1>, join_grid, join_block, 0, stream, 1, p, a.scale,
-                                  a.accumulate ? 1 : 0, dtable, a.ld_out, heads, tails, joins);
+#define WC_JOIN(E)                                                                            \
+    launch_after(join_kernel<TO, E, ACC>,                                                     \
+                 dim3(p.workers, (p.D + kJoinLanes * E - 1) / (kJoinLanes * E)),              \
+                 dim3(kJoinThreads), 0, stream, 1, p, a.scale, dtable, a.ld_out, heads, tails, joins)
+    return e >= 4 ? WC_JOIN(4) : e == 2 ? WC_JOIN(2) : WC_JOIN(1);
+#undef WC_JOIN
+}
+
+template <typename TI, typename TO>
+cudaError_t launch_sum(const EmbeddingGrad &a, const SumPlan &p, int e, const int32_t *order,
+                       const int32_t *rows, const int32_t *row_start, float *heads, float *tails,
+                       int2 *joins, cudaStream_t stream) {
+    return a.accumulate ? launch_sum<TI, TO, true>(a, p, e, order, rows, row_start, heads, tails, joins, stream)
+                        : launch_sum<TI, TO, false>(a, p, e, order, rows, row_start, heads, tails, joins, stream);
 }
 
 }  // namespace
