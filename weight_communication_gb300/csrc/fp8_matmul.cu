@@ -13,6 +13,9 @@
 // on the next buffers.  The inner sum of 128 products is the tensor core's
 // fp32 accumulation; every sum beyond it is an fp32 fma.
 //
+// Where the tiles are too few for the GPU, a cluster of up to eight CTAs shares
+// each tile's blocks of K and adds its sums through shared memory.
+//
 // A persistent CTA has a TMA warp, an MMA warp, a warp that brings scales, and
 // one or two warpgroups of epilogue; they run ahead of one another across
 // tiles.  The operand with its rows on the MMA's 128 rows is called i, the one
@@ -338,6 +341,7 @@ struct Args {
     void *out;
     int64_t ld_out;
     int out_bf16, accumulate, vector_out;
+    int32_t split;           // CTAs (one cluster) that share a tile's blocks
 };
 
 // A warp's part in copying the scales of ROWS rows of a tile, block after block:
@@ -348,18 +352,19 @@ struct ScaleRows {
     static constexpr int kSingles = (ROWS + 31) / 32, kQuads = (ROWS + 127) / 128;
     const float *p[kSingles];
     uint32_t bytes[kQuads];
-    __device__ __forceinline__ void start(const Side &s, int32_t row0, int step, int lane) {
+    __device__ __forceinline__ void start(const Side &s, int32_t row0, int step, int32_t block0, int lane) {
+        const float *from = s.s + block0 * s.ld_s;
         if (ROWS >= 16 && s.quads) {
 #pragma unroll
             for (int r = 0; r < kQuads; ++r) {
                 const int32_t row = row0 + 128 * r + 4 * lane, left = s.rows - row;
-                p[r] = s.s + (left > 0 ? row : 0);
+                p[r] = from + (left > 0 ? row : 0);
                 bytes[r] = left >= 4 ? 16u : left > 0 ? 4u * left : 0u;
             }
         } else {
 #pragma unroll
             for (int r = 0; r < kSingles; ++r)
-                p[r] = s.s + (min(row0 + (32 * r + lane) * step, s.rows - 1) >> s.shift);
+                p[r] = from + (min(row0 + (32 * r + lane) * step, s.rows - 1) >> s.shift);
         }
     }
     __device__ __forceinline__ void copy(const Side &s, uint32_t to, int lane) {
@@ -491,6 +496,60 @@ __device__ __forceinline__ void add_row(const Args &a, const f32x2 (&acc)[COLS /
     }
 }
 
+// Sums of a tile over the CTAs that share its blocks.  Each has left its own in
+// shared memory as lines of 128 consecutive outputs (TRANS: columns of the tile,
+// else rows), kPartialPitch values apart; each adds every split-th line over the
+// cluster and stores it.  It begins with its own part and goes round, so the
+// order is fixed for each line and no CTA is read by all others at once (all from
+// the first one on: 128 x 1003 x 11008 with eight CTAs 15 us, so 10.3).
+constexpr int kPartialPitch = 132;
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+template <bool TRANS, int NT, int WARPS>
+__device__ __forceinline__ void add_partials(const Args &a, int32_t tile, int32_t part, uint32_t partial,
+                                             int warp, int lane) {
+    int32_t ti, tj;
+    tile_at(a, tile, &ti, &tj);
+    const int32_t line0 = TRANS ? tj * NT : ti * kRows, at0 = (TRANS ? ti * kRows : tj * NT) + 4 * lane;
+    const int32_t lines = min(TRANS ? NT : kRows, (TRANS ? a.j.rows : a.i.rows) - line0);
+    const int32_t left = (TRANS ? a.i.rows : a.j.rows) - at0;
+    for (int32_t line = part + a.split * warp; line < lines; line += a.split * WARPS) {
+        const uint32_t addr = partial + (line * kPartialPitch + 4 * lane) * 4;
+        float4 x = ld_cluster_f4(in_cta(addr, part));
+#pragma unroll 2
+        for (int32_t p = 1, from = part; p < a.split; ++p) {
+            if (++from == a.split) from = 0;
+            const float4 y = ld_cluster_f4(in_cta(addr, from));
+            x.x = __fadd_rn(x.x, y.x);
+            x.y = __fadd_rn(x.y, y.y);
+            x.z = __fadd_rn(x.z, y.z);
+            x.w = __fadd_rn(x.w, y.w);
+        }
+        if (left <= 0) continue;
+        const int64_t at = int64_t(line0 + line) * a.ld_out + at0;
+        if (a.vector_out && left >= 4) {
+            if (a.out_bf16)
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+                    make_uint2(f32x2_to_bf16x2_bits(x.x, x.y), f32x2_to_bf16x2_bits(x.z, x.w));
+            else
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = x;
+        } else {
+            put(a, at, x.x);
+            if (left > 1) put(a, at + 1, x.y);
+            if (left > 2) put(a, at + 2, x.z);
+            if (left > 3) put(a, at + 3, x.w);
+        }
+    }
+}
+
 // VECJ: j has a scale per row (one per column of the tile), else one per 128.
 // TRANS: out is [j][i], else [i][j].
 template <int NT, bool VECJ, bool TRANS>
@@ -513,11 +572,16 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
     const uint32_t stages = (smem_of(dynamic_smem) + 1023u) & ~1023u;
     uint8_t *const aligned_smem = dynamic_smem + (stages - smem_of(dynamic_smem));
     float *const scales = reinterpret_cast<float *>(aligned_smem + S::kScalesAt);
+    float *const partial = reinterpret_cast<float *>(aligned_smem);
     const int32_t tiles = a.tiles_i * a.tiles_j;
     // the CTAs of a pair are neighbours in the grid and work on one tile
     const int32_t rank = kPair ? int32_t(blockIdx.x & 1) : 0;
-    const int32_t first_tile = kPair ? int32_t(blockIdx.x >> 1) : int32_t(blockIdx.x);
-    const int32_t tile_step = kPair ? int32_t(gridDim.x >> 1) : int32_t(gridDim.x);
+    const uint32_t sharing = kPair ? 2u : uint32_t(a.split);  // CTAs of a tile
+    const int32_t first_tile = int32_t(blockIdx.x / sharing), tile_step = int32_t(gridDim.x / sharing);
+    // this CTA's blocks of K
+    const int32_t part = kPair ? 0 : int32_t(blockIdx.x % sharing);
+    const int32_t block0 = kPair ? 0 : a.blocks * part / a.split;
+    const int32_t blocks = kPair ? a.blocks : a.blocks * (part + 1) / a.split - block0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
@@ -547,7 +611,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
             for (int32_t t = first_tile; ok && t < tiles; t += tile_step) {
                 int32_t ti, tj;
                 tile_at(a, t, &ti, &tj);
-                for (int32_t kb = 0; kb < a.blocks; ++kb) {
+                for (int32_t kb = 0; kb < blocks; ++kb) {
                     ok = mbar_wait(smem_of(&done[stage]), phase ^ 1u);
                     if (!ok) break;
                     if (elected()) {
@@ -556,8 +620,9 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
                         const uint32_t bar = kPair ? in_cta(local, 0) : local;
                         const uint32_t base = stages + stage * S::kStageBytes;
                         if (rank == 0) mbar_expect(local, S::kStageBytes * (kPair ? 2 : 1));
-                        tma_load<kPair>(base, &map_i, bar, kb * kBlock, ti * kTileRows + rank * kRows);
-                        tma_load<kPair>(base + kRows * kBlock, &map_j, bar, kb * kBlock,
+                        tma_load<kPair>(base, &map_i, bar, (block0 + kb) * kBlock,
+                                        ti * kTileRows + rank * kRows);
+                        tma_load<kPair>(base + kRows * kBlock, &map_j, bar, (block0 + kb) * kBlock,
                                         tj * NT + rank * S::kRowsJ);
                     }
                     __syncwarp();
@@ -573,7 +638,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
             bool ok = true;
             const bool lead = elected();
             for (int32_t t = first_tile; ok && t < tiles; t += tile_step) {
-                for (int32_t kb = 0; kb < a.blocks; ++kb) {
+                for (int32_t kb = 0; kb < blocks; ++kb) {
                     ok = mbar_wait(smem_of(&full[stage]), phase);
                     if (!ok) break;
                     tc_after_sync();
@@ -601,7 +666,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
             }
         } else if (warp == kScaler) {
             const int32_t mine = first_tile < tiles ? (tiles - 1 - first_tile) / tile_step + 1 : 0;
-            const int64_t steps = int64_t(mine) * a.blocks;
+            const int64_t steps = int64_t(mine) * blocks;
             int32_t t = first_tile, kb = 0;  // of the next step to copy
             uint32_t slot = 0, stage = 0, seen = 0, seen_phase = 0;
             ScaleRows<kRows> si;
@@ -615,18 +680,18 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
                         seen_phase ^= 1u;
                     }
                 }
-                if (t < tiles) {
+                if (t < tiles) {  // (blocks > 0)
                     if (kb == 0) {
                         int32_t ti, tj;
                         tile_at(a, t, &ti, &tj);
-                        si.start(a.i, ti * kTileRows + rank * kRows, 1, lane);
-                        sj.start(a.j, tj * NT, VECJ ? 1 : S::kCols, lane);
+                        si.start(a.i, ti * kTileRows + rank * kRows, 1, block0, lane);
+                        sj.start(a.j, tj * NT, VECJ ? 1 : S::kCols, block0, lane);
                     }
                     const uint32_t to = smem_of(scales + slot * S::kScales);
                     si.copy(a.i, to, lane);
                     sj.copy(a.j, to + kRows * 4, lane);
                     if (++slot == S::kScaleSlots) slot = 0;
-                    if (++kb == a.blocks) {
+                    if (++kb == blocks) {
                         kb = 0;
                         t += tile_step;
                     }
@@ -665,7 +730,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
             f32x2 acc[S::kCols / 2];
 #pragma unroll
             for (int c = 0; c < S::kCols / 2; ++c) acc[c] = pack2(0.0f, 0.0f);
-            for (int32_t kb = 0; kb < a.blocks; ++kb) {
+            for (int32_t kb = 0; kb < blocks; ++kb) {
                 if (ok) ok = mbar_wait(smem_of(&done[stage]), phase);
                 tc_after_sync();
                 const uint32_t from = from0 + buf * NT;
@@ -759,7 +824,23 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
                 }
             }
             if (!ok) continue;
-            if (TRANS) {
+            if (!kPair && a.split > 1) {
+                // the last product is complete, so the stages are free
+#pragma unroll
+                for (int c = 0; c < S::kCols; c += 4) {
+                    float x[4];
+                    unpack2(acc[c / 2], x[0], x[1]);
+                    unpack2(acc[c / 2 + 1], x[2], x[3]);
+                    const int at = group * S::kCols + c;
+                    if (TRANS) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) partial[(at + k) * kPartialPitch + in_group] = x[k];
+                    } else {
+                        *reinterpret_cast<float4 *>(partial + in_group * kPartialPitch + at) =
+                            make_float4(x[0], x[1], x[2], x[3]);
+                    }
+                }
+            } else if (TRANS) {
                 if (i < a.i.rows) {
 #pragma unroll
                     for (int c = 0; c < S::kCols; c += 2) {
@@ -783,6 +864,13 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
         }
     }
 
+    if (!kPair && a.split > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (warp < kProducer && first_tile < tiles)
+            add_partials<TRANS, NT, S::kGroups * 4>(a, first_tile, part, smem_of(partial), warp, lane);
+        cluster_sync();
+    }
     tc_before_sync();
     __syncthreads();
     // neither CTA's memory goes before the other one is done with it
@@ -846,6 +934,51 @@ Side side_of(const Fp8Operand &op, int64_t rows) {
     return {op.s, op.ld_s, each ? 0 : 7, each && op.ld_s % 4 == 0, int32_t(rows)};
 }
 
+// Clusters of `size` CTAs that run at once, as the driver counts them (GB300: 76,
+// 46, 36, 28, 23, 15, 15 of 2 to 8 -- the SMs of a GPC do not divide evenly).
+// Every shape of the kernel has an SM to itself, so the count is the GPU's alone
+// and is asked for once.
+template <typename Kernel>
+int clusters_of(Kernel kernel, int threads, int smem, int device, int size) {
+    static std::atomic<int> known[64][9];
+    if (device < 64 && known[device][size].load(std::memory_order_relaxed) > 0)
+        return known[device][size].load(std::memory_order_relaxed);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(size) * kSms);
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = size_t(smem);
+    cudaLaunchAttribute attr[1] = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(size);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;  // no split
+    }
+    if (device < 64) known[device][size].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// CTAs that share a tile's blocks of K: as many as run at once, three blocks or
+// more each, and none where that saves less than adding the sums costs (a block
+// takes 0.3 us; the exchange 2.5 us for 128 x 128 sums, 1 us for fewer columns).
+// One token, 4096 x 11008: 28.9 -> 10.6 us; 128 x 1003 x 11008: 32.9 -> 10.3;
+// 5 blocks on 63 tiles of 128 x 128 would take 8.7 us instead of 7.4.
+template <typename Kernel>
+int32_t split_of(Kernel kernel, int threads, int smem, int device, int64_t tiles, int32_t blocks,
+                 int32_t worth) {
+    if (tiles > kSms / 2) return 1;
+    for (int32_t s = 8; s > 1; --s)
+        if (blocks >= 3 * s && blocks - (blocks + s - 1) / s >= worth &&
+            tiles <= clusters_of(kernel, threads, smem, device, s))
+            return s;
+    return 1;
+}
+
 template <int NT, bool VECJ, bool TRANS>
 cudaError_t run(const Fp8Matmul &m, const Fp8Operand &oi, const Fp8Operand &oj, int64_t rows_i,
                 int64_t rows_j, cudaStream_t stream) {
@@ -879,9 +1012,14 @@ cudaError_t run(const Fp8Matmul &m, const Fp8Operand &oi, const Fp8Operand &oj, 
     a.vector_out = !m.accumulate && m.ld_out % (m.out_bf16 ? 8 : 4) == 0;
     const int64_t tiles = int64_t(a.tiles_i) * a.tiles_j;
     const int64_t places = S::kPair ? kSms / 2 : kSms;
-    const uint32_t grid = uint32_t(tiles < places ? tiles : places) * (S::kPair ? 2 : 1);
+    a.split = 1;
+    if constexpr (!S::kPair)
+        a.split = split_of(fp8_matmul_kernel<NT, VECJ, TRANS>, S::kThreads, S::kSmem, device, tiles,
+                           a.blocks, NT >= 128 ? 8 : 4);
+    const uint32_t cluster = S::kPair ? 2 : uint32_t(a.split);
+    const uint32_t grid = uint32_t(tiles < places ? tiles : places) * cluster;
     return launch_after(fp8_matmul_kernel<NT, VECJ, TRANS>, dim3(grid), dim3(S::kThreads), S::kSmem,
-                        stream, S::kPair ? 2 : 1, map_i, map_j, a);
+                        stream, cluster, map_i, map_j, a);
 }
 
 template <int NT, bool TRANS>
