@@ -53,6 +53,31 @@ __device__ __forceinline__ Scale8 scale_of(float m) {
     return s;
 }
 
+// Rows that start anywhere are read as the aligned chunks of 16 bytes that hold
+// the 8 values (N words, 2 or 3 chunks), and shifted into place: 4411 x 9433 bf16
+// both ways 49 -> 40 us against value by value.
+template <int N>
+__device__ __forceinline__ void load_chunks(const void *p, uint32_t (&t)[N]) {
+    const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) {
+        const uint4 v = __ldg(q + k);  // a neighbour's lane reads it too
+        t[4 * k] = v.x;
+        t[4 * k + 1] = v.y;
+        t[4 * k + 2] = v.z;
+        t[4 * k + 3] = v.w;
+    }
+}
+
+// Drops the first n < 4 of N words.
+template <int N>
+__device__ __forceinline__ void drop_words(uint32_t (&t)[N], uint32_t n) {
+#pragma unroll
+    for (int k = 0; k + 2 < N; ++k) t[k] = (n & 2u) ? t[k + 2] : t[k];
+#pragma unroll
+    for (int k = 0; k + 1 < N; ++k) t[k] = (n & 1u) ? t[k + 1] : t[k];
+}
+
 // The 8 x 8 values of a thread, and the operations on them that depend on the
 // type.  An encoding without its sign orders magnitudes, infinities and NaN
 // above all finite ones; Max holds such encodings (bf16: of two columns).
@@ -69,6 +94,13 @@ struct Values<uint16_t> {
         w[i][1] = q.y;
         w[i][2] = q.z;
         w[i][3] = q.w;
+    }
+    static constexpr int kWords = 8;  // of the chunks of a row
+    __device__ __forceinline__ void shift(int i, const uint16_t *p, uint32_t (&t)[kWords]) {
+        const uint32_t at = uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u;
+        drop_words(t, at >> 2);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[i][k] = __funnelshift_r(t[k], t[k + 1], (at & 2u) * 8u);
     }
     __device__ __forceinline__ void load_edge(int i, const uint16_t *p, int64_t left) {
 #pragma unroll
@@ -105,6 +137,12 @@ struct Values<float> {
         w[i][5] = b.y;
         w[i][6] = b.z;
         w[i][7] = b.w;
+    }
+    static constexpr int kWords = 12;
+    __device__ __forceinline__ void shift(int i, const float *p, uint32_t (&t)[kWords]) {
+        drop_words(t, (uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u) >> 2);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[i][k] = t[k];
     }
     __device__ __forceinline__ void load_edge(int i, const float *p, int64_t left) {
 #pragma unroll
@@ -148,12 +186,26 @@ fp8_quant_kernel(const Fp8Quant a) {
     // the product that follows may set itself up; it waits for this kernel's end
     let_successor_start();
     V v;
+    constexpr int kShifted = sizeof(T) == 2 ? 4 : 2;  // rows in flight
     const T *x = static_cast<const T *>(a.x) + (r0 + 8 * g) * a.ld + c;
+    // (whole chunks are read only where they end inside the matrix)
+    const T *const end = static_cast<const T *>(a.x) + (a.rows - 1) * a.ld + a.cols;
+    if (!VEC && r0 + 8 * g + 7 < a.rows && a.cols - c >= 8 && end - (x + 7 * a.ld) >= 8 + 16 / int(sizeof(T))) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t left = r0 + 8 * g + i < a.rows ? a.cols - c : 0;
-        if (VEC && left >= 8) v.load(i, x + i * a.ld);
-        else v.load_edge(i, x + i * a.ld, left);
+        for (int i0 = 0; i0 < 8; i0 += kShifted) {
+            uint32_t t[kShifted][V::kWords];
+#pragma unroll
+            for (int i = 0; i < kShifted; ++i) load_chunks(x + (i0 + i) * a.ld, t[i]);
+#pragma unroll
+            for (int i = 0; i < kShifted; ++i) v.shift(i0 + i, x + (i0 + i) * a.ld, t[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t left = r0 + 8 * g + i < a.rows ? a.cols - c : 0;
+            if (VEC && left >= 8) v.load(i, x + i * a.ld);
+            else v.load_edge(i, x + i * a.ld, left);
+        }
     }
 
     Scale8 square = {0.0f, 0.0f};
