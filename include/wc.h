@@ -398,7 +398,7 @@ WC_API int wc_grad_clip(const wc_span *spans, const wc_span *dst, int count, dou
  * first + V) of a vocabulary split over ranks contributes its own tokens.
  * table : [V][ld_table], out : [n][ld_out], both of `dtype`; rows of D values.
  * ids   : [n] of `id_type` (WC_I32 or WC_I64).
- * Requires n < 2^31, 0 <= V < 2^31 - 1, D <= 2^22, n * D < 2^40, ld_table >= D,
+ * Requires n and V <= 2^31 - 4096, D <= 2^22, n * D < 2^40, ld_table >= D,
  * ld_out >= D, 0 <= first < 2^62.
  */
 WC_API int wc_embedding(const void *table, int dtype, int64_t ld_table, const void *ids,
@@ -452,13 +452,16 @@ WC_API int wc_fp8_quant(const void *x, int dtype, int64_t rows, int64_t cols, in
  *               (sum over the block's k of A[m][k] * B[n][k])
  * each block's sum on the tensor cores, all else in fp32, rounded once to
  * out's type; accumulate != 0 adds to what out holds (out's own value, widened,
- * plus the fp32 sum, rounded once).
+ * plus the fp32 sum, rounded once).  The order of the sums depends on the sizes
+ * alone (the same bits every run).  The product of the two scales is rounded to
+ * fp32 first: where it overflows the result is infinite or not a number, where it
+ * is subnormal the sum is off by 2^-125 per block at most.
  * a, b : codes [M][lda], [N][ldb], multiples of 16 bytes per row; values past
  *        column K are not read.
  * sa, sb : scales [ceil(K/128)][ldsa], one per row (a_rows_per_scale 1) or per
  *        128 rows (128); the same for b.
  * out  : [M][ld_out] of out_dtype.
- * Requires M, N, K < 2^31, M * N < 2^44, lda, ldb >= K, ld_out >= N, and ldsa,
+ * Requires M, N, K <= 2^31 - 256, M * N < 2^44, lda, ldb >= K, ld_out >= N, and ldsa,
  * ldsb that hold a block's scales.  K = 0 writes zeros (or adds none).
  */
 WC_API int wc_fp8_matmul(const uint8_t *a, int64_t lda, const float *sa, int64_t ldsa,
@@ -478,8 +481,10 @@ WC_API int wc_wait_timeouts(int reset);
 /*
  * wc_checked_violations -- a debugging aid with no counterpart on the pages.
  * A library built with WC_CHECKED=1 compares every global load and store of
- * every kernel with the extent of its buffer, as the call's sizes define it,
- * and skips any access that would fall outside (it never traps).  This call
+ * the kernels of the exchange (quantizations, reductions, qwZ) with the extent
+ * of its buffer, as the call's sizes define it, and skips any access that would
+ * fall outside (it never traps).  The kernels of the training-step operators are
+ * the same in both builds.  This call
  * returns the number of accesses skipped since the last reset, summed over
  * the kernel files: 0 means every launch stayed inside its buffers.  When it
  * is not 0, wc_last_error() names the source file and line of one of them.

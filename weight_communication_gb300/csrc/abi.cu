@@ -475,8 +475,9 @@ int embedding_sizes(const char *fn, int id_type, int64_t n, int64_t first, int64
                     (long long)V, (long long)D);
     if (first < 0 || first >= (int64_t(1) << 62))
         return fail(WC_EINVAL, "%s: first = %lld must be in [0, 2^62)", fn, (long long)first);
-    const int64_t limit = int64_t(1) << 31;
-    if (n >= limit || V >= limit - 1) return fail(WC_ERANGE, "%s: n or V reaches 2^31", fn);
+    // (the kernels step past the last token or row in 32 bits)
+    const int64_t limit = (int64_t(1) << 31) - 4096;
+    if (n > limit || V > limit) return fail(WC_ERANGE, "%s: n or V exceeds 2^31 - 4096", fn);
     if (D > (int64_t(1) << 22)) return fail(WC_ERANGE, "%s: D exceeds 2^22", fn);
     if (D > 0 && n >= (int64_t(1) << 40) / D) return fail(WC_ERANGE, "%s: n * D reaches 2^40", fn);
     return WC_OK;

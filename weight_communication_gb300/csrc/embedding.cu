@@ -27,6 +27,7 @@
 // 50021 fp32 rows 14.5 us.
 #include "wc_device.cuh"
 #include "wc_internal.h"
+#include "wc_launch.cuh"
 
 namespace wc {
 
@@ -237,7 +238,7 @@ sort_kernel(const I *__restrict__ ids, int32_t n, int64_t first, int32_t V, int3
 
     // each warp counts its own consecutive stretch of tokens; one that fits is
     // kept for the second pass
-    const int32_t stretch = ((n + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+    const int32_t stretch = int32_t((int64_t(n) + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
     const int64_t begin = int64_t(stretch) * warp;
     const int64_t end = begin + stretch < int64_t(n) ? begin + stretch : int64_t(n);
     const bool kept = stretch <= 32 * kSortUnroll;
@@ -449,7 +450,7 @@ constexpr int kJoinParts = 4;    // threads that share a row's runs
 constexpr int kJoinThreads = kJoinLanes * kJoinParts;
 constexpr int kJoinUnroll = 4;
 
-// CTA (w, y): if a row that began earlier ends in run w, adds its parts over
+// CTA (y, w): if a row that began earlier ends in run w, adds its parts over
 // the runs, split in four consecutive shares that are added in order.  Up to
 // four parts -- all but the rows with many tokens -- are a share each; a thread
 // adds its columns' alone then, and fewer CTAs have work.  (A CTA per 256
@@ -462,7 +463,7 @@ join_kernel(SumPlan p, float scale, TO *__restrict__ dtable, int64_t ld_out,
             const float *__restrict__ heads, const float *__restrict__ tails,
             const int2 *__restrict__ joins) {
     __shared__ float part[kJoinParts][kJoinLanes * E];
-    const uint32_t w = blockIdx.x;
+    const uint32_t w = blockIdx.y, y = blockIdx.x;
     wait_for_predecessor();
     const int2 join = joins[w];
     if (join.x < 0) return;
@@ -479,7 +480,7 @@ join_kernel(SumPlan p, float scale, TO *__restrict__ dtable, int64_t ld_out,
         write_row<ACC, TO, E>(row + col, sum, scale, old);
     };
     if (count <= uint32_t(kJoinParts)) {
-        const uint32_t col = (blockIdx.y * kJoinThreads + threadIdx.x) * E;
+        const uint32_t col = (y * kJoinThreads + threadIdx.x) * E;
         if (col < p.D) {
             Pack<float, E> x[kJoinParts];
 #pragma unroll
@@ -505,7 +506,7 @@ join_kernel(SumPlan p, float scale, TO *__restrict__ dtable, int64_t ld_out,
     const uint32_t share = (count + kJoinParts - 1) / kJoinParts;
     const uint32_t b = first + s * share < w ? first + s * share : w;
     const uint32_t e = b + share < w ? b + share : w;
-    const uint32_t col = (blockIdx.y * kJoinLanes + c) * E;
+    const uint32_t col = (y * kJoinLanes + c) * E;
     float sum[E];
 #pragma unroll
     for (int k = 0; k < E; ++k) sum[k] = 0.0f;
@@ -618,7 +619,7 @@ cudaError_t launch_sum(const EmbeddingGrad &a, const SumPlan &p, int e, const in
     if (err != cudaSuccess || a.n < 2) return err;  // one token crosses no run
 #define WC_JOIN(E)                                                                            \
     launch_after(join_kernel<TO, E, ACC>,                                                     \
-                 dim3(p.workers, (p.D + kJoinLanes * E - 1) / (kJoinLanes * E)),              \
+                 dim3((p.D + kJoinLanes * E - 1) / (kJoinLanes * E), p.workers),              \
                  dim3(kJoinThreads), 0, stream, 1, p, a.scale, dtable, a.ld_out, heads, tails, joins)
     return e >= 4 ? WC_JOIN(4) : e == 2 ? WC_JOIN(2) : WC_JOIN(1);
 #undef WC_JOIN

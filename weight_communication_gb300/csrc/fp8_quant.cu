@@ -25,6 +25,7 @@
 
 #include "wc_device.cuh"
 #include "wc_internal.h"
+#include "wc_launch.cuh"
 
 namespace wc {
 

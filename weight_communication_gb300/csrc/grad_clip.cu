@@ -32,6 +32,7 @@
 
 #include "wc_device.cuh"
 #include "wc_internal.h"
+#include "wc_launch.cuh"
 
 namespace wc {
 

@@ -333,17 +333,6 @@ __device__ __forceinline__ void accumulate_word(uint32_t x, float table, f32x2 s
     }
 }
 
-// A kernel launched with launch_after() may start before its predecessor in
-// the stream has ended, and calls wait_for_predecessor() before it touches any
-// memory; a predecessor that calls let_successor_start() allows that as soon
-// as all its CTAs have started, any other one when it ends.
-__device__ __forceinline__ void let_successor_start() {
-    asm volatile("griddepcontrol.launch_dependents;");
-}
-__device__ __forceinline__ void wait_for_predecessor() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // Streaming (read-once) and plain vector accesses.
 __device__ __forceinline__ float4 ld_stream_f4(const float *p) {
     return __ldcs(reinterpret_cast<const float4 *>(p));
@@ -353,28 +342,6 @@ __device__ __forceinline__ uint2 ld_stream_u2(const void *p) {
 }
 __device__ __forceinline__ uint4 ld_stream_u4(const void *p) {
     return __ldcs(reinterpret_cast<const uint4 *>(p));
-}
-
-// Launch of a kernel that may overlap its predecessor's end (see above), in
-// clusters of `cluster` CTAs along x.
-template <typename... Params, typename... Args>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
-                         cudaStream_t stream, unsigned cluster, const Args &...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2] = {};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
 }
 
 }  // namespace wc
