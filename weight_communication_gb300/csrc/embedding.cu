@@ -6,7 +6,8 @@
 // ids outside [first, first + V) -- padding, or rows of another rank's shard --
 // read as zero and receive nothing.
 //
-// Lookup: one 16-byte vector per thread and step, four in flight; HBM-bound.
+// Lookup: one 16-byte vector per thread and step, four in flight; HBM-bound
+// (16384 x 2048 bf16 15 us with the table's rows in L2).
 //
 // Gradient: three kernels, no atomics on global memory, the same bits every
 // run.  (1) sort: each CTA owns a run of table rows, reads every id (they sit
@@ -28,6 +29,7 @@
 #include "wc_device.cuh"
 #include "wc_internal.h"
 #include "wc_launch.cuh"
+#include "wc_rows.cuh"
 
 namespace wc {
 
@@ -172,6 +174,74 @@ lookup_kernel(const T *__restrict__ table, int64_t ld_table, const I *__restrict
     }
 }
 
+// The same where rows start on any element: a thread has one aligned chunk of 16
+// bytes of an output row (chunks: of a row at most), and shifts the values that
+// belong there into place; the ends of a row go value by value.
+template <typename T, typename I>
+__global__ void __launch_bounds__(kLookupThreads)
+lookup_any_kernel(const T *__restrict__ table, int64_t ld_table, const I *__restrict__ ids, int64_t n,
+                  int64_t first, int64_t V, int32_t D, uint32_t chunks, float scale, T *__restrict__ out,
+                  int64_t ld_out) {
+    constexpr int W = 16 / int(sizeof(T));  // values of a chunk
+    const int64_t base = int64_t(blockIdx.x) * (kLookupThreads * kLookupUnroll);
+    const int64_t t0 = base / chunks;
+    const uint32_t v0 = uint32_t(base - t0 * chunks);
+    const T *const end = table + (V - 1) * ld_table + D;
+    uint32_t t[kLookupUnroll][8];
+    const T *from[kLookupUnroll];  // of the chunk's first value
+    T *to[kLookupUnroll];
+    int32_t lo[kLookupUnroll], hi[kLookupUnroll];  // values of the chunk that belong to the row
+    bool zero[kLookupUnroll], whole[kLookupUnroll];
+#pragma unroll
+    for (int j = 0; j < kLookupUnroll; ++j) {
+        const uint32_t at = v0 + threadIdx.x + j * kLookupThreads;
+        const uint32_t dt = at / chunks;
+        const int64_t token = t0 + dt;
+        const int64_t row = token < n ? row_of(ids, token, first, V) : -1;
+        T *const dst = out + token * ld_out;
+        const int32_t lead = int32_t(reinterpret_cast<uintptr_t>(dst) & 15u) / int32_t(sizeof(T));
+        const int32_t c = int32_t(at - dt * chunks) * W - lead;  // column of the chunk's first value
+        to[j] = dst + c;
+        lo[j] = max(0, -c);
+        hi[j] = token < n ? min(W, D - c) : 0;
+        zero[j] = row < 0;
+        from[j] = table + row * ld_table + c;
+        whole[j] = !zero[j] && lo[j] == 0 && hi[j] == W && end - from[j] >= 2 * W;
+        if (whole[j]) load_chunks(from[j], t[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kLookupUnroll; ++j) {
+        if (whole[j] || (zero[j] && lo[j] == 0 && hi[j] == W)) {
+            Pack<T, W> r;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r.w[k] = 0u;
+            if (whole[j]) {
+                shift_words(from[j], t[j], r.w);
+                if (scale != 1.0f) {
+                    float x[W];
+#pragma unroll
+                    for (int e = 0; e < W; ++e) x[e] = __fmul_rn(pack_value<T, W>(r, e), scale);
+                    r = pack_of<T, W>(x);
+                }
+            }
+            store_pack<T, W>(to[j], r);
+        } else {
+            for (int32_t e = lo[j]; e < hi[j]; ++e) {
+                Pack<T, 1> r;
+                r.w[0] = 0u;
+                if (!zero[j]) {
+                    r = load_pack<T, 1, false>(from[j] + e);
+                    if (scale != 1.0f) {
+                        const float x[1] = {__fmul_rn(pack_value<T, 1>(r, 0), scale)};
+                        r = pack_of<T, 1>(x);
+                    }
+                }
+                store_pack<T, 1>(to[j] + e, r);
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // gradient (1): stable counting sort of the tokens by row, and zero rows
 // ---------------------------------------------------------------------------
@@ -182,20 +252,24 @@ constexpr int kSortUnroll = 8;
 constexpr int kSortPitch = kSortWarps + 1;  // counters of a row; odd, so that a warp's
                                             // counters of different rows are in different banks
 
-// Zeros for the rows without a token: bytes of a row, distance of rows, and
-// the widest store that every row allows.  base NULL: none are written.
+// Zeros for the rows without a token: bytes of a row and distance of rows, both
+// even.  base NULL: none are written.
 struct ZeroRows {
     char *base;
-    int64_t pitch;
-    uint64_t bytes;
-    uint32_t unit;  // 16, 4 or 2
+    int64_t pitch, bytes;
 };
 
-template <typename W>
-__device__ __forceinline__ void zero_row(char *p, uint64_t bytes, int lane) {
-    const W zero = {};
-    for (uint64_t i = lane * sizeof(W); i < bytes; i += 32 * sizeof(W))
-        __stcs(reinterpret_cast<W *>(p + i), zero);
+// A warp's zeros: 16 bytes at a time, and what lies before the first and after
+// the last 16-byte boundary two by two (two by two alone, a gradient of
+// 32000 x 2047 bf16 takes 131 us instead of 104).
+__device__ __forceinline__ void zero_row(char *p, int64_t bytes, int lane) {
+    const int64_t lead = int64_t(16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15;
+    const int64_t head = lead < bytes ? lead : bytes;
+    const int64_t body = (bytes - head) / 16, tail = bytes - head - 16 * body;
+    if (2 * lane < head) __stcs(reinterpret_cast<uint16_t *>(p) + lane, uint16_t(0));
+    for (int64_t i = lane; i < body; i += 32)
+        __stcs(reinterpret_cast<uint4 *>(p + head) + i, make_uint4(0u, 0u, 0u, 0u));
+    if (2 * lane < tail) __stcs(reinterpret_cast<uint16_t *>(p + head + 16 * body) + lane, uint16_t(0));
 }
 
 // Rows of tokens t, t + 32, ..., as places in [lo, hi), -1 outside; counts the
@@ -294,10 +368,7 @@ sort_kernel(const I *__restrict__ ids, int32_t n, int64_t first, int32_t V, int3
     if (zeros.base != nullptr) {  // drained by the memory system while the rest runs
         for (int32_t r = warp; r < own; r += kSortWarps) {
             if (base[r] != (r + 1 < own ? base[r + 1] : carry)) continue;
-            char *p = zeros.base + int64_t(lo + r) * zeros.pitch;
-            if (zeros.unit == 16) zero_row<uint4>(p, zeros.bytes, lane);
-            else if (zeros.unit == 4) zero_row<uint32_t>(p, zeros.bytes, lane);
-            else zero_row<uint16_t>(p, zeros.bytes, lane);
+            zero_row(zeros.base + int64_t(lo + r) * zeros.pitch, zeros.bytes, lane);
         }
     }
 
@@ -583,6 +654,17 @@ cudaError_t lookup(const void *table, int64_t ld_table, const void *ids, int64_t
                    cudaStream_t stream) {
     int e = vector_width(uint32_t(D), ld_table, int(sizeof(T)), ld_out, int(sizeof(T)));
     if (sizeof(T) == 4 && e > 4) e = 4;
+    // Rows on no more than 4 bytes, unless they are short: 16384 of 2047 bf16 values
+    // 79 us by single values and 31 in chunks, of 151 7.6 and 6.6, of 71 4.7 and 5.8;
+    // by pairs of 2046 43 us and 30, of 502 12.2 and 12.4.
+    if (e * int(sizeof(T)) <= 4 && D * int(sizeof(T)) >= (e == 1 ? 256 : 2048)) {
+        const uint32_t chunks = uint32_t((D * int64_t(sizeof(T)) + 14) / 16 + 1);
+        const int64_t per_cta = kLookupThreads * kLookupUnroll;
+        lookup_any_kernel<T, I><<<uint32_t((n * chunks + per_cta - 1) / per_cta), kLookupThreads, 0, stream>>>(
+            static_cast<const T *>(table), ld_table, static_cast<const I *>(ids), n, first, V, int32_t(D),
+            chunks, scale, static_cast<T *>(out), ld_out);
+        return cudaPeekAtLastError();
+    }
     const uint32_t vecs = uint32_t(D / e);
     const int64_t per = kLookupThreads * kLookupUnroll;
     const uint32_t grid = uint32_t((n * vecs + per - 1) / per);
@@ -691,9 +773,7 @@ cudaError_t launch_embedding_grad(const EmbeddingGrad &a, cudaStream_t stream) {
         const int64_t size = a.out_bf16 ? 2 : 4;
         zeros.base = static_cast<char *>(a.dtable);
         zeros.pitch = a.ld_out * size;
-        zeros.bytes = uint64_t(a.D * size);
-        const uint64_t both = uint64_t(zeros.pitch) | zeros.bytes;
-        zeros.unit = both % 16 == 0 ? 16 : both % 4 == 0 ? 4 : 2;
+        zeros.bytes = a.D * size;
     }
     if (a.wide)
         sort_kernel<int64_t><<<sort_grid, kSortThreads, smem, stream>>>(

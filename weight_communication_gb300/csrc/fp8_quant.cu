@@ -20,12 +20,15 @@
 // so that a lane divides for one row and not for eight; the columns' scales
 // are likewise formed once each, by 128 threads.  The transposed codes go
 // through shared memory as 8-byte words of a column's 8 consecutive rows.
+// Rows that start anywhere are read in aligned chunks and shifted: 4411 x 9433
+// bf16 both ways 49 -> 40 us against value by value.
 // Bound: HBM (2 bytes read and 1 or 2 written per value).
 #include <cuda_fp8.h>
 
 #include "wc_device.cuh"
 #include "wc_internal.h"
 #include "wc_launch.cuh"
+#include "wc_rows.cuh"
 
 namespace wc {
 
@@ -54,31 +57,6 @@ __device__ __forceinline__ Scale8 scale_of(float m) {
     return s;
 }
 
-// Rows that start anywhere are read as the aligned chunks of 16 bytes that hold
-// the 8 values (N words, 2 or 3 chunks), and shifted into place: 4411 x 9433 bf16
-// both ways 49 -> 40 us against value by value.
-template <int N>
-__device__ __forceinline__ void load_chunks(const void *p, uint32_t (&t)[N]) {
-    const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
-#pragma unroll
-    for (int k = 0; k < N / 4; ++k) {
-        const uint4 v = __ldg(q + k);  // a neighbour's lane reads it too
-        t[4 * k] = v.x;
-        t[4 * k + 1] = v.y;
-        t[4 * k + 2] = v.z;
-        t[4 * k + 3] = v.w;
-    }
-}
-
-// Drops the first n < 4 of N words.
-template <int N>
-__device__ __forceinline__ void drop_words(uint32_t (&t)[N], uint32_t n) {
-#pragma unroll
-    for (int k = 0; k + 2 < N; ++k) t[k] = (n & 2u) ? t[k + 2] : t[k];
-#pragma unroll
-    for (int k = 0; k + 1 < N; ++k) t[k] = (n & 1u) ? t[k + 1] : t[k];
-}
-
 // The 8 x 8 values of a thread, and the operations on them that depend on the
 // type.  An encoding without its sign orders magnitudes, infinities and NaN
 // above all finite ones; Max holds such encodings (bf16: of two columns).
@@ -98,10 +76,7 @@ struct Values<uint16_t> {
     }
     static constexpr int kWords = 8;  // of the chunks of a row
     __device__ __forceinline__ void shift(int i, const uint16_t *p, uint32_t (&t)[kWords]) {
-        const uint32_t at = uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u;
-        drop_words(t, at >> 2);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[i][k] = __funnelshift_r(t[k], t[k + 1], (at & 2u) * 8u);
+        shift_words(p, t, w[i]);
     }
     __device__ __forceinline__ void load_edge(int i, const uint16_t *p, int64_t left) {
 #pragma unroll
