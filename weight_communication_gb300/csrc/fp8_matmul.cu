@@ -1030,7 +1030,7 @@ typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, 
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 cudaError_t encoder(EncodeTiled *out) {
-    static EncodeTiled fn = nullptr;  // the driver's function, the same for every call
+    static EncodeTiled fn = nullptr;  // the CUDA driver's function, the same for every call
     if (fn == nullptr) {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -1068,7 +1068,7 @@ Side side_of(const Fp8Operand &op, int64_t rows) {
     return {op.s, op.ld_s, each ? 0 : 7, each && op.ld_s % 4 == 0, int32_t(rows)};
 }
 
-// Clusters of `size` CTAs that run at once, as the driver counts them (GB300: 76,
+// Clusters of `size` CTAs that run at once, as CUDA counts them (GB300: 76,
 // 46, 36, 28, 23, 15, 15 of 2 to 8 -- the SMs of a GPC do not divide evenly).
 // Every shape of the kernel has an SM to itself, so the count is the GPU's alone
 // and is asked for once.
