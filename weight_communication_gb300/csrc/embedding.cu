@@ -664,8 +664,9 @@ cudaError_t lookup(const void *table, int64_t ld_table, const void *ids, int64_t
     if (sizeof(T) == 4 && e > 4) e = 4;
     // Rows on no more than 4 bytes, unless they are short: 16384 of 2047 bf16 values
     // 79 us by single values and 31 in chunks, of 151 7.6 and 6.6, of 71 4.7 and 5.8;
-    // by pairs of 2046 43 us and 30, of 502 12.2 and 12.4.
-    if (e * int(sizeof(T)) <= 4 && D * int(sizeof(T)) >= (e == 1 ? 256 : 2048)) {
+    // by pairs of 2046 43 us and 30, of 502 12.2 and 12.4.  Few values are bound by
+    // latency, which is longer in chunks (37 tokens of 1001 fp32 values 2.0 and 3.1).
+    if (e * int(sizeof(T)) <= 4 && D * int(sizeof(T)) >= (e == 1 ? 256 : 2048) && n * D >= (1 << 18)) {
         const uint32_t chunks = uint32_t((D * int64_t(sizeof(T)) + 14) / 16 + 1);
         const int64_t per_cta = kLookupThreads * kLookupUnroll;
         lookup_any_kernel<T, I><<<uint32_t((n * chunks + per_cta - 1) / per_cta), kLookupThreads, 0, stream>>>(
