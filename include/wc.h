@@ -25,7 +25,8 @@
  * Conventions for every entry point:
  *   - Pointers are DEVICE pointers to memory the caller allocated and owns;
  *     the library allocates nothing, frees nothing and never synchronizes
- *     the host (the debugging call wc_checked_violations excepted).  Every
+ *     the host (the debugging calls wc_checked_violations and
+ *     wc_wait_timeouts excepted).  Every
  *     call is asynchronous on `stream` (a cudaStream_t; NULL is the legacy
  *     default stream) and reads/writes its buffers only in stream order.
  *   - Kernels launch on the calling thread's current device: the pointers
