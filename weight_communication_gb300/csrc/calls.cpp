@@ -298,72 +298,99 @@ constexpr int64_t kBlock = 128;
 int64_t ceil_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 int64_t blocks(int64_t n) { return (n + kBlock - 1) / kBlock; }
 
-// A matrix [rows, cols] in 8 bits, as Python holds it: a tuple of these.
-struct Matrix8 {
-    int64_t codes = 0, ld_codes = 0, scales = 0, ld_scales = 0;
-    int64_t rows = 0, cols = 0, block_rows = 0, gpu = 0;  // gpu -1: host memory
-
-    PyObject *tuple() const {
-        PyObject *t = Py_BuildValue("LLLLLLLL", (long long)codes, (long long)ld_codes, (long long)scales,
-                                    (long long)ld_scales, (long long)rows, (long long)cols,
-                                    (long long)block_rows, (long long)gpu);
-        if (t == nullptr) throw python_error();
-        return t;
-    }
-    static Matrix8 of(PyObject *t) {
-        if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 8) bad_type("not an 8-bit matrix");
-        Matrix8 m;
-        int64_t *fields[] = {&m.codes, &m.ld_codes, &m.scales, &m.ld_scales,
-                             &m.rows,  &m.cols,     &m.block_rows, &m.gpu};
-        for (int i = 0; i < 8; ++i) *fields[i] = integer(PyTuple_GET_ITEM(t, i));
-        return m;
-    }
-    at::Device device() const {
-        return gpu < 0 ? at::Device(at::kCPU) : at::Device(at::kCUDA, c10::DeviceIndex(gpu));
-    }
-    uint8_t *q() const { return reinterpret_cast<uint8_t *>(codes); }
-    float *s() const { return reinterpret_cast<float *>(scales); }
-};
-
-int64_t checked_block_rows(PyObject *o) {
-    const int64_t b = integer(o);
+int64_t checked_block_rows(int64_t b) {
     if (b != 1 && b != kBlock) bad_value("block_rows must be 1 or 128, got ", b);
     return b;
 }
 
-// Codes, then scales, in one buffer.  The scales of a block start on 16 bytes,
-// where a product fetches them four at a time.
+// A matrix [rows, cols] in 8 bits, as a call needs it.  Python holds it as its
+// parts (codes, scales, rows, cols, block_rows), or, for codes and scales in one
+// buffer of bytes, (buffer, None, rows, cols, block_rows): the tensors themselves,
+// so that a copy of the parts is a copy of the matrix.  Addresses are taken, and
+// sizes checked, at each call.
+struct Matrix8 {
+    uint8_t *q = nullptr;
+    float *s = nullptr;
+    int64_t ld_codes = 0, ld_scales = 0, rows = 0, cols = 0, block_rows = 0;
+    at::Device device = at::Device(at::kCPU);
+
+    // Codes, then scales, in one buffer.  The scales of a block start on 16
+    // bytes, where a product fetches them four at a time.  Returns the place of
+    // the scales and, in *bytes, the buffer's size.
+    int64_t lay_out(int64_t *bytes) {
+        ld_codes = ceil_to(cols, 16);
+        ld_scales = ceil_to((rows + block_rows - 1) / block_rows, 4);
+        const int64_t scales_at = ceil_to(rows * ld_codes, 16);
+        *bytes = scales_at + blocks(cols) * ld_scales * 4;
+        return scales_at;
+    }
+    void in_buffer(const at::Tensor &buffer) {
+        int64_t bytes;
+        const int64_t scales_at = lay_out(&bytes);
+        if (buffer.scalar_type() != at::kByte || !buffer.is_contiguous() || buffer.numel() != bytes)
+            bad_value("the buffer of an 8-bit matrix [", rows, ", ", cols, "] must be ", bytes,
+                      " contiguous bytes, got ", buffer.scalar_type(), " ", buffer.sizes());
+        device = buffer.device();
+        q = static_cast<uint8_t *>(buffer.data_ptr());
+        s = reinterpret_cast<float *>(q + scales_at);
+    }
+    void in_tensors(const at::Tensor &codes, const at::Tensor &scales) {
+        if (codes.scalar_type() != at::kFloat8_e4m3fn)
+            bad_type("codes must be float8_e4m3fn, got ", codes.scalar_type());
+        if (scales.scalar_type() != at::kFloat)
+            bad_type("scales must be float32, got ", scales.scalar_type());
+        if (scales.device() != codes.device())
+            bad_value("scales are on ", scales.device(), ", codes on ", codes.device());
+        ld_codes = row_stride(codes, "codes", rows, cols);
+        ld_scales = row_stride(scales, "scales", blocks(cols), (rows + block_rows - 1) / block_rows);
+        // there is no second row to be apart from
+        if (rows <= 1 || codes.size(1) == 0) ld_codes = ceil_to(cols, 16);
+        device = codes.device();
+        q = static_cast<uint8_t *>(codes.data_ptr());
+        s = static_cast<float *>(scales.data_ptr());
+    }
+    static Matrix8 of(PyObject *t) {
+        if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 5) bad_type("not an 8-bit matrix");
+        Matrix8 m;
+        m.rows = integer(PyTuple_GET_ITEM(t, 2));
+        m.cols = integer(PyTuple_GET_ITEM(t, 3));
+        m.block_rows = checked_block_rows(integer(PyTuple_GET_ITEM(t, 4)));
+        const at::Tensor &codes = tensor(PyTuple_GET_ITEM(t, 0), "codes");
+        if (PyTuple_GET_ITEM(t, 1) == Py_None) m.in_buffer(codes);
+        else m.in_tensors(codes, tensor(PyTuple_GET_ITEM(t, 1), "scales"));
+        return m;
+    }
+};
+
+// A new matrix's buffer.
 at::Tensor make(Matrix8 *m, int64_t rows, int64_t cols, int64_t block_rows, at::Device device) {
     if (rows < 0 || cols < 0) bad_value("rows = ", rows, ", cols = ", cols, " must not be negative");
     m->rows = rows;
     m->cols = cols;
     m->block_rows = block_rows;
-    m->ld_codes = ceil_to(cols, 16);
-    m->ld_scales = ceil_to((rows + block_rows - 1) / block_rows, 4);
-    const int64_t scales_at = ceil_to(rows * m->ld_codes, 16);
-    const at::Tensor buffer = bytes_on(device, scales_at + blocks(cols) * m->ld_scales * 4);
-    m->codes = reinterpret_cast<int64_t>(buffer.data_ptr());
-    m->scales = m->codes + scales_at;
-    m->gpu = buffer.is_cuda() ? buffer.device().index() : -1;
+    int64_t bytes;
+    m->lay_out(&bytes);
+    const at::Tensor buffer = bytes_on(device, bytes);
+    m->in_buffer(buffer);
     return buffer;
 }
 
-// (rows, cols, block_rows, device, buffer, parts)
+// Its parts.
 PyObject *described(const Matrix8 &m, const at::Tensor &buffer) {
-    PyObject *device = THPDevice_New(buffer.device());
-    PyObject *t = Py_BuildValue("LLLNNN", (long long)m.rows, (long long)m.cols, (long long)m.block_rows,
-                                device, THPVariable_Wrap(buffer), m.tuple());
+    PyObject *t = Py_BuildValue("NOLLL", THPVariable_Wrap(buffer), Py_None, (long long)m.rows,
+                                (long long)m.cols, (long long)m.block_rows);
     if (t == nullptr) throw python_error();
     return t;
 }
 
-// (rows, cols, block_rows, device) -> described
+// (rows, cols, block_rows, device) -> parts
 PyObject *fp8_empty(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     arguments("fp8_empty", n, 4);
     if (!THPDevice_Check(args[3])) bad_type("device must be a torch.device");
     Matrix8 m;
-    const at::Tensor buffer = make(&m, integer(args[0]), integer(args[1]), checked_block_rows(args[2]),
+    const at::Tensor buffer = make(&m, integer(args[0]), integer(args[1]),
+                                   checked_block_rows(integer(args[2])),
                                    reinterpret_cast<THPDevice *>(args[3])->device);
     return described(m, buffer);
     END_HANDLE_TH_ERRORS
@@ -374,23 +401,14 @@ PyObject *fp8_view(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     arguments("fp8_view", n, 5);
     Matrix8 m;
-    m.block_rows = checked_block_rows(args[4]);
+    m.block_rows = checked_block_rows(integer(args[4]));
     const at::Tensor &codes = tensor(args[0], "codes"), &scales = tensor(args[1], "scales");
     m.rows = integer(args[2]);
     m.cols = integer(args[3]);
-    if (codes.scalar_type() != at::kFloat8_e4m3fn)
-        bad_type("codes must be float8_e4m3fn, got ", codes.scalar_type());
-    if (scales.scalar_type() != at::kFloat) bad_type("scales must be float32, got ", scales.scalar_type());
-    if (scales.device() != codes.device())
-        bad_value("scales are on ", scales.device(), ", codes on ", codes.device());
-    m.ld_codes = row_stride(codes, "codes", m.rows, m.cols);
-    m.ld_scales = row_stride(scales, "scales", blocks(m.cols), (m.rows + m.block_rows - 1) / m.block_rows);
-    // there is no second row to be apart from
-    if (m.rows <= 1 || codes.size(1) == 0) m.ld_codes = ceil_to(m.cols, 16);
-    m.codes = reinterpret_cast<int64_t>(codes.data_ptr());
-    m.scales = reinterpret_cast<int64_t>(scales.data_ptr());
-    m.gpu = codes.is_cuda() ? codes.device().index() : -1;
-    return m.tuple();
+    m.in_tensors(codes, scales);
+    PyObject *t = Py_BuildValue("OOOOO", args[0], args[1], args[2], args[3], args[4]);
+    if (t == nullptr) throw python_error();
+    return t;
     END_HANDLE_TH_ERRORS
 }
 
@@ -399,7 +417,7 @@ void quantize(const at::Tensor &x, const Matrix8 &q, const Matrix8 &qt, bool squ
     const int64_t ld = row_stride(x, "x", rows, cols);
     check("wc_fp8_quant",
           lib.fp8_quant(x.data_ptr(), float_type(x.scalar_type(), "x"), rows, cols, ld, square ? 1 : 0,
-                        q.q(), q.ld_codes, q.s(), q.ld_scales, qt.q(), qt.ld_codes, qt.s(),
+                        q.q, q.ld_codes, q.s, q.ld_scales, qt.q, qt.ld_codes, qt.s,
                         qt.ld_scales, stream_of(x.device())));
 }
 
@@ -409,13 +427,13 @@ const at::Tensor &matrix(PyObject *o) {
     return x;
 }
 
-// (x, rows, columns, block_rows) -> (described or None, described or None)
+// (x, rows, columns, block_rows) -> (parts or None, parts or None)
 PyObject *fp8_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     arguments("fp8_quantize", n, 4);
     const at::Tensor &x = matrix(args[0]);
     const bool rows = truth(args[1]), columns = truth(args[2]);
-    const int64_t block_rows = checked_block_rows(args[3]);
+    const int64_t block_rows = checked_block_rows(integer(args[3]));
     if (!rows && !columns) bad_value("neither rows nor columns asked for");
     on_gpu(x, "x");
     float_type(x.scalar_type(), "x");
@@ -441,7 +459,7 @@ PyObject *fp8_quantize_into(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (args[1] != Py_None) q = Matrix8::of(args[1]);
     if (args[2] != Py_None) qt = Matrix8::of(args[2]);
     const Matrix8 &any = args[1] != Py_None ? q : qt;
-    on_device(x, "x", any.device());
+    on_device(x, "x", any.device);
     if (args[1] != Py_None && (q.rows != x.size(0) || q.cols != x.size(1)))
         bad_value("x has shape ", x.sizes(), ", the 8-bit matrix [", q.rows, ", ", q.cols, "]");
     if (args[2] != Py_None && (qt.rows != x.size(1) || qt.cols != x.size(0)))
@@ -458,9 +476,9 @@ PyObject *fp8_matmul(PyObject *, PyObject *const *args, Py_ssize_t n) {
     arguments("fp8_matmul", n, 5);
     const Matrix8 a = Matrix8::of(args[0]), b = Matrix8::of(args[1]);
     if (a.cols != b.cols) bad_value("a has ", a.cols, " columns, b ", b.cols);
-    const at::Device device = a.device();
-    if (b.gpu != a.gpu) bad_value("b is on ", b.device(), ", expected ", device);
-    if (a.gpu < 0) bad_value("the operands must be CUDA tensors");
+    const at::Device device = a.device;
+    if (b.device != device) bad_value("b is on ", b.device, ", expected ", device);
+    if (!device.is_cuda()) bad_value("the operands must be CUDA tensors");
     const bool accumulate = truth(args[4]);
     const c10::cuda::CUDAGuard guard(device);
     at::Tensor out;
@@ -478,8 +496,8 @@ PyObject *fp8_matmul(PyObject *, PyObject *const *args, Py_ssize_t n) {
         ld_out = row_stride(out, "out", a.rows, b.rows);
     }
     check("wc_fp8_matmul",
-          lib.fp8_matmul(a.q(), a.ld_codes, a.s(), a.ld_scales, int(a.block_rows), b.q(), b.ld_codes,
-                         b.s(), b.ld_scales, int(b.block_rows), a.rows, b.rows, a.cols,
+          lib.fp8_matmul(a.q, a.ld_codes, a.s, a.ld_scales, int(a.block_rows), b.q, b.ld_codes,
+                         b.s, b.ld_scales, int(b.block_rows), a.rows, b.rows, a.cols,
                          out.data_ptr(), float_type(out.scalar_type(), "out"), ld_out,
                          accumulate ? 1 : 0, stream_of(device)));
     return THPVariable_Wrap(out);

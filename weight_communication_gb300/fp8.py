@@ -28,26 +28,36 @@ class Fp8Tensor:
     scales : float32 [ceil(cols / 128), >= rows] (block_rows 1) or
              [ceil(cols / 128), >= ceil(rows / 128)] (block_rows 128)
     Row r, column c stands for codes[r, c] * scales[c // 128, r // block_rows].
-    The two tensors are checked here, once; don't resize them afterwards.
+    A copy (copy.deepcopy, pickle, torch.save) has its own codes and scales.
     """
 
-    __slots__ = ("rows", "cols", "block_rows", "device", "_buffer", "_codes", "_scales", "_parts")
+    __slots__ = ("rows", "cols", "block_rows", "device", "_parts")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int,
                  block_rows: int = 1):
-        # addresses, strides and sizes, as the calls take them
-        self._parts = binding.calls().fp8_view(codes, scales, rows, cols, block_rows)
-        self._codes, self._scales, self.device = codes, scales, codes.device
-        self.rows, self.cols, self.block_rows = rows, cols, block_rows
+        self._set(binding.calls().fp8_view(codes, scales, rows, cols, block_rows))
 
     @classmethod
-    def _made(cls, described: tuple) -> "Fp8Tensor":
-        """From what the calls say of a matrix they have made: codes and scales
-        in one allocation."""
+    def _made(cls, parts: tuple) -> "Fp8Tensor":
         t = cls.__new__(cls)
-        t.rows, t.cols, t.block_rows, t.device, t._buffer, t._parts = described
-        t._codes = t._scales = None
+        t._set(parts)
         return t
+
+    # The parts (codes and scales, or one buffer of both and None, then the
+    # sizes) are the whole state: the calls take the tensors' addresses from
+    # them each time.
+    def _set(self, parts: tuple) -> None:
+        first, _, self.rows, self.cols, self.block_rows = self._parts = parts
+        self.device = first.device
+
+    # (codes as bytes: pickle itself does not know tensors of 8-bit floats)
+    def __getstate__(self) -> tuple:
+        first, scales, *sizes = self._parts
+        return (first if scales is None else first.view(torch.uint8), scales, *sizes)
+
+    def __setstate__(self, state: tuple) -> None:
+        first, scales, *sizes = state
+        self._set((first if scales is None else first.view(torch.float8_e4m3fn), scales, *sizes))
 
     @classmethod
     def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda") -> "Fp8Tensor":
@@ -56,19 +66,21 @@ class Fp8Tensor:
 
     @property
     def codes(self) -> torch.Tensor:
-        if self._codes is None:
-            ld = self._parts[1]
-            self._codes = (self._buffer[:self.rows * ld].view(torch.float8_e4m3fn)
-                           .view(self.rows, ld))
-        return self._codes
+        first, scales = self._parts[:2]
+        if scales is not None:
+            return first
+        ld = -(-self.cols // 16) * 16
+        return first[:self.rows * ld].view(torch.float8_e4m3fn).view(self.rows, ld)
 
     @property
     def scales(self) -> torch.Tensor:
-        if self._scales is None:
-            codes, _, scales, ld = self._parts[:4]
-            self._scales = (self._buffer[scales - codes:].view(torch.float32)
-                            .view(-(-self.cols // BLOCK), ld)[:, :-(-self.rows // self.block_rows)])
-        return self._scales
+        first, scales = self._parts[:2]
+        if scales is not None:
+            return scales
+        blocks, per = -(-self.cols // BLOCK), -(-self.rows // self.block_rows)
+        ld = -(-per // 4) * 4
+        return (first[first.numel() - blocks * ld * 4:].view(torch.float32)
+                .view(blocks, ld)[:, :per])
 
 
 def quantize(x: torch.Tensor, rows: bool = True, columns: bool = False, stream=None):
