@@ -290,22 +290,27 @@ __device__ __forceinline__ void load_rows(const I *ids, int64_t t, int64_t end, 
 
 // order[p], rows[p]: token and row at sorted place p.  row_start[v]: first
 // place of row v; row_start[V]: tokens with a row.  CTA b owns rows
-// [b * per_cta, (b + 1) * per_cta).  Dynamic shared memory: per_cta *
-// (kSortPitch + 1) counters.
+// [b * per_cta, (b + 1) * per_cta).  All of its shared memory is dynamic,
+// sort_smem(per_cta) bytes: what a launch asks for is then what the 48 KB that
+// need no opt-in are compared with.
+__host__ __device__ constexpr size_t sort_smem(int32_t per_cta) {
+    return (size_t(per_cta) * (kSortPitch + 1) + kSortWarps + 1) * 4;
+}
+
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads)
 sort_kernel(const I *__restrict__ ids, int32_t n, int64_t first, int32_t V, int32_t per_cta,
             int32_t *__restrict__ order, int32_t *__restrict__ rows,
             int32_t *__restrict__ row_start, const ZeroRows zeros) {
     extern __shared__ int32_t counters[];
-    __shared__ int32_t warp_total[kSortWarps];
-    __shared__ int32_t below_total;
     let_successor_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t lo = int32_t(blockIdx.x) * per_cta;
     const int32_t hi = min(V, lo + per_cta);
     const int32_t own = hi - lo;
     int32_t *base = counters + per_cta * kSortPitch;  // first place of each row
+    int32_t *warp_total = base + per_cta;
+    int32_t &below_total = warp_total[kSortWarps];
     for (int i = threadIdx.x; i < per_cta * (kSortPitch + 1); i += kSortThreads) counters[i] = 0;
     if (threadIdx.x == 0) below_total = 0;
     __syncthreads();
@@ -618,7 +623,7 @@ join_kernel(SumPlan p, float scale, TO *__restrict__ dtable, int64_t ld_out,
 // ---------------------------------------------------------------------------
 
 constexpr int kSms = 152;
-// The sort's counters fill at most 136 KB of shared memory (larger tables
+// The sort fills at most 137 KB of shared memory (larger tables
 // take more CTAs than SMs).
 constexpr int32_t kSortRowsMax = 1024;
 constexpr int kSumCtas = 4 * kSms;
@@ -767,15 +772,15 @@ cudaError_t launch_embedding_grad(const EmbeddingGrad &a, cudaStream_t stream) {
     int32_t per_cta = int32_t((a.V + kSms - 1) / kSms);
     if (per_cta > kSortRowsMax) per_cta = kSortRowsMax;
     const uint32_t sort_grid = uint32_t((a.V + per_cta - 1) / per_cta);
-    const size_t smem = size_t(per_cta) * (kSortPitch + 1) * 4;
+    const size_t smem = sort_smem(per_cta);
     cudaError_t err = cudaSuccess;
     if (smem > 48 * 1024)
         err = a.wide ? cudaFuncSetAttribute(sort_kernel<int64_t>,
                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            kSortRowsMax * (kSortPitch + 1) * 4)
+                                            int(sort_smem(kSortRowsMax)))
                      : cudaFuncSetAttribute(sort_kernel<int32_t>,
                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            kSortRowsMax * (kSortPitch + 1) * 4);
+                                            int(sort_smem(kSortRowsMax)));
     if (err != cudaSuccess) return err;
     ZeroRows zeros = {};
     if (!a.accumulate) {
