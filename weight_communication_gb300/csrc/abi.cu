@@ -27,6 +27,9 @@ int fail(int code, const char *fmt, ...) {
 
 int from_cuda(cudaError_t err, const char *what) {
     if (err == cudaSuccess) return WC_OK;
+    // Reported here, so cleared: the launches ask for the last error, and a later
+    // call would find this one again.  (One that ended the context stays.)
+    (void)cudaGetLastError();
     return fail(WC_ECUDA, "%s: %s (%s)", what, cudaGetErrorName(err), cudaGetErrorString(err));
 }
 
