@@ -33,7 +33,8 @@
  *     and the stream must belong to it.
  *   - bf16 values are passed as uint16_t bit patterns.
  *   - Every device pointer must be 16-byte aligned (WC_EALIGN otherwise), the
- *     addresses in a wc_span excepted.
+ *     addresses in a wc_span and those of token ids excepted (aligned to their
+ *     values).
  *   - Buffers must not overlap unless an entry point says so.
  *   - Inputs must be finite (not checked) unless an entry point says what
  *     infinities and NaN do.
@@ -398,7 +399,7 @@ WC_API int wc_grad_clip(const wc_span *spans, const wc_span *dst, int count, dou
  * so that negative ids are padding, and a table that holds rows [first,
  * first + V) of a vocabulary split over ranks contributes its own tokens.
  * table : [V][ld_table], out : [n][ld_out], both of `dtype`; rows of D values.
- * ids   : [n] of `id_type` (WC_I32 or WC_I64).
+ * ids   : [n] of `id_type` (WC_I32 or WC_I64), starting on any id.
  * Requires n and V <= 2^31 - 4096, D <= 2^22, n * D < 2^40, ld_table >= D,
  * ld_out >= D, 0 <= first < 2^62.
  */

@@ -486,6 +486,15 @@ int embedding_sizes(const char *fn, int id_type, int64_t n, int64_t first, int64
     return WC_OK;
 }
 
+// Ids are read one at a time, so they start on any id.
+int ids_pointer(const char *fn, const void *ids, int id_type) {
+    const uintptr_t size = id_type == WC_I64 ? 8 : 4;
+    if (ids == nullptr) return fail(WC_EINVAL, "%s: ids is NULL", fn);
+    if (reinterpret_cast<uintptr_t>(ids) % size)
+        return fail(WC_EALIGN, "%s: ids is not aligned to its %d-byte values", fn, int(size));
+    return WC_OK;
+}
+
 int64_t blocks128(int64_t n) { return (n + 127) / 128; }
 
 }  // namespace
@@ -520,7 +529,7 @@ WC_API int wc_embedding(const void *table, int dtype, int64_t ld_table, const vo
                     (long long)ld_table, (long long)ld_out, (long long)D);
     if (n == 0 || D == 0) return WC_OK;
     if (V > 0) WC_REQUIRE_PTR(fn, table);
-    WC_REQUIRE_PTR(fn, ids);
+    if ((rc = ids_pointer(fn, ids, id_type)) != WC_OK) return rc;
     WC_REQUIRE_PTR(fn, out);
     return from_cuda(wc::launch_embedding(table, dtype == WC_BF16, ld_table, ids, id_type == WC_I64,
                                           n, first, V, D, scale, out, ld_out,
@@ -557,7 +566,7 @@ WC_API int wc_embedding_grad(const void *dy, int dy_dtype, int64_t ld_dy, const 
     if (V == 0 || D == 0 || (n == 0 && accumulate)) return WC_OK;
     if (n > 0) {
         WC_REQUIRE_PTR(fn, dy);
-        WC_REQUIRE_PTR(fn, ids);
+        if ((rc = ids_pointer(fn, ids, id_type)) != WC_OK) return rc;
     }
     WC_REQUIRE_PTR(fn, dtable);
     WC_REQUIRE_PTR(fn, workspace);
