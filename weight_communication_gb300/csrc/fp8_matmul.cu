@@ -37,6 +37,7 @@
 #include "wc_device.cuh"
 #include "wc_internal.h"
 #include "wc_launch.cuh"
+#include "wc_wait.cuh"
 
 namespace wc {
 
@@ -48,56 +49,12 @@ namespace {
 
 __device__ unsigned int g_wait_timeouts;
 
-__device__ __forceinline__ uint32_t smem_of(const void *p) {
-    return uint32_t(__cvta_generic_to_shared(p));
-}
-
-// One lane of a converged warp.  (The loops of the TMA and MMA warps are run by
-// all lanes alike, so their counters and descriptors are uniform registers.)
-__device__ __forceinline__ bool elected() {
-    uint32_t r;
-    asm volatile(
-        "{\n.reg .pred p;\n"
-        "elect.sync _|p, 0xFFFFFFFF;\n"
-        "selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(r));
-    return r != 0;
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\n"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        "selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
-// A converged warp waits for the phase of that parity to end.  A wait that does
-// not end within about two seconds is given up: the role that sees it returns,
-// the others run out in turn, and the count of such waits is left for the host.
-// (The vote makes the answer, and the branch on it, uniform.)
+// The warp of a role that gives up a wait returns, the others run out in turn,
+// and the count of such waits is left for the host.  (The loops of the TMA and
+// MMA warps are run by all lanes alike, so their counters and descriptors are
+// uniform registers.)
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-    if (__all_sync(kFull, mbar_try(bar, parity))) return true;
-    unsigned long long start, now;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(start));
-    for (uint32_t i = 0; i < (1u << 28); ++i) {
-        if (__all_sync(kFull, mbar_try(bar, parity))) return true;
-        if ((i & 63u) == 63u) {
-            asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
-            if (__any_sync(kFull, now - start > 2000000000ull)) break;
-        }
-    }
-    if (elected()) atomicAdd(&g_wait_timeouts, 1u);
-    __syncwarp();
-    return false;
+    return wc::mbar_wait(bar, parity, &g_wait_timeouts);
 }
 
 // 16 bytes, those past `bytes` zero.
@@ -112,10 +69,6 @@ __device__ __forceinline__ void copy4(uint32_t dst, const float *src) {
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // The address of the same shared variable in CTA `rank` of the cluster.
