@@ -473,10 +473,11 @@ WC_API int wc_fp8_matmul(const uint8_t *a, int64_t lda, const float *sa, int64_t
 
 /*
  * wc_wait_timeouts -- a debugging aid: waits inside wc_fp8_matmul's kernels
- * that were given up after about two seconds, since the library was loaded or
- * last reset (reset != 0).  0 in every run whose launches were complete; a
- * launch that counted here has left its output unfinished.  Reads device
- * memory synchronously: synchronize the streams it should cover first.
+ * that were given up after about two seconds of running, since the library was
+ * loaded or last reset (reset != 0).  0 in every run whose launches were
+ * complete; a launch that counted here has left NaN in every output that misses
+ * a sum.  Reads device memory synchronously: synchronize the streams it should
+ * cover first.
  */
 WC_API int wc_wait_timeouts(int reset);
 

@@ -49,10 +49,11 @@ namespace {
 
 __device__ unsigned int g_wait_timeouts;
 
-// The warp of a role that gives up a wait returns, the others run out in turn,
-// and the count of such waits is left for the host.  (The loops of the TMA and
-// MMA warps are run by all lanes alike, so their counters and descriptors are
-// uniform registers.)
+// A warp that gives up a wait takes no further part: it arrives on no barrier and
+// starts no copy or product, so what the others still complete is complete, and
+// they run out in turn.  Every output that misses a sum is NaN, and the waits are
+// counted for the host.  (The loops of the TMA and MMA warps are run by all lanes
+// alike, so their counters and descriptors are uniform registers.)
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     return wc::mbar_wait(bar, parity, &g_wait_timeouts);
 }
@@ -142,15 +143,15 @@ __device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint
             : "memory");
 }
 
-// Arrives on the barrier (PAIR: on both CTAs') when the products issued so far
-// have ended.
+// Arrives on the barrier (PAIR: on that of each CTA of the pair in `ctas`) when
+// the products issued so far have ended.
 template <bool PAIR>
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint16_t ctas = 3) {
     if (PAIR)
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
             "[%0], %1;" ::"r"(bar),
-            "h"(uint16_t(3))
+            "h"(ctas)
             : "memory");
     else
         asm volatile(
@@ -359,6 +360,17 @@ __device__ __forceinline__ void put(const Args &a, int64_t at, float x) {
         if (a.accumulate) x = __fadd_rn(*p, x);
         *p = x;
     }
+}
+
+// NaN for a warp's 32 rows x cols columns of a tile, where its sums are missing.
+template <bool TRANS>
+__device__ __forceinline__ void put_nan(const Args &a, int32_t i0, int32_t j0, int cols, int lane) {
+#pragma unroll 1
+    for (int r = 0; r < 32 && i0 + r < a.i.rows; ++r)
+#pragma unroll 1
+        for (int c = lane; c < cols && j0 + c < a.j.rows; c += 32)
+            put(a, TRANS ? int64_t(j0 + c) * a.ld_out + i0 + r : int64_t(i0 + r) * a.ld_out + j0 + c,
+                __uint_as_float(0x7FC00000u));
 }
 
 // What a kernel can do with out: its rows start on 16 bytes and are written; they
@@ -583,7 +595,12 @@ __device__ __forceinline__ void store_tile(const Args &a, const f32x2 (&acc)[COL
 // cluster and stores it.  It begins with its own part and goes round, so the
 // order is fixed for each line and no CTA is read by all others at once (all from
 // the first one on: 128 x 1003 x 11008 with eight CTAs 15 us, so 10.3).
+// missing: a CTA of the cluster gave up, so every line is NaN.
 constexpr int kPartialPitch = 132;
+
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
@@ -596,7 +613,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 
 template <bool TRANS, int NT, int WARPS>
 __device__ __forceinline__ void add_partials(const Args &a, int32_t tile, int32_t part, uint32_t partial,
-                                             int warp, int lane) {
+                                             bool missing, int warp, int lane) {
     int32_t ti, tj;
     tile_at(a, tile, &ti, &tj);
     const int32_t line0 = TRANS ? tj * NT : ti * kRows, at0 = (TRANS ? ti * kRows : tj * NT) + 4 * lane;
@@ -613,6 +630,10 @@ __device__ __forceinline__ void add_partials(const Args &a, int32_t tile, int32_
             x.y = __fadd_rn(x.y, y.y);
             x.z = __fadd_rn(x.z, y.z);
             x.w = __fadd_rn(x.w, y.w);
+        }
+        if (missing) {
+            const float nan = __uint_as_float(0x7FC00000u);
+            x = make_float4(nan, nan, nan, nan);
         }
         if (left <= 0) continue;
         const int64_t at = int64_t(line0 + line) * a.ld_out + at0;
@@ -651,7 +672,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
     // (One barrier to wait for and one to arrive on keep the MMA thread's work
     // beside the products short: the queue of products is two deep.)
     __shared__ uint64_t full[S::kStages], done[S::kStages], drained;
-    __shared__ uint32_t tmem_slot;
+    __shared__ uint32_t tmem_slot, gave_up;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t stages = (smem_of(dynamic_smem) + 1023u) & ~1023u;
     uint8_t *const aligned_smem = dynamic_smem + (stages - smem_of(dynamic_smem));
@@ -673,6 +694,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
             mbar_init(smem_of(&done[s]), 2);
         }
         mbar_init(smem_of(&drained), 1);
+        gave_up = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -743,11 +765,11 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
                     if (++buf == S::kBuffers) buf = 0;
                 }
             }
-            if (!ok) {  // no product may be in flight when the TMEM is freed
-                if (lead) mma_commit<kPair>(smem_of(&drained));
-                __syncwarp();
-                mbar_wait(smem_of(&drained), 0);
-            }
+            // No product may be in flight when the TMEM is freed.  (The epilogue has
+            // waited for the last one too, unless it gave up.)
+            if (lead) mma_commit<kPair>(smem_of(&drained), 1);
+            __syncwarp();
+            mbar_wait(smem_of(&drained), 0);
         } else if (warp == kScaler) {
             const int32_t mine = first_tile < tiles ? (tiles - 1 - first_tile) / tile_step + 1 : 0;
             const int64_t steps = int64_t(mine) * blocks;
@@ -755,10 +777,9 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
             uint32_t slot = 0, stage = 0, seen = 0, seen_phase = 0;
             ScaleRows<kRows> si;
             ScaleRows<VECJ ? NT : S::kGroups> sj;
-            bool ok = true;
-            for (int64_t g = -S::kAhead; ok && g < steps; ++g) {
+            for (int64_t g = -S::kAhead; g < steps; ++g) {
                 if (g + S::kAhead - S::kScaleSlots + S::kBuffers + 1 >= 0) {
-                    ok = mbar_wait(smem_of(&done[seen]), seen_phase);
+                    if (!mbar_wait(smem_of(&done[seen]), seen_phase)) break;
                     if (++seen == S::kStages) {
                         seen = 0;
                         seen_phase ^= 1u;
@@ -804,8 +825,6 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
         uint32_t freed = S::kBuffers;
         for (int b = 0; b < S::kBuffers; ++b)
             if (lead) buffer_free<kPair>(full0 + b * 8);
-        // After a wait that ran out the warps go through the rest without
-        // waiting or storing.
         for (int32_t t = first_tile; t < tiles; t += tile_step) {
             int32_t ti, tj;
             tile_at(a, t, &ti, &tj);
@@ -814,8 +833,9 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
             f32x2 acc[S::kCols / 2];
 #pragma unroll
             for (int c = 0; c < S::kCols / 2; ++c) acc[c] = pack2(0.0f, 0.0f);
-            for (int32_t kb = 0; kb < blocks; ++kb) {
-                if (ok) ok = mbar_wait(smem_of(&done[stage]), phase);
+            for (int32_t kb = 0; ok && kb < blocks; ++kb) {
+                ok = mbar_wait(smem_of(&done[stage]), phase);
+                if (!ok) break;
                 tc_after_sync();
                 const uint32_t from = from0 + buf * NT;
                 const float *sc = scales + slot * S::kScales;
@@ -907,7 +927,14 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
                     if (more) tmem_wait(p[(k + 1) & 1]);
                 }
             }
-            if (!ok) continue;
+            if (!ok) {  // this tile and all later ones of this warp
+                if (!kPair && a.split > 1) {  // its part is missing in every CTA of the cluster
+                    if (lane < a.split) st_cluster_u32(in_cta(smem_of(&gave_up), lane), 1u);
+                    break;
+                }
+                put_nan<TRANS>(a, i - lane, j0, S::kCols, lane);
+                continue;
+            }
             if (!kPair && a.split > 1) {
                 // the last product is complete, so the stages are free
 #pragma unroll
@@ -953,7 +980,9 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_i, const __grid_consta
         __syncwarp();
         cluster_sync();
         if (warp < kProducer && first_tile < tiles)
-            add_partials<TRANS, NT, S::kGroups * 4>(a, first_tile, part, smem_of(partial), warp, lane);
+            add_partials<TRANS, NT, S::kGroups * 4>(a, first_tile, part, smem_of(partial),
+                                                    *reinterpret_cast<volatile uint32_t *>(&gave_up) != 0u,
+                                                    warp, lane);
         cluster_sync();
     }
     tc_before_sync();
