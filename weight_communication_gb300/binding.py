@@ -125,8 +125,10 @@ def calls():
         return _calls
     lib = load()
     if not _build.CALLS.exists():
+        why = _build.CALLS_LOG.read_text().strip() if _build.CALLS_LOG.exists() else ""
         raise RuntimeError(f"extension module {_build.CALLS} is missing: build it with "
-                           "`python -m weight_communication_gb300.build`")
+                           "`python -m weight_communication_gb300.build`"
+                           + (f" (the last build stopped at: {why})" if why else ""))
     loader = importlib.machinery.ExtensionFileLoader("wc_calls", str(_build.CALLS))
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("wc_calls", loader))
     loader.exec_module(module)

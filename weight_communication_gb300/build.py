@@ -6,7 +6,9 @@ Each .cu file under csrc/ compiles to an object in parallel; the objects link
 into one shared library with the CUDA runtime linked statically, so the
 library needs only the driver at run time.  Beside it, csrc/calls.cpp becomes
 wc_calls.so: the Python calls of the training-step operators on torch's
-tensors, which call the library.
+tensors, which call the library.  They alone need torch and the headers of torch
+and Python: without those the library is built all the same, and the calls say
+at their first use why they are missing.
 """
 from __future__ import annotations
 
@@ -24,6 +26,7 @@ INCLUDE = PKG.parent / "include"
 BUILD = PKG / "_build"
 LIB = BUILD / "libwc.so"
 CALLS = BUILD / "wc_calls.so"
+CALLS_LOG = BUILD / "calls.log"
 # The checked build (every kernel access compared with its buffer's extent,
 # see wc_checked_violations in include/wc.h) goes to a folder of its own.
 CHECKED_BUILD = BUILD / "checked"
@@ -76,7 +79,8 @@ def _compile_calls() -> Path:
 
 
 def build(verbose: bool = False, checked: bool = False) -> Path:
-    """Compile every kernel file and link libwc.so, and the Python calls;
+    """Compile every kernel file and link libwc.so, and, where torch and its
+    headers are, the Python calls (what stopped them goes to calls.log);
     checked=True builds the bounds-checked library (WC_CHECKED=1) into its own
     folder instead (the Python calls work with either library)."""
     out, lib = (CHECKED_BUILD, CHECKED_LIB) if checked else (BUILD, LIB)
@@ -94,9 +98,16 @@ def build(verbose: bool = False, checked: bool = False) -> Path:
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", str(tmp),
            *[str(o) for o, _ in results]]
     subprocess.run(cmd, check=True)
-    if calls is not None:
-        os.replace(calls.result(), CALLS)
     os.replace(tmp, lib)
+    if calls is not None:
+        CALLS_LOG.write_text("")
+        try:
+            os.replace(calls.result(), CALLS)
+        except (ImportError, OSError, RuntimeError) as e:
+            CALLS.unlink(missing_ok=True)  # an older one may not fit the new library
+            CALLS_LOG.write_text(f"{type(e).__name__}: {e}\n")
+            print(f"{lib} is built, the Python calls of the training-step operators are not: "
+                  f"see {CALLS_LOG}", file=sys.stderr)
     return lib
 
 
