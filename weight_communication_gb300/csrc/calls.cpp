@@ -250,26 +250,62 @@ PyObject *embedding_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
 // gradient norm
 // ---------------------------------------------------------------------------
 
-// (address of a wc_span array, of the destinations' (0: in place), tensors,
-//  clip, max_norm, eps, stats or None, device) -> stats
+// The wc_span list of a tuple of dense tensors on one GPU (*device, if the tuple
+// is the first of its call).  Made at each call, so it is where the tensors are now.
+using Spans = c10::SmallVector<wc_span, 32>;
+Spans spans_of(PyObject *tuple, const char *name, std::optional<at::Device> *device) {
+    if (!PyTuple_Check(tuple)) bad_type(name, " must be a tuple of tensors, got ", Py_TYPE(tuple)->tp_name);
+    const Py_ssize_t count = PyTuple_GET_SIZE(tuple);
+    if (count > 0x7FFFFFFF) bad_value("a list of ", count, " tensors is too long");
+    Spans spans;
+    spans.reserve(size_t(count));
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        const at::Tensor &t = tensor(PyTuple_GET_ITEM(tuple, i), name);
+        if (!t.is_cuda()) bad_value(name, "[", i, "] must be a CUDA tensor");
+        if (!device->has_value()) *device = t.device();
+        else if (t.device() != **device) bad_value(name, "[", i, "] is on ", t.device(), ", expected ", **device);
+        if (!t.is_contiguous()) bad_value(name, "[", i, "] must be contiguous");
+        const bool f32 = t.scalar_type() == at::kFloat;
+        if (!f32 && t.scalar_type() != at::kBFloat16)
+            bad_type(name, "[", i, "] must be float32 or bfloat16, got ", t.scalar_type());
+        spans.push_back({t.numel() > 0 ? t.data_ptr() : nullptr, t.numel(), f32 ? WC_F32 : WC_BF16, 0});
+    }
+    return spans;
+}
+
+// (tuple of tensors) -> their GPU, or None if there are none
+PyObject *grad_list(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arguments("grad_list", n, 1);
+    std::optional<at::Device> device;
+    spans_of(args[0], "tensors", &device);
+    if (!device.has_value()) Py_RETURN_NONE;
+    return THPDevice_New(*device);
+    END_HANDLE_TH_ERRORS
+}
+
+// (tensors, where their values go or None (in place), clip, max_norm, eps,
+//  stats or None) -> stats
 PyObject *grad_norm(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    arguments("grad_norm", n, 8);
-    const auto *spans = reinterpret_cast<const wc_span *>(integer(args[0]));
-    const auto *dst = reinterpret_cast<const wc_span *>(integer(args[1]));
-    const int64_t listed = integer(args[2]);
-    if (listed > 0x7FFFFFFF) bad_value("a list of ", listed, " tensors is too long");
-    const int count = int(listed);
-    const bool clip = truth(args[3]);
-    if (!THPDevice_Check(args[7])) bad_type("device must be a torch.device");
-    const at::Device device = reinterpret_cast<THPDevice *>(args[7])->device;
+    arguments("grad_norm", n, 6);
+    std::optional<at::Device> found;
+    const Spans spans = spans_of(args[0], "tensors", &found);
+    if (!found.has_value()) bad_value("an empty list has no GPU to run on");
+    const bool in_place = args[1] == Py_None;
+    const Spans dst = in_place ? Spans() : spans_of(args[1], "out", &found);
+    if (!in_place && dst.size() != spans.size())
+        bad_value("out has ", dst.size(), " tensors, expected ", spans.size());
+    const int count = int(spans.size());
+    const bool clip = truth(args[2]);
+    const at::Device device = *found;
     const c10::cuda::CUDAGuard guard(device);
     at::Tensor stats;
     const int64_t values = clip ? 2 : 1;
-    if (args[6] == Py_None) {
+    if (args[5] == Py_None) {
         stats = new_tensor({values}, at::kFloat, device);
     } else {
-        stats = tensor(args[6], "stats");
+        stats = tensor(args[5], "stats");
         on_gpu(stats, "stats");
         on_device(stats, "stats", device);
         if (stats.scalar_type() != at::kFloat) bad_type("stats must be float32, got ", stats.scalar_type());
@@ -280,10 +316,11 @@ PyObject *grad_norm(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const at::Tensor workspace = bytes_on(device, lib.grad_norm_workspace(count));
     auto *out = static_cast<float *>(stats.data_ptr());
     if (clip)
-        check("wc_grad_clip", lib.grad_clip(spans, dst, count, real(args[4]), real(args[5]), out,
-                                            workspace.data_ptr(), workspace.numel(), stream_of(device)));
+        check("wc_grad_clip", lib.grad_clip(spans.data(), in_place ? nullptr : dst.data(), count,
+                                            real(args[3]), real(args[4]), out, workspace.data_ptr(),
+                                            workspace.numel(), stream_of(device)));
     else
-        check("wc_grad_norm", lib.grad_norm(spans, count, out, workspace.data_ptr(),
+        check("wc_grad_norm", lib.grad_norm(spans.data(), count, out, workspace.data_ptr(),
                                             workspace.numel(), stream_of(device)));
     return THPVariable_Wrap(stats);
     END_HANDLE_TH_ERRORS
@@ -535,7 +572,7 @@ PyObject *setup(PyObject *, PyObject *const *args, Py_ssize_t n) {
 #define WC_METHOD(name) \
     { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {WC_METHOD(setup),        WC_METHOD(embedding),    WC_METHOD(embedding_grad),
-                         WC_METHOD(grad_norm),    WC_METHOD(fp8_empty),    WC_METHOD(fp8_view),
+                         WC_METHOD(grad_list),    WC_METHOD(grad_norm),    WC_METHOD(fp8_empty),    WC_METHOD(fp8_view),
                          WC_METHOD(fp8_quantize), WC_METHOD(fp8_quantize_into), WC_METHOD(fp8_matmul),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "wc_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -11,8 +11,6 @@ come back as a tensor that the update, or a log line some steps later, reads.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import binding
@@ -20,14 +18,13 @@ from . import binding
 
 class TensorList:
     """A list of gradient tensors (float32 or bfloat16, contiguous, on one GPU,
-    of any sizes and at any offsets into larger buffers), checked once and
-    described to the library as addresses and lengths.  It keeps the tensors
-    alive; make another one if a gradient moves to another buffer."""
+    of any sizes and at any offsets into larger buffers), checked when it is
+    made and at every call, which takes their addresses and lengths as they are
+    then.  It keeps the tensors alive."""
 
     def __init__(self, tensors):
         self.tensors = tuple(tensors)
-        self.spans, self.device = binding.spans(self.tensors)
-        self.address = ctypes.addressof(self.spans)
+        self.device = binding.calls().grad_list(self.tensors)
 
     def __len__(self) -> int:
         return len(self.tensors)
@@ -41,9 +38,8 @@ def _run(lst: TensorList, dst: TensorList | None, clipping: bool, max_norm: floa
          stats: torch.Tensor | None, stream) -> torch.Tensor:
     if lst.device is None:
         raise ValueError("an empty list has no GPU to run on")
-    return binding.on_stream(stream, lst.device, binding.calls().grad_norm, lst.address,
-                             0 if dst is None else dst.address, len(lst.tensors), clipping,
-                             max_norm, eps, stats, lst.device)
+    return binding.on_stream(stream, lst.device, binding.calls().grad_norm, lst.tensors,
+                             None if dst is None else dst.tensors, clipping, max_norm, eps, stats)
 
 
 def norm(tensors, stats: torch.Tensor | None = None, stream=None) -> torch.Tensor:
