@@ -15,6 +15,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/StringUtil.h>
@@ -133,6 +134,21 @@ int64_t row_stride(const at::Tensor &t, const char *name, int64_t rows, int64_t 
     return t.stride(0);
 }
 
+// The calls stand outside autograd.  A tensor that they write to gets a new
+// version, so that a backward pass that saved its values finds it changed; an
+// input whose gradient ends here is told of.
+void written(const at::Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
+void ends_gradient(const at::Tensor &t, const char *call, const char *name) {
+    if (!t.requires_grad() || !c10::GradMode::is_enabled()) return;
+    const std::string m = c10::str(call, " stands outside autograd: no gradient will reach ", name,
+                                   " through its result (torch.no_grad() or ", name,
+                                   ".detach() says that this is meant)");
+    if (PyErr_WarnEx(PyExc_UserWarning, m.c_str(), 1) < 0) throw python_error();
+}
+
 void *stream_of(at::Device device) {
     return c10::cuda::getCurrentCUDAStream(device.index()).stream();
 }
@@ -189,10 +205,12 @@ PyObject *embedding(PyObject *, PyObject *const *args, Py_ssize_t n) {
             bad_value("out has shape ", out.sizes(), ", expected [", tokens, ", ", D, "]");
         ld_out = row_stride(out, "out", tokens, D);
     }
+    ends_gradient(table, "embedding.lookup", "table");
     check("wc_embedding",
           lib.embedding(table.data_ptr(), type, ld_table, ids.data_ptr(), id_type, tokens,
                         integer(args[3]), V, D, float(real(args[2])), out.data_ptr(), ld_out,
                         stream_of(table.device())));
+    if (args[4] != Py_None) written(out);
     return THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
 }
@@ -234,6 +252,7 @@ PyObject *embedding_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
         ld_out = row_stride(out, "out", V, D);
     }
     const int out_type = float_type(out.scalar_type(), "out");
+    ends_gradient(dy, "embedding.grad", "dy");
     const int64_t bytes = lib.embedding_grad_workspace(tokens, V, D);
     check("wc_embedding_grad_workspace", bytes);
     const at::Tensor workspace = bytes_on(dy.device(), bytes > 16 ? bytes : 16);
@@ -242,6 +261,7 @@ PyObject *embedding_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
                              integer(args[4]), V, D, float(real(args[3])), accumulate ? 1 : 0,
                              out.data_ptr(), out_type, ld_out, workspace.data_ptr(),
                              workspace.numel(), stream_of(dy.device())));
+    if (args[5] != Py_None) written(out);
     return THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
 }
@@ -322,6 +342,11 @@ PyObject *grad_norm(PyObject *, PyObject *const *args, Py_ssize_t n) {
     else
         check("wc_grad_norm", lib.grad_norm(spans.data(), count, out, workspace.data_ptr(),
                                             workspace.numel(), stream_of(device)));
+    if (args[5] != Py_None) written(stats);
+    if (clip) {
+        PyObject *to = in_place ? args[0] : args[1];
+        for (int i = 0; i < count; ++i) written(THPVariable_Unpack(PyTuple_GET_ITEM(to, i)));
+    }
     return THPVariable_Wrap(stats);
     END_HANDLE_TH_ERRORS
 }
@@ -474,6 +499,8 @@ PyObject *fp8_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (!rows && !columns) bad_value("neither rows nor columns asked for");
     on_gpu(x, "x");
     float_type(x.scalar_type(), "x");
+    // (a weight's codes are kept beside it, and its gradient comes from backward)
+    if (block_rows == 1) ends_gradient(x, "fp8.quantize", "x");
     const c10::cuda::CUDAGuard guard(x.device());
     Matrix8 q, qt;
     at::Tensor buffer, buffer_t;
@@ -503,6 +530,9 @@ PyObject *fp8_quantize_into(PyObject *, PyObject *const *args, Py_ssize_t n) {
         bad_value("x has shape ", x.sizes(), ", the transposed 8-bit matrix [", qt.rows, ", ", qt.cols, "]");
     const c10::cuda::CUDAGuard guard(x.device());
     quantize(x, q, qt, any.block_rows == kBlock);
+    for (PyObject *parts : {args[1], args[2]})
+        for (int i = 0; parts != Py_None && i < 2; ++i)
+            if (PyTuple_GET_ITEM(parts, i) != Py_None) written(THPVariable_Unpack(PyTuple_GET_ITEM(parts, i)));
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
@@ -537,6 +567,7 @@ PyObject *fp8_matmul(PyObject *, PyObject *const *args, Py_ssize_t n) {
                          b.s, b.ld_scales, int(b.block_rows), a.rows, b.rows, a.cols,
                          out.data_ptr(), float_type(out.scalar_type(), "out"), ld_out,
                          accumulate ? 1 : 0, stream_of(device)));
+    if (args[2] != Py_None) written(out);
     return THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
 }
