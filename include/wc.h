@@ -363,9 +363,9 @@ WC_API int wc_sr_accumulate_bf16(uint16_t *dst, uint16_t *src, int64_t n,
  *          the output's type)
  * The sum of squares is as exact as in fp64, in a fixed order (the same bits
  * every run), and does not overflow or vanish for finite values.  A norm that
- * is infinite gives coef 0, one that is not a number gives coef NaN, and the
- * values follow by the same product (0 * inf is NaN): look at stats before the
- * update.
+ * is infinite gives coef 0 (for an infinite max_norm too), one that is not a
+ * number gives coef NaN, norm + eps = 0 gives coef 1, and the values follow by
+ * the same product (0 * inf is NaN): look at stats before the update.
  * spans, dst : HOST arrays of count tensors; only the addresses in them are
  *              device memory, aligned to their element (2 or 4 bytes; any
  *              offset into a flat buffer will do).  The arrays may be freed

@@ -244,9 +244,11 @@ __device__ __forceinline__ NormCoef finish(const double *partials, int count, do
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
         if (threadIdx.x == 0) {
-            const double norm = sqrt(v), q = max_norm / (norm + eps);
+            const double norm = sqrt(v), bound = norm + eps;
             shared->norm = float(norm);
-            shared->coef = q >= 1.0 ? 1.0f : float(q);  // not a number stays not a number
+            // (the first two also where the quotient would be inf / inf or 0 / 0; a norm
+            // that is not a number stays one)
+            shared->coef = norm == HUGE_VAL ? 0.0f : bound <= max_norm ? 1.0f : float(max_norm / bound);
         }
     }
     __syncthreads();
