@@ -4,8 +4,13 @@
 //   C[m][n] = sum over blocks kb of
 //             sa[m][kb] * sb[n][kb] * (sum over the block's 128 k of a[m][k] * b[n][k])
 //
-// The scales are any fp32 values, so a block's sum has to leave the tensor
-// core before it is scaled.  One block is one step of the pipeline: TMA
+// The scales are fp32 and not powers of two, so a block's sum has to leave the
+// tensor core before it is scaled.  It is scaled by the two scales' product, taken
+// in fp32: one operation per sum where a side has one scale per 128 rows.  The
+// product of any two blocks' scales should be a normal number (the largest
+// magnitudes of the blocks, multiplied, between 2.4e-33 and 6.8e43); a subnormal
+// one costs up to 2^-125 per block, one that overflows makes the output infinite
+// or not a number, even where the block's sum is 0.  One block is one step of the pipeline: TMA
 // brings 128 bytes of 128 rows of one operand and of NT rows of the other
 // (128-byte swizzle, zero fill at every edge), four tcgen05.mma of K = 32 put
 // the block's sum into a TMEM buffer, and the epilogue warps read that buffer
