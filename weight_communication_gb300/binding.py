@@ -1,6 +1,7 @@
 """ctypes binding of libwc.so (include/wc.h): argument marshalling only.
-(`calls` has the composed calls of the training-step operators, which reach
-the library without ctypes.)
+(`calls` has the calls of the training-step operators, which reach the library
+without ctypes; here are two of them for buffers that the caller lays out,
+`embedding_grad` and `fp8_quant`.)
 
 Every function takes torch CUDA tensors, checks dtype, device, contiguity and
 sizes, and calls the entry point of the same name on the tensors' current
@@ -203,16 +204,6 @@ def _stream(t: torch.Tensor, stream: torch.cuda.Stream | None):
     if stream.device != t.device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
     return ctypes.c_void_p(stream.cuda_stream)
-
-
-def _raw_stream(device: torch.device, stream: torch.cuda.Stream | None) -> int:
-    """_stream as an integer, by the shortest way: the training-step calls are
-    made many times per step."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    return stream.cuda_stream
 
 
 def _dev(t: torch.Tensor | None, name: str, dtype: torch.dtype, numel: int, device=None):
@@ -428,11 +419,6 @@ def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.data_ptr(), _rows_of(t, name, rows, cols)
-
-
-def _rows_of(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
-    """The checks of _matrix that don't depend on the device; the row stride."""
     shape = t.shape
     if len(shape) != 2 or shape[0] != rows or shape[1] < cols:
         raise ValueError(f"{name} has shape {tuple(shape)}, expected ({rows}, {cols})")
@@ -443,50 +429,7 @@ def _rows_of(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
         ld = shape[1]
     elif ld < shape[1]:
         raise ValueError(f"{name} must not have overlapping rows")
-    return ld
-
-
-def spans(tensors, name: str = "tensors"):
-    """The wc_span array of a list of dense CUDA tensors on one GPU, with that
-    GPU (None for an empty list).  It holds addresses: keep the tensors."""
-    arr = (WcSpan * max(1, len(tensors)))()
-    device = None
-    for i, t in enumerate(tensors):
-        if not t.is_cuda:
-            raise ValueError(f"{name}[{i}] must be a CUDA tensor")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name}[{i}] is on {t.device}, expected {device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be contiguous")
-        arr[i] = WcSpan(t.data_ptr() if t.numel() else None, t.numel(),
-                        _float_type(t, f"{name}[{i}]"), 0)
-    return arr, device
-
-
-def grad_norm_workspace(count: int) -> int:
-    """wc_grad_norm_workspace: bytes for a list of count tensors."""
-    return load().wc_grad_norm_workspace(count)
-
-
-def grad_norm(span_array, count: int, stats: torch.Tensor, workspace: torch.Tensor,
-              stream=None) -> None:
-    """wc_grad_norm: stats fp32 [1] <- the norm of the tensors in span_array
-    (see spans); workspace uint8."""
-    d = stats.device
-    _call(d, "wc_grad_norm", span_array, count, _dev(stats, "stats", torch.float32, 1, d),
-          *_workspace(workspace, d), _raw_stream(d, stream))
-
-
-def grad_clip(span_array, dst_array, count: int, max_norm: float, eps: float,
-              stats: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
-    """wc_grad_clip: stats fp32 [2] <- norm and coefficient; the scaled values
-    go to dst_array's tensors, or in place if that is None."""
-    d = stats.device
-    _call(d, "wc_grad_clip", span_array, dst_array, count, max_norm, eps,
-          _dev(stats, "stats", torch.float32, 2, d),
-          *_workspace(workspace, d), _raw_stream(d, stream))
+    return t.data_ptr(), ld
 
 
 def _ids(ids: torch.Tensor, device) -> tuple:
@@ -509,33 +452,6 @@ def _workspace(t: torch.Tensor, device) -> tuple:
     return t.data_ptr(), t.numel()
 
 
-def embedding(table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, scale: float = 1.0,
-              first_row: int = 0, stream=None) -> None:
-    """wc_embedding: out [n, D] <- scale * table[ids - first_row], zero for
-    ids outside the table's rows [first_row, first_row + V)."""
-    d = table.device
-    if table.dim() != 2:
-        raise ValueError(f"table must be a matrix, got shape {tuple(table.shape)}")
-    V, D = table.shape
-    tp, ld_table = _matrix(table, "table", V, D, d)
-    ip, it = _ids(ids, d)
-    if out.dtype != table.dtype:
-        raise TypeError(f"out must be {table.dtype}, got {out.dtype}")
-    n = ids.numel()
-    op, ld_out = _matrix(out, "out", n, D, d)
-    _call(d, "wc_embedding", tp, _float_type(table, "table"), ld_table, ip, it, n, first_row, V,
-          D, scale, op, ld_out, _raw_stream(d, stream))
-
-
-def embedding_grad_workspace(n: int, V: int, D: int) -> int:
-    """wc_embedding_grad_workspace: bytes."""
-    lib = load()
-    rc = lib.wc_embedding_grad_workspace(n, V, D)
-    if rc < 0:
-        raise WcError("wc_embedding_grad_workspace", rc, lib.wc_last_error().decode())
-    return rc
-
-
 def embedding_grad(dy: torch.Tensor, ids: torch.Tensor, dtable: torch.Tensor,
                    workspace: torch.Tensor, scale: float = 1.0, first_row: int = 0,
                    accumulate: bool = False, stream=None) -> None:
@@ -553,14 +469,13 @@ def embedding_grad(dy: torch.Tensor, ids: torch.Tensor, dtable: torch.Tensor,
     op, ld_out = _matrix(dtable, "dtable", V, D, d)
     _call(d, "wc_embedding_grad", yp, _float_type(dy, "dy"), ld_dy, ip, it, n, first_row, V, D,
           scale, 1 if accumulate else 0, op, _float_type(dtable, "dtable"), ld_out,
-          *_workspace(workspace, d), _raw_stream(d, stream))
+          *_workspace(workspace, d), _stream(dy, stream))
 
 
-def _fp8_part(codes, scales, name: str, rows: int, cols: int, square: bool, device,
-              written: bool):
-    """Pointers and strides of codes [rows, >= cols] and scales
-    [ceil(cols/128), >= rows or ceil(rows/128)], or NULLs.  Written codes need
-    room for their rows' padding to 16 bytes."""
+def _fp8_part(codes, scales, name: str, rows: int, cols: int, square: bool, device):
+    """Pointers and strides of codes [rows, >= cols], with room for their rows'
+    padding to 16 bytes, and scales [ceil(cols/128), >= rows or ceil(rows/128)],
+    or NULLs."""
     if (codes is None) != (scales is None):
         raise ValueError(f"{name}: codes and scales must both be given or both be None")
     if codes is None:
@@ -571,7 +486,7 @@ def _fp8_part(codes, scales, name: str, rows: int, cols: int, square: bool, devi
         raise TypeError(f"{name} scales must be float32, got {scales.dtype}")
     per = -(-rows // 128) if square else rows
     padded = -(-cols // 16) * 16
-    cp, ld = _matrix(codes, f"{name} codes", rows, padded if written else cols, device)
+    cp, ld = _matrix(codes, f"{name} codes", rows, padded, device)
     if rows <= 1 or codes.shape[1] == 0:
         ld = padded  # there is no second row to be apart from
     sp, lds = _matrix(scales, f"{name} scales", -(-cols // 128), per, device)
@@ -589,22 +504,7 @@ def fp8_quant(x: torch.Tensor, codes: torch.Tensor | None, scales: torch.Tensor 
     d = x.device
     rows, cols = x.shape
     xp, ld = _matrix(x, "x", rows, cols, d)
-    q, ldq, s, lds = _fp8_part(codes, scales, "row", rows, cols, square, d, True)
-    qt, ldqt, st, ldst = _fp8_part(codes_t, scales_t, "transposed", cols, rows, square, d, True)
+    q, ldq, s, lds = _fp8_part(codes, scales, "row", rows, cols, square, d)
+    qt, ldqt, st, ldst = _fp8_part(codes_t, scales_t, "transposed", cols, rows, square, d)
     _call(d, "wc_fp8_quant", xp, _float_type(x, "x"), rows, cols, ld, 1 if square else 0,
-          q, ldq, s, lds, qt, ldqt, st, ldst, _raw_stream(d, stream))
-
-
-def fp8_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, a_rows_per_scale: int,
-               b_codes: torch.Tensor, b_scales: torch.Tensor, b_rows_per_scale: int, K: int,
-               out: torch.Tensor, accumulate: bool = False, stream=None) -> None:
-    """wc_fp8_matmul: out [M, N] <- (or +=) A B^T of two quantized operands
-    with K columns each."""
-    d = a_codes.device
-    M, N = a_codes.shape[0], b_codes.shape[0]
-    ap, lda, sap, ldsa = _fp8_part(a_codes, a_scales, "a", M, K, a_rows_per_scale == 128, d, False)
-    bp, ldb, sbp, ldsb = _fp8_part(b_codes, b_scales, "b", N, K, b_rows_per_scale == 128, d, False)
-    op, ld_out = _matrix(out, "out", M, N, d)
-    _call(d, "wc_fp8_matmul", ap, lda, sap, ldsa, a_rows_per_scale, bp, ldb, sbp, ldsb,
-          b_rows_per_scale, M, N, K, op, _float_type(out, "out"), ld_out,
-          1 if accumulate else 0, _raw_stream(d, stream))
+          q, ldq, s, lds, qt, ldqt, st, ldst, _stream(x, stream))
