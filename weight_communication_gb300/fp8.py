@@ -147,6 +147,8 @@ class Fp8Linear:
             raise ValueError("backward needs Fp8Linear(training=True)")
         if dy.dim() != 2 or tuple(dy.shape) != (saved.cols, self.N):
             raise ValueError(f"dy has shape {tuple(dy.shape)}, expected ({saved.cols}, {self.N})")
+        if saved.rows != self.K:
+            raise ValueError(f"saved is of {saved.rows} columns, the layer has {self.K}: another layer's?")
         q, qt = quantize(dy, columns=True, stream=stream)
         dx = matmul(q, self.wt, out_dtype=dx_dtype, stream=stream)
         dw = matmul(qt, saved, out=dw, out_dtype=dw_dtype, accumulate=accumulate, stream=stream)
