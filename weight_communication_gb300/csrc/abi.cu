@@ -647,7 +647,7 @@ WC_API int wc_fp8_matmul(const uint8_t *a, int64_t lda, const float *sa, int64_t
         return fail(WC_EINVAL, "%s: M = %lld, N = %lld, K = %lld must not be negative", fn, (long long)M,
                     (long long)N, (long long)K);
     const int64_t limit = int64_t(1) << 31;
-    // (2^31 - 128: the tiles' coordinates are 32-bit and go up to the next 256)
+    // (2^31 - 256: the tiles' coordinates are 32-bit and go up to the next 256)
     if (M > limit - 256 || N > limit - 256 || K > limit - 256)
         return fail(WC_ERANGE, "%s: M, N or K exceeds 2^31 - 256", fn);
     if (N > 0 && M >= (int64_t(1) << 44) / N) return fail(WC_ERANGE, "%s: M * N reaches 2^44", fn);

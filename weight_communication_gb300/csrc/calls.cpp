@@ -6,8 +6,8 @@
 // GPU.  These calls are made many times per step on small tensors, where the
 // host is what takes the time.  Host time on the GB300's Grace, against the
 // same steps in Python through ctypes: one-token 8-bit layer (two calls) 24 ->
-// 11 us, where its kernels take 9.6; layer forward and backward (six) 75 -> 36;
-// embedding lookup 11.3 -> 4.5, gradient 20 -> 9; clipping 21 -> 14.
+// 9 us, where its kernels take 6.8; layer forward and backward (six) 75 -> 31;
+// embedding lookup 11.3 -> 4.0, gradient 20 -> 7.3; clipping 21 -> 12.
 //
 // The entry points reach this module as addresses (setup()), so it works with
 // whichever build of libwc.so the process has loaded.

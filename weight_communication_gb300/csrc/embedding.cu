@@ -21,11 +21,14 @@
 // writes the rows that lie inside its run and leaves fp32 partial sums of the
 // at most two rows that cross its ends.  (3) join: adds those partial sums in
 // order.  Bound: HBM, reading dy once and writing the table's gradient once:
-// 16384 tokens into 32000 x 2048 bf16 take 44.8 us (197 MB, 4.4 TB/s), of which
+// 16384 tokens into 32000 x 2048 bf16 take 45.5 us (197 MB, 4.3 TB/s), of which
 // the sort waits on latencies for about 8 and the zero rows are written in the
 // next 16.  (Zeros for every row at the start of the sort: 52.5 us, its reads
 // queue behind them.)  Few tokens are bound by latencies: 3001 x 1002 into
-// 50021 fp32 rows 14.5 us.
+// 50021 fp32 rows 14.6 us.  Every CTA of the sort reads every id, twice beyond 8192
+// tokens, so tokens x max(152, rows / 1024) ids come from L2: little at these
+// sizes, most of the time with many of both (64 columns added to fp32 rows, 2^20
+// tokens: 0.37 ms into 2^15 rows, 0.65 into 2^18, 2.0 into 2^20).
 #include "wc_device.cuh"
 #include "wc_internal.h"
 #include "wc_launch.cuh"

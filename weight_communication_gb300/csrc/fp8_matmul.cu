@@ -34,7 +34,7 @@
 // 8192 x 11008 x 4096 (weights, one scale per 128 x 128): 0.28 ms, 2.6 PFLOP/s.
 // A scale per row on both sides (a weight's gradient) is bound by the fp32 units,
 // which have two operations per sum and block there: 5504 x 2048 x 4096 into fp32
-// 72 us, 48 with one scale per 128 x 128 on one side.
+// 79 us, 52 with one scale per 128 x 128 on one side.
 #include <cuda.h>
 
 #include <atomic>
@@ -421,8 +421,8 @@ __device__ __forceinline__ void store_pass_bf16(const Args &a, char *base, const
 }
 
 // 32 rows x 16 columns of staged fp32 sums, stored or added to what out holds
-// (added with several reads of out in flight: 8192 x 11008 x 4096 into fp32 455 us
-// with one scale per 128 x 128, 580 with one per row; one by one 1890 and 1420).
+// (added with several reads of out in flight: 8192 x 11008 x 4096 into fp32 438 us
+// with one scale per 128 x 128, 584 with one per row; one by one 1890 and 1420).
 template <bool ADD, typename T>
 __device__ __forceinline__ void store_pass_f32(const Args &a, T *base, const uint8_t *staging, int rows,
                                                int cols, int lane) {
@@ -1087,7 +1087,7 @@ int clusters_of(Kernel kernel, int threads, int smem, int device, int size) {
 // CTAs that share a tile's blocks of K: as many as run at once, three blocks or
 // more each, and none where that saves less than adding the sums costs (a block
 // takes 0.3 us; the exchange 2.5 us for 128 x 128 sums, 1 us for fewer columns).
-// One token, 4096 x 11008: 28.9 -> 10.6 us; 128 x 1003 x 11008: 32.9 -> 10.3;
+// One token, 4096 x 11008: 28.9 -> 10.8 us; 128 x 1003 x 11008: 32.9 -> 10.3;
 // 5 blocks on 63 tiles of 128 x 128 would take 8.7 us instead of 7.4.
 template <typename Kernel>
 int32_t split_of(Kernel kernel, int threads, int smem, int device, int64_t tiles, int32_t blocks,
@@ -1165,7 +1165,7 @@ cudaError_t launch_fp8_matmul(const Fp8Matmul &m, cudaStream_t stream) {
     if (m.M <= 64) return run<64, true>(m, m.b, m.a, m.N, m.M, stream);
     // a block takes a CTA of 128 x 128 as long as a pair of 256 x 256, so the small
     // tiles serve where one wave of them is enough (4411 x 638 x 9433: 175 small
-    // tiles in two waves 55 us, 54 large ones 29)
+    // tiles in two waves 55 us, 54 large ones 34)
     const int64_t small = ((m.M + 127) / 128) * ((m.N + 127) / 128);
     if (small <= kSms) return run<128, false>(m, m.a, m.b, m.M, m.N, stream);
     if (m.accumulate) return run<256, false, kAdded>(m, m.a, m.b, m.M, m.N, stream);

@@ -17,10 +17,10 @@
 // Range: x^2 leaves binary32 for |x| beyond 2^64 or below 2^-63.  A thread
 // sums 32 values at a time in fp32; where that sum is outside
 // [2^-90, 2^100) it is taken again in fp64 from the values it still holds, so
-// any finite gradient has a finite norm and tiny ones do not vanish.  Tile
-// sums are added with their rounding errors kept (TwoSum, Knuth), which makes
-// the result as good as an fp64 sum at the cost of fp32 adds: GB300 does two
-// fp64 fmas per clock and SM.
+// any finite gradient has a finite norm and tiny ones do not vanish.  These
+// sums (7 roundings each) are added with their rounding errors kept (TwoSum,
+// Knuth), as well as in fp64 and at the cost of fp32 adds: GB300 does two fp64
+// fmas per clock and SM.
 //
 // Bound: HBM.  The norm reads each value once (875 M bf16 values: 0.252 ms in
 // all, 6.9 TB/s); clipping has to read it again, and walks the tiles backwards

@@ -20,7 +20,7 @@ from . import binding
 def lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, first_row: int = 0,
            out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """[*ids.shape, D] of the table's type (float32 or bfloat16); ids int32 or
-    int64 of any shape.  `out`: a matrix [ids.numel(), D] to write instead of a
+    int64, contiguous, of any shape.  `out`: a matrix [ids.numel(), D] to write instead of a
     new tensor (its rows may be further apart than D)."""
     return binding.on_stream(stream, table.device, binding.calls().embedding, table, ids, scale,
                              first_row, out)

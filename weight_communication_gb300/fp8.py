@@ -12,6 +12,9 @@ and `Fp8Linear` composes them into a layer's forward and backward pass:
     dx, dw = lin.backward(dy, saved)           # dy W, dy^T x (fp32)
     lin.load(weight)                           # after an update of the weights
 
+Activations and gradients are matrices [tokens, values], their first value on 16
+bytes: a batch [.., tokens, values] goes in as x.view(-1, values).
+
 A product scales each block's sum by the product of the two blocks' scales, in
 fp32.  That should be a normal number: the largest magnitudes of any two blocks
 that meet, multiplied, between 2.4e-33 and 6.8e43.  Below, up to 2^-125 per block
