@@ -474,7 +474,134 @@ WC_API int wc_fp8_matmul(const uint8_t *a, int64_t lda, const float *sa, int64_t
                          void *out, int out_dtype, int64_t ld_out, int accumulate, void *stream);
 
 /*
- * wc_wait_timeouts -- a debugging aid: waits inside wc_fp8_matmul's kernels
+ * wc_fp8_dequant -- a matrix in 8 bits back to its values:
+ *   out[r][c] = code[r][c] * scale   (fp32, rounded once to out's type)
+ * q, s : codes [rows][ld_q] and scales [ceil(cols/128)][ld_s], one per row
+ *        (rows_per_scale 1) or per 128 rows (128), as wc_fp8_quant writes them.
+ * out  : [rows][ld_out] of out_dtype; rows may start on any value.
+ * Requires rows, cols <= 8388480, rows * cols < 2^40, ld_q a multiple of 16 and at
+ * least cols, ld_out >= cols, ld_s that holds a block's scales.
+ */
+WC_API int wc_fp8_dequant(const uint8_t *q, int64_t ld_q, const float *s, int64_t ld_s,
+                          int rows_per_scale, int64_t rows, int64_t cols, void *out, int out_dtype,
+                          int64_t ld_out, void *stream);
+
+/*
+ * A matrix kept in 8 bits from the forward to the backward pass: codes
+ * [rows][ld_codes] and scales [ceil(cols/128)][ld_scales] by the rule of
+ * wc_fp8_quant, one scale per 128 values of a row.  ld_codes is a multiple of 16
+ * and at least cols, ld_scales at least rows; both start on 16 bytes.  Codes
+ * between a row's end and the next multiple of 16 are written as 0.
+ */
+typedef struct {
+    uint8_t *codes;
+    int64_t ld_codes;
+    float *scales;
+    int64_t ld_scales;
+} wc_kept;
+
+/*
+ * wc_activation, wc_activation_grad -- a layer's activation, gated or not, whose
+ * inputs are kept in 8 bits for the backward pass.
+ *   h = act(gate) * up  (act(gate) where up is NULL), rounded once to the type
+ *   dgate = dh * up^ * act'(gate^),  dup = dh * act(gate^)
+ * in fp32, where ^ is what the kept codes stand for.  act by `kind`:
+ *   WC_RELU  max(a, 0)
+ *   WC_SILU  a / (1 + exp(-a))
+ *   WC_GELU  0.5 a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3)))
+ * gate, up, h : [rows][ld] of `dtype`; dh, dgate, dup the same of their `dtype`,
+ *               which need not be the forward pass's.  Rows may start on any value.
+ *               h may be gate or up, dgate or dup may be dh (the same rows); otherwise
+ *               what is written overlaps nothing.
+ * kept_gate, kept_up : HOST structs; NULL where nothing is kept (forward) or there
+ *               is no gate (both); kept_up if and only if up (dup) and kept_gate are.
+ * A block of 128 with a value that is not finite makes its gradients NaN.
+ * Requires rows, cols <= 8388480, rows * cols < 2^40, every ld >= cols.
+ */
+#define WC_RELU 0
+#define WC_SILU 1
+#define WC_GELU 2
+WC_API int wc_activation(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int dtype,
+                         int kind, int64_t rows, int64_t cols, void *h, int64_t ld_h,
+                         const wc_kept *kept_gate, const wc_kept *kept_up, void *stream);
+WC_API int wc_activation_grad(const void *dh, int64_t ld_dh, int dtype, int kind, int64_t rows,
+                              int64_t cols, const wc_kept *kept_gate, const wc_kept *kept_up,
+                              void *dgate, int64_t ld_dgate, void *dup, int64_t ld_dup, void *stream);
+
+/*
+ * wc_rms_norm, wc_rms_norm_grad -- root-mean-square norm of a residual stream,
+ * whose input is kept in 8 bits for the backward pass.
+ *   t = x + add, rounded to the type and written to total  (t = x where add is NULL)
+ *   r = 1 / sqrt(mean of t^2 + eps),  y = t * r * weight
+ *   n = t^ * r, where t^ is what the kept codes stand for
+ *   dx = r * (dy * weight - n * mean of (dy * weight * n)) + add,  the gradient of
+ *        x and of the forward pass's add (add here: what reaches t past the norm)
+ *   dweight = sum over the rows of dy * n   (accumulate != 0: added to its values)
+ * Sums in fp32 in an order that the sizes fix (the same bits every run).
+ * x, add, total, y : [rows][ld] of `dtype`; dy, add, dx the same of their `dtype`.
+ *              Rows may start on any value.  total and y may be x or add, dx may be
+ *              dy or add (the same rows); otherwise what is written overlaps nothing.
+ * weight     : [cols] of weight_dtype.  dweight : [cols] of dweight_dtype.
+ * rstd, kept : r of each row (fp32) and t's codes; both given or both NULL (forward).
+ * workspace  : wc_rms_norm_grad_workspace(rows, cols) bytes, no initial value.
+ * Requires rows <= 8388480, 1 <= cols <= 16384, every ld >= cols, eps >= 0 and finite.
+ * The gradient takes two launches.
+ */
+WC_API int wc_rms_norm(const void *x, int64_t ld_x, const void *add, int64_t ld_add, int dtype,
+                       int64_t rows, int64_t cols, const void *weight, int weight_dtype, double eps,
+                       void *y, int64_t ld_y, void *total, int64_t ld_total, float *rstd,
+                       const wc_kept *kept, void *stream);
+WC_API int64_t wc_rms_norm_grad_workspace(int64_t rows, int64_t cols);
+WC_API int wc_rms_norm_grad(const void *dy, int64_t ld_dy, const void *add, int64_t ld_add, int dtype,
+                            int64_t rows, int64_t cols, const void *weight, int weight_dtype,
+                            const float *rstd, const wc_kept *kept, void *dx, int64_t ld_dx,
+                            void *dweight, int dweight_dtype, int accumulate, void *workspace,
+                            int64_t workspace_bytes, void *stream);
+
+/*
+ * wc_cross_entropy, wc_cross_entropy_grad -- softmax cross entropy of a linear
+ * output layer over a vocabulary, in pieces of the vocabulary, without keeping
+ * the logits s = x w^T:
+ *   lse[t] = log sum over v of exp(s[t][v]),  loss[t] = lse[t] - s[t][targets[t]]
+ *   d[t][v] = g[t] * (exp(s[t][v] - lse[t]) - [v = targets[t]])
+ *   dx = d w,  dw = d^T x   (accumulate != 0: dw is added to its values)
+ * A target outside [0, V) is padding: its loss is 0, and nothing in its row of x
+ * reaches a gradient.  Products of bf16 values in fp32; d is rounded to bf16 for the
+ * products with w and x, so a gradient is a sum of terms that are each within
+ * 2^-8 of their value.  The order of the sums depends on the sizes alone (the same
+ * bits every run).
+ * x, w     : bf16 [T][ld_x] and [V][ld_w].  Rows may start on any value; those that
+ *            do not start on 16 bytes (address and stride) are first copied.
+ * targets  : [T] of id_type (WC_I32 or WC_I64).
+ * losses, lse : fp32 [T]; forward: either may be NULL.  backward: lse of the forward
+ *            pass.
+ * g[t]     : dlosses[t] (fp32), or dloss for every token where dlosses is NULL.
+ * dx, dw   : [T][ld_dx] and [V][ld_dw] of their types, rows that start on any value;
+ *            either may be NULL (the matrix products for it are then not done).
+ * workspace : the *_workspace() bytes for the same arguments, no initial value.  Of
+ *            the backward pass: d for a piece of the vocabulary (256 MB, or as much as
+ *            4 T D if that is more) and, if the pieces are several, dx in fp32.
+ * Requires T, V <= 2^31 - 4096, V and D >= 1, D <= 2^22, T * V < 2^44, T * D and
+ * V * D < 2^40, every ld >= D.
+ */
+WC_API int64_t wc_cross_entropy_workspace(const uint16_t *x, int64_t ld_x, const uint16_t *w,
+                                          int64_t ld_w, int64_t T, int64_t V, int64_t D);
+WC_API int wc_cross_entropy(const uint16_t *x, int64_t ld_x, const uint16_t *w, int64_t ld_w,
+                            const void *targets, int id_type, int64_t T, int64_t V, int64_t D,
+                            float *losses, float *lse, void *workspace, int64_t workspace_bytes,
+                            void *stream);
+WC_API int64_t wc_cross_entropy_grad_workspace(const uint16_t *x, int64_t ld_x, const uint16_t *w,
+                                               int64_t ld_w, int64_t T, int64_t V, int64_t D);
+WC_API int wc_cross_entropy_grad(const uint16_t *x, int64_t ld_x, const uint16_t *w, int64_t ld_w,
+                                 const void *targets, int id_type, int64_t T, int64_t V, int64_t D,
+                                 const float *lse, const float *dlosses, double dloss, void *dx,
+                                 int dx_dtype, int64_t ld_dx, void *dw, int dw_dtype, int64_t ld_dw,
+                                 int accumulate, void *workspace, int64_t workspace_bytes,
+                                 void *stream);
+
+/*
+ * wc_wait_timeouts -- a debugging aid: waits inside wc_fp8_matmul's and the cross
+ * entropy's kernels
  * that were given up after about two seconds of running, since the library was
  * loaded or last reset (reset != 0).  0 in every run whose launches were
  * complete; a launch that counted here has left NaN in every output that misses

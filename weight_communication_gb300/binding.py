@@ -24,6 +24,7 @@ from . import build as _build
 WC_OK, WC_EINVAL, WC_EALIGN, WC_ERANGE, WC_ECUDA = 0, -1, -2, -3, -4
 WC_F32, WC_BF16 = 0, 1
 WC_I32, WC_I64 = 0, 1
+WC_RELU, WC_SILU, WC_GELU = 0, 1, 2
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -39,7 +40,14 @@ class WcSpan(ctypes.Structure):
                 ("pad", ctypes.c_int32)]
 
 
+class WcKept(ctypes.Structure):
+    """wc_kept: a matrix in 8 bits."""
+    _fields_ = [("codes", ctypes.c_void_p), ("ld_codes", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("ld_scales", ctypes.c_int64)]
+
+
 _SPANS = ctypes.POINTER(WcSpan)
+_KEPT = ctypes.POINTER(WcKept)
 
 # name -> argtypes (all return int except those in RESTYPES)
 SIGNATURES = {
@@ -70,13 +78,27 @@ SIGNATURES = {
     "wc_fp8_quant": [_P, _I, _I64, _I64, _I64, _I, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P],
     "wc_fp8_matmul": [_P, _I64, _P, _I64, _I, _P, _I64, _P, _I64, _I, _I64, _I64, _I64, _P, _I,
                       _I64, _I, _P],
+    "wc_fp8_dequant": [_P, _I64, _P, _I64, _I, _I64, _I64, _P, _I, _I64, _P],
+    "wc_activation": [_P, _I64, _P, _I64, _I, _I, _I64, _I64, _P, _I64, _KEPT, _KEPT, _P],
+    "wc_activation_grad": [_P, _I64, _I, _I, _I64, _I64, _KEPT, _KEPT, _P, _I64, _P, _I64, _P],
+    "wc_rms_norm": [_P, _I64, _P, _I64, _I, _I64, _I64, _P, _I, _D, _P, _I64, _P, _I64, _P, _KEPT,
+                    _P],
+    "wc_rms_norm_grad_workspace": [_I64, _I64],
+    "wc_rms_norm_grad": [_P, _I64, _P, _I64, _I, _I64, _I64, _P, _I, _P, _KEPT, _P, _I64, _P, _I,
+                         _I, _P, _I64, _P],
+    "wc_cross_entropy_workspace": [_P, _I64, _P, _I64, _I64, _I64, _I64],
+    "wc_cross_entropy": [_P, _I64, _P, _I64, _P, _I, _I64, _I64, _I64, _P, _P, _P, _I64, _P],
+    "wc_cross_entropy_grad_workspace": [_P, _I64, _P, _I64, _I64, _I64, _I64],
+    "wc_cross_entropy_grad": [_P, _I64, _P, _I64, _P, _I, _I64, _I64, _I64, _P, _P, _D, _P, _I,
+                              _I64, _P, _I, _I64, _I, _P, _I64, _P],
     "wc_wait_timeouts": [_I],
     "wc_checked_violations": [_I],
     "wc_last_error": [],
     "wc_version": [],
 }
 RESTYPES = {"wc_last_error": ctypes.c_char_p, "wc_grad_norm_workspace": _I64,
-            "wc_embedding_grad_workspace": _I64}
+            "wc_embedding_grad_workspace": _I64, "wc_rms_norm_grad_workspace": _I64,
+            "wc_cross_entropy_workspace": _I64, "wc_cross_entropy_grad_workspace": _I64}
 
 
 class WcError(RuntimeError):
@@ -174,7 +196,7 @@ def checked_violations(reset: bool = False, probe: bool = False) -> int:
 
 
 def wait_timeouts(reset: bool = False) -> int:
-    """wc_wait_timeouts: waits of the product's kernels that were given up
+    """wc_wait_timeouts: waits of the matrix products' kernels that were given up
     (synchronize first); 0 unless a launch went wrong."""
     lib = load()
     rc = lib.wc_wait_timeouts(1 if reset else 0)

@@ -1,6 +1,7 @@
 // abi.cu -- the extern "C" entry points declared in include/wc.h: argument
 // validation on the host, then one kernel launch per call (the gradient norm,
-// clipping and the embedding's gradient: two or three, back to back).
+// clipping, the gradients of embedding and norm: two or three, back to back; the
+// cross entropy: two or three per piece of its work).
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -497,6 +498,107 @@ int ids_pointer(const char *fn, const void *ids, int id_type) {
 
 int64_t blocks128(int64_t n) { return (n + 127) / 128; }
 
+// Rows of values may start on any value.
+int values_pointer(const char *fn, const char *name, const void *p, int dtype) {
+    const uintptr_t size = dtype == WC_BF16 ? 2 : 4;
+    if (p == nullptr) return fail(WC_EINVAL, "%s: %s is NULL", fn, name);
+    if (reinterpret_cast<uintptr_t>(p) % size)
+        return fail(WC_EALIGN, "%s: %s is not aligned to its %d-byte values", fn, name, int(size));
+    return WC_OK;
+}
+
+int row_pitch(const char *fn, const char *name, int64_t ld, int64_t cols) {
+    if (ld < cols)
+        return fail(WC_EINVAL, "%s: ld_%s = %lld is below %lld columns", fn, name, (long long)ld, (long long)cols);
+    if (ld >= (int64_t(1) << 40)) return fail(WC_ERANGE, "%s: ld_%s reaches 2^40", fn, name);
+    return WC_OK;
+}
+
+int block_sizes(const char *fn, int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0)
+        return fail(WC_EINVAL, "%s: rows = %lld, cols = %lld must not be negative", fn, (long long)rows, (long long)cols);
+    if (rows > 65535 * 128 || cols > 65535 * 128)
+        return fail(WC_ERANGE, "%s: rows or cols exceeds 8388480", fn);
+    if (cols > 0 && rows >= (int64_t(1) << 40) / cols) return fail(WC_ERANGE, "%s: rows * cols reaches 2^40", fn);
+    return WC_OK;
+}
+
+int activation_kind(const char *fn, int dtype, int kind) {
+    if (!float_type(dtype)) return fail(WC_EINVAL, "%s: dtype %d is neither WC_F32 nor WC_BF16", fn, dtype);
+    if (kind != WC_RELU && kind != WC_SILU && kind != WC_GELU)
+        return fail(WC_EINVAL, "%s: kind %d is none of WC_RELU, WC_SILU, WC_GELU", fn, kind);
+    return WC_OK;
+}
+
+// `k` as the kernels take it; NULL is an empty one.
+int kept_matrix(const char *fn, const char *name, const wc_kept *k, int64_t rows, int64_t cols, wc::Kept8 *to) {
+    if (k == nullptr) return WC_OK;
+    if (k->codes == nullptr || k->scales == nullptr)
+        return fail(WC_EINVAL, "%s: %s has no codes or no scales", fn, name);
+    if (!aligned16(k->codes) || !aligned16(k->scales))
+        return fail(WC_EALIGN, "%s: codes or scales of %s are not 16-byte aligned", fn, name);
+    if (k->ld_codes % 16 || k->ld_codes < cols)
+        return fail(WC_EINVAL, "%s: ld_codes = %lld of %s must be a multiple of 16 and at least cols", fn,
+                    (long long)k->ld_codes, name);
+    if (k->ld_scales < rows)
+        return fail(WC_EINVAL, "%s: ld_scales = %lld of %s does not hold a block's scales", fn,
+                    (long long)k->ld_scales, name);
+    *to = {k->codes, k->ld_codes, k->scales, k->ld_scales};
+    return WC_OK;
+}
+
+int norm_sizes(const char *fn, int64_t rows, int64_t cols, int dtype, int weight_dtype) {
+    if (!float_type(dtype) || !float_type(weight_dtype))
+        return fail(WC_EINVAL, "%s: dtype %d or weight_dtype %d is neither WC_F32 nor WC_BF16", fn, dtype, weight_dtype);
+    if (rows < 0 || cols < 1)
+        return fail(WC_EINVAL, "%s: rows = %lld must not be negative, cols = %lld must be at least 1", fn,
+                    (long long)rows, (long long)cols);
+    if (rows > 65535 * 128) return fail(WC_ERANGE, "%s: rows exceeds 8388480", fn);
+    if (cols > wc::kNormCols) return fail(WC_ERANGE, "%s: cols exceeds %lld", fn, (long long)wc::kNormCols);
+    return WC_OK;
+}
+
+int cross_entropy_sizes(const char *fn, const uint16_t *x, int64_t ld_x, const uint16_t *w, int64_t ld_w,
+                        int64_t T, int64_t V, int64_t D, wc::CrossEntropy *c) {
+    if (T < 0 || V < 1 || D < 1)
+        return fail(WC_EINVAL, "%s: T = %lld must not be negative, V = %lld and D = %lld must be at least 1", fn,
+                    (long long)T, (long long)V, (long long)D);
+    // (the kernels step past the last token or row in 32 bits)
+    const int64_t limit = (int64_t(1) << 31) - 4096;
+    if (T > limit || V > limit) return fail(WC_ERANGE, "%s: T or V exceeds 2^31 - 4096", fn);
+    if (D > (int64_t(1) << 22)) return fail(WC_ERANGE, "%s: D exceeds 2^22", fn);
+    if (T >= (int64_t(1) << 44) / V) return fail(WC_ERANGE, "%s: T * V reaches 2^44", fn);
+    if (T >= (int64_t(1) << 40) / D || V >= (int64_t(1) << 40) / D)
+        return fail(WC_ERANGE, "%s: T * D or V * D reaches 2^40", fn);
+    int rc = row_pitch(fn, "x", ld_x, D);
+    if (rc == WC_OK) rc = row_pitch(fn, "w", ld_w, D);
+    if (rc != WC_OK) return rc;
+    c->x = x;
+    c->w = w;
+    c->ld_x = ld_x;
+    c->ld_w = ld_w;
+    c->T = T;
+    c->V = V;
+    c->D = D;
+    return WC_OK;
+}
+
+int cross_entropy_inputs(const char *fn, wc::CrossEntropy *c, const void *targets, int id_type) {
+    if (id_type != WC_I32 && id_type != WC_I64)
+        return fail(WC_EINVAL, "%s: id_type %d is neither WC_I32 nor WC_I64", fn, id_type);
+    if (c->T == 0) return WC_OK;
+    int rc = values_pointer(fn, "x", c->x, WC_BF16);
+    if (rc == WC_OK) rc = values_pointer(fn, "w", c->w, WC_BF16);
+    if (rc != WC_OK) return rc;
+    const uintptr_t size = id_type == WC_I64 ? 8 : 4;
+    if (targets == nullptr) return fail(WC_EINVAL, "%s: targets is NULL", fn);
+    if (reinterpret_cast<uintptr_t>(targets) % size)
+        return fail(WC_EALIGN, "%s: targets is not aligned to its %d-byte values", fn, int(size));
+    c->targets = targets;
+    c->wide = id_type == WC_I64;
+    return WC_OK;
+}
+
 }  // namespace
 
 WC_API int64_t wc_grad_norm_workspace(int count) {
@@ -684,12 +786,288 @@ WC_API int wc_fp8_matmul(const uint8_t *a, int64_t lda, const float *sa, int64_t
     return from_cuda(wc::launch_fp8_matmul(m, static_cast<cudaStream_t>(stream)), fn);
 }
 
+WC_API int wc_fp8_dequant(const uint8_t *q, int64_t ld_q, const float *s, int64_t ld_s,
+                          int rows_per_scale, int64_t rows, int64_t cols, void *out, int out_dtype,
+                          int64_t ld_out, void *stream) {
+    static const char *fn = "wc_fp8_dequant";
+    int rc = block_sizes(fn, rows, cols);
+    if (rc != WC_OK) return rc;
+    if (!float_type(out_dtype))
+        return fail(WC_EINVAL, "%s: out_dtype %d is neither WC_F32 nor WC_BF16", fn, out_dtype);
+    if (rows_per_scale != 1 && rows_per_scale != 128)
+        return fail(WC_EINVAL, "%s: rows per scale (%d) must be 1 or 128", fn, rows_per_scale);
+    if (ld_q % 16 || ld_q < cols)
+        return fail(WC_EINVAL, "%s: ld_q = %lld must be a multiple of 16 and at least cols", fn, (long long)ld_q);
+    if (ld_s < (rows_per_scale == 128 ? blocks128(rows) : rows))
+        return fail(WC_EINVAL, "%s: ld_s = %lld does not hold a block's scales", fn, (long long)ld_s);
+    if ((rc = row_pitch(fn, "out", ld_out, cols)) != WC_OK) return rc;
+    if (rows == 0 || cols == 0) return WC_OK;
+    WC_REQUIRE_PTR(fn, q);
+    WC_REQUIRE_PTR(fn, s);
+    if ((rc = values_pointer(fn, "out", out, out_dtype)) != WC_OK) return rc;
+    const wc::Fp8Dequant a = {q, ld_q, s, ld_s, rows_per_scale, rows, cols, out, out_dtype == WC_BF16, ld_out};
+    return from_cuda(wc::launch_fp8_dequant(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+WC_API int wc_activation(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int dtype,
+                         int kind, int64_t rows, int64_t cols, void *h, int64_t ld_h,
+                         const wc_kept *kept_gate, const wc_kept *kept_up, void *stream) {
+    static const char *fn = "wc_activation";
+    int rc = block_sizes(fn, rows, cols);
+    if (rc == WC_OK) rc = activation_kind(fn, dtype, kind);
+    if (rc == WC_OK) rc = row_pitch(fn, "gate", ld_gate, cols);
+    if (rc == WC_OK && up) rc = row_pitch(fn, "up", ld_up, cols);
+    if (rc == WC_OK) rc = row_pitch(fn, "h", ld_h, cols);
+    if (rc != WC_OK) return rc;
+    if (rows == 0 || cols == 0) return WC_OK;
+    if ((kept_up != nullptr) != (up != nullptr && kept_gate != nullptr))
+        return fail(WC_EINVAL, "%s: kept_up must be given if and only if up and kept_gate are", fn);
+    if ((rc = values_pointer(fn, "gate", gate, dtype)) != WC_OK) return rc;
+    if (up && (rc = values_pointer(fn, "up", up, dtype)) != WC_OK) return rc;
+    if ((rc = values_pointer(fn, "h", h, dtype)) != WC_OK) return rc;
+    wc::Activation a = {};
+    if ((rc = kept_matrix(fn, "kept_gate", kept_gate, rows, cols, &a.kept_gate)) != WC_OK) return rc;
+    if ((rc = kept_matrix(fn, "kept_up", kept_up, rows, cols, &a.kept_up)) != WC_OK) return rc;
+    a.gate = gate;
+    a.up = up;
+    a.ld_gate = ld_gate;
+    a.ld_up = ld_up;
+    a.bf16 = dtype == WC_BF16;
+    a.kind = kind;
+    a.rows = rows;
+    a.cols = cols;
+    a.h = h;
+    a.ld_h = ld_h;
+    return from_cuda(wc::launch_activation(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+WC_API int wc_activation_grad(const void *dh, int64_t ld_dh, int dtype, int kind, int64_t rows,
+                              int64_t cols, const wc_kept *kept_gate, const wc_kept *kept_up,
+                              void *dgate, int64_t ld_dgate, void *dup, int64_t ld_dup, void *stream) {
+    static const char *fn = "wc_activation_grad";
+    int rc = block_sizes(fn, rows, cols);
+    if (rc == WC_OK) rc = activation_kind(fn, dtype, kind);
+    if (rc == WC_OK) rc = row_pitch(fn, "dh", ld_dh, cols);
+    if (rc == WC_OK) rc = row_pitch(fn, "dgate", ld_dgate, cols);
+    if (rc == WC_OK && dup) rc = row_pitch(fn, "dup", ld_dup, cols);
+    if (rc != WC_OK) return rc;
+    if (rows == 0 || cols == 0) return WC_OK;
+    if (kept_gate == nullptr) return fail(WC_EINVAL, "%s: kept_gate is NULL", fn);
+    if ((kept_up != nullptr) != (dup != nullptr))
+        return fail(WC_EINVAL, "%s: kept_up must be given if and only if dup is", fn);
+    if ((rc = values_pointer(fn, "dh", dh, dtype)) != WC_OK) return rc;
+    if ((rc = values_pointer(fn, "dgate", dgate, dtype)) != WC_OK) return rc;
+    if (dup && (rc = values_pointer(fn, "dup", dup, dtype)) != WC_OK) return rc;
+    wc::ActivationGrad a = {};
+    if ((rc = kept_matrix(fn, "kept_gate", kept_gate, rows, cols, &a.kept_gate)) != WC_OK) return rc;
+    if ((rc = kept_matrix(fn, "kept_up", kept_up, rows, cols, &a.kept_up)) != WC_OK) return rc;
+    a.dh = dh;
+    a.ld_dh = ld_dh;
+    a.bf16 = dtype == WC_BF16;
+    a.kind = kind;
+    a.rows = rows;
+    a.cols = cols;
+    a.dgate = dgate;
+    a.dup = dup;
+    a.ld_dgate = ld_dgate;
+    a.ld_dup = ld_dup;
+    return from_cuda(wc::launch_activation_grad(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+WC_API int wc_rms_norm(const void *x, int64_t ld_x, const void *add, int64_t ld_add, int dtype,
+                       int64_t rows, int64_t cols, const void *weight, int weight_dtype, double eps,
+                       void *y, int64_t ld_y, void *total, int64_t ld_total, float *rstd,
+                       const wc_kept *kept, void *stream) {
+    static const char *fn = "wc_rms_norm";
+    int rc = norm_sizes(fn, rows, cols, dtype, weight_dtype);
+    if (rc == WC_OK) rc = row_pitch(fn, "x", ld_x, cols);
+    if (rc == WC_OK && add) rc = row_pitch(fn, "add", ld_add, cols);
+    if (rc == WC_OK) rc = row_pitch(fn, "y", ld_y, cols);
+    if (rc == WC_OK && add) rc = row_pitch(fn, "total", ld_total, cols);
+    if (rc != WC_OK) return rc;
+    if (!(eps >= 0.0 && eps < HUGE_VAL)) return fail(WC_EINVAL, "%s: eps = %g must be finite and at least 0", fn, eps);
+    if (rows == 0) return WC_OK;
+    if ((rstd != nullptr) != (kept != nullptr))
+        return fail(WC_EINVAL, "%s: rstd and kept must both be given or both be NULL", fn);
+    if ((total != nullptr) != (add != nullptr))
+        return fail(WC_EINVAL, "%s: total must be given if and only if add is", fn);
+    if ((rc = values_pointer(fn, "x", x, dtype)) != WC_OK) return rc;
+    if (add && (rc = values_pointer(fn, "add", add, dtype)) != WC_OK) return rc;
+    if ((rc = values_pointer(fn, "weight", weight, weight_dtype)) != WC_OK) return rc;
+    if ((rc = values_pointer(fn, "y", y, dtype)) != WC_OK) return rc;
+    if (total && (rc = values_pointer(fn, "total", total, dtype)) != WC_OK) return rc;
+    if (rstd && (rc = values_pointer(fn, "rstd", rstd, WC_F32)) != WC_OK) return rc;
+    wc::RmsNorm a = {};
+    if ((rc = kept_matrix(fn, "kept", kept, rows, cols, &a.kept)) != WC_OK) return rc;
+    a.x = x;
+    a.add = add;
+    a.ld_x = ld_x;
+    a.ld_add = ld_add;
+    a.bf16 = dtype == WC_BF16;
+    a.rows = rows;
+    a.cols = cols;
+    a.weight = weight;
+    a.weight_bf16 = weight_dtype == WC_BF16;
+    a.eps = float(eps);
+    a.y = y;
+    a.total = total;
+    a.ld_y = ld_y;
+    a.ld_total = ld_total;
+    a.rstd = rstd;
+    return from_cuda(wc::launch_rms_norm(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+WC_API int64_t wc_rms_norm_grad_workspace(int64_t rows, int64_t cols) {
+    static const char *fn = "wc_rms_norm_grad_workspace";
+    const int rc = norm_sizes(fn, rows, cols, WC_F32, WC_F32);
+    if (rc != WC_OK) return rc;
+    return rows > 0 ? 4 * wc::rms_norm_grad_partials(rows, cols) : 0;
+}
+
+WC_API int wc_rms_norm_grad(const void *dy, int64_t ld_dy, const void *add, int64_t ld_add, int dtype,
+                            int64_t rows, int64_t cols, const void *weight, int weight_dtype,
+                            const float *rstd, const wc_kept *kept, void *dx, int64_t ld_dx,
+                            void *dweight, int dweight_dtype, int accumulate, void *workspace,
+                            int64_t workspace_bytes, void *stream) {
+    static const char *fn = "wc_rms_norm_grad";
+    int rc = norm_sizes(fn, rows, cols, dtype, weight_dtype);
+    if (rc != WC_OK) return rc;
+    if (!float_type(dweight_dtype))
+        return fail(WC_EINVAL, "%s: dweight_dtype %d is neither WC_F32 nor WC_BF16", fn, dweight_dtype);
+    if ((rc = row_pitch(fn, "dy", ld_dy, cols)) != WC_OK) return rc;
+    if (add && (rc = row_pitch(fn, "add", ld_add, cols)) != WC_OK) return rc;
+    if ((rc = row_pitch(fn, "dx", ld_dx, cols)) != WC_OK) return rc;
+    if ((rc = values_pointer(fn, "dweight", dweight, dweight_dtype)) != WC_OK) return rc;
+    wc::RmsNormGrad a = {};
+    if (rows > 0) {
+        if (kept == nullptr) return fail(WC_EINVAL, "%s: kept is NULL", fn);
+        if ((rc = values_pointer(fn, "dy", dy, dtype)) != WC_OK) return rc;
+        if (add && (rc = values_pointer(fn, "add", add, dtype)) != WC_OK) return rc;
+        if ((rc = values_pointer(fn, "weight", weight, weight_dtype)) != WC_OK) return rc;
+        if ((rc = values_pointer(fn, "rstd", rstd, WC_F32)) != WC_OK) return rc;
+        if ((rc = values_pointer(fn, "dx", dx, dtype)) != WC_OK) return rc;
+        if ((rc = kept_matrix(fn, "kept", kept, rows, cols, &a.kept)) != WC_OK) return rc;
+        WC_REQUIRE_PTR(fn, workspace);
+        const int64_t need = wc_rms_norm_grad_workspace(rows, cols);
+        if (workspace_bytes < need)
+            return fail(WC_EINVAL, "%s: workspace of %lld bytes, %lld are needed", fn, (long long)workspace_bytes,
+                        (long long)need);
+    } else if (accumulate) {
+        return WC_OK;
+    }
+    a.dy = dy;
+    a.add = add;
+    a.ld_dy = ld_dy;
+    a.ld_add = ld_add;
+    a.bf16 = dtype == WC_BF16;
+    a.rows = rows;
+    a.cols = cols;
+    a.weight = weight;
+    a.weight_bf16 = weight_dtype == WC_BF16;
+    a.rstd = rstd;
+    a.dx = dx;
+    a.ld_dx = ld_dx;
+    a.dweight = dweight;
+    a.dweight_bf16 = dweight_dtype == WC_BF16;
+    a.accumulate = accumulate != 0;
+    a.partials = static_cast<float *>(workspace);
+    return from_cuda(wc::launch_rms_norm_grad(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+WC_API int64_t wc_cross_entropy_workspace(const uint16_t *x, int64_t ld_x, const uint16_t *w,
+                                          int64_t ld_w, int64_t T, int64_t V, int64_t D) {
+    wc::CrossEntropy c = {};
+    const int rc = cross_entropy_sizes("wc_cross_entropy_workspace", x, ld_x, w, ld_w, T, V, D, &c);
+    if (rc != WC_OK) return rc;
+    return T > 0 ? wc::cross_entropy_workspace(c) : 0;
+}
+
+WC_API int wc_cross_entropy(const uint16_t *x, int64_t ld_x, const uint16_t *w, int64_t ld_w,
+                            const void *targets, int id_type, int64_t T, int64_t V, int64_t D,
+                            float *losses, float *lse, void *workspace, int64_t workspace_bytes,
+                            void *stream) {
+    static const char *fn = "wc_cross_entropy";
+    wc::CrossEntropy c = {};
+    int rc = cross_entropy_sizes(fn, x, ld_x, w, ld_w, T, V, D, &c);
+    if (rc != WC_OK) return rc;
+    if ((rc = cross_entropy_inputs(fn, &c, targets, id_type)) != WC_OK) return rc;
+    if (T == 0) return WC_OK;
+    if (losses == nullptr && lse == nullptr) return fail(WC_EINVAL, "%s: losses and lse are both NULL", fn);
+    if (losses && (rc = values_pointer(fn, "losses", losses, WC_F32)) != WC_OK) return rc;
+    if (lse && (rc = values_pointer(fn, "lse", lse, WC_F32)) != WC_OK) return rc;
+    WC_REQUIRE_PTR(fn, workspace);
+    const int64_t need = wc::cross_entropy_workspace(c);
+    if (workspace_bytes < need)
+        return fail(WC_EINVAL, "%s: workspace of %lld bytes, %lld are needed", fn, (long long)workspace_bytes,
+                    (long long)need);
+    c.workspace = workspace;
+    c.losses = losses;
+    c.lse = lse;
+    return from_cuda(wc::launch_cross_entropy(c, static_cast<cudaStream_t>(stream)), fn);
+}
+
+WC_API int64_t wc_cross_entropy_grad_workspace(const uint16_t *x, int64_t ld_x, const uint16_t *w,
+                                               int64_t ld_w, int64_t T, int64_t V, int64_t D) {
+    wc::CrossEntropyGrad c = {};
+    const int rc = cross_entropy_sizes("wc_cross_entropy_grad_workspace", x, ld_x, w, ld_w, T, V, D, &c);
+    if (rc != WC_OK) return rc;
+    return T > 0 ? wc::cross_entropy_grad_workspace(c) : 0;
+}
+
+WC_API int wc_cross_entropy_grad(const uint16_t *x, int64_t ld_x, const uint16_t *w, int64_t ld_w,
+                                 const void *targets, int id_type, int64_t T, int64_t V, int64_t D,
+                                 const float *lse, const float *dlosses, double dloss, void *dx,
+                                 int dx_dtype, int64_t ld_dx, void *dw, int dw_dtype, int64_t ld_dw,
+                                 int accumulate, void *workspace, int64_t workspace_bytes,
+                                 void *stream) {
+    static const char *fn = "wc_cross_entropy_grad";
+    wc::CrossEntropyGrad c = {};
+    int rc = cross_entropy_sizes(fn, x, ld_x, w, ld_w, T, V, D, &c);
+    if (rc != WC_OK) return rc;
+    if (dx == nullptr && dw == nullptr) return fail(WC_EINVAL, "%s: dx and dw are both NULL", fn);
+    if ((dx && !float_type(dx_dtype)) || (dw && !float_type(dw_dtype)))
+        return fail(WC_EINVAL, "%s: dx_dtype %d or dw_dtype %d is neither WC_F32 nor WC_BF16", fn, dx_dtype, dw_dtype);
+    if (dx && (rc = row_pitch(fn, "dx", ld_dx, D)) != WC_OK) return rc;
+    if (dw && (rc = row_pitch(fn, "dw", ld_dw, D)) != WC_OK) return rc;
+    if ((rc = cross_entropy_inputs(fn, &c, targets, id_type)) != WC_OK) return rc;
+    if (dw && (rc = values_pointer(fn, "dw", dw, dw_dtype)) != WC_OK) return rc;
+    if (T == 0) {
+        if (dw == nullptr || accumulate) return WC_OK;
+        const size_t size = dw_dtype == WC_BF16 ? 2 : 4;
+        return from_cuda(cudaMemset2DAsync(dw, size_t(ld_dw) * size, 0, size_t(D) * size, size_t(V),
+                                           static_cast<cudaStream_t>(stream)),
+                         fn);
+    }
+    if (dx && (rc = values_pointer(fn, "dx", dx, dx_dtype)) != WC_OK) return rc;
+    if ((rc = values_pointer(fn, "lse", lse, WC_F32)) != WC_OK) return rc;
+    if (dlosses && (rc = values_pointer(fn, "dlosses", dlosses, WC_F32)) != WC_OK) return rc;
+    WC_REQUIRE_PTR(fn, workspace);
+    const int64_t need = wc::cross_entropy_grad_workspace(c);
+    if (workspace_bytes < need)
+        return fail(WC_EINVAL, "%s: workspace of %lld bytes, %lld are needed", fn, (long long)workspace_bytes,
+                    (long long)need);
+    c.workspace = workspace;
+    c.lse_in = lse;
+    c.dlosses = dlosses;
+    c.dloss = float(dloss);
+    c.dx = dx;
+    c.dx_bf16 = dx_dtype == WC_BF16;
+    c.ld_dx = ld_dx;
+    c.dw = dw;
+    c.dw_bf16 = dw_dtype == WC_BF16;
+    c.ld_dw = ld_dw;
+    c.accumulate = accumulate != 0;
+    return from_cuda(wc::launch_cross_entropy_grad(c, static_cast<cudaStream_t>(stream)), fn);
+}
+
 WC_API int wc_wait_timeouts(int reset) {
     static const char *fn = "wc_wait_timeouts";
-    unsigned int n = 0;
-    const cudaError_t e = wc::fp8_wait_timeouts(&n, reset != 0);
+    unsigned int n = 0, m = 0;
+    cudaError_t e = wc::fp8_wait_timeouts(&n, reset != 0);
+    if (e == cudaSuccess) e = wc::cross_entropy_wait_timeouts(&m, reset != 0);
     if (e != cudaSuccess) return from_cuda(e, fn);
-    return n > 0x7FFFFFFFu ? 0x7FFFFFFF : int(n);
+    const uint64_t all = uint64_t(n) + m;
+    return all > 0x7FFFFFFFu ? 0x7FFFFFFF : int(all);
 }
 
 WC_API int wc_checked_violations(int flags) {

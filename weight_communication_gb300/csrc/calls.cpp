@@ -1,5 +1,5 @@
 // calls.cpp -- the Python calls of the training-step operators (fp8, embedding,
-// gradnorm), as an extension module on torch's tensors.
+// gradnorm, activation, norm, loss), as an extension module on torch's tensors.
 //
 // Each function checks its tensors, allocates what the caller did not give,
 // and calls the C entry point of libwc.so on the current stream of the tensors'
@@ -45,6 +45,16 @@ struct Library {
     decltype(&wc_embedding_grad) embedding_grad;
     decltype(&wc_fp8_quant) fp8_quant;
     decltype(&wc_fp8_matmul) fp8_matmul;
+    decltype(&wc_fp8_dequant) fp8_dequant;
+    decltype(&wc_activation) activation;
+    decltype(&wc_activation_grad) activation_grad;
+    decltype(&wc_rms_norm) rms_norm;
+    decltype(&wc_rms_norm_grad_workspace) rms_norm_grad_workspace;
+    decltype(&wc_rms_norm_grad) rms_norm_grad;
+    decltype(&wc_cross_entropy_workspace) cross_entropy_workspace;
+    decltype(&wc_cross_entropy) cross_entropy;
+    decltype(&wc_cross_entropy_grad_workspace) cross_entropy_grad_workspace;
+    decltype(&wc_cross_entropy_grad) cross_entropy_grad;
 };
 Library lib;
 PyObject *wc_error;  // binding.WcError
@@ -132,6 +142,49 @@ int64_t row_stride(const at::Tensor &t, const char *name, int64_t rows, int64_t 
     if (rows <= 1) return t.size(1);
     if (t.stride(0) < t.size(1)) bad_value(name, " must not have overlapping rows");
     return t.stride(0);
+}
+
+// A tensor of activations [.., columns] as a matrix: one of two dimensions whose
+// rows are consecutive values, or a contiguous one of any.
+struct Rows {
+    void *data;
+    int64_t rows, cols, ld;
+    int type;
+};
+Rows rows_of(const at::Tensor &t, const char *name) {
+    on_gpu(t, name);
+    const int type = float_type(t.scalar_type(), name);
+    if (t.dim() < 1) bad_value(name, " must have a dimension of columns");
+    const int64_t cols = t.size(-1);
+    if (t.dim() == 2) return {t.data_ptr(), t.size(0), cols, row_stride(t, name, t.size(0), cols), type};
+    if (!t.is_contiguous()) bad_value(name, " must be a matrix or contiguous");
+    int64_t rows = 1;
+    for (int64_t d = 0; d + 1 < t.dim(); ++d) rows *= t.size(d);
+    return {t.data_ptr(), rows, cols, cols, type};
+}
+
+// One of the same shape, type and GPU as another.
+Rows rows_like(PyObject *o, const char *name, const at::Tensor &like) {
+    const at::Tensor &t = tensor(o, name);
+    on_device(t, name, like.device());
+    if (t.scalar_type() != like.scalar_type()) bad_type(name, " must be ", like.scalar_type(), ", got ", t.scalar_type());
+    if (t.sizes() != like.sizes()) bad_value(name, " has shape ", t.sizes(), ", expected ", like.sizes());
+    return rows_of(t, name);
+}
+
+// A contiguous vector of values of a row.
+const at::Tensor &vector_of(PyObject *o, const char *name, int64_t n, at::Device device) {
+    const at::Tensor &t = tensor(o, name);
+    on_device(t, name, device);
+    if (t.numel() != n) bad_value(name, " has shape ", t.sizes(), ", expected ", n, " values");
+    if (!t.is_contiguous()) bad_value(name, " must be contiguous");
+    return t;
+}
+
+const at::Tensor &floats_of(PyObject *o, const char *name, int64_t n, at::Device device) {
+    const at::Tensor &t = vector_of(o, name, n, device);
+    if (t.scalar_type() != at::kFloat) bad_type(name, " must be float32, got ", t.scalar_type());
+    return t;
 }
 
 // The calls stand outside autograd.  A tensor that they write to gets a new
@@ -572,6 +625,290 @@ PyObject *fp8_matmul(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// (parts, out or None, out_dtype) -> out
+PyObject *fp8_dequantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arguments("fp8_dequantize", n, 3);
+    const Matrix8 q = Matrix8::of(args[0]);
+    if (!q.device.is_cuda()) bad_value("the 8-bit matrix must be on a GPU");
+    const c10::cuda::CUDAGuard guard(q.device);
+    at::Tensor out;
+    int64_t ld_out = q.cols;
+    if (args[1] == Py_None) {
+        const at::ScalarType type = dtype(args[2], "out_dtype");
+        float_type(type, "out_dtype");
+        out = new_tensor({q.rows, q.cols}, type, q.device);
+    } else {
+        out = tensor(args[1], "out");
+        if (out.dim() == 2 && out.size(1) != q.cols)
+            bad_value("out has shape ", out.sizes(), ", expected [", q.rows, ", ", q.cols, "]");
+        on_device(out, "out", q.device);
+        ld_out = row_stride(out, "out", q.rows, q.cols);
+    }
+    check("wc_fp8_dequant",
+          lib.fp8_dequant(q.q, q.ld_codes, q.s, q.ld_scales, int(q.block_rows), q.rows, q.cols, out.data_ptr(),
+                          float_type(out.scalar_type(), "out"), ld_out, stream_of(q.device)));
+    if (args[1] != Py_None) written(out);
+    return THPVariable_Wrap(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// ---------------------------------------------------------------------------
+// activations and norms kept in 8 bits
+// ---------------------------------------------------------------------------
+
+wc_kept kept_of(const Matrix8 &m) { return {m.q, m.ld_codes, m.s, m.ld_scales}; }
+
+// A matrix [rows, cols] that a forward pass kept.
+Matrix8 kept_matrix(PyObject *parts, const char *name, int64_t rows, int64_t cols, at::Device device) {
+    const Matrix8 m = Matrix8::of(parts);
+    if (m.rows != rows || m.cols != cols || m.block_rows != 1)
+        bad_value(name, " is [", m.rows, ", ", m.cols, "] with ", m.block_rows, " rows per scale, expected [", rows,
+                  ", ", cols, "] with 1");
+    if (m.device != device) bad_value(name, " is on ", m.device, ", expected ", device);
+    return m;
+}
+
+// (gate, up or None, kind, save, out or None) -> (h, parts of gate or None, parts of up or None)
+PyObject *activation(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arguments("activation", n, 5);
+    const at::Tensor &gate = tensor(args[0], "gate");
+    const Rows g = rows_of(gate, "gate");
+    const bool gated = args[1] != Py_None, save = truth(args[3]);
+    const Rows u = gated ? rows_like(args[1], "up", gate) : Rows{nullptr, 0, 0, g.cols, 0};
+    const int kind = int(integer(args[2]));
+    const at::Device device = gate.device();
+    const c10::cuda::CUDAGuard guard(device);
+    at::Tensor h;
+    Rows o;
+    if (args[4] == Py_None) {
+        h = new_tensor(gate.sizes(), gate.scalar_type(), device);
+        o = {h.data_ptr(), g.rows, g.cols, g.cols, g.type};
+    } else {
+        o = rows_like(args[4], "out", gate);
+        h = tensor(args[4], "out");
+    }
+    ends_gradient(gate, "activation.forward", "gate");
+    if (gated) ends_gradient(tensor(args[1], "up"), "activation.forward", "up");
+    Matrix8 kg, ku;
+    at::Tensor buffer, buffer_up;
+    if (save) buffer = make(&kg, g.rows, g.cols, 1, device);
+    if (save && gated) buffer_up = make(&ku, g.rows, g.cols, 1, device);
+    const wc_kept k = kept_of(kg), k_up = kept_of(ku);
+    check("wc_activation",
+          lib.activation(g.data, g.ld, u.data, u.ld, g.type, kind, g.rows, g.cols, o.data, o.ld, save ? &k : nullptr,
+                         save && gated ? &k_up : nullptr, stream_of(device)));
+    if (args[4] != Py_None) written(h);
+    PyObject *a = save ? described(kg, buffer) : Py_NewRef(Py_None);
+    PyObject *b = save && gated ? described(ku, buffer_up) : Py_NewRef(Py_None);
+    return Py_BuildValue("NNN", THPVariable_Wrap(h), a, b);
+    END_HANDLE_TH_ERRORS
+}
+
+// (dh, kind, parts of gate, parts of up or None) -> (dgate, dup or None)
+PyObject *activation_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arguments("activation_grad", n, 4);
+    const at::Tensor &dh = tensor(args[0], "dh");
+    const Rows d = rows_of(dh, "dh");
+    const int kind = int(integer(args[1]));
+    const bool gated = args[3] != Py_None;
+    const at::Device device = dh.device();
+    const Matrix8 kg = kept_matrix(args[2], "the kept gate", d.rows, d.cols, device);
+    const Matrix8 ku = gated ? kept_matrix(args[3], "the kept up", d.rows, d.cols, device) : Matrix8();
+    const c10::cuda::CUDAGuard guard(device);
+    ends_gradient(dh, "activation.backward", "dh");
+    const at::Tensor dgate = new_tensor(dh.sizes(), dh.scalar_type(), device);
+    at::Tensor dup;
+    if (gated) dup = new_tensor(dh.sizes(), dh.scalar_type(), device);
+    const wc_kept k = kept_of(kg), k_up = kept_of(ku);
+    check("wc_activation_grad",
+          lib.activation_grad(d.data, d.ld, d.type, kind, d.rows, d.cols, &k, gated ? &k_up : nullptr,
+                              dgate.data_ptr(), d.cols, gated ? dup.data_ptr() : nullptr, d.cols, stream_of(device)));
+    return Py_BuildValue("NN", THPVariable_Wrap(dgate), gated ? THPVariable_Wrap(dup) : Py_NewRef(Py_None));
+    END_HANDLE_TH_ERRORS
+}
+
+// (x, weight, eps, add or None, save) -> (y, total or None, rstd or None, parts or None)
+PyObject *rms_norm(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arguments("rms_norm", n, 5);
+    const at::Tensor &x = tensor(args[0], "x");
+    const Rows r = rows_of(x, "x");
+    const at::Device device = x.device();
+    const at::Tensor &weight = vector_of(args[1], "weight", r.cols, device);
+    const int weight_type = float_type(weight.scalar_type(), "weight");
+    const bool adds = args[3] != Py_None, save = truth(args[4]);
+    const Rows a = adds ? rows_like(args[3], "add", x) : Rows{nullptr, 0, 0, r.cols, 0};
+    const c10::cuda::CUDAGuard guard(device);
+    ends_gradient(x, "norm.rms", "x");
+    ends_gradient(weight, "norm.rms", "weight");
+    if (adds) ends_gradient(tensor(args[3], "add"), "norm.rms", "add");
+    const at::Tensor y = new_tensor(x.sizes(), x.scalar_type(), device);
+    at::Tensor total, rstd, buffer;
+    if (adds) total = new_tensor(x.sizes(), x.scalar_type(), device);
+    Matrix8 m;
+    if (save) {
+        rstd = new_tensor({r.rows}, at::kFloat, device);
+        buffer = make(&m, r.rows, r.cols, 1, device);
+    }
+    const wc_kept k = kept_of(m);
+    check("wc_rms_norm",
+          lib.rms_norm(r.data, r.ld, a.data, a.ld, r.type, r.rows, r.cols, weight.data_ptr(), weight_type,
+                       real(args[2]), y.data_ptr(), r.cols, adds ? total.data_ptr() : nullptr, r.cols,
+                       save ? static_cast<float *>(rstd.data_ptr()) : nullptr, save ? &k : nullptr,
+                       stream_of(device)));
+    PyObject *t = adds ? THPVariable_Wrap(total) : Py_NewRef(Py_None);
+    PyObject *s = save ? THPVariable_Wrap(rstd) : Py_NewRef(Py_None);
+    PyObject *q = save ? described(m, buffer) : Py_NewRef(Py_None);
+    return Py_BuildValue("NNNN", THPVariable_Wrap(y), t, s, q);
+    END_HANDLE_TH_ERRORS
+}
+
+// (dy, weight, rstd, parts, add or None, dweight or None, accumulate) -> (dx, dweight)
+PyObject *rms_norm_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arguments("rms_norm_grad", n, 7);
+    const at::Tensor &dy = tensor(args[0], "dy");
+    const Rows d = rows_of(dy, "dy");
+    const at::Device device = dy.device();
+    const at::Tensor &weight = vector_of(args[1], "weight", d.cols, device);
+    const int weight_type = float_type(weight.scalar_type(), "weight");
+    const at::Tensor &rstd = floats_of(args[2], "rstd", d.rows, device);
+    const Matrix8 m = kept_matrix(args[3], "the kept input", d.rows, d.cols, device);
+    const bool adds = args[4] != Py_None, accumulate = truth(args[6]);
+    const Rows a = adds ? rows_like(args[4], "add", dy) : Rows{nullptr, 0, 0, d.cols, 0};
+    const c10::cuda::CUDAGuard guard(device);
+    at::Tensor dweight;
+    if (args[5] == Py_None) {
+        if (accumulate) bad_value("accumulate needs the gradient to add to as dweight");
+        dweight = new_tensor({d.cols}, at::kFloat, device);
+    } else {
+        dweight = vector_of(args[5], "dweight", d.cols, device);
+    }
+    ends_gradient(dy, "norm.rms_grad", "dy");
+    const at::Tensor dx = new_tensor(dy.sizes(), dy.scalar_type(), device);
+    const int64_t bytes = lib.rms_norm_grad_workspace(d.rows, d.cols);
+    check("wc_rms_norm_grad_workspace", bytes);
+    const at::Tensor workspace = bytes_on(device, bytes > 16 ? bytes : 16);
+    const wc_kept k = kept_of(m);
+    check("wc_rms_norm_grad",
+          lib.rms_norm_grad(d.data, d.ld, a.data, a.ld, d.type, d.rows, d.cols, weight.data_ptr(), weight_type,
+                            static_cast<float *>(rstd.data_ptr()), &k, dx.data_ptr(), d.cols, dweight.data_ptr(),
+                            float_type(dweight.scalar_type(), "dweight"), accumulate ? 1 : 0, workspace.data_ptr(),
+                            workspace.numel(), stream_of(device)));
+    if (args[5] != Py_None) written(dweight);
+    return Py_BuildValue("NN", THPVariable_Wrap(dx), THPVariable_Wrap(dweight));
+    END_HANDLE_TH_ERRORS
+}
+
+// ---------------------------------------------------------------------------
+// cross entropy
+// ---------------------------------------------------------------------------
+
+// x [.., D], weight [V, D] and targets (one per row of x) of both directions.
+struct Tokens {
+    const at::Tensor &x, &w, &targets;
+    int64_t T, V, D, ld_x, ld_w;
+    int id_type;
+    const uint16_t *px() const { return static_cast<const uint16_t *>(x.data_ptr()); }
+    const uint16_t *pw() const { return static_cast<const uint16_t *>(w.data_ptr()); }
+};
+Tokens tokens_of(PyObject *const *args) {
+    const at::Tensor &x = tensor(args[0], "x"), &w = tensor(args[1], "weight"), &y = tensor(args[2], "targets");
+    const Rows r = rows_of(x, "x");
+    if (r.type != WC_BF16) bad_type("x must be bfloat16, got ", x.scalar_type());
+    if (w.scalar_type() != at::kBFloat16) bad_type("weight must be bfloat16, got ", w.scalar_type());
+    on_device(w, "weight", x.device());
+    if (w.dim() != 2 || w.size(1) != r.cols)
+        bad_value("weight has shape ", w.sizes(), ", expected [rows, ", r.cols, "]");
+    if (y.scalar_type() != at::kInt && y.scalar_type() != at::kLong)
+        bad_type("targets must be int32 or int64, got ", y.scalar_type());
+    on_device(y, "targets", x.device());
+    if (!y.is_contiguous()) bad_value("targets must be contiguous");
+    if (y.numel() != r.rows) bad_value("targets has shape ", y.sizes(), ", expected one for each of ", r.rows, " rows of x");
+    return {x, w, y, r.rows, w.size(0), r.cols, r.ld, row_stride(w, "weight", w.size(0), r.cols),
+            y.scalar_type() == at::kLong ? WC_I64 : WC_I32};
+}
+
+// (x, weight, targets) -> (losses, lse)
+PyObject *cross_entropy(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arguments("cross_entropy", n, 3);
+    const Tokens t = tokens_of(args);
+    const at::Device device = t.x.device();
+    const c10::cuda::CUDAGuard guard(device);
+    ends_gradient(t.x, "loss.cross_entropy", "x");
+    ends_gradient(t.w, "loss.cross_entropy", "weight");
+    const at::Tensor losses = new_tensor(t.targets.sizes(), at::kFloat, device);
+    const at::Tensor lse = new_tensor(t.targets.sizes(), at::kFloat, device);
+    const int64_t bytes = lib.cross_entropy_workspace(t.px(), t.ld_x, t.pw(), t.ld_w, t.T, t.V, t.D);
+    check("wc_cross_entropy_workspace", bytes);
+    const at::Tensor workspace = bytes_on(device, bytes > 16 ? bytes : 16);
+    check("wc_cross_entropy",
+          lib.cross_entropy(t.px(), t.ld_x, t.pw(), t.ld_w, t.targets.data_ptr(), t.id_type, t.T, t.V, t.D,
+                            static_cast<float *>(losses.data_ptr()), static_cast<float *>(lse.data_ptr()),
+                            workspace.data_ptr(), workspace.numel(), stream_of(device)));
+    return Py_BuildValue("NN", THPVariable_Wrap(losses), THPVariable_Wrap(lse));
+    END_HANDLE_TH_ERRORS
+}
+
+// (x, weight, targets, lse, dlosses (tensor or number), dx wanted, dw wanted, dw or None,
+//  dw_dtype or None, accumulate) -> (dx or None, dw or None)
+PyObject *cross_entropy_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arguments("cross_entropy_grad", n, 10);
+    const Tokens t = tokens_of(args);
+    const at::Device device = t.x.device();
+    const at::Tensor &lse = floats_of(args[3], "lse", t.T, device);
+    const float *dlosses = nullptr;
+    double dloss = 0.0;
+    if (THPVariable_Check(args[4])) {
+        const at::Tensor &d = floats_of(args[4], "dlosses", t.T, device);
+        ends_gradient(d, "loss.cross_entropy_grad", "dlosses");
+        dlosses = static_cast<const float *>(d.data_ptr());
+    } else {
+        dloss = real(args[4]);
+    }
+    const bool want_dx = truth(args[5]), want_dw = truth(args[6]), accumulate = truth(args[9]);
+    if (!want_dx && !want_dw) bad_value("neither dx nor dw asked for");
+    const c10::cuda::CUDAGuard guard(device);
+    at::Tensor dx, dw;
+    int64_t ld_dw = t.D;
+    if (want_dx) dx = new_tensor(t.x.sizes(), at::kBFloat16, device);
+    if (!want_dw) {
+        if (accumulate || args[7] != Py_None) bad_value("dw is given and not asked for");
+    } else if (args[7] == Py_None) {
+        if (accumulate) bad_value("accumulate needs the gradient to add to as dw");
+        const at::ScalarType type = args[8] == Py_None ? at::kBFloat16 : dtype(args[8], "dw_dtype");
+        float_type(type, "dw_dtype");
+        dw = new_tensor({t.V, t.D}, type, device);
+    } else {
+        dw = tensor(args[7], "dw");
+        if (args[8] != Py_None && dw.scalar_type() != dtype(args[8], "dw_dtype"))
+            bad_type("dw must be ", dtype(args[8], "dw_dtype"), ", got ", dw.scalar_type());
+        if (dw.dim() == 2 && dw.size(1) != t.D)
+            bad_value("dw has shape ", dw.sizes(), ", expected [", t.V, ", ", t.D, "]");
+        on_device(dw, "dw", device);
+        ld_dw = row_stride(dw, "dw", t.V, t.D);
+    }
+    const int dw_type = want_dw ? float_type(dw.scalar_type(), "dw") : WC_BF16;
+    const int64_t bytes = lib.cross_entropy_grad_workspace(t.px(), t.ld_x, t.pw(), t.ld_w, t.T, t.V, t.D);
+    check("wc_cross_entropy_grad_workspace", bytes);
+    const at::Tensor workspace = bytes_on(device, bytes > 16 ? bytes : 16);
+    check("wc_cross_entropy_grad",
+          lib.cross_entropy_grad(t.px(), t.ld_x, t.pw(), t.ld_w, t.targets.data_ptr(), t.id_type, t.T, t.V, t.D,
+                                 static_cast<const float *>(lse.data_ptr()), dlosses, dloss,
+                                 want_dx ? dx.data_ptr() : nullptr, WC_BF16, t.D,
+                                 want_dw ? dw.data_ptr() : nullptr, dw_type, ld_dw, accumulate ? 1 : 0,
+                                 workspace.data_ptr(), workspace.numel(), stream_of(device)));
+    if (args[7] != Py_None) written(dw);
+    return Py_BuildValue("NN", want_dx ? THPVariable_Wrap(dx) : Py_NewRef(Py_None),
+                         want_dw ? THPVariable_Wrap(dw) : Py_NewRef(Py_None));
+    END_HANDLE_TH_ERRORS
+}
+
 // ---------------------------------------------------------------------------
 // module
 // ---------------------------------------------------------------------------
@@ -594,6 +931,16 @@ PyObject *setup(PyObject *, PyObject *const *args, Py_ssize_t n) {
     entry("wc_embedding_grad", &lib.embedding_grad);
     entry("wc_fp8_quant", &lib.fp8_quant);
     entry("wc_fp8_matmul", &lib.fp8_matmul);
+    entry("wc_fp8_dequant", &lib.fp8_dequant);
+    entry("wc_activation", &lib.activation);
+    entry("wc_activation_grad", &lib.activation_grad);
+    entry("wc_rms_norm", &lib.rms_norm);
+    entry("wc_rms_norm_grad_workspace", &lib.rms_norm_grad_workspace);
+    entry("wc_rms_norm_grad", &lib.rms_norm_grad);
+    entry("wc_cross_entropy_workspace", &lib.cross_entropy_workspace);
+    entry("wc_cross_entropy", &lib.cross_entropy);
+    entry("wc_cross_entropy_grad_workspace", &lib.cross_entropy_grad_workspace);
+    entry("wc_cross_entropy_grad", &lib.cross_entropy_grad);
     Py_INCREF(args[1]);
     Py_XSETREF(wc_error, args[1]);
     Py_RETURN_NONE;
@@ -605,6 +952,9 @@ PyObject *setup(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyMethodDef methods[] = {WC_METHOD(setup),        WC_METHOD(embedding),    WC_METHOD(embedding_grad),
                          WC_METHOD(grad_list),    WC_METHOD(grad_norm),    WC_METHOD(fp8_empty),    WC_METHOD(fp8_view),
                          WC_METHOD(fp8_quantize), WC_METHOD(fp8_quantize_into), WC_METHOD(fp8_matmul),
+                         WC_METHOD(fp8_dequantize), WC_METHOD(activation), WC_METHOD(activation_grad),
+                         WC_METHOD(rms_norm),     WC_METHOD(rms_norm_grad), WC_METHOD(cross_entropy),
+                         WC_METHOD(cross_entropy_grad),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "wc_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,882 @@
+// cross_entropy.cu -- softmax cross entropy of a linear output layer over a large
+// vocabulary, and its gradient, in pieces of the vocabulary and without keeping
+// the logits.
+//
+//   s[t][v]  = x[t] . w[v],   lse[t] = log sum over v of exp(s[t][v])
+//   loss[t]  = lse[t] - s[t][y(t)]
+//   d[t][v]  = g[t] (exp(s[t][v] - lse[t]) - [v = y(t)])
+//   dx = d w,   dw = d^T x
+//
+// Forward: tiles of 256 tokens by 256 rows of w on the tensor cores.  A tile's
+// epilogue reduces its logits, as they leave the tensor memory, to each token's
+// maximum and sum of exponentials over 128 columns; a second kernel joins those.
+// Backward: for one piece of the vocabulary after the other, the logits once
+// more, whose epilogue writes d (bf16, its only rounding) to a buffer, and one
+// launch for the two products that read it, dx summed over the pieces in fp32.
+// So a pass multiplies four times where one that keeps T x V logits multiplies
+// three times.
+//
+// One kernel does all products (bf16 operands, fp32 sums): pairs of SMs
+// (cta_group::2) on tiles of 256 x 256, 64 values of K to a stage.  Operands come
+// by TMA as they lie: those whose rows run along K are K-major (logits, d in
+// dx), the others MN-major (w in dx, d and x in dw), so nothing is transposed.
+// Warps 0-7 are the epilogue, 8 brings operands, 9 multiplies; two tiles' sums
+// fit the tensor memory, so a tile's epilogue runs beside the next tile's
+// products.
+#include <atomic>
+
+#include "wc_device.cuh"
+#include "wc_internal.h"
+#include "wc_launch.cuh"
+#include "wc_tcgen05.cuh"
+#include "wc_wait.cuh"
+
+namespace wc {
+
+namespace {
+
+__device__ unsigned int g_wait_timeouts;
+
+// A warp that gives up takes no further part: it arrives on no barrier and starts
+// no copy or product, the others run out in turn, and every output that misses a
+// sum is NaN.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+    return wc::mbar_wait(bar, parity, &g_wait_timeouts);
+}
+
+constexpr int kSms = 152;
+constexpr int kHalf = 128;                  // rows of an operand that a CTA brings
+constexpr int kTile = 2 * kHalf;
+constexpr int kDepth = 64;                  // values of K in a stage
+constexpr int kOperand = kHalf * kDepth * 2;
+constexpr int kStageBytes = 2 * kOperand;
+constexpr int kStages = 6;
+constexpr int kBuffers = 2;                 // tiles of sums in tensor memory
+constexpr int kEpilogueWarps = 8, kProducer = 8, kMma = 9;
+constexpr int kThreads = 320;
+// Epilogue staging of a warp: 64 bytes of each of its 32 rows, 80 bytes apart to
+// keep 16-byte accesses off one another's banks.
+constexpr int kPitch = 80;
+constexpr int kStagingBytes = 32 * kPitch;
+constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * kStagingBytes + 1024;
+
+constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float nan32() { return __uint_as_float(0x7FC00000u); }
+
+// One product C[i][j] = sum over k of A[i][k] B[j][k].
+struct Job {
+    int32_t tiles_i, tiles_j;
+    int32_t split;          // parts of K with sums of their own
+    int32_t blocks;         // of K
+    int32_t rows_i, rows_j;
+    int32_t mn_i, mn_j;     // MN-major: rows of the operand are contiguous in memory
+    int32_t j_at, kj_at;    // where B's rows and its K begin in its matrix
+    // what becomes of a product: out [split][rows_i][ld], added to what `add` holds
+    void *out;
+    const void *add;
+    int64_t ld_out, ld_add, split_out, split_add;
+    int32_t out_bf16, add_bf16, vec;
+};
+
+struct Args {
+    Job job[2];
+    int32_t units[2];       // tiles x split
+    // of the logits' epilogues
+    const void *targets;
+    int32_t wide;           // 64-bit targets
+    int32_t V;
+    float2 *parts;          // [2 tiles_j][rows_i]: maximum (times log2 e), sum
+    float *target_logit;    // [rows_i]
+    const float *lse, *dlosses;
+    float dloss;
+};
+
+enum Mode { kStats, kGradient, kProducts };
+
+// Row of w that token t is to predict, or -1.
+__device__ __forceinline__ int32_t target_of(const void *targets, int wide, int32_t V, int64_t t) {
+    const int64_t y = wide ? static_cast<const int64_t *>(targets)[t] : int64_t(static_cast<const int32_t *>(targets)[t]);
+    return y >= 0 && y < V ? int32_t(y) : -1;
+}
+
+// Tile order: bands of 16 tiles of i, all of j within a band, so that the CTAs
+// at work together share operand rows in L2.
+__device__ __forceinline__ void tile_at(const Job &a, int32_t t, int32_t *ti, int32_t *tj) {
+    const int32_t band = t / (16 * a.tiles_j);
+    const int32_t first = band * 16;
+    const int32_t high = min(16, a.tiles_i - first);
+    const int32_t in = t - band * 16 * a.tiles_j;
+    *ti = first + in % high;
+    *tj = in / high;
+}
+
+struct Unit {
+    int32_t job, ti, tj, part, block0, blocks;
+};
+template <Mode MODE>
+__device__ __forceinline__ Unit unit_at(const Args &a, int32_t u) {
+    Unit r;
+    r.job = MODE == kProducts && u >= a.units[0] ? 1 : 0;
+    const Job &j = a.job[r.job];
+    if (r.job) u -= a.units[0];
+    const int32_t tile = MODE == kProducts ? u / j.split : u;
+    r.part = MODE == kProducts ? u - tile * j.split : 0;
+    tile_at(j, tile, &r.ti, &r.tj);
+    r.block0 = MODE == kProducts ? int32_t(int64_t(j.blocks) * r.part / j.split) : 0;
+    r.blocks = MODE == kProducts ? int32_t(int64_t(j.blocks) * (r.part + 1) / j.split) - r.block0 : j.blocks;
+    return r;
+}
+
+// 128 rows x 64 of K of an operand, to 16 KB of shared memory with 128-byte swizzle:
+// K-major 128 lines of 64 values of K, MN-major twice 64 lines (one per k) of 64 rows.
+__device__ __forceinline__ void load_operand(uint32_t to, const CUtensorMap *map, uint32_t bar, int mn, int32_t row,
+                                             int32_t k) {
+    if (mn) {
+        tma_load<true>(to, map, bar, row, k);
+        tma_load<true>(to + kOperand / 2, map, bar, row + 64, k);
+    } else {
+        tma_load<true>(to, map, bar, k, row);
+    }
+}
+
+// Shared-memory operand descriptor (addresses and strides in 16-byte units; bit 46
+// is its version, 2 << 61 the 128-byte swizzle).  Groups of 8 lines are 1024 bytes
+// apart: K-major of rows, MN-major of k, whose two halves of 64 rows are 8 KB apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, int mn) {
+    return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(mn ? kOperand / 2 / 16 : 1) << 16) | (uint64_t(64) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// Instruction descriptor: fp32 sums, bf16 x bf16, 256 x 256.
+__device__ __forceinline__ uint32_t instr_desc(int mn_i, int mn_j) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(mn_i) << 15) | (uint32_t(mn_j) << 16) |
+           (uint32_t(kTile >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// epilogues: a warp's 32 rows x 32 columns, one row per lane
+// ---------------------------------------------------------------------------
+
+// The running maximum and sum of a row.  `top` is the maximum times log2 e, as
+// the exponentials use it.
+struct Running {
+    float top, sum;
+};
+
+// cols: columns of these that exist (at least 1).
+__device__ __forceinline__ void stats(Running &r, uint32_t (&v)[32], int cols) {
+    if (cols < 32) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (c >= cols) v[c] = 0xFF800000u;  // -infinity
+    }
+    float m[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) m[c] = __uint_as_float(v[c]);
+#pragma unroll
+    for (int c = 4; c < 32; ++c) m[c & 3] = fmaxf(m[c & 3], __uint_as_float(v[c]));
+    const float top = fmaxf(r.top, __fmul_rn(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), kLog2E));
+    float s[4] = {__fmul_rn(r.sum, ex2(__fadd_rn(r.top, -top))), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < 32; ++c) s[c & 3] = __fadd_rn(s[c & 3], ex2(__fmaf_rn(__uint_as_float(v[c]), kLog2E, -top)));
+    r.top = top;
+    r.sum = __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
+}
+
+// v[at] of a lane's registers (any other value if `at` is outside).
+__device__ __forceinline__ float pick(const uint32_t (&v)[32], int at) {
+    uint32_t x = v[0];
+#pragma unroll
+    for (int c = 1; c < 32; ++c) x = at == c ? v[c] : x;
+    return __uint_as_float(x);
+}
+
+// 32 rows of 64 bytes, staged one per lane, to rows `pitch` bytes apart: 64
+// consecutive bytes of 8 rows at a time.
+__device__ __forceinline__ void store_staged(const uint8_t *staging, char *base, int64_t pitch, int rows, int lane) {
+    const int seg = (lane & 3) * 16;
+#pragma unroll
+    for (int r = lane >> 2; r < 32; r += 8)
+        if (r < rows)
+            *reinterpret_cast<uint4 *>(base + r * pitch + seg) =
+                *reinterpret_cast<const uint4 *>(staging + r * kPitch + seg);
+}
+
+__device__ __forceinline__ void stage_bf16(uint8_t *staging, const float (&x)[32], int lane) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = f32x2_to_bf16x2_bits(x[8 * q + 2 * k], x[8 * q + 2 * k + 1]);
+        *reinterpret_cast<uint4 *>(staging + lane * kPitch + q * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// A product's sums.  (row0, col0): the first row of the warp, the first column.
+__device__ __forceinline__ void store_sums(const Job &a, int32_t part, const float (&x)[32], uint8_t *staging,
+                                           int32_t row0, int32_t col0, int lane) {
+    const int rows = a.rows_i - row0, cols = a.rows_j - col0;
+    if (rows <= 0 || cols <= 0) return;
+    if (a.out_bf16 && a.add == nullptr && a.vec && cols >= 32) {
+        stage_bf16(staging, x, lane);
+        __syncwarp();
+        store_staged(staging, static_cast<char *>(a.out) + (int64_t(row0) * a.ld_out + col0) * 2, a.ld_out * 2, rows, lane);
+        __syncwarp();
+        return;
+    }
+    // 16 columns at a time, four to a lane
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float4 *>(staging + lane * kPitch + q * 16) =
+                make_float4(x[16 * h + 4 * q], x[16 * h + 4 * q + 1], x[16 * h + 4 * q + 2], x[16 * h + 4 * q + 3]);
+        __syncwarp();
+        const int c = 16 * h + 4 * (lane & 3), left = cols - c;
+#pragma unroll 2
+        for (int r = lane >> 2; r < 32; r += 8) {
+            if (r >= rows || left <= 0) continue;
+            const float4 v = *reinterpret_cast<const float4 *>(staging + r * kPitch + (lane & 3) * 16);
+            float y[4] = {v.x, v.y, v.z, v.w};
+            const int64_t at = part * a.split_out + (row0 + r) * a.ld_out + col0 + c;
+            const int64_t from = part * a.split_add + (row0 + r) * a.ld_add + col0 + c;
+            const bool whole = a.vec && left >= 4;
+            if (a.add) {
+                if (a.add_bf16) {
+                    const uint16_t *p = static_cast<const uint16_t *>(a.add) + from;
+                    if (whole) {
+                        const uint2 o = *reinterpret_cast<const uint2 *>(p);
+                        y[0] = __fadd_rn(__uint_as_float(o.x << 16), y[0]);
+                        y[1] = __fadd_rn(__uint_as_float(o.x & 0xFFFF0000u), y[1]);
+                        y[2] = __fadd_rn(__uint_as_float(o.y << 16), y[2]);
+                        y[3] = __fadd_rn(__uint_as_float(o.y & 0xFFFF0000u), y[3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < left) y[k] = __fadd_rn(bf16_bits_to_f32(p[k]), y[k]);
+                    }
+                } else {
+                    const float *p = static_cast<const float *>(a.add) + from;
+                    if (whole) {
+                        const float4 o = *reinterpret_cast<const float4 *>(p);
+                        y[0] = __fadd_rn(o.x, y[0]);
+                        y[1] = __fadd_rn(o.y, y[1]);
+                        y[2] = __fadd_rn(o.z, y[2]);
+                        y[3] = __fadd_rn(o.w, y[3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < left) y[k] = __fadd_rn(p[k], y[k]);
+                    }
+                }
+            }
+            if (a.out_bf16) {
+                uint16_t *p = static_cast<uint16_t *>(a.out) + at;
+                if (whole) {
+                    *reinterpret_cast<uint2 *>(p) = make_uint2(f32x2_to_bf16x2_bits(y[0], y[1]), f32x2_to_bf16x2_bits(y[2], y[3]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < left) p[k] = f32_to_bf16_bits(y[k]);
+                }
+            } else {
+                float *p = static_cast<float *>(a.out) + at;
+                if (whole) {
+                    *reinterpret_cast<float4 *>(p) = make_float4(y[0], y[1], y[2], y[3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < left) p[k] = y[k];
+                }
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// kernel
+// ---------------------------------------------------------------------------
+
+template <Mode MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant__ CUtensorMap map_j0,
+               const __grid_constant__ CUtensorMap map_i1, const __grid_constant__ CUtensorMap map_j1,
+               const __grid_constant__ Args a) {
+    extern __shared__ uint8_t dynamic_smem[];
+    // full: a stage's operands are here (both CTAs', counted in the first one).
+    // empty: its products have ended.  sums: a tile is complete.  taken: its
+    // sums have been read (both CTAs', counted in the first one).
+    __shared__ uint64_t full[kStages], empty[kStages], sums[kBuffers], taken[kBuffers], drained;
+    __shared__ uint32_t tmem_slot;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t stages = (smem_of(dynamic_smem) + 1023u) & ~1023u;
+    const int32_t rank = int32_t(blockIdx.x & 1);
+    const int32_t first = int32_t(blockIdx.x >> 1), step = int32_t(gridDim.x >> 1);
+    const int32_t units = a.units[0] + (MODE == kProducts ? a.units[1] : 0);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_of(&full[s]), 1);
+            mbar_init(smem_of(&empty[s]), 1);
+        }
+        for (int b = 0; b < kBuffers; ++b) {
+            mbar_init(smem_of(&sums[b]), 1);
+            mbar_init(smem_of(&taken[b]), 2 * kEpilogueWarps);
+        }
+        mbar_init(smem_of(&drained), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncwarp();
+    if (warp == kMma) tmem_alloc<true>(smem_of(&tmem_slot), kBuffers * kTile);
+    tc_before_sync();
+    __syncthreads();
+    cluster_sync();  // the other CTA's barriers are ready too
+    tc_after_sync();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&tmem_slot);
+    wait_for_predecessor();  // all above is set-up that reads no operand
+
+    if (warp == kProducer) {
+        uint32_t stage = 0, phase = 0;
+        bool ok = true;
+        for (int32_t t = first; ok && t < units; t += step) {
+            const Unit u = unit_at<MODE>(a, t);
+            const Job &job = a.job[u.job];
+            const CUtensorMap *map_i = u.job ? &map_i1 : &map_i0, *map_j = u.job ? &map_j1 : &map_j0;
+            const int32_t row_i = u.ti * kTile + rank * kHalf, row_j = job.j_at + u.tj * kTile + rank * kHalf;
+            for (int32_t b = 0; b < u.blocks; ++b) {
+                ok = mbar_wait(smem_of(&empty[stage]), phase ^ 1u);
+                if (!ok) break;
+                if (elected()) {
+                    const uint32_t local = smem_of(&full[stage]), bar = in_cta(local, 0);
+                    const uint32_t base = stages + stage * kStageBytes;
+                    const int32_t k = (u.block0 + b) * kDepth;
+                    if (rank == 0) mbar_expect(local, 2 * kStageBytes);
+                    load_operand(base, map_i, bar, job.mn_i, row_i, k);
+                    load_operand(base + kOperand, map_j, bar, job.mn_j, row_j, job.kj_at + k);
+                }
+                __syncwarp();
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok) wait_ms(20);  // for the copies in flight to land before the CTA goes
+    } else if (warp == kMma && rank == 0) {
+        uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+        bool ok = true;
+        const bool lead = elected();
+        for (int32_t t = first; ok && t < units; t += step) {
+            const Unit u = unit_at<MODE>(a, t);
+            const Job &job = a.job[u.job];
+            const uint32_t idesc = instr_desc(job.mn_i, job.mn_j);
+            // 16 values of K on: 32 bytes of every line, or 16 lines
+            const uint64_t step_i = job.mn_i ? 128 : 2, step_j = job.mn_j ? 128 : 2;
+            ok = mbar_wait(smem_of(&taken[buf]), buf_phase ^ 1u);
+            if (!ok) break;
+            tc_after_sync();
+            for (int32_t b = 0; b < u.blocks; ++b) {
+                ok = mbar_wait(smem_of(&full[stage]), phase);
+                if (!ok) break;
+                tc_after_sync();
+                if (lead) {
+                    const uint32_t base = stages + stage * kStageBytes;
+                    uint64_t di = smem_desc(base, job.mn_i), dj = smem_desc(base + kOperand, job.mn_j);
+#pragma unroll
+                    for (int k = 0; k < kDepth / 16; ++k) {
+                        mma(tmem + buf * kTile, di, dj, idesc, b > 0 || k > 0);
+                        di += step_i;
+                        dj += step_j;
+                    }
+                    mma_commit<true>(smem_of(&empty[stage]));
+                }
+                __syncwarp();
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) break;
+            if (lead) mma_commit<true>(smem_of(&sums[buf]));
+            __syncwarp();
+            if (++buf == kBuffers) {
+                buf = 0;
+                buf_phase ^= 1u;
+            }
+        }
+        // No product may be in flight when the tensor memory is freed.
+        if (lead) mma_commit<true>(smem_of(&drained), 1);
+        __syncwarp();
+        mbar_wait(smem_of(&drained), 0);
+    } else if (warp < kEpilogueWarps) {
+        const int group = warp >> 2;
+        uint8_t *const staging = dynamic_smem + (stages - smem_of(dynamic_smem)) + kStages * kStageBytes + warp * kStagingBytes;
+        const uint32_t from0 = tmem + (uint32_t(warp & 3) << 21) + group * kHalf;
+        const uint32_t taken0 = in_cta(smem_of(&taken[0]), 0);
+        uint32_t buf = 0, phase = 0;
+        bool ok = true;
+        for (int32_t t = first; t < units; t += step) {
+            const Unit u = unit_at<MODE>(a, t);
+            const Job &job = a.job[u.job];
+            const int32_t row0 = u.ti * kTile + rank * kHalf + (warp & 3) * 32, row = row0 + lane;
+            const int32_t col0 = u.tj * kTile + group * kHalf;
+            const bool live = row < job.rows_i;
+            // (columns of this group that exist)
+            const int32_t cols = max(0, min(job.rows_j - col0, kHalf));
+            int32_t target = -1;  // its column in this group, or any number outside
+            bool padding = true;
+            float lse2 = 0.0f, g = 0.0f;
+            if (MODE != kProducts && live) {
+                const int32_t y = target_of(a.targets, a.wide, a.V, row);
+                padding = y < 0;
+                if (!padding) target = y - job.j_at - col0;
+                if (MODE == kGradient && !padding) {
+                    lse2 = __fmul_rn(a.lse[row], kLog2E);
+                    g = a.dlosses ? a.dlosses[row] : a.dloss;
+                }
+            }
+            if (ok) ok = mbar_wait(smem_of(&sums[buf]), phase);
+            tc_after_sync();
+            Running run = {-INFINITY, 0.0f};
+            uint32_t v[2][32];
+            if (ok) {
+                tmem_load(from0 + buf * kTile, v[0]);
+                tmem_wait(v[0]);
+            }
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 32) {
+                uint32_t(&w)[32] = v[(c / 32) & 1];
+                if (!ok) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) w[k] = 0x7FC00000u;
+                } else if (c + 32 < kHalf) {
+                    tmem_load(from0 + buf * kTile + c + 32, v[(c / 32 + 1) & 1]);
+                } else {
+                    tc_before_sync();  // all read: the next tile may have the buffer
+                    __syncwarp();
+                    if (elected()) mbar_arrive_cluster(taken0 + buf * 8);
+                }
+                if (MODE == kStats) {
+                    if (c < cols) {
+                        const int at = target - c;
+                        if (__any_sync(kFull, at >= 0 && at < 32)) {
+                            const float s = pick(w, at);
+                            if (at >= 0 && at < 32) a.target_logit[row] = s;
+                        }
+                        stats(run, w, cols - c);
+                    }
+                } else if (MODE == kGradient) {
+                    float x[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        float p = ex2(__fmaf_rn(__uint_as_float(w[k]), kLog2E, -lse2));
+                        if (target - c == k) p = __fadd_rn(p, -1.0f);
+                        x[k] = __fmul_rn(g, p);
+                        // (padding tokens have no gradient whatever their logits are)
+                        if (c + k >= cols || padding) x[k] = 0.0f;
+                    }
+                    stage_bf16(staging, x, lane);
+                    __syncwarp();
+                    store_staged(staging, static_cast<char *>(job.out) + (int64_t(row0) * job.ld_out + col0 + c) * 2,
+                                 job.ld_out * 2, job.rows_i - row0, lane);
+                    __syncwarp();
+                } else {
+                    float x[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(w[k]);
+                    store_sums(job, u.part, x, staging, row0, col0 + c, lane);
+                }
+                if (ok && c + 32 < kHalf) tmem_wait(v[(c / 32 + 1) & 1]);
+            }
+            if (MODE == kStats && live) {
+                if (!ok) run = {nan32(), nan32()};
+                a.parts[(int64_t(u.tj) * 2 + group) * job.rows_i + row] = make_float2(run.top, run.sum);
+            }
+            if (++buf == kBuffers) {
+                buf = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+
+    tc_before_sync();
+    __syncthreads();
+    // neither CTA's memory goes before the other one is done with it
+    cluster_sync();
+    tc_after_sync();
+    if (warp == kMma) tmem_free<true>(tmem, kBuffers * kTile);
+}
+
+// ---------------------------------------------------------------------------
+// small kernels
+// ---------------------------------------------------------------------------
+
+// lse and loss of each token from the parts of its row: 32 tokens by 32 warps of
+// a CTA, each warp every 32nd part, then the warps in turn.
+__global__ void __launch_bounds__(1024) join_stats_kernel(const float2 *parts, int32_t count, int32_t T,
+                                                          const float *target_logit, const void *targets, int wide,
+                                                          int32_t V, float *losses, float *lse) {
+    __shared__ float2 row[32][33];
+    wait_for_predecessor();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t t = blockIdx.x * 32 + lane;
+    // (a part that has no columns is (-infinity, 0))
+    auto joined = [](float2 a, float2 b) {
+        const float top = fmaxf(a.x, b.x);
+        const float x = a.x == -INFINITY && a.y == 0.0f ? 0.0f : __fmul_rn(a.y, ex2(__fadd_rn(a.x, -top)));
+        const float y = b.x == -INFINITY && b.y == 0.0f ? 0.0f : __fmul_rn(b.y, ex2(__fadd_rn(b.x, -top)));
+        return make_float2(top, __fadd_rn(x, y));
+    };
+    float2 r = make_float2(-INFINITY, 0.0f);
+    if (t < T)
+#pragma unroll 4
+        for (int32_t p = warp; p < count; p += 32) r = joined(r, parts[int64_t(p) * T + t]);
+    row[warp][lane] = r;
+    __syncthreads();
+    r = row[lane][warp];  // warp w has token w
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+        const float2 other = make_float2(__shfl_xor_sync(kFull, r.x, o), __shfl_xor_sync(kFull, r.y, o));
+        r = lane & o ? joined(other, r) : joined(r, other);
+    }
+    const int32_t at = blockIdx.x * 32 + warp;
+    if (lane != 0 || at >= T) return;
+    const float l = __fmul_rn(__fadd_rn(r.x, log2f(r.y)), kLn2);
+    if (lse) lse[at] = l;
+    if (losses) losses[at] = target_of(targets, wide, V, at) >= 0 ? __fadd_rn(l, -target_logit[at]) : 0.0f;
+}
+
+// A matrix with rows that start on 16 bytes, from one whose rows may start
+// anywhere.  Rows whose target is padding become 0 (targets may be NULL).
+__global__ void __launch_bounds__(256) lay_out_kernel(const uint16_t *src, int64_t ld, int64_t rows, int32_t cols,
+                                                      const void *targets, int wide, int32_t V, uint16_t *dst,
+                                                      int32_t ld_dst, int vec) {
+    wait_for_predecessor();
+    const int32_t chunks = ld_dst / 8;
+    const int64_t n = rows * chunks;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+        const int64_t r = i / chunks;
+        const int32_t c = int32_t(i - r * chunks) * 8;
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        if (targets == nullptr || target_of(targets, wide, V, r) >= 0) {
+            const uint16_t *p = src + r * ld + c;
+            if (vec && c + 8 <= cols) {
+                q = ld_stream_u4(p);
+            } else {
+                uint32_t w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[k] = c + k < cols ? p[k] : 0u;
+                q = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+            }
+        }
+        *reinterpret_cast<uint4 *>(dst + r * ld_dst + c) = q;
+    }
+}
+
+// out = the sum of `count` matrices [rows][ld_part] of fp32, in order.
+__global__ void __launch_bounds__(256) join_sums_kernel(const float *parts, int32_t count, int64_t rows, int32_t cols,
+                                                        int64_t ld_part, void *out, int bf16, int64_t ld_out) {
+    wait_for_predecessor();
+    const int64_t stride = rows * ld_part, n = rows * cols;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+        const int64_t r = i / cols, c = i - r * cols;
+        const float *p = parts + r * ld_part + c;
+        float x = p[0];
+        for (int32_t k = 1; k < count; ++k) x = __fadd_rn(x, p[k * stride]);
+        if (bf16) static_cast<uint16_t *>(out)[r * ld_out + c] = f32_to_bf16_bits(x);
+        else static_cast<float *>(out)[r * ld_out + c] = x;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t up256(int64_t bytes) { return ceil_div(bytes, 256) * 256; }
+
+struct Bf16Matrix {
+    const uint16_t *p;
+    int64_t ld, rows, cols;
+};
+
+// Boxes of 128 rows x 64 of K, or MN-major of 64 rows x 64 of K.
+cudaError_t describe(CUtensorMap *map, const Bf16Matrix &m, bool mn) {
+    EncodeTiled encode;
+    const cudaError_t e = encoder(&encode);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t dims[2] = {cuuint64_t(m.cols), cuuint64_t(m.rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(m.ld) * 2};
+    const cuuint32_t box[2] = {64, cuuint32_t(mn ? 64 : kHalf)};
+    const cuuint32_t step[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(m.p), dims, strides,
+                              box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <Mode MODE>
+cudaError_t run(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
+    // once for each GPU: the kernel's attribute stays set
+    static std::atomic<uint64_t> prepared{0};
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (device & 63);
+    if (device > 63 || !(prepared.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(product_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        prepared.fetch_or(bit, std::memory_order_relaxed);
+    }
+    for (int k = 0; k < 2; ++k) a.units[k] = a.job[k].tiles_i * a.job[k].tiles_j * a.job[k].split;
+    const int64_t units = int64_t(a.units[0]) + (MODE == kProducts ? a.units[1] : 0);
+    const uint32_t grid = 2 * uint32_t(units < kSms / 2 ? units : kSms / 2);
+    return launch_after(product_kernel<MODE>, dim3(grid), dim3(kThreads), kSmem, stream, 2, maps[0], maps[1],
+                        maps[2], maps[3], a);
+}
+
+bool aligned(const uint16_t *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
+
+// Tokens of one forward launch: it leaves 16 bytes per token and 256 rows of w.
+constexpr int64_t kTokens = 65536;
+
+// The workspace's parts, one after another.
+struct Layout {
+    int64_t bytes = 0;
+    int64_t take(int64_t n) {
+        const int64_t at = bytes;
+        bytes += up256(n);
+        return at;
+    }
+};
+
+struct Forward {
+    int64_t parts, target_logit, x, w, bytes;
+    explicit Forward(const CrossEntropy &c) {
+        Layout l;
+        const int64_t T = c.T < kTokens ? c.T : kTokens;
+        parts = l.take(ceil_div(c.V, kTile) * 2 * T * int64_t(sizeof(float2)));
+        target_logit = l.take(T * 4);
+        x = aligned(c.x, c.ld_x) ? -1 : l.take(c.T * ceil_div(c.D, 8) * 16);
+        w = aligned(c.w, c.ld_w) ? -1 : l.take(c.V * ceil_div(c.D, 8) * 16);
+        bytes = l.bytes;
+    }
+};
+
+// Columns of a piece: its gradients of the logits (bf16) take 256 MB, or as much
+// as dx's sums where that is more, so that those are not moved more often than
+// the pieces themselves.
+int64_t piece_of(const CrossEntropy &c) {
+    const int64_t budget = int64_t(1) << 28, sums = 4 * c.T * c.D;
+    int64_t cols = (budget > sums ? budget : sums) / (2 * c.T) / kTile * kTile;
+    if (cols < kTile) cols = kTile;
+    const int64_t pieces = ceil_div(c.V, cols);
+    return ceil_div(ceil_div(c.V, pieces), kTile) * kTile;
+}
+
+struct Backward {
+    int64_t x, w, d, dx, bytes;
+    int64_t piece, split, ld_dx;
+    explicit Backward(const CrossEntropy &c) {
+        Layout l;
+        const int64_t ld = ceil_div(c.D, 8) * 16;
+        x = l.take(c.T * ld);
+        w = aligned(c.w, c.ld_w) ? -1 : l.take(c.V * ld);
+        piece = piece_of(c);
+        d = l.take(c.T * piece * 2);
+        // dx has few tiles where tokens are few, and its K is the vocabulary
+        const int64_t tiles = ceil_div(c.T, kTile) * ceil_div(c.D, kTile), blocks = ceil_div(piece, kDepth);
+        split = tiles < kSms / 2 ? kSms / 2 / tiles : 1;
+        if (split > blocks / 8) split = blocks / 8 > 1 ? blocks / 8 : 1;
+        ld_dx = ceil_div(c.D, 4) * 4;
+        dx = split > 1 || piece < c.V ? l.take(split * c.T * ld_dx * 4) : -1;
+        bytes = l.bytes;
+    }
+};
+
+cudaError_t lay_out(const uint16_t *src, int64_t ld, int64_t rows, int64_t cols, const CrossEntropy *mask,
+                    uint16_t *dst, cudaStream_t stream) {
+    const int64_t ld_dst = ceil_div(cols, 8) * 8, ctas = ceil_div(rows * ld_dst / 8, 256);
+    return launch_after(lay_out_kernel, dim3(uint32_t(ctas < 16 * kSms ? ctas : 16 * kSms)), dim3(256), 0, stream, 1,
+                        src, ld, rows, int32_t(cols), mask ? mask->targets : nullptr, mask && mask->wide ? 1 : 0,
+                        int32_t(mask ? mask->V : 0), dst, int32_t(ld_dst), aligned(src, ld) ? 1 : 0);
+}
+
+Job job_of(int64_t rows_i, int64_t rows_j, int64_t K) {
+    Job j = {};
+    j.tiles_i = int32_t(ceil_div(rows_i, kTile));
+    j.tiles_j = int32_t(ceil_div(rows_j, kTile));
+    j.split = 1;
+    j.blocks = int32_t(ceil_div(K, kDepth));
+    j.rows_i = int32_t(rows_i);
+    j.rows_j = int32_t(rows_j);
+    return j;
+}
+
+}  // namespace
+
+int64_t cross_entropy_workspace(const CrossEntropy &c) { return Forward(c).bytes; }
+
+cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
+    const Forward f(c);
+    char *const ws = static_cast<char *>(c.workspace);
+    Bf16Matrix x = {c.x, c.ld_x, c.T, c.D}, w = {c.w, c.ld_w, c.V, c.D};
+    cudaError_t e = cudaSuccess;
+    if (f.x >= 0) {
+        x.p = reinterpret_cast<uint16_t *>(ws + f.x);
+        x.ld = ceil_div(c.D, 8) * 8;
+        e = lay_out(c.x, c.ld_x, c.T, c.D, nullptr, reinterpret_cast<uint16_t *>(ws + f.x), stream);
+        if (e != cudaSuccess) return e;
+    }
+    if (f.w >= 0) {
+        w.p = reinterpret_cast<uint16_t *>(ws + f.w);
+        w.ld = ceil_div(c.D, 8) * 8;
+        e = lay_out(c.w, c.ld_w, c.V, c.D, nullptr, reinterpret_cast<uint16_t *>(ws + f.w), stream);
+        if (e != cudaSuccess) return e;
+    }
+    CUtensorMap maps[4];
+    if ((e = describe(&maps[1], w, false)) != cudaSuccess) return e;
+    const int64_t id = c.wide ? 8 : 4;
+    for (int64_t t0 = 0; t0 < c.T; t0 += kTokens) {
+        Bf16Matrix some = x;
+        some.p += t0 * x.ld;
+        some.rows = c.T - t0 < kTokens ? c.T - t0 : kTokens;
+        if ((e = describe(&maps[0], some, false)) != cudaSuccess) return e;
+        maps[2] = maps[0];
+        maps[3] = maps[1];
+        Args a = {};
+        a.job[0] = job_of(some.rows, c.V, c.D);
+        a.targets = static_cast<const char *>(c.targets) + t0 * id;
+        a.wide = c.wide;
+        a.V = int32_t(c.V);
+        a.parts = reinterpret_cast<float2 *>(ws + f.parts);
+        a.target_logit = reinterpret_cast<float *>(ws + f.target_logit);
+        if ((e = run<kStats>(maps, a, stream)) != cudaSuccess) return e;
+        e = launch_after(join_stats_kernel, dim3(uint32_t(ceil_div(some.rows, 32))), dim3(1024), 0, stream, 1,
+                         static_cast<const float2 *>(a.parts), 2 * a.job[0].tiles_j, int32_t(some.rows),
+                         static_cast<const float *>(a.target_logit), a.targets, a.wide, a.V,
+                         c.losses ? c.losses + t0 : nullptr, c.lse ? c.lse + t0 : nullptr);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+int64_t cross_entropy_grad_workspace(const CrossEntropy &c) { return Backward(c).bytes; }
+
+cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t stream) {
+    const Backward f(c);
+    char *const ws = static_cast<char *>(c.workspace);
+    // x with its padding tokens 0, so that nothing that they hold reaches dw
+    const Bf16Matrix x = {reinterpret_cast<uint16_t *>(ws + f.x), ceil_div(c.D, 8) * 8, c.T, c.D};
+    cudaError_t e = lay_out(c.x, c.ld_x, c.T, c.D, &c, reinterpret_cast<uint16_t *>(ws + f.x), stream);
+    if (e != cudaSuccess) return e;
+    Bf16Matrix w = {c.w, c.ld_w, c.V, c.D};
+    if (f.w >= 0) {
+        w.p = reinterpret_cast<uint16_t *>(ws + f.w);
+        w.ld = x.ld;
+        e = lay_out(c.w, c.ld_w, c.V, c.D, nullptr, reinterpret_cast<uint16_t *>(ws + f.w), stream);
+        if (e != cudaSuccess) return e;
+    }
+    const Bf16Matrix d = {reinterpret_cast<uint16_t *>(ws + f.d), f.piece, c.T, f.piece};
+    CUtensorMap logits[4], products[4];
+    if ((e = describe(&logits[0], x, false)) != cudaSuccess) return e;
+    if ((e = describe(&logits[1], w, false)) != cudaSuccess) return e;
+    logits[2] = logits[0];
+    logits[3] = logits[1];
+    if ((e = describe(&products[0], d, false)) != cudaSuccess) return e;
+    if ((e = describe(&products[1], w, true)) != cudaSuccess) return e;
+    if ((e = describe(&products[2], d, true)) != cudaSuccess) return e;
+    if ((e = describe(&products[3], x, true)) != cudaSuccess) return e;
+    float *const sums = f.dx >= 0 ? reinterpret_cast<float *>(ws + f.dx) : nullptr;
+    const int64_t size = c.dw_bf16 ? 2 : 4;
+
+    for (int64_t v0 = 0; v0 < c.V; v0 += f.piece) {
+        const int64_t cols = c.V - v0 < f.piece ? c.V - v0 : f.piece;
+        const bool last = v0 + cols == c.V;
+        Args a = {};
+        a.job[0] = job_of(c.T, cols, c.D);
+        a.job[0].j_at = int32_t(v0);
+        a.job[0].out = ws + f.d;
+        a.job[0].ld_out = f.piece;
+        a.targets = c.targets;
+        a.wide = c.wide;
+        a.V = int32_t(c.V);
+        a.lse = c.lse_in;
+        a.dlosses = c.dlosses;
+        a.dloss = c.dloss;
+        if ((e = run<kGradient>(logits, a, stream)) != cudaSuccess) return e;
+
+        Args p = {};
+        if (c.dx) {
+            Job &j = p.job[0] = job_of(c.T, c.D, cols);
+            j.mn_j = 1;
+            j.kj_at = int32_t(v0);
+            j.split = int32_t(f.split < j.blocks ? f.split : j.blocks);
+            if (sums && !(last && f.split == 1)) {
+                j.out = sums;
+                j.ld_out = f.ld_dx;
+                j.split_out = c.T * f.ld_dx;
+                j.vec = 1;
+            } else {
+                j.out = c.dx;
+                j.out_bf16 = c.dx_bf16;
+                j.ld_out = c.ld_dx;
+                j.vec = aligned(static_cast<const uint16_t *>(c.dx), c.ld_dx);
+            }
+            if (v0 > 0) {
+                j.add = sums;
+                j.ld_add = f.ld_dx;
+                j.split_add = c.T * f.ld_dx;
+            }
+        }
+        if (c.dw) {
+            Job &j = p.job[1] = job_of(cols, c.D, c.T);
+            j.mn_i = j.mn_j = 1;
+            j.out = static_cast<char *>(c.dw) + v0 * c.ld_dw * size;
+            j.out_bf16 = c.dw_bf16;
+            j.ld_out = c.ld_dw;
+            j.vec = aligned(static_cast<const uint16_t *>(c.dw), c.ld_dw);
+            if (c.accumulate) {
+                j.add = j.out;
+                j.add_bf16 = c.dw_bf16;
+                j.ld_add = c.ld_dw;
+            }
+        }
+        if ((e = run<kProducts>(products, p, stream)) != cudaSuccess) return e;
+    }
+    if (c.dx && f.split > 1) {
+        const int64_t ctas = ceil_div(c.T * c.D, 256);
+        return launch_after(join_sums_kernel, dim3(uint32_t(ctas < 16 * kSms ? ctas : 16 * kSms)), dim3(256), 0,
+                            stream, 1, static_cast<const float *>(sums), int32_t(f.split), c.T, int32_t(c.D), f.ld_dx,
+                            c.dx, c.dx_bf16 ? 1 : 0, c.ld_dx);
+    }
+    return cudaSuccess;
+}
+
+cudaError_t cross_entropy_wait_timeouts(unsigned int *count, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(count, g_wait_timeouts, sizeof(*count));
+    if (e == cudaSuccess && reset) {
+        const unsigned int zero = 0u;
+        e = cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(zero));
+    }
+    return e;
+}
+
+}  // namespace wc

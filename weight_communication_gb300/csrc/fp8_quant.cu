@@ -1,14 +1,8 @@
 // fp8_quant.cu -- quantization to 8-bit floating point (e4m3) with one fp32
 // scale per block of 128 values along the axis that a product sums over.
 //
-//   m = max |x| of the block
-//   m < 448 * 2^-126 (the scale would not be normal): scale 0, codes 0
-//   m infinite or not a number:                       scale NaN, codes 0
-//   else scale = m / 448, code = e4m3(x * fl(448 / m)), to nearest, ties to even
-//
-// 448 is e4m3's largest value, so no code saturates.  NaN as the scale of a
-// block with a value that is not finite makes every sum it enters NaN, as
-// the unquantized product would be.
+// The rule is in wc_fp8.cuh.  NaN as the scale of a block with a value that is
+// not finite makes every sum it enters NaN, as the unquantized product would be.
 //
 // One CTA per tile of 128 x 128 reads it once and can write both layouts a
 // training step needs: the rows' codes (blocks along the columns) and the
@@ -23,9 +17,8 @@
 // Rows that start anywhere are read in aligned chunks and shifted: 4411 x 9433
 // bf16 both ways 49 -> 40 us against value by value.
 // Bound: HBM (2 bytes read and 1 or 2 written per value).
-#include <cuda_fp8.h>
-
 #include "wc_device.cuh"
+#include "wc_fp8.cuh"
 #include "wc_internal.h"
 #include "wc_launch.cuh"
 #include "wc_rows.cuh"
@@ -36,26 +29,6 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kThreads = 256;
-constexpr float kTop = 448.0f;
-
-struct Scale8 {
-    float scale, inv;
-};
-
-__device__ __forceinline__ Scale8 scale_of(float m) {
-    Scale8 s;
-    if (m < kTop * kMinNormal) {  // exact product
-        s.scale = 0.0f;
-        s.inv = 0.0f;
-    } else if (m <= 3.40282346638528859812e38f) {
-        s.scale = __fdiv_rn(m, kTop);
-        s.inv = __fdiv_rn(kTop, m);
-    } else {
-        s.scale = __uint_as_float(0x7FC00000u);
-        s.inv = 0.0f;
-    }
-    return s;
-}
 
 // The 8 x 8 values of a thread, and the operations on them that depend on the
 // type.  An encoding without its sign orders magnitudes, infinities and NaN
@@ -130,17 +103,6 @@ struct Values<float> {
     static __device__ __forceinline__ uint32_t single(uint32_t m) { return m; }
     static __device__ __forceinline__ uint32_t column(const uint32_t *m, int j) { return m[j]; }
 };
-
-// Codes of 8 values of blocks with one inv.  inv 0 gives codes 0 also where
-// the product is not a number.
-__device__ __forceinline__ uint2 codes_of(const float (&x)[8], float inv) {
-    uint32_t h[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        h[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(x[2 * j], inv), __fmul_rn(x[2 * j + 1], inv)),
-                                        __NV_SATFINITE, __NV_E4M3);
-    return inv == 0.0f ? make_uint2(0u, 0u) : make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-}
 
 // Shared transposed codes: column c's 128 rows as 16 words of 8 bytes, word w
 // at slot w ^ (c / 8 % 16), so that the 16 lanes of a store hit all banks.

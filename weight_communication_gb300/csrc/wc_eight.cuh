@@ -1,0 +1,172 @@
+// wc_eight.cuh -- a row's block of 128 values over 16 lanes, 8 values each.
+//
+// VEC: lane l holds columns 8l .. 8l + 7, moved 16 bytes at a time; rows then
+// start on 16 bytes and have a multiple of 8 columns.  Otherwise lane l holds
+// columns l, l + 16, .., l + 112, moved one at a time, so that rows may start on
+// any value and end on any column and neighbouring lanes still touch
+// neighbouring values.
+#pragma once
+
+#include <stdint.h>
+
+#include "wc_device.cuh"
+#include "wc_fp8.cuh"
+
+namespace wc {
+
+constexpr int kBlock8 = 128;  // values per scale
+
+template <bool VEC>
+__device__ __forceinline__ int column_of(int l, int j) {
+    return VEC ? 8 * l + j : l + 16 * j;
+}
+
+// Values as they are stored: bf16 two to a word.  mag(): the largest magnitude's
+// encoding, in which infinities and NaN are above all finite values.
+template <typename T>
+struct Eight;
+
+template <>
+struct Eight<uint16_t> {
+    uint32_t w[4];
+    // `p`: the block's first value, `left`: columns from there to the row's end
+    template <bool VEC>
+    __device__ __forceinline__ void load(const uint16_t *p, int l, int left) {
+        if (VEC) {
+            const uint4 q = 8 * l < left ? ld_stream_u4(p + 8 * l) : make_uint4(0u, 0u, 0u, 0u);
+            w[0] = q.x;
+            w[1] = q.y;
+            w[2] = q.z;
+            w[3] = q.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int c = l + 32 * k;
+                const uint32_t lo = c < left ? p[c] : 0u, hi = c + 16 < left ? p[c + 16] : 0u;
+                w[k] = lo | (hi << 16);
+            }
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = 0u;
+    }
+    __device__ __forceinline__ float at(int j) const {
+        return __uint_as_float((j & 1) ? (w[j / 2] & 0xFFFF0000u) : (w[j / 2] << 16));
+    }
+    __device__ __forceinline__ uint32_t mag() const {
+        uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+        for (int k = 1; k < 4; ++k) m = __vmaxu2(m, w[k] & 0x7FFF7FFFu);
+        return max(m << 16, m & 0xFFFF0000u);
+    }
+    __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = f32x2_to_bf16x2_bits(x[2 * k], x[2 * k + 1]);
+    }
+    template <bool VEC>
+    __device__ __forceinline__ void store(uint16_t *p, int l, int left) const {
+        if (VEC) {
+            if (8 * l < left) *reinterpret_cast<uint4 *>(p + 8 * l) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int c = l + 32 * k;
+                if (c < left) p[c] = uint16_t(w[k]);
+                if (c + 16 < left) p[c + 16] = uint16_t(w[k] >> 16);
+            }
+        }
+    }
+};
+
+template <>
+struct Eight<float> {
+    uint32_t w[8];
+    template <bool VEC>
+    __device__ __forceinline__ void load(const float *p, int l, int left) {
+        if (VEC) {
+            uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+            if (8 * l < left) {
+                a = ld_stream_u4(p + 8 * l);
+                b = ld_stream_u4(p + 8 * l + 4);
+            }
+            w[0] = a.x;
+            w[1] = a.y;
+            w[2] = a.z;
+            w[3] = a.w;
+            w[4] = b.x;
+            w[5] = b.y;
+            w[6] = b.z;
+            w[7] = b.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = l + 16 * j < left ? __float_as_uint(p[l + 16 * j]) : 0u;
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 0u;
+    }
+    __device__ __forceinline__ float at(int j) const { return __uint_as_float(w[j]); }
+    __device__ __forceinline__ uint32_t mag() const {
+        uint32_t m = w[0] & 0x7FFFFFFFu;
+#pragma unroll
+        for (int j = 1; j < 8; ++j) m = max(m, w[j] & 0x7FFFFFFFu);
+        return m;
+    }
+    __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[j]);
+    }
+    template <bool VEC>
+    __device__ __forceinline__ void store(float *p, int l, int left) const {
+        if (VEC) {
+            if (8 * l < left) {
+                *reinterpret_cast<uint4 *>(p + 8 * l) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(p + 8 * l + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (l + 16 * j < left) p[l + 16 * j] = __uint_as_float(w[j]);
+        }
+    }
+};
+
+// The maximum over the 16 lanes of a block.
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
+#pragma unroll
+    for (int o = 8; o > 0; o /= 2) m = max(m, __shfl_xor_sync(kFull, m, o));
+    return m;
+}
+
+// Codes of the block's rows at `q`, whose rows go on to the next multiple of 16
+// (`left` is of the row's columns; the codes past them are written as 0).
+template <bool VEC>
+__device__ __forceinline__ void store_codes(uint8_t *q, uint2 codes, int l, int left) {
+    const int end = (left + 15) & ~15;
+    if (VEC) {
+        if (8 * l < end) *reinterpret_cast<uint2 *>(q + 8 * l) = codes;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (l + 16 * j < end) q[l + 16 * j] = uint8_t((j < 4 ? codes.x : codes.y) >> (8 * (j & 3)));
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ uint2 load_codes(const uint8_t *q, int l, int left) {
+    uint2 codes = make_uint2(0u, 0u);
+    if (VEC) {
+        if (8 * l < left) codes = ld_stream_u2(q + 8 * l);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (l + 16 * j < left) codes.x |= uint32_t(q[l + 16 * j]) << (8 * j);
+            if (l + 64 + 16 * j < left) codes.y |= uint32_t(q[l + 64 + 16 * j]) << (8 * j);
+        }
+    }
+    return codes;
+}
+
+}  // namespace wc

@@ -107,6 +107,111 @@ struct Fp8Quant {
     int64_t ld_st;
 };
 cudaError_t launch_fp8_quant(const Fp8Quant &a, cudaStream_t stream);
+// A matrix kept in that form, one scale per 1 x 128; q NULL if there is none.
+struct Kept8 {
+    uint8_t *q;
+    int64_t ld_q;
+    float *s;
+    int64_t ld_s;
+};
+
+struct Fp8Dequant {
+    const uint8_t *q;          // [rows][ld_q]
+    int64_t ld_q;
+    const float *s;            // [ceil(cols/128)][ld_s]
+    int64_t ld_s;
+    int rows_per_scale;        // 1 or 128
+    int64_t rows, cols;
+    void *out;                 // [rows][ld_out]
+    bool out_bf16;
+    int64_t ld_out;
+};
+cudaError_t launch_fp8_dequant(const Fp8Dequant &a, cudaStream_t stream);
+
+// Activations.  up, dup: NULL where there is no gate.
+constexpr int kActRelu = 0, kActSilu = 1, kActGelu = 2;
+struct Activation {
+    const void *gate, *up;
+    int64_t ld_gate, ld_up;
+    bool bf16;
+    int kind;
+    int64_t rows, cols;
+    void *h;
+    int64_t ld_h;
+    Kept8 kept_gate, kept_up;
+};
+struct ActivationGrad {
+    const void *dh;
+    int64_t ld_dh;
+    bool bf16;
+    int kind;
+    int64_t rows, cols;
+    Kept8 kept_gate, kept_up;
+    void *dgate, *dup;
+    int64_t ld_dgate, ld_dup;
+};
+cudaError_t launch_activation(const Activation &a, cudaStream_t stream);
+cudaError_t launch_activation_grad(const ActivationGrad &a, cudaStream_t stream);
+
+// Root-mean-square norm.  Rows of up to kNormCols columns.
+constexpr int64_t kNormCols = 16384;
+struct RmsNorm {
+    const void *x, *add;       // [rows][ld]; add may be NULL
+    int64_t ld_x, ld_add;
+    bool bf16;
+    int64_t rows, cols;
+    const void *weight;        // [cols]
+    bool weight_bf16;
+    float eps;
+    void *y, *total;           // total: x + add, with add
+    int64_t ld_y, ld_total;
+    float *rstd;               // [rows], with kept
+    Kept8 kept;
+};
+struct RmsNormGrad {
+    const void *dy, *add;      // add: gradient of the sum's other use, or NULL
+    int64_t ld_dy, ld_add;
+    bool bf16;
+    int64_t rows, cols;
+    const void *weight;
+    bool weight_bf16;
+    const float *rstd;
+    Kept8 kept;
+    void *dx;
+    int64_t ld_dx;
+    void *dweight;             // [cols]
+    bool dweight_bf16, accumulate;
+    float *partials;
+};
+cudaError_t launch_rms_norm(const RmsNorm &a, cudaStream_t stream);
+// Values (fp32) of workspace.
+int64_t rms_norm_grad_partials(int64_t rows, int64_t cols);
+cudaError_t launch_rms_norm_grad(const RmsNormGrad &a, cudaStream_t stream);
+
+// Cross entropy of a linear layer over a vocabulary; bf16 operands.
+struct CrossEntropy {
+    const uint16_t *x, *w;     // [T][ld_x], [V][ld_w]
+    int64_t ld_x, ld_w, T, V, D;
+    const void *targets;       // [T]
+    bool wide;                 // 64-bit targets
+    void *workspace;
+    float *losses, *lse;       // [T]; forward only, each may be NULL
+};
+struct CrossEntropyGrad : CrossEntropy {
+    const float *lse_in;       // [T]
+    const float *dlosses;      // [T], or NULL for dloss
+    float dloss;
+    void *dx, *dw;             // [T][ld_dx], [V][ld_dw]; each may be NULL
+    bool dx_bf16, dw_bf16, accumulate;
+    int64_t ld_dx, ld_dw;
+};
+// Bytes of workspace; read the sizes, x, w and their strides alone.
+int64_t cross_entropy_workspace(const CrossEntropy &c);
+int64_t cross_entropy_grad_workspace(const CrossEntropy &c);
+cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream);
+cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t stream);
+cudaError_t cross_entropy_wait_timeouts(unsigned int *count, bool reset);
+
 struct Fp8Operand {
     const uint8_t *q;          // [rows][ld]
     int64_t ld;

@@ -3,7 +3,7 @@
 A matrix is held as e4m3 codes and fp32 scales: one scale for every 128 values
 along the axis that a product sums over (activations and gradients), or one
 for every 128 x 128 (weights).  `quantize` and `quantize_weight` make such
-matrices, `matmul` multiplies two of them on the tensor cores with fp32 sums,
+matrices, `dequantize` gives their values back, `matmul` multiplies two of them on the tensor cores with fp32 sums,
 and `Fp8Linear` composes them into a layer's forward and backward pass:
 
     lin = Fp8Linear(weight)                    # [N, K] bf16 or fp32
@@ -117,6 +117,13 @@ def matmul(a: Fp8Tensor, b: Fp8Tensor, out: torch.Tensor | None = None,
     or `out`; with accumulate, added to what `out` holds."""
     return binding.on_stream(stream, a.device, binding.calls().fp8_matmul, a._parts, b._parts, out,
                              out_dtype, accumulate)
+
+
+def dequantize(q: Fp8Tensor, out_dtype: torch.dtype = torch.bfloat16,
+               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """What `q` stands for, [rows, cols] in bf16 or fp32: a new tensor or `out`
+    (whose rows may start on any value)."""
+    return binding.on_stream(stream, q.device, binding.calls().fp8_dequantize, q._parts, out, out_dtype)
 
 
 class Fp8Linear:
