@@ -9,7 +9,9 @@
 //
 // Forward: tiles of 256 tokens by 256 rows of w on the tensor cores.  A tile's
 // epilogue reduces its logits, as they leave the tensor memory, to each token's
-// maximum and sum of exponentials over 128 columns; a second kernel joins those.
+// maximum and sum of exponentials over 128 columns, its target left out; a second
+// kernel joins those with the target's logit, as log1p(sum over v != y of
+// exp(s[t][v] - s[t][y])).
 // Backward: for one piece of the vocabulary after the other, the logits once
 // more, whose epilogue writes d (bf16, its only rounding) to a buffer, and one
 // launch for the two products that read it, dx summed over the pieces in fp32.
@@ -23,6 +25,14 @@
 // Warps 0-7 are the epilogue, 8 brings operands, 9 multiplies; two tiles' sums
 // fit the tensor memory, so a tile's epilogue runs beside the next tile's
 // products.
+//
+// The tensor core cuts sums off where fp32 would round them, so logits come out
+// nearer to 0 by some 2^-25 of themselves for each 16 values of K (D = 2048: 8e-6
+// for a logit of 4).  Over the vocabulary that largely cancels; a target's logit
+// stands alone, so it is summed by itself in fp32 (warps 10 and 11 of the forward
+// pass, the kernel that lays x out in the backward pass), and d of a target
+// is expm1(s[t][y] - lse[t]).  (Losses of 8192 x 32000 x 2048: 8.1e-6 off rms with the
+// tensor core's target.)
 #include <atomic>
 
 #include "wc_device.cuh"
@@ -52,8 +62,8 @@ constexpr int kOperand = kHalf * kDepth * 2;
 constexpr int kStageBytes = 2 * kOperand;
 constexpr int kStages = 6;
 constexpr int kBuffers = 2;                 // tiles of sums in tensor memory
-constexpr int kEpilogueWarps = 8, kProducer = 8, kMma = 9;
-constexpr int kThreads = 320;
+constexpr int kEpilogueWarps = 8, kProducer = 8, kMma = 9, kTargets = 10, kWarps = 12;
+constexpr int kThreads = kWarps * 32;
 // Epilogue staging of a warp: 64 bytes of each of its 32 rows, 80 bytes apart to
 // keep 16-byte accesses off one another's banks.
 constexpr int kPitch = 80;
@@ -93,6 +103,9 @@ struct Args {
     int32_t V;
     float2 *parts;          // [2 tiles_j][rows_i]: maximum (times log2 e), sum
     float *target_logit;    // [rows_i]
+    const uint16_t *x, *w;  // for it, as they were given
+    int64_t ld_x, ld_w;
+    int32_t D, vec;         // vec: rows of x and w start on 16 bytes
     const float *lse, *dlosses;
     float dloss;
 };
@@ -103,6 +116,42 @@ enum Mode { kStats, kGradient, kProducts };
 __device__ __forceinline__ int32_t target_of(const void *targets, int wide, int32_t V, int64_t t) {
     const int64_t y = wide ? static_cast<const int64_t *>(targets)[t] : int64_t(static_cast<const int32_t *>(targets)[t]);
     return y >= 0 && y < V ? int32_t(y) : -1;
+}
+
+__device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float sum) {
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        sum = __fmaf_rn(__uint_as_float(u[k] << 16), __uint_as_float(v[k] << 16), sum);
+        sum = __fmaf_rn(__uint_as_float(u[k] & 0xFFFF0000u), __uint_as_float(v[k] & 0xFFFF0000u), sum);
+    }
+    return sum;
+}
+
+// A warp's sum over D of x[d] w[d], in fp32, the same in every lane.
+__device__ __forceinline__ float row_dot(const uint16_t *x, const uint16_t *w, int32_t D, int vec, int lane) {
+    float s[2] = {0.0f, 0.0f};
+    if (vec) {
+        int32_t d = 8 * lane;
+        for (; d + 264 <= D; d += 512) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x + d)), b = __ldg(reinterpret_cast<const uint4 *>(w + d));
+            const uint4 c = __ldg(reinterpret_cast<const uint4 *>(x + d + 256)), e = __ldg(reinterpret_cast<const uint4 *>(w + d + 256));
+            s[0] = dot8(a, b, s[0]);
+            s[1] = dot8(c, e, s[1]);
+        }
+        for (; d < D; d += 256) {
+            if (d + 8 <= D) s[0] = dot8(__ldg(reinterpret_cast<const uint4 *>(x + d)), __ldg(reinterpret_cast<const uint4 *>(w + d)), s[0]);
+            else
+                for (int32_t c = d; c < D; ++c) s[0] = __fmaf_rn(bf16_bits_to_f32(x[c]), bf16_bits_to_f32(w[c]), s[0]);
+        }
+    } else {
+#pragma unroll 8
+        for (int32_t d = lane; d < D; d += 32) s[0] = __fmaf_rn(bf16_bits_to_f32(x[d]), bf16_bits_to_f32(w[d]), s[0]);
+    }
+    float sum = __fadd_rn(s[0], s[1]);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, o));
+    return sum;
 }
 
 // Tile order: bands of 16 tiles of i, all of j within a band, so that the CTAs
@@ -191,19 +240,20 @@ __device__ __forceinline__ void stats(Running &r, uint32_t (&v)[32], int cols) {
 #pragma unroll
     for (int c = 4; c < 32; ++c) m[c & 3] = fmaxf(m[c & 3], __uint_as_float(v[c]));
     const float top = fmaxf(r.top, __fmul_rn(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), kLog2E));
-    float s[4] = {__fmul_rn(r.sum, ex2(__fadd_rn(r.top, -top))), 0.0f, 0.0f, 0.0f};
+    const float from = top == -INFINITY ? 0.0f : -top;  // nothing yet: every exponential is 0
+    float s[4] = {__fmul_rn(r.sum, ex2(__fadd_rn(r.top, from))), 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int c = 0; c < 32; ++c) s[c & 3] = __fadd_rn(s[c & 3], ex2(__fmaf_rn(__uint_as_float(v[c]), kLog2E, -top)));
+    for (int c = 0; c < 32; ++c) s[c & 3] = __fadd_rn(s[c & 3], ex2(__fmaf_rn(__uint_as_float(v[c]), kLog2E, from)));
     r.top = top;
     r.sum = __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
 }
 
-// v[at] of a lane's registers (any other value if `at` is outside).
-__device__ __forceinline__ float pick(const uint32_t (&v)[32], int at) {
-    uint32_t x = v[0];
-#pragma unroll
-    for (int c = 1; c < 32; ++c) x = at == c ? v[c] : x;
-    return __uint_as_float(x);
+// Two parts of a row (one that has no columns is (-infinity, 0)).
+__device__ __forceinline__ float2 joined_stats(float2 a, float2 b) {
+    const float top = fmaxf(a.x, b.x);
+    const float x = a.y == 0.0f ? 0.0f : __fmul_rn(a.y, ex2(__fadd_rn(a.x, -top)));
+    const float y = b.y == 0.0f ? 0.0f : __fmul_rn(b.y, ex2(__fadd_rn(b.x, -top)));
+    return make_float2(top, __fadd_rn(x, y));
 }
 
 // 32 rows of 64 bytes, staged one per lane, to rows `pitch` bytes apart: 64
@@ -442,7 +492,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
             const int32_t cols = max(0, min(job.rows_j - col0, kHalf));
             int32_t target = -1;  // its column in this group, or any number outside
             bool padding = true;
-            float lse2 = 0.0f, g = 0.0f;
+            float lse2 = 0.0f, g = 0.0f, own = 0.0f;  // own: d of the target
             if (MODE != kProducts && live) {
                 const int32_t y = target_of(a.targets, a.wide, a.V, row);
                 padding = y < 0;
@@ -450,8 +500,10 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                 if (MODE == kGradient && !padding) {
                     lse2 = __fmul_rn(a.lse[row], kLog2E);
                     g = a.dlosses ? a.dlosses[row] : a.dloss;
+                    own = __fmul_rn(g, expm1f(__fadd_rn(a.target_logit[row], -a.lse[row])));
                 }
             }
+            const int last = padding ? 0 : cols;  // of the columns with a gradient
             if (ok) ok = mbar_wait(smem_of(&sums[buf]), phase);
             tc_after_sync();
             Running run = {-INFINITY, 0.0f};
@@ -477,8 +529,8 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                     if (c < cols) {
                         const int at = target - c;
                         if (__any_sync(kFull, at >= 0 && at < 32)) {
-                            const float s = pick(w, at);
-                            if (at >= 0 && at < 32) a.target_logit[row] = s;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) w[k] = at == k ? 0xFF800000u : w[k];  // -infinity
                         }
                         stats(run, w, cols - c);
                     }
@@ -486,11 +538,9 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                     float x[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        float p = ex2(__fmaf_rn(__uint_as_float(w[k]), kLog2E, -lse2));
-                        if (target - c == k) p = __fadd_rn(p, -1.0f);
-                        x[k] = __fmul_rn(g, p);
+                        const float p = __fmul_rn(g, ex2(__fmaf_rn(__uint_as_float(w[k]), kLog2E, -lse2)));
                         // (padding tokens have no gradient whatever their logits are)
-                        if (c + k >= cols || padding) x[k] = 0.0f;
+                        x[k] = c + k >= last ? 0.0f : target - c == k ? own : p;
                     }
                     stage_bf16(staging, x, lane);
                     __syncwarp();
@@ -516,12 +566,149 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
         }
     }
 
+    if (MODE == kStats && warp >= kTargets) {
+        for (int32_t t = int32_t(blockIdx.x) + int32_t(gridDim.x) * (warp - kTargets); t < a.job[0].rows_i;
+             t += int32_t(gridDim.x) * (kWarps - kTargets)) {
+            const int32_t y = target_of(a.targets, a.wide, a.V, t);
+            if (y < 0) continue;
+            const float s = row_dot(a.x + t * a.ld_x, a.w + y * a.ld_w, a.D, a.vec, lane);
+            if (lane == 0) a.target_logit[t] = s;
+        }
+    }
+
     tc_before_sync();
     __syncthreads();
     // neither CTA's memory goes before the other one is done with it
     cluster_sync();
     tc_after_sync();
     if (warp == kMma) tmem_free<true>(tmem, kBuffers * kTile);
+}
+
+// ---------------------------------------------------------------------------
+// few tokens
+// ---------------------------------------------------------------------------
+
+// The forward pass of T tokens, one reading of w at the memory's rate: a warp has
+// kFewRows rows of w at a time, their products with all tokens (fp32 in shared
+// memory) in fp32, and the tokens' maxima and sums over its rows in registers.
+constexpr int kFewRows = 4, kFewThreads = 256, kFewWarps = kFewThreads / 32;
+
+struct Few {
+    const uint16_t *x, *w;
+    int64_t ld_x, ld_w;
+    int32_t V, D;
+    const void *targets;
+    int32_t wide;
+    float2 *parts;           // [gridDim.x][T]
+    float *target_logit;
+};
+
+template <int T, bool VEC>
+__global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
+    extern __shared__ __align__(16) float tokens[];  // [T][padded D]
+    __shared__ float2 joined[kFewWarps][T];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t pitch = (a.D + 7) & ~7;
+    wait_for_predecessor();
+    let_successor_start();
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        for (int32_t d = threadIdx.x; d < pitch; d += kFewThreads)
+            tokens[t * pitch + d] = d < a.D ? bf16_bits_to_f32(a.x[t * a.ld_x + d]) : 0.0f;
+    int32_t y[T];
+    Running run[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        y[t] = target_of(a.targets, a.wide, a.V, t);
+        run[t] = {-INFINITY, 0.0f};
+    }
+    __syncthreads();
+    const int64_t step = int64_t(gridDim.x) * kFewWarps * kFewRows;
+    for (int64_t v = (int64_t(blockIdx.x) * kFewWarps + warp) * kFewRows; v < a.V; v += step) {
+        float s[kFewRows][T];
+        const uint16_t *row[kFewRows];
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r) {
+            // (rows past the last are read as the last, and dropped below)
+            row[r] = a.w + (v + r < a.V ? v + r : a.V - 1) * a.ld_w;
+#pragma unroll
+            for (int t = 0; t < T; ++t) s[r][t] = 0.0f;
+        }
+        if (VEC) {
+#pragma unroll 4
+            for (int32_t d = 8 * lane; d < pitch; d += 256) {
+                uint4 q[kFewRows];
+                if (d + 8 <= a.D) {
+#pragma unroll
+                    for (int r = 0; r < kFewRows; ++r) q[r] = ld_stream_u4(row[r] + d);
+                } else {  // the row's end
+#pragma unroll
+                    for (int r = 0; r < kFewRows; ++r) {
+                        uint32_t e[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) e[k] = d + k < a.D ? row[r][d + k] : 0u;
+                        q[r] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                    const float4 lo = *reinterpret_cast<const float4 *>(tokens + t * pitch + d);
+                    const float4 hi = *reinterpret_cast<const float4 *>(tokens + t * pitch + d + 4);
+#pragma unroll
+                    for (int r = 0; r < kFewRows; ++r) {
+                        s[r][t] = __fmaf_rn(__uint_as_float(q[r].x << 16), lo.x, s[r][t]);
+                        s[r][t] = __fmaf_rn(__uint_as_float(q[r].x & 0xFFFF0000u), lo.y, s[r][t]);
+                        s[r][t] = __fmaf_rn(__uint_as_float(q[r].y << 16), lo.z, s[r][t]);
+                        s[r][t] = __fmaf_rn(__uint_as_float(q[r].y & 0xFFFF0000u), lo.w, s[r][t]);
+                        s[r][t] = __fmaf_rn(__uint_as_float(q[r].z << 16), hi.x, s[r][t]);
+                        s[r][t] = __fmaf_rn(__uint_as_float(q[r].z & 0xFFFF0000u), hi.y, s[r][t]);
+                        s[r][t] = __fmaf_rn(__uint_as_float(q[r].w << 16), hi.z, s[r][t]);
+                        s[r][t] = __fmaf_rn(__uint_as_float(q[r].w & 0xFFFF0000u), hi.w, s[r][t]);
+                    }
+                }
+            }
+        } else {
+#pragma unroll 4
+            for (int32_t d = lane; d < a.D; d += 32) {
+                float q[kFewRows];
+#pragma unroll
+                for (int r = 0; r < kFewRows; ++r) q[r] = bf16_bits_to_f32(row[r][d]);
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                    const float e = tokens[t * pitch + d];
+#pragma unroll
+                    for (int r = 0; r < kFewRows; ++r) s[r][t] = __fmaf_rn(q[r], e, s[r][t]);
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            float z[kFewRows], top = run[t].top;
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) {
+                float sum = s[r][t];
+#pragma unroll
+                for (int o = 16; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, o));
+                if (v + r == y[t] && lane == 0) a.target_logit[t] = sum;
+                z[r] = v + r == y[t] || v + r >= a.V ? -INFINITY : sum;
+                top = fmaxf(top, __fmul_rn(z[r], kLog2E));
+            }
+            const float from = top == -INFINITY ? 0.0f : -top;
+            float sum = __fmul_rn(run[t].sum, ex2(__fadd_rn(run[t].top, from)));
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) sum = __fadd_rn(sum, ex2(__fmaf_rn(z[r], kLog2E, from)));
+            run[t] = {top, sum};
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        if (lane == 0) joined[warp][t] = make_float2(run[t].top, run[t].sum);
+    __syncthreads();
+    if (threadIdx.x < T) {
+        float2 r = joined[0][threadIdx.x];
+        for (int w = 1; w < kFewWarps; ++w) r = joined_stats(r, joined[w][threadIdx.x]);
+        a.parts[int64_t(blockIdx.x) * T + threadIdx.x] = r;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -537,56 +724,72 @@ __global__ void __launch_bounds__(1024) join_stats_kernel(const float2 *parts, i
     wait_for_predecessor();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t t = blockIdx.x * 32 + lane;
-    // (a part that has no columns is (-infinity, 0))
-    auto joined = [](float2 a, float2 b) {
-        const float top = fmaxf(a.x, b.x);
-        const float x = a.x == -INFINITY && a.y == 0.0f ? 0.0f : __fmul_rn(a.y, ex2(__fadd_rn(a.x, -top)));
-        const float y = b.x == -INFINITY && b.y == 0.0f ? 0.0f : __fmul_rn(b.y, ex2(__fadd_rn(b.x, -top)));
-        return make_float2(top, __fadd_rn(x, y));
-    };
     float2 r = make_float2(-INFINITY, 0.0f);
     if (t < T)
 #pragma unroll 4
-        for (int32_t p = warp; p < count; p += 32) r = joined(r, parts[int64_t(p) * T + t]);
+        for (int32_t p = warp; p < count; p += 32) r = joined_stats(r, parts[int64_t(p) * T + t]);
     row[warp][lane] = r;
     __syncthreads();
     r = row[lane][warp];  // warp w has token w
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) {
         const float2 other = make_float2(__shfl_xor_sync(kFull, r.x, o), __shfl_xor_sync(kFull, r.y, o));
-        r = lane & o ? joined(other, r) : joined(r, other);
+        r = lane & o ? joined_stats(other, r) : joined_stats(r, other);
     }
     const int32_t at = blockIdx.x * 32 + warp;
     if (lane != 0 || at >= T) return;
-    const float l = __fmul_rn(__fadd_rn(r.x, log2f(r.y)), kLn2);
-    if (lse) lse[at] = l;
-    if (losses) losses[at] = target_of(targets, wide, V, at) >= 0 ? __fadd_rn(l, -target_logit[at]) : 0.0f;
+    if (target_of(targets, wide, V, at) < 0) {
+        if (lse) lse[at] = __fmul_rn(__fadd_rn(r.x, log2f(r.y)), kLn2);
+        if (losses) losses[at] = 0.0f;
+        return;
+    }
+    // log2 of the others' sum over the target's exponential (-infinity if there are none)
+    const float s = target_logit[at];
+    const float more = r.y == 0.0f ? -INFINITY : __fadd_rn(__fmaf_rn(-s, kLog2E, r.x), log2f(r.y));
+    const float loss = __fadd_rn(more > 0.0f ? __fmul_rn(more, kLn2) : 0.0f, log1pf(exp2f(-fabsf(more))));
+    if (lse) lse[at] = __fadd_rn(s, loss);
+    if (losses) losses[at] = loss;
 }
 
 // A matrix with rows that start on 16 bytes, from one whose rows may start
-// anywhere.  Rows whose target is padding become 0 (targets may be NULL).
-__global__ void __launch_bounds__(256) lay_out_kernel(const uint16_t *src, int64_t ld, int64_t rows, int32_t cols,
-                                                      const void *targets, int wide, int32_t V, uint16_t *dst,
-                                                      int32_t ld_dst, int vec) {
+// anywhere.  With targets, of which each row has one: rows whose target is padding
+// become 0, and the others' products with their target's row of w go to
+// target_logit.
+struct LayOut {
+    const uint16_t *src;
+    int64_t ld, rows;
+    int32_t cols, ld_dst;
+    uint16_t *dst;
+    int32_t vec;             // rows of src start on 16 bytes
+    const void *targets;     // or NULL
+    const uint16_t *w;
+    int64_t ld_w;
+    int32_t wide, V, vec_w;
+    float *target_logit;
+};
+
+__global__ void __launch_bounds__(256) lay_out_kernel(const LayOut a) {
     wait_for_predecessor();
-    const int32_t chunks = ld_dst / 8;
-    const int64_t n = rows * chunks;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
-        const int64_t r = i / chunks;
-        const int32_t c = int32_t(i - r * chunks) * 8;
-        uint4 q = make_uint4(0u, 0u, 0u, 0u);
-        if (targets == nullptr || target_of(targets, wide, V, r) >= 0) {
-            const uint16_t *p = src + r * ld + c;
-            if (vec && c + 8 <= cols) {
-                q = ld_stream_u4(p);
-            } else {
+    const int lane = threadIdx.x & 31;
+    for (int64_t r = (int64_t(blockIdx.x) * 256 + threadIdx.x) >> 5; r < a.rows; r += int64_t(gridDim.x) * 8) {
+        const int32_t y = a.targets ? target_of(a.targets, a.wide, a.V, r) : 0;
+        const uint16_t *p = a.src + r * a.ld;
+        uint16_t *to = a.dst + r * a.ld_dst;
+        for (int32_t c = 8 * lane; c < a.ld_dst; c += 256) {
+            uint4 q = make_uint4(0u, 0u, 0u, 0u);
+            if (y >= 0 && a.vec && c + 8 <= a.cols) {
+                q = __ldg(reinterpret_cast<const uint4 *>(p + c));
+            } else if (y >= 0) {
                 uint32_t w[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) w[k] = c + k < cols ? p[k] : 0u;
+                for (int k = 0; k < 8; ++k) w[k] = c + k < a.cols ? p[c + k] : 0u;
                 q = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
             }
+            *reinterpret_cast<uint4 *>(to + c) = q;
         }
-        *reinterpret_cast<uint4 *>(dst + r * ld_dst + c) = q;
+        if (a.targets == nullptr || y < 0) continue;
+        const float s = row_dot(p, a.w + y * a.ld_w, a.cols, a.vec && a.vec_w, lane);
+        if (lane == 0) a.target_logit[r] = s;
     }
 }
 
@@ -667,6 +870,18 @@ struct Layout {
     }
 };
 
+int64_t few_grid(const CrossEntropy &c);
+
+struct FewLayout {
+    int64_t parts, target_logit, bytes;
+    explicit FewLayout(const CrossEntropy &c) {
+        Layout l;
+        parts = l.take(few_grid(c) * c.T * int64_t(sizeof(float2)));
+        target_logit = l.take(c.T * 4);
+        bytes = l.bytes;
+    }
+};
+
 struct Forward {
     int64_t parts, target_logit, x, w, bytes;
     explicit Forward(const CrossEntropy &c) {
@@ -692,13 +907,14 @@ int64_t piece_of(const CrossEntropy &c) {
 }
 
 struct Backward {
-    int64_t x, w, d, dx, bytes;
+    int64_t x, w, target_logit, d, dx, bytes;
     int64_t piece, split, ld_dx;
     explicit Backward(const CrossEntropy &c) {
         Layout l;
         const int64_t ld = ceil_div(c.D, 8) * 16;
         x = l.take(c.T * ld);
         w = aligned(c.w, c.ld_w) ? -1 : l.take(c.V * ld);
+        target_logit = l.take(c.T * 4);
         piece = piece_of(c);
         d = l.take(c.T * piece * 2);
         // dx has few tiles where tokens are few, and its K is the vocabulary
@@ -711,12 +927,22 @@ struct Backward {
     }
 };
 
+// `mask`: src is its x, whose padding tokens become 0; the targets' logits go to
+// target_logit.
 cudaError_t lay_out(const uint16_t *src, int64_t ld, int64_t rows, int64_t cols, const CrossEntropy *mask,
-                    uint16_t *dst, cudaStream_t stream) {
-    const int64_t ld_dst = ceil_div(cols, 8) * 8, ctas = ceil_div(rows * ld_dst / 8, 256);
-    return launch_after(lay_out_kernel, dim3(uint32_t(ctas < 16 * kSms ? ctas : 16 * kSms)), dim3(256), 0, stream, 1,
-                        src, ld, rows, int32_t(cols), mask ? mask->targets : nullptr, mask && mask->wide ? 1 : 0,
-                        int32_t(mask ? mask->V : 0), dst, int32_t(ld_dst), aligned(src, ld) ? 1 : 0);
+                    float *target_logit, uint16_t *dst, cudaStream_t stream) {
+    LayOut a = {src, ld, rows, int32_t(cols), int32_t(ceil_div(cols, 8) * 8), dst, aligned(src, ld)};
+    if (mask) {
+        a.targets = mask->targets;
+        a.w = mask->w;
+        a.ld_w = mask->ld_w;
+        a.wide = mask->wide;
+        a.V = int32_t(mask->V);
+        a.vec_w = aligned(mask->w, mask->ld_w);
+        a.target_logit = target_logit;
+    }
+    const int64_t ctas = ceil_div(rows, 8);
+    return launch_after(lay_out_kernel, dim3(uint32_t(ctas < 16 * kSms ? ctas : 16 * kSms)), dim3(256), 0, stream, 1, a);
 }
 
 Job job_of(int64_t rows_i, int64_t rows_j, int64_t K) {
@@ -730,11 +956,62 @@ Job job_of(int64_t rows_i, int64_t rows_j, int64_t K) {
     return j;
 }
 
+// Few tokens?  Their fp32 values fit shared memory twice per SM.
+bool few_tokens(const CrossEntropy &c) { return c.T <= 4 && c.T * (c.D + 7) * 4 <= 96 * 1024; }
+
+int64_t few_grid(const CrossEntropy &c) {
+    const int64_t ctas = ceil_div(c.V, kFewWarps * kFewRows);
+    return ctas < 2 * kSms ? ctas : 2 * kSms;
+}
+
+template <int T, bool VEC>
+cudaError_t run_few(const Few &a, uint32_t grid, size_t smem, cudaStream_t stream) {
+    static std::atomic<uint64_t> prepared{0};
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (device & 63);
+    if (device > 63 || !(prepared.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(few_kernel<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+        if (e != cudaSuccess) return e;
+        prepared.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return launch_after(few_kernel<T, VEC>, dim3(grid), dim3(kFewThreads), smem, stream, 1, a);
+}
+
+cudaError_t join_stats(const CrossEntropy &c, const float2 *parts, int32_t count, int64_t t0, int64_t tokens,
+                       const float *target_logit, cudaStream_t stream) {
+    return launch_after(join_stats_kernel, dim3(uint32_t(ceil_div(tokens, 32))), dim3(1024), 0, stream, 1, parts, count,
+                        int32_t(tokens), target_logit,
+                        static_cast<const void *>(static_cast<const char *>(c.targets) + t0 * (c.wide ? 8 : 4)),
+                        c.wide ? 1 : 0, int32_t(c.V), c.losses ? c.losses + t0 : nullptr, c.lse ? c.lse + t0 : nullptr);
+}
+
+cudaError_t launch_few(const CrossEntropy &c, cudaStream_t stream) {
+    const FewLayout f(c);
+    char *const ws = static_cast<char *>(c.workspace);
+    const Few a = {c.x, c.w, c.ld_x, c.ld_w, int32_t(c.V), int32_t(c.D), c.targets, c.wide,
+                   reinterpret_cast<float2 *>(ws + f.parts), reinterpret_cast<float *>(ws + f.target_logit)};
+    const uint32_t grid = uint32_t(few_grid(c));
+    const size_t smem = size_t(c.T) * ((c.D + 7) / 8 * 8) * 4;
+    const bool vec = aligned(c.w, c.ld_w);
+    cudaError_t e;
+    switch (c.T) {
+        case 1: e = vec ? run_few<1, true>(a, grid, smem, stream) : run_few<1, false>(a, grid, smem, stream); break;
+        case 2: e = vec ? run_few<2, true>(a, grid, smem, stream) : run_few<2, false>(a, grid, smem, stream); break;
+        case 3: e = vec ? run_few<3, true>(a, grid, smem, stream) : run_few<3, false>(a, grid, smem, stream); break;
+        default: e = vec ? run_few<4, true>(a, grid, smem, stream) : run_few<4, false>(a, grid, smem, stream); break;
+    }
+    if (e != cudaSuccess) return e;
+    return join_stats(c, a.parts, int32_t(grid), 0, c.T, a.target_logit, stream);
+}
+
 }  // namespace
 
-int64_t cross_entropy_workspace(const CrossEntropy &c) { return Forward(c).bytes; }
+int64_t cross_entropy_workspace(const CrossEntropy &c) { return few_tokens(c) ? FewLayout(c).bytes : Forward(c).bytes; }
 
 cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
+    if (few_tokens(c)) return launch_few(c, stream);
     const Forward f(c);
     char *const ws = static_cast<char *>(c.workspace);
     Bf16Matrix x = {c.x, c.ld_x, c.T, c.D}, w = {c.w, c.ld_w, c.V, c.D};
@@ -742,13 +1019,13 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
     if (f.x >= 0) {
         x.p = reinterpret_cast<uint16_t *>(ws + f.x);
         x.ld = ceil_div(c.D, 8) * 8;
-        e = lay_out(c.x, c.ld_x, c.T, c.D, nullptr, reinterpret_cast<uint16_t *>(ws + f.x), stream);
+        e = lay_out(c.x, c.ld_x, c.T, c.D, nullptr, nullptr, reinterpret_cast<uint16_t *>(ws + f.x), stream);
         if (e != cudaSuccess) return e;
     }
     if (f.w >= 0) {
         w.p = reinterpret_cast<uint16_t *>(ws + f.w);
         w.ld = ceil_div(c.D, 8) * 8;
-        e = lay_out(c.w, c.ld_w, c.V, c.D, nullptr, reinterpret_cast<uint16_t *>(ws + f.w), stream);
+        e = lay_out(c.w, c.ld_w, c.V, c.D, nullptr, nullptr, reinterpret_cast<uint16_t *>(ws + f.w), stream);
         if (e != cudaSuccess) return e;
     }
     CUtensorMap maps[4];
@@ -768,11 +1045,14 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
         a.V = int32_t(c.V);
         a.parts = reinterpret_cast<float2 *>(ws + f.parts);
         a.target_logit = reinterpret_cast<float *>(ws + f.target_logit);
+        a.x = c.x + t0 * c.ld_x;
+        a.w = c.w;
+        a.ld_x = c.ld_x;
+        a.ld_w = c.ld_w;
+        a.D = int32_t(c.D);
+        a.vec = aligned(c.x, c.ld_x) && aligned(c.w, c.ld_w);
         if ((e = run<kStats>(maps, a, stream)) != cudaSuccess) return e;
-        e = launch_after(join_stats_kernel, dim3(uint32_t(ceil_div(some.rows, 32))), dim3(1024), 0, stream, 1,
-                         static_cast<const float2 *>(a.parts), 2 * a.job[0].tiles_j, int32_t(some.rows),
-                         static_cast<const float *>(a.target_logit), a.targets, a.wide, a.V,
-                         c.losses ? c.losses + t0 : nullptr, c.lse ? c.lse + t0 : nullptr);
+        e = join_stats(c, a.parts, 2 * a.job[0].tiles_j, t0, some.rows, a.target_logit, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -785,13 +1065,14 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
     char *const ws = static_cast<char *>(c.workspace);
     // x with its padding tokens 0, so that nothing that they hold reaches dw
     const Bf16Matrix x = {reinterpret_cast<uint16_t *>(ws + f.x), ceil_div(c.D, 8) * 8, c.T, c.D};
-    cudaError_t e = lay_out(c.x, c.ld_x, c.T, c.D, &c, reinterpret_cast<uint16_t *>(ws + f.x), stream);
+    float *const target_logit = reinterpret_cast<float *>(ws + f.target_logit);
+    cudaError_t e = lay_out(c.x, c.ld_x, c.T, c.D, &c, target_logit, reinterpret_cast<uint16_t *>(ws + f.x), stream);
     if (e != cudaSuccess) return e;
     Bf16Matrix w = {c.w, c.ld_w, c.V, c.D};
     if (f.w >= 0) {
         w.p = reinterpret_cast<uint16_t *>(ws + f.w);
         w.ld = x.ld;
-        e = lay_out(c.w, c.ld_w, c.V, c.D, nullptr, reinterpret_cast<uint16_t *>(ws + f.w), stream);
+        e = lay_out(c.w, c.ld_w, c.V, c.D, nullptr, nullptr, reinterpret_cast<uint16_t *>(ws + f.w), stream);
         if (e != cudaSuccess) return e;
     }
     const Bf16Matrix d = {reinterpret_cast<uint16_t *>(ws + f.d), f.piece, c.T, f.piece};
@@ -818,6 +1099,7 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
         a.targets = c.targets;
         a.wide = c.wide;
         a.V = int32_t(c.V);
+        a.target_logit = target_logit;
         a.lse = c.lse_in;
         a.dlosses = c.dlosses;
         a.dloss = c.dloss;
