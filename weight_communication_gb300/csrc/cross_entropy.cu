@@ -38,6 +38,8 @@
 #include "wc_device.cuh"
 #include "wc_internal.h"
 #include "wc_launch.cuh"
+#include "wc_rows.cuh"
+#include "wc_store.cuh"
 #include "wc_tcgen05.cuh"
 #include "wc_wait.cuh"
 
@@ -64,10 +66,6 @@ constexpr int kStages = 6;
 constexpr int kBuffers = 2;                 // tiles of sums in tensor memory
 constexpr int kEpilogueWarps = 8, kProducer = 8, kMma = 9, kTargets = 10, kWarps = 12;
 constexpr int kThreads = kWarps * 32;
-// Epilogue staging of a warp: 64 bytes of each of its 32 rows, 80 bytes apart to
-// keep 16-byte accesses off one another's banks.
-constexpr int kPitch = 80;
-constexpr int kStagingBytes = 32 * kPitch;
 constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * kStagingBytes + 1024;
 
 constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
@@ -105,7 +103,7 @@ struct Args {
     float *target_logit;    // [rows_i]
     const uint16_t *x, *w;  // for it, as they were given
     int64_t ld_x, ld_w;
-    int32_t D, vec;         // vec: rows of x and w start on 16 bytes
+    int32_t D;
     const float *lse, *dlosses;
     float dloss;
 };
@@ -128,27 +126,50 @@ __device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float sum)
     return sum;
 }
 
-// A warp's sum over D of x[d] w[d], in fp32, the same in every lane.
-__device__ __forceinline__ float row_dot(const uint16_t *x, const uint16_t *w, int32_t D, int vec, int lane) {
-    float s[2] = {0.0f, 0.0f};
-    if (vec) {
-        int32_t d = 8 * lane;
-        for (; d + 264 <= D; d += 512) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x + d)), b = __ldg(reinterpret_cast<const uint4 *>(w + d));
-            const uint4 c = __ldg(reinterpret_cast<const uint4 *>(x + d + 256)), e = __ldg(reinterpret_cast<const uint4 *>(w + d + 256));
-            s[0] = dot8(a, b, s[0]);
-            s[1] = dot8(c, e, s[1]);
+// A row of a bf16 matrix that starts on any value.
+struct Row {
+    const uint16_t *p, *end;  // of the row, of the matrix
+    int32_t D;
+    // values d .. d + 7, those past the row's end 0
+    __device__ __forceinline__ uint4 at(int32_t d) const {
+        const uint16_t *q = p + d;
+        if (d + 8 <= D && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) return __ldg(reinterpret_cast<const uint4 *>(q));
+        uint32_t w[4];
+        if (d + 8 <= D && end - q >= 16) {  // (the second chunk ends inside the matrix)
+            uint32_t t[8];
+            load_chunks(q, t);
+            shift_words(q, t, w);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t lo = d + 2 * k < D ? q[2 * k] : 0u, hi = d + 2 * k + 1 < D ? q[2 * k + 1] : 0u;
+                w[k] = lo | hi << 16;
+            }
         }
-        for (; d < D; d += 256) {
-            if (d + 8 <= D) s[0] = dot8(__ldg(reinterpret_cast<const uint4 *>(x + d)), __ldg(reinterpret_cast<const uint4 *>(w + d)), s[0]);
-            else
-                for (int32_t c = d; c < D; ++c) s[0] = __fmaf_rn(bf16_bits_to_f32(x[c]), bf16_bits_to_f32(w[c]), s[0]);
-        }
-    } else {
-#pragma unroll 8
-        for (int32_t d = lane; d < D; d += 32) s[0] = __fmaf_rn(bf16_bits_to_f32(x[d]), bf16_bits_to_f32(w[d]), s[0]);
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    float sum = __fadd_rn(s[0], s[1]);
+};
+
+__device__ __forceinline__ Row row_of(const uint16_t *p, int64_t ld, int64_t rows, int32_t D, int64_t r) {
+    return {p + r * ld, p + (rows - 1) * ld + D, D};
+}
+
+// A warp's sum over D of x[d] w[d], in fp32, the same in every lane.
+__device__ __forceinline__ float row_dot(const Row &x, const Row &w, int lane) {
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int32_t d = 8 * lane;
+    for (; d + 768 < x.D; d += 1024) {
+        uint4 a[4], b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            a[k] = x.at(d + 256 * k);
+            b[k] = w.at(d + 256 * k);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] = dot8(a[k], b[k], s[k]);
+    }
+    for (; d < x.D; d += 256) s[0] = dot8(x.at(d), w.at(d), s[0]);
+    float sum = __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, o));
     return sum;
@@ -264,7 +285,7 @@ __device__ __forceinline__ void store_staged(const uint8_t *staging, char *base,
     for (int r = lane >> 2; r < 32; r += 8)
         if (r < rows)
             *reinterpret_cast<uint4 *>(base + r * pitch + seg) =
-                *reinterpret_cast<const uint4 *>(staging + r * kPitch + seg);
+                *reinterpret_cast<const uint4 *>(staging + r * kStagingPitch + seg);
 }
 
 __device__ __forceinline__ void stage_bf16(uint8_t *staging, const float (&x)[32], int lane) {
@@ -273,7 +294,7 @@ __device__ __forceinline__ void stage_bf16(uint8_t *staging, const float (&x)[32
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) w[k] = f32x2_to_bf16x2_bits(x[8 * q + 2 * k], x[8 * q + 2 * k + 1]);
-        *reinterpret_cast<uint4 *>(staging + lane * kPitch + q * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(staging + lane * kStagingPitch + q * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -289,69 +310,60 @@ __device__ __forceinline__ void store_sums(const Job &a, int32_t part, const flo
         __syncwarp();
         return;
     }
-    // 16 columns at a time, four to a lane
+    if (a.out_bf16 && a.add == nullptr) {
+        stage_bf16(staging, x, lane);
+        __syncwarp();
+        store_pass_bf16(static_cast<char *>(a.out) + (int64_t(row0) * a.ld_out + col0) * 2, a.ld_out, staging, rows,
+                        min(cols, 32), lane);
+        __syncwarp();
+        return;
+    }
+    // 16 columns of fp32 at a time
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<float4 *>(staging + lane * kPitch + q * 16) =
+            *reinterpret_cast<float4 *>(staging + lane * kStagingPitch + q * 16) =
                 make_float4(x[16 * h + 4 * q], x[16 * h + 4 * q + 1], x[16 * h + 4 * q + 2], x[16 * h + 4 * q + 3]);
         __syncwarp();
-        const int c = 16 * h + 4 * (lane & 3), left = cols - c;
-#pragma unroll 2
-        for (int r = lane >> 2; r < 32; r += 8) {
-            if (r >= rows || left <= 0) continue;
-            const float4 v = *reinterpret_cast<const float4 *>(staging + r * kPitch + (lane & 3) * 16);
-            float y[4] = {v.x, v.y, v.z, v.w};
-            const int64_t at = part * a.split_out + (row0 + r) * a.ld_out + col0 + c;
-            const int64_t from = part * a.split_add + (row0 + r) * a.ld_add + col0 + c;
-            const bool whole = a.vec && left >= 4;
-            if (a.add) {
-                if (a.add_bf16) {
-                    const uint16_t *p = static_cast<const uint16_t *>(a.add) + from;
-                    if (whole) {
-                        const uint2 o = *reinterpret_cast<const uint2 *>(p);
-                        y[0] = __fadd_rn(__uint_as_float(o.x << 16), y[0]);
-                        y[1] = __fadd_rn(__uint_as_float(o.x & 0xFFFF0000u), y[1]);
-                        y[2] = __fadd_rn(__uint_as_float(o.y << 16), y[2]);
-                        y[3] = __fadd_rn(__uint_as_float(o.y & 0xFFFF0000u), y[3]);
-                    } else {
+        const int left = cols - 16 * h;
+        const int64_t at = part * a.split_out + int64_t(row0) * a.ld_out + col0 + 16 * h;
+        if (!a.out_bf16 && !a.add_bf16 && a.vec && left >= 16) {
+            float *out = static_cast<float *>(a.out) + at + 4 * (lane & 3);
+            const float *add = static_cast<const float *>(a.add);
+            if (add) add += part * a.split_add + int64_t(row0) * a.ld_add + col0 + 16 * h + 4 * (lane & 3);
+            float4 old[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (k < left) y[k] = __fadd_rn(bf16_bits_to_f32(p[k]), y[k]);
-                    }
-                } else {
-                    const float *p = static_cast<const float *>(a.add) + from;
-                    if (whole) {
-                        const float4 o = *reinterpret_cast<const float4 *>(p);
-                        y[0] = __fadd_rn(o.x, y[0]);
-                        y[1] = __fadd_rn(o.y, y[1]);
-                        y[2] = __fadd_rn(o.z, y[2]);
-                        y[3] = __fadd_rn(o.w, y[3]);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (k < left) y[k] = __fadd_rn(p[k], y[k]);
-                    }
-                }
+            for (int k = 0; k < 4; ++k) {
+                const int r = (lane >> 2) + 8 * k;
+                old[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (add && r < rows) old[k] = *reinterpret_cast<const float4 *>(add + r * a.ld_add);
             }
-            if (a.out_bf16) {
-                uint16_t *p = static_cast<uint16_t *>(a.out) + at;
-                if (whole) {
-                    *reinterpret_cast<uint2 *>(p) = make_uint2(f32x2_to_bf16x2_bits(y[0], y[1]), f32x2_to_bf16x2_bits(y[2], y[3]));
-                } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < left) p[k] = f32_to_bf16_bits(y[k]);
-                }
-            } else {
-                float *p = static_cast<float *>(a.out) + at;
-                if (whole) {
-                    *reinterpret_cast<float4 *>(p) = make_float4(y[0], y[1], y[2], y[3]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < left) p[k] = y[k];
+            for (int k = 0; k < 4; ++k) {
+                const int r = (lane >> 2) + 8 * k;
+                float4 v = *reinterpret_cast<const float4 *>(staging + r * kStagingPitch + (lane & 3) * 16);
+                if (add) v = make_float4(__fadd_rn(old[k].x, v.x), __fadd_rn(old[k].y, v.y), __fadd_rn(old[k].z, v.z),
+                                         __fadd_rn(old[k].w, v.w));
+                if (r < rows) *reinterpret_cast<float4 *>(out + r * a.ld_out) = v;
+            }
+        } else if (a.add == a.out && a.out_bf16) {
+            store_pass_f32<true>(static_cast<uint16_t *>(a.out) + at, a.ld_out, staging, rows, left, lane);
+        } else if (a.add == a.out) {
+            store_pass_f32<true>(static_cast<float *>(a.out) + at, a.ld_out, staging, rows, left, lane);
+        } else if (a.add == nullptr) {
+            store_pass_f32<false>(static_cast<float *>(a.out) + at, a.ld_out, staging, rows, left, lane);
+        } else {  // fp32 sums of earlier pieces, then to out
+            const float *add = static_cast<const float *>(a.add) + part * a.split_add + int64_t(row0) * a.ld_add + col0 + 16 * h;
+            const int c = lane & 15;
+            if (c < left) {
+#pragma unroll 8
+                for (int r = lane >> 4; r < 32; r += 2) {
+                    if (r >= rows) break;
+                    const float y = __fadd_rn(add[r * a.ld_add + c],
+                                              *reinterpret_cast<const float *>(staging + r * kStagingPitch + 4 * c));
+                    if (a.out_bf16) static_cast<uint16_t *>(a.out)[at + r * a.ld_out + c] = f32_to_bf16_bits(y);
+                    else static_cast<float *>(a.out)[at + r * a.ld_out + c] = y;
                 }
             }
         }
@@ -472,9 +484,11 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
             }
         }
         // No product may be in flight when the tensor memory is freed.
-        if (lead) mma_commit<true>(smem_of(&drained), 1);
-        __syncwarp();
-        mbar_wait(smem_of(&drained), 0);
+        if (first < units) {
+            if (lead) mma_commit<true>(smem_of(&drained), 1);
+            __syncwarp();
+            mbar_wait(smem_of(&drained), 0);
+        }
     } else if (warp < kEpilogueWarps) {
         const int group = warp >> 2;
         uint8_t *const staging = dynamic_smem + (stages - smem_of(dynamic_smem)) + kStages * kStageBytes + warp * kStagingBytes;
@@ -566,13 +580,20 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
         }
     }
 
-    if (MODE == kStats && warp >= kTargets) {
-        for (int32_t t = int32_t(blockIdx.x) + int32_t(gridDim.x) * (warp - kTargets); t < a.job[0].rows_i;
-             t += int32_t(gridDim.x) * (kWarps - kTargets)) {
-            const int32_t y = target_of(a.targets, a.wide, a.V, t);
-            if (y < 0) continue;
-            const float s = row_dot(a.x + t * a.ld_x, a.w + y * a.ld_w, a.D, a.vec, lane);
-            if (lane == 0) a.target_logit[t] = s;
+    if (MODE == kStats) {
+        // the targets' logits: two warps of each CTA, ten of one without tiles
+        const int32_t busy = min(int32_t(gridDim.x), 2 * units), cta = int32_t(blockIdx.x);
+        const bool idle = cta >= busy;
+        const int32_t of_cta = warp >= kTargets ? warp - kTargets : idle && warp < kEpilogueWarps ? warp + 2 : -1;
+        if (of_cta >= 0) {
+            const int32_t mine = idle ? 2 * busy + 10 * (cta - busy) + of_cta : 2 * cta + of_cta;
+            const int32_t all = 2 * busy + 10 * (int32_t(gridDim.x) - busy), T = a.job[0].rows_i;
+            for (int32_t t = mine; t < T; t += all) {
+                const int32_t y = target_of(a.targets, a.wide, a.V, t);
+                if (y < 0) continue;
+                const float s = row_dot(row_of(a.x, a.ld_x, T, a.D, t), row_of(a.w, a.ld_w, a.V, a.D, y), lane);
+                if (lane == 0) a.target_logit[t] = s;
+            }
         }
     }
 
@@ -626,29 +647,24 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
     const int64_t step = int64_t(gridDim.x) * kFewWarps * kFewRows;
     for (int64_t v = (int64_t(blockIdx.x) * kFewWarps + warp) * kFewRows; v < a.V; v += step) {
         float s[kFewRows][T];
-        const uint16_t *row[kFewRows];
+        Row row[kFewRows];
 #pragma unroll
         for (int r = 0; r < kFewRows; ++r) {
             // (rows past the last are read as the last, and dropped below)
-            row[r] = a.w + (v + r < a.V ? v + r : a.V - 1) * a.ld_w;
+            row[r] = row_of(a.w, a.ld_w, a.V, a.D, v + r < a.V ? v + r : a.V - 1);
 #pragma unroll
             for (int t = 0; t < T; ++t) s[r][t] = 0.0f;
         }
-        if (VEC) {
-#pragma unroll 4
+        {
+#pragma unroll VEC ? 4 : 2
             for (int32_t d = 8 * lane; d < pitch; d += 256) {
                 uint4 q[kFewRows];
-                if (d + 8 <= a.D) {
+                if (VEC && d + 8 <= a.D) {
 #pragma unroll
-                    for (int r = 0; r < kFewRows; ++r) q[r] = ld_stream_u4(row[r] + d);
-                } else {  // the row's end
+                    for (int r = 0; r < kFewRows; ++r) q[r] = ld_stream_u4(row[r].p + d);
+                } else {
 #pragma unroll
-                    for (int r = 0; r < kFewRows; ++r) {
-                        uint32_t e[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) e[k] = d + k < a.D ? row[r][d + k] : 0u;
-                        q[r] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-                    }
+                    for (int r = 0; r < kFewRows; ++r) q[r] = row[r].at(d);
                 }
 #pragma unroll
                 for (int t = 0; t < T; ++t) {
@@ -665,19 +681,6 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
                         s[r][t] = __fmaf_rn(__uint_as_float(q[r].w << 16), hi.z, s[r][t]);
                         s[r][t] = __fmaf_rn(__uint_as_float(q[r].w & 0xFFFF0000u), hi.w, s[r][t]);
                     }
-                }
-            }
-        } else {
-#pragma unroll 4
-            for (int32_t d = lane; d < a.D; d += 32) {
-                float q[kFewRows];
-#pragma unroll
-                for (int r = 0; r < kFewRows; ++r) q[r] = bf16_bits_to_f32(row[r][d]);
-#pragma unroll
-                for (int t = 0; t < T; ++t) {
-                    const float e = tokens[t * pitch + d];
-#pragma unroll
-                    for (int r = 0; r < kFewRows; ++r) s[r][t] = __fmaf_rn(q[r], e, s[r][t]);
                 }
             }
         }
@@ -751,44 +754,48 @@ __global__ void __launch_bounds__(1024) join_stats_kernel(const float2 *parts, i
     if (losses) losses[at] = loss;
 }
 
-// A matrix with rows that start on 16 bytes, from one whose rows may start
-// anywhere.  With targets, of which each row has one: rows whose target is padding
-// become 0, and the others' products with their target's row of w go to
-// target_logit.
+// A matrix [rows][D] with rows that start on 16 bytes, from one whose rows may
+// start anywhere.
 struct LayOut {
-    const uint16_t *src;
+    const uint16_t *src;     // NULL: nothing to do
     int64_t ld, rows;
-    int32_t cols, ld_dst;
     uint16_t *dst;
-    int32_t vec;             // rows of src start on 16 bytes
-    const void *targets;     // or NULL
-    const uint16_t *w;
-    int64_t ld_w;
-    int32_t wide, V, vec_w;
-    float *target_logit;
 };
 
-__global__ void __launch_bounds__(256) lay_out_kernel(const LayOut a) {
+// x and w laid out, a warp per row.  With target_logit, x's rows whose target is
+// padding become 0, and the others' products with their target's row of w go there.
+struct LayOuts {
+    LayOut x, w;
+    int32_t D, ctas_x;       // CTAs at work on x
+    const void *targets;
+    const uint16_t *given_w;
+    int64_t ld_w;
+    int32_t wide, V;
+    float *target_logit;     // or NULL
+};
+
+__global__ void __launch_bounds__(256) lay_out_kernel(const LayOuts a) {
     wait_for_predecessor();
     const int lane = threadIdx.x & 31;
-    for (int64_t r = (int64_t(blockIdx.x) * 256 + threadIdx.x) >> 5; r < a.rows; r += int64_t(gridDim.x) * 8) {
-        const int32_t y = a.targets ? target_of(a.targets, a.wide, a.V, r) : 0;
-        const uint16_t *p = a.src + r * a.ld;
-        uint16_t *to = a.dst + r * a.ld_dst;
-        for (int32_t c = 8 * lane; c < a.ld_dst; c += 256) {
-            uint4 q = make_uint4(0u, 0u, 0u, 0u);
-            if (y >= 0 && a.vec && c + 8 <= a.cols) {
-                q = __ldg(reinterpret_cast<const uint4 *>(p + c));
-            } else if (y >= 0) {
-                uint32_t w[8];
+    const bool of_x = int32_t(blockIdx.x) < a.ctas_x;
+    const LayOut &m = of_x ? a.x : a.w;
+    const int64_t cta = of_x ? blockIdx.x : blockIdx.x - a.ctas_x, ctas = of_x ? a.ctas_x : gridDim.x - a.ctas_x;
+    const int32_t ld = (a.D + 7) & ~7;
+    for (int64_t r = cta * 8 + (threadIdx.x >> 5); r < m.rows; r += ctas * 8) {
+        const int32_t y = of_x && a.target_logit ? target_of(a.targets, a.wide, a.V, r) : 0;
+        const Row row = row_of(m.src, m.ld, m.rows, a.D, r);
+        uint16_t *to = m.dst + r * ld;
+        int32_t c = 8 * lane;
+        for (; c + 768 < ld; c += 1024) {
+            uint4 q[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) w[k] = c + k < a.cols ? p[c + k] : 0u;
-                q = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-            }
-            *reinterpret_cast<uint4 *>(to + c) = q;
+            for (int k = 0; k < 4; ++k) q[k] = y < 0 ? make_uint4(0u, 0u, 0u, 0u) : row.at(c + 256 * k);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(to + c + 256 * k) = q[k];
         }
-        if (a.targets == nullptr || y < 0) continue;
-        const float s = row_dot(p, a.w + y * a.ld_w, a.cols, a.vec && a.vec_w, lane);
+        for (; c < ld; c += 256) *reinterpret_cast<uint4 *>(to + c) = y < 0 ? make_uint4(0u, 0u, 0u, 0u) : row.at(c);
+        if (!of_x || a.target_logit == nullptr || y < 0) continue;
+        const float s = row_dot(row, row_of(a.given_w, a.ld_w, a.V, a.D, y), lane);
         if (lane == 0) a.target_logit[r] = s;
     }
 }
@@ -850,7 +857,9 @@ cudaError_t run(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
     }
     for (int k = 0; k < 2; ++k) a.units[k] = a.job[k].tiles_i * a.job[k].tiles_j * a.job[k].split;
     const int64_t units = int64_t(a.units[0]) + (MODE == kProducts ? a.units[1] : 0);
-    const uint32_t grid = 2 * uint32_t(units < kSms / 2 ? units : kSms / 2);
+    // (CTAs without tiles sum targets' logits, ten warps with one token at a time)
+    const int64_t more = MODE == kStats ? units + ceil_div(a.job[0].rows_i, 20) : 0, pairs = units > more ? units : more;
+    const uint32_t grid = 2 * uint32_t(pairs < kSms / 2 ? pairs : kSms / 2);
     return launch_after(product_kernel<MODE>, dim3(grid), dim3(kThreads), kSmem, stream, 2, maps[0], maps[1],
                         maps[2], maps[3], a);
 }
@@ -927,22 +936,21 @@ struct Backward {
     }
 };
 
-// `mask`: src is its x, whose padding tokens become 0; the targets' logits go to
-// target_logit.
-cudaError_t lay_out(const uint16_t *src, int64_t ld, int64_t rows, int64_t cols, const CrossEntropy *mask,
-                    float *target_logit, uint16_t *dst, cudaStream_t stream) {
-    LayOut a = {src, ld, rows, int32_t(cols), int32_t(ceil_div(cols, 8) * 8), dst, aligned(src, ld)};
-    if (mask) {
-        a.targets = mask->targets;
-        a.w = mask->w;
-        a.ld_w = mask->ld_w;
-        a.wide = mask->wide;
-        a.V = int32_t(mask->V);
-        a.vec_w = aligned(mask->w, mask->ld_w);
-        a.target_logit = target_logit;
-    }
-    const int64_t ctas = ceil_div(rows, 8);
-    return launch_after(lay_out_kernel, dim3(uint32_t(ctas < 16 * kSms ? ctas : 16 * kSms)), dim3(256), 0, stream, 1, a);
+// x and w to the places given, each if it is not NULL; target_logit as above.
+cudaError_t lay_out(const CrossEntropy &c, uint16_t *x, uint16_t *w, float *target_logit, cudaStream_t stream) {
+    auto ctas = [](int64_t rows) { return int32_t(rows < 128 * kSms ? ceil_div(rows, 8) : 16 * kSms); };
+    LayOuts a = {};
+    if (x) a.x = {c.x, c.ld_x, c.T, x};
+    if (w) a.w = {c.w, c.ld_w, c.V, w};
+    a.D = int32_t(c.D);
+    a.ctas_x = ctas(a.x.rows);
+    a.targets = c.targets;
+    a.given_w = c.w;
+    a.ld_w = c.ld_w;
+    a.wide = c.wide;
+    a.V = int32_t(c.V);
+    a.target_logit = target_logit;
+    return launch_after(lay_out_kernel, dim3(uint32_t(a.ctas_x + ctas(a.w.rows))), dim3(256), 0, stream, 1, a);
 }
 
 Job job_of(int64_t rows_i, int64_t rows_j, int64_t K) {
@@ -1016,16 +1024,11 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
     char *const ws = static_cast<char *>(c.workspace);
     Bf16Matrix x = {c.x, c.ld_x, c.T, c.D}, w = {c.w, c.ld_w, c.V, c.D};
     cudaError_t e = cudaSuccess;
-    if (f.x >= 0) {
-        x.p = reinterpret_cast<uint16_t *>(ws + f.x);
-        x.ld = ceil_div(c.D, 8) * 8;
-        e = lay_out(c.x, c.ld_x, c.T, c.D, nullptr, nullptr, reinterpret_cast<uint16_t *>(ws + f.x), stream);
-        if (e != cudaSuccess) return e;
-    }
-    if (f.w >= 0) {
-        w.p = reinterpret_cast<uint16_t *>(ws + f.w);
-        w.ld = ceil_div(c.D, 8) * 8;
-        e = lay_out(c.w, c.ld_w, c.V, c.D, nullptr, nullptr, reinterpret_cast<uint16_t *>(ws + f.w), stream);
+    if (f.x >= 0) x = {reinterpret_cast<uint16_t *>(ws + f.x), ceil_div(c.D, 8) * 8, c.T, c.D};
+    if (f.w >= 0) w = {reinterpret_cast<uint16_t *>(ws + f.w), ceil_div(c.D, 8) * 8, c.V, c.D};
+    if (f.x >= 0 || f.w >= 0) {
+        e = lay_out(c, f.x >= 0 ? const_cast<uint16_t *>(x.p) : nullptr, f.w >= 0 ? const_cast<uint16_t *>(w.p) : nullptr,
+                    nullptr, stream);
         if (e != cudaSuccess) return e;
     }
     CUtensorMap maps[4];
@@ -1050,7 +1053,6 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
         a.ld_x = c.ld_x;
         a.ld_w = c.ld_w;
         a.D = int32_t(c.D);
-        a.vec = aligned(c.x, c.ld_x) && aligned(c.w, c.ld_w);
         if ((e = run<kStats>(maps, a, stream)) != cudaSuccess) return e;
         e = join_stats(c, a.parts, 2 * a.job[0].tiles_j, t0, some.rows, a.target_logit, stream);
         if (e != cudaSuccess) return e;
@@ -1066,15 +1068,11 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
     // x with its padding tokens 0, so that nothing that they hold reaches dw
     const Bf16Matrix x = {reinterpret_cast<uint16_t *>(ws + f.x), ceil_div(c.D, 8) * 8, c.T, c.D};
     float *const target_logit = reinterpret_cast<float *>(ws + f.target_logit);
-    cudaError_t e = lay_out(c.x, c.ld_x, c.T, c.D, &c, target_logit, reinterpret_cast<uint16_t *>(ws + f.x), stream);
-    if (e != cudaSuccess) return e;
     Bf16Matrix w = {c.w, c.ld_w, c.V, c.D};
-    if (f.w >= 0) {
-        w.p = reinterpret_cast<uint16_t *>(ws + f.w);
-        w.ld = x.ld;
-        e = lay_out(c.w, c.ld_w, c.V, c.D, nullptr, nullptr, reinterpret_cast<uint16_t *>(ws + f.w), stream);
-        if (e != cudaSuccess) return e;
-    }
+    if (f.w >= 0) w = {reinterpret_cast<uint16_t *>(ws + f.w), x.ld, c.V, c.D};
+    cudaError_t e = lay_out(c, const_cast<uint16_t *>(x.p), f.w >= 0 ? const_cast<uint16_t *>(w.p) : nullptr,
+                            target_logit, stream);
+    if (e != cudaSuccess) return e;
     const Bf16Matrix d = {reinterpret_cast<uint16_t *>(ws + f.d), f.piece, c.T, f.piece};
     CUtensorMap logits[4], products[4];
     if ((e = describe(&logits[0], x, false)) != cudaSuccess) return e;

@@ -13,9 +13,12 @@
 //
 // The weight's gradient is summed over rows in registers: a group has the same
 // columns in every row it works on.  Each group leaves its sums, which a second
-// launch adds in a fixed order.
+// launch adds in a fixed order.  Those sums leave few registers, so the rows to
+// come are brought to shared memory ahead of their turn, each thread's own values
+// by cp.async.
 //
 // Bound: HBM.
+#include <atomic>
 #include <type_traits>
 
 #include "wc_eight.cuh"
@@ -137,20 +140,54 @@ __global__ void __launch_bounds__(Shape<TPR, PIECES>::kThreads) rms_norm_kernel(
     }
 }
 
-// Row groups of the gradient's grid: what the GPU runs at once, and no more than rows.
-template <typename S>
-int64_t groups_of(int64_t rows) {
-    const int64_t most = int64_t(kSms) * (1024 / S::kThreads) * S::kRows;
-    const int64_t ctas = ((rows < most ? rows : most) + S::kRows - 1) / S::kRows;
-    return ctas * S::kRows;
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *to, const void *from) {
+    const uint32_t at = uint32_t(__cvta_generic_to_shared(to));
+    if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
 }
 
+// A row's values as one thread takes them: 16-byte words of dy and add, codes and
+// scale of each piece, and r.  In shared memory each of them lies by threads.
+template <typename T, int THREADS, int PIECES>
+struct Stage {
+    static constexpr int kWords = sizeof(T) / 2;  // 16-byte words of 8 values
+    uint4 dy[PIECES * kWords][THREADS], add[PIECES * kWords][THREADS];
+    uint2 codes[PIECES][THREADS];
+    float scale[PIECES][THREADS];
+    float r[THREADS];
+};
+
+// CTAs of the gradient that an SM holds at once, and the stages that then fit
+// its shared memory (fewer than two are of no use).
+template <typename T, typename S, int PIECES>
+struct Plan {
+    static constexpr bool kHalf = sizeof(T) == 2;
+    static constexpr int kCtas = S::kThreads <= 256 ? (kHalf ? 3 : 2) : S::kThreads <= 512 && kHalf ? 2 : 1;
+    // the weight beside them, where there is room: it would come from L2 twice a row
+    static constexpr bool kWeight = S::kThreads <= 256;
+    static constexpr int kWeightBytes = kWeight ? S::kThreads * PIECES * 32 : 0;
+    static constexpr int kFit = (224 * 1024 / kCtas - kWeightBytes) / int(sizeof(Stage<T, S::kThreads, PIECES>));
+    static constexpr int kStages = kFit < 2 ? 0 : kFit < 3 ? kFit : 3;
+    // Row groups of the grid: what the GPU runs at once, and no more than rows.
+    static int64_t groups(int64_t rows) {
+        const int64_t most = int64_t(kSms) * kCtas * S::kRows;
+        return ((rows < most ? rows : most) + S::kRows - 1) / S::kRows * S::kRows;
+    }
+};
+
 template <typename T, bool VEC, int TPR, int PIECES>
-__global__ void __launch_bounds__(Shape<TPR, PIECES>::kThreads) rms_norm_grad_kernel(const RmsNormGrad a) {
+__global__ void __launch_bounds__(Shape<TPR, PIECES>::kThreads, Plan<T, Shape<TPR, PIECES>, PIECES>::kCtas)
+rms_norm_grad_kernel(const RmsNormGrad a) {
     using S = Shape<TPR, PIECES>;
+    constexpr int kStages = VEC ? Plan<T, S, PIECES>::kStages : 0, kAhead = kStages - 1;
+    constexpr bool kRing = kStages > 0, kWeight = kRing && Plan<T, S, PIECES>::kWeight;
+    using Ring = Stage<T, S::kThreads, PIECES>;
+    extern __shared__ __align__(16) uint8_t ring_bytes[];
     __shared__ float slots[2][S::kThreads / 32];
-    const int in_row = threadIdx.x % TPR, l = in_row & 15;
-    const int64_t group = int64_t(blockIdx.x) * S::kRows + threadIdx.x / TPR;
+    Ring *const ring = reinterpret_cast<Ring *>(ring_bytes);
+    const int me = threadIdx.x, in_row = me % TPR, l = in_row & 15;
+    const int64_t group = int64_t(blockIdx.x) * S::kRows + me / TPR;
     const int64_t groups = int64_t(gridDim.x) * S::kRows;
     const int cols = int(a.cols);
     const float each = __fdiv_rn(1.0f, float(cols));
@@ -159,29 +196,108 @@ __global__ void __launch_bounds__(Shape<TPR, PIECES>::kThreads) rms_norm_grad_ke
     for (int p = 0; p < PIECES; ++p)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[p][j] = 0.0f;
+    // [two words of each piece][threads], each thread's own
+    float4 *const own_weight = reinterpret_cast<float4 *>(ring_bytes + kStages * sizeof(Ring)) + me;
+    if constexpr (kWeight) {
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) {
+            const int col = (p * TPR + in_row) / 16 * kBlock8;
+            float w[8];
+            weights<VEC>(a.weight, a.weight_bf16, col, l, cols - col, w);
+            own_weight[2 * p * S::kThreads] = make_float4(w[0], w[1], w[2], w[3]);
+            own_weight[(2 * p + 1) * S::kThreads] = make_float4(w[4], w[5], w[6], w[7]);
+        }
+    }
+    auto weight_of = [&](int p, int col, float(&w)[8]) {
+        if constexpr (kWeight) {
+            const float4 x = own_weight[2 * p * S::kThreads], y = own_weight[(2 * p + 1) * S::kThreads];
+            w[0] = x.x;
+            w[1] = x.y;
+            w[2] = x.z;
+            w[3] = x.w;
+            w[4] = y.x;
+            w[5] = y.y;
+            w[6] = y.z;
+            w[7] = y.w;
+        } else {
+            weights<VEC>(a.weight, a.weight_bf16, col, l, cols - col, w);
+        }
+    };
+    // the copies of one row, a group of them even if there is none
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < a.rows) {
+            Ring &s = ring[stage];
+            copy_async<4>(&s.r[me], a.rstd + row);
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) {
+                const int col = (p * TPR + in_row) / 16 * kBlock8;
+                if (col + 8 * l < cols) {
+                    const T *dy = static_cast<const T *>(a.dy) + row * a.ld_dy + col + 8 * l;
+                    const T *add = static_cast<const T *>(a.add) + (a.add ? row * a.ld_add + col + 8 * l : 0);
+#pragma unroll
+                    for (int k = 0; k < Ring::kWords; ++k) {
+                        copy_async<16>(&s.dy[p * Ring::kWords + k][me], dy + k * 4);
+                        if (a.add) copy_async<16>(&s.add[p * Ring::kWords + k][me], add + k * 4);
+                    }
+                    copy_async<8>(&s.codes[p][me], a.kept.q + row * a.kept.ld_q + col + 8 * l);
+                    copy_async<4>(&s.scale[p][me], a.kept.s + col / kBlock8 * a.kept.ld_s + row);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     // every group of a CTA takes as many turns, for the CTA's barriers
     const int64_t turns = (a.rows - int64_t(blockIdx.x) * S::kRows + groups - 1) / groups;
     int64_t row = group;
+    if constexpr (kRing)
+        for (int k = 0; k < kAhead; ++k) fetch(row + k * groups, k);
+    int stage = 0;
     for (int64_t i = 0; i < turns; ++i, row += groups) {
         const bool live = row < a.rows;
-        const float r = live ? a.rstd[row] : 0.0f;
+        float r = 0.0f;
         Eight<T> dy[PIECES];
-        uint2 codes[PIECES];
-        float scale[PIECES], n[PIECES][8];
+        float n[PIECES][8];
+        if constexpr (kRing) {
+            // (the stage that the row before has left)
+            fetch(row + kAhead * groups, stage == 0 ? kStages - 1 : stage - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+            const Ring &s = ring[stage];
+            if (live) r = s.r[me];
 #pragma unroll
-        for (int p = 0; p < PIECES; ++p) {
-            const int col = (p * TPR + in_row) / 16 * kBlock8, left = live ? cols - col : 0;
-            dy[p].template load<VEC>(static_cast<const T *>(a.dy) + row * a.ld_dy + col, l, left);
-            codes[p] = load_codes<VEC>(a.kept.q + row * a.kept.ld_q + col, l, left);
-            scale[p] = left > 0 ? a.kept.s[col / kBlock8 * a.kept.ld_s + row] : 0.0f;
+            for (int p = 0; p < PIECES; ++p) {
+                dy[p].zero();
+                uint2 codes = make_uint2(0u, 0u);
+                float scale = 0.0f;
+                if (live && (p * TPR + in_row) / 16 * kBlock8 + 8 * l < cols) {
+#pragma unroll
+                    for (int k = 0; k < Ring::kWords; ++k) {
+                        const uint4 q = s.dy[p * Ring::kWords + k][me];
+                        dy[p].w[4 * k] = q.x;
+                        dy[p].w[4 * k + 1] = q.y;
+                        dy[p].w[4 * k + 2] = q.z;
+                        dy[p].w[4 * k + 3] = q.w;
+                    }
+                    codes = s.codes[p][me];
+                    scale = s.scale[p][me];
+                }
+                values_of(codes, scale, n[p]);
+            }
+        } else {
+            if (live) r = a.rstd[row];
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) {
+                const int col = (p * TPR + in_row) / 16 * kBlock8, left = live ? cols - col : 0;
+                dy[p].template load<VEC>(static_cast<const T *>(a.dy) + row * a.ld_dy + col, l, left);
+                const uint2 codes = load_codes<VEC>(a.kept.q + row * a.kept.ld_q + col, l, left);
+                values_of(codes, left > 0 ? a.kept.s[col / kBlock8 * a.kept.ld_s + row] : 0.0f, n[p]);
+            }
         }
         float sum = 0.0f;
 #pragma unroll
         for (int p = 0; p < PIECES; ++p) {
             const int col = (p * TPR + in_row) / 16 * kBlock8;
             float w[8];
-            weights<VEC>(a.weight, a.weight_bf16, col, l, cols - col, w);
-            values_of(codes[p], scale[p], n[p]);
+            weight_of(p, col, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 n[p][j] = __fmul_rn(n[p][j], r);
@@ -194,13 +310,27 @@ __global__ void __launch_bounds__(Shape<TPR, PIECES>::kThreads) rms_norm_grad_ke
         for (int p = 0; p < PIECES; ++p) {
             const int col = (p * TPR + in_row) / 16 * kBlock8, left = live ? cols - col : 0;
             float w[8], x[8];
-            weights<VEC>(a.weight, a.weight_bf16, col, l, cols - col, w);
+            weight_of(p, col, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 x[j] = __fmul_rn(r, __fmaf_rn(-n[p][j], mean, __fmul_rn(dy[p].at(j), w[j])));
             if (a.add) {
                 Eight<T> o;
-                o.template load<VEC>(static_cast<const T *>(a.add) + row * a.ld_add + col, l, left);
+                if constexpr (kRing) {
+                    o.zero();
+                    if (8 * l < left) {
+#pragma unroll
+                        for (int k = 0; k < Ring::kWords; ++k) {
+                            const uint4 q = ring[stage].add[p * Ring::kWords + k][me];
+                            o.w[4 * k] = q.x;
+                            o.w[4 * k + 1] = q.y;
+                            o.w[4 * k + 2] = q.z;
+                            o.w[4 * k + 3] = q.w;
+                        }
+                    }
+                } else {
+                    o.template load<VEC>(static_cast<const T *>(a.add) + row * a.ld_add + col, l, left);
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(x[j], o.at(j));
             }
@@ -208,6 +338,7 @@ __global__ void __launch_bounds__(Shape<TPR, PIECES>::kThreads) rms_norm_grad_ke
             out.set(x);
             out.template store<VEC>(static_cast<T *>(a.dx) + row * a.ld_dx + col, l, left);
         }
+        if (++stage == kStages) stage = 0;
     }
 #pragma unroll
     for (int p = 0; p < PIECES; ++p) {
@@ -265,6 +396,13 @@ auto with_shape(int64_t cols, F f) {
     return f(Shape<1024, 2>(), std::integral_constant<int, 1024>(), std::integral_constant<int, 2>());
 }
 
+template <typename T>
+int64_t groups_of(int64_t rows, int64_t cols) {
+    return with_shape(cols, [&](auto shape, auto, auto pieces) {
+        return Plan<T, decltype(shape), decltype(pieces)::value>::groups(rows);
+    });
+}
+
 bool vector_rows(const void *p, int64_t ld, bool bf16) {
     return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % (bf16 ? 8 : 4) == 0);
 }
@@ -279,13 +417,33 @@ void launch(const RmsNorm &a, cudaStream_t stream) {
     });
 }
 
+template <typename T, bool VEC, int TPR, int PIECES>
+cudaError_t launch_grad(const RmsNormGrad &a, cudaStream_t stream) {
+    using S = Shape<TPR, PIECES>;
+    using P = Plan<T, S, PIECES>;
+    constexpr size_t smem = VEC && P::kStages > 0 ? P::kStages * sizeof(Stage<T, S::kThreads, PIECES>) + P::kWeightBytes : 0;
+    if constexpr (smem > 48 * 1024) {
+        // once for each GPU: the kernel's attribute stays set
+        static std::atomic<uint64_t> prepared{0};
+        int device = 0;
+        cudaError_t e = cudaGetDevice(&device);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = uint64_t(1) << (device & 63);
+        if (device > 63 || !(prepared.load(std::memory_order_relaxed) & bit)) {
+            e = cudaFuncSetAttribute(rms_norm_grad_kernel<T, VEC, TPR, PIECES>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+            if (e != cudaSuccess) return e;
+            prepared.fetch_or(bit, std::memory_order_relaxed);
+        }
+    }
+    rms_norm_grad_kernel<T, VEC, TPR, PIECES>
+        <<<uint32_t(P::groups(a.rows) / S::kRows), S::kThreads, smem, stream>>>(a);
+    return cudaPeekAtLastError();
+}
+
 template <typename T, bool VEC>
-void launch(const RmsNormGrad &a, cudaStream_t stream) {
-    with_shape(a.cols, [&](auto shape, auto tpr, auto pieces) {
-        using S = decltype(shape);
-        rms_norm_grad_kernel<T, VEC, decltype(tpr)::value, decltype(pieces)::value>
-            <<<uint32_t(groups_of<S>(a.rows) / S::kRows), S::kThreads, 0, stream>>>(a);
-        return 0;
+cudaError_t launch(const RmsNormGrad &a, cudaStream_t stream) {
+    return with_shape(a.cols, [&](auto, auto tpr, auto pieces) {
+        return launch_grad<T, VEC, decltype(tpr)::value, decltype(pieces)::value>(a, stream);
     });
 }
 
@@ -303,21 +461,21 @@ cudaError_t launch_rms_norm(const RmsNorm &a, cudaStream_t stream) {
 }
 
 int64_t rms_norm_grad_partials(int64_t rows, int64_t cols) {
-    return cols * with_shape(cols, [&](auto shape, auto, auto) { return groups_of<decltype(shape)>(rows); });
+    // (bf16 rows are in no fewer groups than fp32 ones)
+    return cols * groups_of<uint16_t>(rows, cols);
 }
 
 cudaError_t launch_rms_norm_grad(const RmsNormGrad &a, cudaStream_t stream) {
     const bool vec = a.cols % 8 == 0 && vector_rows(a.dy, a.ld_dy, a.bf16) && vector_rows(a.add, a.ld_add, a.bf16) &&
                      vector_rows(a.dx, a.ld_dx, a.bf16) && vector_rows(a.weight, 0, a.weight_bf16);
     if (a.rows > 0) {
-        if (a.bf16 && vec) launch<uint16_t, true>(a, stream);
-        else if (a.bf16) launch<uint16_t, false>(a, stream);
-        else if (vec) launch<float, true>(a, stream);
-        else launch<float, false>(a, stream);
-        const cudaError_t e = cudaPeekAtLastError();
+        const cudaError_t e = a.bf16 && vec ? launch<uint16_t, true>(a, stream)
+                              : a.bf16      ? launch<uint16_t, false>(a, stream)
+                              : vec         ? launch<float, true>(a, stream)
+                                            : launch<float, false>(a, stream);
         if (e != cudaSuccess) return e;
     }
-    const int64_t groups = a.rows > 0 ? rms_norm_grad_partials(a.rows, a.cols) / a.cols : 0;
+    const int64_t groups = a.rows == 0 ? 0 : a.bf16 ? groups_of<uint16_t>(a.rows, a.cols) : groups_of<float>(a.rows, a.cols);
     return launch_after(dweight_kernel, dim3(uint32_t((a.cols + 31) / 32)), dim3(1024), 0, stream, 1,
                         static_cast<const float *>(a.partials), groups, int(a.cols), a.dweight,
                         a.dweight_bf16 ? 1 : 0, a.accumulate ? 1 : 0);
