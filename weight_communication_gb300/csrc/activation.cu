@@ -13,7 +13,7 @@
 //
 // Bound: HBM.  Each value is read once and written once; the codes are made
 // from the values that the forward pass holds in registers anyway.  16 lanes
-// have a block of 128 (wc_eight.cuh) and a CTA 16 rows by two blocks, so that
+// have a block of 128 (wc_eight.cuh) and a CTA 16 rows by one or four blocks, so that
 // the scales, which lie by blocks first and rows second, are written 64 bytes at
 // a time.
 #include "wc_eight.cuh"
@@ -25,7 +25,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRows = kThreads / 16;  // of a CTA
-constexpr int kAcross = 2;            // blocks of a row that a thread has
+// Blocks of a row that a thread has (ACROSS), all in flight at once: 8192 x 11008 gated,
+// both ways, one block 263 us, two 246, four 232.  Where the CTAs would not fill
+// the GPU, one (333 x 1003 fp32: four 10.6 us, two 7.1).
+constexpr int kMany = 4;
 
 constexpr float kGelu1 = 1.59576912160573071176f;                  // 2 sqrt(2 / pi)
 constexpr float kGelu3 = 1.59576912160573071176f * 0.044715f;
@@ -91,17 +94,18 @@ struct Place {
     int32_t block;
 };
 
+template <int ACROSS>
 __device__ __forceinline__ Place place(int32_t across) {
     const int64_t tile = blockIdx.x;
     const int64_t down = tile / across;
-    const int32_t block = int32_t(tile - down * across) * kAcross;
+    const int32_t block = int32_t(tile - down * across) * ACROSS;
     return {down * kRows + (threadIdx.x >> 4), int64_t(block) * kBlock8, block};
 }
 
-template <typename T, bool VEC, bool GATED, bool KEEP>
+template <typename T, bool VEC, bool GATED, bool KEEP, int kAcross>
 __global__ void __launch_bounds__(kThreads) act_kernel(const Activation a, int32_t across) {
     constexpr bool kFast = sizeof(T) == 2;
-    const Place at = place(across);
+    const Place at = place<kAcross>(across);
     const int l = threadIdx.x & 15;
     const bool live = at.row < a.rows;
     const T *gate = static_cast<const T *>(a.gate) + at.row * a.ld_gate + at.col;
@@ -128,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const Activation a, int32
         out.template store<VEC>(h + k * kBlock8, l, left - k * kBlock8);
     }
     if (!KEEP) return;
-    // a lane divides for one block: lanes 0 and 1 of four for gate's, 2 and 3 for up's
+    // a lane divides for one block, gate's first and then up's
     constexpr int kEach = GATED ? 2 * kAcross : kAcross;
     uint32_t mine = 0u;
 #pragma unroll
@@ -160,10 +164,10 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const Activation a, int32
     }
 }
 
-template <typename T, bool VEC, bool GATED>
+template <typename T, bool VEC, bool GATED, int kAcross>
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActivationGrad a, int32_t across) {
     constexpr bool kFast = sizeof(T) == 2;
-    const Place at = place(across);
+    const Place at = place<kAcross>(across);
     const int l = threadIdx.x & 15;
     if (at.row >= a.rows) return;
     const int left = int(min(a.cols - at.col, int64_t(kAcross * kBlock8)));
@@ -221,44 +225,54 @@ bool vector_rows(const void *p, int64_t ld) {
     return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % (16 / int(sizeof(T))) == 0);
 }
 
-uint32_t tiles(int64_t rows, int64_t cols, int32_t *across) {
-    *across = int32_t((cols + kAcross * kBlock8 - 1) / (kAcross * kBlock8));
+uint32_t tiles(int64_t rows, int64_t cols, int each, int32_t *across) {
+    *across = int32_t((cols + each * kBlock8 - 1) / (each * kBlock8));
     return uint32_t((rows + kRows - 1) / kRows * *across);
 }
 
-template <typename T, bool VEC>
+bool many(int64_t rows, int64_t cols) {
+    int32_t across;
+    return tiles(rows, cols, kMany, &across) >= 4 * 152;
+}
+
+template <typename T, bool VEC, int ACROSS>
 void launch(const Activation &a, cudaStream_t stream) {
     int32_t across;
-    const uint32_t grid = tiles(a.rows, a.cols, &across);
+    const uint32_t grid = tiles(a.rows, a.cols, ACROSS, &across);
     const bool keep = a.kept_gate.q != nullptr;
-    if (a.up && keep) act_kernel<T, VEC, true, true><<<grid, kThreads, 0, stream>>>(a, across);
-    else if (a.up) act_kernel<T, VEC, true, false><<<grid, kThreads, 0, stream>>>(a, across);
-    else if (keep) act_kernel<T, VEC, false, true><<<grid, kThreads, 0, stream>>>(a, across);
-    else act_kernel<T, VEC, false, false><<<grid, kThreads, 0, stream>>>(a, across);
+    if (a.up && keep) act_kernel<T, VEC, true, true, ACROSS><<<grid, kThreads, 0, stream>>>(a, across);
+    else if (a.up) act_kernel<T, VEC, true, false, ACROSS><<<grid, kThreads, 0, stream>>>(a, across);
+    else if (keep) act_kernel<T, VEC, false, true, ACROSS><<<grid, kThreads, 0, stream>>>(a, across);
+    else act_kernel<T, VEC, false, false, ACROSS><<<grid, kThreads, 0, stream>>>(a, across);
+}
+
+template <typename T, bool VEC, int ACROSS>
+void launch(const ActivationGrad &a, cudaStream_t stream) {
+    int32_t across;
+    const uint32_t grid = tiles(a.rows, a.cols, ACROSS, &across);
+    if (a.dup) act_grad_kernel<T, VEC, true, ACROSS><<<grid, kThreads, 0, stream>>>(a, across);
+    else act_grad_kernel<T, VEC, false, ACROSS><<<grid, kThreads, 0, stream>>>(a, across);
+}
+
+template <typename T, typename Call>
+void launch(const Call &a, bool vec, cudaStream_t stream) {
+    const bool m = many(a.rows, a.cols);
+    if (vec && m) launch<T, true, kMany>(a, stream);
+    else if (vec) launch<T, true, 1>(a, stream);
+    else if (m) launch<T, false, kMany>(a, stream);
+    else launch<T, false, 1>(a, stream);
 }
 
 template <typename T>
 void launch(const Activation &a, cudaStream_t stream) {
-    const bool vec = a.cols % 8 == 0 && vector_rows<T>(a.gate, a.ld_gate) && vector_rows<T>(a.up, a.ld_up) &&
-                     vector_rows<T>(a.h, a.ld_h);
-    if (vec) launch<T, true>(a, stream);
-    else launch<T, false>(a, stream);
-}
-
-template <typename T, bool VEC>
-void launch(const ActivationGrad &a, cudaStream_t stream) {
-    int32_t across;
-    const uint32_t grid = tiles(a.rows, a.cols, &across);
-    if (a.dup) act_grad_kernel<T, VEC, true><<<grid, kThreads, 0, stream>>>(a, across);
-    else act_grad_kernel<T, VEC, false><<<grid, kThreads, 0, stream>>>(a, across);
+    launch<T>(a, a.cols % 8 == 0 && vector_rows<T>(a.gate, a.ld_gate) && vector_rows<T>(a.up, a.ld_up) &&
+                     vector_rows<T>(a.h, a.ld_h), stream);
 }
 
 template <typename T>
 void launch(const ActivationGrad &a, cudaStream_t stream) {
-    const bool vec = a.cols % 8 == 0 && vector_rows<T>(a.dh, a.ld_dh) && vector_rows<T>(a.dgate, a.ld_dgate) &&
-                     vector_rows<T>(a.dup, a.ld_dup);
-    if (vec) launch<T, true>(a, stream);
-    else launch<T, false>(a, stream);
+    launch<T>(a, a.cols % 8 == 0 && vector_rows<T>(a.dh, a.ld_dh) && vector_rows<T>(a.dgate, a.ld_dgate) &&
+                     vector_rows<T>(a.dup, a.ld_dup), stream);
 }
 
 }  // namespace

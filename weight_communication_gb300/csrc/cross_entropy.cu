@@ -80,6 +80,7 @@ __device__ __forceinline__ float nan32() { return __uint_as_float(0x7FC00000u); 
 // One product C[i][j] = sum over k of A[i][k] B[j][k].
 struct Job {
     int32_t tiles_i, tiles_j;
+    int32_t width;          // columns of a tile: 256, 128 or (K-major B) 192, 64
     int32_t split;          // parts of K with sums of their own
     int32_t blocks;         // of K
     int32_t rows_i, rows_j;
@@ -95,6 +96,7 @@ struct Job {
 struct Args {
     Job job[2];
     int32_t units[2];       // tiles x split
+    int32_t sooner;         // see unit_of
     // of the logits' epilogues
     const void *targets;
     int32_t wide;           // 64-bit targets
@@ -186,6 +188,25 @@ __device__ __forceinline__ void tile_at(const Job &a, int32_t t, int32_t *ti, in
     *tj = in / high;
 }
 
+// Number of the unit that a pair of SMs works on as its i-th, of `pairs`; past all
+// units there is none.  Job 0's units, which may be much longer, are dealt first.  Some
+// pairs then have one less than others; those get the `sooner` units of job 1 that
+// take about as long, and the rest is dealt to all.  (8192 x 32000 x 2048: dealing all in
+// turn leaves some pairs 5 % more than the mean.)
+template <Mode MODE>
+__device__ __forceinline__ int32_t unit_of(const Args &a, int32_t pair, int32_t i, int32_t pairs) {
+    if (MODE != kProducts) return pair + i * pairs;
+    const int32_t more = a.units[0] % pairs, of_0 = a.units[0] / pairs + (pair < more ? 1 : 0);
+    if (i < of_0) return pair + i * pairs;
+    i -= of_0;
+    const int32_t early = more > 0 ? pairs - more : 0;
+    if (early > 0 && pair >= more) {
+        if (i < a.sooner) return a.units[0] + pair - more + i * early;
+        i -= a.sooner;
+    }
+    return a.units[0] + a.sooner * early + pair + i * pairs;
+}
+
 struct Unit {
     int32_t job, ti, tj, part, block0, blocks;
 };
@@ -203,13 +224,14 @@ __device__ __forceinline__ Unit unit_at(const Args &a, int32_t u) {
     return r;
 }
 
-// 128 rows x 64 of K of an operand, to 16 KB of shared memory with 128-byte swizzle:
-// K-major 128 lines of 64 values of K, MN-major twice 64 lines (one per k) of 64 rows.
-__device__ __forceinline__ void load_operand(uint32_t to, const CUtensorMap *map, uint32_t bar, int mn, int32_t row,
-                                             int32_t k) {
+// `rows` (128, or B's of a narrow tile) x 64 of K of an operand, to up to 16 KB of shared
+// memory with 128-byte swizzle: K-major lines of 64 values of K, MN-major 64 lines
+// (one per k) of 64 rows, then those of the next 64 rows.
+__device__ __forceinline__ void load_operand(uint32_t to, const CUtensorMap *map, uint32_t bar, int mn, int32_t rows,
+                                             int32_t row, int32_t k) {
     if (mn) {
         tma_load<true>(to, map, bar, row, k);
-        tma_load<true>(to + kOperand / 2, map, bar, row + 64, k);
+        if (rows > 64) tma_load<true>(to + kOperand / 2, map, bar, row + 64, k);
     } else {
         tma_load<true>(to, map, bar, k, row);
     }
@@ -223,10 +245,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, int mn) {
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
-// Instruction descriptor: fp32 sums, bf16 x bf16, 256 x 256.
-__device__ __forceinline__ uint32_t instr_desc(int mn_i, int mn_j) {
+// Instruction descriptor: fp32 sums, bf16 x bf16, 256 x width.
+__device__ __forceinline__ uint32_t instr_desc(int mn_i, int mn_j, int width) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(mn_i) << 15) | (uint32_t(mn_j) << 16) |
-           (uint32_t(kTile >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
+           (uint32_t(width >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
 }
 
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
@@ -389,7 +411,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t stages = (smem_of(dynamic_smem) + 1023u) & ~1023u;
     const int32_t rank = int32_t(blockIdx.x & 1);
-    const int32_t first = int32_t(blockIdx.x >> 1), step = int32_t(gridDim.x >> 1);
+    const int32_t pair = int32_t(blockIdx.x >> 1), pairs = int32_t(gridDim.x >> 1);
     const int32_t units = a.units[0] + (MODE == kProducts ? a.units[1] : 0);
 
     if (threadIdx.x == 0) {
@@ -413,15 +435,17 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
     tc_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&tmem_slot);
     wait_for_predecessor();  // all above is set-up that reads no operand
+    let_successor_start();   // (its CTAs find room as these end)
 
     if (warp == kProducer) {
         uint32_t stage = 0, phase = 0;
         bool ok = true;
-        for (int32_t t = first; ok && t < units; t += step) {
+        for (int32_t i = 0, t; ok && (t = unit_of<MODE>(a, pair, i, pairs)) < units; ++i) {
             const Unit u = unit_at<MODE>(a, t);
             const Job &job = a.job[u.job];
             const CUtensorMap *map_i = u.job ? &map_i1 : &map_i0, *map_j = u.job ? &map_j1 : &map_j0;
-            const int32_t row_i = u.ti * kTile + rank * kHalf, row_j = job.j_at + u.tj * kTile + rank * kHalf;
+            const int32_t half = job.width / 2;
+            const int32_t row_i = u.ti * kTile + rank * kHalf, row_j = job.j_at + u.tj * job.width + rank * half;
             for (int32_t b = 0; b < u.blocks; ++b) {
                 ok = mbar_wait(smem_of(&empty[stage]), phase ^ 1u);
                 if (!ok) break;
@@ -429,9 +453,9 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                     const uint32_t local = smem_of(&full[stage]), bar = in_cta(local, 0);
                     const uint32_t base = stages + stage * kStageBytes;
                     const int32_t k = (u.block0 + b) * kDepth;
-                    if (rank == 0) mbar_expect(local, 2 * kStageBytes);
-                    load_operand(base, map_i, bar, job.mn_i, row_i, k);
-                    load_operand(base + kOperand, map_j, bar, job.mn_j, row_j, job.kj_at + k);
+                    if (rank == 0) mbar_expect(local, 2 * (kHalf + half) * kDepth * 2);
+                    load_operand(base, map_i, bar, job.mn_i, kHalf, row_i, k);
+                    load_operand(base + kOperand, map_j, bar, job.mn_j, half, row_j, job.kj_at + k);
                 }
                 __syncwarp();
                 if (++stage == kStages) {
@@ -445,10 +469,10 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
         uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
         bool ok = true;
         const bool lead = elected();
-        for (int32_t t = first; ok && t < units; t += step) {
+        for (int32_t i = 0, t; ok && (t = unit_of<MODE>(a, pair, i, pairs)) < units; ++i) {
             const Unit u = unit_at<MODE>(a, t);
             const Job &job = a.job[u.job];
-            const uint32_t idesc = instr_desc(job.mn_i, job.mn_j);
+            const uint32_t idesc = instr_desc(job.mn_i, job.mn_j, job.width);
             // 16 values of K on: 32 bytes of every line, or 16 lines
             const uint64_t step_i = job.mn_i ? 128 : 2, step_j = job.mn_j ? 128 : 2;
             ok = mbar_wait(smem_of(&taken[buf]), buf_phase ^ 1u);
@@ -484,7 +508,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
             }
         }
         // No product may be in flight when the tensor memory is freed.
-        if (first < units) {
+        if (pair < units) {
             if (lead) mma_commit<true>(smem_of(&drained), 1);
             __syncwarp();
             mbar_wait(smem_of(&drained), 0);
@@ -492,18 +516,18 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
     } else if (warp < kEpilogueWarps) {
         const int group = warp >> 2;
         uint8_t *const staging = dynamic_smem + (stages - smem_of(dynamic_smem)) + kStages * kStageBytes + warp * kStagingBytes;
-        const uint32_t from0 = tmem + (uint32_t(warp & 3) << 21) + group * kHalf;
         const uint32_t taken0 = in_cta(smem_of(&taken[0]), 0);
         uint32_t buf = 0, phase = 0;
         bool ok = true;
-        for (int32_t t = first; t < units; t += step) {
+        for (int32_t i = 0, t; (t = unit_of<MODE>(a, pair, i, pairs)) < units; ++i) {
             const Unit u = unit_at<MODE>(a, t);
             const Job &job = a.job[u.job];
             const int32_t row0 = u.ti * kTile + rank * kHalf + (warp & 3) * 32, row = row0 + lane;
-            const int32_t col0 = u.tj * kTile + group * kHalf;
+            const int32_t half = job.width / 2, col0 = u.tj * job.width + group * half;
+            const uint32_t from = tmem + (uint32_t(warp & 3) << 21) + buf * kTile + group * half;
             const bool live = row < job.rows_i;
             // (columns of this group that exist)
-            const int32_t cols = max(0, min(job.rows_j - col0, kHalf));
+            const int32_t cols = max(0, min(job.rows_j - col0, half));
             int32_t target = -1;  // its column in this group, or any number outside
             bool padding = true;
             float lse2 = 0.0f, g = 0.0f, own = 0.0f;  // own: d of the target
@@ -523,17 +547,18 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
             Running run = {-INFINITY, 0.0f};
             uint32_t v[2][32];
             if (ok) {
-                tmem_load(from0 + buf * kTile, v[0]);
+                tmem_load(from, v[0]);
                 tmem_wait(v[0]);
             }
 #pragma unroll
             for (int c = 0; c < kHalf; c += 32) {
+                if (c >= half) break;
                 uint32_t(&w)[32] = v[(c / 32) & 1];
                 if (!ok) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) w[k] = 0x7FC00000u;
-                } else if (c + 32 < kHalf) {
-                    tmem_load(from0 + buf * kTile + c + 32, v[(c / 32 + 1) & 1]);
+                } else if (c + 32 < half) {
+                    tmem_load(from + c + 32, v[(c / 32 + 1) & 1]);
                 } else {
                     tc_before_sync();  // all read: the next tile may have the buffer
                     __syncwarp();
@@ -551,10 +576,13 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                 } else if (MODE == kGradient) {
                     float x[32];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const float p = __fmul_rn(g, ex2(__fmaf_rn(__uint_as_float(w[k]), kLog2E, -lse2)));
-                        // (padding tokens have no gradient whatever their logits are)
-                        x[k] = c + k >= last ? 0.0f : target - c == k ? own : p;
+                    for (int k = 0; k < 32; ++k)
+                        x[k] = __fmul_rn(g, ex2(__fmaf_rn(__uint_as_float(w[k]), kLog2E, -lse2)));
+                    if (__any_sync(kFull, padding || (target >= c && target < c + 32) || last < c + 32)) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            // (padding tokens have no gradient whatever their logits are)
+                            x[k] = c + k >= last ? 0.0f : target - c == k ? own : x[k];
                     }
                     stage_bf16(staging, x, lane);
                     __syncwarp();
@@ -567,7 +595,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                     for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(w[k]);
                     store_sums(job, u.part, x, staging, row0, col0 + c, lane);
                 }
-                if (ok && c + 32 < kHalf) tmem_wait(v[(c / 32 + 1) & 1]);
+                if (ok && c + 32 < half) tmem_wait(v[(c / 32 + 1) & 1]);
             }
             if (MODE == kStats && live) {
                 if (!ok) run = {nan32(), nan32()};
@@ -609,10 +637,12 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
 // few tokens
 // ---------------------------------------------------------------------------
 
-// The forward pass of T tokens, one reading of w at the memory's rate: a warp has
-// kFewRows rows of w at a time, their products with all tokens (fp32 in shared
+// The forward pass of up to T tokens, one reading of w at the memory's rate: a warp
+// has ROWS rows of w at a time, their products with all tokens (fp32 in shared
 // memory) in fp32, and the tokens' maxima and sums over its rows in registers.
-constexpr int kFewRows = 4, kFewThreads = 256, kFewWarps = kFewThreads / 32;
+// (One token, 32000 x 2048: 22 us of 19.4 at the copy rate; the tensor cores, with
+// 256 rows for it, 38.)
+constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 
 struct Few {
     const uint16_t *x, *w;
@@ -620,11 +650,12 @@ struct Few {
     int32_t V, D;
     const void *targets;
     int32_t wide;
-    float2 *parts;           // [gridDim.x][T]
+    float2 *parts;           // [gridDim.x][tokens]
     float *target_logit;
+    int32_t tokens;          // at most T
 };
 
-template <int T, bool VEC>
+template <int T, bool VEC, int ROWS>
 __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
     extern __shared__ __align__(16) float tokens[];  // [T][padded D]
     __shared__ float2 joined[kFewWarps][T];
@@ -635,21 +666,21 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
 #pragma unroll
     for (int t = 0; t < T; ++t)
         for (int32_t d = threadIdx.x; d < pitch; d += kFewThreads)
-            tokens[t * pitch + d] = d < a.D ? bf16_bits_to_f32(a.x[t * a.ld_x + d]) : 0.0f;
+            tokens[t * pitch + d] = d < a.D && t < a.tokens ? bf16_bits_to_f32(a.x[t * a.ld_x + d]) : 0.0f;
     int32_t y[T];
     Running run[T];
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-        y[t] = target_of(a.targets, a.wide, a.V, t);
+        y[t] = t < a.tokens ? target_of(a.targets, a.wide, a.V, t) : -1;
         run[t] = {-INFINITY, 0.0f};
     }
     __syncthreads();
-    const int64_t step = int64_t(gridDim.x) * kFewWarps * kFewRows;
-    for (int64_t v = (int64_t(blockIdx.x) * kFewWarps + warp) * kFewRows; v < a.V; v += step) {
-        float s[kFewRows][T];
-        Row row[kFewRows];
+    const int64_t step = int64_t(gridDim.x) * kFewWarps * ROWS;
+    for (int64_t v = (int64_t(blockIdx.x) * kFewWarps + warp) * ROWS; v < a.V; v += step) {
+        float s[ROWS][T];
+        Row row[ROWS];
 #pragma unroll
-        for (int r = 0; r < kFewRows; ++r) {
+        for (int r = 0; r < ROWS; ++r) {
             // (rows past the last are read as the last, and dropped below)
             row[r] = row_of(a.w, a.ld_w, a.V, a.D, v + r < a.V ? v + r : a.V - 1);
 #pragma unroll
@@ -658,20 +689,20 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
         {
 #pragma unroll VEC ? 4 : 2
             for (int32_t d = 8 * lane; d < pitch; d += 256) {
-                uint4 q[kFewRows];
+                uint4 q[ROWS];
                 if (VEC && d + 8 <= a.D) {
 #pragma unroll
-                    for (int r = 0; r < kFewRows; ++r) q[r] = ld_stream_u4(row[r].p + d);
+                    for (int r = 0; r < ROWS; ++r) q[r] = ld_stream_u4(row[r].p + d);
                 } else {
 #pragma unroll
-                    for (int r = 0; r < kFewRows; ++r) q[r] = row[r].at(d);
+                    for (int r = 0; r < ROWS; ++r) q[r] = row[r].at(d);
                 }
 #pragma unroll
                 for (int t = 0; t < T; ++t) {
                     const float4 lo = *reinterpret_cast<const float4 *>(tokens + t * pitch + d);
                     const float4 hi = *reinterpret_cast<const float4 *>(tokens + t * pitch + d + 4);
 #pragma unroll
-                    for (int r = 0; r < kFewRows; ++r) {
+                    for (int r = 0; r < ROWS; ++r) {
                         s[r][t] = __fmaf_rn(__uint_as_float(q[r].x << 16), lo.x, s[r][t]);
                         s[r][t] = __fmaf_rn(__uint_as_float(q[r].x & 0xFFFF0000u), lo.y, s[r][t]);
                         s[r][t] = __fmaf_rn(__uint_as_float(q[r].y << 16), lo.z, s[r][t]);
@@ -686,9 +717,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
         }
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            float z[kFewRows], top = run[t].top;
+            float z[ROWS], top = run[t].top;
 #pragma unroll
-            for (int r = 0; r < kFewRows; ++r) {
+            for (int r = 0; r < ROWS; ++r) {
                 float sum = s[r][t];
 #pragma unroll
                 for (int o = 16; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, o));
@@ -699,7 +730,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
             const float from = top == -INFINITY ? 0.0f : -top;
             float sum = __fmul_rn(run[t].sum, ex2(__fadd_rn(run[t].top, from)));
 #pragma unroll
-            for (int r = 0; r < kFewRows; ++r) sum = __fadd_rn(sum, ex2(__fmaf_rn(z[r], kLog2E, from)));
+            for (int r = 0; r < ROWS; ++r) sum = __fadd_rn(sum, ex2(__fmaf_rn(z[r], kLog2E, from)));
             run[t] = {top, sum};
         }
     }
@@ -707,10 +738,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
     for (int t = 0; t < T; ++t)
         if (lane == 0) joined[warp][t] = make_float2(run[t].top, run[t].sum);
     __syncthreads();
-    if (threadIdx.x < T) {
+    if (threadIdx.x < a.tokens) {
         float2 r = joined[0][threadIdx.x];
         for (int w = 1; w < kFewWarps; ++w) r = joined_stats(r, joined[w][threadIdx.x]);
-        a.parts[int64_t(blockIdx.x) * T + threadIdx.x] = r;
+        a.parts[int64_t(blockIdx.x) * a.tokens + threadIdx.x] = r;
     }
 }
 
@@ -776,6 +807,7 @@ struct LayOuts {
 
 __global__ void __launch_bounds__(256) lay_out_kernel(const LayOuts a) {
     wait_for_predecessor();
+    let_successor_start();
     const int lane = threadIdx.x & 31;
     const bool of_x = int32_t(blockIdx.x) < a.ctas_x;
     const LayOut &m = of_x ? a.x : a.w;
@@ -800,18 +832,36 @@ __global__ void __launch_bounds__(256) lay_out_kernel(const LayOuts a) {
     }
 }
 
-// out = the sum of `count` matrices [rows][ld_part] of fp32, in order.
+// out = the sum of `count` matrices [rows][ld_part] of fp32, in order; ld_part is a
+// multiple of 4, and a thread has 4 columns.
 __global__ void __launch_bounds__(256) join_sums_kernel(const float *parts, int32_t count, int64_t rows, int32_t cols,
-                                                        int64_t ld_part, void *out, int bf16, int64_t ld_out) {
+                                                        int32_t ld_part, void *out, int bf16, int64_t ld_out, int vec) {
     wait_for_predecessor();
-    const int64_t stride = rows * ld_part, n = rows * cols;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
-        const int64_t r = i / cols, c = i - r * cols;
-        const float *p = parts + r * ld_part + c;
-        float x = p[0];
-        for (int32_t k = 1; k < count; ++k) x = __fadd_rn(x, p[k * stride]);
-        if (bf16) static_cast<uint16_t *>(out)[r * ld_out + c] = f32_to_bf16_bits(x);
-        else static_cast<float *>(out)[r * ld_out + c] = x;
+    const int32_t quads = ld_part / 4;
+    const int64_t stride = rows * ld_part;
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+        const int32_t q = int32_t(blockIdx.x) * 256 + threadIdx.x;
+        if (q >= quads) continue;
+        const float4 *p = reinterpret_cast<const float4 *>(parts + r * ld_part) + q;
+        float4 x = *p;
+#pragma unroll 4
+        for (int32_t k = 1; k < count; ++k) {
+            const float4 y = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + k * stride);
+            x = make_float4(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y), __fadd_rn(x.z, y.z), __fadd_rn(x.w, y.w));
+        }
+        const int64_t at = r * ld_out + 4 * q;
+        const float e[4] = {x.x, x.y, x.z, x.w};
+        if (vec && bf16 && 4 * q + 4 <= cols) {
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) =
+                make_uint2(f32x2_to_bf16x2_bits(x.x, x.y), f32x2_to_bf16x2_bits(x.z, x.w));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (4 * q + k >= cols) break;
+                if (bf16) static_cast<uint16_t *>(out)[at + k] = f32_to_bf16_bits(e[k]);
+                else static_cast<float *>(out)[at + k] = e[k];
+            }
+        }
     }
 }
 
@@ -827,14 +877,14 @@ struct Bf16Matrix {
     int64_t ld, rows, cols;
 };
 
-// Boxes of 128 rows x 64 of K, or MN-major of 64 rows x 64 of K.
-cudaError_t describe(CUtensorMap *map, const Bf16Matrix &m, bool mn) {
+// Boxes of `rows` rows x 64 of K, or MN-major of 64 rows x 64 of K.
+cudaError_t describe(CUtensorMap *map, const Bf16Matrix &m, bool mn, int rows = kHalf) {
     EncodeTiled encode;
     const cudaError_t e = encoder(&encode);
     if (e != cudaSuccess) return e;
     const cuuint64_t dims[2] = {cuuint64_t(m.cols), cuuint64_t(m.rows)};
     const cuuint64_t strides[1] = {cuuint64_t(m.ld) * 2};
-    const cuuint32_t box[2] = {64, cuuint32_t(mn ? 64 : kHalf)};
+    const cuuint32_t box[2] = {64, cuuint32_t(mn ? 64 : rows)};
     const cuuint32_t step[2] = {1, 1};
     const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(m.p), dims, strides,
                               box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -857,6 +907,12 @@ cudaError_t run(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
     }
     for (int k = 0; k < 2; ++k) a.units[k] = a.job[k].tiles_i * a.job[k].tiles_j * a.job[k].split;
     const int64_t units = int64_t(a.units[0]) + (MODE == kProducts ? a.units[1] : 0);
+    a.sooner = 0;
+    if (MODE == kProducts && a.units[0] > 0 && a.units[1] > 0) {
+        auto cycles = [](const Job &j) { return int64_t(j.blocks) / j.split * (j.width + 256) + 1500; };
+        const int64_t each = cycles(a.job[1]);
+        a.sooner = int32_t((cycles(a.job[0]) + each / 2) / each);
+    }
     // (CTAs without tiles sum targets' logits, ten warps with one token at a time)
     const int64_t more = MODE == kStats ? units + ceil_div(a.job[0].rows_i, 20) : 0, pairs = units > more ? units : more;
     const uint32_t grid = 2 * uint32_t(pairs < kSms / 2 ? pairs : kSms / 2);
@@ -865,6 +921,24 @@ cudaError_t run(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
 }
 
 bool aligned(const uint16_t *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
+
+// Columns of a tile of logits.  A stage of a narrow tile takes not much less time than
+// of a wide one, as it brings x all the same (16 stages of 64 in one wave: 256 columns
+// 12.8 us, 128 10.8; 1024 x 32000 x 2048, many waves: 74 us, 117), so narrow ones serve
+// where the wide ones leave SMs without work.
+int width_of(int64_t T, int64_t V) {
+    const int64_t tiles = ceil_div(T, kTile);
+    int best = kTile;
+    int64_t least = 0;
+    for (int w = kTile; w >= 64; w -= 64) {
+        const int64_t cost = ceil_div(tiles * ceil_div(V, w), kSms / 2) * (w + 256);
+        if (w == kTile || cost < least) {
+            best = w;
+            least = cost;
+        }
+    }
+    return best;
+}
 
 // Tokens of one forward launch: it leaves 16 bytes per token and 256 rows of w.
 constexpr int64_t kTokens = 65536;
@@ -879,7 +953,14 @@ struct Layout {
     }
 };
 
-int64_t few_grid(const CrossEntropy &c);
+// Rows of w that a warp has at a time: four share a token's values, and one keeps
+// more of the GPU busy where rows are few (4 x 1043 x 3009: 24 us with four).
+int64_t few_rows(const CrossEntropy &c) { return c.V > 4 * kSms * kFewWarps ? 4 : 1; }
+
+int64_t few_grid(const CrossEntropy &c) {
+    const int64_t ctas = ceil_div(c.V, kFewWarps * few_rows(c));
+    return ctas < 2 * kSms ? ctas : 2 * kSms;
+}
 
 struct FewLayout {
     int64_t parts, target_logit, bytes;
@@ -896,7 +977,7 @@ struct Forward {
     explicit Forward(const CrossEntropy &c) {
         Layout l;
         const int64_t T = c.T < kTokens ? c.T : kTokens;
-        parts = l.take(ceil_div(c.V, kTile) * 2 * T * int64_t(sizeof(float2)));
+        parts = l.take(ceil_div(c.V, width_of(T, c.V)) * 2 * T * int64_t(sizeof(float2)));
         target_logit = l.take(T * 4);
         x = aligned(c.x, c.ld_x) ? -1 : l.take(c.T * ceil_div(c.D, 8) * 16);
         w = aligned(c.w, c.ld_w) ? -1 : l.take(c.V * ceil_div(c.D, 8) * 16);
@@ -918,6 +999,29 @@ int64_t piece_of(const CrossEntropy &c) {
 struct Backward {
     int64_t x, w, target_logit, d, dx, bytes;
     int64_t piece, split, ld_dx;
+    int width;  // of a tile of the products
+    // dx's K is the vocabulary, so where tokens are few its tiles are few and long.
+    // How many parts each is split into, and the tiles' width: the least of an
+    // estimate of the launch in cycles -- a stage takes w + 256, a tile 1500 beside its
+    // stages, the parts' join 5000 and their memory traffic.
+    // (1024 x 32000 x 2048: dx whole 204 us, in four parts 161 and 10 for the join.)
+    void plan(const CrossEntropy &c) {
+        const int64_t blocks = ceil_div(piece, kDepth), rows = ceil_div(c.T, kTile);
+        int64_t least = 0;
+        for (int w = kTile; w >= kTile / 2; w /= 2)
+            for (int64_t s = 1; s <= 32 && (s == 1 || blocks / s >= 4); s += s < 4 ? 1 : s / 2) {
+                const int64_t across = ceil_div(c.D, w), stage = w + 256;
+                const int64_t unit_dx = ceil_div(blocks, s) * stage + 1500, unit_dw = ceil_div(c.T, kDepth) * stage + 1500;
+                const int64_t all = rows * across * s * unit_dx + ceil_div(piece, kTile) * across * unit_dw;
+                const int64_t longest = unit_dx > unit_dw ? unit_dx : unit_dw, even = all / (kSms / 2) + longest / 2;
+                const int64_t cost = (even > longest ? even : longest) + (s > 1 ? 5000 + s * c.T * c.D / 300 : 0);
+                if (least == 0 || cost < least) {
+                    least = cost;
+                    split = s;
+                    width = w;
+                }
+            }
+    }
     explicit Backward(const CrossEntropy &c) {
         Layout l;
         const int64_t ld = ceil_div(c.D, 8) * 16;
@@ -926,11 +1030,8 @@ struct Backward {
         target_logit = l.take(c.T * 4);
         piece = piece_of(c);
         d = l.take(c.T * piece * 2);
-        // dx has few tiles where tokens are few, and its K is the vocabulary
-        const int64_t tiles = ceil_div(c.T, kTile) * ceil_div(c.D, kTile), blocks = ceil_div(piece, kDepth);
-        split = tiles < kSms / 2 ? kSms / 2 / tiles : 1;
-        if (split > blocks / 8) split = blocks / 8 > 1 ? blocks / 8 : 1;
         ld_dx = ceil_div(c.D, 4) * 4;
+        plan(c);
         dx = split > 1 || piece < c.V ? l.take(split * c.T * ld_dx * 4) : -1;
         bytes = l.bytes;
     }
@@ -953,10 +1054,11 @@ cudaError_t lay_out(const CrossEntropy &c, uint16_t *x, uint16_t *w, float *targ
     return launch_after(lay_out_kernel, dim3(uint32_t(a.ctas_x + ctas(a.w.rows))), dim3(256), 0, stream, 1, a);
 }
 
-Job job_of(int64_t rows_i, int64_t rows_j, int64_t K) {
+Job job_of(int64_t rows_i, int64_t rows_j, int64_t K, int width) {
     Job j = {};
     j.tiles_i = int32_t(ceil_div(rows_i, kTile));
-    j.tiles_j = int32_t(ceil_div(rows_j, kTile));
+    j.tiles_j = int32_t(ceil_div(rows_j, width));
+    j.width = width;
     j.split = 1;
     j.blocks = int32_t(ceil_div(K, kDepth));
     j.rows_i = int32_t(rows_i);
@@ -965,26 +1067,30 @@ Job job_of(int64_t rows_i, int64_t rows_j, int64_t K) {
 }
 
 // Few tokens?  Their fp32 values fit shared memory twice per SM.
-bool few_tokens(const CrossEntropy &c) { return c.T <= 4 && c.T * (c.D + 7) * 4 <= 96 * 1024; }
+constexpr int kFewBytes = 112 * 1024;
+int64_t few_tokens_held(const CrossEntropy &c) { return c.T <= 2 ? c.T : 4; }
+bool few_tokens(const CrossEntropy &c) { return c.T <= 4 && few_tokens_held(c) * (c.D + 7) * 4 <= kFewBytes; }
 
-int64_t few_grid(const CrossEntropy &c) {
-    const int64_t ctas = ceil_div(c.V, kFewWarps * kFewRows);
-    return ctas < 2 * kSms ? ctas : 2 * kSms;
-}
-
-template <int T, bool VEC>
+template <int T, bool VEC, int ROWS>
 cudaError_t run_few(const Few &a, uint32_t grid, size_t smem, cudaStream_t stream) {
+    // once for each GPU: the kernel's attribute stays set
     static std::atomic<uint64_t> prepared{0};
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
     const uint64_t bit = uint64_t(1) << (device & 63);
     if (device > 63 || !(prepared.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(few_kernel<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+        e = cudaFuncSetAttribute(few_kernel<T, VEC, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewBytes);
         if (e != cudaSuccess) return e;
         prepared.fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_after(few_kernel<T, VEC>, dim3(grid), dim3(kFewThreads), smem, stream, 1, a);
+    return launch_after(few_kernel<T, VEC, ROWS>, dim3(grid), dim3(kFewThreads), smem, stream, 1, a);
+}
+
+template <int T>
+cudaError_t run_few(const Few &a, bool vec, int64_t rows, uint32_t grid, size_t smem, cudaStream_t stream) {
+    if (rows == 1) return vec ? run_few<T, true, 1>(a, grid, smem, stream) : run_few<T, false, 1>(a, grid, smem, stream);
+    return vec ? run_few<T, true, 4>(a, grid, smem, stream) : run_few<T, false, 4>(a, grid, smem, stream);
 }
 
 cudaError_t join_stats(const CrossEntropy &c, const float2 *parts, int32_t count, int64_t t0, int64_t tokens,
@@ -999,17 +1105,15 @@ cudaError_t launch_few(const CrossEntropy &c, cudaStream_t stream) {
     const FewLayout f(c);
     char *const ws = static_cast<char *>(c.workspace);
     const Few a = {c.x, c.w, c.ld_x, c.ld_w, int32_t(c.V), int32_t(c.D), c.targets, c.wide,
-                   reinterpret_cast<float2 *>(ws + f.parts), reinterpret_cast<float *>(ws + f.target_logit)};
+                   reinterpret_cast<float2 *>(ws + f.parts), reinterpret_cast<float *>(ws + f.target_logit), int32_t(c.T)};
     const uint32_t grid = uint32_t(few_grid(c));
-    const size_t smem = size_t(c.T) * ((c.D + 7) / 8 * 8) * 4;
+    const int held = int(few_tokens_held(c));
+    const size_t smem = size_t(held) * ((c.D + 7) / 8 * 8) * 4;
     const bool vec = aligned(c.w, c.ld_w);
-    cudaError_t e;
-    switch (c.T) {
-        case 1: e = vec ? run_few<1, true>(a, grid, smem, stream) : run_few<1, false>(a, grid, smem, stream); break;
-        case 2: e = vec ? run_few<2, true>(a, grid, smem, stream) : run_few<2, false>(a, grid, smem, stream); break;
-        case 3: e = vec ? run_few<3, true>(a, grid, smem, stream) : run_few<3, false>(a, grid, smem, stream); break;
-        default: e = vec ? run_few<4, true>(a, grid, smem, stream) : run_few<4, false>(a, grid, smem, stream); break;
-    }
+    const int64_t rows = few_rows(c);
+    const cudaError_t e = held == 1   ? run_few<1>(a, vec, rows, grid, smem, stream)
+                          : held == 2 ? run_few<2>(a, vec, rows, grid, smem, stream)
+                                      : run_few<4>(a, vec, rows, grid, smem, stream);
     if (e != cudaSuccess) return e;
     return join_stats(c, a.parts, int32_t(grid), 0, c.T, a.target_logit, stream);
 }
@@ -1032,7 +1136,9 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     CUtensorMap maps[4];
-    if ((e = describe(&maps[1], w, false)) != cudaSuccess) return e;
+    // (the last tokens of several launches have the first ones' width)
+    const int width = width_of(c.T < kTokens ? c.T : kTokens, c.V);
+    if ((e = describe(&maps[1], w, false, width / 2)) != cudaSuccess) return e;
     const int64_t id = c.wide ? 8 : 4;
     for (int64_t t0 = 0; t0 < c.T; t0 += kTokens) {
         Bf16Matrix some = x;
@@ -1042,7 +1148,7 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
         maps[2] = maps[0];
         maps[3] = maps[1];
         Args a = {};
-        a.job[0] = job_of(some.rows, c.V, c.D);
+        a.job[0] = job_of(some.rows, c.V, c.D, width);
         a.targets = static_cast<const char *>(c.targets) + t0 * id;
         a.wide = c.wide;
         a.V = int32_t(c.V);
@@ -1076,7 +1182,8 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
     const Bf16Matrix d = {reinterpret_cast<uint16_t *>(ws + f.d), f.piece, c.T, f.piece};
     CUtensorMap logits[4], products[4];
     if ((e = describe(&logits[0], x, false)) != cudaSuccess) return e;
-    if ((e = describe(&logits[1], w, false)) != cudaSuccess) return e;
+    const int width = width_of(c.T, f.piece < c.V ? f.piece : c.V);
+    if ((e = describe(&logits[1], w, false, width / 2)) != cudaSuccess) return e;
     logits[2] = logits[0];
     logits[3] = logits[1];
     if ((e = describe(&products[0], d, false)) != cudaSuccess) return e;
@@ -1090,7 +1197,7 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
         const int64_t cols = c.V - v0 < f.piece ? c.V - v0 : f.piece;
         const bool last = v0 + cols == c.V;
         Args a = {};
-        a.job[0] = job_of(c.T, cols, c.D);
+        a.job[0] = job_of(c.T, cols, c.D, width);
         a.job[0].j_at = int32_t(v0);
         a.job[0].out = ws + f.d;
         a.job[0].ld_out = f.piece;
@@ -1105,7 +1212,7 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
 
         Args p = {};
         if (c.dx) {
-            Job &j = p.job[0] = job_of(c.T, c.D, cols);
+            Job &j = p.job[0] = job_of(c.T, c.D, cols, f.width);
             j.mn_j = 1;
             j.kj_at = int32_t(v0);
             j.split = int32_t(f.split < j.blocks ? f.split : j.blocks);
@@ -1127,7 +1234,7 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
             }
         }
         if (c.dw) {
-            Job &j = p.job[1] = job_of(cols, c.D, c.T);
+            Job &j = p.job[1] = job_of(cols, c.D, c.T, f.width);
             j.mn_i = j.mn_j = 1;
             j.out = static_cast<char *>(c.dw) + v0 * c.ld_dw * size;
             j.out_bf16 = c.dw_bf16;
@@ -1142,10 +1249,10 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
         if ((e = run<kProducts>(products, p, stream)) != cudaSuccess) return e;
     }
     if (c.dx && f.split > 1) {
-        const int64_t ctas = ceil_div(c.T * c.D, 256);
-        return launch_after(join_sums_kernel, dim3(uint32_t(ctas < 16 * kSms ? ctas : 16 * kSms)), dim3(256), 0,
-                            stream, 1, static_cast<const float *>(sums), int32_t(f.split), c.T, int32_t(c.D), f.ld_dx,
-                            c.dx, c.dx_bf16 ? 1 : 0, c.ld_dx);
+        const uint32_t across = uint32_t(ceil_div(f.ld_dx / 4, 256)), down = uint32_t(c.T < 65535 ? c.T : 65535);
+        return launch_after(join_sums_kernel, dim3(across, down), dim3(256), 0, stream, 1,
+                            static_cast<const float *>(sums), int32_t(f.split), c.T, int32_t(c.D), int32_t(f.ld_dx),
+                            c.dx, c.dx_bf16 ? 1 : 0, c.ld_dx, aligned(static_cast<const uint16_t *>(c.dx), c.ld_dx) ? 1 : 0);
     }
     return cudaSuccess;
 }
