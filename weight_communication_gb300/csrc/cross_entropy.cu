@@ -14,7 +14,10 @@
 // exp(s[t][v] - s[t][y])).
 // Backward: for one piece of the vocabulary after the other, the logits once
 // more, whose epilogue writes d (bf16, its only rounding) to a buffer, and one
-// launch for the two products that read it, dx summed over the pieces in fp32.
+// launch for the two products that read it, dx summed over the pieces in fp32.  A g
+// that is the same for all tokens multiplies the products instead: in d it would
+// move every target's d, near -1 for all that the model does not know, off a value
+// that bf16 holds, in the same direction (up to 2^-8 of the gradient).
 // So a pass multiplies four times where one that keeps T x V logits multiplies
 // three times.
 //
@@ -91,6 +94,7 @@ struct Job {
     const void *add;
     int64_t ld_out, ld_add, split_out, split_add;
     int32_t out_bf16, add_bf16, vec;
+    float alpha;            // factor of the product
 };
 
 struct Args {
@@ -103,11 +107,10 @@ struct Args {
     int32_t V;
     float2 *parts;          // [2 tiles_j][rows_i]: maximum (times log2 e), sum
     float *target_logit;    // [rows_i]
-    const uint16_t *x, *w;  // for it, as they were given
+    const uint16_t *x, *w;  // for it, as they were given; x NULL if it is there
     int64_t ld_x, ld_w;
     int32_t D;
     const float *lse, *dlosses;
-    float dloss;
 };
 
 enum Mode { kStats, kGradient, kProducts };
@@ -537,7 +540,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                 if (!padding) target = y - job.j_at - col0;
                 if (MODE == kGradient && !padding) {
                     lse2 = __fmul_rn(a.lse[row], kLog2E);
-                    g = a.dlosses ? a.dlosses[row] : a.dloss;
+                    g = a.dlosses ? a.dlosses[row] : 1.0f;
                     own = __fmul_rn(g, expm1f(__fadd_rn(a.target_logit[row], -a.lse[row])));
                 }
             }
@@ -592,7 +595,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                 } else {
                     float x[32];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(w[k]);
+                    for (int k = 0; k < 32; ++k) x[k] = __fmul_rn(job.alpha, __uint_as_float(w[k]));
                     store_sums(job, u.part, x, staging, row0, col0 + c, lane);
                 }
                 if (ok && c + 32 < half) tmem_wait(v[(c / 32 + 1) & 1]);
@@ -608,7 +611,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
         }
     }
 
-    if (MODE == kStats) {
+    if (MODE == kStats && a.x != nullptr) {
         // the targets' logits: two warps of each CTA, ten of one without tiles
         const int32_t busy = min(int32_t(gridDim.x), 2 * units), cta = int32_t(blockIdx.x);
         const bool idle = cta >= busy;
@@ -793,11 +796,12 @@ struct LayOut {
     uint16_t *dst;
 };
 
-// x and w laid out, a warp per row.  With target_logit, x's rows whose target is
-// padding become 0, and the others' products with their target's row of w go there.
+// x and w laid out, a warp per row; x may have no place to go.  With target_logit, the
+// products of x's rows with their target's row of w go there, and with `mask` rows
+// whose target is padding become 0.
 struct LayOuts {
     LayOut x, w;
-    int32_t D, ctas_x;       // CTAs at work on x
+    int32_t D, ctas_x, mask; // CTAs at work on x
     const void *targets;
     const uint16_t *given_w;
     int64_t ld_w;
@@ -817,15 +821,16 @@ __global__ void __launch_bounds__(256) lay_out_kernel(const LayOuts a) {
         const int32_t y = of_x && a.target_logit ? target_of(a.targets, a.wide, a.V, r) : 0;
         const Row row = row_of(m.src, m.ld, m.rows, a.D, r);
         uint16_t *to = m.dst + r * ld;
-        int32_t c = 8 * lane;
+        const bool zero = y < 0 && a.mask;
+        int32_t c = m.dst ? 8 * lane : ld;
         for (; c + 768 < ld; c += 1024) {
             uint4 q[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) q[k] = y < 0 ? make_uint4(0u, 0u, 0u, 0u) : row.at(c + 256 * k);
+            for (int k = 0; k < 4; ++k) q[k] = zero ? make_uint4(0u, 0u, 0u, 0u) : row.at(c + 256 * k);
 #pragma unroll
             for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(to + c + 256 * k) = q[k];
         }
-        for (; c < ld; c += 256) *reinterpret_cast<uint4 *>(to + c) = y < 0 ? make_uint4(0u, 0u, 0u, 0u) : row.at(c);
+        for (; c < ld; c += 256) *reinterpret_cast<uint4 *>(to + c) = zero ? make_uint4(0u, 0u, 0u, 0u) : row.at(c);
         if (!of_x || a.target_logit == nullptr || y < 0) continue;
         const float s = row_dot(row, row_of(a.given_w, a.ld_w, a.V, a.D, y), lane);
         if (lane == 0) a.target_logit[r] = s;
@@ -914,7 +919,7 @@ cudaError_t run(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
         a.sooner = int32_t((cycles(a.job[0]) + each / 2) / each);
     }
     // (CTAs without tiles sum targets' logits, ten warps with one token at a time)
-    const int64_t more = MODE == kStats ? units + ceil_div(a.job[0].rows_i, 20) : 0, pairs = units > more ? units : more;
+    const int64_t more = MODE == kStats && a.x ? units + ceil_div(a.job[0].rows_i, 20) : 0, pairs = units > more ? units : more;
     const uint32_t grid = 2 * uint32_t(pairs < kSms / 2 ? pairs : kSms / 2);
     return launch_after(product_kernel<MODE>, dim3(grid), dim3(kThreads), kSmem, stream, 2, maps[0], maps[1],
                         maps[2], maps[3], a);
@@ -978,7 +983,7 @@ struct Forward {
         Layout l;
         const int64_t T = c.T < kTokens ? c.T : kTokens;
         parts = l.take(ceil_div(c.V, width_of(T, c.V)) * 2 * T * int64_t(sizeof(float2)));
-        target_logit = l.take(T * 4);
+        target_logit = l.take(c.T * 4);
         x = aligned(c.x, c.ld_x) ? -1 : l.take(c.T * ceil_div(c.D, 8) * 16);
         w = aligned(c.w, c.ld_w) ? -1 : l.take(c.V * ceil_div(c.D, 8) * 16);
         bytes = l.bytes;
@@ -1037,14 +1042,16 @@ struct Backward {
     }
 };
 
-// x and w to the places given, each if it is not NULL; target_logit as above.
-cudaError_t lay_out(const CrossEntropy &c, uint16_t *x, uint16_t *w, float *target_logit, cudaStream_t stream) {
+// x and w to the places given, each if it is not NULL; target_logit and mask as above.
+cudaError_t lay_out(const CrossEntropy &c, uint16_t *x, uint16_t *w, float *target_logit, bool mask,
+                    cudaStream_t stream) {
     auto ctas = [](int64_t rows) { return int32_t(rows < 128 * kSms ? ceil_div(rows, 8) : 16 * kSms); };
     LayOuts a = {};
-    if (x) a.x = {c.x, c.ld_x, c.T, x};
+    if (x || target_logit) a.x = {c.x, c.ld_x, c.T, x};
     if (w) a.w = {c.w, c.ld_w, c.V, w};
     a.D = int32_t(c.D);
     a.ctas_x = ctas(a.x.rows);
+    a.mask = mask;
     a.targets = c.targets;
     a.given_w = c.w;
     a.ld_w = c.ld_w;
@@ -1130,14 +1137,21 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
     if (f.x >= 0) x = {reinterpret_cast<uint16_t *>(ws + f.x), ceil_div(c.D, 8) * 8, c.T, c.D};
     if (f.w >= 0) w = {reinterpret_cast<uint16_t *>(ws + f.w), ceil_div(c.D, 8) * 8, c.V, c.D};
-    if (f.x >= 0 || f.w >= 0) {
+    // The targets' logits: beside the rows that are laid out anyway, in the products'
+    // spare warps, or, where those would take longer than the products, by themselves
+    // (a warp takes some 2 us for each 1024 of D, a stage of a tile 0.3 us; 6614 x 627 x
+    // 2274: 148 us in the spare warps).
+    const int width = width_of(c.T < kTokens ? c.T : kTokens, c.V);
+    const int64_t tiles = ceil_div(c.T, kTile) * ceil_div(c.V, width);
+    const bool apart = f.x >= 0 || f.w >= 0 ||
+                       ceil_div(c.T, 2 * kSms) * ceil_div(c.D, 1024) * 7 > ceil_div(tiles, kSms / 2) * ceil_div(c.D, kDepth);
+    float *const target_logit = reinterpret_cast<float *>(ws + f.target_logit);
+    if (apart) {
         e = lay_out(c, f.x >= 0 ? const_cast<uint16_t *>(x.p) : nullptr, f.w >= 0 ? const_cast<uint16_t *>(w.p) : nullptr,
-                    nullptr, stream);
+                    target_logit, false, stream);
         if (e != cudaSuccess) return e;
     }
     CUtensorMap maps[4];
-    // (the last tokens of several launches have the first ones' width)
-    const int width = width_of(c.T < kTokens ? c.T : kTokens, c.V);
     if ((e = describe(&maps[1], w, false, width / 2)) != cudaSuccess) return e;
     const int64_t id = c.wide ? 8 : 4;
     for (int64_t t0 = 0; t0 < c.T; t0 += kTokens) {
@@ -1153,8 +1167,8 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
         a.wide = c.wide;
         a.V = int32_t(c.V);
         a.parts = reinterpret_cast<float2 *>(ws + f.parts);
-        a.target_logit = reinterpret_cast<float *>(ws + f.target_logit);
-        a.x = c.x + t0 * c.ld_x;
+        a.target_logit = target_logit + t0;
+        a.x = apart ? nullptr : c.x + t0 * c.ld_x;
         a.w = c.w;
         a.ld_x = c.ld_x;
         a.ld_w = c.ld_w;
@@ -1177,7 +1191,7 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
     Bf16Matrix w = {c.w, c.ld_w, c.V, c.D};
     if (f.w >= 0) w = {reinterpret_cast<uint16_t *>(ws + f.w), x.ld, c.V, c.D};
     cudaError_t e = lay_out(c, const_cast<uint16_t *>(x.p), f.w >= 0 ? const_cast<uint16_t *>(w.p) : nullptr,
-                            target_logit, stream);
+                            target_logit, true, stream);
     if (e != cudaSuccess) return e;
     const Bf16Matrix d = {reinterpret_cast<uint16_t *>(ws + f.d), f.piece, c.T, f.piece};
     CUtensorMap logits[4], products[4];
@@ -1192,6 +1206,8 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
     if ((e = describe(&products[3], x, true)) != cudaSuccess) return e;
     float *const sums = f.dx >= 0 ? reinterpret_cast<float *>(ws + f.dx) : nullptr;
     const int64_t size = c.dw_bf16 ? 2 : 4;
+    // one gradient for all losses is applied to the products, after d's rounding
+    const float alpha = c.dlosses ? 1.0f : c.dloss;
 
     for (int64_t v0 = 0; v0 < c.V; v0 += f.piece) {
         const int64_t cols = c.V - v0 < f.piece ? c.V - v0 : f.piece;
@@ -1207,13 +1223,13 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
         a.target_logit = target_logit;
         a.lse = c.lse_in;
         a.dlosses = c.dlosses;
-        a.dloss = c.dloss;
         if ((e = run<kGradient>(logits, a, stream)) != cudaSuccess) return e;
 
         Args p = {};
         if (c.dx) {
             Job &j = p.job[0] = job_of(c.T, c.D, cols, f.width);
             j.mn_j = 1;
+            j.alpha = alpha;
             j.kj_at = int32_t(v0);
             j.split = int32_t(f.split < j.blocks ? f.split : j.blocks);
             if (sums && !(last && f.split == 1)) {
@@ -1236,6 +1252,7 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
         if (c.dw) {
             Job &j = p.job[1] = job_of(cols, c.D, c.T, f.width);
             j.mn_i = j.mn_j = 1;
+            j.alpha = alpha;
             j.out = static_cast<char *>(c.dw) + v0 * c.ld_dw * size;
             j.out_bf16 = c.dw_bf16;
             j.ld_out = c.ld_dw;

@@ -43,7 +43,7 @@ struct Shape {
 template <typename T, typename S>
 constexpr int per_sm() {
     constexpr bool half = sizeof(T) == 2;
-    return S::kThreads == 256 ? (half ? 3 : 2) : 1;
+    return S::kThreads == 256 ? (half ? 3 : 2) : S::kThreads == 512 && half ? 2 : 1;
 }
 
 // Column of the first value of this thread's block of piece p.

@@ -42,6 +42,9 @@ struct Eight<uint16_t> {
             w[1] = q.y;
             w[2] = q.z;
             w[3] = q.w;
+        } else if (left >= kBlock8) {  // (most blocks, without comparisons)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = uint32_t(p[l + 32 * k]) | (uint32_t(p[l + 32 * k + 16]) << 16);
         } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -72,6 +75,12 @@ struct Eight<uint16_t> {
     __device__ __forceinline__ void store(uint16_t *p, int l, int left) const {
         if (VEC) {
             if (8 * l < left) st_stream_u4(p + 8 * l, make_uint4(w[0], w[1], w[2], w[3]));
+        } else if (left >= kBlock8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                p[l + 32 * k] = uint16_t(w[k]);
+                p[l + 32 * k + 16] = uint16_t(w[k] >> 16);
+            }
         } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -102,6 +111,9 @@ struct Eight<float> {
             w[5] = b.y;
             w[6] = b.z;
             w[7] = b.w;
+        } else if (left >= kBlock8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(p[l + 16 * j]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = l + 16 * j < left ? __float_as_uint(p[l + 16 * j]) : 0u;
@@ -129,6 +141,9 @@ struct Eight<float> {
                 st_stream_u4(p + 8 * l, make_uint4(w[0], w[1], w[2], w[3]));
                 st_stream_u4(p + 8 * l + 4, make_uint4(w[4], w[5], w[6], w[7]));
             }
+        } else if (left >= kBlock8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[l + 16 * j] = __uint_as_float(w[j]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
