@@ -103,7 +103,7 @@ __device__ __forceinline__ Place place(int32_t across) {
 }
 
 template <typename T, bool VEC, bool GATED, bool KEEP, int kAcross>
-__global__ void __launch_bounds__(kThreads) act_kernel(const Activation a, int32_t across) {
+__global__ void __launch_bounds__(kThreads, kAcross == 1 ? 5 : sizeof(T) == 2 ? 4 : 3) act_kernel(const Activation a, int32_t across) {
     constexpr bool kFast = sizeof(T) == 2;
     const Place at = place<kAcross>(across);
     const int l = threadIdx.x & 15;
@@ -113,11 +113,11 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const Activation a, int32
     T *h = static_cast<T *>(a.h) + at.row * a.ld_h + at.col;
     const int left = live ? int(min(a.cols - at.col, int64_t(kAcross * kBlock8))) : 0;
 
-    Eight<T> g[kAcross], u[kAcross];
+    Eight<T, VEC> g[kAcross], u[kAcross];
 #pragma unroll
     for (int k = 0; k < kAcross; ++k) {
-        g[k].template load<VEC>(gate + k * kBlock8, l, left - k * kBlock8);
-        if (GATED) u[k].template load<VEC>(up + k * kBlock8, l, left - k * kBlock8);
+        g[k].load(gate + k * kBlock8, l, left - k * kBlock8);
+        if (GATED) u[k].load(up + k * kBlock8, l, left - k * kBlock8);
     }
 #pragma unroll
     for (int k = 0; k < kAcross; ++k) {
@@ -127,9 +127,9 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const Activation a, int32
             x[j] = act<kFast>(a.kind, g[k].at(j));
             if (GATED) x[j] = __fmul_rn(x[j], u[k].at(j));
         }
-        Eight<T> out;
+        Eight<T, VEC> out;
         out.set(x);
-        out.template store<VEC>(h + k * kBlock8, l, left - k * kBlock8);
+        out.store(h + k * kBlock8, l, left - k * kBlock8);
     }
     if (!KEEP) return;
     // a lane divides for one block, gate's first and then up's
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const Activation a, int32
 }
 
 template <typename T, bool VEC, bool GATED, int kAcross>
-__global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActivationGrad a, int32_t across) {
+__global__ void __launch_bounds__(kThreads, kAcross == 1 ? 5 : sizeof(T) == 2 ? 4 : 3) act_grad_kernel(const ActivationGrad a, int32_t across) {
     constexpr bool kFast = sizeof(T) == 2;
     const Place at = place<kAcross>(across);
     const int l = threadIdx.x & 15;
@@ -177,13 +177,13 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActivationGrad
     T *dg = static_cast<T *>(a.dgate) + at.row * a.ld_dgate + at.col;
     T *du = static_cast<T *>(a.dup) + (GATED ? at.row * a.ld_dup + at.col : 0);
 
-    Eight<T> d[kAcross];
+    Eight<T, VEC> d[kAcross];
     uint2 cg[kAcross], cu[kAcross];
     float sg[kAcross], su[kAcross];
 #pragma unroll
     for (int k = 0; k < kAcross; ++k) {
         const int rest = left - k * kBlock8;
-        d[k].template load<VEC>(dh + k * kBlock8, l, rest);
+        d[k].load(dh + k * kBlock8, l, rest);
         cg[k] = load_codes<VEC>(qg + k * kBlock8, l, rest);
         sg[k] = rest > 0 ? a.kept_gate.s[(at.block + k) * a.kept_gate.ld_s + at.row] : 0.0f;
         if (GATED) {
@@ -209,12 +209,12 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActivationGrad
                 x[j] = __fmul_rn(t, df);
             }
         }
-        Eight<T> out;
+        Eight<T, VEC> out;
         out.set(x);
-        out.template store<VEC>(dg + k * kBlock8, l, rest);
+        out.store(dg + k * kBlock8, l, rest);
         if (GATED) {
             out.set(y);
-            out.template store<VEC>(du + k * kBlock8, l, rest);
+            out.store(du + k * kBlock8, l, rest);
         }
     }
 }
@@ -259,8 +259,7 @@ void launch(const Call &a, bool vec, cudaStream_t stream) {
     const bool m = many(a.rows, a.cols);
     if (vec && m) launch<T, true, kMany>(a, stream);
     else if (vec) launch<T, true, 1>(a, stream);
-    else if (m) launch<T, false, kMany>(a, stream);
-    else launch<T, false, 1>(a, stream);
+    else launch<T, false, 1>(a, stream);  // (many instructions, so rather many warps)
 }
 
 template <typename T>

@@ -38,9 +38,9 @@ __global__ void __launch_bounds__(kThreads) fp8_dequant_kernel(const Fp8Dequant 
     for (int k = 0; k < kAcross; ++k) {
         float x[8];
         values_of(codes[k], scale[k], x);
-        Eight<T> v;
+        Eight<T, VEC> v;
         v.set(x);
-        v.template store<VEC>(out + k * kBlock8, l, left - k * kBlock8);
+        v.store(out + k * kBlock8, l, left - k * kBlock8);
     }
 }
 

@@ -43,7 +43,7 @@ struct Shape {
 template <typename T, typename S>
 constexpr int per_sm() {
     constexpr bool half = sizeof(T) == 2;
-    return S::kThreads == 256 ? (half ? 3 : 2) : S::kThreads == 512 && half ? 2 : 1;
+    return S::kThreads == 256 ? (half || S::kPieces == 1 ? 3 : 2) : S::kThreads == 512 && (half || S::kPieces == 1) ? 2 : 1;
 }
 
 // Column of the first value of this thread's block of piece p.
@@ -99,8 +99,8 @@ __device__ __forceinline__ float inverse_root(float v) {
     return v > 0.0f && v < INFINITY ? __fmaf_rn(__fmul_rn(r, 0.5f), e, r) : r;
 }
 
-template <typename T>
-__device__ __forceinline__ f32x2 pair_of(const Eight<T> &v, int k) {
+template <typename T, bool VEC>
+__device__ __forceinline__ f32x2 pair_of(const Eight<T, VEC> &v, int k) {
     return pack2(v.at(2 * k), v.at(2 * k + 1));
 }
 
@@ -122,13 +122,13 @@ __global__ void __launch_bounds__(S::kThreads, per_sm<T, S>()) rms_norm_kernel(c
 #pragma unroll
         for (int k = 0; k < 4; ++k) weight[p][k] = pack2(w[2 * k], w[2 * k + 1]);
     }
-    Eight<T> x[PIECES], o[PIECES];
+    Eight<T, VEC> x[PIECES], o[PIECES];
     auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int p = 0; p < PIECES; ++p) {
             const int col = block_column<S>(in_row, p), left = row < a.rows ? cols - col : 0;
-            x[p].template load<VEC>(static_cast<const T *>(a.x) + row * a.ld_x + col, l, left);
-            if (a.add) o[p].template load<VEC>(static_cast<const T *>(a.add) + row * a.ld_add + col, l, left);
+            x[p].load(static_cast<const T *>(a.x) + row * a.ld_x + col, l, left);
+            if (a.add) o[p].load(static_cast<const T *>(a.add) + row * a.ld_add + col, l, left);
         }
     };
     // every row group of a CTA takes as many turns, for the CTA's barriers
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(S::kThreads, per_sm<T, S>()) rms_norm_kernel(c
     fetch(row);
     for (int64_t i = 0; i < turns; ++i, row += step) {
         const bool live = row < a.rows;
-        Eight<T> t[PIECES];
+        Eight<T, VEC> t[PIECES];
         f32x2 sum = zero;
 #pragma unroll
         for (int p = 0; p < PIECES; ++p) {
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(S::kThreads, per_sm<T, S>()) rms_norm_kernel(c
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s[j] = __fadd_rn(x[p].at(j), o[p].at(j));
                 t[p].set(s);
-                t[p].template store<VEC>(static_cast<T *>(a.total) + row * a.ld_total + col, l, live ? cols - col : 0);
+                t[p].store(static_cast<T *>(a.total) + row * a.ld_total + col, l, live ? cols - col : 0);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) sum = fma2_rn(pair_of(t[p], k), pair_of(t[p], k), sum);
@@ -166,15 +166,15 @@ __global__ void __launch_bounds__(S::kThreads, per_sm<T, S>()) rms_norm_kernel(c
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 unpack2(fma2_rn(fma2_rn(pair_of(t[p], k), rr, zero), weight[p][k], zero), y[2 * k], y[2 * k + 1]);
-            Eight<T> out;
+            Eight<T, VEC> out;
             out.set(y);
-            out.template store<VEC>(static_cast<T *>(a.y) + row * a.ld_y + col, l, live ? cols - col : 0);
+            out.store(static_cast<T *>(a.y) + row * a.ld_y + col, l, live ? cols - col : 0);
         }
         if (a.kept.q == nullptr) continue;
         if (in_row == 0 && live) a.rstd[row] = r;
         // a lane divides for one piece: the even ones for the first, the odd ones for the second
         uint32_t mine = block_max(t[0].mag());
-        if (PIECES == 2) {
+        if (PIECES > 1) {
             const uint32_t second = block_max(t[PIECES - 1].mag());
             if (l & 1) mine = second;
         }
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(S::kThreads, per_sm<T, S>()) rms_norm_kernel(c
 // CTAs of the gradient that an SM holds at once.
 template <typename S>
 struct Plan {
-    static constexpr int kCtas = S::kThreads == 256 ? 2 : 1;
+    static constexpr int kCtas = S::kThreads == 256 ? (S::kPieces == 1 ? 3 : 2) : S::kThreads == 512 && S::kPieces == 1 ? 2 : 1;
     // the groups' sums, where a CTA has several
     static constexpr int kSums = S::kRows > 1 ? S::kThreads * S::kPieces * 8 : 1;
     static int64_t ctas(int64_t rows) {
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(S::kThreads, Plan<S>::kCtas) rms_norm_grad_ker
         }
     }
     // the next row
-    Eight<T> dy[PIECES], add[PIECES];
+    Eight<T, VEC> dy[PIECES], add[PIECES];
     uint2 codes[PIECES];
     float scale[PIECES], r = 0.0f;
     auto fetch = [&](int64_t row) {
@@ -239,23 +239,23 @@ __global__ void __launch_bounds__(S::kThreads, Plan<S>::kCtas) rms_norm_grad_ker
 #pragma unroll
         for (int p = 0; p < PIECES; ++p) {
             const int col = block_column<S>(in_row, p), left = live ? cols - col : 0;
-            dy[p].template load<VEC>(static_cast<const T *>(a.dy) + row * a.ld_dy + col, l, left);
+            dy[p].load(static_cast<const T *>(a.dy) + row * a.ld_dy + col, l, left);
             codes[p] = load_codes<VEC>(a.kept.q + row * a.kept.ld_q + col, l, left);
             scale[p] = left > 0 ? a.kept.s[col / kBlock8 * a.kept.ld_s + row] : 0.0f;
-            if (a.add) add[p].template load<VEC>(static_cast<const T *>(a.add) + row * a.ld_add + col, l, left);
+            if (a.add) add[p].load(static_cast<const T *>(a.add) + row * a.ld_add + col, l, left);
             else add[p].zero();
         }
     };
     // every row group of a CTA takes as many turns, for the CTA's barriers
     const int64_t turns = (a.rows - first + step - 1) / step;
     int64_t row = first + me / S::kTpr;
-    constexpr bool kAhead = S::kThreads < 1024;  // (1024 threads have no registers for it)
+    constexpr bool kAhead = S::kThreads * PIECES < 2048;  // (the longest rows leave no registers for it)
     if (kAhead) fetch(row);
     for (int64_t i = 0; i < turns; ++i, row += step) {
         if (!kAhead) fetch(row);
         // n, and dy * w
         f32x2 n[PIECES][4], wd[PIECES][4], sum = zero;
-        Eight<T> past[PIECES];
+        Eight<T, VEC> past[PIECES];
         const f32x2 rr = pack2(r, r);
 #pragma unroll
         for (int p = 0; p < PIECES; ++p) {
@@ -283,9 +283,9 @@ __global__ void __launch_bounds__(S::kThreads, Plan<S>::kCtas) rms_norm_grad_ker
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 unpack2(fma2_rn(fma2_rn(n[p][k], mm, wd[p][k]), rr, pair_of(past[p], k)), x[2 * k], x[2 * k + 1]);
-            Eight<T> out;
+            Eight<T, VEC> out;
             out.set(x);
-            out.template store<VEC>(static_cast<T *>(a.dx) + row * a.ld_dx + col, l, row < a.rows ? cols - col : 0);
+            out.store(static_cast<T *>(a.dx) + row * a.ld_dx + col, l, row < a.rows ? cols - col : 0);
         }
     }
     // the CTA's sum over its groups
@@ -349,15 +349,24 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float *partials, in
 }
 
 // f(the shape of rows of `cols` columns).
-template <typename F>
+template <bool VEC, typename F>
 auto with_shape(int64_t cols, F f) {
     if (cols <= Shape<16, 1>::kCols) return f(Shape<16, 1>());
     if (cols <= Shape<32, 1>::kCols) return f(Shape<32, 1>());
-    if (cols <= Shape<32, 2>::kCols) return f(Shape<32, 2>());
-    if (cols <= Shape<64, 2>::kCols) return f(Shape<64, 2>());
-    if (cols <= Shape<128, 2>::kCols) return f(Shape<128, 2>());
-    if (cols <= Shape<256, 2>::kCols) return f(Shape<256, 2>());
-    if (cols <= Shape<512, 2>::kCols) return f(Shape<512, 2>());
+    if constexpr (VEC) {
+        if (cols <= Shape<32, 2>::kCols) return f(Shape<32, 2>());
+        if (cols <= Shape<64, 2>::kCols) return f(Shape<64, 2>());
+        if (cols <= Shape<128, 2>::kCols) return f(Shape<128, 2>());
+        if (cols <= Shape<256, 2>::kCols) return f(Shape<256, 2>());
+        if (cols <= Shape<512, 2>::kCols) return f(Shape<512, 2>());
+    } else {
+        // value by value: more instructions, so more warps to hide their latency
+        if (cols <= Shape<64, 1>::kCols) return f(Shape<64, 1>());
+        if (cols <= Shape<128, 1>::kCols) return f(Shape<128, 1>());
+        if (cols <= Shape<256, 1>::kCols) return f(Shape<256, 1>());
+        if (cols <= Shape<512, 1>::kCols) return f(Shape<512, 1>());
+        if (cols <= Shape<1024, 1>::kCols) return f(Shape<1024, 1>());
+    }
     static_assert(Shape<1024, 2>::kCols == kNormCols, "the largest shape has the longest row");
     return f(Shape<1024, 2>());
 }
@@ -368,7 +377,7 @@ bool vector_rows(const void *p, int64_t ld, bool bf16) {
 
 template <typename T, bool VEC>
 void launch(const RmsNorm &a, cudaStream_t stream) {
-    with_shape(a.cols, [&](auto shape) {
+    with_shape<VEC>(a.cols, [&](auto shape) {
         using S = decltype(shape);
         const int64_t need = (a.rows + S::kRows - 1) / S::kRows, most = int64_t(kSms) * per_sm<T, S>();
         rms_norm_kernel<T, VEC, S><<<uint32_t(need < most ? need : most), S::kThreads, 0, stream>>>(a);
@@ -378,15 +387,16 @@ void launch(const RmsNorm &a, cudaStream_t stream) {
 
 template <typename T, bool VEC>
 void launch(const RmsNormGrad &a, cudaStream_t stream) {
-    with_shape(a.cols, [&](auto shape) {
+    with_shape<VEC>(a.cols, [&](auto shape) {
         using S = decltype(shape);
         rms_norm_grad_kernel<T, VEC, S><<<uint32_t(Plan<S>::ctas(a.rows)), S::kThreads, 0, stream>>>(a);
         return 0;
     });
 }
 
-int64_t grad_ctas(int64_t rows, int64_t cols) {
-    return with_shape(cols, [&](auto shape) { return Plan<decltype(shape)>::ctas(rows); });
+int64_t grad_ctas(int64_t rows, int64_t cols, bool vec) {
+    auto ctas = [&](auto shape) { return Plan<decltype(shape)>::ctas(rows); };
+    return vec ? with_shape<true>(cols, ctas) : with_shape<false>(cols, ctas);
 }
 
 }  // namespace
@@ -402,7 +412,10 @@ cudaError_t launch_rms_norm(const RmsNorm &a, cudaStream_t stream) {
     return cudaPeekAtLastError();
 }
 
-int64_t rms_norm_grad_partials(int64_t rows, int64_t cols) { return cols * grad_ctas(rows, cols); }
+int64_t rms_norm_grad_partials(int64_t rows, int64_t cols) {
+    const int64_t a = grad_ctas(rows, cols, true), b = grad_ctas(rows, cols, false);
+    return cols * (a > b ? a : b);
+}
 
 cudaError_t launch_rms_norm_grad(const RmsNormGrad &a, cudaStream_t stream) {
     const bool vec = a.cols % 8 == 0 && vector_rows(a.dy, a.ld_dy, a.bf16) && vector_rows(a.add, a.ld_add, a.bf16) &&
@@ -415,7 +428,7 @@ cudaError_t launch_rms_norm_grad(const RmsNormGrad &a, cudaStream_t stream) {
         const cudaError_t e = cudaPeekAtLastError();
         if (e != cudaSuccess) return e;
     }
-    const int64_t count = a.rows > 0 ? grad_ctas(a.rows, a.cols) : 0;
+    const int64_t count = a.rows > 0 ? grad_ctas(a.rows, a.cols, vec) : 0;
     return launch_after(dweight_kernel, dim3(uint32_t((a.cols + 31) / 32)), dim3(1024), 0, stream, 1,
                         static_cast<const float *>(a.partials), count, int(a.cols), a.dweight,
                         a.dweight_bf16 ? 1 : 0, a.accumulate ? 1 : 0);

@@ -25,34 +25,23 @@ __device__ __forceinline__ int column_of(int l, int j) {
     return VEC ? 8 * l + j : l + 16 * j;
 }
 
-// Values as they are stored: bf16 two to a word.  mag(): the largest magnitude's
-// encoding, in which infinities and NaN are above all finite values.
-template <typename T>
+// Values as they are stored: bf16 two to a word where they come so, else one to a
+// word, as a load leaves it, so that nothing waits for it before the value is used.
+// `p`: the block's first value, `left`: columns from there to the row's end.  mag():
+// the largest magnitude's encoding, in which infinities and NaN are above all finite
+// values.
+template <typename T, bool VEC>
 struct Eight;
 
 template <>
-struct Eight<uint16_t> {
+struct Eight<uint16_t, true> {
     uint32_t w[4];
-    // `p`: the block's first value, `left`: columns from there to the row's end
-    template <bool VEC>
     __device__ __forceinline__ void load(const uint16_t *p, int l, int left) {
-        if (VEC) {
-            const uint4 q = 8 * l < left ? ld_stream_u4(p + 8 * l) : make_uint4(0u, 0u, 0u, 0u);
-            w[0] = q.x;
-            w[1] = q.y;
-            w[2] = q.z;
-            w[3] = q.w;
-        } else if (left >= kBlock8) {  // (most blocks, without comparisons)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = uint32_t(p[l + 32 * k]) | (uint32_t(p[l + 32 * k + 16]) << 16);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int c = l + 32 * k;
-                const uint32_t lo = c < left ? p[c] : 0u, hi = c + 16 < left ? p[c + 16] : 0u;
-                w[k] = lo | (hi << 16);
-            }
-        }
+        const uint4 q = 8 * l < left ? ld_stream_u4(p + 8 * l) : make_uint4(0u, 0u, 0u, 0u);
+        w[0] = q.x;
+        w[1] = q.y;
+        w[2] = q.z;
+        w[3] = q.w;
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -71,31 +60,57 @@ struct Eight<uint16_t> {
 #pragma unroll
         for (int k = 0; k < 4; ++k) w[k] = f32x2_to_bf16x2_bits(x[2 * k], x[2 * k + 1]);
     }
-    template <bool VEC>
     __device__ __forceinline__ void store(uint16_t *p, int l, int left) const {
-        if (VEC) {
-            if (8 * l < left) st_stream_u4(p + 8 * l, make_uint4(w[0], w[1], w[2], w[3]));
-        } else if (left >= kBlock8) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                p[l + 32 * k] = uint16_t(w[k]);
-                p[l + 32 * k + 16] = uint16_t(w[k] >> 16);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int c = l + 32 * k;
-                if (c < left) p[c] = uint16_t(w[k]);
-                if (c + 16 < left) p[c + 16] = uint16_t(w[k] >> 16);
-            }
-        }
+        if (8 * l < left) st_stream_u4(p + 8 * l, make_uint4(w[0], w[1], w[2], w[3]));
     }
 };
 
 template <>
-struct Eight<float> {
+struct Eight<uint16_t, false> {
     uint32_t w[8];
-    template <bool VEC>
+    __device__ __forceinline__ void load(const uint16_t *p, int l, int left) {
+        if (left >= kBlock8) {  // (most blocks, without comparisons)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = p[l + 16 * j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = l + 16 * j < left ? p[l + 16 * j] : 0u;
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 0u;
+    }
+    __device__ __forceinline__ float at(int j) const { return __uint_as_float(w[j] << 16); }
+    __device__ __forceinline__ uint32_t mag() const {
+        uint32_t m = w[0] & 0x7FFFu;
+#pragma unroll
+        for (int j = 1; j < 8; ++j) m = max(m, w[j] & 0x7FFFu);
+        return m << 16;
+    }
+    __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t both = f32x2_to_bf16x2_bits(x[2 * k], x[2 * k + 1]);
+            w[2 * k] = both & 0xFFFFu;
+            w[2 * k + 1] = both >> 16;
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t *p, int l, int left) const {
+        if (left >= kBlock8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[l + 16 * j] = uint16_t(w[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (l + 16 * j < left) p[l + 16 * j] = uint16_t(w[j]);
+        }
+    }
+};
+
+template <bool VEC>
+struct Eight<float, VEC> {
+    uint32_t w[8];
     __device__ __forceinline__ void load(const float *p, int l, int left) {
         if (VEC) {
             uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
@@ -134,7 +149,6 @@ struct Eight<float> {
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[j]);
     }
-    template <bool VEC>
     __device__ __forceinline__ void store(float *p, int l, int left) const {
         if (VEC) {
             if (8 * l < left) {
