@@ -487,6 +487,9 @@ WC_API int wc_fp8_dequant(const uint8_t *q, int64_t ld_q, const float *s, int64_
                           int64_t ld_out, void *stream);
 
 /*
+ * (In the calls from here on every row distance is below 2^38 values, and rows times
+ * it at most 2^60.)
+ *
  * A matrix kept in 8 bits from the forward to the backward pass: codes
  * [rows][ld_codes] and scales [ceil(cols/128)][ld_scales] by the rule of
  * wc_fp8_quant, one scale per 128 values of a row.  ld_codes is a multiple of 16

@@ -507,10 +507,13 @@ int values_pointer(const char *fn, const char *name, const void *p, int dtype) {
     return WC_OK;
 }
 
-int row_pitch(const char *fn, const char *name, int64_t ld, int64_t cols) {
+// Rows at most 2^38 values apart (what a TMA descriptor takes), and offsets of 2^60
+// values at most.
+int row_pitch(const char *fn, const char *name, int64_t ld, int64_t rows, int64_t cols) {
     if (ld < cols)
         return fail(WC_EINVAL, "%s: ld_%s = %lld is below %lld columns", fn, name, (long long)ld, (long long)cols);
-    if (ld >= (int64_t(1) << 40)) return fail(WC_ERANGE, "%s: ld_%s reaches 2^40", fn, name);
+    if (ld >= (int64_t(1) << 38) || (rows > 0 && ld >= (int64_t(1) << 60) / rows))
+        return fail(WC_ERANGE, "%s: ld_%s = %lld is too large", fn, name, (long long)ld);
     return WC_OK;
 }
 
@@ -540,6 +543,8 @@ int kept_matrix(const char *fn, const char *name, const wc_kept *k, int64_t rows
     if (k->ld_codes % 16 || k->ld_codes < cols)
         return fail(WC_EINVAL, "%s: ld_codes = %lld of %s must be a multiple of 16 and at least cols", fn,
                     (long long)k->ld_codes, name);
+    if (k->ld_codes >= (int64_t(1) << 38) || k->ld_scales >= (int64_t(1) << 38))
+        return fail(WC_ERANGE, "%s: ld_codes or ld_scales of %s reaches 2^38", fn, name);
     if (k->ld_scales < rows)
         return fail(WC_EINVAL, "%s: ld_scales = %lld of %s does not hold a block's scales", fn,
                     (long long)k->ld_scales, name);
@@ -570,8 +575,8 @@ int cross_entropy_sizes(const char *fn, const uint16_t *x, int64_t ld_x, const u
     if (T >= (int64_t(1) << 44) / V) return fail(WC_ERANGE, "%s: T * V reaches 2^44", fn);
     if (T >= (int64_t(1) << 40) / D || V >= (int64_t(1) << 40) / D)
         return fail(WC_ERANGE, "%s: T * D or V * D reaches 2^40", fn);
-    int rc = row_pitch(fn, "x", ld_x, D);
-    if (rc == WC_OK) rc = row_pitch(fn, "w", ld_w, D);
+    int rc = row_pitch(fn, "x", ld_x, T, D);
+    if (rc == WC_OK) rc = row_pitch(fn, "w", ld_w, V, D);
     if (rc != WC_OK) return rc;
     c->x = x;
     c->w = w;
@@ -800,7 +805,9 @@ WC_API int wc_fp8_dequant(const uint8_t *q, int64_t ld_q, const float *s, int64_
         return fail(WC_EINVAL, "%s: ld_q = %lld must be a multiple of 16 and at least cols", fn, (long long)ld_q);
     if (ld_s < (rows_per_scale == 128 ? blocks128(rows) : rows))
         return fail(WC_EINVAL, "%s: ld_s = %lld does not hold a block's scales", fn, (long long)ld_s);
-    if ((rc = row_pitch(fn, "out", ld_out, cols)) != WC_OK) return rc;
+    if ((rc = row_pitch(fn, "out", ld_out, rows, cols)) != WC_OK) return rc;
+    if (ld_q >= (int64_t(1) << 38) || ld_s >= (int64_t(1) << 38))
+        return fail(WC_ERANGE, "%s: ld_q or ld_s reaches 2^38", fn);
     if (rows == 0 || cols == 0) return WC_OK;
     WC_REQUIRE_PTR(fn, q);
     WC_REQUIRE_PTR(fn, s);
@@ -815,9 +822,9 @@ WC_API int wc_activation(const void *gate, int64_t ld_gate, const void *up, int6
     static const char *fn = "wc_activation";
     int rc = block_sizes(fn, rows, cols);
     if (rc == WC_OK) rc = activation_kind(fn, dtype, kind);
-    if (rc == WC_OK) rc = row_pitch(fn, "gate", ld_gate, cols);
-    if (rc == WC_OK && up) rc = row_pitch(fn, "up", ld_up, cols);
-    if (rc == WC_OK) rc = row_pitch(fn, "h", ld_h, cols);
+    if (rc == WC_OK) rc = row_pitch(fn, "gate", ld_gate, rows, cols);
+    if (rc == WC_OK && up) rc = row_pitch(fn, "up", ld_up, rows, cols);
+    if (rc == WC_OK) rc = row_pitch(fn, "h", ld_h, rows, cols);
     if (rc != WC_OK) return rc;
     if (rows == 0 || cols == 0) return WC_OK;
     if ((kept_up != nullptr) != (up != nullptr && kept_gate != nullptr))
@@ -847,9 +854,9 @@ WC_API int wc_activation_grad(const void *dh, int64_t ld_dh, int dtype, int kind
     static const char *fn = "wc_activation_grad";
     int rc = block_sizes(fn, rows, cols);
     if (rc == WC_OK) rc = activation_kind(fn, dtype, kind);
-    if (rc == WC_OK) rc = row_pitch(fn, "dh", ld_dh, cols);
-    if (rc == WC_OK) rc = row_pitch(fn, "dgate", ld_dgate, cols);
-    if (rc == WC_OK && dup) rc = row_pitch(fn, "dup", ld_dup, cols);
+    if (rc == WC_OK) rc = row_pitch(fn, "dh", ld_dh, rows, cols);
+    if (rc == WC_OK) rc = row_pitch(fn, "dgate", ld_dgate, rows, cols);
+    if (rc == WC_OK && dup) rc = row_pitch(fn, "dup", ld_dup, rows, cols);
     if (rc != WC_OK) return rc;
     if (rows == 0 || cols == 0) return WC_OK;
     if (kept_gate == nullptr) return fail(WC_EINVAL, "%s: kept_gate is NULL", fn);
@@ -880,10 +887,10 @@ WC_API int wc_rms_norm(const void *x, int64_t ld_x, const void *add, int64_t ld_
                        const wc_kept *kept, void *stream) {
     static const char *fn = "wc_rms_norm";
     int rc = norm_sizes(fn, rows, cols, dtype, weight_dtype);
-    if (rc == WC_OK) rc = row_pitch(fn, "x", ld_x, cols);
-    if (rc == WC_OK && add) rc = row_pitch(fn, "add", ld_add, cols);
-    if (rc == WC_OK) rc = row_pitch(fn, "y", ld_y, cols);
-    if (rc == WC_OK && add) rc = row_pitch(fn, "total", ld_total, cols);
+    if (rc == WC_OK) rc = row_pitch(fn, "x", ld_x, rows, cols);
+    if (rc == WC_OK && add) rc = row_pitch(fn, "add", ld_add, rows, cols);
+    if (rc == WC_OK) rc = row_pitch(fn, "y", ld_y, rows, cols);
+    if (rc == WC_OK && add) rc = row_pitch(fn, "total", ld_total, rows, cols);
     if (rc != WC_OK) return rc;
     if (!(eps >= 0.0 && eps < HUGE_VAL)) return fail(WC_EINVAL, "%s: eps = %g must be finite and at least 0", fn, eps);
     if (rows == 0) return WC_OK;
@@ -934,9 +941,9 @@ WC_API int wc_rms_norm_grad(const void *dy, int64_t ld_dy, const void *add, int6
     if (rc != WC_OK) return rc;
     if (!float_type(dweight_dtype))
         return fail(WC_EINVAL, "%s: dweight_dtype %d is neither WC_F32 nor WC_BF16", fn, dweight_dtype);
-    if ((rc = row_pitch(fn, "dy", ld_dy, cols)) != WC_OK) return rc;
-    if (add && (rc = row_pitch(fn, "add", ld_add, cols)) != WC_OK) return rc;
-    if ((rc = row_pitch(fn, "dx", ld_dx, cols)) != WC_OK) return rc;
+    if ((rc = row_pitch(fn, "dy", ld_dy, rows, cols)) != WC_OK) return rc;
+    if (add && (rc = row_pitch(fn, "add", ld_add, rows, cols)) != WC_OK) return rc;
+    if ((rc = row_pitch(fn, "dx", ld_dx, rows, cols)) != WC_OK) return rc;
     if ((rc = values_pointer(fn, "dweight", dweight, dweight_dtype)) != WC_OK) return rc;
     wc::RmsNormGrad a = {};
     if (rows > 0) {
@@ -1027,8 +1034,8 @@ WC_API int wc_cross_entropy_grad(const uint16_t *x, int64_t ld_x, const uint16_t
     if (dx == nullptr && dw == nullptr) return fail(WC_EINVAL, "%s: dx and dw are both NULL", fn);
     if ((dx && !float_type(dx_dtype)) || (dw && !float_type(dw_dtype)))
         return fail(WC_EINVAL, "%s: dx_dtype %d or dw_dtype %d is neither WC_F32 nor WC_BF16", fn, dx_dtype, dw_dtype);
-    if (dx && (rc = row_pitch(fn, "dx", ld_dx, D)) != WC_OK) return rc;
-    if (dw && (rc = row_pitch(fn, "dw", ld_dw, D)) != WC_OK) return rc;
+    if (dx && (rc = row_pitch(fn, "dx", ld_dx, T, D)) != WC_OK) return rc;
+    if (dw && (rc = row_pitch(fn, "dw", ld_dw, V, D)) != WC_OK) return rc;
     if ((rc = cross_entropy_inputs(fn, &c, targets, id_type)) != WC_OK) return rc;
     if (dw && (rc = values_pointer(fn, "dw", dw, dw_dtype)) != WC_OK) return rc;
     if (T == 0) {

@@ -587,11 +587,13 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                             // (padding tokens have no gradient whatever their logits are)
                             x[k] = c + k >= last ? 0.0f : target - c == k ? own : x[k];
                     }
-                    stage_bf16(staging, x, lane);
-                    __syncwarp();
-                    store_staged(staging, static_cast<char *>(job.out) + (int64_t(row0) * job.ld_out + col0 + c) * 2,
-                                 job.ld_out * 2, job.rows_i - row0, lane);
-                    __syncwarp();
+                    if (col0 + c < job.ld_out) {  // (tiles of 192 columns may go past the buffer's rows)
+                        stage_bf16(staging, x, lane);
+                        __syncwarp();
+                        store_staged(staging, static_cast<char *>(job.out) + (int64_t(row0) * job.ld_out + col0 + c) * 2,
+                                     job.ld_out * 2, job.rows_i - row0, lane);
+                        __syncwarp();
+                    }
                 } else {
                     float x[32];
 #pragma unroll
@@ -888,7 +890,8 @@ cudaError_t describe(CUtensorMap *map, const Bf16Matrix &m, bool mn, int rows = 
     const cudaError_t e = encoder(&encode);
     if (e != cudaSuccess) return e;
     const cuuint64_t dims[2] = {cuuint64_t(m.cols), cuuint64_t(m.rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(m.ld) * 2};
+    // (a single row is apart from none)
+    const cuuint64_t strides[1] = {cuuint64_t(m.rows > 1 ? m.ld : ceil_div(m.cols, 8) * 8) * 2};
     const cuuint32_t box[2] = {64, cuuint32_t(mn ? 64 : rows)};
     const cuuint32_t step[2] = {1, 1};
     const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(m.p), dims, strides,
