@@ -196,9 +196,10 @@ __global__ void __launch_bounds__(S::kThreads, per_sm<T, S>()) rms_norm_kernel(c
 }
 
 // CTAs of the gradient that an SM holds at once.
-template <typename S>
+template <bool VEC, typename S>
 struct Plan {
-    static constexpr int kCtas = S::kPieces == 1 ? 1024 / S::kThreads : S::kThreads == 256 ? 2 : 1;
+    static constexpr int kCtas = S::kThreads == 256 ? (S::kPieces == 2 ? 2 : VEC ? 3 : 4)
+                                 : S::kThreads == 512 && S::kPieces == 1 ? 2 : 1;
     // the groups' sums, where a CTA has several
     static constexpr int kSums = S::kRows > 1 ? S::kThreads * S::kPieces * 8 : 1;
     static int64_t ctas(int64_t rows) {
@@ -208,10 +209,10 @@ struct Plan {
 };
 
 template <typename T, bool VEC, typename S>
-__global__ void __launch_bounds__(S::kThreads, Plan<S>::kCtas) rms_norm_grad_kernel(const RmsNormGrad a) {
+__global__ void __launch_bounds__(S::kThreads, Plan<VEC, S>::kCtas) rms_norm_grad_kernel(const RmsNormGrad a) {
     constexpr int PIECES = S::kPieces;
     __shared__ float slots[2][S::kThreads / 32];
-    __shared__ float sums[Plan<S>::kSums];
+    __shared__ float sums[Plan<VEC, S>::kSums];
     const int me = threadIdx.x, in_row = me % S::kTpr, l = in_row & 15;
     const int64_t first = int64_t(blockIdx.x) * S::kRows, step = int64_t(gridDim.x) * S::kRows;
     const int cols = int(a.cols);
@@ -391,14 +392,14 @@ template <typename T, bool VEC>
 void launch(const RmsNormGrad &a, cudaStream_t stream) {
     with_shape<VEC>(a.cols, [&](auto shape) {
         using S = decltype(shape);
-        rms_norm_grad_kernel<T, VEC, S><<<uint32_t(Plan<S>::ctas(a.rows)), S::kThreads, 0, stream>>>(a);
+        rms_norm_grad_kernel<T, VEC, S><<<uint32_t(Plan<VEC, S>::ctas(a.rows)), S::kThreads, 0, stream>>>(a);
         return 0;
     });
 }
 
 int64_t grad_ctas(int64_t rows, int64_t cols, bool vec) {
-    auto ctas = [&](auto shape) { return Plan<decltype(shape)>::ctas(rows); };
-    return vec ? with_shape<true>(cols, ctas) : with_shape<false>(cols, ctas);
+    if (vec) return with_shape<true>(cols, [&](auto shape) { return Plan<true, decltype(shape)>::ctas(rows); });
+    return with_shape<false>(cols, [&](auto shape) { return Plan<false, decltype(shape)>::ctas(rows); });
 }
 
 }  // namespace
