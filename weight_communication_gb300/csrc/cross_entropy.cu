@@ -153,7 +153,31 @@ struct Row {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
+    __device__ __forceinline__ bool chunks_at(int32_t d) const { return d + 8 <= D && end - (p + d) >= 16; }
 };
+
+// Eight values each of N places, row[k] at d + k * step, with all loads under way at
+// once (one place after the other waits for each: 1 x 32001 x 2047 81 us, so 46).
+template <int N>
+__device__ __forceinline__ void values_at(const Row (&row)[N], int32_t d, int32_t step, uint4 (&q)[N]) {
+    bool inside = true;
+#pragma unroll
+    for (int k = 0; k < N; ++k) inside = inside && row[k].chunks_at(d + k * step);
+    if (inside) {
+        uint32_t t[N][8];
+#pragma unroll
+        for (int k = 0; k < N; ++k) load_chunks(row[k].p + d + k * step, t[k]);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            uint32_t w[4];
+            shift_words(row[k].p + d + k * step, t[k], w);
+            q[k] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) q[k] = row[k].at(d + k * step);
+    }
+}
 
 __device__ __forceinline__ Row row_of(const uint16_t *p, int64_t ld, int64_t rows, int32_t D, int64_t r) {
     return {p + r * ld, p + (rows - 1) * ld + D, D};
@@ -163,13 +187,11 @@ __device__ __forceinline__ Row row_of(const uint16_t *p, int64_t ld, int64_t row
 __device__ __forceinline__ float row_dot(const Row &x, const Row &w, int lane) {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     int32_t d = 8 * lane;
+    const Row xs[4] = {x, x, x, x}, ws[4] = {w, w, w, w};
     for (; d + 768 < x.D; d += 1024) {
         uint4 a[4], b[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            a[k] = x.at(d + 256 * k);
-            b[k] = w.at(d + 256 * k);
-        }
+        values_at(xs, d, 256, a);
+        values_at(ws, d, 256, b);
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[k] = dot8(a[k], b[k], s[k]);
     }
@@ -180,13 +202,16 @@ __device__ __forceinline__ float row_dot(const Row &x, const Row &w, int lane) {
     return sum;
 }
 
-// Tile order: bands of 16 tiles of i, all of j within a band, so that the CTAs
-// at work together share operand rows in L2.
+// Tile order: bands of tiles of i, all of j within a band, so that the CTAs at work
+// together share operand rows in L2.  Where j has few tiles a band is no higher than
+// that all of them are at work at once (16 tiles high, the gradients' products of
+// 8192 x 32000 x 2048 read 1.67 GB from memory for each piece, so 1.40: 585 -> 575 us).
 __device__ __forceinline__ void tile_at(const Job &a, int32_t t, int32_t *ti, int32_t *tj) {
-    const int32_t band = t / (16 * a.tiles_j);
-    const int32_t first = band * 16;
-    const int32_t high = min(16, a.tiles_i - first);
-    const int32_t in = t - band * 16 * a.tiles_j;
+    const int32_t height = a.tiles_j >= 16 ? 16 : kSms / 2 / a.tiles_j;
+    const int32_t band = t / (height * a.tiles_j);
+    const int32_t first = band * height;
+    const int32_t high = min(height, a.tiles_i - first);
+    const int32_t in = t - band * height * a.tiles_j;
     *ti = first + in % high;
     *tj = in / high;
 }
@@ -645,7 +670,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
 // The forward pass of up to T tokens, one reading of w at the memory's rate: a warp
 // has ROWS rows of w at a time, their products with all tokens (fp32 in shared
 // memory) in fp32, and the tokens' maxima and sums over its rows in registers.
-// (One token, 32000 x 2048: 22 us of 19.4 at the copy rate; the tensor cores, with
+// (One token, 32000 x 2048: 25 us with the join, 19.4 at the copy rate; the tensor cores, with
 // 256 rows for it, 38.)
 constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 
@@ -699,8 +724,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
 #pragma unroll
                     for (int r = 0; r < ROWS; ++r) q[r] = ld_stream_u4(row[r].p + d);
                 } else {
-#pragma unroll
-                    for (int r = 0; r < ROWS; ++r) q[r] = row[r].at(d);
+                    values_at(row, d, 0, q);
                 }
 #pragma unroll
                 for (int t = 0; t < T; ++t) {
@@ -821,16 +845,15 @@ __global__ void __launch_bounds__(256) lay_out_kernel(const LayOuts a) {
     const int32_t ld = (a.D + 7) & ~7;
     for (int64_t r = cta * 8 + (threadIdx.x >> 5); r < m.rows; r += ctas * 8) {
         const int32_t y = of_x && a.target_logit ? target_of(a.targets, a.wide, a.V, r) : 0;
-        const Row row = row_of(m.src, m.ld, m.rows, a.D, r);
+        const Row row = row_of(m.src, m.ld, m.rows, a.D, r), rows[4] = {row, row, row, row};
         uint16_t *to = m.dst + r * ld;
         const bool zero = y < 0 && a.mask;
         int32_t c = m.dst ? 8 * lane : ld;
         for (; c + 768 < ld; c += 1024) {
             uint4 q[4];
+            values_at(rows, c, 256, q);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) q[k] = zero ? make_uint4(0u, 0u, 0u, 0u) : row.at(c + 256 * k);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(to + c + 256 * k) = q[k];
+            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(to + c + 256 * k) = zero ? make_uint4(0u, 0u, 0u, 0u) : q[k];
         }
         for (; c < ld; c += 256) *reinterpret_cast<uint4 *>(to + c) = zero ? make_uint4(0u, 0u, 0u, 0u) : row.at(c);
         if (!of_x || a.target_logit == nullptr || y < 0) continue;
@@ -962,8 +985,8 @@ struct Layout {
 };
 
 // Rows of w that a warp has at a time: four share a token's values, and one keeps
-// more of the GPU busy where rows are few (4 x 1043 x 3009: 24 us with four).
-int64_t few_rows(const CrossEntropy &c) { return c.V > 4 * kSms * kFewWarps ? 4 : 1; }
+// more of the GPU busy where rows are few (4 x 1043 x 3009: 24 us with four, 14 with one).
+int64_t few_rows(const CrossEntropy &c) { return c.V <= 4 * kSms * kFewWarps ? 1 : 4; }
 
 int64_t few_grid(const CrossEntropy &c) {
     const int64_t ctas = ceil_div(c.V, kFewWarps * few_rows(c));
