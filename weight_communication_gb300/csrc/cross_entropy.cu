@@ -135,67 +135,86 @@ __device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float sum)
 struct Row {
     const uint16_t *p, *end;  // of the row, of the matrix
     int32_t D;
-    // values d .. d + 7, those past the row's end 0
-    __device__ __forceinline__ uint4 at(int32_t d) const {
-        const uint16_t *q = p + d;
-        if (d + 8 <= D && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) return __ldg(reinterpret_cast<const uint4 *>(q));
-        uint32_t w[4];
-        if (d + 8 <= D && end - q >= 16) {  // (the second chunk ends inside the matrix)
-            uint32_t t[8];
-            load_chunks(q, t);
-            shift_words(q, t, w);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t lo = d + 2 * k < D ? q[2 * k] : 0u, hi = d + 2 * k + 1 < D ? q[2 * k + 1] : 0u;
-                w[k] = lo | hi << 16;
-            }
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    __device__ __forceinline__ bool chunks_at(int32_t d) const { return d + 8 <= D && end - (p + d) >= 16; }
 };
-
-// Eight values each of N places, row[k] at d + k * step, with all loads under way at
-// once (one place after the other waits for each: 1 x 32001 x 2047 81 us, so 46).
-template <int N>
-__device__ __forceinline__ void values_at(const Row (&row)[N], int32_t d, int32_t step, uint4 (&q)[N]) {
-    bool inside = true;
-#pragma unroll
-    for (int k = 0; k < N; ++k) inside = inside && row[k].chunks_at(d + k * step);
-    if (inside) {
-        uint32_t t[N][8];
-#pragma unroll
-        for (int k = 0; k < N; ++k) load_chunks(row[k].p + d + k * step, t[k]);
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            uint32_t w[4];
-            shift_words(row[k].p + d + k * step, t[k], w);
-            q[k] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) q[k] = row[k].at(d + k * step);
-    }
-}
 
 __device__ __forceinline__ Row row_of(const uint16_t *p, int64_t ld, int64_t rows, int32_t D, int64_t r) {
     return {p + r * ld, p + (rows - 1) * ld + D, D};
 }
 
+// Eight values each from N places of a matrix that ends at `end`, the n[k] first of them
+// (the rest 0; none if n[k] <= 0).  All loads are under way at once: one place after
+// the other waits for each (1 x 32001 x 2047 81 us, so 46).
+template <int N>
+__device__ __forceinline__ void values_at(const uint16_t *const (&at)[N], const int32_t (&n)[N], const uint16_t *end,
+                                          uint4 (&q)[N]) {
+    bool direct = true, inside = true;  // all on 16 bytes; whole chunks end inside the matrix
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        direct = direct && (reinterpret_cast<uintptr_t>(at[k]) & 15u) == 0 && n[k] >= 8;
+        inside = inside && end - at[k] >= 16;
+    }
+    if (direct) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) q[k] = __ldg(reinterpret_cast<const uint4 *>(at[k]));
+        return;
+    }
+    uint32_t w[N][4];
+    if (inside) {
+        uint32_t t[N][8];
+#pragma unroll
+        for (int k = 0; k < N; ++k) load_chunks(at[k], t[k]);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            shift_words(at[k], t[k], w[k]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[k][j] = 2 * j + 1 < n[k] ? w[k][j] : 2 * j < n[k] ? w[k][j] & 0xFFFFu : 0u;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t lo = 2 * j < n[k] ? at[k][2 * j] : 0u, hi = 2 * j + 1 < n[k] ? at[k][2 * j + 1] : 0u;
+                w[k][j] = lo | hi << 16;
+            }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) q[k] = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+}
+
+// The same of row[k] at d + k * step.  (Places past a row's end are read at its start.)
+template <int N>
+__device__ __forceinline__ void values_at(const Row (&row)[N], int32_t d, int32_t step, uint4 (&q)[N]) {
+    const uint16_t *at[N];
+    int32_t n[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        n[k] = row[k].D - (d + k * step);
+        at[k] = row[k].p + (n[k] > 0 ? d + k * step : 0);
+    }
+    values_at(at, n, row[0].end, q);
+}
+
 // A warp's sum over D of x[d] w[d], in fp32, the same in every lane.
 __device__ __forceinline__ float row_dot(const Row &x, const Row &w, int lane) {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    int32_t d = 8 * lane;
     const Row xs[4] = {x, x, x, x}, ws[4] = {w, w, w, w};
-    for (; d + 768 < x.D; d += 1024) {
+    int32_t d = 0;
+    for (; d + 256 < x.D; d += 1024) {
         uint4 a[4], b[4];
-        values_at(xs, d, 256, a);
-        values_at(ws, d, 256, b);
+        values_at(xs, d + 8 * lane, 256, a);
+        values_at(ws, d + 8 * lane, 256, b);
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[k] = dot8(a[k], b[k], s[k]);
     }
-    for (; d < x.D; d += 256) s[0] = dot8(x.at(d), w.at(d), s[0]);
+    if (d < x.D) {  // (at most 256 values)
+        const Row x1[1] = {x}, w1[1] = {w};
+        uint4 a[1], b[1];
+        values_at(x1, d + 8 * lane, 0, a);
+        values_at(w1, d + 8 * lane, 0, b);
+        s[0] = dot8(a[0], b[0], s[0]);
+    }
     float sum = __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, o));
@@ -720,7 +739,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
 #pragma unroll VEC ? 4 : 2
             for (int32_t d = 8 * lane; d < pitch; d += 256) {
                 uint4 q[ROWS];
-                if (VEC && d + 8 <= a.D) {
+                if (VEC) {  // (a multiple of 8 columns)
 #pragma unroll
                     for (int r = 0; r < ROWS; ++r) q[r] = ld_stream_u4(row[r].p + d);
                 } else {
@@ -822,7 +841,7 @@ struct LayOut {
     uint16_t *dst;
 };
 
-// x and w laid out, a warp per row; x may have no place to go.  With target_logit, the
+// x and w laid out, x a warp per row; x may have no place to go.  With target_logit, the
 // products of x's rows with their target's row of w go there, and with `mask` rows
 // whose target is padding become 0.
 struct LayOuts {
@@ -843,20 +862,51 @@ __global__ void __launch_bounds__(256) lay_out_kernel(const LayOuts a) {
     const LayOut &m = of_x ? a.x : a.w;
     const int64_t cta = of_x ? blockIdx.x : blockIdx.x - a.ctas_x, ctas = of_x ? a.ctas_x : gridDim.x - a.ctas_x;
     const int32_t ld = (a.D + 7) & ~7;
+    if (!of_x) {
+        // four places of 8 values per thread, a grid's width apart
+        const int64_t chunks = ld / 8, n = m.rows * chunks, step = ctas * 256;
+        const uint16_t *const end = row_of(m.src, m.ld, m.rows, a.D, 0).end;
+        for (int64_t i = cta * 256 + threadIdx.x; i < n; i += 4 * step) {
+            const uint16_t *at[4];
+            int32_t left[4];
+            int64_t to[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t j = i + k * step < n ? i + k * step : i, r = j / chunks;
+                const int32_t c = int32_t(j - r * chunks) * 8;
+                at[k] = m.src + r * m.ld + c;
+                left[k] = a.D - c;
+                to[k] = 8 * j;
+            }
+            uint4 q[4];
+            values_at(at, left, end, q);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(m.dst + to[k]) = q[k];
+        }
+        return;
+    }
     for (int64_t r = cta * 8 + (threadIdx.x >> 5); r < m.rows; r += ctas * 8) {
-        const int32_t y = of_x && a.target_logit ? target_of(a.targets, a.wide, a.V, r) : 0;
+        const int32_t y = a.target_logit ? target_of(a.targets, a.wide, a.V, r) : 0;
         const Row row = row_of(m.src, m.ld, m.rows, a.D, r), rows[4] = {row, row, row, row};
         uint16_t *to = m.dst + r * ld;
         const bool zero = y < 0 && a.mask;
-        int32_t c = m.dst ? 8 * lane : ld;
-        for (; c + 768 < ld; c += 1024) {
+        int32_t d = m.dst ? 0 : ld;
+        for (; d + 256 < ld; d += 1024) {
+            const int32_t c = d + 8 * lane;
             uint4 q[4];
             values_at(rows, c, 256, q);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(to + c + 256 * k) = zero ? make_uint4(0u, 0u, 0u, 0u) : q[k];
+            for (int k = 0; k < 4; ++k)
+                if (c + 256 * k < ld)
+                    *reinterpret_cast<uint4 *>(to + c + 256 * k) = zero ? make_uint4(0u, 0u, 0u, 0u) : q[k];
         }
-        for (; c < ld; c += 256) *reinterpret_cast<uint4 *>(to + c) = zero ? make_uint4(0u, 0u, 0u, 0u) : row.at(c);
-        if (!of_x || a.target_logit == nullptr || y < 0) continue;
+        if (d + 8 * lane < ld) {
+            const Row one[1] = {row};
+            uint4 q[1];
+            values_at(one, d + 8 * lane, 0, q);
+            *reinterpret_cast<uint4 *>(to + d + 8 * lane) = zero ? make_uint4(0u, 0u, 0u, 0u) : q[0];
+        }
+        if (a.target_logit == nullptr || y < 0) continue;
         const float s = row_dot(row, row_of(a.given_w, a.ld_w, a.V, a.D, y), lane);
         if (lane == 0) a.target_logit[r] = s;
     }
@@ -1084,7 +1134,10 @@ cudaError_t lay_out(const CrossEntropy &c, uint16_t *x, uint16_t *w, float *targ
     a.wide = c.wide;
     a.V = int32_t(c.V);
     a.target_logit = target_logit;
-    return launch_after(lay_out_kernel, dim3(uint32_t(a.ctas_x + ctas(a.w.rows))), dim3(256), 0, stream, 1, a);
+    // (1024 places of w per CTA and turn)
+    const int64_t places = ceil_div(a.w.rows * ceil_div(c.D, 8), 1024);
+    const int32_t ctas_w = int32_t(places < 32 * kSms ? places : 32 * kSms);
+    return launch_after(lay_out_kernel, dim3(uint32_t(a.ctas_x + ctas_w)), dim3(256), 0, stream, 1, a);
 }
 
 Job job_of(int64_t rows_i, int64_t rows_j, int64_t K, int width) {
@@ -1142,7 +1195,7 @@ cudaError_t launch_few(const CrossEntropy &c, cudaStream_t stream) {
     const uint32_t grid = uint32_t(few_grid(c));
     const int held = int(few_tokens_held(c));
     const size_t smem = size_t(held) * ((c.D + 7) / 8 * 8) * 4;
-    const bool vec = aligned(c.w, c.ld_w);
+    const bool vec = aligned(c.w, c.ld_w) && c.D % 8 == 0;
     const int64_t rows = few_rows(c);
     const cudaError_t e = held == 1   ? run_few<1>(a, vec, rows, grid, smem, stream)
                           : held == 2 ? run_few<2>(a, vec, rows, grid, smem, stream)
