@@ -244,6 +244,22 @@ def test_extreme_logits(dev):
         got = loss.cross_entropy(rows, sure, torch.full((len(rows),), 7, device=dev))
         # exponentials of up to 64: their arguments' roundings
         close(got, want, want * 1e-5, "losses")
+    # an impossible target: its loss is infinite, its gradient that of probability 0
+    never = torch.zeros(50, 8, device=dev, dtype=torch.bfloat16)
+    never[9, 0] = -float("inf")
+    for T2 in (3, 20):
+        one = torch.ones(T2, 8, device=dev, dtype=torch.bfloat16)
+        y2 = torch.full((T2,), 9, device=dev)
+        y2[0] = 3
+        got, lse = loss.cross_entropy(one, never, y2, save=True)
+        assert bool(got[1:].isinf().all()) and float(got[0]) == pytest.approx(float(torch.tensor(49.0).log()), rel=1e-6)
+        close(lse, torch.full((T2,), 49.0, device=dev).log(), torch.full((T2,), 1e-5, device=dev), "lse")
+        _, dw = loss.cross_entropy_grad(one, never, y2, lse, 1.0, dw_dtype=torch.float32, needs_dx=False)
+        # 1 / 49 in bf16 for each token, -1 for the targets
+        want = torch.full((50, 8), T2 / 49.0, device=dev)
+        want[9] = 1.0 - T2
+        want[3] -= 1.0
+        close(dw, want, want.abs() * 2 ** -8 * 1.01 + 2 ** -8 * T2 / 49 * 1.01, "dw")
     # impossible rows, and rows of x that are not finite
     w2 = w.clone()
     w2[11] = 0.0

@@ -828,8 +828,10 @@ __global__ void __launch_bounds__(1024) join_stats_kernel(const float2 *parts, i
     // log2 of the others' sum over the target's exponential (-infinity if there are none)
     const float s = target_logit[at];
     const float more = r.y == 0.0f ? -INFINITY : __fadd_rn(__fmaf_rn(-s, kLog2E, r.x), log2f(r.y));
-    const float loss = __fadd_rn(more > 0.0f ? __fmul_rn(more, kLn2) : 0.0f, log1pf(exp2f(-fabsf(more))));
-    if (lse) lse[at] = __fadd_rn(s, loss);
+    const float rest = log1pf(exp2f(-fabsf(more)));
+    const float loss = __fadd_rn(more > 0.0f ? __fmul_rn(more, kLn2) : 0.0f, rest);
+    // from the larger of the two (a target may be impossible, its logit -infinity)
+    if (lse) lse[at] = more > 0.0f ? __fadd_rn(__fmul_rn(__fadd_rn(r.x, log2f(r.y)), kLn2), rest) : __fadd_rn(s, loss);
     if (losses) losses[at] = loss;
 }
 
