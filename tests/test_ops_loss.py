@@ -386,3 +386,37 @@ def test_refusals(dev):
         with pytest.raises(kind, match=match):
             loss.cross_entropy_grad(x, w, y, *args, **kw)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T,V,D", [(70, 700, 1100), (300, 2000, 2048), (257, 511, 2500), (5, 130, 9001), (600, 900, 4500),
+                                   (20, 3000, 8200), (130, 20000, 1032)])
+def test_long_rows(dev, T, V, D):
+    """Rows whose products are summed in several chunks."""
+    from weight_communication_gb300 import binding, loss
+    x, w, y = inputs(dev, T, V, D, seed=11)
+    losses, lse = loss.cross_entropy(x, w, y, save=True)
+    dx, dw = loss.cross_entropy_grad(x, w, y, lse, 1.0 / T)
+    torch.cuda.synchronize()
+    assert binding.wait_timeouts() == 0
+    check(x, w, y, 1.0 / T, losses, lse, dx, dw)
+    assert torch.equal(loss.cross_entropy(x, w, y), losses)
+
+
+@pytest.mark.parametrize("D", [1024, 4096, 16384, 50000])
+def test_what_sums_lose_does_not_grow_with_the_row(dev, D):
+    """Products of one sign, whose sums only grow: what each step cuts off adds up."""
+    from weight_communication_gb300 import loss
+    g = torch.Generator(device=dev)
+    g.manual_seed(D)
+    x = torch.rand(8, D, generator=g, device=dev).add_(0.5).bfloat16()
+    w = (torch.rand(300, D, generator=g, device=dev).add_(0.5) * (6 / D)).bfloat16()
+    y = torch.arange(8, device=dev)
+    losses, lse = loss.cross_entropy(x, w, y, save=True)
+    s = x.double() @ w.double().t()
+    want = torch.logsumexp(s, 1)
+    # 64 steps of 16 values to a chunk, each of which may lose an ulp of what is summed so
+    # far; a rounding for each chunk that is added; and those of the exponentials and
+    # logarithms, at arguments of up to 64
+    off = s.amax(1) * (64 * 2 ** -23 + -(-D // 1024) * 2 ** -24) + 64 * 4 * 2 ** -24
+    close(lse, want, off, "lse")
+    close(losses, want - s[torch.arange(8), y], off + s.amax(1) * D ** 0.5 * 2 ** -24, "losses")

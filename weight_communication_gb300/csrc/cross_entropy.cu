@@ -31,11 +31,13 @@
 //
 // The tensor core cuts sums off where fp32 would round them, so logits come out
 // nearer to 0 by some 2^-25 of themselves for each 16 values of K (D = 2048: 8e-6
-// for a logit of 4).  Over the vocabulary that largely cancels; a target's logit
+// for a logit of 4).  So it sums 1024 values of K at a time, and the epilogue adds
+// those sums up, rounded (losses of 64 x 8000 x 4096: 6.4e-6 off rms without, 1.6e-6
+// with it).  What is left largely cancels over the vocabulary; a target's logit
 // stands alone, so it is summed by itself in fp32 (warps 10 and 11 of the forward
 // pass, the kernel that lays x out in the backward pass), and d of a target
 // is expm1(s[t][y] - lse[t]).  (Losses of 8192 x 32000 x 2048: 8.1e-6 off rms with the
-// tensor core's target.)
+// tensor core's target, 1.8e-6 with one chunk, 1.0e-6 with both.)
 #include <atomic>
 
 #include "wc_device.cuh"
@@ -86,6 +88,7 @@ struct Job {
     int32_t width;          // columns of a tile: 256, 128 or (K-major B) 192, 64
     int32_t split;          // parts of K with sums of their own
     int32_t blocks;         // of K
+    int32_t chunks;         // LONG: of a tile's K, each summed by itself
     int32_t rows_i, rows_j;
     int32_t mn_i, mn_j;     // MN-major: rows of the operand are contiguous in memory
     int32_t j_at, kj_at;    // where B's rows and its K begin in its matrix
@@ -143,7 +146,7 @@ __device__ __forceinline__ Row row_of(const uint16_t *p, int64_t ld, int64_t row
 
 // Eight values each from N places of a matrix that ends at `end`, the n[k] first of them
 // (the rest 0; none if n[k] <= 0).  All loads are under way at once: one place after
-// the other waits for each (1 x 32001 x 2047 81 us, so 46).
+// the other waits for each (1 x 32001 x 2047 81 us, so 40).
 template <int N>
 __device__ __forceinline__ void values_at(const uint16_t *const (&at)[N], const int32_t (&n)[N], const uint16_t *end,
                                           uint4 (&q)[N]) {
@@ -444,11 +447,18 @@ __device__ __forceinline__ void store_sums(const Job &a, int32_t part, const flo
 // kernel
 // ---------------------------------------------------------------------------
 
-template <Mode MODE>
+// LONG: logits whose K is summed in several chunks.  The tensor core's sums of a chunk
+// leave the tensor memory as soon as it is complete and are added up, rounded, in the
+// epilogue's registers, so that what is cut off does not grow with K.  For those
+// 128 sums of a thread the epilogue takes registers over from the other four warps.
+template <Mode MODE, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant__ CUtensorMap map_j0,
                const __grid_constant__ CUtensorMap map_i1, const __grid_constant__ CUtensorMap map_j1,
                const __grid_constant__ Args a) {
+    // LONG: registers of a thread of the epilogue and of the others, 384 x 168 in all as at
+    // the launch (those that neither side spills)
+    constexpr int kTaken = MODE == kStats ? 208 : 224, kGiven = 3 * 168 - 2 * kTaken;
     extern __shared__ uint8_t dynamic_smem[];
     // full: a stage's operands are here (both CTAs', counted in the first one).
     // empty: its products have ended.  sums: a tile is complete.  taken: its
@@ -484,83 +494,107 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
     wait_for_predecessor();  // all above is set-up that reads no operand
     let_successor_start();   // (its CTAs find room as these end)
 
-    if (warp == kProducer) {
-        uint32_t stage = 0, phase = 0;
-        bool ok = true;
-        for (int32_t i = 0, t; ok && (t = unit_of<MODE>(a, pair, i, pairs)) < units; ++i) {
-            const Unit u = unit_at<MODE>(a, t);
-            const Job &job = a.job[u.job];
-            const CUtensorMap *map_i = u.job ? &map_i1 : &map_i0, *map_j = u.job ? &map_j1 : &map_j0;
-            const int32_t half = job.width / 2;
-            const int32_t row_i = u.ti * kTile + rank * kHalf, row_j = job.j_at + u.tj * job.width + rank * half;
-            for (int32_t b = 0; b < u.blocks; ++b) {
-                ok = mbar_wait(smem_of(&empty[stage]), phase ^ 1u);
-                if (!ok) break;
-                if (elected()) {
-                    const uint32_t local = smem_of(&full[stage]), bar = in_cta(local, 0);
-                    const uint32_t base = stages + stage * kStageBytes;
-                    const int32_t k = (u.block0 + b) * kDepth;
-                    if (rank == 0) mbar_expect(local, 2 * (kHalf + half) * kDepth * 2);
-                    load_operand(base, map_i, bar, job.mn_i, kHalf, row_i, k);
-                    load_operand(base + kOperand, map_j, bar, job.mn_j, half, row_j, job.kj_at + k);
-                }
-                __syncwarp();
-                if (++stage == kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
+    // The targets' logits: two warps of each CTA, ten of one without tiles.
+    auto targets = [&](int32_t of_cta, bool idle) {
+        const int32_t busy = min(int32_t(gridDim.x), 2 * units), cta = int32_t(blockIdx.x);
+        const int32_t mine = idle ? 2 * busy + 10 * (cta - busy) + of_cta : 2 * cta + of_cta;
+        const int32_t all = 2 * busy + 10 * (int32_t(gridDim.x) - busy), T = a.job[0].rows_i;
+        for (int32_t t = mine; t < T; t += all) {
+            const int32_t y = target_of(a.targets, a.wide, a.V, t);
+            if (y < 0) continue;
+            const float s = row_dot(row_of(a.x, a.ld_x, T, a.D, t), row_of(a.w, a.ld_w, a.V, a.D, y), lane);
+            if (lane == 0) a.target_logit[t] = s;
         }
-        if (!ok) wait_ms(20);  // for the copies in flight to land before the CTA goes
-    } else if (warp == kMma && rank == 0) {
-        uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
-        bool ok = true;
-        const bool lead = elected();
-        for (int32_t i = 0, t; ok && (t = unit_of<MODE>(a, pair, i, pairs)) < units; ++i) {
-            const Unit u = unit_at<MODE>(a, t);
-            const Job &job = a.job[u.job];
-            const uint32_t idesc = instr_desc(job.mn_i, job.mn_j, job.width);
-            // 16 values of K on: 32 bytes of every line, or 16 lines
-            const uint64_t step_i = job.mn_i ? 128 : 2, step_j = job.mn_j ? 128 : 2;
-            ok = mbar_wait(smem_of(&taken[buf]), buf_phase ^ 1u);
-            if (!ok) break;
-            tc_after_sync();
-            for (int32_t b = 0; b < u.blocks; ++b) {
-                ok = mbar_wait(smem_of(&full[stage]), phase);
-                if (!ok) break;
-                tc_after_sync();
-                if (lead) {
-                    const uint32_t base = stages + stage * kStageBytes;
-                    uint64_t di = smem_desc(base, job.mn_i), dj = smem_desc(base + kOperand, job.mn_j);
-#pragma unroll
-                    for (int k = 0; k < kDepth / 16; ++k) {
-                        mma(tmem + buf * kTile, di, dj, idesc, b > 0 || k > 0);
-                        di += step_i;
-                        dj += step_j;
+    };
+    const bool has_targets = MODE == kStats && a.x != nullptr, idle = int32_t(blockIdx.x) >= 2 * units;
+
+    if (warp >= kEpilogueWarps) {
+        if (LONG) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGiven));
+        if (warp == kProducer) {
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            for (int32_t i = 0, t; ok && (t = unit_of<MODE>(a, pair, i, pairs)) < units; ++i) {
+                const Unit u = unit_at<MODE>(a, t);
+                const Job &job = a.job[u.job];
+                const CUtensorMap *map_i = u.job ? &map_i1 : &map_i0, *map_j = u.job ? &map_j1 : &map_j0;
+                const int32_t half = job.width / 2;
+                const int32_t row_i = u.ti * kTile + rank * kHalf, row_j = job.j_at + u.tj * job.width + rank * half;
+                for (int32_t b = 0; b < u.blocks; ++b) {
+                    ok = mbar_wait(smem_of(&empty[stage]), phase ^ 1u);
+                    if (!ok) break;
+                    if (elected()) {
+                        const uint32_t local = smem_of(&full[stage]), bar = in_cta(local, 0);
+                        const uint32_t base = stages + stage * kStageBytes;
+                        const int32_t k = (u.block0 + b) * kDepth;
+                        if (rank == 0) mbar_expect(local, 2 * (kHalf + half) * kDepth * 2);
+                        load_operand(base, map_i, bar, job.mn_i, kHalf, row_i, k);
+                        load_operand(base + kOperand, map_j, bar, job.mn_j, half, row_j, job.kj_at + k);
                     }
-                    mma_commit<true>(smem_of(&empty[stage]));
+                    __syncwarp();
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
+            }
+            if (!ok) wait_ms(20);  // for the copies in flight to land before the CTA goes
+        } else if (warp == kMma && rank == 0) {
+            uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+            bool ok = true;
+            const bool lead = elected();
+            for (int32_t i = 0, t; ok && (t = unit_of<MODE>(a, pair, i, pairs)) < units; ++i) {
+                const Unit u = unit_at<MODE>(a, t);
+                const Job &job = a.job[u.job];
+                const uint32_t idesc = instr_desc(job.mn_i, job.mn_j, job.width);
+                // 16 values of K on: 32 bytes of every line, or 16 lines
+                const uint64_t step_i = job.mn_i ? 128 : 2, step_j = job.mn_j ? 128 : 2;
+                const int32_t chunks = LONG ? job.chunks : 1;
+                for (int32_t part = 0, b = 0; part < chunks; ++part) {
+                    const int32_t first = b, end = LONG ? int32_t(int64_t(u.blocks) * (part + 1) / chunks) : u.blocks;
+                    ok = mbar_wait(smem_of(&taken[buf]), buf_phase ^ 1u);
+                    if (!ok) break;
+                    tc_after_sync();
+                    for (; b < end; ++b) {
+                        ok = mbar_wait(smem_of(&full[stage]), phase);
+                        if (!ok) break;
+                        tc_after_sync();
+                        if (lead) {
+                            const uint32_t base = stages + stage * kStageBytes;
+                            uint64_t di = smem_desc(base, job.mn_i), dj = smem_desc(base + kOperand, job.mn_j);
+#pragma unroll
+                            for (int k = 0; k < kDepth / 16; ++k) {
+                                mma(tmem + buf * kTile, di, dj, idesc, b > first || k > 0);
+                                di += step_i;
+                                dj += step_j;
+                            }
+                            mma_commit<true>(smem_of(&empty[stage]));
+                        }
+                        __syncwarp();
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    if (lead) mma_commit<true>(smem_of(&sums[buf]));
+                    __syncwarp();
+                    if (++buf == kBuffers) {
+                        buf = 0;
+                        buf_phase ^= 1u;
+                    }
+                }
+            }
+            // No product may be in flight when the tensor memory is freed.
+            if (pair < units) {
+                if (lead) mma_commit<true>(smem_of(&drained), 1);
                 __syncwarp();
-                if (++stage == kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+                mbar_wait(smem_of(&drained), 0);
             }
-            if (!ok) break;
-            if (lead) mma_commit<true>(smem_of(&sums[buf]));
-            __syncwarp();
-            if (++buf == kBuffers) {
-                buf = 0;
-                buf_phase ^= 1u;
-            }
+        } else if (warp >= kTargets && has_targets) {
+            targets(warp - kTargets, idle);
         }
-        // No product may be in flight when the tensor memory is freed.
-        if (pair < units) {
-            if (lead) mma_commit<true>(smem_of(&drained), 1);
-            __syncwarp();
-            mbar_wait(smem_of(&drained), 0);
-        }
-    } else if (warp < kEpilogueWarps) {
+    } else {
+        if (LONG) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTaken));
         const int group = warp >> 2;
         uint8_t *const staging = dynamic_smem + (stages - smem_of(dynamic_smem)) + kStages * kStageBytes + warp * kStagingBytes;
         const uint32_t taken0 = in_cta(smem_of(&taken[0]), 0);
@@ -571,7 +605,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
             const Job &job = a.job[u.job];
             const int32_t row0 = u.ti * kTile + rank * kHalf + (warp & 3) * 32, row = row0 + lane;
             const int32_t half = job.width / 2, col0 = u.tj * job.width + group * half;
-            const uint32_t from = tmem + (uint32_t(warp & 3) << 21) + buf * kTile + group * half;
+            const uint32_t of_group = tmem + (uint32_t(warp & 3) << 21) + group * half;
             const bool live = row < job.rows_i;
             // (columns of this group that exist)
             const int32_t cols = max(0, min(job.rows_j - col0, half));
@@ -589,6 +623,34 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                 }
             }
             const int last = padding ? 0 : cols;  // of the columns with a gradient
+            float before[LONG ? kHalf : 1];  // the sums of the chunks before the last
+            if (LONG) {
+                for (int32_t part = 0; part + 1 < job.chunks; ++part) {
+                    if (ok) ok = mbar_wait(smem_of(&sums[buf]), phase);
+                    if (!ok) break;
+                    tc_after_sync();
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += 32) {
+                        if (c >= half) break;
+                        uint32_t w[32];
+                        tmem_load(of_group + buf * kTile + c, w);
+                        tmem_wait(w);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const float x = __uint_as_float(w[k]);
+                            before[LONG ? c + k : 0] = part == 0 ? x : __fadd_rn(before[LONG ? c + k : 0], x);
+                        }
+                    }
+                    tc_before_sync();
+                    __syncwarp();
+                    if (elected()) mbar_arrive_cluster(taken0 + buf * 8);
+                    if (++buf == kBuffers) {
+                        buf = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            const uint32_t from = of_group + buf * kTile;
             if (ok) ok = mbar_wait(smem_of(&sums[buf]), phase);
             tc_after_sync();
             Running run = {-INFINITY, 0.0f};
@@ -600,12 +662,21 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
 #pragma unroll
             for (int c = 0; c < kHalf; c += 32) {
                 if (c >= half) break;
-                uint32_t(&w)[32] = v[(c / 32) & 1];
+                uint32_t(&w)[32] = v[LONG ? 0 : (c / 32) & 1];
+                if (LONG && ok) {
+                    if (c > 0) {
+                        tmem_load(from + c, w);
+                        tmem_wait(w);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        w[k] = __float_as_uint(__fadd_rn(before[LONG ? c + k : 0], __uint_as_float(w[k])));
+                }
                 if (!ok) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) w[k] = 0x7FC00000u;
                 } else if (c + 32 < half) {
-                    tmem_load(from + c + 32, v[(c / 32 + 1) & 1]);
+                    if (!LONG) tmem_load(from + c + 32, v[(c / 32 + 1) & 1]);
                 } else {
                     tc_before_sync();  // all read: the next tile may have the buffer
                     __syncwarp();
@@ -644,7 +715,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                     for (int k = 0; k < 32; ++k) x[k] = __fmul_rn(job.alpha, __uint_as_float(w[k]));
                     store_sums(job, u.part, x, staging, row0, col0 + c, lane);
                 }
-                if (ok && c + 32 < half) tmem_wait(v[(c / 32 + 1) & 1]);
+                if (!LONG && ok && c + 32 < half) tmem_wait(v[(c / 32 + 1) & 1]);
             }
             if (MODE == kStats && live) {
                 if (!ok) run = {nan32(), nan32()};
@@ -655,23 +726,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                 phase ^= 1u;
             }
         }
-    }
-
-    if (MODE == kStats && a.x != nullptr) {
-        // the targets' logits: two warps of each CTA, ten of one without tiles
-        const int32_t busy = min(int32_t(gridDim.x), 2 * units), cta = int32_t(blockIdx.x);
-        const bool idle = cta >= busy;
-        const int32_t of_cta = warp >= kTargets ? warp - kTargets : idle && warp < kEpilogueWarps ? warp + 2 : -1;
-        if (of_cta >= 0) {
-            const int32_t mine = idle ? 2 * busy + 10 * (cta - busy) + of_cta : 2 * cta + of_cta;
-            const int32_t all = 2 * busy + 10 * (int32_t(gridDim.x) - busy), T = a.job[0].rows_i;
-            for (int32_t t = mine; t < T; t += all) {
-                const int32_t y = target_of(a.targets, a.wide, a.V, t);
-                if (y < 0) continue;
-                const float s = row_dot(row_of(a.x, a.ld_x, T, a.D, t), row_of(a.w, a.ld_w, a.V, a.D, y), lane);
-                if (lane == 0) a.target_logit[t] = s;
-            }
-        }
+        if (has_targets && idle) targets(warp + 2, idle);
     }
 
     tc_before_sync();
@@ -975,7 +1030,7 @@ cudaError_t describe(CUtensorMap *map, const Bf16Matrix &m, bool mn, int rows = 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <Mode MODE>
+template <Mode MODE, bool LONG>
 cudaError_t run(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
     // once for each GPU: the kernel's attribute stays set
     static std::atomic<uint64_t> prepared{0};
@@ -984,7 +1039,7 @@ cudaError_t run(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = uint64_t(1) << (device & 63);
     if (device > 63 || !(prepared.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(product_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(product_kernel<MODE, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         prepared.fetch_or(bit, std::memory_order_relaxed);
     }
@@ -999,8 +1054,19 @@ cudaError_t run(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
     // (CTAs without tiles sum targets' logits, ten warps with one token at a time)
     const int64_t more = MODE == kStats && a.x ? units + ceil_div(a.job[0].rows_i, 20) : 0, pairs = units > more ? units : more;
     const uint32_t grid = 2 * uint32_t(pairs < kSms / 2 ? pairs : kSms / 2);
-    return launch_after(product_kernel<MODE>, dim3(grid), dim3(kThreads), kSmem, stream, 2, maps[0], maps[1],
+    return launch_after(product_kernel<MODE, LONG>, dim3(grid), dim3(kThreads), kSmem, stream, 2, maps[0], maps[1],
                         maps[2], maps[3], a);
+}
+
+// Stages of K whose products the tensor core sums by itself: 1024 values for the
+// losses; 4096 for d, which is rounded to 8 bits (with 1024, 8192 x 32000 x 2048: 1705
+// us instead of 1692 for both gradients).  The forward pass takes no longer for it (513
+// us either way; 8192 x 32000 x 4096: 1000), as the sums leave beside the next chunk's products.
+template <Mode MODE>
+cudaError_t run_logits(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
+    const int32_t chunk = (MODE == kStats ? 1024 : 4096) / kDepth;
+    a.job[0].chunks = (a.job[0].blocks + chunk - 1) / chunk;
+    return a.job[0].chunks > 1 ? run<MODE, true>(maps, a, stream) : run<MODE, false>(maps, a, stream);
 }
 
 bool aligned(const uint16_t *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
@@ -1254,7 +1320,7 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
         a.ld_x = c.ld_x;
         a.ld_w = c.ld_w;
         a.D = int32_t(c.D);
-        if ((e = run<kStats>(maps, a, stream)) != cudaSuccess) return e;
+        if ((e = run_logits<kStats>(maps, a, stream)) != cudaSuccess) return e;
         e = join_stats(c, a.parts, 2 * a.job[0].tiles_j, t0, some.rows, a.target_logit, stream);
         if (e != cudaSuccess) return e;
     }
@@ -1304,7 +1370,7 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
         a.target_logit = target_logit;
         a.lse = c.lse_in;
         a.dlosses = c.dlosses;
-        if ((e = run<kGradient>(logits, a, stream)) != cudaSuccess) return e;
+        if ((e = run_logits<kGradient>(logits, a, stream)) != cudaSuccess) return e;
 
         Args p = {};
         if (c.dx) {
@@ -1344,7 +1410,7 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
                 j.ld_add = c.ld_dw;
             }
         }
-        if ((e = run<kProducts>(products, p, stream)) != cudaSuccess) return e;
+        if ((e = run<kProducts, false>(products, p, stream)) != cudaSuccess) return e;
     }
     if (c.dx && f.split > 1) {
         const uint32_t across = uint32_t(ceil_div(f.ld_dx / 4, 256)), down = uint32_t(c.T < 65535 ? c.T : 65535);
