@@ -571,10 +571,10 @@ WC_API int wc_rms_norm_grad(const void *dy, int64_t ld_dy, const void *add, int6
  * A target outside [0, V) is padding: its loss is 0, and nothing in its row of x
  * reaches a gradient.  Products of bf16 values in fp32; d is rounded to bf16 for the
  * products with w and x, so a gradient is a sum of terms that are each within
- * 2^-8 of their value.  The order of the sums depends on the sizes alone (the same
+ * 2^-8 of their value (not rounded for T <= 4 and D <= 4096).  The order of the sums depends on the sizes alone (the same
  * bits every run).
  * x, w     : bf16 [T][ld_x] and [V][ld_w].  Rows may start on any value; those that
- *            do not start on 16 bytes (address and stride) are first copied.
+ *            do not start on 16 bytes (address and stride) are first copied where T > 4.
  * targets  : [T] of id_type (WC_I32 or WC_I64).
  * losses, lse : fp32 [T]; forward: either may be NULL.  backward: lse of the forward
  *            pass.
@@ -583,7 +583,8 @@ WC_API int wc_rms_norm_grad(const void *dy, int64_t ld_dy, const void *add, int6
  *            either may be NULL (the matrix products for it are then not done).
  * workspace : the *_workspace() bytes for the same arguments, no initial value.  Of
  *            the backward pass: d for a piece of the vocabulary (256 MB, or as much as
- *            4 T D if that is more) and, if the pieces are several, dx in fp32.
+ *            4 T D if that is more) and, if the pieces are several, dx in fp32 (for
+ *            T <= 4 and D <= 4096: some 300 T D sums of dx at most).
  * Requires T, V <= 2^31 - 4096, V and D >= 1, D <= 2^22, T * V < 2^44, T * D and
  * V * D < 2^40, every ld >= D.
  */

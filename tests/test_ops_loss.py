@@ -141,6 +141,57 @@ def test_weight_gradients_and_accumulation(dev, dtype, T, V, D):
     assert none is None and torch.equal(only, dw)
 
 
+@pytest.mark.parametrize("T", [1, 2, 3, 4])
+@pytest.mark.parametrize("V,D", [(1, 1), (3, 8), (700, 257), (2000, 64), (5001, 1001), (600, 512), (900, 1024), (20003, 2048),
+                                 (700, 4096), (333, 4090), (300, 4104)])
+def test_few_tokens_gradients(dev, T, V, D):
+    from weight_communication_gb300 import loss
+    x, w, y = inputs(dev, T, V, D, wide=T % 2 == 0, padding=False, seed=T + 20)
+    if T > 2:
+        y[1] = -1
+        x[1] = float("nan")
+    _, lse = loss.cross_entropy(x, w, y, save=True)
+    g = torch.randn(T, device=dev) if T % 2 else 0.3
+    clean = x.clone()
+    clean[(y < 0)] = 0
+    (_, _, dx0, dw0), (_, _, off_dx, off_dw) = reference(clean, w, y, g)
+    if D <= 4096:
+        # d is not rounded: a term's bound there without its half step of bf16
+        xd, wd = clean.double(), w.double()
+        s = xd @ wd.t()
+        live = (y >= 0)[:, None]
+        p = torch.where(live, torch.exp(s - torch.logsumexp(s, 1)[:, None]), 0.0)
+        d = p.clone()
+        d.scatter_add_(1, torch.where(y >= 0, y.long(), 0)[:, None], torch.where(live, -1.0, 0.0).double())
+        gd = torch.as_tensor(g, device=dev, dtype=torch.float64).expand(T)[:, None].abs()
+        rounding = (HALF_STEP[torch.bfloat16] - 4 * ULP) * (gd * d.abs())
+        off_dx, off_dw = off_dx - rounding @ wd.abs(), off_dw - rounding.t() @ xd.abs()
+    dx, dw = loss.cross_entropy_grad(x, w, y, lse, g)
+    assert bool((dx[y < 0] == 0).all())
+    close(dx, dx0, off_dx + dx0.abs() * HALF_STEP[torch.bfloat16] * 1.01 + 1e-37, "dx")
+    close(dw, dw0, off_dw + dw0.abs() * HALF_STEP[torch.bfloat16] * 1.01 + 1e-37, "dw")
+    again = loss.cross_entropy_grad(x, w, y, lse, g)
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+    only, none = loss.cross_entropy_grad(x, w, y, lse, g, needs_dw=False)
+    assert none is None and torch.equal(only, dx)
+    for dtype in (torch.bfloat16, torch.float32):
+        old = (torch.randn(V, D, device=dev) * 0.01).to(dtype)
+        for ld, at in ((D, 0), (D + 3, 1), ((D + 15) // 8 * 8, 8)):
+            buf = strided(old, ld, at)
+            around = buf._base.clone() if buf._base is not None else None
+            none, got = loss.cross_entropy_grad(x, w, y, lse, g, dw=buf, accumulate=True, needs_dx=False)
+            assert none is None and got is buf
+            total = dw0 + old.double()
+            close(got, total, off_dw + total.abs() * HALF_STEP[dtype] * 1.01 + 1e-37, "dw")
+            if around is not None:
+                buf.copy_(old)
+                assert torch.equal(buf._base, around)     # nothing beside it is written
+    ws = strided(w, D + 5, 3)
+    dx, dw = loss.cross_entropy_grad(strided(x, D + 1, 1), ws, y, lse, g, dw_dtype=torch.float32)
+    close(dx, dx0, off_dx + dx0.abs() * HALF_STEP[torch.bfloat16] * 1.01 + 1e-37, "dx")
+    close(dw, dw0, off_dw + dw0.abs() * ULP + 1e-37, "dw")
+
+
 def test_pieces_of_the_vocabulary(dev):
     """More logits' gradients than the buffer holds: dx is summed over pieces."""
     from weight_communication_gb300 import binding, loss

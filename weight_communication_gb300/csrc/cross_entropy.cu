@@ -20,6 +20,8 @@
 // that bf16 holds, in the same direction (up to 2^-8 of the gradient).
 // So a pass multiplies four times where one that keeps T x V logits multiplies
 // three times.
+// Up to four tokens have kernels of their own for both directions, on the ordinary cores
+// with one reading of w.
 //
 // One kernel does all products (bf16 operands, fp32 sums): pairs of SMs
 // (cta_group::2) on tiles of 256 x 256, 64 values of K to a stage.  Operands come
@@ -39,6 +41,7 @@
 // is expm1(s[t][y] - lse[t]).  (Losses of 8192 x 32000 x 2048: 8.1e-6 off rms with the
 // tensor core's target, 1.8e-6 with one chunk, 1.0e-6 with both.)
 #include <atomic>
+#include <type_traits>
 
 #include "wc_device.cuh"
 #include "wc_internal.h"
@@ -848,6 +851,269 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
     }
 }
 
+// The backward pass of up to T tokens, one reading of w: WARPS warps have R rows of it at
+// a time in registers, a thread 8 columns.  From the rows' products with the tokens come
+// their d (fp32, not rounded), from those the rows of dw, written at once, and the sums
+// of dx, which stay in registers until the CTA's last row; a second kernel adds the CTAs'.
+// Bound: HBM for one token (32000 x 2048: 46 us, 38.7 at the copy rate, 138 by way of the
+// tensor cores, which read w three times and d as often), for four the registers that
+// hold tokens and dx, which leave a CTA little to have in flight (78 us, so 140; rows that
+// start anywhere, 3 x 5043 x 1995: 26, so 47).  R: as many rows as are not spilled (four
+// rows for four tokens: 32000 x 4096 160 us, two 153).
+template <int T_, int WARPS>
+struct FewShape {
+    static constexpr int T = T_, kWarps = WARPS, kLanes = 32 * WARPS;      // of a row
+    static constexpr int kThreads = kLanes < 256 ? 256 : kLanes, kGroups = kThreads / kLanes;
+    static constexpr int kPerSm = 512 / kThreads;
+    static constexpr int R = T == 1 ? 8 : T == 2 ? 4 : 2, N = R * T;
+    static constexpr int kSums = kGroups > 1 ? kThreads * 8 * T : 1;       // the groups' sums of dx
+    static int64_t ctas(int64_t V) {
+        const int64_t need = (V + kGroups * R - 1) / (kGroups * R), most = int64_t(kSms) * kPerSm;
+        return need < most ? need : most;
+    }
+};
+
+struct FewGrad {
+    const uint16_t *x, *w;
+    int64_t ld_x, ld_w;
+    int32_t V, D;
+    const void *targets;
+    int32_t wide;
+    const float *lse, *dlosses;
+    float dloss;
+    void *dw;                // or NULL
+    int64_t ld_dw;
+    int32_t dw_bf16, accumulate;
+    float *parts;            // [gridDim.x][tokens][D], or NULL
+    int32_t tokens;          // at most T
+};
+
+// Sums over a warp of N values a lane; lane i has that of value i / (32 / N).
+template <int N>
+__device__ __forceinline__ float sums_over_warp(float (&p)[N], int lane) {
+    int bit = 16;
+#pragma unroll
+    for (int half = N / 2; half > 0; half /= 2) {
+        const bool upper = lane & bit;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float give = upper ? p[i] : p[i + half], keep = upper ? p[i + half] : p[i];
+            p[i] = __fadd_rn(keep, __shfl_xor_sync(kFull, give, bit));
+        }
+        bit /= 2;
+    }
+#pragma unroll
+    for (; bit > 0; bit /= 2) p[0] = __fadd_rn(p[0], __shfl_xor_sync(kFull, p[0], bit));
+    return p[0];
+}
+
+// VEC: a thread's 8 columns are neighbours and lie on 16 bytes in w and dw; else they are
+// kLanes apart and move one at a time.
+template <bool VEC, typename S>
+__global__ void __launch_bounds__(S::kThreads, S::kPerSm) few_grad_kernel(const FewGrad a) {
+    constexpr int T = S::T, R = S::R, N = S::N;
+    __shared__ float slots[2][S::kThreads / 32][N];
+    __shared__ float sums[S::kSums];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = threadIdx.x / S::kLanes, in = threadIdx.x % S::kLanes;
+    const int32_t D = a.D;
+    auto column = [&](int j) { return VEC ? 8 * in + j : in + S::kLanes * j; };
+    // (single values past a row's end or past the last row are read at its last one and
+    // dropped: a branch for each would wait for each)
+    auto inside = [&](int j) { return min(column(j), D - 1); };
+    const f32x2 zero = pack2(0.0f, 0.0f);
+    wait_for_predecessor();
+    let_successor_start();
+    f32x2 x[T][4], dx[T][4];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        const int token = min(t, a.tokens - 1);
+        const bool live = t < a.tokens && target_of(a.targets, a.wide, a.V, token) >= 0;
+        float e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = bf16_bits_to_f32(a.x[token * a.ld_x + inside(j)]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            x[t][k] = pack2(live && column(2 * k) < D ? e[2 * k] : 0.0f, live && column(2 * k + 1) < D ? e[2 * k + 1] : 0.0f);
+            dx[t][k] = zero;
+        }
+    }
+    // this lane's d: of row `of_row` for token `of_token`
+    constexpr int kEach = 32 / N;
+    const int of_token = lane / kEach % T, of_row = lane / kEach / T;
+    const int32_t y = of_token < a.tokens ? target_of(a.targets, a.wide, a.V, of_token) : -1;
+    const float lse = y >= 0 ? a.lse[of_token] : 0.0f;
+    const float g = y < 0 ? 0.0f : a.dlosses ? a.dlosses[of_token] : a.dloss;
+
+    const int64_t first = int64_t(blockIdx.x) * S::kGroups * R, step = int64_t(gridDim.x) * S::kGroups * R;
+    int64_t v0 = first + group * R;
+    uint32_t next[R][VEC ? 4 : 8];
+    auto fetch = [&](int64_t v) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint16_t *row = a.w + (VEC || v + r < a.V ? v + r : int64_t(a.V) - 1) * a.ld_w;
+            if (VEC) {
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                if (v + r < a.V && 8 * in < D) q = ld_stream_u4(row + 8 * in);
+                next[r][0] = q.x;
+                next[r][1] = q.y;
+                next[r][2] = q.z;
+                next[r][3] = q.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < (VEC ? 4 : 8); ++j) next[r][j] = row[inside(j)];
+            }
+        }
+    };
+    // every group of a CTA takes as many turns, for the CTA's barriers
+    const int64_t turns = (a.V - first + step - 1) / step;
+    if (VEC) fetch(v0);
+    for (int64_t i = 0; i < turns; ++i, v0 += step) {
+        if (!VEC) fetch(v0);
+        uint32_t cur[R][VEC ? 4 : 8];
+        float p[N];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int j = 0; j < (VEC ? 4 : 8); ++j)
+                cur[r][j] = VEC || (v0 + r < a.V && column(j) < D) ? next[r][j] : 0u;
+        }
+        auto pair = [&](int r, int k) {
+            return VEC ? pack2(__uint_as_float(cur[r][k] << 16), __uint_as_float(cur[r][k] & 0xFFFF0000u))
+                       : pack2(__uint_as_float(cur[r][VEC ? 0 : 2 * k] << 16), __uint_as_float(cur[r][VEC ? 0 : 2 * k + 1] << 16));
+        };
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            f32x2 s[T];
+#pragma unroll
+            for (int t = 0; t < T; ++t) s[t] = zero;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int t = 0; t < T; ++t) s[t] = fma2_rn(pair(r, k), x[t][k], s[t]);
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                float even, odd;
+                unpack2(s[t], even, odd);
+                p[r * T + t] = __fadd_rn(even, odd);
+            }
+        }
+        if (VEC && i + 1 < turns) fetch(v0 + step);
+        float s = sums_over_warp(p, lane);
+        if (S::kWarps > 1) {
+            if (lane % kEach == 0) slots[i & 1][warp][lane / kEach] = s;
+            __syncthreads();
+            s = slots[i & 1][group * S::kWarps][lane / kEach];
+#pragma unroll
+            for (int k = 1; k < S::kWarps; ++k) s = __fadd_rn(s, slots[i & 1][group * S::kWarps + k][lane / kEach]);
+        }
+        const int64_t v = v0 + of_row;
+        float d = 0.0f;
+        if (y >= 0 && v < a.V) d = __fmul_rn(g, v == y ? expm1f(__fadd_rn(s, -lse)) : expf(__fadd_rn(s, -lse)));
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            f32x2 out[4] = {zero, zero, zero, zero};
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const float one = __shfl_sync(kFull, d, (r * T + t) * kEach);
+                const f32x2 both = pack2(one, one);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    out[k] = fma2_rn(both, x[t][k], out[k]);
+                    dx[t][k] = fma2_rn(both, pair(r, k), dx[t][k]);
+                }
+            }
+            if (a.dw == nullptr || v0 + r >= a.V) continue;
+            float e[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) unpack2(out[k], e[2 * k], e[2 * k + 1]);
+            const int64_t at = (v0 + r) * a.ld_dw;
+            if (VEC && 8 * in < D && a.dw_bf16) {
+                uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dw) + at + 8 * in);
+                if (a.accumulate) {
+                    const uint4 q = *to;
+                    const uint32_t old[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        e[j] = __fadd_rn(__uint_as_float(j & 1 ? old[j / 2] & 0xFFFF0000u : old[j / 2] << 16), e[j]);
+                }
+                __stcs(to, make_uint4(f32x2_to_bf16x2_bits(e[0], e[1]), f32x2_to_bf16x2_bits(e[2], e[3]),
+                                      f32x2_to_bf16x2_bits(e[4], e[5]), f32x2_to_bf16x2_bits(e[6], e[7])));
+            } else if (VEC && 8 * in < D) {
+                float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(a.dw) + at + 8 * in);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float4 old = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (a.accumulate) old = to[h];
+                    __stcs(to + h, make_float4(__fadd_rn(old.x, e[4 * h]), __fadd_rn(old.y, e[4 * h + 1]),
+                                               __fadd_rn(old.z, e[4 * h + 2]), __fadd_rn(old.w, e[4 * h + 3])));
+                }
+            } else if (!VEC) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (column(j) >= D) continue;
+                    if (a.dw_bf16) {
+                        uint16_t *to = static_cast<uint16_t *>(a.dw) + at + column(j);
+                        *to = f32_to_bf16_bits(a.accumulate ? __fadd_rn(bf16_bits_to_f32(*to), e[j]) : e[j]);
+                    } else {
+                        float *to = static_cast<float *>(a.dw) + at + column(j);
+                        *to = a.accumulate ? __fadd_rn(*to, e[j]) : e[j];
+                    }
+                }
+            }
+        }
+    }
+    if (a.parts == nullptr) return;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        if (t >= a.tokens) break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float e[2];
+            unpack2(dx[t][k], e[0], e[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int32_t c = column(2 * k + h);
+                if (c >= D) continue;
+                if (S::kGroups > 1) sums[(group * T + t) * D + c] = e[h];
+                else a.parts[(int64_t(blockIdx.x) * a.tokens + t) * D + c] = e[h];
+            }
+        }
+    }
+    if (S::kGroups == 1) return;
+    __syncthreads();
+    for (int32_t c = threadIdx.x; c < a.tokens * D; c += S::kThreads) {
+        float e = sums[c];
+#pragma unroll
+        for (int k = 1; k < S::kGroups; ++k) e = __fadd_rn(e, sums[k * T * D + c]);
+        a.parts[int64_t(blockIdx.x) * a.tokens * D + c] = e;
+    }
+}
+
+// dx of few tokens: the CTAs' sums, 32 values by 32 warps of a CTA, each warp every 32nd
+// sum, then the warps in turn.
+__global__ void __launch_bounds__(1024) join_few_kernel(const float *parts, int32_t count, int32_t tokens, int32_t D,
+                                                        void *dx, int bf16, int64_t ld_dx) {
+    __shared__ float sums[32][33];
+    wait_for_predecessor();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t n = tokens * D, c = blockIdx.x * 32 + lane;
+    float x = 0.0f;
+    if (c < n)
+#pragma unroll 8
+        for (int32_t g = warp; g < count; g += 32) x = __fadd_rn(x, parts[int64_t(g) * n + c]);
+    sums[warp][lane] = x;
+    __syncthreads();
+    x = sums[lane][warp];  // warp w has value w
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) x = __fadd_rn(x, __shfl_xor_sync(kFull, x, o));
+    const int32_t at = blockIdx.x * 32 + warp;
+    if (lane != 0 || at >= n) return;
+    const int32_t t = at / D;
+    if (bf16) static_cast<uint16_t *>(dx)[t * ld_dx + at - t * D] = f32_to_bf16_bits(x);
+    else static_cast<float *>(dx)[t * ld_dx + at - t * D] = x;
+}
+
 // ---------------------------------------------------------------------------
 // small kernels
 // ---------------------------------------------------------------------------
@@ -1272,6 +1538,45 @@ cudaError_t launch_few(const CrossEntropy &c, cudaStream_t stream) {
     return join_stats(c, a.parts, int32_t(grid), 0, c.T, a.target_logit, stream);
 }
 
+// Few tokens' gradients?  A thread has 8 columns, a CTA at most 512 threads.
+bool few_gradients(const CrossEntropy &c) { return c.T <= 4 && c.D <= 4096; }
+
+// f(the shape for c's tokens and columns).
+template <typename F>
+auto with_few_shape(const CrossEntropy &c, F f) {
+    auto of = [&](auto warps) {
+        constexpr int W = decltype(warps)::value;
+        if (c.T == 1) return f(FewShape<1, W>());
+        if (c.T == 2) return f(FewShape<2, W>());
+        return f(FewShape<4, W>());
+    };
+    if (c.D <= 256) return of(std::integral_constant<int, 1>());
+    if (c.D <= 512) return of(std::integral_constant<int, 2>());
+    if (c.D <= 1024) return of(std::integral_constant<int, 4>());
+    if (c.D <= 2048) return of(std::integral_constant<int, 8>());
+    return of(std::integral_constant<int, 16>());
+}
+
+int64_t few_grad_ctas(const CrossEntropy &c) {
+    return with_few_shape(c, [&](auto shape) { return decltype(shape)::ctas(c.V); });
+}
+
+cudaError_t launch_few_grad(const CrossEntropyGrad &c, cudaStream_t stream) {
+    const int64_t ctas = few_grad_ctas(c);
+    float *const parts = c.dx ? static_cast<float *>(c.workspace) : nullptr;
+    const FewGrad a = {c.x, c.w, c.ld_x, c.ld_w, int32_t(c.V), int32_t(c.D), c.targets, c.wide, c.lse_in, c.dlosses,
+                       c.dloss, c.dw, c.ld_dw, c.dw_bf16, c.accumulate, parts, int32_t(c.T)};
+    const bool vec = c.D % 8 == 0 && aligned(c.w, c.ld_w) && (!c.dw || aligned(static_cast<const uint16_t *>(c.dw), c.ld_dw));
+    const cudaError_t e = with_few_shape(c, [&](auto shape) {
+        using S = decltype(shape);
+        return vec ? launch_after(few_grad_kernel<true, S>, dim3(uint32_t(ctas)), dim3(S::kThreads), 0, stream, 1, a)
+                   : launch_after(few_grad_kernel<false, S>, dim3(uint32_t(ctas)), dim3(S::kThreads), 0, stream, 1, a);
+    });
+    if (e != cudaSuccess || !c.dx) return e;
+    return launch_after(join_few_kernel, dim3(uint32_t(ceil_div(c.T * c.D, 32))), dim3(1024), 0, stream, 1,
+                        static_cast<const float *>(parts), int32_t(ctas), int32_t(c.T), int32_t(c.D), c.dx, c.dx_bf16 ? 1 : 0, c.ld_dx);
+}
+
 }  // namespace
 
 int64_t cross_entropy_workspace(const CrossEntropy &c) { return few_tokens(c) ? FewLayout(c).bytes : Forward(c).bytes; }
@@ -1327,9 +1632,12 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
     return cudaSuccess;
 }
 
-int64_t cross_entropy_grad_workspace(const CrossEntropy &c) { return Backward(c).bytes; }
+int64_t cross_entropy_grad_workspace(const CrossEntropy &c) {
+    return few_gradients(c) ? up256(few_grad_ctas(c) * c.T * c.D * 4) : Backward(c).bytes;
+}
 
 cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t stream) {
+    if (few_gradients(c)) return launch_few_grad(c, stream);
     const Backward f(c);
     char *const ws = static_cast<char *>(c.workspace);
     // x with its padding tokens 0, so that nothing that they hold reaches dw

@@ -9,8 +9,8 @@ pieces of the vocabulary and without keeping the logits.
 x [.., D] and weight [V, D] are bf16 and multiplied on the tensor cores with fp32
 sums.  A target outside [0, V) is padding: its loss is 0, and nothing in its row of
 x reaches a gradient.  The backward pass multiplies the logits again, a piece
-of the vocabulary at a time, with d rounded to bf16 for the products.  The same
-bits every run.
+of the vocabulary at a time, with d rounded to bf16 for the products (not for up to
+four tokens of up to 4096 values).  The same bits every run.
 
     losses, lse = loss.cross_entropy(x, weight, targets, save=True)
     dx, dw = loss.cross_entropy_grad(x, weight, targets, lse, 1.0 / tokens)
