@@ -93,6 +93,7 @@ struct Job {
     int32_t blocks;         // of K
     int32_t chunks;         // LONG: of a tile's K, each summed by itself
     int32_t rows_i, rows_j;
+    int32_t box_i;          // rows of A in a copy: 128, or fewer if there are fewer
     int32_t mn_i, mn_j;     // MN-major: rows of the operand are contiguous in memory
     int32_t j_at, kj_at;    // where B's rows and its K begin in its matrix
     // what becomes of a product: out [split][rows_i][ld], added to what `add` holds
@@ -521,6 +522,9 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                 const Job &job = a.job[u.job];
                 const CUtensorMap *map_i = u.job ? &map_i1 : &map_i0, *map_j = u.job ? &map_j1 : &map_j0;
                 const int32_t half = job.width / 2;
+                // (rows of A past its box are not brought: what the tensor core makes of those that
+                // lie there is not looked at)
+                const uint32_t bytes = (2 * job.box_i + job.width) * kDepth * 2;
                 const int32_t row_i = u.ti * kTile + rank * kHalf, row_j = job.j_at + u.tj * job.width + rank * half;
                 for (int32_t b = 0; b < u.blocks; ++b) {
                     ok = mbar_wait(smem_of(&empty[stage]), phase ^ 1u);
@@ -529,7 +533,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                         const uint32_t local = smem_of(&full[stage]), bar = in_cta(local, 0);
                         const uint32_t base = stages + stage * kStageBytes;
                         const int32_t k = (u.block0 + b) * kDepth;
-                        if (rank == 0) mbar_expect(local, 2 * (kHalf + half) * kDepth * 2);
+                        if (rank == 0) mbar_expect(local, bytes);
                         load_operand(base, map_i, bar, job.mn_i, kHalf, row_i, k);
                         load_operand(base + kOperand, map_j, bar, job.mn_j, half, row_j, job.kj_at + k);
                     }
@@ -1296,6 +1300,10 @@ cudaError_t describe(CUtensorMap *map, const Bf16Matrix &m, bool mn, int rows = 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Rows of a copy of tokens (a multiple of 8, as the swizzle repeats): with 128 the copies of
+// rows that do not exist take as long as those of w (5 x 32000 x 2048: 39.5 us, so 32.5).
+int box_of(int64_t T) { return T < kHalf ? int(ceil_div(T, 8) * 8) : kHalf; }
+
 template <Mode MODE, bool LONG>
 cudaError_t run(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
     // once for each GPU: the kernel's attribute stays set
@@ -1483,6 +1491,7 @@ Job job_of(int64_t rows_i, int64_t rows_j, int64_t K, int width) {
     j.blocks = int32_t(ceil_div(K, kDepth));
     j.rows_i = int32_t(rows_i);
     j.rows_j = int32_t(rows_j);
+    j.box_i = kHalf;
     return j;
 }
 
@@ -1610,11 +1619,12 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
         Bf16Matrix some = x;
         some.p += t0 * x.ld;
         some.rows = c.T - t0 < kTokens ? c.T - t0 : kTokens;
-        if ((e = describe(&maps[0], some, false)) != cudaSuccess) return e;
+        if ((e = describe(&maps[0], some, false, box_of(some.rows))) != cudaSuccess) return e;
         maps[2] = maps[0];
         maps[3] = maps[1];
         Args a = {};
         a.job[0] = job_of(some.rows, c.V, c.D, width);
+        a.job[0].box_i = box_of(some.rows);
         a.targets = static_cast<const char *>(c.targets) + t0 * id;
         a.wide = c.wide;
         a.V = int32_t(c.V);
@@ -1650,7 +1660,7 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
     if (e != cudaSuccess) return e;
     const Bf16Matrix d = {reinterpret_cast<uint16_t *>(ws + f.d), f.piece, c.T, f.piece};
     CUtensorMap logits[4], products[4];
-    if ((e = describe(&logits[0], x, false)) != cudaSuccess) return e;
+    if ((e = describe(&logits[0], x, false, box_of(c.T))) != cudaSuccess) return e;
     const int width = width_of(c.T, f.piece < c.V ? f.piece : c.V);
     if ((e = describe(&logits[1], w, false, width / 2)) != cudaSuccess) return e;
     logits[2] = logits[0];
@@ -1669,6 +1679,7 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
         const bool last = v0 + cols == c.V;
         Args a = {};
         a.job[0] = job_of(c.T, cols, c.D, width);
+        a.job[0].box_i = box_of(c.T);
         a.job[0].j_at = int32_t(v0);
         a.job[0].out = ws + f.d;
         a.job[0].ld_out = f.piece;
