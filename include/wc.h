@@ -574,7 +574,8 @@ WC_API int wc_rms_norm_grad(const void *dy, int64_t ld_dy, const void *add, int6
  * 2^-8 of their value (not rounded for T <= 4 and D <= 4096).  The order of the sums depends on the sizes alone (the same
  * bits every run).
  * x, w     : bf16 [T][ld_x] and [V][ld_w].  Rows may start on any value; those that
- *            do not start on 16 bytes (address and stride) are first copied where T > 4.
+ *            do not start on 16 bytes (address and stride) are first copied (but for T <= 4
+ *            and D <= 4096).
  * targets  : [T] of id_type (WC_I32 or WC_I64).
  * losses, lse : fp32 [T]; forward: either may be NULL.  backward: lse of the forward
  *            pass.
