@@ -76,11 +76,15 @@ constexpr int kEpilogueWarps = 8, kProducer = 8, kMma = 9, kTargets = 10, kWarps
 constexpr int kThreads = kWarps * 32;
 constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * kStagingBytes + 1024;
 
-constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLog2E = 1.44269504088896340736f;
 
-__device__ __forceinline__ float ex2(float x) {
+// exp(x).  Of a difference of logits: the difference comes first, exact where the two
+// are near, and then the factor log2 e.  The other way round, with a rounded product
+// log2 e * maximum to subtract, even the maximum's own exponential is off by that
+// rounding, however large the logits are (9 % at 1e6, 0 or infinity from 4e9 on).
+__device__ __forceinline__ float exp_of(float x) {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__fmul_rn(x, kLog2E)));
     return y;
 }
 __device__ __forceinline__ float nan32() { return __uint_as_float(0x7FC00000u); }
@@ -112,7 +116,7 @@ struct Args {
     const void *targets;
     int32_t wide;           // 64-bit targets
     int32_t V;
-    float2 *parts;          // [2 tiles_j][rows_i]: maximum (times log2 e), sum
+    float2 *parts;          // [2 tiles_j][rows_i]: maximum, sum of exponentials less it
     float *target_logit;    // [rows_i]
     const uint16_t *x, *w;  // for it, as they were given; x NULL if it is there
     int64_t ld_x, ld_w;
@@ -318,11 +322,14 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 // epilogues: a warp's 32 rows x 32 columns, one row per lane
 // ---------------------------------------------------------------------------
 
-// The running maximum and sum of a row.  `top` is the maximum times log2 e, as
-// the exponentials use it.
+// The running maximum and sum of a row, of exponentials of the differences to it.  A row
+// without columns, or with impossible ones alone, is (-infinity, 0); a sum of NaN stays.
 struct Running {
     float top, sum;
 };
+
+// What is subtracted: the maximum, or 0 where every exponential is 0.
+__device__ __forceinline__ float base_of(float top) { return top == -INFINITY ? 0.0f : top; }
 
 // cols: columns of these that exist (at least 1).
 __device__ __forceinline__ void stats(Running &r, uint32_t (&v)[32], int cols) {
@@ -336,20 +343,20 @@ __device__ __forceinline__ void stats(Running &r, uint32_t (&v)[32], int cols) {
     for (int c = 0; c < 4; ++c) m[c] = __uint_as_float(v[c]);
 #pragma unroll
     for (int c = 4; c < 32; ++c) m[c & 3] = fmaxf(m[c & 3], __uint_as_float(v[c]));
-    const float top = fmaxf(r.top, __fmul_rn(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), kLog2E));
-    const float from = top == -INFINITY ? 0.0f : -top;  // nothing yet: every exponential is 0
-    float s[4] = {__fmul_rn(r.sum, ex2(__fadd_rn(r.top, from))), 0.0f, 0.0f, 0.0f};
+    const float top = fmaxf(r.top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+    const float from = -base_of(top);
+    float s[4] = {__fmul_rn(r.sum, exp_of(__fadd_rn(r.top, from))), 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int c = 0; c < 32; ++c) s[c & 3] = __fadd_rn(s[c & 3], ex2(__fmaf_rn(__uint_as_float(v[c]), kLog2E, from)));
+    for (int c = 0; c < 32; ++c) s[c & 3] = __fadd_rn(s[c & 3], exp_of(__fadd_rn(__uint_as_float(v[c]), from)));
     r.top = top;
     r.sum = __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
 }
 
-// Two parts of a row (one that has no columns is (-infinity, 0)).
+// Two parts of a row.
 __device__ __forceinline__ float2 joined_stats(float2 a, float2 b) {
     const float top = fmaxf(a.x, b.x);
-    const float x = a.y == 0.0f ? 0.0f : __fmul_rn(a.y, ex2(__fadd_rn(a.x, -top)));
-    const float y = b.y == 0.0f ? 0.0f : __fmul_rn(b.y, ex2(__fadd_rn(b.x, -top)));
+    const float x = a.x == -INFINITY ? a.y : __fmul_rn(a.y, exp_of(__fadd_rn(a.x, -top)));
+    const float y = b.x == -INFINITY ? b.y : __fmul_rn(b.y, exp_of(__fadd_rn(b.x, -top)));
     return make_float2(top, __fadd_rn(x, y));
 }
 
@@ -618,15 +625,15 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
             const int32_t cols = max(0, min(job.rows_j - col0, half));
             int32_t target = -1;  // its column in this group, or any number outside
             bool padding = true;
-            float lse2 = 0.0f, g = 0.0f, own = 0.0f;  // own: d of the target
+            float lse = 0.0f, g = 0.0f, own = 0.0f;  // own: d of the target
             if (MODE != kProducts && live) {
                 const int32_t y = target_of(a.targets, a.wide, a.V, row);
                 padding = y < 0;
                 if (!padding) target = y - job.j_at - col0;
                 if (MODE == kGradient && !padding) {
-                    lse2 = __fmul_rn(a.lse[row], kLog2E);
+                    lse = a.lse[row];
                     g = a.dlosses ? a.dlosses[row] : 1.0f;
-                    own = __fmul_rn(g, expm1f(__fadd_rn(a.target_logit[row], -a.lse[row])));
+                    own = __fmul_rn(g, expm1f(__fadd_rn(a.target_logit[row], -lse)));
                 }
             }
             const int last = padding ? 0 : cols;  // of the columns with a gradient
@@ -702,7 +709,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                     float x[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        x[k] = __fmul_rn(g, ex2(__fmaf_rn(__uint_as_float(w[k]), kLog2E, -lse2)));
+                        x[k] = __fmul_rn(g, exp_of(__fadd_rn(__uint_as_float(w[k]), -lse)));
                     if (__any_sync(kFull, padding || (target >= c && target < c + 32) || last < c + 32)) {
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
@@ -835,12 +842,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
                 for (int o = 16; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, o));
                 if (v + r == y[t] && lane == 0) a.target_logit[t] = sum;
                 z[r] = v + r == y[t] || v + r >= a.V ? -INFINITY : sum;
-                top = fmaxf(top, __fmul_rn(z[r], kLog2E));
+                top = fmaxf(top, z[r]);
             }
-            const float from = top == -INFINITY ? 0.0f : -top;
-            float sum = __fmul_rn(run[t].sum, ex2(__fadd_rn(run[t].top, from)));
+            const float from = -base_of(top);
+            float sum = __fmul_rn(run[t].sum, exp_of(__fadd_rn(run[t].top, from)));
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r) sum = __fadd_rn(sum, ex2(__fmaf_rn(z[r], kLog2E, from)));
+            for (int r = 0; r < ROWS; ++r) sum = __fadd_rn(sum, exp_of(__fadd_rn(z[r], from)));
             run[t] = {top, sum};
         }
     }
@@ -1146,17 +1153,17 @@ __global__ void __launch_bounds__(1024) join_stats_kernel(const float2 *parts, i
     const int32_t at = blockIdx.x * 32 + warp;
     if (lane != 0 || at >= T) return;
     if (target_of(targets, wide, V, at) < 0) {
-        if (lse) lse[at] = __fmul_rn(__fadd_rn(r.x, log2f(r.y)), kLn2);
+        if (lse) lse[at] = __fadd_rn(r.x, logf(r.y));
         if (losses) losses[at] = 0.0f;
         return;
     }
-    // log2 of the others' sum over the target's exponential (-infinity if there are none)
+    // the log of the others' sum over the target's exponential (-infinity if there are none)
     const float s = target_logit[at];
-    const float more = r.y == 0.0f ? -INFINITY : __fadd_rn(__fmaf_rn(-s, kLog2E, r.x), log2f(r.y));
-    const float rest = log1pf(exp2f(-fabsf(more)));
-    const float loss = __fadd_rn(more > 0.0f ? __fmul_rn(more, kLn2) : 0.0f, rest);
+    const float more = r.y == 0.0f ? -INFINITY : __fadd_rn(__fadd_rn(r.x, -s), logf(r.y));
+    const float rest = log1pf(expf(-fabsf(more)));
+    const float loss = __fadd_rn(more > 0.0f ? more : 0.0f, rest);
     // from the larger of the two (a target may be impossible, its logit -infinity)
-    if (lse) lse[at] = more > 0.0f ? __fadd_rn(__fmul_rn(__fadd_rn(r.x, log2f(r.y)), kLn2), rest) : __fadd_rn(s, loss);
+    if (lse) lse[at] = more > 0.0f ? __fadd_rn(__fadd_rn(r.x, logf(r.y)), rest) : __fadd_rn(s, loss);
     if (losses) losses[at] = loss;
 }
 
