@@ -55,7 +55,10 @@ def check(x, w, y, s, top, off, g, losses, lse, dx, dw):
 
 @pytest.mark.parametrize("scale", SCALES)
 @pytest.mark.parametrize("T,V,D", [(5, 700, 64), (16, 5000, 1000), (300, 700, 64), (260, 1003, 333), (700, 300, 1024),
-                                   (70, 20001, 128)])
+                                   (70, 20001, 128),
+                                   # rows whose products are summed in several chunks
+                                   (5, 700, 2048), (300, 700, 2500), (130, 1003, 4104), (600, 900, 4500), (16, 300, 9001),
+                                   (1000, 1500, 2048)])
 def test_a_column_that_decides(dev, T, V, D, scale):
     from weight_communication_gb300 import binding, loss
     x, w, y, s, top, off = decided(dev, T, V, D, scale, seed=T)

@@ -1339,13 +1339,15 @@ cudaError_t run(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
                         maps[2], maps[3], a);
 }
 
-// Stages of K whose products the tensor core sums by itself: 1024 values for the
-// losses; 4096 for d, which is rounded to 8 bits (with 1024, 8192 x 32000 x 2048: 1705
-// us instead of 1692 for both gradients).  The forward pass takes no longer for it (513
-// us either way; 8192 x 32000 x 4096: 1000), as the sums leave beside the next chunk's products.
+// Stages of K whose products the tensor core sums by itself: 1024 values.  The forward
+// pass takes no longer for it (8192 x 32000 x 2048: 513 us either way), as the sums leave
+// beside the next chunk's products; both gradients take 1705 us instead of 1692 with chunks
+// of 4096.  Both directions have the same chunks, so that they have the same logits, bit for
+// bit: the log-sum is one of the forward pass's logits where one decides a row, and what
+// another order of the sums would be off by, some 2^-22 of a logit, is in the exponent.
 template <Mode MODE>
 cudaError_t run_logits(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
-    const int32_t chunk = (MODE == kStats ? 1024 : 4096) / kDepth;
+    constexpr int32_t chunk = 1024 / kDepth;
     a.job[0].chunks = (a.job[0].blocks + chunk - 1) / chunk;
     return a.job[0].chunks > 1 ? run<MODE, true>(maps, a, stream) : run<MODE, false>(maps, a, stream);
 }
