@@ -104,3 +104,46 @@ def test_finite_and_infinite_logits_of_a_row(dev, T):
     want[577, 0], want[400, 0] = T, -T
     assert torch.equal(dw, want)
     assert bool((loss.cross_entropy(x, w, torch.full((T,), 577, device=dev)) == 0).all())
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("T", [1, 2, 3, 4])
+@pytest.mark.parametrize("V,D", [(700, 64), (5001, 333), (20001, 130), (1200, 512), (2001, 1000), (1200, 2048), (900, 4096), (333, 4090),
+                                 (300, 4104), (300, 4500), (9000, 4999), (300, 9001), (200, 30008)])
+def test_few_tokens_that_a_column_decides(dev, T, V, D, scale):
+    from weight_communication_gb300 import binding, loss
+    x, w, y, s, top, off = decided(dev, T, V, D, scale, seed=T + 20)
+    g = 0.25 if T % 2 else torch.rand(T, device=dev)
+    first = None
+    for rows in (w, strided(w, D + 3, 1), strided(w, (D + 15) // 8 * 8, 8)):
+        losses, lse = loss.cross_entropy(x, rows, y, save=True)
+        for ld, at in ((D, 0), (D + 5, 3)):
+            dw = strided(torch.zeros(V, D, device=dev), ld, at)
+            dx, dw = loss.cross_entropy_grad(x, rows, y, lse, g, dw=dw)
+            check(x, w, y, s, top, off, g, losses, lse, dx, dw)
+            # where rows lie changes no bit
+            first = first or (losses, lse, dx, dw)
+            assert all(torch.equal(a, b) for a, b in zip(first, (losses, lse, dx, dw)))
+        losses, lse = loss.cross_entropy(x, rows, top, save=True)
+        dx, dw = loss.cross_entropy_grad(x, rows, top, lse, 1.0)
+        assert bool((losses == 0).all()) and bool((dx == 0).all()) and bool((dw == 0).all())
+    assert binding.wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("V,D", [(5000, 256), (700, 2048), (333, 4104)])
+def test_padding_beside_a_column_that_decides(dev, T, V, D):
+    """A token of padding has a log-sum and no gradient."""
+    from weight_communication_gb300 import loss
+    x, w, y, s, top, off = decided(dev, T, V, D, 1e6, seed=T + 30)
+    y[T // 2] = V + 3
+    losses, lse = loss.cross_entropy(x, w, y, save=True)
+    best = s.amax(1)
+    close(lse, best, off + 4 * ULP * (best.abs() + s.abs().amax(1)), "lse")
+    dx, dw = loss.cross_entropy_grad(x, w, y, lse, 1.0)
+    live = torch.arange(T, device=dev) != T // 2
+    assert float(losses[T // 2]) == 0.0 and bool((dx[T // 2] == 0).all())
+    if T > 1:
+        check(x[live], w, y[live], s[live], top[live], off[live], 1.0, losses[live], lse[live], dx[live], dw)
+    else:
+        assert bool((dw == 0).all())

@@ -20,8 +20,13 @@
 // that bf16 holds, in the same direction (up to 2^-8 of the gradient).
 // So a pass multiplies four times where one that keeps T x V logits multiplies
 // three times.
-// Up to four tokens have kernels of their own for both directions, on the ordinary cores
-// with one reading of w.
+// Up to four tokens have kernels of their own for the logits of both directions, on the
+// ordinary cores with one reading of w.
+//
+// Both directions sum a logit in the same order, whatever kernel it is: a difference would
+// be in d's exponent, and at logits of 1e6 the rounding of a sum is some tenths.  So a column
+// that decides a row has d = g there, however large its logit is.  lse is one fp32 number, and
+// each d carries its rounding, |lse| 2^-24 of d.
 //
 // One kernel does all products (bf16 operands, fp32 sums): pairs of SMs
 // (cta_group::2) on tiles of 256 x 256, 64 values of K to a stage.  Operands come
@@ -755,11 +760,13 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
 // few tokens
 // ---------------------------------------------------------------------------
 
-// The forward pass of up to T tokens, one reading of w at the memory's rate: a warp
-// has ROWS rows of w at a time, their products with all tokens (fp32 in shared
-// memory) in fp32, and the tokens' maxima and sums over its rows in registers.
-// (One token, 32000 x 2048: 25 us with the join, 19.4 at the copy rate; the tensor cores, with
-// 256 rows for it, 38.)
+// Up to four tokens have kernels of their own, on the ordinary cores with one reading of w:
+// rows of up to 4096 values few_rows_kernel, longer ones whose tokens fit shared memory
+// few_kernel.  Either has both directions, so that both have the same logits, bit for bit.
+
+// Rows of more than 4096 values: a warp has ROWS rows of w at a time, their products with
+// all tokens (fp32 in shared memory) in fp32.  GRAD: d (bf16) for the products, instead of the
+// tokens' maxima and sums over the warp's rows.
 constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 
 struct Few {
@@ -768,12 +775,17 @@ struct Few {
     int32_t V, D;
     const void *targets;
     int32_t wide;
+    int32_t tokens;          // at most T
+    int32_t first, rows;     // rows of w here, the first of them at w
     float2 *parts;           // [gridDim.x][tokens]
     float *target_logit;
-    int32_t tokens;          // at most T
+    // GRAD
+    const float *lse, *dlosses;
+    uint16_t *d;             // [tokens][ld_d], written up to a multiple of 64 columns
+    int64_t ld_d;
 };
 
-template <int T, bool VEC, int ROWS>
+template <int T, bool VEC, int ROWS, bool GRAD>
 __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
     extern __shared__ __align__(16) float tokens[];  // [T][padded D]
     __shared__ float2 joined[kFewWarps][T];
@@ -793,14 +805,14 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
         run[t] = {-INFINITY, 0.0f};
     }
     __syncthreads();
-    const int64_t step = int64_t(gridDim.x) * kFewWarps * ROWS;
-    for (int64_t v = (int64_t(blockIdx.x) * kFewWarps + warp) * ROWS; v < a.V; v += step) {
+    const int64_t step = int64_t(gridDim.x) * kFewWarps * ROWS, end = GRAD ? (int64_t(a.rows) + 63) / 64 * 64 : a.rows;
+    for (int64_t v = (int64_t(blockIdx.x) * kFewWarps + warp) * ROWS; v < end; v += step) {
         float s[ROWS][T];
         Row row[ROWS];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             // (rows past the last are read as the last, and dropped below)
-            row[r] = row_of(a.w, a.ld_w, a.V, a.D, v + r < a.V ? v + r : a.V - 1);
+            row[r] = row_of(a.w, a.ld_w, a.rows, a.D, v + r < a.rows ? v + r : a.rows - 1);
 #pragma unroll
             for (int t = 0; t < T; ++t) s[r][t] = 0.0f;
         }
@@ -840,10 +852,22 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
                 float sum = s[r][t];
 #pragma unroll
                 for (int o = 16; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, o));
-                if (v + r == y[t] && lane == 0) a.target_logit[t] = sum;
-                z[r] = v + r == y[t] || v + r >= a.V ? -INFINITY : sum;
+                const bool own = y[t] >= 0 && v + r == y[t] - a.first;
+                if (GRAD) {
+                    if (lane != 0 || t >= a.tokens) continue;
+                    float d = 0.0f;
+                    if (y[t] >= 0 && v + r < a.rows) {
+                        const float less = __fadd_rn(sum, -a.lse[t]);
+                        d = __fmul_rn(a.dlosses ? a.dlosses[t] : 1.0f, own ? expm1f(less) : exp_of(less));
+                    }
+                    a.d[t * a.ld_d + v + r] = f32_to_bf16_bits(d);
+                    continue;
+                }
+                if (own && lane == 0) a.target_logit[t] = sum;
+                z[r] = own || v + r >= a.rows ? -INFINITY : sum;
                 top = fmaxf(top, z[r]);
             }
+            if (GRAD) continue;
             const float from = -base_of(top);
             float sum = __fmul_rn(run[t].sum, exp_of(__fadd_rn(run[t].top, from)));
 #pragma unroll
@@ -851,52 +875,65 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const Few a) {
             run[t] = {top, sum};
         }
     }
+    if constexpr (!GRAD) {
 #pragma unroll
-    for (int t = 0; t < T; ++t)
-        if (lane == 0) joined[warp][t] = make_float2(run[t].top, run[t].sum);
-    __syncthreads();
-    if (threadIdx.x < a.tokens) {
-        float2 r = joined[0][threadIdx.x];
-        for (int w = 1; w < kFewWarps; ++w) r = joined_stats(r, joined[w][threadIdx.x]);
-        a.parts[int64_t(blockIdx.x) * a.tokens + threadIdx.x] = r;
+        for (int t = 0; t < T; ++t)
+            if (lane == 0) joined[warp][t] = make_float2(run[t].top, run[t].sum);
+        __syncthreads();
+        if (threadIdx.x < a.tokens) {
+            float2 r = joined[0][threadIdx.x];
+            for (int w = 1; w < kFewWarps; ++w) r = joined_stats(r, joined[w][threadIdx.x]);
+            a.parts[int64_t(blockIdx.x) * a.tokens + threadIdx.x] = r;
+        }
     }
 }
 
-// The backward pass of up to T tokens, one reading of w: WARPS warps have R rows of it at
-// a time in registers, a thread 8 columns.  From the rows' products with the tokens come
-// their d (fp32, not rounded), from those the rows of dw, written at once, and the sums
+// Rows of up to 4096 values: WARPS warps have R rows of w at a time in registers, a thread
+// 8 columns, whose products with the tokens are summed over the row's threads.  Forward:
+// each lane then keeps the maximum and sum of the logits that end in it.  GRAD: from the
+// logits come d (fp32, not rounded), from those the rows of dw, written at once, and the sums
 // of dx, which stay in registers until the CTA's last row; a second kernel adds the CTAs'.
-// Bound: HBM for one token (32000 x 2048: 46 us, 38.7 at the copy rate, 138 by way of the
+//
+// Bound, forward: HBM (32000 x 2048, 19.4 us at the copy rate: one token 24.5 with the join,
+// four 33; the tensor cores, with 256 rows for one token, 38).  Rows that start anywhere are
+// shifted into place, a third of the instructions (1 x 32001 x 2047: 38).
+// Backward: HBM for one token (32000 x 2048: 46 us, 38.7 at the copy rate, 138 by way of the
 // tensor cores, which read w three times and d as often), for four the registers that
-// hold tokens and dx, which leave a CTA little to have in flight (78 us, so 140; rows that
-// start anywhere, 3 x 5043 x 1995: 26, so 47).  R: as many rows as are not spilled (four
-// rows for four tokens: 32000 x 4096 160 us, two 153).
-template <int T_, int WARPS>
+// hold tokens and dx, which leave a CTA little to have in flight (78 us, so 140); rows that
+// start anywhere also leave by way of shared memory (1 x 32001 x 2047: 74, 3 x 5043 x 1995:
+// 29, by way of the tensor cores 47).
+// R: as many rows as are not spilled (four rows for four tokens' gradients: 32000 x 4096
+// 160 us, two 153; eight for one token's log-sums of rows that start anywhere: 41 us, four 38).
+template <int T_, int WARPS, bool VEC, bool GRAD>
 struct FewShape {
     static constexpr int T = T_, kWarps = WARPS, kLanes = 32 * WARPS;      // of a row
     static constexpr int kThreads = kLanes < 256 ? 256 : kLanes, kGroups = kThreads / kLanes;
     static constexpr int kPerSm = 512 / kThreads;
-    static constexpr int R = T == 1 ? 8 : T == 2 ? 4 : 2, N = R * T;
-    static constexpr int kSums = kGroups > 1 ? kThreads * 8 * T : 1;       // the groups' sums of dx
+    static constexpr int R = VEC ? (T == 1 ? 8 : T == 2 ? (GRAD ? 4 : 8) : GRAD ? 2 : 4) : GRAD && T == 4 ? 2 : 4, N = R * T;
+    static constexpr int kSums = GRAD && kGroups > 1 ? kThreads * 8 * T : 1;  // the groups' sums of dx
     static int64_t ctas(int64_t V) {
         const int64_t need = (V + kGroups * R - 1) / (kGroups * R), most = int64_t(kSms) * kPerSm;
         return need < most ? need : most;
     }
 };
 
-struct FewGrad {
+struct FewRows {
     const uint16_t *x, *w;
     int64_t ld_x, ld_w;
     int32_t V, D;
     const void *targets;
     int32_t wide;
+    int32_t tokens;          // at most T
+    // forward
+    float2 *stats;           // [gridDim.x][tokens]
+    float *target_logit;
+    // GRAD
     const float *lse, *dlosses;
     float dloss;
     void *dw;                // or NULL
     int64_t ld_dw;
     int32_t dw_bf16, accumulate;
     float *parts;            // [gridDim.x][tokens][D], or NULL
-    int32_t tokens;          // at most T
 };
 
 // Sums over a warp of N values a lane; lane i has that of value i / (32 / N).
@@ -918,20 +955,20 @@ __device__ __forceinline__ float sums_over_warp(float (&p)[N], int lane) {
     return p[0];
 }
 
-// VEC: a thread's 8 columns are neighbours and lie on 16 bytes in w and dw; else they are
-// kLanes apart and move one at a time.
-template <bool VEC, typename S>
-__global__ void __launch_bounds__(S::kThreads, S::kPerSm) few_grad_kernel(const FewGrad a) {
+// A thread's 8 columns are neighbours.  VEC: rows of w, and of dw, start on 16 bytes and have
+// a multiple of 8 columns; else rows of w are shifted into place and those of dw leave by way
+// of shared memory, neighbouring values by neighbouring lanes.
+template <bool VEC, typename S, bool GRAD>
+__global__ void __launch_bounds__(S::kThreads, S::kPerSm) few_rows_kernel(const FewRows a) {
     constexpr int T = S::T, R = S::R, N = S::N;
     __shared__ float slots[2][S::kThreads / 32][N];
     __shared__ float sums[S::kSums];
+    __shared__ float2 joined[S::kGroups][T];
+    __shared__ __align__(16) float staging[GRAD && !VEC ? S::kThreads * 8 : 4];  // 256 columns of each warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = threadIdx.x / S::kLanes, in = threadIdx.x % S::kLanes;
     const int32_t D = a.D;
-    auto column = [&](int j) { return VEC ? 8 * in + j : in + S::kLanes * j; };
-    // (single values past a row's end or past the last row are read at its last one and
-    // dropped: a branch for each would wait for each)
-    auto inside = [&](int j) { return min(column(j), D - 1); };
+    auto column = [&](int j) { return 8 * in + j; };
     const f32x2 zero = pack2(0.0f, 0.0f);
     wait_for_predecessor();
     let_successor_start();
@@ -939,60 +976,77 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) few_grad_kernel(const 
 #pragma unroll
     for (int t = 0; t < T; ++t) {
         const int token = min(t, a.tokens - 1);
-        const bool live = t < a.tokens && target_of(a.targets, a.wide, a.V, token) >= 0;
+        // (a token of padding has a log-sum, and no gradient whatever its row of x holds)
+        const bool live = t < a.tokens && (!GRAD || target_of(a.targets, a.wide, a.V, token) >= 0);
         float e[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) e[j] = bf16_bits_to_f32(a.x[token * a.ld_x + inside(j)]);
+        for (int j = 0; j < 8; ++j) e[j] = bf16_bits_to_f32(a.x[token * a.ld_x + min(column(j), D - 1)]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             x[t][k] = pack2(live && column(2 * k) < D ? e[2 * k] : 0.0f, live && column(2 * k + 1) < D ? e[2 * k + 1] : 0.0f);
             dx[t][k] = zero;
         }
     }
-    // this lane's d: of row `of_row` for token `of_token`
+    // this lane's logit: of row `of_row` for token `of_token`
     constexpr int kEach = 32 / N;
     const int of_token = lane / kEach % T, of_row = lane / kEach / T;
     const int32_t y = of_token < a.tokens ? target_of(a.targets, a.wide, a.V, of_token) : -1;
-    const float lse = y >= 0 ? a.lse[of_token] : 0.0f;
-    const float g = y < 0 ? 0.0f : a.dlosses ? a.dlosses[of_token] : a.dloss;
+    const float lse = GRAD && y >= 0 ? a.lse[of_token] : 0.0f;
+    const float g = !GRAD || y < 0 ? 0.0f : a.dlosses ? a.dlosses[of_token] : a.dloss;
+    Running run = {-INFINITY, 0.0f};
 
     const int64_t first = int64_t(blockIdx.x) * S::kGroups * R, step = int64_t(gridDim.x) * S::kGroups * R;
     int64_t v0 = first + group * R;
+    // a row's 8 values, or the two chunks of 16 bytes that they lie in
     uint32_t next[R][VEC ? 4 : 8];
+    const uint16_t *const end = a.w + (int64_t(a.V) - 1) * a.ld_w + D;
     auto fetch = [&](int64_t v) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const uint16_t *row = a.w + (VEC || v + r < a.V ? v + r : int64_t(a.V) - 1) * a.ld_w;
-            if (VEC) {
-                uint4 q = make_uint4(0u, 0u, 0u, 0u);
-                if (v + r < a.V && 8 * in < D) q = ld_stream_u4(row + 8 * in);
-                next[r][0] = q.x;
-                next[r][1] = q.y;
-                next[r][2] = q.z;
-                next[r][3] = q.w;
-            } else {
+            const uint16_t *at = a.w + (v + r) * a.ld_w + 8 * in;
+            const bool here = v + r < a.V && 8 * in < D;
 #pragma unroll
-                for (int j = 0; j < (VEC ? 4 : 8); ++j) next[r][j] = row[inside(j)];
+            for (int k = 0; k < (VEC ? 1 : 2); ++k) {
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                if (VEC) {
+                    if (here) q = ld_stream_u4(at);
+                } else {  // (of the second one, the matrix may have ended)
+                    const uint4 *chunk = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(at) & ~uintptr_t(15)) + k;
+                    if (here && reinterpret_cast<const uint16_t *>(chunk) < end) q = __ldg(chunk);
+                }
+                next[r][4 * k] = q.x;
+                next[r][4 * k + 1] = q.y;
+                next[r][4 * k + 2] = q.z;
+                next[r][4 * k + 3] = q.w;
             }
         }
     };
+    uint32_t keep[4];  // of a row's last columns
+#pragma unroll
+    for (int j = 0; j < 4; ++j) keep[j] = column(2 * j + 1) < D ? 0xFFFFFFFFu : column(2 * j) < D ? 0xFFFFu : 0u;
     // every group of a CTA takes as many turns, for the CTA's barriers
     const int64_t turns = (a.V - first + step - 1) / step;
-    if (VEC) fetch(v0);
+    // the next rows are under way beside these (but where that is spilled: 4 x 32001 x 2047 132
+    // us with it, 126 without)
+    constexpr bool kAhead = VEC || !GRAD || T < 4 || S::kWarps > 8;
+    if (kAhead) fetch(v0);
     for (int64_t i = 0; i < turns; ++i, v0 += step) {
-        if (!VEC) fetch(v0);
-        uint32_t cur[R][VEC ? 4 : 8];
+        if (!kAhead) fetch(v0);
+        uint32_t cur[R][4];
         float p[N];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            if (VEC) {
 #pragma unroll
-            for (int j = 0; j < (VEC ? 4 : 8); ++j)
-                cur[r][j] = VEC || (v0 + r < a.V && column(j) < D) ? next[r][j] : 0u;
+                for (int j = 0; j < 4; ++j) cur[r][j] = next[r][j];
+            } else {
+                const uint32_t at = (uint32_t(reinterpret_cast<uintptr_t>(a.w)) + 2u * uint32_t(v0 + r) * uint32_t(a.ld_w)) & 15u;
+                shift_words(at, next[r], cur[r]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) cur[r][j] &= keep[j];
+            }
         }
-        auto pair = [&](int r, int k) {
-            return VEC ? pack2(__uint_as_float(cur[r][k] << 16), __uint_as_float(cur[r][k] & 0xFFFF0000u))
-                       : pack2(__uint_as_float(cur[r][VEC ? 0 : 2 * k] << 16), __uint_as_float(cur[r][VEC ? 0 : 2 * k + 1] << 16));
-        };
+        auto pair = [&](int r, int k) { return pack2(__uint_as_float(cur[r][k] << 16), __uint_as_float(cur[r][k] & 0xFFFF0000u)); };
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             f32x2 s[T];
@@ -1009,7 +1063,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) few_grad_kernel(const 
                 p[r * T + t] = __fadd_rn(even, odd);
             }
         }
-        if (VEC && i + 1 < turns) fetch(v0 + step);
+        if (kAhead && i + 1 < turns) fetch(v0 + step);
         float s = sums_over_warp(p, lane);
         if (S::kWarps > 1) {
             if (lane % kEach == 0) slots[i & 1][warp][lane / kEach] = s;
@@ -1019,6 +1073,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) few_grad_kernel(const 
             for (int k = 1; k < S::kWarps; ++k) s = __fadd_rn(s, slots[i & 1][group * S::kWarps + k][lane / kEach]);
         }
         const int64_t v = v0 + of_row;
+        if (!GRAD) {
+            if (v == y && lane % kEach == 0 && warp % S::kWarps == 0) a.target_logit[of_token] = s;
+            const float z = v == y || v >= a.V ? -INFINITY : s, top = fmaxf(run.top, z), from = -base_of(top);
+            run.sum = __fadd_rn(__fmul_rn(run.sum, exp_of(__fadd_rn(run.top, from))), exp_of(__fadd_rn(z, from)));
+            run.top = top;
+            continue;
+        }
         float d = 0.0f;
         if (y >= 0 && v < a.V) d = __fmul_rn(g, v == y ? expm1f(__fadd_rn(s, -lse)) : expf(__fadd_rn(s, -lse)));
 #pragma unroll
@@ -1060,19 +1121,41 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) few_grad_kernel(const 
                                                __fadd_rn(old.z, e[4 * h + 2]), __fadd_rn(old.w, e[4 * h + 3])));
                 }
             } else if (!VEC) {
+                float4 *const st = reinterpret_cast<float4 *>(staging + warp * 256);
+                st[2 * lane] = make_float4(e[0], e[1], e[2], e[3]);
+                st[2 * lane + 1] = make_float4(e[4], e[5], e[6], e[7]);
+                __syncwarp();
+                const int32_t c0 = warp % S::kWarps * 256 + lane;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    if (column(j) >= D) continue;
+                    if (c0 + 32 * j >= D) continue;
+                    const float one = staging[warp * 256 + lane + 32 * j];
                     if (a.dw_bf16) {
-                        uint16_t *to = static_cast<uint16_t *>(a.dw) + at + column(j);
-                        *to = f32_to_bf16_bits(a.accumulate ? __fadd_rn(bf16_bits_to_f32(*to), e[j]) : e[j]);
+                        uint16_t *to = static_cast<uint16_t *>(a.dw) + at + c0 + 32 * j;
+                        *to = f32_to_bf16_bits(a.accumulate ? __fadd_rn(bf16_bits_to_f32(*to), one) : one);
                     } else {
-                        float *to = static_cast<float *>(a.dw) + at + column(j);
-                        *to = a.accumulate ? __fadd_rn(*to, e[j]) : e[j];
+                        float *to = static_cast<float *>(a.dw) + at + c0 + 32 * j;
+                        *to = a.accumulate ? __fadd_rn(*to, one) : one;
                     }
                 }
+                __syncwarp();
             }
         }
+    }
+    if (!GRAD) {
+        // a token's rows of this warp, then the groups' (a group's warps all hold the same)
+        float2 r = make_float2(run.top, run.sum);
+#pragma unroll
+        for (int o = 16; o >= kEach * T; o /= 2)
+            r = joined_stats(r, make_float2(__shfl_xor_sync(kFull, r.x, o), __shfl_xor_sync(kFull, r.y, o)));
+        if (of_row == 0 && lane % kEach == 0 && warp % S::kWarps == 0) joined[group][of_token] = r;
+        __syncthreads();
+        if (threadIdx.x < a.tokens) {
+            r = joined[0][threadIdx.x];
+            for (int k = 1; k < S::kGroups; ++k) r = joined_stats(r, joined[k][threadIdx.x]);
+            a.stats[int64_t(blockIdx.x) * a.tokens + threadIdx.x] = r;
+        }
+        return;
     }
     if (a.parts == nullptr) return;
 #pragma unroll
@@ -1385,20 +1468,54 @@ struct Layout {
     }
 };
 
-// Rows of w that a warp has at a time: four share a token's values, and one keeps
-// more of the GPU busy where rows are few (4 x 1043 x 3009: 24 us with four, 14 with one).
-int64_t few_rows(const CrossEntropy &c) { return c.V <= 4 * kSms * kFewWarps ? 1 : 4; }
+// Few tokens with rows of up to 4096 values?  A thread has 8 columns, a CTA at most 512 threads.
+bool few_short(const CrossEntropy &c) { return c.T <= 4 && c.D <= 4096; }
 
-int64_t few_grid(const CrossEntropy &c) {
-    const int64_t ctas = ceil_div(c.V, kFewWarps * few_rows(c));
+// Few tokens with longer rows?  Their fp32 values fit shared memory twice per SM.
+constexpr int kFewBytes = 112 * 1024;
+int64_t few_tokens_held(const CrossEntropy &c) { return c.T <= 2 ? c.T : 4; }
+bool few_long(const CrossEntropy &c) {
+    return c.T <= 4 && c.D > 4096 && few_tokens_held(c) * (c.D + 7) * 4 <= kFewBytes;
+}
+
+// f(the shape for c's tokens and columns).
+template <bool VEC, bool GRAD, typename F>
+auto with_few_shape(const CrossEntropy &c, F f) {
+    auto of = [&](auto warps) {
+        constexpr int W = decltype(warps)::value;
+        if (c.T == 1) return f(FewShape<1, W, VEC, GRAD>());
+        if (c.T == 2) return f(FewShape<2, W, VEC, GRAD>());
+        return f(FewShape<4, W, VEC, GRAD>());
+    };
+    if (c.D <= 256) return of(std::integral_constant<int, 1>());
+    if (c.D <= 512) return of(std::integral_constant<int, 2>());
+    if (c.D <= 1024) return of(std::integral_constant<int, 4>());
+    if (c.D <= 2048) return of(std::integral_constant<int, 8>());
+    return of(std::integral_constant<int, 16>());
+}
+
+// vec: of what is written.
+template <bool GRAD>
+int64_t few_ctas(const CrossEntropy &c, bool vec) {
+    auto ctas = [&](auto shape) { return decltype(shape)::ctas(c.V); };
+    return vec && c.D % 8 == 0 && aligned(c.w, c.ld_w) ? with_few_shape<true, GRAD>(c, ctas) : with_few_shape<false, GRAD>(c, ctas);
+}
+
+// Rows of w that a warp of few_kernel has at a time: four share a token's values, and one
+// keeps more of the GPU busy where rows are few (4 x 1043 x 3009: 24 us with four, 14 with one).
+int64_t few_rows(int64_t V) { return V <= 4 * kSms * kFewWarps ? 1 : 4; }
+
+int64_t few_grid(int64_t V) {
+    const int64_t ctas = ceil_div(V, kFewWarps * few_rows(V));
     return ctas < 2 * kSms ? ctas : 2 * kSms;
 }
 
 struct FewLayout {
-    int64_t parts, target_logit, bytes;
+    int64_t ctas, parts, target_logit, bytes;
     explicit FewLayout(const CrossEntropy &c) {
         Layout l;
-        parts = l.take(few_grid(c) * c.T * int64_t(sizeof(float2)));
+        ctas = few_short(c) ? few_ctas<false>(c, true) : few_grid(c.V);
+        parts = l.take(ctas * c.T * int64_t(sizeof(float2)));
         target_logit = l.take(c.T * 4);
         bytes = l.bytes;
     }
@@ -1504,12 +1621,7 @@ Job job_of(int64_t rows_i, int64_t rows_j, int64_t K, int width) {
     return j;
 }
 
-// Few tokens?  Their fp32 values fit shared memory twice per SM.
-constexpr int kFewBytes = 112 * 1024;
-int64_t few_tokens_held(const CrossEntropy &c) { return c.T <= 2 ? c.T : 4; }
-bool few_tokens(const CrossEntropy &c) { return c.T <= 4 && few_tokens_held(c) * (c.D + 7) * 4 <= kFewBytes; }
-
-template <int T, bool VEC, int ROWS>
+template <int T, bool VEC, int ROWS, bool GRAD>
 cudaError_t run_few(const Few &a, uint32_t grid, size_t smem, cudaStream_t stream) {
     // once for each GPU: the kernel's attribute stays set
     static std::atomic<uint64_t> prepared{0};
@@ -1518,17 +1630,43 @@ cudaError_t run_few(const Few &a, uint32_t grid, size_t smem, cudaStream_t strea
     if (e != cudaSuccess) return e;
     const uint64_t bit = uint64_t(1) << (device & 63);
     if (device > 63 || !(prepared.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(few_kernel<T, VEC, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewBytes);
+        e = cudaFuncSetAttribute(few_kernel<T, VEC, ROWS, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewBytes);
         if (e != cudaSuccess) return e;
         prepared.fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_after(few_kernel<T, VEC, ROWS>, dim3(grid), dim3(kFewThreads), smem, stream, 1, a);
+    return launch_after(few_kernel<T, VEC, ROWS, GRAD>, dim3(grid), dim3(kFewThreads), smem, stream, 1, a);
 }
 
-template <int T>
+template <int T, bool GRAD>
 cudaError_t run_few(const Few &a, bool vec, int64_t rows, uint32_t grid, size_t smem, cudaStream_t stream) {
-    if (rows == 1) return vec ? run_few<T, true, 1>(a, grid, smem, stream) : run_few<T, false, 1>(a, grid, smem, stream);
-    return vec ? run_few<T, true, 4>(a, grid, smem, stream) : run_few<T, false, 4>(a, grid, smem, stream);
+    if (rows == 1)
+        return vec ? run_few<T, true, 1, GRAD>(a, grid, smem, stream) : run_few<T, false, 1, GRAD>(a, grid, smem, stream);
+    return vec ? run_few<T, true, 4, GRAD>(a, grid, smem, stream) : run_few<T, false, 4, GRAD>(a, grid, smem, stream);
+}
+
+// The rows first .. first + rows - 1 of w, whose results `a` says where to leave.
+template <bool GRAD>
+cudaError_t run_few(const CrossEntropy &c, Few a, int64_t first, int64_t rows, cudaStream_t stream) {
+    a.x = c.x;
+    a.w = c.w + first * c.ld_w;
+    a.ld_x = c.ld_x;
+    a.ld_w = c.ld_w;
+    a.V = int32_t(c.V);
+    a.D = int32_t(c.D);
+    a.targets = c.targets;
+    a.wide = c.wide;
+    a.tokens = int32_t(c.T);
+    a.first = int32_t(first);
+    a.rows = int32_t(rows);
+    const int64_t padded = GRAD ? ceil_div(rows, kDepth) * kDepth : rows;
+    const uint32_t grid = uint32_t(few_grid(padded));
+    const int held = int(few_tokens_held(c));
+    const size_t smem = size_t(held) * ((c.D + 7) / 8 * 8) * 4;
+    const bool vec = aligned(c.w, c.ld_w) && c.D % 8 == 0;
+    const int64_t each = few_rows(padded);
+    return held == 1   ? run_few<1, GRAD>(a, vec, each, grid, smem, stream)
+           : held == 2 ? run_few<2, GRAD>(a, vec, each, grid, smem, stream)
+                       : run_few<4, GRAD>(a, vec, each, grid, smem, stream);
 }
 
 cudaError_t join_stats(const CrossEntropy &c, const float2 *parts, int32_t count, int64_t t0, int64_t tokens,
@@ -1539,57 +1677,61 @@ cudaError_t join_stats(const CrossEntropy &c, const float2 *parts, int32_t count
                         c.wide ? 1 : 0, int32_t(c.V), c.losses ? c.losses + t0 : nullptr, c.lse ? c.lse + t0 : nullptr);
 }
 
+template <bool GRAD>
+cudaError_t run_few_rows(const CrossEntropy &c, FewRows a, bool vec, cudaStream_t stream) {
+    a.x = c.x;
+    a.w = c.w;
+    a.ld_x = c.ld_x;
+    a.ld_w = c.ld_w;
+    a.V = int32_t(c.V);
+    a.D = int32_t(c.D);
+    a.targets = c.targets;
+    a.wide = c.wide;
+    a.tokens = int32_t(c.T);
+    auto launch = [&](auto kernel, auto shape) {
+        using S = decltype(shape);
+        return launch_after(kernel, dim3(uint32_t(S::ctas(c.V))), dim3(S::kThreads), 0, stream, 1, a);
+    };
+    if (vec && c.D % 8 == 0 && aligned(c.w, c.ld_w))
+        return with_few_shape<true, GRAD>(c, [&](auto shape) { return launch(few_rows_kernel<true, decltype(shape), GRAD>, shape); });
+    return with_few_shape<false, GRAD>(c, [&](auto shape) { return launch(few_rows_kernel<false, decltype(shape), GRAD>, shape); });
+}
+
 cudaError_t launch_few(const CrossEntropy &c, cudaStream_t stream) {
     const FewLayout f(c);
     char *const ws = static_cast<char *>(c.workspace);
-    const Few a = {c.x, c.w, c.ld_x, c.ld_w, int32_t(c.V), int32_t(c.D), c.targets, c.wide,
-                   reinterpret_cast<float2 *>(ws + f.parts), reinterpret_cast<float *>(ws + f.target_logit), int32_t(c.T)};
-    const uint32_t grid = uint32_t(few_grid(c));
-    const int held = int(few_tokens_held(c));
-    const size_t smem = size_t(held) * ((c.D + 7) / 8 * 8) * 4;
-    const bool vec = aligned(c.w, c.ld_w) && c.D % 8 == 0;
-    const int64_t rows = few_rows(c);
-    const cudaError_t e = held == 1   ? run_few<1>(a, vec, rows, grid, smem, stream)
-                          : held == 2 ? run_few<2>(a, vec, rows, grid, smem, stream)
-                                      : run_few<4>(a, vec, rows, grid, smem, stream);
+    float2 *const parts = reinterpret_cast<float2 *>(ws + f.parts);
+    float *const target_logit = reinterpret_cast<float *>(ws + f.target_logit);
+    cudaError_t e;
+    if (few_short(c)) {
+        FewRows a = {};
+        a.stats = parts;
+        a.target_logit = target_logit;
+        e = run_few_rows<false>(c, a, true, stream);
+    } else {
+        Few a = {};
+        a.parts = parts;
+        a.target_logit = target_logit;
+        e = run_few<false>(c, a, 0, c.V, stream);
+    }
     if (e != cudaSuccess) return e;
-    return join_stats(c, a.parts, int32_t(grid), 0, c.T, a.target_logit, stream);
-}
-
-// Few tokens' gradients?  A thread has 8 columns, a CTA at most 512 threads.
-bool few_gradients(const CrossEntropy &c) { return c.T <= 4 && c.D <= 4096; }
-
-// f(the shape for c's tokens and columns).
-template <typename F>
-auto with_few_shape(const CrossEntropy &c, F f) {
-    auto of = [&](auto warps) {
-        constexpr int W = decltype(warps)::value;
-        if (c.T == 1) return f(FewShape<1, W>());
-        if (c.T == 2) return f(FewShape<2, W>());
-        return f(FewShape<4, W>());
-    };
-    if (c.D <= 256) return of(std::integral_constant<int, 1>());
-    if (c.D <= 512) return of(std::integral_constant<int, 2>());
-    if (c.D <= 1024) return of(std::integral_constant<int, 4>());
-    if (c.D <= 2048) return of(std::integral_constant<int, 8>());
-    return of(std::integral_constant<int, 16>());
-}
-
-int64_t few_grad_ctas(const CrossEntropy &c) {
-    return with_few_shape(c, [&](auto shape) { return decltype(shape)::ctas(c.V); });
+    return join_stats(c, parts, int32_t(f.ctas), 0, c.T, target_logit, stream);
 }
 
 cudaError_t launch_few_grad(const CrossEntropyGrad &c, cudaStream_t stream) {
-    const int64_t ctas = few_grad_ctas(c);
+    const bool vec = !c.dw || aligned(static_cast<const uint16_t *>(c.dw), c.ld_dw);
+    const int64_t ctas = few_ctas<true>(c, vec);
     float *const parts = c.dx ? static_cast<float *>(c.workspace) : nullptr;
-    const FewGrad a = {c.x, c.w, c.ld_x, c.ld_w, int32_t(c.V), int32_t(c.D), c.targets, c.wide, c.lse_in, c.dlosses,
-                       c.dloss, c.dw, c.ld_dw, c.dw_bf16, c.accumulate, parts, int32_t(c.T)};
-    const bool vec = c.D % 8 == 0 && aligned(c.w, c.ld_w) && (!c.dw || aligned(static_cast<const uint16_t *>(c.dw), c.ld_dw));
-    const cudaError_t e = with_few_shape(c, [&](auto shape) {
-        using S = decltype(shape);
-        return vec ? launch_after(few_grad_kernel<true, S>, dim3(uint32_t(ctas)), dim3(S::kThreads), 0, stream, 1, a)
-                   : launch_after(few_grad_kernel<false, S>, dim3(uint32_t(ctas)), dim3(S::kThreads), 0, stream, 1, a);
-    });
+    FewRows a = {};
+    a.lse = c.lse_in;
+    a.dlosses = c.dlosses;
+    a.dloss = c.dloss;
+    a.dw = c.dw;
+    a.ld_dw = c.ld_dw;
+    a.dw_bf16 = c.dw_bf16;
+    a.accumulate = c.accumulate;
+    a.parts = parts;
+    const cudaError_t e = run_few_rows<true>(c, a, vec, stream);
     if (e != cudaSuccess || !c.dx) return e;
     return launch_after(join_few_kernel, dim3(uint32_t(ceil_div(c.T * c.D, 32))), dim3(1024), 0, stream, 1,
                         static_cast<const float *>(parts), int32_t(ctas), int32_t(c.T), int32_t(c.D), c.dx, c.dx_bf16 ? 1 : 0, c.ld_dx);
@@ -1597,10 +1739,12 @@ cudaError_t launch_few_grad(const CrossEntropyGrad &c, cudaStream_t stream) {
 
 }  // namespace
 
-int64_t cross_entropy_workspace(const CrossEntropy &c) { return few_tokens(c) ? FewLayout(c).bytes : Forward(c).bytes; }
+int64_t cross_entropy_workspace(const CrossEntropy &c) {
+    return few_short(c) || few_long(c) ? FewLayout(c).bytes : Forward(c).bytes;
+}
 
 cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
-    if (few_tokens(c)) return launch_few(c, stream);
+    if (few_short(c) || few_long(c)) return launch_few(c, stream);
     const Forward f(c);
     char *const ws = static_cast<char *>(c.workspace);
     Bf16Matrix x = {c.x, c.ld_x, c.T, c.D}, w = {c.w, c.ld_w, c.V, c.D};
@@ -1652,11 +1796,13 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, cudaStream_t stream) {
 }
 
 int64_t cross_entropy_grad_workspace(const CrossEntropy &c) {
-    return few_gradients(c) ? up256(few_grad_ctas(c) * c.T * c.D * 4) : Backward(c).bytes;
+    if (!few_short(c)) return Backward(c).bytes;
+    const int64_t a = few_ctas<true>(c, true), b = few_ctas<true>(c, false);
+    return up256((a > b ? a : b) * c.T * c.D * 4);
 }
 
 cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t stream) {
-    if (few_gradients(c)) return launch_few_grad(c, stream);
+    if (few_short(c)) return launch_few_grad(c, stream);
     const Backward f(c);
     char *const ws = static_cast<char *>(c.workspace);
     // x with its padding tokens 0, so that nothing that they hold reaches dw
@@ -1686,19 +1832,29 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
     for (int64_t v0 = 0; v0 < c.V; v0 += f.piece) {
         const int64_t cols = c.V - v0 < f.piece ? c.V - v0 : f.piece;
         const bool last = v0 + cols == c.V;
-        Args a = {};
-        a.job[0] = job_of(c.T, cols, c.D, width);
-        a.job[0].box_i = box_of(c.T);
-        a.job[0].j_at = int32_t(v0);
-        a.job[0].out = ws + f.d;
-        a.job[0].ld_out = f.piece;
-        a.targets = c.targets;
-        a.wide = c.wide;
-        a.V = int32_t(c.V);
-        a.target_logit = target_logit;
-        a.lse = c.lse_in;
-        a.dlosses = c.dlosses;
-        if ((e = run_logits<kGradient>(logits, a, stream)) != cudaSuccess) return e;
+        if (few_long(c)) {
+            Few a = {};
+            a.lse = c.lse_in;
+            a.dlosses = c.dlosses;
+            a.d = reinterpret_cast<uint16_t *>(ws + f.d);
+            a.ld_d = f.piece;
+            e = run_few<true>(c, a, v0, cols, stream);
+        } else {
+            Args a = {};
+            a.job[0] = job_of(c.T, cols, c.D, width);
+            a.job[0].box_i = box_of(c.T);
+            a.job[0].j_at = int32_t(v0);
+            a.job[0].out = ws + f.d;
+            a.job[0].ld_out = f.piece;
+            a.targets = c.targets;
+            a.wide = c.wide;
+            a.V = int32_t(c.V);
+            a.target_logit = target_logit;
+            a.lse = c.lse_in;
+            a.dlosses = c.dlosses;
+            e = run_logits<kGradient>(logits, a, stream);
+        }
+        if (e != cudaSuccess) return e;
 
         Args p = {};
         if (c.dx) {

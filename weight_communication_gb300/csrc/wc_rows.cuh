@@ -31,14 +31,18 @@ __device__ __forceinline__ void drop_words(uint32_t (&t)[N], uint32_t n) {
     for (int k = 0; k + 1 < N; ++k) t[k] = (n & 1u) ? t[k + 1] : t[k];
 }
 
-// The first M words from *p (a 2-byte boundary) of the N > M words that
+// The first M words from byte `at` < 16 (a multiple of 2) of the N > M words that
 // load_chunks() gave.
 template <int M, int N>
-__device__ __forceinline__ void shift_words(const void *p, uint32_t (&t)[N], uint32_t (&out)[M]) {
-    const uint32_t at = uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u;
+__device__ __forceinline__ void shift_words(uint32_t at, uint32_t (&t)[N], uint32_t (&out)[M]) {
     drop_words(t, at >> 2);
 #pragma unroll
     for (int k = 0; k < M; ++k) out[k] = __funnelshift_r(t[k], t[k + 1], (at & 2u) * 8u);
+}
+// The same of those from *p.
+template <int M, int N>
+__device__ __forceinline__ void shift_words(const void *p, uint32_t (&t)[N], uint32_t (&out)[M]) {
+    shift_words(uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u, t, out);
 }
 
 }  // namespace wc
