@@ -1,0 +1,51 @@
+"""Gradients of the cross entropy whose sums run over many tokens or a large vocabulary,
+against 64-bit formulas, and against differences along the gradient itself."""
+import pytest
+import torch
+
+from gpu_util import dev  # noqa: F401
+from layers_util import HALF_STEP, ULP, close
+from test_ops_loss import inputs, reference
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [8192, 16385, 140001, 1 << 20])
+def test_what_sums_lose_does_not_grow_with_the_tokens(dev, T, dtype, accumulate):
+    """Terms of one sign: two rows of weight that are 0 have probabilities of a half each."""
+    from weight_communication_gb300 import binding, loss
+    g = torch.Generator(device=dev)
+    g.manual_seed(T)
+    x = torch.rand(T, 72, generator=g, device=dev).add_(0.5).bfloat16()
+    w = torch.zeros(2, 72, device=dev, dtype=torch.bfloat16)
+    y = torch.zeros(T, device=dev, dtype=torch.int64)
+    _, lse = loss.cross_entropy(x, w, y, save=True)
+    old = torch.rand(2, 72, generator=g, device=dev).to(dtype)
+    dx, dw = loss.cross_entropy_grad(x, w, y, lse, 1.0, dw=old.clone(), accumulate=accumulate)
+    torch.cuda.synchronize()
+    assert binding.wait_timeouts() == 0
+    half = 0.5 * x.double().sum(0)
+    # d is exact; 1024 steps of 16 values to a chunk, each of which may lose an ulp of what is
+    # summed so far, and a rounding for each chunk that is added; then the result's
+    off = half * (1024 * 2 ** -23 + -(-T // 16384) * ULP)
+    want = torch.stack([-half, half]) + (old.double() if accumulate else 0.0)
+    close(dw, want, off + want.abs() * HALF_STEP[dtype] * 1.01, "dw")
+    assert bool((dx == 0).all())
+
+
+@pytest.mark.parametrize("T,V,D", [(20000, 700, 72), (8192, 40000, 264), (40001, 1003, 130), (3500, 60000, 72)])
+def test_many_terms(dev, T, V, D):
+    from weight_communication_gb300 import binding, loss
+    x, w, y = inputs(dev, T, V, D, seed=12)
+    losses, lse = loss.cross_entropy(x, w, y, save=True)
+    dx, dw = loss.cross_entropy_grad(x, w, y, lse, 1.0 / T, dw_dtype=torch.float32)
+    again = loss.cross_entropy_grad(x, w, y, lse, 1.0 / T, dw_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert binding.wait_timeouts() == 0
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+    want, off = reference(x, w, y, 1.0 / T)
+    close(losses, want[0], off[0] + want[0].abs() * 2 * ULP, "losses")
+    close(dx, want[2], off[2] + want[2].abs() * HALF_STEP[dx.dtype] * 1.01 + 1e-37, "dx")
+    close(dw, want[3], off[3] + want[3].abs() * ULP + 1e-37, "dw")

@@ -478,7 +478,7 @@ __device__ __forceinline__ void store_sums(const Job &a, int32_t part, const flo
 // kernel
 // ---------------------------------------------------------------------------
 
-// LONG: logits whose K is summed in several chunks.  The tensor core's sums of a chunk
+// LONG: products whose K is summed in several chunks (of all of them, or of one job's).  The tensor core's sums of a chunk
 // leave the tensor memory as soon as it is complete and are added up, rounded, in the
 // epilogue's registers, so that what is cut off does not grow with K.  For those
 // 128 sums of a thread the epilogue takes registers over from the other four warps.
@@ -659,6 +659,10 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
             const int last = padding ? 0 : cols;  // of the columns with a gradient
             float before[LONG ? kHalf : 1];  // the sums of the chunks before the last
             if (LONG) {
+                if (MODE == kProducts && job.chunks == 1) {
+#pragma unroll
+                    for (int c = 0; c < kHalf; ++c) before[LONG ? c : 0] = -0.0f;
+                }
                 for (int32_t part = 0; part + 1 < job.chunks; ++part) {
                     if (ok) ok = mbar_wait(smem_of(&sums[buf]), phase);
                     if (!ok) break;
@@ -1453,6 +1457,20 @@ cudaError_t run_logits(const CUtensorMap (&maps)[4], Args &a, cudaStream_t strea
     return a.job[0].chunks > 1 ? run<MODE, true>(maps, a, stream) : run<MODE, false>(maps, a, stream);
 }
 
+// The same of dx's and dw's products, whose K are the vocabulary and the tokens: 16384 values,
+// so that what is cut off, some 2^-15 of a sum at most, does not grow with them (dw of a million
+// tokens, terms of one sign: 3.7e-3 without).  The chunks cost a percent where there are
+// several (8192 x 32000 x 2048 with dx in two 2560 us, whole 2520), and d is rounded to 2^-9.
+cudaError_t run_products(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
+    constexpr int32_t chunk = 16384 / kDepth;
+    bool several = false;
+    for (Job &j : a.job) {
+        j.chunks = j.split > 0 ? (j.blocks + j.split * chunk - 1) / (j.split * chunk) : 0;
+        several = several || j.chunks > 1;
+    }
+    return several ? run<kProducts, true>(maps, a, stream) : run<kProducts, false>(maps, a, stream);
+}
+
 bool aligned(const uint16_t *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
 
 // Columns of a tile of logits.  A stage of a narrow tile takes not much less time than
@@ -1912,7 +1930,7 @@ cudaError_t launch_cross_entropy_grad(const CrossEntropyGrad &c, cudaStream_t st
                 j.ld_add = c.ld_dw;
             }
         }
-        if ((e = run<kProducts, false>(products, p, stream)) != cudaSuccess) return e;
+        if ((e = run_products(products, p, stream)) != cudaSuccess) return e;
     }
     if (c.dx && f.split > 1) {
         const uint32_t across = uint32_t(ceil_div(f.ld_dx / 4, 256)), down = uint32_t(c.T < 65535 ? c.T : 65535);
