@@ -49,3 +49,28 @@ def test_many_terms(dev, T, V, D):
     close(losses, want[0], off[0] + want[0].abs() * 2 * ULP, "losses")
     close(dx, want[2], off[2] + want[2].abs() * HALF_STEP[dx.dtype] * 1.01 + 1e-37, "dx")
     close(dw, want[3], off[3] + want[3].abs() * ULP + 1e-37, "dw")
+
+
+@pytest.mark.parametrize("T,V,D", [(64, 300, 128), (3, 300, 128), (2, 300, 4104), (300, 1000, 1100)])
+def test_gradient_against_differences_along_itself(dev, T, V, D):
+    """The loss's change along the gradient's own direction is the gradient's length: a gradient of
+    another sign, length or place does not pass (along a random direction nearly all do)."""
+    from weight_communication_gb300 import loss
+    x, w, y = inputs(dev, T, V, D, padding=T > 3, seed=13)
+    _, lse = loss.cross_entropy(x, w, y, save=True)
+    g = torch.rand(T, device=dev)
+    dx, dw = loss.cross_entropy_grad(x, w, y, lse, g, dw_dtype=torch.float32)
+    value = lambda a, b: float((loss.cross_entropy(a, b, y).double() * g.double()).sum())  # noqa: E731
+    for arg, d in ((x, dx), (w, dw)):
+        # a fiftieth of the values that the gradient is mostly of: all, or the targets' rows
+        rows = arg if arg is x else arg[y[(y >= 0) & (y < V)].unique()]
+        step = 0.02 * float(rows.double().norm()) * d.double() / float(d.double().norm())
+        plus, minus = (arg.double() + step).bfloat16(), (arg.double() - step).bfloat16()
+        slope = value(plus, w) - value(minus, w) if arg is x else value(x, plus) - value(x, minus)
+        moved = plus.double() - minus.double()
+        # the loss's third derivative over such a step (0.003 of the slope over 60 seeds in 64
+        # bits), d's rounding to 2^-9, and the ends' middle, off arg by as much
+        bound = 0.03
+        assert slope == pytest.approx(float((d.double() * moved).sum()), rel=bound)
+        for wrong in (-d, 2 * d, 0.5 * d, d.flip(0), d.roll(1, 1)):
+            assert slope != pytest.approx(float((wrong.double() * moved).sum()), rel=bound)
