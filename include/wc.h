@@ -582,6 +582,9 @@ WC_API int wc_rms_norm_grad(const void *dy, int64_t ld_dy, const void *add, int6
  * g[t]     : dlosses[t] (fp32), or dloss for every token where dlosses is NULL.
  * dx, dw   : [T][ld_dx] and [V][ld_dw] of their types, rows that start on any value;
  *            either may be NULL (the matrix products for it are then not done).
+ * What is written (losses and lse, dx and dw, workspace) overlaps neither the rest of that
+ * nor what is read: dw that overlaps w, for one, is refused (WC_EINVAL).  Matrices that lie
+ * between one another's rows do not overlap.
  * workspace : the *_workspace() bytes for the same arguments, no initial value.  Of
  *            the backward pass: d for a piece of the vocabulary (256 MB, or as much as
  *            4 T D if that is more) and, if the pieces are several, dx in fp32 (for

@@ -74,3 +74,24 @@ def test_gradient_against_differences_along_itself(dev, T, V, D):
         assert slope == pytest.approx(float((d.double() * moved).sum()), rel=bound)
         for wrong in (-d, 2 * d, 0.5 * d, d.flip(0), d.roll(1, 1)):
             assert slope != pytest.approx(float((wrong.double() * moved).sum()), rel=bound)
+
+
+@pytest.mark.parametrize("T", [2, 20])
+def test_results_have_memory_of_their_own(dev, T):
+    """A weight is not updated in place; a gradient beside it in one tensor is."""
+    from weight_communication_gb300 import binding, loss
+    x, w, y = inputs(dev, T, 300, 64, padding=False, seed=14)
+    _, lse = loss.cross_entropy(x, w, y, save=True)
+    dx, dw = loss.cross_entropy_grad(x, w, y, lse, 0.5)
+    both = torch.cat([w, torch.zeros_like(w)], 1)
+    before = both.clone()
+    for out, weight in ((both[:, :64], both[:, :64]), (both[:, 32:96], both[:, :64]), (both.view(-1)[64:64 + 300 * 64].view(300, 64), both[:, :64])):
+        for accumulate in (False, True):
+            with pytest.raises(binding.WcError, match="dw overlaps w"):
+                loss.cross_entropy_grad(x, weight, y, lse, 0.5, dw=out, accumulate=accumulate)
+    with pytest.raises(binding.WcError, match="dw overlaps x"):
+        loss.cross_entropy_grad(both[:T, 64:], w, y, lse, 0.5, dw=both[:, 64:])
+    torch.cuda.synchronize()
+    assert torch.equal(both, before)
+    dx2, dw2 = loss.cross_entropy_grad(x, both[:, :64], y, lse, 0.5, dw=both[:, 64:])
+    assert torch.equal(dx2, dx) and torch.equal(dw2, dw) and torch.equal(both[:, :64], w)

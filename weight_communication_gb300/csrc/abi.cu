@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <new>
 #include <vector>
 
@@ -517,6 +518,53 @@ int row_pitch(const char *fn, const char *name, int64_t ld, int64_t rows, int64_
     return WC_OK;
 }
 
+// Memory that a call reads or writes: rows of `width` bytes, `pitch` bytes apart.
+struct Region {
+    const char *name;
+    const void *p;  // NULL: none
+    int64_t rows, width, pitch;
+};
+Region matrix(const char *name, const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t size) {
+    return {name, p, rows, cols * size, ld * size};
+}
+Region bytes(const char *name, const void *p, int64_t n) { return {name, p, 1, n, n}; }
+
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0 ? 1 : 0); }  // b > 0
+
+// A byte of both?  (Matrices that lie between one another's rows have none.)
+bool overlap(Region a, Region b) {
+    if (a.p == nullptr || b.p == nullptr || a.rows == 0 || b.rows == 0 || a.width == 0 || b.width == 0) return false;
+    const int64_t at_a = int64_t(reinterpret_cast<uintptr_t>(a.p)), at_b = int64_t(reinterpret_cast<uintptr_t>(b.p));
+    const int64_t end_a = at_a + (a.rows - 1) * a.pitch + a.width, end_b = at_b + (b.rows - 1) * b.pitch + b.width;
+    if (end_a <= at_b || end_b <= at_a) return false;
+    if (a.rows == 1) a.pitch = b.pitch;
+    if (b.rows == 1) b.pitch = a.pitch;
+    if (a.pitch == b.pitch) {
+        // rows i and i + k, whose starts are apart + k pitch bytes from one another
+        const int64_t apart = at_b - at_a, first = floor_div(-b.width - apart, a.pitch) + 1;
+        const int64_t k = first > 1 - a.rows ? first : 1 - a.rows;
+        return k < b.rows && apart + k * a.pitch < a.width;
+    }
+    if (a.rows > b.rows) return overlap(b, a);
+    for (int64_t i = 0; i < a.rows; ++i) {
+        const int64_t start = at_a + i * a.pitch, first = floor_div(start - b.width - at_b, b.pitch) + 1;
+        const int64_t j = first > 0 ? first : 0;
+        if (j < b.rows && at_b + j * b.pitch < start + a.width) return true;
+    }
+    return false;
+}
+
+// What is written overlaps neither what is read nor what else is written.
+int written_apart(const char *fn, std::initializer_list<Region> written, std::initializer_list<Region> read) {
+    for (const Region *w = written.begin(); w < written.end(); ++w) {
+        for (const Region *other = w + 1; other < written.end(); ++other)
+            if (overlap(*w, *other)) return fail(WC_EINVAL, "%s: %s overlaps %s", fn, w->name, other->name);
+        for (const Region &r : read)
+            if (overlap(*w, r)) return fail(WC_EINVAL, "%s: %s overlaps %s", fn, w->name, r.name);
+    }
+    return WC_OK;
+}
+
 int block_sizes(const char *fn, int64_t rows, int64_t cols) {
     if (rows < 0 || cols < 0)
         return fail(WC_EINVAL, "%s: rows = %lld, cols = %lld must not be negative", fn, (long long)rows, (long long)cols);
@@ -1007,6 +1055,10 @@ WC_API int wc_cross_entropy(const uint16_t *x, int64_t ld_x, const uint16_t *w, 
     if (workspace_bytes < need)
         return fail(WC_EINVAL, "%s: workspace of %lld bytes, %lld are needed", fn, (long long)workspace_bytes,
                     (long long)need);
+    rc = written_apart(fn, {bytes("losses", losses, 4 * T), bytes("lse", lse, 4 * T), bytes("workspace", workspace, need)},
+                       {matrix("x", x, T, D, ld_x, 2), matrix("w", w, V, D, ld_w, 2),
+                        bytes("targets", targets, T * (id_type == WC_I64 ? 8 : 4))});
+    if (rc != WC_OK) return rc;
     c.workspace = workspace;
     c.losses = losses;
     c.lse = lse;
@@ -1053,6 +1105,12 @@ WC_API int wc_cross_entropy_grad(const uint16_t *x, int64_t ld_x, const uint16_t
     if (workspace_bytes < need)
         return fail(WC_EINVAL, "%s: workspace of %lld bytes, %lld are needed", fn, (long long)workspace_bytes,
                     (long long)need);
+    rc = written_apart(fn, {matrix("dx", dx, T, D, ld_dx, dx_dtype == WC_BF16 ? 2 : 4),
+                            matrix("dw", dw, V, D, ld_dw, dw_dtype == WC_BF16 ? 2 : 4), bytes("workspace", workspace, need)},
+                       {matrix("x", x, T, D, ld_x, 2), matrix("w", w, V, D, ld_w, 2),
+                        bytes("targets", targets, T * (id_type == WC_I64 ? 8 : 4)), bytes("lse", lse, 4 * T),
+                        bytes("dlosses", dlosses, 4 * T)});
+    if (rc != WC_OK) return rc;
     c.workspace = workspace;
     c.lse_in = lse;
     c.dlosses = dlosses;

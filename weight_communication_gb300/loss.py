@@ -36,7 +36,8 @@ def cross_entropy_grad(x: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
                        needs_dx: bool = True, needs_dw: bool = True, stream=None):
     """(dx, dw): dx bf16 of x's shape; dw [V, D], a new tensor of dw_dtype (bf16
     unless given), or the given buffer (bf16 or fp32, rows that start anywhere),
-    written or, with accumulate, added to.  dlosses: the gradient of each token's
+    written or, with accumulate, added to, which shares no memory with the inputs (a
+    weight cannot be updated in place).  dlosses: the gradient of each token's
     loss, fp32 [tokens], or one number for all.  A gradient that is not needed is
     not computed, and None."""
     return binding.on_stream(stream, x.device, binding.calls().cross_entropy_grad, x, weight, targets, lse,
