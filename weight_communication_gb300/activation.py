@@ -43,7 +43,7 @@ def forward(gate: torch.Tensor, up: torch.Tensor | None = None, kind: str = "sil
     """h of gate's shape and type; with save, (h, Kept).  kind: "relu", "silu" or
     "gelu" (its tanh form).  gate, up, out: float32 or bfloat16, matrices whose rows
     are consecutive values, or contiguous tensors [.., columns]; out may be gate
-    or up."""
+    or up, and shares no other memory with them."""
     h, g, u = binding.on_stream(stream, gate.device, binding.calls().activation, gate, up, _kind(kind), save, out)
     if not save:
         return h

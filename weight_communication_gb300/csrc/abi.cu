@@ -565,6 +565,13 @@ int written_apart(const char *fn, std::initializer_list<Region> written, std::in
     return WC_OK;
 }
 
+// What is read, unless it is the very rows that are written, which a call may allow.
+Region unless_same(const Region &read, const Region &written) {
+    Region r = read;
+    if (r.p == written.p && r.width == written.width && (r.pitch == written.pitch || r.rows == 1)) r.p = nullptr;
+    return r;
+}
+
 int block_sizes(const char *fn, int64_t rows, int64_t cols) {
     if (rows < 0 || cols < 0)
         return fail(WC_EINVAL, "%s: rows = %lld, cols = %lld must not be negative", fn, (long long)rows, (long long)cols);
@@ -598,6 +605,13 @@ int kept_matrix(const char *fn, const char *name, const wc_kept *k, int64_t rows
                     (long long)k->ld_scales, name);
     *to = {k->codes, k->ld_codes, k->scales, k->ld_scales};
     return WC_OK;
+}
+
+Region codes_of(const char *name, const wc::Kept8 &k, int64_t rows, int64_t cols) {
+    return {name, k.q, rows, (cols + 15) / 16 * 16, k.ld_q};
+}
+Region scales_of(const char *name, const wc::Kept8 &k, int64_t rows, int64_t cols) {
+    return matrix(name, k.s, blocks128(cols), rows, k.ld_s, 4);
 }
 
 int norm_sizes(const char *fn, int64_t rows, int64_t cols, int dtype, int weight_dtype) {
@@ -860,6 +874,10 @@ WC_API int wc_fp8_dequant(const uint8_t *q, int64_t ld_q, const float *s, int64_
     WC_REQUIRE_PTR(fn, q);
     WC_REQUIRE_PTR(fn, s);
     if ((rc = values_pointer(fn, "out", out, out_dtype)) != WC_OK) return rc;
+    const bool per_row = rows_per_scale == 1;
+    rc = written_apart(fn, {matrix("out", out, rows, cols, ld_out, out_dtype == WC_BF16 ? 2 : 4)},
+                       {{"q", q, rows, cols, ld_q}, matrix("s", s, blocks128(cols), per_row ? rows : blocks128(rows), ld_s, 4)});
+    if (rc != WC_OK) return rc;
     const wc::Fp8Dequant a = {q, ld_q, s, ld_s, rows_per_scale, rows, cols, out, out_dtype == WC_BF16, ld_out};
     return from_cuda(wc::launch_fp8_dequant(a, static_cast<cudaStream_t>(stream)), fn);
 }
@@ -883,6 +901,13 @@ WC_API int wc_activation(const void *gate, int64_t ld_gate, const void *up, int6
     wc::Activation a = {};
     if ((rc = kept_matrix(fn, "kept_gate", kept_gate, rows, cols, &a.kept_gate)) != WC_OK) return rc;
     if ((rc = kept_matrix(fn, "kept_up", kept_up, rows, cols, &a.kept_up)) != WC_OK) return rc;
+    const int64_t size = dtype == WC_BF16 ? 2 : 4;
+    const Region in_gate = matrix("gate", gate, rows, cols, ld_gate, size), in_up = matrix("up", up, rows, cols, ld_up, size);
+    const Region out = matrix("h", h, rows, cols, ld_h, size);
+    const Region qg = codes_of("codes of kept_gate", a.kept_gate, rows, cols), qu = codes_of("codes of kept_up", a.kept_up, rows, cols);
+    const Region sg = scales_of("scales of kept_gate", a.kept_gate, rows, cols), su = scales_of("scales of kept_up", a.kept_up, rows, cols);
+    if ((rc = written_apart(fn, {out}, {unless_same(in_gate, out), unless_same(in_up, out)})) != WC_OK) return rc;
+    if (kept_gate && (rc = written_apart(fn, {qg, sg, qu, su}, {in_gate, in_up, out})) != WC_OK) return rc;
     a.gate = gate;
     a.up = up;
     a.ld_gate = ld_gate;
@@ -916,6 +941,16 @@ WC_API int wc_activation_grad(const void *dh, int64_t ld_dh, int dtype, int kind
     wc::ActivationGrad a = {};
     if ((rc = kept_matrix(fn, "kept_gate", kept_gate, rows, cols, &a.kept_gate)) != WC_OK) return rc;
     if ((rc = kept_matrix(fn, "kept_up", kept_up, rows, cols, &a.kept_up)) != WC_OK) return rc;
+    const int64_t size = dtype == WC_BF16 ? 2 : 4;
+    const Region in = matrix("dh", dh, rows, cols, ld_dh, size);
+    const Region og = matrix("dgate", dgate, rows, cols, ld_dgate, size), ou = matrix("dup", dup, rows, cols, ld_dup, size);
+    rc = written_apart(fn, {og, ou}, {codes_of("codes of kept_gate", a.kept_gate, rows, cols),
+                                      scales_of("scales of kept_gate", a.kept_gate, rows, cols),
+                                      codes_of("codes of kept_up", a.kept_up, rows, cols),
+                                      scales_of("scales of kept_up", a.kept_up, rows, cols)});
+    for (const Region &out : {og, ou})
+        if (rc == WC_OK) rc = written_apart(fn, {out}, {unless_same(in, out)});
+    if (rc != WC_OK) return rc;
     a.dh = dh;
     a.ld_dh = ld_dh;
     a.bf16 = dtype == WC_BF16;
@@ -954,6 +989,18 @@ WC_API int wc_rms_norm(const void *x, int64_t ld_x, const void *add, int64_t ld_
     if (rstd && (rc = values_pointer(fn, "rstd", rstd, WC_F32)) != WC_OK) return rc;
     wc::RmsNorm a = {};
     if ((rc = kept_matrix(fn, "kept", kept, rows, cols, &a.kept)) != WC_OK) return rc;
+    const int64_t size = dtype == WC_BF16 ? 2 : 4;
+    const Region in = matrix("x", x, rows, cols, ld_x, size), in_add = matrix("add", add, rows, cols, ld_add, size);
+    const Region out = matrix("y", y, rows, cols, ld_y, size), sum = matrix("total", total, rows, cols, ld_total, size);
+    const Region w = bytes("weight", weight, cols * (weight_dtype == WC_BF16 ? 2 : 4));
+    rc = written_apart(fn, {out, sum, bytes("rstd", rstd, 4 * rows), codes_of("codes of kept", a.kept, rows, cols),
+                            scales_of("scales of kept", a.kept, rows, cols)}, {w});
+    for (const Region &o : {out, sum})
+        if (rc == WC_OK) rc = written_apart(fn, {o}, {unless_same(in, o), unless_same(in_add, o)});
+    if (rc == WC_OK && kept)
+        rc = written_apart(fn, {bytes("rstd", rstd, 4 * rows), codes_of("codes of kept", a.kept, rows, cols),
+                                scales_of("scales of kept", a.kept, rows, cols)}, {in, in_add});
+    if (rc != WC_OK) return rc;
     a.x = x;
     a.add = add;
     a.ld_x = ld_x;
@@ -1007,6 +1054,19 @@ WC_API int wc_rms_norm_grad(const void *dy, int64_t ld_dy, const void *add, int6
         if (workspace_bytes < need)
             return fail(WC_EINVAL, "%s: workspace of %lld bytes, %lld are needed", fn, (long long)workspace_bytes,
                         (long long)need);
+        // (dweight may be weight: it is written when all rows are done)
+        const int64_t size = dtype == WC_BF16 ? 2 : 4;
+        const Region in = matrix("dy", dy, rows, cols, ld_dy, size), in_add = matrix("add", add, rows, cols, ld_add, size);
+        const Region out = matrix("dx", dx, rows, cols, ld_dx, size);
+        const Region w = bytes("weight", weight, cols * (weight_dtype == WC_BF16 ? 2 : 4));
+        const Region sums = bytes("dweight", dweight, cols * (dweight_dtype == WC_BF16 ? 2 : 4)), ws = bytes("workspace", workspace, need);
+        const Region r = bytes("rstd", rstd, 4 * rows), q = codes_of("codes of kept", a.kept, rows, cols),
+                     s = scales_of("scales of kept", a.kept, rows, cols);
+        rc = written_apart(fn, {out, sums, ws}, {r, q, s});
+        if (rc == WC_OK) rc = written_apart(fn, {out}, {w, unless_same(in, out), unless_same(in_add, out)});
+        if (rc == WC_OK) rc = written_apart(fn, {sums}, {unless_same(w, sums), in, in_add});
+        if (rc == WC_OK) rc = written_apart(fn, {ws}, {w, in, in_add});
+        if (rc != WC_OK) return rc;
     } else if (accumulate) {
         return WC_OK;
     }
