@@ -27,9 +27,9 @@ def test_what_sums_lose_does_not_grow_with_the_tokens(dev, T, dtype, accumulate)
     torch.cuda.synchronize()
     assert binding.wait_timeouts() == 0
     half = 0.5 * x.double().sum(0)
-    # d is exact; 1024 steps of 16 values to a chunk, each of which may lose an ulp of what is
+    # d is exact; 512 steps of 16 values to a chunk, each of which may lose an ulp of what is
     # summed so far, and a rounding for each chunk that is added; then the result's
-    off = half * (1024 * 2 ** -23 + -(-T // 16384) * ULP)
+    off = half * (512 * 2 ** -23 + -(-T // 8192) * ULP)
     want = torch.stack([-half, half]) + (old.double() if accumulate else 0.0)
     close(dw, want, off + want.abs() * HALF_STEP[dtype] * 1.01, "dw")
     assert bool((dx == 0).all())

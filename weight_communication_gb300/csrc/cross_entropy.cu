@@ -657,13 +657,10 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                 }
             }
             const int last = padding ? 0 : cols;  // of the columns with a gradient
-            float before[LONG ? kHalf : 1];  // the sums of the chunks before the last
+            // LONG: the chunks' sums, each of which leaves the tensor memory at once
+            float all[LONG ? kHalf : 1];
             if (LONG) {
-                if (MODE == kProducts && job.chunks == 1) {
-#pragma unroll
-                    for (int c = 0; c < kHalf; ++c) before[LONG ? c : 0] = -0.0f;
-                }
-                for (int32_t part = 0; part + 1 < job.chunks; ++part) {
+                for (int32_t part = 0; part < job.chunks; ++part) {
                     if (ok) ok = mbar_wait(smem_of(&sums[buf]), phase);
                     if (!ok) break;
                     tc_after_sync();
@@ -676,7 +673,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
                             const float x = __uint_as_float(w[k]);
-                            before[LONG ? c + k : 0] = part == 0 ? x : __fadd_rn(before[LONG ? c + k : 0], x);
+                            all[LONG ? c + k : 0] = part == 0 ? x : __fadd_rn(all[LONG ? c + k : 0], x);
                         }
                     }
                     tc_before_sync();
@@ -689,11 +686,11 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                 }
             }
             const uint32_t from = of_group + buf * kTile;
-            if (ok) ok = mbar_wait(smem_of(&sums[buf]), phase);
-            tc_after_sync();
+            if (!LONG && ok) ok = mbar_wait(smem_of(&sums[buf]), phase);
+            if (!LONG) tc_after_sync();
             Running run = {-INFINITY, 0.0f};
             uint32_t v[2][32];
-            if (ok) {
+            if (!LONG && ok) {
                 tmem_load(from, v[0]);
                 tmem_wait(v[0]);
             }
@@ -701,20 +698,14 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
             for (int c = 0; c < kHalf; c += 32) {
                 if (c >= half) break;
                 uint32_t(&w)[32] = v[LONG ? 0 : (c / 32) & 1];
-                if (LONG && ok) {
-                    if (c > 0) {
-                        tmem_load(from + c, w);
-                        tmem_wait(w);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        w[k] = __float_as_uint(__fadd_rn(before[LONG ? c + k : 0], __uint_as_float(w[k])));
-                }
                 if (!ok) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) w[k] = 0x7FC00000u;
+                } else if (LONG) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(all[LONG ? c + k : 0]);
                 } else if (c + 32 < half) {
-                    if (!LONG) tmem_load(from + c + 32, v[(c / 32 + 1) & 1]);
+                    tmem_load(from + c + 32, v[(c / 32 + 1) & 1]);
                 } else {
                     tc_before_sync();  // all read: the next tile may have the buffer
                     __syncwarp();
@@ -762,7 +753,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
                 if (!ok) run = {nan32(), nan32()};
                 a.parts[(int64_t(u.tj) * 2 + group) * job.rows_i + row] = make_float2(run.top, run.sum);
             }
-            if (++buf == kBuffers) {
+            if (!LONG && ++buf == kBuffers) {
                 buf = 0;
                 phase ^= 1u;
             }
@@ -1444,10 +1435,10 @@ cudaError_t run(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
                         maps[2], maps[3], a);
 }
 
-// Stages of K whose products the tensor core sums by itself: 1024 values.  The forward
-// pass takes no longer for it (8192 x 32000 x 2048: 513 us either way), as the sums leave
-// beside the next chunk's products; both gradients take 1705 us instead of 1692 with chunks
-// of 4096.  Both directions have the same chunks, so that they have the same logits, bit for
+// Stages of K whose products the tensor core sums by itself: 1024 values.  They take little
+// longer for it, as the sums leave beside the next chunk's products (8192 x 32000 x 2048:
+// losses 513 us either way; both gradients, with the chunks of their products, 1707 instead
+// of 1689).  Both directions have the same chunks, so that they have the same logits, bit for
 // bit: the log-sum is one of the forward pass's logits where one decides a row, and what
 // another order of the sums would be off by, some 2^-22 of a logit, is in the exponent.
 template <Mode MODE>
@@ -1457,12 +1448,12 @@ cudaError_t run_logits(const CUtensorMap (&maps)[4], Args &a, cudaStream_t strea
     return a.job[0].chunks > 1 ? run<MODE, true>(maps, a, stream) : run<MODE, false>(maps, a, stream);
 }
 
-// The same of dx's and dw's products, whose K are the vocabulary and the tokens: 16384 values,
-// so that what is cut off, some 2^-15 of a sum at most, does not grow with them (dw of a million
-// tokens, terms of one sign: 3.7e-3 without).  The chunks cost a percent where there are
-// several (8192 x 32000 x 2048 with dx in two 2560 us, whole 2520), and d is rounded to 2^-9.
+// The same of dx's and dw's products, whose K are the vocabulary and the tokens: 8192 values,
+// so that what is cut off, some 2^-16 of a sum at most, does not grow with them (dw of a million
+// tokens, terms of one sign: 3.7e-3 without).  (8192 x 32000 x 2048, dx in two chunks 2510 us, in
+// one 2500; both in chunks of 4096 2590.)
 cudaError_t run_products(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
-    constexpr int32_t chunk = 16384 / kDepth;
+    constexpr int32_t chunk = 8192 / kDepth;
     bool several = false;
     for (Job &j : a.job) {
         j.chunks = j.split > 0 ? (j.blocks + j.split * chunk - 1) / (j.split * chunk) : 0;
