@@ -147,3 +147,35 @@ def test_padding_beside_a_column_that_decides(dev, T, V, D):
         check(x[live], w, y[live], s[live], top[live], off[live], 1.0, losses[live], lse[live], dx[live], dw)
     else:
         assert bool((dw == 0).all())
+
+
+@pytest.mark.parametrize("T,V,D", [(1, 1100000, 2049), (3, 1100000, 2049), (2, 1100000, 2048), (2, 600000, 4104), (3, 600000, 4105)])
+def test_offsets_beyond_32_bits_for_few_tokens(dev, T, V, D):
+    """Weights of 2^31 values and more, of which all rows but a few are 0."""
+    from weight_communication_gb300 import loss
+    g = torch.Generator(device=dev)
+    g.manual_seed(T + D)
+    rows = torch.tensor([0, 5, V // 2, (1 << 31) // D, (1 << 31) // D + 1, V - 2, V - 1], device=dev)
+    w = torch.zeros(V, D, device=dev, dtype=torch.bfloat16)
+    w[rows] = torch.randn(7, D, generator=g, device=dev).bfloat16()
+    x = (torch.randn(T, D, generator=g, device=dev) * 0.2).bfloat16()
+    at = torch.arange(T, device=dev) + 3
+    losses, lse = loss.cross_entropy(x, w, rows[at], save=True)
+    dx, dw = loss.cross_entropy_grad(x, w, rows[at], lse, 1.0)
+    s = x.double() @ w[rows].double().t()
+    want = torch.log(torch.exp(s).sum(1) + (V - 7))
+    off = (D + 16) * 2 * ULP * (x.double().abs() @ w[rows].double().abs().t()).amax(1) + (s.abs().amax(1) + 200) * 4 * ULP
+    close(lse, want, off, "lse")
+    close(losses, want - s.gather(1, at[:, None])[:, 0], 2 * off, "losses")
+    d = torch.exp(s - want[:, None])
+    off_d = d * (3 * off[:, None] + HALF_STEP[torch.bfloat16]) * 1.01
+    d.scatter_add_(1, at[:, None], torch.full((T, 1), -1.0, device=dev, dtype=torch.float64))
+    off_d += d.abs() * HALF_STEP[torch.bfloat16] * 1.01
+    for got, total, bound, what in ((dx, d @ w[rows].double(), off_d @ w[rows].double().abs(), "dx"),
+                                    (dw[rows], d.t() @ x.double(), off_d.t() @ x.double().abs(), "dw")):
+        close(got, total, bound + total.abs() * HALF_STEP[torch.bfloat16] * 1.01 + 1e-37, what)
+    # all other rows have the same gradient: the tokens by 1 / sum
+    other = (x.double() / torch.exp(want)[:, None]).sum(0)
+    bound = (x.double().abs() / torch.exp(want)[:, None]).sum(0) * (3 * off.max() + HALF_STEP[torch.bfloat16] * 2.02) + 1e-37
+    for r in (1, V // 2 + 1, (1 << 31) // D - 1, (1 << 31) // D + 2, V - 3):
+        close(dw[r], other, bound, f"row {r}")

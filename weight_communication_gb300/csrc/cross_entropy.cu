@@ -39,12 +39,12 @@
 // The tensor core cuts sums off where fp32 would round them, so logits come out
 // nearer to 0 by some 2^-25 of themselves for each 16 values of K (D = 2048: 8e-6
 // for a logit of 4).  So it sums 1024 values of K at a time, and the epilogue adds
-// those sums up, rounded (losses of 64 x 8000 x 4096: 6.4e-6 off rms without, 1.6e-6
+// those sums up, rounded (losses of 64 x 8000 x 4096: 6.4e-6 off rms without, 1.5e-6
 // with it).  What is left largely cancels over the vocabulary; a target's logit
 // stands alone, so it is summed by itself in fp32 (warps 10 and 11 of the forward
 // pass, the kernel that lays x out in the backward pass), and d of a target
 // is expm1(s[t][y] - lse[t]).  (Losses of 8192 x 32000 x 2048: 8.1e-6 off rms with the
-// tensor core's target, 1.8e-6 with one chunk, 1.0e-6 with both.)
+// tensor core's target, 1.8e-6 with one chunk, 0.9e-6 with both.)
 #include <atomic>
 #include <type_traits>
 
@@ -659,31 +659,34 @@ product_kernel(const __grid_constant__ CUtensorMap map_i0, const __grid_constant
             const int last = padding ? 0 : cols;  // of the columns with a gradient
             // LONG: the chunks' sums, each of which leaves the tensor memory at once
             float all[LONG ? kHalf : 1];
-            if (LONG) {
-                for (int32_t part = 0; part < job.chunks; ++part) {
-                    if (ok) ok = mbar_wait(smem_of(&sums[buf]), phase);
-                    if (!ok) break;
-                    tc_after_sync();
+            auto take = [&](auto first) {
+                if (ok) ok = mbar_wait(smem_of(&sums[buf]), phase);
+                if (!ok) return;
+                tc_after_sync();
 #pragma unroll
-                    for (int c = 0; c < kHalf; c += 32) {
-                        if (c >= half) break;
-                        uint32_t w[32];
-                        tmem_load(of_group + buf * kTile + c, w);
-                        tmem_wait(w);
+                for (int c = 0; c < kHalf; c += 32) {
+                    if (c >= half) break;
+                    uint32_t w[32];
+                    tmem_load(of_group + buf * kTile + c, w);
+                    tmem_wait(w);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const float x = __uint_as_float(w[k]);
-                            all[LONG ? c + k : 0] = part == 0 ? x : __fadd_rn(all[LONG ? c + k : 0], x);
-                        }
-                    }
-                    tc_before_sync();
-                    __syncwarp();
-                    if (elected()) mbar_arrive_cluster(taken0 + buf * 8);
-                    if (++buf == kBuffers) {
-                        buf = 0;
-                        phase ^= 1u;
+                    for (int k = 0; k < 32; ++k) {
+                        const float x = __uint_as_float(w[k]);
+                        float &sum = all[LONG ? c + k : 0];
+                        sum = decltype(first)::value ? x : __fadd_rn(sum, x);
                     }
                 }
+                tc_before_sync();
+                __syncwarp();
+                if (elected()) mbar_arrive_cluster(taken0 + buf * 8);
+                if (++buf == kBuffers) {
+                    buf = 0;
+                    phase ^= 1u;
+                }
+            };
+            if (LONG) {
+                take(std::true_type());
+                for (int32_t part = 1; part < job.chunks; ++part) take(std::false_type());
             }
             const uint32_t from = of_group + buf * kTile;
             if (!LONG && ok) ok = mbar_wait(smem_of(&sums[buf]), phase);
@@ -1437,8 +1440,8 @@ cudaError_t run(const CUtensorMap (&maps)[4], Args &a, cudaStream_t stream) {
 
 // Stages of K whose products the tensor core sums by itself: 1024 values.  They take little
 // longer for it, as the sums leave beside the next chunk's products (8192 x 32000 x 2048:
-// losses 513 us either way; both gradients, with the chunks of their products, 1707 instead
-// of 1689).  Both directions have the same chunks, so that they have the same logits, bit for
+// losses 528 us either way; both gradients, with the chunks of their products, 1711 instead
+// of 1692).  Both directions have the same chunks, so that they have the same logits, bit for
 // bit: the log-sum is one of the forward pass's logits where one decides a row, and what
 // another order of the sums would be off by, some 2^-22 of a logit, is in the exponent.
 template <Mode MODE>

@@ -8,9 +8,10 @@ pieces of the vocabulary and without keeping the logits.
 
 x [.., D] and weight [V, D] are bf16 and multiplied on the tensor cores with fp32
 sums.  A target outside [0, V) is padding: its loss is 0, and nothing in its row of
-x reaches a gradient.  The backward pass multiplies the logits again, a piece
-of the vocabulary at a time, with d rounded to bf16 for the products (not for up to
-four tokens of up to 4096 values).  The same bits every run.
+x reaches a gradient.  The backward pass multiplies the logits again, the same bits, a
+piece of the vocabulary at a time, with d rounded to bf16 for the products (not for up to
+four tokens of up to 4096 values).  lse is one fp32 number, so each exponential of d carries
+its rounding, |lse| 2^-24 of itself.  The same bits every run.
 
     losses, lse = loss.cross_entropy(x, weight, targets, save=True)
     dx, dw = loss.cross_entropy_grad(x, weight, targets, lse, 1.0 / tokens)
@@ -38,7 +39,7 @@ def cross_entropy_grad(x: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
     unless given), or the given buffer (bf16 or fp32, rows that start anywhere),
     written or, with accumulate, added to, which shares no memory with the inputs (a
     weight cannot be updated in place).  dlosses: the gradient of each token's
-    loss, fp32 [tokens], or one number for all.  A gradient that is not needed is
+    loss, fp32 [tokens], or one Python number for all.  A gradient that is not needed is
     not computed, and None."""
     return binding.on_stream(stream, x.device, binding.calls().cross_entropy_grad, x, weight, targets, lse,
                              dlosses, needs_dx, needs_dw, dw, dw_dtype, accumulate)
