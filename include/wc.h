@@ -571,24 +571,35 @@ WC_API int wc_rms_norm_grad(const void *dy, int64_t ld_dy, const void *add, int6
  * A target outside [0, V) is padding: its loss is 0, and nothing in its row of x
  * reaches a gradient.  Products of bf16 values in fp32; d is rounded to bf16 for the
  * products with w and x, so a gradient is a sum of terms that are each within
- * 2^-8 of their value (not rounded for T <= 4 and D <= 4096).  The order of the sums depends on the sizes alone (the same
- * bits every run).
- * x, w     : bf16 [T][ld_x] and [V][ld_w].  Rows may start on any value; those that
- *            do not start on 16 bytes (address and stride) are first copied (but for T <= 4
- *            and D <= 4096).
+ * 2^-8 of their value (not rounded for T <= 4 and D <= 4096).  lse is one fp32 number, so
+ * each exponential of d carries its rounding, |lse| 2^-24 of itself; both directions
+ * compute the same logits, and a column that outweighs all others has probability 1 at any
+ * finite size of the logits.  On the tensor cores a gradient's sum over tokens or
+ * vocabulary loses some 2^-16 of itself at most, however long it is.  The order of the sums
+ * depends on the sizes alone (the same bits every run).
+ * x, w     : bf16 [T][ld_x] and [V][ld_w].  Rows may start on any value; what is copied to
+ *            rows that start on 16 bytes first is said under workspace.
  * targets  : [T] of id_type (WC_I32 or WC_I64).
  * losses, lse : fp32 [T]; forward: either may be NULL.  backward: lse of the forward
- *            pass.
+ *            pass, of the same x, w and T.
  * g[t]     : dlosses[t] (fp32), or dloss for every token where dlosses is NULL.
  * dx, dw   : [T][ld_dx] and [V][ld_dw] of their types, rows that start on any value;
  *            either may be NULL (the matrix products for it are then not done).
  * What is written (losses and lse, dx and dw, workspace) overlaps neither the rest of that
  * nor what is read: dw that overlaps w, for one, is refused (WC_EINVAL).  Matrices that lie
  * between one another's rows do not overlap.
- * workspace : the *_workspace() bytes for the same arguments, no initial value.  Of
- *            the backward pass: d for a piece of the vocabulary (256 MB, or as much as
- *            4 T D if that is more) and, if the pieces are several, dx in fp32 (for
- *            T <= 4 and D <= 4096: some 300 T D sums of dx at most).
+ * workspace : the *_workspace() bytes for the same arguments, no initial value.
+ *   forward  : 8 bytes for each token of a launch (up to 65536) and half tile of the
+ *              vocabulary, min(T, 65536) * V / 16 bytes with tiles of 256 columns and up to four
+ *              times that with narrower ones, which only few tokens have; copies of x and of w,
+ *              each if its rows do not start on 16 bytes (address and stride).
+ *   backward : a copy of x; one of w if its rows do not start on 16 bytes; d for a piece of the
+ *              vocabulary (256 MB, or as much as 4 T D if that is more, at least 512 T); and
+ *              sums of dx, up to 32 times 4 T D where tokens are few, once where the
+ *              pieces are several, else none.
+ *   Up to four tokens have none of these where, forward, they fit shared memory as fp32 (T
+ *   rounded up to 1, 2 or 4 times D up to some 28000) or, backward, D <= 4096: some 2.5 KB
+ *   a token, and backward some 300 T D sums of dx at most.
  * Requires T, V <= 2^31 - 4096, V and D >= 1, D <= 2^22, T * V < 2^44, T * D and
  * V * D < 2^40, every ld >= D.
  */
