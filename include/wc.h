@@ -540,7 +540,8 @@ WC_API int wc_activation_grad(const void *dh, int64_t ld_dh, int dtype, int kind
  *   dx = r * (dy * weight - n * mean of (dy * weight * n)) + add,  the gradient of
  *        x and of the forward pass's add (add here: what reaches t past the norm)
  *   dweight = sum over the rows of dy * n   (accumulate != 0: added to its values)
- * Sums in fp32 in an order that the sizes fix (the same bits every run).
+ * Sums in fp32 in an order that the sizes fix, and whether all rows start on 16 bytes and
+ * have a multiple of 8 values (the same bits every run).
  * x, add, total, y : [rows][ld] of `dtype`; dy, add, dx the same of their `dtype`.
  *              Rows may start on any value.  total and y may be x or add, dx may be
  *              dy or add (the same rows); otherwise what is written overlaps nothing.
@@ -576,7 +577,8 @@ WC_API int wc_rms_norm_grad(const void *dy, int64_t ld_dy, const void *add, int6
  * compute the same logits, and a column that outweighs all others has probability 1 at any
  * finite size of the logits.  On the tensor cores a gradient's sum over tokens or
  * vocabulary loses some 2^-16 of itself at most, however long it is.  The order of the sums
- * depends on the sizes alone (the same bits every run).
+ * depends on the sizes alone and, for T <= 4, that over the vocabulary also on whether rows
+ * of w and dw start on 16 bytes (the same bits every run).
  * x, w     : bf16 [T][ld_x] and [V][ld_w].  Rows may start on any value; what is copied to
  *            rows that start on 16 bytes first is said under workspace.
  * targets  : [T] of id_type (WC_I32 or WC_I64).

@@ -121,7 +121,7 @@ def test_few_tokens_that_a_column_decides(dev, T, V, D, scale):
             dw = strided(torch.zeros(V, D, device=dev), ld, at)
             dx, dw = loss.cross_entropy_grad(x, rows, y, lse, g, dw=dw)
             check(x, w, y, s, top, off, g, losses, lse, dx, dw)
-            # where rows lie changes no bit
+            # where rows lie changes no bit of a logit
             first = first or (losses, lse, dx, dw)
             assert all(torch.equal(a, b) for a, b in zip(first, (losses, lse, dx, dw)))
         losses, lse = loss.cross_entropy(x, rows, top, save=True)
